@@ -319,6 +319,118 @@ pa_status pa_paged_prefill_attn_fp8(const void *q, int n_tokens, int n_q_heads, 
                                     const float *v_scale, void *workspace, size_t workspace_bytes, void *out,
                                     cudaStream_t st);
 
+/* ---------------------------------------- e4m3 cache with scales per block
+ * No counterpart on the pages.  An e4m3 cache whose scales follow the data: a
+ * power of two for each block of `block` consecutive slots (slots
+ * [i * block, (i + 1) * block)) and kv head, K and V apart.  Buffers uint8
+ * [n_layers, size, n_kv_heads, head_dim] as above; exponents k_exp, v_exp uint8
+ * [n_layers, ceil(size / block), n_kv_heads], one byte e each; an element is
+ *     e4m3_value(byte) * 2^(e - 127)        (e = 0: 0, a block nothing was stored in)
+ * block is a power of two from 1 (a scale per token) to 128.  head_dim 64 or
+ * 128.  Zeroed buffers and exponents are an empty cache.
+ *
+ * pa_kv_store_fp8_block: the new tokens' K/V at slots loc[t].  For the rows x
+ * of the call that fall into a block, and one kv head,
+ *     e    = max(e_old, the smallest e in [1, 254] with amax |x| <= 448 * 2^(e - 127))
+ *     byte = e4m3(x * 2^(127 - e))     (nearest even; finite overflow and
+ *            infinities saturate to +-448, a NaN stays NaN; amax over finite x)
+ * and where e > e_old > 0 the block's other rows are rounded to the new scale:
+ * byte' = e4m3(e4m3_value(byte) * 2^(e_old - e)).  An exponent never falls:
+ * hand a page out again through pa_kv_reset_fp8_block, or its rows keep the
+ * largest scale the block ever had.  The tokens of one call that fall into one
+ * block must stand next to each other in loc (true where a block belongs to
+ * one request and its tokens are packed in order), and locations must be
+ * distinct, else the block's bytes are undefined.  Bad locations are skipped
+ * (PA_DEVERR_SLOT), as in pa_kv_store.  n_tokens == 0 is a no-op. */
+pa_status pa_kv_store_fp8_block(void *k_buf, void *v_buf, pa_kv_shape s, int layer_id, const void *k_new,
+                                const void *v_new, const int32_t *loc, int n_tokens, uint8_t *k_exp,
+                                uint8_t *v_exp, int block, int32_t *error_word, cudaStream_t st);
+
+/* Mark the n listed blocks empty in every layer: k_exp and v_exp, uint8
+ * [n_layers, n_blocks, n_kv_heads], become 0 there.  blocks: int32 [n]
+ * (device).  An index outside [0, n_blocks) is skipped (PA_DEVERR_SLOT). */
+pa_status pa_kv_reset_fp8_block(uint8_t *k_exp, uint8_t *v_exp, int n_layers, int n_blocks, int n_kv_heads,
+                                const int32_t *blocks, int n, int32_t *error_word, cudaStream_t st);
+
+/* pa_paged_decode_attn_fp8_block: what pa_paged_decode_attn computes, over this
+ * cache.  Supported: head_dim 64 or 128, 1 <= G <= 16, batch <= 4096.  QK^T and
+ * PV run on tcgen05 with the e4m3 rows as they are; q and the softmax weights
+ * enter as sums of e4m3 terms (q within 2^-22 of its head's largest element,
+ * weights to 12 bits), products and sums in fp32.  Two kernels on `st`:
+ * decode, and a merge of the (request, kv head) pairs that more than one CTA
+ * worked on, in a fixed order (run-to-run bit-identical).  Workspace: at least
+ * pa_decode_fp8_block_workspace_bytes, whatever the batch; nothing in it is
+ * kept between calls, and calls that share one are ordered on a stream.  A
+ * request row out of range sets PA_DEVERR_ROW and gives zeros, a length outside
+ * [0, max_ctx] is clamped and sets PA_DEVERR_LEN, a slot outside [0, size) is
+ * masked and sets PA_DEVERR_SLOT; a request with nothing to attend to gives
+ * zeros.  Under PA_OVERLAP_EARLY_KV it behaves as in early-metadata mode. */
+size_t pa_decode_fp8_block_workspace_bytes(int n_q_heads, int n_kv_heads, int head_dim);
+pa_status pa_paged_decode_attn_fp8_block(const void *q, int batch, int n_q_heads, const void *k_buf,
+                                         const void *v_buf, pa_kv_shape s, int layer_id,
+                                         const int32_t *req_to_token, int req_rows, int max_ctx,
+                                         const int32_t *req_pool_indices, const int32_t *seq_lens, float scale,
+                                         const uint8_t *k_exp, const uint8_t *v_exp, int block, void *workspace,
+                                         size_t workspace_bytes, void *out, cudaStream_t st);
+
+/* pa_paged_prefill_attn_fp8_block: pa_paged_prefill_attn over this cache, the
+ * same arguments, workspace, limits and error reporting plus the exponents.
+ * The tiles are widened to bf16 with their scale (exact) before the MMAs. */
+pa_status pa_paged_prefill_attn_fp8_block(const void *q, int n_tokens, int n_q_heads, const void *k_buf,
+                                          const void *v_buf, pa_kv_shape s, int layer_id, const int32_t *qo_indptr,
+                                          const int32_t *kv_indptr, int n_reqs, const int32_t *req_to_token,
+                                          int req_rows, int max_ctx, const int32_t *req_pool_indices, float scale,
+                                          const uint8_t *k_exp, const uint8_t *v_exp, int block, void *workspace,
+                                          size_t workspace_bytes, void *out, cudaStream_t st);
+
+/* --------------------------------------- attention weights and eviction
+ * No counterpart on the pages: keeping a request's cache within a budget by
+ * dropping the tokens that attention uses least.
+ *
+ * pa_paged_decode_attn_weights: decode attention (block == 0: over the bf16
+ * cache of pa_paged_decode_attn, k_exp and v_exp NULL; block >= 1: over the
+ * block-scaled e4m3 cache) that also adds each cached token's attention weight,
+ * summed over the query heads, to `weights`, fp32 [req_rows, max_ctx], laid out
+ * like req_to_token:
+ *     weights[row_b, j] += sum_hq softmax(s_hq)_j      for j < seq_lens[b]
+ * (a request's additions of one call sum to n_q_heads; calls of several layers
+ * may add to one table).  Entries j >= seq_lens[b] are not touched: the caller
+ * zeroes a row when it hands it out.  The requests of a call must have rows of
+ * their own: a request whose row an earlier one has sets PA_DEVERR_ROW and adds
+ * nothing (its output is right).  Workspace:
+ * pa_decode_weights_workspace_bytes for at most max_batch requests of
+ * max_tokens cached tokens in all; a call with more sets PA_DEVERR_LEN and adds
+ * nothing for the requests' tiles past that (outputs are right).  Else as
+ * pa_paged_decode_attn_fp8_block (bf16: the weights enter PV as two bf16 terms). */
+size_t pa_decode_weights_workspace_bytes(int max_batch, int64_t max_tokens, int n_q_heads, int n_kv_heads,
+                                         int head_dim);
+pa_status pa_paged_decode_attn_weights(const void *q, int batch, int n_q_heads, const void *k_buf, const void *v_buf,
+                                       pa_kv_shape s, int layer_id, const int32_t *req_to_token, int req_rows,
+                                       int max_ctx, const int32_t *req_pool_indices, const int32_t *seq_lens,
+                                       float scale, const uint8_t *k_exp, const uint8_t *v_exp, int block,
+                                       float *weights, void *workspace, size_t workspace_bytes, void *out,
+                                       cudaStream_t st);
+
+/* pa_kv_evict: cut every request of more than `budget` tokens to `budget`.
+ * Kept are its last `recent` tokens (0 <= recent <= budget) and, of the others,
+ * the budget - recent with the largest weights; ties go to the lowest position,
+ * a NaN counts as minus infinity.  For such a request, n = seq_lens[b], the
+ * table row's first `budget` entries become the kept tokens' slots and the
+ * weights' first `budget` entries their weights, both in position order;
+ * weights[row, budget .. n) become 0, table entries from `budget` on are left as
+ * they are; freed[b, 0 .. n - budget) lists the evicted slots in position order
+ * (freed: int32 [batch, max_ctx]); new_lens[b] = budget.  A request of at most
+ * `budget` tokens keeps its row and weights and new_lens[b] = n.  Keys stay as
+ * they were rotated: positions given to later tokens go on counting from the
+ * original length.  K/V rows are not moved; with a block-scaled cache, hand
+ * slots out again only when all slots of their block are free.  new_lens may be
+ * seq_lens.  A row out of range, or one that an earlier request of the call has
+ * too, sets PA_DEVERR_ROW, a length outside [0, max_ctx] PA_DEVERR_LEN; such a
+ * request is left as it is (new_lens[b] is its length, clamped). */
+pa_status pa_kv_evict(int32_t *req_to_token, int req_rows, int max_ctx, const int32_t *req_pool_indices,
+                      const int32_t *seq_lens, int batch, float *weights, int budget, int recent,
+                      int32_t *new_lens, int32_t *freed, int32_t *error_word, cudaStream_t st);
+
 /* ------------------------------------------------------ fused decode step
  * One layer's decode step in one launch (commit 398e8a3: the CUDA-graph
  * decode step over packed inputs, rotary embedding on packed 3-D inputs, K/V

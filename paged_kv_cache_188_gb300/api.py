@@ -9,7 +9,8 @@ device memory and streams only.
 Dtypes follow the pages (AstrAI commit 398e8a3, tests/inference/test_cache.py):
 bf16 activations and KV buffers, int32 page-table / request-row / location
 indices; the fp8 entry points take e4m3 caches (uint8 or float8_e4m3fn
-tensors) with fp32 [n_layers, n_kv_heads] scales.  Other dtypes are rejected
+tensors) with fp32 [n_layers, n_kv_heads] scales, or uint8 exponents per
+(layer, block of slots, kv head).  Other dtypes are rejected
 here, before any launch.
 """
 from __future__ import annotations
@@ -51,7 +52,10 @@ EXPORTS = ["pa_status_string", "pa_decode_workspace_bytes", "pa_prefill_workspac
            "pa_set_launch_overlap", "pa_get_launch_overlap", "pa_decode_step",
            "pa_paged_prefill_attn_last", "pa_dense_prefill_attn", "pa_cascade_workspace_bytes",
            "pa_paged_decode_attn_cascade", "pa_kv_store_fp8", "pa_paged_decode_attn_fp8",
-           "pa_paged_prefill_attn_fp8", "pa_set_wait_timeout_ns", "pa_get_wait_timeout_ns"]
+           "pa_paged_prefill_attn_fp8", "pa_set_wait_timeout_ns", "pa_get_wait_timeout_ns",
+           "pa_kv_store_fp8_block", "pa_kv_reset_fp8_block", "pa_decode_fp8_block_workspace_bytes",
+           "pa_paged_decode_attn_fp8_block", "pa_paged_prefill_attn_fp8_block", "pa_decode_weights_workspace_bytes",
+           "pa_paged_decode_attn_weights", "pa_kv_evict"]
 
 _lib = None
 
@@ -96,6 +100,17 @@ def lib():
                                            i32, P, P]
     L.pa_paged_prefill_attn_fp8.argtypes = [P, i32, i32, P, P, KvShape, i32, P, P, i32, P, i32, i32, P, f32, P, P,
                                             P, sz, P, P]
+    L.pa_kv_store_fp8_block.argtypes = [P, P, KvShape, i32, P, P, P, i32, P, P, i32, P, P]
+    L.pa_kv_reset_fp8_block.argtypes = [P, P, i32, i32, i32, P, i32, P, P]
+    L.pa_decode_fp8_block_workspace_bytes.argtypes = [i32, i32, i32]
+    L.pa_paged_decode_attn_fp8_block.argtypes = [P, i32, i32, P, P, KvShape, i32, P, i32, i32, P, P, f32, P, P, i32, P,
+                                                 sz, P, P]
+    L.pa_paged_prefill_attn_fp8_block.argtypes = [P, i32, i32, P, P, KvShape, i32, P, P, i32, P, i32, i32, P, f32, P, P,
+                                                  i32, P, sz, P, P]
+    L.pa_decode_weights_workspace_bytes.argtypes = [i32, ctypes.c_int64, i32, i32, i32]
+    L.pa_paged_decode_attn_weights.argtypes = [P, i32, i32, P, P, KvShape, i32, P, i32, i32, P, P, f32, P, P, i32, P, P,
+                                               sz, P, P]
+    L.pa_kv_evict.argtypes = [P, i32, i32, P, P, i32, P, i32, i32, P, P, P, P]
     L.pa_set_launch_overlap.argtypes = [i32]
     L.pa_get_launch_overlap.argtypes = []
     L.pa_set_wait_timeout_ns.argtypes = [ctypes.c_uint64]
@@ -103,6 +118,8 @@ def lib():
     for name in EXPORTS[3:]:
         getattr(L, name).restype = i32
     L.pa_cascade_workspace_bytes.restype = sz
+    L.pa_decode_fp8_block_workspace_bytes.restype = sz
+    L.pa_decode_weights_workspace_bytes.restype = sz
     L.pa_set_wait_timeout_ns.restype = None
     L.pa_get_wait_timeout_ns.restype = ctypes.c_uint64
     _lib = L
@@ -236,6 +253,66 @@ def pa_kv_store_fp8(k_buf, v_buf, layer_id, k_new, v_new, loc, k_scale, v_scale,
                                                  T, _p(k_scale), _p(v_scale), _p(error_word), _stream(stream)))
 
 
+def _one_device(*tensors):
+    """All on one device, and that the current one: the library works on the
+    current device and stream."""
+    devs = {t.device for t in tensors if t is not None}
+    if len(devs) != 1 or next(iter(devs)).index != torch.cuda.current_device():
+        raise ValueError(f"tensors must be on the current CUDA device, got {sorted(map(str, devs))}")
+
+
+def _kv_shape_block(k_buf, v_buf, k_exp, v_exp, block):
+    """A block-scaled e4m3 cache: byte buffers [n_layers, size, Hkv, D] and uint8
+    exponents [n_layers, ceil(size / block), Hkv]."""
+    for t, name in ((k_buf, "k_buf"), (v_buf, "v_buf")):
+        if t.dtype not in FP8_DTYPES:
+            raise TypeError(f"{name} must be uint8 or float8_e4m3fn, got {t.dtype}")
+        _need(t, t.dtype, name, 4)
+    if k_buf.shape != v_buf.shape:
+        raise ValueError("k_buf and v_buf shapes differ")
+    _need(k_exp, torch.uint8, "k_exp", 3)
+    _need(v_exp, torch.uint8, "v_exp", 3)
+    n_layers, size, Hkv, _ = k_buf.shape
+    if block not in (1, 2, 4, 8, 16, 32, 64, 128):
+        raise ValueError(f"block must be a power of two from 1 to 128, got {block}")
+    if tuple(k_exp.shape) != (n_layers, -(-size // block), Hkv) or v_exp.shape != k_exp.shape:
+        raise ValueError("k_exp / v_exp must be [n_layers, ceil(size / block), n_kv_heads]")
+    return KvShape(*k_buf.shape)
+
+
+def pa_kv_store_fp8_block(k_buf, v_buf, layer_id, k_new, v_new, loc, k_exp, v_exp, block, error_word=None, stream=None):
+    """KV store into an e4m3 cache with a power-of-two scale per (block of slots,
+    kv head): scales rise as needed, a block's earlier rows are rounded to a
+    risen scale.  Tokens of one block stand next to each other in ``loc``."""
+    s = _kv_shape_block(k_buf, v_buf, k_exp, v_exp, block)
+    _need(k_new, torch.bfloat16, "k_new", 3)
+    _need(v_new, torch.bfloat16, "v_new", 3)
+    _need(loc, torch.int32, "loc", 1)
+    T = loc.numel()
+    if tuple(k_new.shape) != (T, s.n_kv_heads, s.head_dim) or v_new.shape != k_new.shape:
+        raise ValueError("k_new / v_new must be [n_tokens, n_kv_heads, head_dim]")
+    if error_word is not None:
+        _need(error_word, torch.int32, "error_word")
+    _one_device(k_buf, v_buf, k_new, v_new, loc, k_exp, v_exp, error_word)
+    _ok("pa_kv_store_fp8_block", lib().pa_kv_store_fp8_block(
+        _p(k_buf), _p(v_buf), s, layer_id, _p(k_new), _p(v_new), _p(loc), T, _p(k_exp), _p(v_exp), block,
+        _p(error_word), _stream(stream)))
+
+
+def pa_kv_reset_fp8_block(k_exp, v_exp, blocks, error_word=None, stream=None):
+    """Mark the listed blocks (int32) empty in every layer of a block-scaled cache."""
+    _need(k_exp, torch.uint8, "k_exp", 3)
+    _need(v_exp, torch.uint8, "v_exp", 3)
+    _need(blocks, torch.int32, "blocks", 1)
+    if v_exp.shape != k_exp.shape:
+        raise ValueError("k_exp and v_exp shapes differ")
+    if error_word is not None:
+        _need(error_word, torch.int32, "error_word")
+    _one_device(k_exp, v_exp, blocks, error_word)
+    _ok("pa_kv_reset_fp8_block", lib().pa_kv_reset_fp8_block(
+        _p(k_exp), _p(v_exp), *k_exp.shape, _p(blocks), blocks.numel(), _p(error_word), _stream(stream)))
+
+
 def pa_rope_packed(q, k, positions, cos_tab, sin_tab, error_word=None, stream=None):
     _need(q, torch.bfloat16, "q", 3)
     _need(positions, torch.int32, "positions", 1)
@@ -291,6 +368,86 @@ def pa_paged_decode_attn_fp8(q, k_buf, v_buf, layer_id, req_to_token, req_pool_i
         _p(q), B, Hq, _p(k_buf), _p(v_buf), s, layer_id, _p(req_to_token), req_to_token.shape[0],
         req_to_token.shape[1], _p(req_pool_indices), _p(seq_lens), float(scale), _p(k_scale), _p(v_scale),
         _p(workspace), workspace.numel(), max_splits, _p(out), _stream(stream)))
+
+
+def pa_decode_fp8_block_workspace_bytes(n_q_heads, n_kv_heads, head_dim):
+    return int(lib().pa_decode_fp8_block_workspace_bytes(n_q_heads, n_kv_heads, head_dim))
+
+
+def pa_decode_weights_workspace_bytes(max_batch, max_tokens, n_q_heads, n_kv_heads, head_dim):
+    """Workspace of :func:`pa_paged_decode_attn_weights` for at most ``max_batch``
+    requests with ``max_tokens`` cached tokens in all."""
+    return int(lib().pa_decode_weights_workspace_bytes(max_batch, max_tokens, n_q_heads, n_kv_heads, head_dim))
+
+
+def _decode_tensors(q, out, req_to_token, req_pool_indices, seq_lens, workspace, s):
+    _need(q, torch.bfloat16, "q", 3)
+    _need(out, torch.bfloat16, "out", 3)
+    _need(req_to_token, torch.int32, "req_to_token", 2)
+    _need(req_pool_indices, torch.int32, "req_pool_indices", 1)
+    _need(seq_lens, torch.int32, "seq_lens", 1)
+    _need(workspace, torch.uint8, "workspace")
+    B, Hq, D = q.shape
+    if out.shape != q.shape or D != s.head_dim or req_pool_indices.numel() != B or seq_lens.numel() != B:
+        raise ValueError("q/out [batch, n_q_heads, head_dim], req_pool_indices/seq_lens [batch] expected")
+    return B, Hq
+
+
+def pa_paged_decode_attn_fp8_block(q, k_buf, v_buf, layer_id, req_to_token, req_pool_indices, seq_lens, scale,
+                                   k_exp, v_exp, block, workspace, out, stream=None):
+    """Decode attention over a block-scaled e4m3 cache."""
+    s = _kv_shape_block(k_buf, v_buf, k_exp, v_exp, block)
+    B, Hq = _decode_tensors(q, out, req_to_token, req_pool_indices, seq_lens, workspace, s)
+    _one_device(q, k_buf, v_buf, req_to_token, req_pool_indices, seq_lens, k_exp, v_exp, workspace, out)
+    _ok("pa_paged_decode_attn_fp8_block", lib().pa_paged_decode_attn_fp8_block(
+        _p(q), B, Hq, _p(k_buf), _p(v_buf), s, layer_id, _p(req_to_token), req_to_token.shape[0],
+        req_to_token.shape[1], _p(req_pool_indices), _p(seq_lens), float(scale), _p(k_exp), _p(v_exp), block,
+        _p(workspace), workspace.numel(), _p(out), _stream(stream)))
+
+
+def pa_paged_decode_attn_weights(q, k_buf, v_buf, layer_id, req_to_token, req_pool_indices, seq_lens, scale, weights,
+                                 workspace, out, k_exp=None, v_exp=None, block=0, stream=None):
+    """Decode attention over a bf16 cache, or (``block`` >= 1, with ``k_exp`` and
+    ``v_exp``) a block-scaled e4m3 cache, that also adds each cached token's
+    attention weight, summed over the query heads, to ``weights`` (fp32, shaped
+    like ``req_to_token``)."""
+    if block == 0 and k_exp is None and v_exp is None:
+        s = _kv_shape(k_buf, v_buf)
+    else:
+        s = _kv_shape_block(k_buf, v_buf, k_exp, v_exp, block)
+    B, Hq = _decode_tensors(q, out, req_to_token, req_pool_indices, seq_lens, workspace, s)
+    _need(weights, torch.float32, "weights", 2)
+    if weights.shape != req_to_token.shape:
+        raise ValueError("weights must have the shape of req_to_token")
+    _one_device(q, k_buf, v_buf, req_to_token, req_pool_indices, seq_lens, k_exp, v_exp, weights, workspace, out)
+    _ok("pa_paged_decode_attn_weights", lib().pa_paged_decode_attn_weights(
+        _p(q), B, Hq, _p(k_buf), _p(v_buf), s, layer_id, _p(req_to_token), req_to_token.shape[0],
+        req_to_token.shape[1], _p(req_pool_indices), _p(seq_lens), float(scale), _p(k_exp), _p(v_exp), block,
+        _p(weights), _p(workspace), workspace.numel(), _p(out), _stream(stream)))
+
+
+def pa_kv_evict(req_to_token, req_pool_indices, seq_lens, weights, budget, recent, new_lens, freed, error_word=None,
+                stream=None):
+    """Cut every request of more than ``budget`` tokens to its last ``recent`` and
+    its heaviest others: table row and weights compacted in place, the evicted
+    slots listed in ``freed`` (int32 [batch, max_ctx]), lengths in ``new_lens``."""
+    _need(req_to_token, torch.int32, "req_to_token", 2)
+    _need(req_pool_indices, torch.int32, "req_pool_indices", 1)
+    _need(seq_lens, torch.int32, "seq_lens", 1)
+    _need(weights, torch.float32, "weights", 2)
+    _need(new_lens, torch.int32, "new_lens", 1)
+    _need(freed, torch.int32, "freed", 2)
+    B = seq_lens.numel()
+    if weights.shape != req_to_token.shape or req_pool_indices.numel() != B or new_lens.numel() != B:
+        raise ValueError("weights like req_to_token, req_pool_indices / seq_lens / new_lens [batch] expected")
+    if tuple(freed.shape) != (B, req_to_token.shape[1]):
+        raise ValueError("freed must be [batch, max_ctx]")
+    if error_word is not None:
+        _need(error_word, torch.int32, "error_word")
+    _one_device(req_to_token, req_pool_indices, seq_lens, weights, new_lens, freed, error_word)
+    _ok("pa_kv_evict", lib().pa_kv_evict(
+        _p(req_to_token), req_to_token.shape[0], req_to_token.shape[1], _p(req_pool_indices), _p(seq_lens), B,
+        _p(weights), int(budget), int(recent), _p(new_lens), _p(freed), _p(error_word), _stream(stream)))
 
 
 def pa_decode_step(q, k_new, v_new, positions, cos_tab, sin_tab, k_buf, v_buf, layer_id, loc, req_to_token,
@@ -373,6 +530,28 @@ def pa_paged_prefill_attn_fp8(q, k_buf, v_buf, layer_id, qo_indptr, kv_indptr, r
     _ok("pa_paged_prefill_attn_fp8", lib().pa_paged_prefill_attn_fp8(
         _p(q), T, Hq, _p(k_buf), _p(v_buf), s, layer_id, _p(qo_indptr), _p(kv_indptr), R, _p(req_to_token),
         req_to_token.shape[0], req_to_token.shape[1], _p(req_pool_indices), float(scale), _p(k_scale), _p(v_scale),
+        _p(workspace), workspace.numel(), _p(out), _stream(stream)))
+
+
+def pa_paged_prefill_attn_fp8_block(q, k_buf, v_buf, layer_id, qo_indptr, kv_indptr, req_to_token, req_pool_indices,
+                                    scale, k_exp, v_exp, block, workspace, out, stream=None):
+    """Ragged causal prefill over a block-scaled e4m3 cache."""
+    s = _kv_shape_block(k_buf, v_buf, k_exp, v_exp, block)
+    _need(q, torch.bfloat16, "q", 3)
+    _need(out, torch.bfloat16, "out", 3)
+    _need(qo_indptr, torch.int32, "qo_indptr", 1)
+    _need(kv_indptr, torch.int32, "kv_indptr", 1)
+    _need(req_to_token, torch.int32, "req_to_token", 2)
+    _need(req_pool_indices, torch.int32, "req_pool_indices", 1)
+    _need(workspace, torch.uint8, "workspace")
+    T, Hq, D = q.shape
+    R = qo_indptr.numel() - 1
+    if out.shape != q.shape or D != s.head_dim or kv_indptr.numel() != R + 1 or req_pool_indices.numel() != R:
+        raise ValueError("q/out [T, Hq, D], qo/kv_indptr [R+1], req_pool_indices [R] expected")
+    _one_device(q, k_buf, v_buf, qo_indptr, kv_indptr, req_to_token, req_pool_indices, k_exp, v_exp, workspace, out)
+    _ok("pa_paged_prefill_attn_fp8_block", lib().pa_paged_prefill_attn_fp8_block(
+        _p(q), T, Hq, _p(k_buf), _p(v_buf), s, layer_id, _p(qo_indptr), _p(kv_indptr), R, _p(req_to_token),
+        req_to_token.shape[0], req_to_token.shape[1], _p(req_pool_indices), float(scale), _p(k_exp), _p(v_exp), block,
         _p(workspace), workspace.numel(), _p(out), _stream(stream)))
 
 

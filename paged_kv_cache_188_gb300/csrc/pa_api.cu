@@ -105,6 +105,16 @@ bool encode_tmap_u8(CUtensorMap *m, const void *ptr, int rank, const cuuint64_t 
                        box);
 }
 
+bool encode_tmap_rows(CUtensorMap *m, const void *ptr, bool bf16, cuuint64_t inner, cuuint64_t rows,
+                      cuuint32_t box_inner, cuuint32_t box_rows, int swizzle_bytes)
+{
+    const cuuint64_t dims[2] = {inner, rows}, strides[1] = {inner * (bf16 ? 2 : 1)};
+    const cuuint32_t box[2] = {box_inner, box_rows};
+    return encode_tmap(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8,
+                       swizzle_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, ptr, 2, dims,
+                       strides, box);
+}
+
 DecodeWsLayout decode_ws_layout(size_t workspace_bytes, int n_q_heads, int n_kv_heads, int head_dim,
                                 int max_splits)
 {

@@ -163,6 +163,14 @@ __device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t two)
     return pack_bf16x2(__half2float(__half(lo)), __half2float(__half(hi)));
 }
 
+// Product of two bf16x2 words.
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
 // bf16x2 word -> f16x2 word, each value clamped to the f16 range first (f16
 // holds bf16's 8 significant bits; magnitudes below 2^-14 lose low bits).
 __device__ __forceinline__ uint32_t bf16x2_to_f16x2_sat(uint32_t w)
@@ -185,6 +193,38 @@ __device__ __forceinline__ uint4 quant_e4m3x16(const float (&x)[16], float scale
         w[i] = (uint32_t)a | ((uint32_t)b << 16);
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Two fp32 values as e4m3 bytes (a in the low byte): nearest even, saturating
+// to +-448 (infinities too), NaN stays NaN.
+__device__ __forceinline__ uint32_t e4m3x2_of(float a, float b)
+{
+    return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+// Two e4m3 bytes (a in the low byte) as fp32, exact.
+__device__ __forceinline__ void e4m3x2_floats(uint32_t two, float &a, float &b)
+{
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(two & 0xFFFFu), __NV_E4M3);
+    const float2 f = __half22float2(__half2(h));
+    a = f.x;
+    b = f.y;
+}
+// Exponent byte of a block's scale: the smallest e in [1, 254] with
+// amax <= 448 * 2^(e - 127) (448 = 1.75 * 2^8), 0 for amax = 0.
+__device__ __forceinline__ int block_exponent(float amax)
+{
+    const uint32_t u = __float_as_uint(amax);
+    const int e = (int)(u >> 23) - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    return amax > 0.f ? max(e, 1) : 0;
+}
+
+__device__ __forceinline__ void st_shared_u8(uint32_t addr, uint32_t v)
+{
+    asm volatile("st.shared.u8 [%0], %1;\n" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void st_shared_u16(uint32_t addr, uint32_t v)
+{
+    asm volatile("{\n .reg .b16 h;\n cvt.u16.u32 h, %1;\n st.shared.b16 [%0], h;\n}\n" ::"r"(addr), "r"(v) : "memory");
 }
 
 // Rotate one interleaved bf16 pair (x0, x1) stored as a 32-bit word by the

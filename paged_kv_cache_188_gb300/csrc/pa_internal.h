@@ -22,6 +22,9 @@ inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 
 inline bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 inline bool aligned256(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
 
+// block sizes of a block-scaled cache: powers of two from 1 to 128
+inline bool block_ok(int block) { return block >= 1 && block <= 128 && (block & (block - 1)) == 0; }
+
 // SM count of the current device (cached per device; a property, not call state).
 int num_sms();
 
@@ -72,6 +75,11 @@ bool encode_tmap_bf16(CUtensorMap *m, const void *ptr, int rank, const cuuint64_
 // lands in the 128-byte XOR-swizzled layout.
 bool encode_tmap_u8(CUtensorMap *m, const void *ptr, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
                     const cuuint32_t *box, bool swizzle128 = false);
+
+// A 2-D map over rows of `inner` elements (bf16, or bytes), boxes of
+// box_inner x box_rows, swizzled in 128- or 64-byte rows.
+bool encode_tmap_rows(CUtensorMap *m, const void *ptr, bool bf16, cuuint64_t inner, cuuint64_t rows,
+                      cuuint32_t box_inner, cuuint32_t box_rows, int swizzle_bytes);
 
 // Decode workspace geometry, a pure function of its arguments.
 struct DecodeWsLayout {

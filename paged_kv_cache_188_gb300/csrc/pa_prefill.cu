@@ -78,7 +78,7 @@ constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, 0, 0);   // Q (K-major) x 
 // 128-byte aligned, so single-row boxes need that pitch): for D = 128 it lands
 // in the upper half of the bf16 stage it is widened into, where e4m3 row r
 // shares its 128 bytes with bf16 row r of half 1 and with nothing else.
-template <int D, bool F8 = false>
+template <int D, bool F8 = false, bool BLK = false>
 struct PfLayout {
     static constexpr int kHalves = D / 64;
     static constexpr int kOffQA = 0;
@@ -93,7 +93,9 @@ struct PfLayout {
     static constexpr int kOffMisc = kOffBar + 32 * 8;
     static constexpr int kOffRing = kOffMisc + 64;      // kRing work-item descriptions
     static constexpr int kOffStage = kOffMisc + 256;
-    static constexpr int kOffPref = kOffStage + 8 * kStageBytes;
+    // block-scaled cache: exponent bytes of K stages 0, 1 and V stages 0, 1
+    static constexpr int kOffExp = kOffStage + 8 * kStageBytes;
+    static constexpr int kOffPref = kOffExp + (BLK ? 4 * kPfKeys : 0);
     // tensor-memory columns: S_A | S_B | O_A | O_B
     static constexpr uint32_t kColOA = 256, kColOB = 256 + D;
     static constexpr uint32_t kIdescPV = idesc_bf16_f32(128, D, 0, 1);  // P (tensor memory) x V (MN-major)
@@ -119,6 +121,9 @@ struct PrefillParams {
     float scale_log2;
     const float *k_scale;      // fp8 mode: the layer's per-kv-head K / V scales [Hkv]
     const float *v_scale;
+    const uint8_t *k_exp;      // block-scaled e4m3 cache: the layer's exponents [n_blocks, Hkv]
+    const uint8_t *v_exp;
+    int block_shift;
     const __nv_bfloat16 *k_rows;   // bf16 K / V rows (row r at r * row_elems): the cp.async gather
     const __nv_bfloat16 *v_rows;
     int row_elems;
@@ -139,9 +144,11 @@ static_assert(N_BARS <= 32, "barrier area holds 32 barriers");
 // (c / 8) halves + r * 128 + ((c % 8) ^ (r % 8)) * 16).  D / 16 lanes share a
 // row, each widening one 16-byte chunk into two; every row's bytes are read
 // (and the warp synchronised) before any of its bf16 chunks is written, so
-// the in-place D = 128 layout is safe.  Exact: e4m3 values are bf16 numbers.
-template <int D>
-__device__ __forceinline__ void widen_e4m3_tile(uint32_t src, uint32_t dst, int lane)
+// the in-place D = 128 layout is safe.  Exact: e4m3 values are bf16 numbers,
+// and so are their products with a block-scaled row's power of two (BLK:
+// exps[r] is row r's exponent byte e, and e << 7 the bf16 number 2^(e - 127)).
+template <int D, bool BLK = false>
+__device__ __forceinline__ void widen_e4m3_tile(uint32_t src, uint32_t dst, int lane, const unsigned char *exps = nullptr)
 {
     constexpr int LPR = D / 16;     // lanes per row
     constexpr int RPP = 32 / LPR;   // rows per pass of the warp
@@ -156,13 +163,17 @@ __device__ __forceinline__ void widen_e4m3_tile(uint32_t src, uint32_t dst, int 
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int r = r0 + u * RPP + rr;
+            const uint32_t sc = BLK ? (uint32_t)exps[r] * 0x00800080u : 0u;
+            auto wide = [&](uint32_t two) -> uint32_t {
+                const uint32_t w = e4m3x2_to_bf16x2(two);
+                return BLK ? mul_bf16x2(w, sc) : w;
+            };
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const uint32_t a = half ? v[u].z : v[u].x, b = half ? v[u].w : v[u].y;
                 const int c = 2 * j + half;   // bf16 chunk: d = 8 c .. 8 c + 7
                 st_shared_v4(dst + (uint32_t)((c >> 3) * kHalf + r * 128 + (((c & 7) ^ (r & 7)) << 4)),
-                             e4m3x2_to_bf16x2(a), e4m3x2_to_bf16x2(a >> 16), e4m3x2_to_bf16x2(b),
-                             e4m3x2_to_bf16x2(b >> 16));
+                             wide(a), wide(a >> 16), wide(b), wide(b >> 16));
             }
         }
         __syncwarp();
@@ -206,11 +217,14 @@ __device__ __forceinline__ PfItem pf_item(const PrefillParams &p, const int *s_p
     return I;
 }
 
-template <int D, bool DENSE, bool LAST, bool F8>
+// F8: an e4m3 cache, with a scale per kv head or (BLK) per block of slots and
+// kv head.
+template <int D, bool DENSE, bool LAST, bool F8, bool BLK>
 __global__ void __launch_bounds__(F8 ? kPfThreadsF8 : kPfThreads, 1)
     paged_prefill_kernel(const __grid_constant__ PrefillParams p)
 {
-    using PL = PfLayout<D, F8>;
+    using PL = PfLayout<D, F8, BLK>;
+    static_assert(F8 || !BLK, "block scales belong to an e4m3 cache");
     constexpr int QH = PL::kHalves;   // 64-column halves of a q, K or V row
     constexpr int NT = F8 ? kPfThreadsF8 : kPfThreads;
     static_assert(!(F8 && (DENSE || LAST)), "the e4m3 mode is paged prefill only");
@@ -384,11 +398,49 @@ __global__ void __launch_bounds__(F8 ? kPfThreadsF8 : kPfThreads, 1)
                 }
             };
             if (I.ntiles > 0) load_raw(0);
+            // block scales: a tile's exponents hang on its table entries, so
+            // both run one tile further ahead (nraw is tile t + 1 on entry)
+            int traw[4] = {-1, -1, -1, -1}, exk[4] = {0, 0, 0, 0}, exv[4] = {0, 0, 0, 0};
+            auto load_exp = [&](const int (&r)[4]) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const bool in = r[e] >= 0 && r[e] < p.size;
+                    const int64_t at = in ? (int64_t)(r[e] >> p.block_shift) * p.Hkv + I.h : 0;
+                    exk[e] = in ? __ldcg(p.k_exp + at) : 0;
+                    exv[e] = in ? __ldcg(p.v_exp + at) : 0;
+                }
+            };
+            if constexpr (BLK) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) traw[e] = nraw[e];
+                load_exp(traw);
+                if (I.ntiles > 1) load_raw(1);
+            }
             for (int t = 0; t < I.ntiles; ++t, ++kt) {
                 const int st = kt & 1;
                 const uint32_t ph_prev = ((kt >> 1) - 1) & 1;
-                const int raw[4] = {nraw[0], nraw[1], nraw[2], nraw[3]};
-                if (t + 1 < I.ntiles) load_raw(t + 1);
+                const int raw[4] = {BLK ? traw[0] : nraw[0], BLK ? traw[1] : nraw[1], BLK ? traw[2] : nraw[2],
+                                    BLK ? traw[3] : nraw[3]};
+                const int ek[4] = {exk[0], exk[1], exk[2], exk[3]}, ev[4] = {exv[0], exv[1], exv[2], exv[3]};
+                if constexpr (BLK) {
+                    if (t + 1 < I.ntiles) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) traw[e] = nraw[e];
+                        load_exp(traw);
+                    }
+                    if (t + 2 < I.ntiles) load_raw(t + 2);
+                } else {
+                    if (t + 1 < I.ntiles) load_raw(t + 1);
+                }
+                // this lane's four exponent bytes into their stage, before the
+                // tile's barrier is armed
+                auto put_exps = [&](const int (&x)[4], int area) {
+                    if constexpr (BLK) {
+                        reinterpret_cast<uint32_t *>(sb + PL::kOffExp + area * kPfKeys)[lane] =
+                            (uint32_t)(x[0] | x[1] << 8 | x[2] << 16 | x[3] << 24);
+                        __syncwarp();
+                    }
+                };
                 // slots of positions k0 + 4*lane + e
                 const int k0 = t * kPfKeys;
                 int slot[4];
@@ -485,6 +537,7 @@ __global__ void __launch_bounds__(F8 ? kPfThreadsF8 : kPfThreads, 1)
                         __syncwarp();
                     }
                     ++nk;
+                    put_exps(ek, st);
                     if (lane == 0) mbar_arrive_expect_tx(bar(kb + st), tile_bytes);
                     __syncwarp();
                     issue(&p.tm_k16, &p.tm_k1, F8 ? raw_tile(false, st) : sK + st * QH * kHalf, bar(kb + st));
@@ -501,6 +554,7 @@ __global__ void __launch_bounds__(F8 ? kPfThreadsF8 : kPfThreads, 1)
                         __syncwarp();
                     }
                     ++nv;
+                    put_exps(ev, 2 + st);
                     if (lane == 0) mbar_arrive_expect_tx(bar(vb + st), tile_bytes);
                     __syncwarp();
                     issue(&p.tm_v16, &p.tm_v1, F8 ? raw_tile(true, st) : sV + st * QH * kHalf, bar(vb + st));
@@ -542,7 +596,8 @@ __global__ void __launch_bounds__(F8 ? kPfThreadsF8 : kPfThreads, 1)
                     ok = false;
                     break;
                 }
-                widen_e4m3_tile<D>(raw_tile(isv, st), (isv ? sV : sK) + st * QH * kHalf, lane);
+                widen_e4m3_tile<D, BLK>(raw_tile(isv, st), (isv ? sV : sK) + st * QH * kHalf, lane,
+                                        BLK ? sb + PL::kOffExp + ((isv ? 2 : 0) + st) * kPfKeys : nullptr);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar((isv ? V_FULL : K_FULL) + st));
@@ -695,7 +750,7 @@ __global__ void __launch_bounds__(F8 ? kPfThreadsF8 : kPfThreads, 1)
             const int nq = X ? I.nqb : I.nqa;
             if (nq <= 0) continue;                // no tile B in this pair
             const int q0 = I.q0 + X * p.TQ;
-            if constexpr (F8) sl2 = p.scale_log2 * __ldg(p.k_scale + I.h);   // the head's K scale joins the softmax scale
+            if constexpr (F8 && !BLK) sl2 = p.scale_log2 * __ldg(p.k_scale + I.h);   // the head's K scale joins the softmax scale
             const int tok = row / G;              // token of this row within the tile
             const int qpos = I.p + q0 + tok;      // its position in the request
             float m_run = -INFINITY, l_run = 0.f;
@@ -788,7 +843,7 @@ __global__ void __launch_bounds__(F8 ? kPfThreadsF8 : kPfThreads, 1)
             tc_fence_before();
             mbar_arrive(bar(b_o_empty));          // O_X is in registers: the next item may overwrite it
             // fp8: the head's V scale multiplies the normalised output
-            const float inv_l = l_run > 0.f ? (F8 ? __ldg(p.v_scale + I.h) : 1.f) / l_run : 0.f;
+            const float inv_l = l_run > 0.f ? (F8 && !BLK ? __ldg(p.v_scale + I.h) : 1.f) / l_run : 0.f;
             uint32_t ob[D / 2];                   // O / l as bf16 pairs
 #pragma unroll
             for (int c = 0; c < D / 2; ++c)
@@ -849,11 +904,11 @@ using namespace pa;
 
 namespace pa {
 
-template <int D, bool DENSE, bool LAST, bool F8 = false>
+template <int D, bool DENSE, bool LAST, bool F8 = false, bool BLK = false>
 static pa_status launch_prefill(const PrefillParams &prm, cudaStream_t st)
 {
-    auto kern = paged_prefill_kernel<D, DENSE, LAST, F8>;
-    const size_t smem = (size_t)PfLayout<D, F8>::kOffPref + (size_t)(prm.R + 1) * 4 + 1024;
+    auto kern = paged_prefill_kernel<D, DENSE, LAST, F8, BLK>;
+    const size_t smem = (size_t)PfLayout<D, F8, BLK>::kOffPref + (size_t)(prm.R + 1) * 4 + 1024;
     if (!ensure_dynamic_smem(reinterpret_cast<const void *>(kern), smem)) return PA_ERR_CUDA;
     if (launch_kernel(kern, dim3(num_sms()), dim3(F8 ? kPfThreadsF8 : kPfThreads), smem, st, prm) != cudaSuccess)
         return PA_ERR_CUDA;
@@ -861,12 +916,14 @@ static pa_status launch_prefill(const PrefillParams &prm, cudaStream_t st)
 }
 static_assert(PfLayout<128>::kOffPref + (kPfMaxReqs + 1) * 4 + 1024 <= 232448, "bf16 prefill smem");
 static_assert(PfLayout<128, true>::kOffPref + (kPfMaxReqs + 1) * 4 + 1024 <= 232448, "fp8 prefill smem");
+static_assert(PfLayout<128, true, true>::kOffPref + (kPfMaxReqs + 1) * 4 + 1024 <= 232448, "block-scaled prefill smem");
+static_assert(PfLayout<64, true, true>::kOffPref + (kPfMaxReqs + 1) * 4 + 1024 <= 232448, "block-scaled prefill smem, D = 64");
 static_assert(PfLayout<64, true>::kOffPref + (kPfMaxReqs + 1) * 4 + 1024 <= 232448, "fp8 prefill smem, D = 64");
 
 // Shared host path of the paged and dense entry points.  Paged: K/V rows are
 // slots of layer `layer_id` of [n_layers, size, Hkv, D] buffers, reached
 // through req_to_token (bf16, or e4m3 bytes with per-kv-head scales when
-// k_scale != NULL).  Dense: K/V are the packed new tokens' rows
+// k_scale != NULL, per-block exponents when k_exp != NULL).  Dense: K/V are the packed new tokens' rows
 // [n_tokens, Hkv, D] (no prefix: kv length = query length).
 static pa_status prefill_call(const void *q, int n_tokens, int n_q_heads, const void *k_rows, const void *v_rows,
                               int n_kv_heads, int D, int64_t total_rows, int layer_row0, int size,
@@ -874,11 +931,12 @@ static pa_status prefill_call(const void *q, int n_tokens, int n_q_heads, const 
                               const int32_t *req_to_token, int req_rows, int max_ctx,
                               const int32_t *req_pool_indices, float scale, void *workspace, size_t workspace_bytes,
                               void *out, void *last_out, bool dense, cudaStream_t st,
-                              const float *k_scale = nullptr, const float *v_scale = nullptr)
+                              const float *k_scale = nullptr, const float *v_scale = nullptr,
+                              const uint8_t *k_exp = nullptr, const uint8_t *v_exp = nullptr, int block = 1)
 {
     PrefillParams prm;
     memset(&prm, 0, sizeof prm);
-    const bool f8 = k_scale != nullptr;
+    const bool f8 = k_scale != nullptr || k_exp != nullptr;
     const int G = n_q_heads / n_kv_heads;
     const int TQ = kPfRows / G;
     {
@@ -930,11 +988,15 @@ static pa_status prefill_call(const void *q, int n_tokens, int n_q_heads, const 
     prm.early_meta = early_metadata();
     prm.k_scale = k_scale;
     prm.v_scale = v_scale;
+    prm.k_exp = k_exp;
+    prm.v_exp = v_exp;
+    while ((1 << prm.block_shift) < block) ++prm.block_shift;
     prm.k_rows = static_cast<const __nv_bfloat16 *>(k_rows);
     prm.v_rows = static_cast<const __nv_bfloat16 *>(v_rows);
     prm.row_elems = n_kv_heads * D;
     prm.wait_ns = wait_limit_ns();
 
+    if (k_exp) return D == 64 ? launch_prefill<64, false, false, true, true>(prm, st) : launch_prefill<128, false, false, true, true>(prm, st);
     if (f8) return D == 64 ? launch_prefill<64, false, false, true>(prm, st) : launch_prefill<128, false, false, true>(prm, st);
     if (D == 64) {
         if (dense) return last_out ? launch_prefill<64, true, true>(prm, st) : launch_prefill<64, true, false>(prm, st);
@@ -1032,6 +1094,27 @@ extern "C" pa_status pa_paged_prefill_attn_fp8(const void *q, int n_tokens, int 
                         layer_id * s.size, s.size, qo_indptr, kv_indptr, n_reqs, req_to_token, req_rows, max_ctx,
                         req_pool_indices, scale, workspace, workspace_bytes, out, nullptr, false, st,
                         k_scale + sc_off, v_scale + sc_off);
+}
+
+extern "C" pa_status pa_paged_prefill_attn_fp8_block(const void *q, int n_tokens, int n_q_heads, const void *k_buf,
+                                                     const void *v_buf, pa_kv_shape s, int layer_id,
+                                                     const int32_t *qo_indptr, const int32_t *kv_indptr, int n_reqs,
+                                                     const int32_t *req_to_token, int req_rows, int max_ctx,
+                                                     const int32_t *req_pool_indices, float scale, const uint8_t *k_exp,
+                                                     const uint8_t *v_exp, int block, void *workspace,
+                                                     size_t workspace_bytes, void *out, cudaStream_t st)
+{
+    if (!block_ok(block)) return PA_ERR_SHAPE;
+    pa_status rc = check_paged(q, n_tokens, n_q_heads, k_buf, v_buf, s, layer_id, qo_indptr, kv_indptr, n_reqs,
+                               req_to_token, req_rows, max_ctx, req_pool_indices, workspace, workspace_bytes, out,
+                               nullptr);
+    if (rc != PA_OK || n_tokens == 0 || n_reqs == 0) return rc;
+    if (!k_exp || !v_exp) return PA_ERR_NULL;
+    const int64_t off = (int64_t)layer_id * ((s.size + block - 1) / block) * s.n_kv_heads;   // the layer's exponents
+    return prefill_call(q, n_tokens, n_q_heads, k_buf, v_buf, s.n_kv_heads, s.head_dim, (int64_t)s.n_layers * s.size,
+                        layer_id * s.size, s.size, qo_indptr, kv_indptr, n_reqs, req_to_token, req_rows, max_ctx,
+                        req_pool_indices, scale, workspace, workspace_bytes, out, nullptr, false, st, nullptr, nullptr,
+                        k_exp + off, v_exp + off, block);
 }
 
 extern "C" pa_status pa_dense_prefill_attn(const void *q, int n_tokens, int n_q_heads, const void *k, const void *v,
