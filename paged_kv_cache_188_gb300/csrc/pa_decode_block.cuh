@@ -35,8 +35,9 @@
 // Work: every (kv head, request) is a segment of 128-token tiles (at least
 // one), laid end to end head-major; CTA c takes tiles [c W, (c + 1) W).  A CTA
 // has at most two segments it shares with others, its first and its last, so
-// the fp32 partials are two slots per CTA whatever the batch is; a second
-// kernel merges them in CTA order (deterministic) and adds the weights.
+// the fp32 partials are two slots per CTA whatever the batch is.  The CTA that
+// finishes a shared segment's last piece (a ticket per segment) merges its
+// pieces in CTA order (deterministic); a second kernel adds the weights (WT).
 //
 // Roles: two warpgroups take the tiles in turn (softmax of one beside the
 // products of the other), each issuing its own MMAs; warp 8 loads K tiles and
@@ -68,9 +69,10 @@ struct BlkArgs {
     const uint8_t *k_exp, *v_exp;               // the layer's [n_blocks, Hkv] (e4m3 cache)
     __nv_bfloat16 *out;
     int32_t *err;
+    int32_t *tickets;                           // [CTAs]: finished pieces of the shared segment that starts in that CTA
     float *ml_part;                             // [2 CTAs][G][2]: maximum (log2 units), sum
     float *o_part;                              // [2 CTAs][G][D]: relative to that maximum
-    float *lse;                                 // [batch, Hq]: log2-sum-exp of unsplit segments (WT)
+    float *lse;                                 // [batch, Hq]: log2-sum-exp (WT)
     float *scores;                              // [Hkv][cap_tiles][128][G], log2 units (WT)
     float *weights;                             // [req_rows, max_ctx] (WT)
     int batch, Hq, Hkv, G, size, req_rows, max_ctx, layer_row0, block_shift, stages, cap_tiles, early_meta, grid;
@@ -232,16 +234,21 @@ __device__ __forceinline__ int blk_width(const int *s_pref, int B, int Hkv, int 
 
 // ------------------------------------------------------------------ loader
 // K (isv false) or V rows and exponents of every tile of the CTA, in order.
-// The next tile's exponents and the one after's table entries are requested
-// while a tile's copies are issued.
+// Table entries and exponents come through registers in batches of kBlkAhead
+// tiles: a batch's table entries are requested while the batch before it is
+// copied, its exponents (which hang on them) half a batch later, so a tile's
+// copies wait for neither round trip.
+constexpr int kBlkAhead = 4;
+
 template <int D, bool E8, int GP>
 __device__ __forceinline__ void blk_loader(const BlkArgs &a, const int *s_pref, int W, uint32_t ring, unsigned char *meta,
                                            uint32_t full, uint32_t empty, volatile int *s_abort, bool isv, int lane)
 {
     using C = BlkCfg<D, E8, GP>;
     struct Tile {
-        int h, n, p0, row;      // kv head, tokens of the request, first position, table row (-1: no more tiles)
-        int slot[4];
+        int h, n, p0;           // kv head, tokens of the request (0: no more tiles), first position
+        int slot[4];            // table entries of positions p0 + 4 lane + e
+        int ex[4];              // exponent bytes
     };
     const CUtensorMap *m16 = isv ? &a.tm_v16 : &a.tm_k16, *m1 = isv ? &a.tm_v1 : &a.tm_k1;
     const uint8_t *exps = isv ? a.v_exp : a.k_exp;
@@ -255,53 +262,45 @@ __device__ __forceinline__ void blk_loader(const BlkArgs &a, const int *s_pref, 
             more = blk_piece(a, s_pref, k);
             i = 0;
         }
-        t.row = -1;
-        t.n = 0;
-        t.p0 = 0;
-        t.h = 0;
+        t.n = t.p0 = t.h = 0;
+        int64_t row = 0;
         if (more) {
-            t.row = k.row;
+            row = k.row;
             t.h = k.h;
             t.n = k.n;
             t.p0 = (k.t0 + i) * kBlkTile;
             ++i;
         }
+        const int32_t *src = a.req_to_token + row * a.max_ctx;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int p = t.p0 + 4 * lane + e;
-            t.slot[e] = ld_nc_ordered_s32_if(p < t.n, a.req_to_token + (int64_t)max(t.row, 0) * a.max_ctx + (p < t.n ? p : 0));
+            t.slot[e] = ld_nc_ordered_s32_if(p < t.n, src + (p < t.n ? p : 0));
         }
     };
-    int ex[4], exn[4];
-    auto load_exps = [&](const Tile &t, int (&x)[4]) {
+    auto load_exps = [&](Tile &t) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const bool ok = t.slot[e] >= 0 && t.slot[e] < a.size;
-            x[e] = !ok ? kMasked : !E8 ? 0 : __ldcg(exps + (int64_t)(t.slot[e] >> a.block_shift) * a.Hkv + t.h);
+            t.ex[e] = !ok ? kMasked : !E8 ? 0 : __ldcg(exps + (int64_t)(t.slot[e] >> a.block_shift) * a.Hkv + t.h);
         }
     };
-    Tile cur, nxt;
-    fetch(cur);
-    fetch(nxt);
-    load_exps(cur, ex);
     int st = 0, issued = 0;
     uint32_t ph = 0;
-    while (cur.row >= 0) {
-        Tile after;
-        fetch(after);
-        load_exps(nxt, exn);
+    // copies of one tile; false if the wait for its stage timed out
+    auto put = [&](const Tile &c) -> bool {
         // the stage's previous tile has been multiplied
         if (issued >= a.stages &&
             !__all_sync(0xffffffffu, mbar_wait(empty + st * 8, ph ^ 1, s_abort, a.err, PA_DEVERR_TIMEOUT, a.wait_ns)))
-            break;
+            return false;
         const uint32_t dst = ring + st * C::STAGE + (isv ? C::TILE : 0), fb = full + st * 8;
         bool ok[4];
         int sl[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            sl[e] = cur.slot[e];
+            sl[e] = c.slot[e];
             ok[e] = sl[e] >= 0 && sl[e] < a.size;
-            if (!ok[e] && cur.p0 + 4 * lane + e < cur.n) errs |= PA_DEVERR_SLOT;
+            if (!ok[e] && c.p0 + 4 * lane + e < c.n) errs |= PA_DEVERR_SLOT;
         }
         const int mine = ok[0] ? sl[0] : ok[1] ? sl[1] : ok[2] ? sl[2] : ok[3] ? sl[3] : -1;
         const unsigned has = __ballot_sync(0xffffffffu, mine >= 0);
@@ -313,7 +312,7 @@ __device__ __forceinline__ void blk_loader(const BlkArgs &a, const int *s_pref, 
         if (has) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) sl[e] = a.layer_row0 + (ok[e] ? sl[e] : some);
-            const int col = cur.h * D;
+            const int col = c.h * D;
             if (page) {
                 if ((lane & 3) == 0) {
 #pragma unroll
@@ -332,7 +331,7 @@ __device__ __forceinline__ void blk_loader(const BlkArgs &a, const int *s_pref, 
             fence_proxy_async_smem();
         }
         reinterpret_cast<uint32_t *>(meta + ((isv ? kBlkMaxStages : 0) + st) * kBlkTile)[lane] =
-            (uint32_t)(ex[0] | ex[1] << 8 | ex[2] << 16 | ex[3] << 24);
+            (uint32_t)(c.ex[0] | c.ex[1] << 8 | c.ex[2] << 16 | c.ex[3] << 24);
         __syncwarp();
         if (lane == 0) mbar_arrive_expect_tx(fb, has ? C::TILE : 0u);
         ++issued;
@@ -340,10 +339,27 @@ __device__ __forceinline__ void blk_loader(const BlkArgs &a, const int *s_pref, 
             st = 0;
             ph ^= 1;
         }
-        cur = nxt;
-        nxt = after;
+        return true;
+    };
+    Tile cur[kBlkAhead], nxt[kBlkAhead];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) ex[e] = exn[e];
+    for (int u = 0; u < kBlkAhead; ++u) fetch(cur[u]);
+#pragma unroll
+    for (int u = 0; u < kBlkAhead; ++u) load_exps(cur[u]);
+    bool go = true;
+    while (go) {
+#pragma unroll
+        for (int u = 0; u < kBlkAhead; ++u) fetch(nxt[u]);
+#pragma unroll
+        for (int u = 0; u < kBlkAhead; ++u) {
+            if (u == kBlkAhead / 2) {
+#pragma unroll
+                for (int w = 0; w < kBlkAhead; ++w) load_exps(nxt[w]);
+            }
+            if (go) go = cur[u].n > 0 && put(cur[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kBlkAhead; ++u) cur[u] = nxt[u];
     }
     if (*s_abort) {
         // aborted: the copies already issued land before the shared memory goes away
@@ -351,6 +367,68 @@ __device__ __forceinline__ void blk_loader(const BlkArgs &a, const int *s_pref, 
     }
     if (errs) set_error(a.err, errs);
     __syncwarp();
+}
+
+// Pieces of segment (b, h): CTAs c0 .. c1; a piece that does not start its
+// CTA's range is that CTA's last (slot 1).
+struct BlkSpan {
+    int c0, c1, S0;
+};
+__device__ __forceinline__ BlkSpan blk_span(const int *s_pref, int B, int W, int b, int h)
+{
+    BlkSpan s;
+    s.S0 = h * s_pref[B] + s_pref[b];
+    s.c0 = s.S0 / W;
+    s.c1 = (s.S0 + s_pref[b + 1] - s_pref[b] - 1) / W;
+    return s;
+}
+__device__ __forceinline__ int blk_slot(const BlkSpan &s, int c, int W) { return 2 * c + (s.S0 > c * W ? 1 : 0); }
+
+// Merge of a shared segment by the CTA that finished its last piece: every
+// element summed in CTA order.  All consumer threads; a warp's elements belong
+// to one head.  The first pieces' partials are requested before the (m, l)
+// pairs (ordered loads: one round trip for both).
+template <int D, int GP, bool WT>
+__device__ __forceinline__ void blk_merge(const BlkArgs &a, const BlkSpan &s, int W, int b, int h)
+{
+    constexpr int SB = 16;
+    const int tid = threadIdx.x, lane = tid & 31, G = a.G, np = s.c1 - s.c0 + 1;
+    // piece p of the segment: its partials' slot
+    auto slot = [&](int p) { return blk_slot(s, s.c0 + p, W); };
+    for (int e = tid; e < G * D; e += kBlkConsumers) {
+        const int g = e / D;
+        float v[SB];
+#pragma unroll
+        for (int p = 0; p < SB; ++p) v[p] = ld_cg_ordered_if(p < np, a.o_part + ((int64_t)slot(min(p, np - 1)) * G * D + e));
+        float M = -INFINITY;
+        for (int p0 = 0; p0 < np; p0 += 32) {
+            const int p = p0 + lane;
+            M = fmaxf(M, p < np ? __ldcg(a.ml_part + (slot(p) * G + g) * 2) : -INFINITY);
+        }
+        M = warp_max(M);
+        const float Mz = M == -INFINITY ? 0.f : M;
+        float L = 0.f, O = 0.f;
+        for (int p0 = 0; p0 < np; p0 += 32) {
+            const int p = p0 + lane;
+            float w = 0.f, l = 0.f;
+            if (p < np) {
+                w = blk_ex2(__ldcg(a.ml_part + (slot(p) * G + g) * 2) - Mz);
+                l = w * __ldcg(a.ml_part + (slot(p) * G + g) * 2 + 1);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+            L += l;
+            if (p0 == 0) {
+#pragma unroll
+                for (int q = 0; q < SB; ++q) O += __shfl_sync(0xffffffffu, w, q) * v[q];
+            }
+            for (int q = p0 == 0 ? SB : 0; q < 32 && p0 + q < np; ++q)
+                O += __shfl_sync(0xffffffffu, w, q) * __ldcg(a.o_part + ((int64_t)slot(p0 + q) * G * D + e));
+        }
+        const int64_t hq = (int64_t)b * a.Hq + h * G + g;
+        a.out[hq * D + (e - g * D)] = __float2bfloat16_rn(L != 0.f ? O / L : 0.f);
+        if (WT && e == g * D) a.lse[hq] = L != 0.f ? M + log2f(L) : INFINITY;
+    }
 }
 
 // ------------------------------------------------------------------ kernel
@@ -363,6 +441,7 @@ __global__ void __launch_bounds__(kBlkThreads, 1) decode_block_kernel(const __gr
     __shared__ int s_w[kBlkThreads / 32];
     __shared__ int s_abort_storage;
     __shared__ uint32_t s_tmem;
+    __shared__ int s_last[2];
     const uint32_t raw = smem_u32(smem_raw), ring = (raw + 1023u) & ~1023u;
     unsigned char *base = smem_raw + (ring - raw) + (size_t)a.stages * C::STAGE;
     volatile int *s_abort = &s_abort_storage;
@@ -428,6 +507,8 @@ __global__ void __launch_bounds__(kBlkThreads, 1) decode_block_kernel(const __gr
         auto wait = [&](uint32_t bar, uint32_t parity) {
             if (!bad) bad = !__all_sync(0xffffffffu, mbar_wait(bar, parity, s_abort, a.err, PA_DEVERR_TIMEOUT, a.wait_ns));
         };
+        int shared_b[2], shared_h[2], shared = 0;   // segments of which this CTA has a piece: at most two
+        int ticket[2];
         BlkWalk k = blk_begin(s_pref, a.batch, a.Hkv, W, blockIdx.x);
         for (; blk_piece(a, s_pref, k); blk_next(a, k)) {
             if (a.wait_ns == 0 && !bad) {
@@ -652,8 +733,8 @@ __global__ void __launch_bounds__(kBlkThreads, 1) decode_block_kernel(const __gr
                 }
             }
             named_bar_sync(3, kBlkConsumers);
+            const bool whole = k.t0 == 0 && k.t1 == k.tb;
             if (wg == 0 && t < D && !bad) {
-                const bool whole = k.t0 == 0 && k.t1 == k.tb;
                 const int part = (int)blockIdx.x * 2 + (k.t0 == 0 && k.S0 > (int)blockIdx.x * W ? 1 : 0);
 #pragma unroll
                 for (int g = 0; g < GP; ++g) {
@@ -675,6 +756,33 @@ __global__ void __launch_bounds__(kBlkThreads, 1) decode_block_kernel(const __gr
                     }
                 }
             }
+            if (!whole) {
+                // a ticket for the piece: the barrier orders the partials' stores before thread 0's acquire-release
+                // addition; the answer is looked at after the CTA's last piece
+                if (wg == 0) {
+                    named_bar_sync(1, 128);
+                    if (t == 0 && !bad) {
+                        const int old = atom_add_acq_rel_gpu(a.tickets + k.S0 / W, 1);
+                        if (shared == 0) ticket[0] = old;
+                        else ticket[1] = old;
+                    }
+                }
+                if (shared == 0) shared_b[0] = k.b, shared_h[0] = k.h;
+                else shared_b[1] = k.b, shared_h[1] = k.h;
+                ++shared;
+            }
+        }
+        // shared segments whose last piece was this CTA's
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (i >= shared) break;
+            const BlkSpan s = blk_span(s_pref, a.batch, W, shared_b[i], shared_h[i]);
+            if (tid == 0) s_last[i] = !bad && ticket[i] == s.c1 - s.c0;
+            named_bar_sync(3, kBlkConsumers);
+            if (s_last[i]) {
+                blk_merge<D, GP, WT>(a, s, W, shared_b[i], shared_h[i]);
+                if (tid == 0) a.tickets[s.c0] = 0;
+            }
         }
         if (__any_sync(0xffffffffu, *s_abort) && (warp & 3) == 0) {
             // aborted: every MMA this lane issued completes before tensor memory is freed
@@ -691,103 +799,48 @@ __global__ void __launch_bounds__(kBlkThreads, 1) decode_block_kernel(const __gr
     }
 }
 
-// ------------------------------------------------------- merge and weights
-// Pieces of segment (b, h): CTAs c0 .. c1; a piece that does not start its
-// CTA's range is that CTA's last (slot 1).
-struct BlkSpan {
-    int c0, c1, S0;
-};
-__device__ __forceinline__ BlkSpan blk_span(const int *s_pref, int B, int W, int b, int h)
-{
-    BlkSpan s;
-    s.S0 = h * s_pref[B] + s_pref[b];
-    s.c0 = s.S0 / W;
-    s.c1 = (s.S0 + s_pref[b + 1] - s_pref[b] - 1) / W;
-    return s;
-}
-__device__ __forceinline__ int blk_slot(const BlkSpan &s, int c, int W) { return 2 * c + (s.S0 > c * W ? 1 : 0); }
+// ---------------------------------------------------------------- weights
+constexpr int kBlkWeightThreads = 128;
 
-constexpr int kBlkMergeThreads = 128;
-
-// Blocks take (request, kv head) pairs of more than one piece, then (WT)
-// 128-token tiles of the requests' weights.  Pieces are summed in CTA order.
-template <int D, bool WT>
-__global__ void __launch_bounds__(kBlkMergeThreads) decode_block_merge_kernel(const __grid_constant__ BlkArgs a)
+// weights[row, j] += sum over the heads of 2^(score - lse), one 128-token tile
+// of a request at a time, heads in order.
+static __global__ void __launch_bounds__(kBlkWeightThreads) decode_block_weights_kernel(const __grid_constant__ BlkArgs a)
 {
-    extern __shared__ int s_pref[];                 // [batch + 1], then (WT) float [Hq]
-    __shared__ int s_w[kBlkMergeThreads / 32];
+    extern __shared__ int s_pref[];                 // [batch + 1], then float [Hq]
+    __shared__ int s_w[kBlkWeightThreads / 32];
     const int tid = threadIdx.x, B = a.batch, G = a.G;
+    float *s_lse = reinterpret_cast<float *>(s_pref + B + 1);
     if (!a.early_meta) pdl_wait();
-    blk_plan<kBlkMergeThreads>(a, s_pref, s_w);
+    blk_plan<kBlkWeightThreads>(a, s_pref, s_w);
     if (a.early_meta) pdl_wait();
     pdl_launch_dependents();
-    const int W = blk_width(s_pref, B, a.Hkv, a.grid);
-    const int pairs = B * a.Hkv, tiles = WT ? s_pref[B] : 0;
-    for (int p = blockIdx.x; p < pairs; p += gridDim.x) {
-        const int b = p / a.Hkv, h = p - b * a.Hkv;
-        const BlkSpan s = blk_span(s_pref, B, W, b, h);
-        if (s.c0 == s.c1) continue;
-        for (int e = tid; e < G * D; e += kBlkMergeThreads) {
-            const int g = e / D;
-            float M = -INFINITY;
-            for (int c = s.c0; c <= s.c1; ++c) M = fmaxf(M, __ldcg(a.ml_part + (blk_slot(s, c, W) * G + g) * 2));
-            const float Mz = M == -INFINITY ? 0.f : M;
-            float L = 0.f, O = 0.f;
-            for (int c = s.c0; c <= s.c1; ++c) {
-                const int sl = blk_slot(s, c, W);
-                const float w = blk_ex2(__ldcg(a.ml_part + (sl * G + g) * 2) - Mz);
-                L += w * __ldcg(a.ml_part + (sl * G + g) * 2 + 1);
-                O += w * __ldcg(a.o_part + (int64_t)sl * G * D + e);
-            }
-            a.out[((int64_t)b * a.Hq + h * G) * D + e] = __float2bfloat16_rn(L != 0.f ? O / L : 0.f);
+    const int tiles = s_pref[B];
+    for (int x = blockIdx.x; x < tiles; x += gridDim.x) {
+        int lo = 0, hi = B;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (s_pref[mid] <= x) lo = mid; else hi = mid;
         }
-    }
-    if constexpr (WT) {
-        float *s_lse = reinterpret_cast<float *>(s_pref + B + 1);
-        for (int x = blockIdx.x; x < tiles; x += gridDim.x) {
-            int lo = 0, hi = B;
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (s_pref[mid] <= x) lo = mid; else hi = mid;
+        const int b = lo, n = blk_len(a, b), row = __ldg(a.req_pool_indices + b);
+        // two requests of a row would both add to it: the later one is refused
+        int again = 0;
+        for (int c = tid; c < b; c += kBlkWeightThreads) again |= __ldg(a.req_pool_indices + c) == row;
+        __syncthreads();   // s_lse is free
+        for (int hq = tid; hq < a.Hq; hq += kBlkWeightThreads) s_lse[hq] = __ldcg(a.lse + (int64_t)b * a.Hq + hq);
+        again = __syncthreads_or(again);
+        if (n <= 0) continue;
+        if (again || x >= a.cap_tiles) {
+            if (tid == 0) set_error(a.err, again ? PA_DEVERR_ROW : PA_DEVERR_LEN);
+            continue;
+        }
+        const int j = (x - s_pref[b]) * kBlkTile + tid;
+        if (j < n) {
+            float w = 0.f;
+            for (int h = 0; h < a.Hkv; ++h) {
+                const float *sc = a.scores + (((int64_t)h * a.cap_tiles + x) * kBlkTile + tid) * G;
+                for (int g = 0; g < G; ++g) w += blk_ex2(__ldcg(sc + g) - s_lse[h * G + g]);
             }
-            const int b = lo, n = blk_len(a, b), row = __ldg(a.req_pool_indices + b);
-            // two requests of a row would both add to it: the later one is refused
-            int again = 0;
-            for (int c = tid; c < b; c += kBlkMergeThreads) again |= __ldg(a.req_pool_indices + c) == row;
-            __syncthreads();   // s_lse is free
-            for (int hq = tid; hq < a.Hq; hq += kBlkMergeThreads) {
-                const int h = hq / G, g = hq - h * G;
-                const BlkSpan s = blk_span(s_pref, B, W, b, h);
-                float lse;
-                if (s.c0 == s.c1) {
-                    lse = __ldcg(a.lse + (int64_t)b * a.Hq + hq);
-                } else {
-                    float M = -INFINITY, L = 0.f;
-                    for (int c = s.c0; c <= s.c1; ++c) M = fmaxf(M, __ldcg(a.ml_part + (blk_slot(s, c, W) * G + g) * 2));
-                    const float Mz = M == -INFINITY ? 0.f : M;
-                    for (int c = s.c0; c <= s.c1; ++c) {
-                        const float *ml = a.ml_part + (blk_slot(s, c, W) * G + g) * 2;
-                        L += blk_ex2(__ldcg(ml) - Mz) * __ldcg(ml + 1);
-                    }
-                    lse = L != 0.f ? M + log2f(L) : INFINITY;
-                }
-                s_lse[hq] = lse;
-            }
-            again = __syncthreads_or(again);
-            if (n <= 0) continue;
-            if (again || x >= a.cap_tiles) {
-                if (tid == 0) set_error(a.err, again ? PA_DEVERR_ROW : PA_DEVERR_LEN);
-                continue;
-            }
-            const int j = (x - s_pref[b]) * kBlkTile + tid;
-            if (j < n) {
-                float w = 0.f;
-                for (int h = 0; h < a.Hkv; ++h) {
-                    const float *sc = a.scores + (((int64_t)h * a.cap_tiles + x) * kBlkTile + tid) * G;
-                    for (int g = 0; g < G; ++g) w += blk_ex2(__ldcg(sc + g) - s_lse[h * G + g]);
-                }
-                a.weights[(int64_t)row * a.max_ctx + j] += w;
-            }
+            a.weights[(int64_t)row * a.max_ctx + j] += w;
         }
     }
 }
@@ -804,12 +857,12 @@ static pa_status launch_block(BlkArgs a, cudaStream_t st)
     if (!ensure_dynamic_smem(reinterpret_cast<const void *>(kern), smem)) return PA_ERR_CUDA;
     a.grid = num_sms() < kBlkMaxCtas ? num_sms() : kBlkMaxCtas;
     if (launch_kernel(kern, dim3(a.grid), dim3(kBlkThreads), smem, st, a) != cudaSuccess) return PA_ERR_CUDA;
-    auto merge = decode_block_merge_kernel<D, WT>;
-    const size_t msmem = ((size_t)a.batch + 1) * 4 + (WT ? (size_t)a.Hq * 4 : 0);
-    const int pairs = a.batch * a.Hkv;
-    const int mgrid = WT ? 4 * a.grid : (pairs < 8 * a.grid ? pairs : 8 * a.grid);
-    if (!ensure_dynamic_smem(reinterpret_cast<const void *>(merge), msmem)) return PA_ERR_CUDA;
-    if (launch_kernel(merge, dim3(mgrid), dim3(kBlkMergeThreads), msmem, st, a) != cudaSuccess) return PA_ERR_CUDA;
+    if constexpr (WT) {
+        const size_t wsmem = ((size_t)a.batch + 1) * 4 + (size_t)a.Hq * 4;
+        if (!ensure_dynamic_smem(reinterpret_cast<const void *>(decode_block_weights_kernel), wsmem)) return PA_ERR_CUDA;
+        if (launch_kernel(decode_block_weights_kernel, dim3(4 * a.grid), dim3(kBlkWeightThreads), wsmem, st, a) != cudaSuccess)
+            return PA_ERR_CUDA;
+    }
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

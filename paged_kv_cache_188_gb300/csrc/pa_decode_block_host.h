@@ -5,17 +5,18 @@
 
 namespace pa {
 
-// Workspace: header, partials (two slots per CTA), log-sum-exps, then the
-// score tiles (weights calls).  Every offset but the last region's length
-// depends on the head counts alone, and nothing is kept between calls.
+// Workspace: header, tickets (one per CTA, zero between calls), partials (two
+// slots per CTA), log-sum-exps, then the score tiles (weights calls).  Offsets
+// depend on the head counts alone; the tickets' on nothing.
 struct BlkWs {
-    size_t ml_off, o_off, lse_off, scores_off;
+    size_t tickets_off, ml_off, o_off, lse_off, scores_off;
 };
 inline BlkWs blk_ws(int Hq, int Hkv, int D)
 {
     const int G = Hq / Hkv;
     BlkWs w;
-    w.ml_off = kWorkspaceHeader;
+    w.tickets_off = kWorkspaceHeader;
+    w.ml_off = align_up(w.tickets_off + kBlkMaxCtas * 4, 256);
     w.o_off = align_up(w.ml_off + (size_t)2 * kBlkMaxCtas * G * 2 * 4, 256);
     w.lse_off = align_up(w.o_off + (size_t)2 * kBlkMaxCtas * G * D * 4, 256);
     w.scores_off = align_up(w.lse_off + (size_t)kBlkMaxBatch * Hq * 4, 256);
@@ -87,6 +88,7 @@ inline bool fill_block(BlkArgs &a, const void *q, int batch, int Hq, const void 
     }
     a.out = static_cast<__nv_bfloat16 *>(out);
     a.err = reinterpret_cast<int32_t *>(w);
+    a.tickets = reinterpret_cast<int32_t *>(w + ws.tickets_off);
     a.ml_part = reinterpret_cast<float *>(w + ws.ml_off);
     a.o_part = reinterpret_cast<float *>(w + ws.o_off);
     a.lse = reinterpret_cast<float *>(w + ws.lse_off);
