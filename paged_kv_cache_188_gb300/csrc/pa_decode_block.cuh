@@ -55,7 +55,8 @@ using namespace sm100;
 
 constexpr int kBlkTile = 128;          // tokens per tile: the MMA's M
 constexpr int kBlkConsumers = 256;     // two warpgroups
-constexpr int kBlkThreads = kBlkConsumers + 64;
+constexpr int kBlkLoaders = 2;         // loader warps per operand, taking its tiles in turn
+constexpr int kBlkThreads = kBlkConsumers + 64 * kBlkLoaders;
 constexpr int kBlkMaxCtas = 160;       // partial slots in the workspace (152 SMs)
 constexpr int kBlkMaxStages = 8;
 constexpr int kBlkMaxBatch = 4096;
@@ -105,8 +106,10 @@ struct BlkCfg {
     static constexpr int OffMeta = OffP + 2 * align_k(PB);
     static constexpr int OffBar = OffMeta + 2 * kBlkMaxStages * kBlkTile;
     static constexpr int OffRed = OffBar + 256;            // fp32: [2][4][2 GP] maxima, [2][4][GP] sums, [GP] q factors, m, l
-    static constexpr int OffPref = OffRed + (16 * GP + 8 * GP + GP + 4 * GP) * 4;
-    static constexpr size_t fixed(int batch) { return 1024 + (size_t)OffPref + ((size_t)batch + 1) * 4; }
+    static constexpr int OffPref = (OffRed + (16 * GP + 8 * GP + GP + 4 * GP) * 4 + 7) & ~7;
+    // after the prefix array [batch + 1]: each request's (length, table row), int2 [batch]
+    __host__ __device__ static constexpr int off_req(int batch) { return OffPref + (batch + 2) / 2 * 8; }
+    static constexpr size_t fixed(int batch) { return 1024 + (size_t)off_req(batch) + (size_t)batch * 8; }
     static constexpr size_t bytes(int batch, int stages) { return fixed(batch) + (size_t)stages * STAGE; }
     static_assert(2 * align_k(PB) >= GP * D * 4, "the item-end scratch reuses the P tiles");
 };
@@ -154,10 +157,11 @@ __device__ __forceinline__ int blk_len(const BlkArgs &a, int b)
     return (row < 0 || row >= a.req_rows || n < 0) ? 0 : min(n, a.max_ctx);
 }
 
-// s_pref[0 .. batch] = first tile of each request within one kv head's run.
-// Whole block of NT threads; s_w holds one int per warp.
+// s_pref[0 .. batch] = first tile of each request within one kv head's run;
+// s_req (may be null) = each request's length and table row.  Whole block of
+// NT threads; s_w holds one int per warp.
 template <int NT>
-__device__ __forceinline__ void blk_plan(const BlkArgs &a, int *s_pref, int *s_w)
+__device__ __forceinline__ void blk_plan(const BlkArgs &a, int *s_pref, int2 *s_req, int *s_w)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = a.batch;
     const int per = (B + NT - 1) / NT, lo = min(B, tid * per), hi = min(B, lo + per);
@@ -176,7 +180,9 @@ __device__ __forceinline__ void blk_plan(const BlkArgs &a, int *s_pref, int *s_w
     int excl = base + incl - run;
     for (int b = lo; b < hi; ++b) {
         s_pref[b] = excl;
-        excl += blk_tiles(blk_len(a, b));
+        const int n = blk_len(a, b);
+        if (s_req) s_req[b] = make_int2(n, __ldg(a.req_pool_indices + b));
+        excl += blk_tiles(n);
     }
     if (tid == NT - 1) s_pref[B] = base + incl;
     __syncthreads();
@@ -206,15 +212,15 @@ __device__ __forceinline__ BlkWalk blk_begin(const int *s_pref, int B, int Hkv, 
     return k;
 }
 // the piece at k.x; false past the end
-__device__ __forceinline__ bool blk_piece(const BlkArgs &a, const int *s_pref, BlkWalk &k)
+__device__ __forceinline__ bool blk_piece(const BlkArgs &a, const int *s_pref, const int2 *s_req, BlkWalk &k)
 {
     if (k.x >= k.xe) return false;
     k.S0 = k.h * s_pref[a.batch] + s_pref[k.b];
     k.tb = s_pref[k.b + 1] - s_pref[k.b];
     k.t0 = k.x - k.S0;
     k.t1 = min(k.xe - k.S0, k.tb);
-    k.n = blk_len(a, k.b);
-    k.row = __ldg(a.req_pool_indices + k.b);
+    k.n = s_req[k.b].x;
+    k.row = s_req[k.b].y;
     k.live = k.n > 0 ? k.t1 - k.t0 : 0;
     return true;
 }
@@ -233,7 +239,10 @@ __device__ __forceinline__ int blk_width(const int *s_pref, int B, int Hkv, int 
 }
 
 // ------------------------------------------------------------------ loader
-// K (isv false) or V rows and exponents of every tile of the CTA, in order.
+// K (isv false) or V rows and exponents of tiles first, first + kBlkLoaders, ...
+// of the CTA, in order.  (A TMA instruction costs its warp about 100 cycles of
+// issue, a tile of 16-slot pages eight of them: one warp per operand fell
+// behind HBM, 1830 cycles a tile against 1460.)
 // Table entries and exponents come through registers in batches of kBlkAhead
 // tiles: a batch's table entries are requested while the batch before it is
 // copied, its exponents (which hang on them) half a batch later, so a tile's
@@ -241,8 +250,9 @@ __device__ __forceinline__ int blk_width(const int *s_pref, int B, int Hkv, int 
 constexpr int kBlkAhead = 4;
 
 template <int D, bool E8, int GP>
-__device__ __forceinline__ void blk_loader(const BlkArgs &a, const int *s_pref, int W, uint32_t ring, unsigned char *meta,
-                                           uint32_t full, uint32_t empty, volatile int *s_abort, bool isv, int lane)
+__device__ __forceinline__ void blk_loader(const BlkArgs &a, const int *s_pref, const int2 *s_req, int W, uint32_t ring,
+                                           unsigned char *meta, uint32_t full, uint32_t empty, volatile int *s_abort,
+                                           bool isv, int first, int lane)
 {
     using C = BlkCfg<D, E8, GP>;
     struct Tile {
@@ -253,14 +263,14 @@ __device__ __forceinline__ void blk_loader(const BlkArgs &a, const int *s_pref, 
     const CUtensorMap *m16 = isv ? &a.tm_v16 : &a.tm_k16, *m1 = isv ? &a.tm_v1 : &a.tm_k1;
     const uint8_t *exps = isv ? a.v_exp : a.k_exp;
     BlkWalk k = blk_begin(s_pref, a.batch, a.Hkv, W, blockIdx.x);
-    bool more = blk_piece(a, s_pref, k);
-    int i = 0;                  // next tile of the piece
+    bool more = blk_piece(a, s_pref, s_req, k);
+    int i = first;              // next tile of the piece
     int errs = 0;
     auto fetch = [&](Tile &t) {
         while (more && i >= k.live) {
+            i -= k.live;
             blk_next(a, k);
-            more = blk_piece(a, s_pref, k);
-            i = 0;
+            more = blk_piece(a, s_pref, s_req, k);
         }
         t.n = t.p0 = t.h = 0;
         int64_t row = 0;
@@ -269,7 +279,7 @@ __device__ __forceinline__ void blk_loader(const BlkArgs &a, const int *s_pref, 
             t.h = k.h;
             t.n = k.n;
             t.p0 = (k.t0 + i) * kBlkTile;
-            ++i;
+            i += kBlkLoaders;
         }
         const int32_t *src = a.req_to_token + row * a.max_ctx;
 #pragma unroll
@@ -285,12 +295,12 @@ __device__ __forceinline__ void blk_loader(const BlkArgs &a, const int *s_pref, 
             t.ex[e] = !ok ? kMasked : !E8 ? 0 : __ldcg(exps + (int64_t)(t.slot[e] >> a.block_shift) * a.Hkv + t.h);
         }
     };
-    int st = 0, issued = 0;
+    int st = first, seq = first;    // ring stage and number of the next tile (stages >= kBlkLoaders)
     uint32_t ph = 0;
     // copies of one tile; false if the wait for its stage timed out
     auto put = [&](const Tile &c) -> bool {
         // the stage's previous tile has been multiplied
-        if (issued >= a.stages &&
+        if (seq >= a.stages &&
             !__all_sync(0xffffffffu, mbar_wait(empty + st * 8, ph ^ 1, s_abort, a.err, PA_DEVERR_TIMEOUT, a.wait_ns)))
             return false;
         const uint32_t dst = ring + st * C::STAGE + (isv ? C::TILE : 0), fb = full + st * 8;
@@ -334,9 +344,10 @@ __device__ __forceinline__ void blk_loader(const BlkArgs &a, const int *s_pref, 
             (uint32_t)(c.ex[0] | c.ex[1] << 8 | c.ex[2] << 16 | c.ex[3] << 24);
         __syncwarp();
         if (lane == 0) mbar_arrive_expect_tx(fb, has ? C::TILE : 0u);
-        ++issued;
-        if (++st == a.stages) {
-            st = 0;
+        seq += kBlkLoaders;
+        st += kBlkLoaders;
+        if (st >= a.stages) {
+            st -= a.stages;
             ph ^= 1;
         }
         return true;
@@ -363,7 +374,8 @@ __device__ __forceinline__ void blk_loader(const BlkArgs &a, const int *s_pref, 
     }
     if (*s_abort) {
         // aborted: the copies already issued land before the shared memory goes away
-        for (int j = max(0, issued - a.stages); j < issued; ++j) mbar_drain(full + (j % a.stages) * 8, (j / a.stages) & 1);
+        for (int j = seq - kBlkLoaders; j >= 0 && j >= seq - kBlkLoaders - a.stages; j -= kBlkLoaders)
+            mbar_drain(full + (j % a.stages) * 8, (j / a.stages) & 1);
     }
     if (errs) set_error(a.err, errs);
     __syncwarp();
@@ -386,25 +398,33 @@ __device__ __forceinline__ int blk_slot(const BlkSpan &s, int c, int W) { return
 
 // Merge of a shared segment by the CTA that finished its last piece: every
 // element summed in CTA order.  All consumer threads; a warp's elements belong
-// to one head.  The first pieces' partials are requested before the (m, l)
-// pairs (ordered loads: one round trip for both).
+// to one head.  The first pieces' partials and the (m, l) pairs of the first 32
+// are all requested before any is used: one round trip, for the 20 pieces that
+// a single long request has as for two.
 template <int D, int GP, bool WT>
 __device__ __forceinline__ void blk_merge(const BlkArgs &a, const BlkSpan &s, int W, int b, int h)
 {
-    constexpr int SB = 16;
+    constexpr int EPT = GP * D / kBlkConsumers;      // elements per thread
+    constexpr int SB = EPT <= 2 ? 20 : 8;            // pieces requested at once (registers)
     const int tid = threadIdx.x, lane = tid & 31, G = a.G, np = s.c1 - s.c0 + 1;
-    // piece p of the segment: its partials' slot
-    auto slot = [&](int p) { return blk_slot(s, s.c0 + p, W); };
-    for (int e = tid; e < G * D; e += kBlkConsumers) {
-        const int g = e / D;
-        float v[SB];
+    auto slot = [&](int p) { return blk_slot(s, s.c0 + p, W); };   // piece p's partials
+    float v[EPT][SB], mv[EPT], lv[EPT];
 #pragma unroll
-        for (int p = 0; p < SB; ++p) v[p] = ld_cg_ordered_if(p < np, a.o_part + ((int64_t)slot(min(p, np - 1)) * G * D + e));
-        float M = -INFINITY;
-        for (int p0 = 0; p0 < np; p0 += 32) {
-            const int p = p0 + lane;
-            M = fmaxf(M, p < np ? __ldcg(a.ml_part + (slot(p) * G + g) * 2) : -INFINITY);
-        }
+    for (int k = 0; k < EPT; ++k) {
+        const int e = tid + k * kBlkConsumers, g = e / D;
+        const bool in = g < G;
+#pragma unroll
+        for (int p = 0; p < SB; ++p)
+            v[k][p] = ld_cg_ordered_if(in && p < np, a.o_part + ((int64_t)slot(p) * G * D + e));
+        mv[k] = ld_cg_ordered_if(in && lane < np, a.ml_part + (slot(lane) * G + g) * 2);
+        lv[k] = ld_cg_ordered_if(in && lane < np, a.ml_part + (slot(lane) * G + g) * 2 + 1);
+    }
+#pragma unroll
+    for (int k = 0; k < EPT; ++k) {
+        const int e = tid + k * kBlkConsumers, g = e / D;
+        if (g >= G) break;
+        float M = lane < np ? mv[k] : -INFINITY;
+        for (int p = 32 + lane; p < np; p += 32) M = fmaxf(M, __ldcg(a.ml_part + (slot(p) * G + g) * 2));
         M = warp_max(M);
         const float Mz = M == -INFINITY ? 0.f : M;
         float L = 0.f, O = 0.f;
@@ -412,15 +432,15 @@ __device__ __forceinline__ void blk_merge(const BlkArgs &a, const BlkSpan &s, in
             const int p = p0 + lane;
             float w = 0.f, l = 0.f;
             if (p < np) {
-                w = blk_ex2(__ldcg(a.ml_part + (slot(p) * G + g) * 2) - Mz);
-                l = w * __ldcg(a.ml_part + (slot(p) * G + g) * 2 + 1);
+                w = blk_ex2((p0 == 0 ? mv[k] : __ldcg(a.ml_part + (slot(p) * G + g) * 2)) - Mz);
+                l = w * (p0 == 0 ? lv[k] : __ldcg(a.ml_part + (slot(p) * G + g) * 2 + 1));
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
             L += l;
             if (p0 == 0) {
 #pragma unroll
-                for (int q = 0; q < SB; ++q) O += __shfl_sync(0xffffffffu, w, q) * v[q];
+                for (int q = 0; q < SB; ++q) O += __shfl_sync(0xffffffffu, w, q) * v[k][q];
             }
             for (int q = p0 == 0 ? SB : 0; q < 32 && p0 + q < np; ++q)
                 O += __shfl_sync(0xffffffffu, w, q) * __ldcg(a.o_part + ((int64_t)slot(p0 + q) * G * D + e));
@@ -470,11 +490,12 @@ __global__ void __launch_bounds__(kBlkThreads, 1) decode_block_kernel(const __gr
     }
     if (warp == 0) tmem_alloc(smem_u32(&s_tmem), kBlkTmemCols);
     if (warp >= 8 && lane == 0) {
-        prefetch_tmap(warp == 8 ? &a.tm_k16 : &a.tm_v16);
-        prefetch_tmap(warp == 8 ? &a.tm_k1 : &a.tm_v1);
+        prefetch_tmap(warp & 1 ? &a.tm_v16 : &a.tm_k16);
+        prefetch_tmap(warp & 1 ? &a.tm_v1 : &a.tm_k1);
     }
     if (!a.early_meta) pdl_wait();
-    blk_plan<kBlkThreads>(a, s_pref, s_w);
+    int2 *s_req = reinterpret_cast<int2 *>(base + C::off_req(a.batch));
+    blk_plan<kBlkThreads>(a, s_pref, s_req, s_w);
     if (a.early_meta) pdl_wait();
     pdl_launch_dependents();
     if (blockIdx.x == 0) {
@@ -489,7 +510,7 @@ __global__ void __launch_bounds__(kBlkThreads, 1) decode_block_kernel(const __gr
     const int W = blk_width(s_pref, a.batch, a.Hkv, a.grid);
 
     if (warp >= 8) {
-        blk_loader<D, E8, GP>(a, s_pref, W, ring, meta, full, empty, s_abort, warp == 9, lane);
+        blk_loader<D, E8, GP>(a, s_pref, s_req, W, ring, meta, full, empty, s_abort, warp & 1, (warp - 8) >> 1, lane);
     } else {
         const int wg = warp >> 2, t = tid & 127;
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
@@ -509,8 +530,19 @@ __global__ void __launch_bounds__(kBlkThreads, 1) decode_block_kernel(const __gr
         };
         int shared_b[2], shared_h[2], shared = 0;   // segments of which this CTA has a piece: at most two
         int ticket[2];
-        BlkWalk k = blk_begin(s_pref, a.batch, a.Hkv, W, blockIdx.x);
-        for (; blk_piece(a, s_pref, k); blk_next(a, k)) {
+        // this thread's chunk of the piece's query rows, requested while the piece before it ends
+        constexpr int CH = D / 8;               // 8-element chunks of a head row
+        const int qg = tid / CH, qc = tid % CH;
+        auto load_q = [&](const BlkWalk &k) -> uint4 {
+            if (qg >= a.G) return make_uint4(0u, 0u, 0u, 0u);
+            return __ldg(reinterpret_cast<const uint4 *>(a.q + ((int64_t)k.b * a.Hq + k.h * a.G + qg) * D) + qc);
+        };
+        BlkWalk k = blk_begin(s_pref, a.batch, a.Hkv, W, blockIdx.x), kn = k;
+        uint4 qn = make_uint4(0u, 0u, 0u, 0u);
+        bool more = blk_piece(a, s_pref, s_req, kn);
+        if (more) qn = load_q(kn);
+        while (more) {
+            k = kn;
             if (a.wait_ns == 0 && !bad) {
                 // a wait limit of 0: give up at the first item, as a timed-out wait would
                 *s_abort = 1;
@@ -519,10 +551,8 @@ __global__ void __launch_bounds__(kBlkThreads, 1) decode_block_kernel(const __gr
             }
             // ---- q as the B operand, rows (term, head)
             {
-                constexpr int CH = D / 8;               // 8-element chunks of a head row
-                const int g = tid / CH, c = tid % CH;
-                uint4 w = make_uint4(0u, 0u, 0u, 0u);
-                if (g < a.G) w = __ldg(reinterpret_cast<const uint4 *>(a.q + ((int64_t)k.b * a.Hq + k.h * a.G + g) * D) + c);
+                const int g = qg, c = qc;
+                const uint4 w = qn;
                 if constexpr (E8) {
                     float x[8];
 #pragma unroll
@@ -708,6 +738,9 @@ __global__ void __launch_bounds__(kBlkThreads, 1) decode_block_kernel(const __gr
             }
 
             // ---- the item ends: the warpgroup's sums, then both warpgroups
+            blk_next(a, kn);
+            more = blk_piece(a, s_pref, s_req, kn);
+            if (more) qn = load_q(kn);
 #pragma unroll
             for (int g = 0; g < GP; ++g) {
                 float s = l[g];
@@ -811,7 +844,7 @@ static __global__ void __launch_bounds__(kBlkWeightThreads) decode_block_weights
     const int tid = threadIdx.x, B = a.batch, G = a.G;
     float *s_lse = reinterpret_cast<float *>(s_pref + B + 1);
     if (!a.early_meta) pdl_wait();
-    blk_plan<kBlkWeightThreads>(a, s_pref, s_w);
+    blk_plan<kBlkWeightThreads>(a, s_pref, nullptr, s_w);
     if (a.early_meta) pdl_wait();
     pdl_launch_dependents();
     const int tiles = s_pref[B];
