@@ -32,18 +32,24 @@
 //   * l sums 2^(s - m) in fp32 with the running maximum m; each thread keeps
 //     its own tokens' sum until the item ends.
 //
-// Work: every (kv head, request) is a segment of 128-token tiles (at least
-// one), laid end to end head-major; CTA c takes tiles [c W, (c + 1) W).  A CTA
-// has at most two segments it shares with others, its first and its last, so
-// the fp32 partials are two slots per CTA whatever the batch is.  The CTA that
-// finishes a shared segment's last piece (a ticket per segment) merges its
-// pieces in CTA order (deterministic); a second kernel adds the weights (WT).
+// Work: the requests' 128-token tiles (at least one each), laid end to end, are
+// cut into equal ranges of W tiles, as many as there are warpgroups (two on an
+// SM) per kv head; unit (range i, head h) is worker i Hkv + h's.  All heads of a
+// token are then read at about the same time: a row's 128 bytes of one head
+// alone, 1 KB apart, reach 4.6 TB/s, its neighbours beside them let HBM finish
+// a page it has opened.  A unit has at most two (request, head) segments it
+// shares with others, its first and its last, so the fp32 partials are two
+// slots per unit whatever the batch is.  The one that finishes a shared segment's
+// last piece (a ticket per segment) merges its pieces in order (deterministic);
+// a second kernel adds the weights (WT).
 //
-// Roles: two warpgroups take the tiles in turn (softmax of one beside the
-// products of the other), each issuing its own MMAs; warp 8 loads K tiles and
-// K exponents, warp 9 the V's.  16 consecutive slots move as one TMA box, any
-// other four rows as one gather4 copy.  Positions past the end repeat a valid
-// row (weight zero), so nothing behind the last token is read.
+// Roles: the two warpgroups work apart, each on its own range, ring and
+// tensor-memory columns, so one's softmax, item starts and item ends run beside
+// the other's products; each issues its own MMAs.  Two loader warps serve each
+// warpgroup: one the K tiles and exponents, one the V's.  16 consecutive slots
+// move as one TMA box, any other four rows as one gather4 copy.  Positions past
+// the end repeat a valid row (weight zero), so nothing behind the last token is
+// read.
 #include <math.h>
 #include <string.h>
 
@@ -54,12 +60,12 @@ namespace pa {
 using namespace sm100;
 
 constexpr int kBlkTile = 128;          // tokens per tile: the MMA's M
-constexpr int kBlkConsumers = 256;     // two warpgroups
-constexpr int kBlkLoaders = 2;         // loader warps per operand, taking its tiles in turn
-constexpr int kBlkThreads = kBlkConsumers + 64 * kBlkLoaders;
-constexpr int kBlkMaxCtas = 160;       // partial slots in the workspace (152 SMs)
-constexpr int kBlkMaxStages = 8;
+constexpr int kBlkThreads = 256 + 128;  // two warpgroups, two loader warps for each
+constexpr int kBlkMaxWorkers = 320;     // warpgroups of a launch: two per SM (152 SMs)
+constexpr int kBlkMaxStages = 6;        // per warpgroup and operand
 constexpr int kBlkMaxBatch = 4096;
+constexpr int kBlkAhead = 4;            // tiles of a loader's batch
+constexpr int kBlkStageBytes = (kBlkAhead * (32 * 20 + 12) + 15) / 16 * 16;
 constexpr uint32_t kBlkTmemCols = 256; // per warpgroup 128: S at 0, O at 64
 constexpr int kMasked = 255;           // exponent byte of a position without a token
 
@@ -70,13 +76,14 @@ struct BlkArgs {
     const uint8_t *k_exp, *v_exp;               // the layer's [n_blocks, Hkv] (e4m3 cache)
     __nv_bfloat16 *out;
     int32_t *err;
-    int32_t *tickets;                           // [CTAs]: finished pieces of the shared segment that starts in that CTA
-    float *ml_part;                             // [2 CTAs][G][2]: maximum (log2 units), sum
-    float *o_part;                              // [2 CTAs][G][D]: relative to that maximum
+    int32_t *tickets;                           // [workers]: finished pieces of the shared segment that starts there
+    float *ml_part;                             // [2 workers][G][2]: maximum (log2 units), sum
+    float *o_part;                              // [2 workers][G][D]: relative to that maximum
     float *lse;                                 // [batch, Hq]: log2-sum-exp (WT)
     float *scores;                              // [Hkv][cap_tiles][128][G], log2 units (WT)
     float *weights;                             // [req_rows, max_ctx] (WT)
-    int batch, Hq, Hkv, G, size, req_rows, max_ctx, layer_row0, block_shift, stages, cap_tiles, early_meta, grid;
+    int batch, Hq, Hkv, G, size, req_rows, max_ctx, layer_row0, block_shift, cap_tiles, early_meta;
+    int workers, stages_k, stages_v;            // two workers per CTA; ring stages per worker
     uint64_t wait_ns;
     float scale_log2;
 };
@@ -95,23 +102,23 @@ struct BlkCfg {
     static constexpr int HALVES = RB / AW;
     static constexpr int HALF = kBlkTile * AW;
     static constexpr int TILE = kBlkTile * RB;
-    static constexpr int STAGE = 2 * TILE;
-    static constexpr int QB = NQ * RB;
-    static constexpr int PB = NP * kBlkTile * ES;         // one warpgroup's P
+    static constexpr int QB = NQ * RB;                    // one warpgroup's q
+    static constexpr int PB = NP * kBlkTile * ES;         // and P
     static constexpr int QSteps = RB / 32, PSteps = kBlkTile * ES / 32;   // a K step is 32 bytes of either type
-    // offsets behind the ring of `stages` tiles
+    // offsets behind the rings
     __host__ __device__ static constexpr int align_k(int x) { return (x + 1023) & ~1023; }
     static constexpr int OffQ = 0;
-    static constexpr int OffP = align_k(QB);
-    static constexpr int OffMeta = OffP + 2 * align_k(PB);
-    static constexpr int OffBar = OffMeta + 2 * kBlkMaxStages * kBlkTile;
-    static constexpr int OffRed = OffBar + 256;            // fp32: [2][4][2 GP] maxima, [2][4][GP] sums, [GP] q factors, m, l
-    static constexpr int OffPref = (OffRed + (16 * GP + 8 * GP + GP + 4 * GP) * 4 + 7) & ~7;
+    static constexpr int OffP = 2 * align_k(QB);
+    static constexpr int OffMeta = OffP + 2 * align_k(PB);              // exponent bytes [2][K, V][stages][128]
+    static constexpr int OffStage = OffMeta + 4 * kBlkMaxStages * kBlkTile;   // the loaders' batches
+    static constexpr int OffBar = OffStage + 4 * kBlkStageBytes;
+    static constexpr int kBars = 4 * kBlkMaxStages + 3;   // per warpgroup: K and V full and empty, S, O, drain
+    static constexpr int OffRed = OffBar + 2 * kBars * 8; // fp32 per warpgroup: [4][2 GP] maxima, [4][GP] sums, [GP] q factors
+    static constexpr int kRed = 13 * GP;
+    static constexpr int OffPref = (OffRed + 2 * kRed * 4 + 7) & ~7;
     // after the prefix array [batch + 1]: each request's (length, table row), int2 [batch]
     __host__ __device__ static constexpr int off_req(int batch) { return OffPref + (batch + 2) / 2 * 8; }
     static constexpr size_t fixed(int batch) { return 1024 + (size_t)off_req(batch) + (size_t)batch * 8; }
-    static constexpr size_t bytes(int batch, int stages) { return fixed(batch) + (size_t)stages * STAGE; }
-    static_assert(2 * align_k(PB) >= GP * D * 4, "the item-end scratch reuses the P tiles");
 };
 constexpr size_t kBlkSmemLimit = 232448 - 512;   // opt-in maximum minus static shared memory
 
@@ -188,35 +195,38 @@ __device__ __forceinline__ void blk_plan(const BlkArgs &a, int *s_pref, int2 *s_
     __syncthreads();
 }
 
-// One CTA's walk over its pieces of segments.
+// Ranges per head, and their length in tiles.
+__device__ __forceinline__ int blk_ranges(int workers, int Hkv) { return max(workers / Hkv, 1); }
+__device__ __forceinline__ int blk_width(const int *s_pref, int B, int ranges) { return (s_pref[B] + ranges - 1) / ranges; }
+
+// The walk over one unit's pieces of segments.
 struct BlkWalk {
-    int x, xe, h, b;       // next tile, end of the CTA's range, segment
-    int S0, tb;            // the segment's first tile and its tiles
-    int t0, t1, n, row;    // the piece: tiles [t0, t1) of the segment, tokens and table row of the request
+    int x, xe, h, b;       // next tile and end of the range, head, request
+    int S0, tb;            // the request's first tile and its tiles
+    int t0, t1, n, row;    // the piece: tiles [t0, t1) of the request, its tokens and table row
     int live;              // tiles of the piece with tokens: t1 - t0, or 0
 };
-__device__ __forceinline__ BlkWalk blk_begin(const int *s_pref, int B, int Hkv, int W, int cta)
+__device__ __forceinline__ BlkWalk blk_begin(const int *s_pref, int B, int Hkv, int W, int unit)
 {
     BlkWalk k;
-    const int tph = s_pref[B];
-    k.x = min((long long)cta * W, (long long)Hkv * tph);
-    k.xe = min((long long)k.x + W, (long long)Hkv * tph);
-    k.h = k.x / tph;
-    const int local = k.x - k.h * tph;
+    const int i = unit / Hkv, total = s_pref[B];
+    k.h = unit - i * Hkv;
+    k.x = (int)min((long long)i * W, (long long)total);
+    k.xe = min(k.x + W, total);
     int lo = 0, hi = B;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (s_pref[mid] <= local) lo = mid; else hi = mid;
+        if (s_pref[mid] <= k.x) lo = mid; else hi = mid;
     }
     k.b = lo;
     return k;
 }
 // the piece at k.x; false past the end
-__device__ __forceinline__ bool blk_piece(const BlkArgs &a, const int *s_pref, const int2 *s_req, BlkWalk &k)
+__device__ __forceinline__ bool blk_piece(const int *s_pref, const int2 *s_req, BlkWalk &k)
 {
     if (k.x >= k.xe) return false;
-    k.S0 = k.h * s_pref[a.batch] + s_pref[k.b];
-    k.tb = s_pref[k.b + 1] - s_pref[k.b];
+    k.S0 = s_pref[k.b];
+    k.tb = s_pref[k.b + 1] - k.S0;
     k.t0 = k.x - k.S0;
     k.t1 = min(k.xe - k.S0, k.tb);
     k.n = s_req[k.b].x;
@@ -224,231 +234,267 @@ __device__ __forceinline__ bool blk_piece(const BlkArgs &a, const int *s_pref, c
     k.live = k.n > 0 ? k.t1 - k.t0 : 0;
     return true;
 }
-__device__ __forceinline__ void blk_next(const BlkArgs &a, BlkWalk &k)
+__device__ __forceinline__ void blk_next(BlkWalk &k)
 {
     k.x = k.S0 + k.t1;
-    if (k.t1 == k.tb && ++k.b == a.batch) {
-        k.b = 0;
-        ++k.h;
-    }
-}
-__device__ __forceinline__ int blk_width(const int *s_pref, int B, int Hkv, int grid)
-{
-    const long long T = (long long)Hkv * s_pref[B];
-    return (int)((T + grid - 1) / grid);
+    if (k.t1 == k.tb) ++k.b;
 }
 
 // ------------------------------------------------------------------ loader
-// K (isv false) or V rows and exponents of tiles first, first + kBlkLoaders, ...
-// of the CTA, in order.  (A TMA instruction costs its warp about 100 cycles of
-// issue, a tile of 16-slot pages eight of them: one warp per operand fell
-// behind HBM, 1830 cycles a tile against 1460.)
-// Table entries and exponents come through registers in batches of kBlkAhead
-// tiles: a batch's table entries are requested while the batch before it is
-// copied, its exponents (which hang on them) half a batch later, so a tile's
-// copies wait for neither round trip.
-constexpr int kBlkAhead = 4;
+// K (isv false) or V rows and exponents of a worker's tiles, in order of its
+// units (unit, unit + workers, ...), in
+// batches of kBlkAhead: while a batch is copied, the next one's table entries
+// are on their way to registers and, from its middle on, the exponents that
+// hang on them.  (With tens of MB in flight a read takes several microseconds;
+// one or two tiles of look-ahead left the copies waiting for their indices.)
+// A batch that has arrived is put in shared memory, so that the copies are one
+// rolled loop: a TMA instruction costs its warp about 100 cycles of issue, a
+// tile of 16-slot pages eight of them per operand.
+struct BlkStage {
+    int4 slot[kBlkAhead][32];       // table entries of positions p0 + 4 lane + e
+    uint32_t ex[kBlkAhead][32];     // their exponent bytes
+    int h[kBlkAhead], n[kBlkAhead], p0[kBlkAhead];   // kv head, tokens of the request (0: no more tiles), first position
+};
+static_assert(sizeof(BlkStage) <= kBlkStageBytes, "a batch fits its area");
 
 template <int D, bool E8, int GP>
-__device__ __forceinline__ void blk_loader(const BlkArgs &a, const int *s_pref, const int2 *s_req, int W, uint32_t ring,
-                                           unsigned char *meta, uint32_t full, uint32_t empty, volatile int *s_abort,
-                                           bool isv, int first, int lane)
+__device__ __forceinline__ void blk_loader(const BlkArgs &a, const int *s_pref, const int2 *s_req, int W, int unit,
+                                           uint32_t ring, int stages, BlkStage *stage, unsigned char *meta, uint32_t full,
+                                           uint32_t empty, volatile int *s_abort, bool isv, int lane)
 {
     using C = BlkCfg<D, E8, GP>;
-    struct Tile {
-        int h, n, p0;           // kv head, tokens of the request (0: no more tiles), first position
-        int slot[4];            // table entries of positions p0 + 4 lane + e
-        int ex[4];              // exponent bytes
-    };
     const CUtensorMap *m16 = isv ? &a.tm_v16 : &a.tm_k16, *m1 = isv ? &a.tm_v1 : &a.tm_k1;
     const uint8_t *exps = isv ? a.v_exp : a.k_exp;
-    BlkWalk k = blk_begin(s_pref, a.batch, a.Hkv, W, blockIdx.x);
-    bool more = blk_piece(a, s_pref, s_req, k);
-    int i = first;              // next tile of the piece
-    int errs = 0;
-    auto fetch = [&](Tile &t) {
-        while (more && i >= k.live) {
-            i -= k.live;
-            blk_next(a, k);
-            more = blk_piece(a, s_pref, s_req, k);
-        }
-        t.n = t.p0 = t.h = 0;
-        int64_t row = 0;
-        if (more) {
-            row = k.row;
-            t.h = k.h;
-            t.n = k.n;
-            t.p0 = (k.t0 + i) * kBlkTile;
-            i += kBlkLoaders;
-        }
-        const int32_t *src = a.req_to_token + row * a.max_ctx;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int p = t.p0 + 4 * lane + e;
-            t.slot[e] = ld_nc_ordered_s32_if(p < t.n, src + (p < t.n ? p : 0));
+    const int units = blk_ranges(a.workers, a.Hkv) * a.Hkv;
+    BlkWalk k;
+    bool more = false;
+    // to the next unit that has a piece
+    auto open = [&]() {
+        for (more = false; !more && unit < units; unit += a.workers) {
+            k = blk_begin(s_pref, a.batch, a.Hkv, W, unit);
+            more = blk_piece(s_pref, s_req, k);
         }
     };
-    auto load_exps = [&](Tile &t) {
+    open();
+    int i = 0;                  // next tile of the piece
+    // the batch on its way
+    int slot[kBlkAhead][4], ex[kBlkAhead][4], h[kBlkAhead], n[kBlkAhead], p0[kBlkAhead];
+    auto fetch = [&]() {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const bool ok = t.slot[e] >= 0 && t.slot[e] < a.size;
-            t.ex[e] = !ok ? kMasked : !E8 ? 0 : __ldcg(exps + (int64_t)(t.slot[e] >> a.block_shift) * a.Hkv + t.h);
-        }
-    };
-    int st = first, seq = first;    // ring stage and number of the next tile (stages >= kBlkLoaders)
-    uint32_t ph = 0;
-    // copies of one tile; false if the wait for its stage timed out
-    auto put = [&](const Tile &c) -> bool {
-        // the stage's previous tile has been multiplied
-        if (seq >= a.stages &&
-            !__all_sync(0xffffffffu, mbar_wait(empty + st * 8, ph ^ 1, s_abort, a.err, PA_DEVERR_TIMEOUT, a.wait_ns)))
-            return false;
-        const uint32_t dst = ring + st * C::STAGE + (isv ? C::TILE : 0), fb = full + st * 8;
-        bool ok[4];
-        int sl[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            sl[e] = c.slot[e];
-            ok[e] = sl[e] >= 0 && sl[e] < a.size;
-            if (!ok[e] && c.p0 + 4 * lane + e < c.n) errs |= PA_DEVERR_SLOT;
-        }
-        const int mine = ok[0] ? sl[0] : ok[1] ? sl[1] : ok[2] ? sl[2] : ok[3] ? sl[3] : -1;
-        const unsigned has = __ballot_sync(0xffffffffu, mine >= 0);
-        const int some = __shfl_sync(0xffffffffu, mine, has ? __ffs(has) - 1 : 0);   // a valid row of the tile
-        const int s0 = __shfl_sync(0xffffffffu, sl[0], lane & ~3);
-        const bool run = ok[0] && ok[1] && ok[2] && ok[3] && sl[0] == s0 + 4 * (lane & 3) && sl[1] == sl[0] + 1 &&
-                         sl[2] == sl[0] + 2 && sl[3] == sl[0] + 3;
-        const bool page = ((__ballot_sync(0xffffffffu, run) >> (lane & ~3)) & 0xFu) == 0xFu;
-        if (has) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sl[e] = a.layer_row0 + (ok[e] ? sl[e] : some);
-            const int col = c.h * D;
-            if (page) {
-                if ((lane & 3) == 0) {
-#pragma unroll
-                    for (int hh = 0; hh < C::HALVES; ++hh)
-                        tma_load_2d(dst + hh * C::HALF + (lane >> 2) * 16 * C::AW, m16, col + hh * (C::AW / C::ES), sl[0], fb);
-                }
-            } else {
-#pragma unroll
-                for (int hh = 0; hh < C::HALVES; ++hh)
-                    tma_gather4(dst + hh * C::HALF + lane * 4 * C::AW, m1, col + hh * (C::AW / C::ES), sl[0], sl[1], sl[2],
-                                sl[3], fb);
+        for (int u = 0; u < kBlkAhead; ++u) {
+            while (more && i >= k.live) {
+                blk_next(k);
+                more = blk_piece(s_pref, s_req, k);
+                if (!more) open();
+                i = 0;
             }
-        } else {
-            // no valid row at all: zeros (weight zero times whatever bits lie there could be NaN)
-            for (int o = lane * 16; o < C::TILE; o += 512) st_shared_v4(dst + o, 0u, 0u, 0u, 0u);
-            fence_proxy_async_smem();
+            n[u] = p0[u] = h[u] = 0;
+            int64_t row = 0;
+            if (more) {
+                row = k.row;
+                h[u] = k.h;
+                n[u] = k.n;
+                p0[u] = (k.t0 + i) * kBlkTile;
+                ++i;
+            }
+            const int32_t *src = a.req_to_token + row * a.max_ctx;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int p = p0[u] + 4 * lane + e;
+                slot[u][e] = ld_nc_ordered_s32_if(p < n[u], src + (p < n[u] ? p : 0));
+            }
         }
-        reinterpret_cast<uint32_t *>(meta + ((isv ? kBlkMaxStages : 0) + st) * kBlkTile)[lane] =
-            (uint32_t)(c.ex[0] | c.ex[1] << 8 | c.ex[2] << 16 | c.ex[3] << 24);
-        __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(fb, has ? C::TILE : 0u);
-        seq += kBlkLoaders;
-        st += kBlkLoaders;
-        if (st >= a.stages) {
-            st -= a.stages;
-            ph ^= 1;
-        }
-        return true;
     };
-    Tile cur[kBlkAhead], nxt[kBlkAhead];
+    auto load_exps = [&]() {
 #pragma unroll
-    for (int u = 0; u < kBlkAhead; ++u) fetch(cur[u]);
+        for (int u = 0; u < kBlkAhead; ++u)
 #pragma unroll
-    for (int u = 0; u < kBlkAhead; ++u) load_exps(cur[u]);
+            for (int e = 0; e < 4; ++e) {
+                const bool ok = slot[u][e] >= 0 && slot[u][e] < a.size;
+                ex[u][e] = !ok ? kMasked : !E8 ? 0 : __ldcg(exps + (int64_t)(slot[u][e] >> a.block_shift) * a.Hkv + h[u]);
+            }
+    };
+    fetch();
+    load_exps();
+    int st = 0, seq = 0, errs = 0;      // ring stage and number of the next tile
+    uint32_t ph = 0;
     bool go = true;
     while (go) {
 #pragma unroll
-        for (int u = 0; u < kBlkAhead; ++u) fetch(nxt[u]);
-#pragma unroll
         for (int u = 0; u < kBlkAhead; ++u) {
-            if (u == kBlkAhead / 2) {
-#pragma unroll
-                for (int w = 0; w < kBlkAhead; ++w) load_exps(nxt[w]);
+            stage->slot[u][lane] = make_int4(slot[u][0], slot[u][1], slot[u][2], slot[u][3]);
+            stage->ex[u][lane] = (uint32_t)(ex[u][0] | ex[u][1] << 8 | ex[u][2] << 16 | ex[u][3] << 24);
+            if (lane == 0) {
+                stage->h[u] = h[u];
+                stage->n[u] = n[u];
+                stage->p0[u] = p0[u];
             }
-            if (go) go = cur[u].n > 0 && put(cur[u]);
         }
+        __syncwarp();
+        fetch();
+#pragma unroll 1
+        for (int u = 0; u < kBlkAhead; ++u) {
+            const int tn = stage->n[u];
+            if (tn <= 0) {
+                go = false;
+                break;
+            }
+            if (u == kBlkAhead / 2) load_exps();
+            // the stage's previous tile has been multiplied
+            if (seq >= stages &&
+                !__all_sync(0xffffffffu, mbar_wait(empty + st * 8, ph ^ 1, s_abort, a.err, PA_DEVERR_TIMEOUT, a.wait_ns))) {
+                go = false;
+                break;
+            }
+            const uint32_t dst = ring + st * C::TILE, fb = full + st * 8;
+            const int4 raw = stage->slot[u][lane];
+            int sl[4] = {raw.x, raw.y, raw.z, raw.w};
+            bool ok[4];
 #pragma unroll
-        for (int u = 0; u < kBlkAhead; ++u) cur[u] = nxt[u];
+            for (int e = 0; e < 4; ++e) {
+                ok[e] = sl[e] >= 0 && sl[e] < a.size;
+                if (!ok[e] && stage->p0[u] + 4 * lane + e < tn) errs |= PA_DEVERR_SLOT;
+            }
+            const int mine = ok[0] ? sl[0] : ok[1] ? sl[1] : ok[2] ? sl[2] : ok[3] ? sl[3] : -1;
+            const unsigned has = __ballot_sync(0xffffffffu, mine >= 0);
+            const int some = __shfl_sync(0xffffffffu, mine, has ? __ffs(has) - 1 : 0);   // a valid row of the tile
+            const int s0 = __shfl_sync(0xffffffffu, sl[0], lane & ~3);
+            const bool run = ok[0] && ok[1] && ok[2] && ok[3] && sl[0] == s0 + 4 * (lane & 3) && sl[1] == sl[0] + 1 &&
+                             sl[2] == sl[0] + 2 && sl[3] == sl[0] + 3;
+            const bool page = ((__ballot_sync(0xffffffffu, run) >> (lane & ~3)) & 0xFu) == 0xFu;
+            if (has) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sl[e] = a.layer_row0 + (ok[e] ? sl[e] : some);
+                const int col = stage->h[u] * D;
+                if (page) {
+                    if ((lane & 3) == 0) {
+#pragma unroll
+                        for (int hh = 0; hh < C::HALVES; ++hh)
+                            tma_load_2d(dst + hh * C::HALF + (lane >> 2) * 16 * C::AW, m16, col + hh * (C::AW / C::ES), sl[0], fb);
+                    }
+                } else {
+#pragma unroll
+                    for (int hh = 0; hh < C::HALVES; ++hh)
+                        tma_gather4(dst + hh * C::HALF + lane * 4 * C::AW, m1, col + hh * (C::AW / C::ES), sl[0], sl[1], sl[2],
+                                    sl[3], fb);
+                }
+            } else {
+                // no valid row at all: zeros (weight zero times whatever bits lie there could be NaN)
+                for (int o = lane * 16; o < C::TILE; o += 512) st_shared_v4(dst + o, 0u, 0u, 0u, 0u);
+                fence_proxy_async_smem();
+            }
+            reinterpret_cast<uint32_t *>(meta + st * kBlkTile)[lane] = stage->ex[u][lane];
+            __syncwarp();
+            if (lane == 0) mbar_arrive_expect_tx(fb, has ? C::TILE : 0u);
+            ++seq;
+            if (++st == stages) {
+                st = 0;
+                ph ^= 1;
+            }
+        }
+        __syncwarp();
     }
     if (*s_abort) {
         // aborted: the copies already issued land before the shared memory goes away
-        for (int j = seq - kBlkLoaders; j >= 0 && j >= seq - kBlkLoaders - a.stages; j -= kBlkLoaders)
-            mbar_drain(full + (j % a.stages) * 8, (j / a.stages) & 1);
+        for (int j = max(0, seq - stages); j < seq; ++j) mbar_drain(full + (j % stages) * 8, (j / stages) & 1);
     }
     if (errs) set_error(a.err, errs);
     __syncwarp();
 }
 
-// Pieces of segment (b, h): CTAs c0 .. c1; a piece that does not start its
-// CTA's range is that CTA's last (slot 1).
+// Pieces of request b's segments: ranges i0 .. i1.  A piece that does not start
+// its range is the unit's last (slot 1).
 struct BlkSpan {
-    int c0, c1, S0;
+    int i0, i1, first;      // first: piece 0 does not start range i0
 };
-__device__ __forceinline__ BlkSpan blk_span(const int *s_pref, int B, int W, int b, int h)
+__device__ __forceinline__ BlkSpan blk_span(const int *s_pref, int W, int b)
 {
     BlkSpan s;
-    s.S0 = h * s_pref[B] + s_pref[b];
-    s.c0 = s.S0 / W;
-    s.c1 = (s.S0 + s_pref[b + 1] - s_pref[b] - 1) / W;
+    const int S0 = s_pref[b];
+    s.i0 = S0 / W;
+    s.i1 = (s_pref[b + 1] - 1) / W;
+    s.first = S0 > s.i0 * W;
     return s;
 }
-__device__ __forceinline__ int blk_slot(const BlkSpan &s, int c, int W) { return 2 * c + (s.S0 > c * W ? 1 : 0); }
 
-// Merge of a shared segment by the CTA that finished its last piece: every
-// element summed in CTA order.  All consumer threads; a warp's elements belong
-// to one head.  The first pieces' partials and the (m, l) pairs of the first 32
-// are all requested before any is used: one round trip, for the 20 pieces that
-// a single long request has as for two.
+// Merge of a shared segment by the warpgroup that finished its last piece.
+// Warp w sums pieces w, w + 4, ... (a piece's [G][D] partials are contiguous:
+// 16-byte loads), then the four sums are added in order, so the result does not
+// depend on who merges.  The first pieces are requested before the (m, l)
+// pairs, so both travel in one round trip; the weights go through `scratch`,
+// the worker's ring, which is free by now.
 template <int D, int GP, bool WT>
-__device__ __forceinline__ void blk_merge(const BlkArgs &a, const BlkSpan &s, int W, int b, int h)
+__device__ __forceinline__ void blk_merge(const BlkArgs &a, const BlkSpan &s, int b, int h, int t, int bar_id,
+                                          float *scratch)
 {
-    constexpr int EPT = GP * D / kBlkConsumers;      // elements per thread
-    constexpr int SB = EPT <= 2 ? 20 : 8;            // pieces requested at once (registers)
-    const int tid = threadIdx.x, lane = tid & 31, G = a.G, np = s.c1 - s.c0 + 1;
-    auto slot = [&](int p) { return blk_slot(s, s.c0 + p, W); };   // piece p's partials
-    float v[EPT][SB], mv[EPT], lv[EPT];
+    constexpr int NJ = GP * D / 128;                       // 16-byte loads per lane and piece
+    constexpr int PF = NJ <= 4 ? 4 : NJ <= 8 ? 2 : 1;      // pieces per warp requested at once
+    const int lane = t & 31, warp = t >> 5, G = a.G, np = s.i1 - s.i0 + 1;
+    auto slot = [&](int p) { return 2 * ((s.i0 + p) * a.Hkv + h) + (p == 0 ? s.first : 0); };   // piece p's partials
+    float *s_lse = scratch, *s_wt = scratch + 2 * 16;      // [G] log-sum-exp, [G] sums; [np][G] weights
+    float4 v[PF][NJ], acc[NJ];
+    auto load = [&](int p0) {
 #pragma unroll
-    for (int k = 0; k < EPT; ++k) {
-        const int e = tid + k * kBlkConsumers, g = e / D;
-        const bool in = g < G;
+        for (int q = 0; q < PF; ++q) {
+            const int p = p0 + 4 * q;
+            const float4 *src = reinterpret_cast<const float4 *>(a.o_part + (int64_t)slot(min(p, np - 1)) * G * D) + lane;
 #pragma unroll
-        for (int p = 0; p < SB; ++p)
-            v[k][p] = ld_cg_ordered_if(in && p < np, a.o_part + ((int64_t)slot(p) * G * D + e));
-        mv[k] = ld_cg_ordered_if(in && lane < np, a.ml_part + (slot(lane) * G + g) * 2);
-        lv[k] = ld_cg_ordered_if(in && lane < np, a.ml_part + (slot(lane) * G + g) * 2 + 1);
-    }
-#pragma unroll
-    for (int k = 0; k < EPT; ++k) {
-        const int e = tid + k * kBlkConsumers, g = e / D;
-        if (g >= G) break;
-        float M = lane < np ? mv[k] : -INFINITY;
-        for (int p = 32 + lane; p < np; p += 32) M = fmaxf(M, __ldcg(a.ml_part + (slot(p) * G + g) * 2));
+            for (int j = 0; j < NJ; ++j)
+                v[q][j] = ld_cg_ordered_f4_if(p < np && (j * 32 + lane) * 4 < G * D, src + j * 32);
+        }
+    };
+    load(warp);
+    for (int g = warp; g < G; g += 4) {
+        float M = -INFINITY;
+        for (int p = lane; p < np; p += 32) M = fmaxf(M, __ldcg(a.ml_part + (slot(p) * G + g) * 2));
         M = warp_max(M);
         const float Mz = M == -INFINITY ? 0.f : M;
-        float L = 0.f, O = 0.f;
-        for (int p0 = 0; p0 < np; p0 += 32) {
-            const int p = p0 + lane;
-            float w = 0.f, l = 0.f;
-            if (p < np) {
-                w = blk_ex2((p0 == 0 ? mv[k] : __ldcg(a.ml_part + (slot(p) * G + g) * 2)) - Mz);
-                l = w * (p0 == 0 ? lv[k] : __ldcg(a.ml_part + (slot(p) * G + g) * 2 + 1));
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-            L += l;
-            if (p0 == 0) {
-#pragma unroll
-                for (int q = 0; q < SB; ++q) O += __shfl_sync(0xffffffffu, w, q) * v[k][q];
-            }
-            for (int q = p0 == 0 ? SB : 0; q < 32 && p0 + q < np; ++q)
-                O += __shfl_sync(0xffffffffu, w, q) * __ldcg(a.o_part + ((int64_t)slot(p0 + q) * G * D + e));
+        float L = 0.f;
+        for (int p = lane; p < np; p += 32) {
+            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.ml_part + (slot(p) * G + g) * 2));
+            const float w = blk_ex2(ml.x - Mz);
+            s_wt[p * G + g] = w;
+            L += w * ml.y;
         }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+        if (lane == 0) {
+            s_lse[g] = L != 0.f ? M + log2f(L) : INFINITY;
+            s_lse[16 + g] = L;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    named_bar_sync(bar_id, 128);
+    for (int p0 = warp; p0 < np; p0 += 4 * PF) {
+        if (p0 != warp) load(p0);
+#pragma unroll
+        for (int q = 0; q < PF; ++q) {
+            if (p0 + 4 * q >= np) break;
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                const float w = s_wt[(p0 + 4 * q) * G + min((j * 32 + lane) * 4 / D, G - 1)];
+                acc[j].x += w * v[q][j].x;
+                acc[j].y += w * v[q][j].y;
+                acc[j].z += w * v[q][j].z;
+                acc[j].w += w * v[q][j].w;
+            }
+        }
+    }
+    float4 *s_o = reinterpret_cast<float4 *>(scratch + 2 * 16 + (np * G + 3) / 4 * 4);   // [4 warps][G D]
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+        if ((j * 32 + lane) * 4 < G * D) s_o[warp * (GP * D / 4) + j * 32 + lane] = acc[j];
+    named_bar_sync(bar_id, 128);
+    for (int e = t; e < G * D; e += 128) {
+        const float *so = reinterpret_cast<const float *>(s_o) + e;
+        const int g = e / D;
+        const float L = s_lse[16 + g], O = so[0] + so[GP * D] + so[2 * GP * D] + so[3 * GP * D];
         const int64_t hq = (int64_t)b * a.Hq + h * G + g;
         a.out[hq * D + (e - g * D)] = __float2bfloat16_rn(L != 0.f ? O / L : 0.f);
-        if (WT && e == g * D) a.lse[hq] = L != 0.f ? M + log2f(L) : INFINITY;
+        if (WT && e == g * D) a.lse[hq] = s_lse[g];
     }
+    named_bar_sync(bar_id, 128);                           // scratch reuse
 }
 
 // ------------------------------------------------------------------ kernel
@@ -461,40 +507,34 @@ __global__ void __launch_bounds__(kBlkThreads, 1) decode_block_kernel(const __gr
     __shared__ int s_w[kBlkThreads / 32];
     __shared__ int s_abort_storage;
     __shared__ uint32_t s_tmem;
-    __shared__ int s_last[2];
-    const uint32_t raw = smem_u32(smem_raw), ring = (raw + 1023u) & ~1023u;
-    unsigned char *base = smem_raw + (ring - raw) + (size_t)a.stages * C::STAGE;
+    __shared__ int s_last[2][2];
+    const uint32_t raw = smem_u32(smem_raw), rings = (raw + 1023u) & ~1023u;
+    const int ring_bytes = (a.stages_k + a.stages_v) * C::TILE;          // one worker's
+    unsigned char *base = smem_raw + (rings - raw) + (size_t)2 * ring_bytes;
     volatile int *s_abort = &s_abort_storage;
-    unsigned char *meta = base + C::OffMeta;
-    float *s_max = reinterpret_cast<float *>(base + C::OffRed);     // [2][4][2 GP]
-    float *s_sum = s_max + 16 * GP;                                 // [2][4][GP]
-    float *s_fq = s_sum + 8 * GP;                                   // [GP]
-    float *s_ml = s_fq + GP;                                        // [2][GP][2]
     int *s_pref = reinterpret_cast<int *>(base + C::OffPref);
-    const uint32_t bars = smem_u32(base + C::OffBar);
-    const uint32_t full = bars, empty = bars + 64, sfull = bars + 128, ofull = bars + 144, drain = bars + 160;
+    int2 *s_req = reinterpret_cast<int2 *>(base + C::off_req(a.batch));
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (tid == 0) {
-        s_abort_storage = 0;
-        for (int i = 0; i < kBlkMaxStages; ++i) {
-            mbar_init(full + i * 8, 2);
-            mbar_init(empty + i * 8, 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(sfull + i * 8, 1);
-            mbar_init(ofull + i * 8, 1);
-            mbar_init(drain + i * 8, 1);
-        }
-        fence_mbar_init();
-    }
-    if (warp == 0) tmem_alloc(smem_u32(&s_tmem), kBlkTmemCols);
+    // this warp's warpgroup (loaders: the one they serve) and its barriers
+    const int wg = warp < 8 ? warp >> 2 : (warp - 8) >> 1;
+    const uint32_t all_bars = smem_u32(base + C::OffBar), bars = all_bars + wg * C::kBars * 8;
+    const uint32_t kfull = bars, vfull = bars + kBlkMaxStages * 8, kempty = vfull + kBlkMaxStages * 8,
+                   vempty = kempty + kBlkMaxStages * 8, sfull = vempty + kBlkMaxStages * 8, ofull = sfull + 8, drain = ofull + 8;
+    const uint32_t kring = rings + wg * ring_bytes, vring = kring + a.stages_k * C::TILE;
+    unsigned char *kmeta = base + C::OffMeta + wg * 2 * kBlkMaxStages * kBlkTile, *vmeta = kmeta + kBlkMaxStages * kBlkTile;
+
+    if (tid < 2 * C::kBars) mbar_init(all_bars + tid * 8, 1);
+    if (tid < 32) fence_mbar_init();
+    static_assert(2 * C::kBars <= 64, "the first two warps initialise the barriers");
+    if (tid >= 32 && tid < 64) fence_mbar_init();
+    if (tid == 0) s_abort_storage = 0;
+    if (warp == 4) tmem_alloc(smem_u32(&s_tmem), kBlkTmemCols);
     if (warp >= 8 && lane == 0) {
         prefetch_tmap(warp & 1 ? &a.tm_v16 : &a.tm_k16);
         prefetch_tmap(warp & 1 ? &a.tm_v1 : &a.tm_k1);
     }
     if (!a.early_meta) pdl_wait();
-    int2 *s_req = reinterpret_cast<int2 *>(base + C::off_req(a.batch));
     blk_plan<kBlkThreads>(a, s_pref, s_req, s_w);
     if (a.early_meta) pdl_wait();
     pdl_launch_dependents();
@@ -507,42 +547,56 @@ __global__ void __launch_bounds__(kBlkThreads, 1) decode_block_kernel(const __gr
     }
     tc_fence_after();
     const uint32_t tmem = s_tmem;
-    const int W = blk_width(s_pref, a.batch, a.Hkv, a.grid);
+    const int ranges = blk_ranges(a.workers, a.Hkv), units = ranges * a.Hkv, W = blk_width(s_pref, a.batch, ranges);
+    // few units: one per SM; else the heads of a range side by side on an SM
+    const int worker = (s_pref[a.batch] + W - 1) / W * a.Hkv <= (int)gridDim.x ? (int)blockIdx.x + wg * (int)gridDim.x
+                                                                           : 2 * (int)blockIdx.x + wg;
 
     if (warp >= 8) {
-        blk_loader<D, E8, GP>(a, s_pref, s_req, W, ring, meta, full, empty, s_abort, warp & 1, (warp - 8) >> 1, lane);
+        const bool isv = warp & 1;
+        blk_loader<D, E8, GP>(a, s_pref, s_req, W, worker, isv ? vring : kring, isv ? a.stages_v : a.stages_k,
+                              reinterpret_cast<BlkStage *>(base + C::OffStage + (warp - 8) * kBlkStageBytes), isv ? vmeta : kmeta, isv ? vfull : kfull, isv ? vempty : kempty, s_abort, isv, lane);
     } else {
-        const int wg = warp >> 2, t = tid & 127;
+        const int t = tid & 127, bar_id = 1 + wg;
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_col = tmem + wg * 128, o_col = s_col + 64;
-        const uint32_t sQ = smem_u32(base + C::OffQ), sP = smem_u32(base + C::OffP) + wg * C::align_k(C::PB);
+        const uint32_t sQ = smem_u32(base + C::OffQ) + wg * C::align_k(C::QB), sP = smem_u32(base + C::OffP) + wg * C::align_k(C::PB);
+        float *s_max = reinterpret_cast<float *>(base + C::OffRed) + wg * C::kRed;    // [4][2 GP]
+        float *s_sum = s_max + 8 * GP, *s_fq = s_sum + 4 * GP;                         // [4][GP], [GP]
         constexpr uint32_t kFmt = E8 ? 0u : (1u << 7 | 1u << 10);      // e4m3 : bf16
         constexpr uint32_t kIdS = 1u << 4 | kFmt | (uint32_t)(C::NQ >> 3) << 17 | 8u << 24;
         constexpr uint32_t kIdO = 1u << 4 | kFmt | 1u << 15 | (uint32_t)(C::NP >> 3) << 17 | 8u << 24;   // A is MN-major
         constexpr float kShift = E8 ? 8.f : 0.f;    // P' reaches 2^8, within e4m3's 448
         bool bad = false;
-        int st = 0, seq = 0, done = 0;              // ring stage, tile of the CTA, tiles of this warpgroup
-        uint32_t ph = 0;
+        int done = 0;                               // tiles of this worker
+        int stk = 0, stv = 0;                       // ring stages
+        uint32_t phk = 0, phv = 0;
         // warp-uniform; after a time-out the warps run through the remaining
         // barriers without issuing or waiting, so none of them is left behind
         auto wait = [&](uint32_t bar, uint32_t parity) {
             if (!bad) bad = !__all_sync(0xffffffffu, mbar_wait(bar, parity, s_abort, a.err, PA_DEVERR_TIMEOUT, a.wait_ns));
         };
-        int shared_b[2], shared_h[2], shared = 0;   // segments of which this CTA has a piece: at most two
+        int shared_b[2], shared = 0;                // requests of whose segment the unit has a part: at most two
         int ticket[2];
-        // this thread's chunk of the piece's query rows, requested while the piece before it ends
-        constexpr int CH = D / 8;               // 8-element chunks of a head row
-        const int qg = tid / CH, qc = tid % CH;
-        auto load_q = [&](const BlkWalk &k) -> uint4 {
-            if (qg >= a.G) return make_uint4(0u, 0u, 0u, 0u);
-            return __ldg(reinterpret_cast<const uint4 *>(a.q + ((int64_t)k.b * a.Hq + k.h * a.G + qg) * D) + qc);
+        // this thread's chunks of the piece's query rows, requested while the piece before it ends
+        constexpr int CH = D / 8;                   // 8-element chunks of a head row
+        constexpr int QR = (GP * CH + 127) / 128;   // chunks per thread
+        uint4 qn[QR];
+        auto load_q = [&](const BlkWalk &k) {
+#pragma unroll
+            for (int r = 0; r < QR; ++r) {
+                const int g = (t + r * 128) / CH, c = (t + r * 128) % CH;
+                qn[r] = make_uint4(0u, 0u, 0u, 0u);
+                if (g < a.G) qn[r] = __ldg(reinterpret_cast<const uint4 *>(a.q + ((int64_t)k.b * a.Hq + k.h * a.G + g) * D) + c);
+            }
         };
-        BlkWalk k = blk_begin(s_pref, a.batch, a.Hkv, W, blockIdx.x), kn = k;
-        uint4 qn = make_uint4(0u, 0u, 0u, 0u);
-        bool more = blk_piece(a, s_pref, s_req, kn);
-        if (more) qn = load_q(kn);
+        for (int unit = worker; unit < units; unit += a.workers) {
+        BlkWalk kn = blk_begin(s_pref, a.batch, a.Hkv, W, unit);
+        bool more = blk_piece(s_pref, s_req, kn);
+        if (more) load_q(kn);
+        shared = 0;
         while (more) {
-            k = kn;
+            const BlkWalk k = kn;
             if (a.wait_ns == 0 && !bad) {
                 // a wait limit of 0: give up at the first item, as a timed-out wait would
                 *s_abort = 1;
@@ -550,9 +604,10 @@ __global__ void __launch_bounds__(kBlkThreads, 1) decode_block_kernel(const __gr
                 bad = true;
             }
             // ---- q as the B operand, rows (term, head)
-            {
-                const int g = qg, c = qc;
-                const uint4 w = qn;
+#pragma unroll
+            for (int r0 = 0; r0 < QR; ++r0) {
+                const int g = (t + r0 * 128) / CH, c = (t + r0 * 128) % CH;
+                const uint4 w = qn[r0];
                 if constexpr (E8) {
                     float x[8];
 #pragma unroll
@@ -588,24 +643,17 @@ __global__ void __launch_bounds__(kBlkThreads, 1) decode_block_kernel(const __gr
                     st_shared_v4(sQ + (c >> 3) * (C::NQ * 128) + blk_off<AW>(g, c & 7), w.x, w.y, w.z, w.w);
                     if (c == 0) s_fq[g] = a.scale_log2;
                 }
-                fence_proxy_async_smem();
-                named_bar_sync(3, kBlkConsumers);
             }
+            fence_proxy_async_smem();
+            named_bar_sync(bar_id, 128);
             float m[GP], r[GP], l[GP], o[GP];
 #pragma unroll
             for (int g = 0; g < GP; ++g) m[g] = r[g] = -INFINITY, l[g] = o[g] = 0.f;
 
-            for (int i = 0; i < k.live; ++i, ++seq) {
-                const int cst = st;
-                const uint32_t cph = ph;
-                if (++st == a.stages) {
-                    st = 0;
-                    ph ^= 1;
-                }
-                if ((seq & 1) != wg) continue;
-                const uint32_t kt = ring + cst * C::STAGE, vt = kt + C::TILE;
-                wait(full + cst * 8, cph);
+            for (int i = 0; i < k.live; ++i, ++done) {
+                const uint32_t kt = kring + stk * C::TILE, vt = vring + stv * C::TILE;
                 // S = K Q^T
+                wait(kfull + stk * 8, phk);
                 if ((warp & 3) == 0) {
                     tc_fence_after();
                     if (!bad) if (elect_one()) {
@@ -616,12 +664,15 @@ __global__ void __launch_bounds__(kBlkThreads, 1) decode_block_kernel(const __gr
                             const uint64_t db = blk_desc<AW>(sQ + (s / SPH) * (C::NQ * AW) + (s % SPH) * 32, 16, 8 * AW);
                             blk_umma<E8>(s_col, da, db, kIdS, s > 0);
                         }
-                        umma_commit(sfull + wg * 8);
+                        umma_commit(sfull);
                     }
                     __syncwarp();
                 }
-                const int ek = meta[cst * kBlkTile + t], ev = E8 ? meta[(kBlkMaxStages + cst) * kBlkTile + t] : 0;
-                wait(sfull + wg * 8, done & 1);
+                const int ek = kmeta[stk * kBlkTile + t];
+                // the V tile has long landed when the weights are there; its exponents are read now
+                wait(vfull + stv * 8, phv);
+                const int ev = E8 ? vmeta[stv * kBlkTile + t] : 0;
+                wait(sfull, done & 1);
                 tc_fence_after();
                 uint32_t sr[C::NQ];
 #pragma unroll
@@ -645,7 +696,7 @@ __global__ void __launch_bounds__(kBlkThreads, 1) decode_block_kernel(const __gr
                     }
                 }
                 // the tile's maxima of s (for l) and of s + ev (for P')
-                float *red = s_max + (wg * 4 + (warp & 3)) * 2 * GP;
+                float *red = s_max + (warp & 3) * 2 * GP;
 #pragma unroll
                 for (int g = 0; g < GP; ++g) {
                     const float mx = warp_max(x[g]), rx = E8 ? warp_max(x[g] + (float)ev) : mx;
@@ -654,12 +705,12 @@ __global__ void __launch_bounds__(kBlkThreads, 1) decode_block_kernel(const __gr
                         red[GP + g] = rx;
                     }
                 }
-                named_bar_sync(1 + wg, 128);
+                named_bar_sync(bar_id, 128);
                 float bt[GP], at[GP];
                 float pp[GP];
 #pragma unroll
                 for (int g = 0; g < GP; ++g) {
-                    const float *w = s_max + wg * 8 * GP + g;
+                    const float *w = s_max + g;
                     const float mt = fmaxf(fmaxf(w[0], w[2 * GP]), fmaxf(w[4 * GP], w[6 * GP]));
                     const float rt = E8 ? fmaxf(fmaxf(w[GP], w[3 * GP]), fmaxf(w[5 * GP], w[7 * GP])) : mt;
                     const float mn = fmaxf(m[g], mt), rn = fmaxf(r[g], rt);
@@ -699,11 +750,12 @@ __global__ void __launch_bounds__(kBlkThreads, 1) decode_block_kernel(const __gr
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
-                named_bar_sync(1 + wg, 128);
-                // O^T = V^T P^T
+                named_bar_sync(bar_id, 128);
+                // O^T = V^T P^T; K's stage is free: its products are done and every thread has read its exponents
                 if ((warp & 3) == 0) {
                     tc_fence_after();
                     if (!bad) if (elect_one()) {
+                        mbar_arrive(kempty + stk * 8);
 #pragma unroll
                         for (int s = 0; s < C::PSteps; ++s) {
                             // V is [token][d]: 32 / ES tokens per step; the second 128-byte half of a bf16 row is the
@@ -712,13 +764,20 @@ __global__ void __launch_bounds__(kBlkThreads, 1) decode_block_kernel(const __gr
                             const uint64_t db = blk_desc<128>(sP + (s >> 2) * (C::NP * 128) + (s & 3) * 32, 16, 1024);
                             blk_umma<E8>(o_col, da, db, kIdO, s > 0);
                         }
-                        umma_commit(ofull + wg * 8);
-                        umma_commit(empty + cst * 8);
+                        umma_commit(ofull);
+                        umma_commit(vempty + stv * 8);
                     }
                     __syncwarp();
                 }
-                wait(ofull + wg * 8, done & 1);
-                ++done;
+                if (++stk == a.stages_k) {
+                    stk = 0;
+                    phk ^= 1;
+                }
+                if (++stv == a.stages_v) {
+                    stv = 0;
+                    phv ^= 1;
+                }
+                wait(ofull, done & 1);
                 tc_fence_after();
                 uint32_t orr[C::NP];
 #pragma unroll
@@ -737,53 +796,36 @@ __global__ void __launch_bounds__(kBlkThreads, 1) decode_block_kernel(const __gr
                 }
             }
 
-            // ---- the item ends: the warpgroup's sums, then both warpgroups
-            blk_next(a, kn);
-            more = blk_piece(a, s_pref, s_req, kn);
-            if (more) qn = load_q(kn);
+            // ---- the piece ends
+            blk_next(kn);
+            more = blk_piece(s_pref, s_req, kn);
+            if (more) load_q(kn);
 #pragma unroll
             for (int g = 0; g < GP; ++g) {
                 float s = l[g];
 #pragma unroll
                 for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-                if (lane == 0) s_sum[(wg * 4 + (warp & 3)) * GP + g] = s;
-                // this warpgroup's O relative to its m: 2^(r - 127 - 8 - m)
-                const float mz = m[g] == -INFINITY ? 0.f : m[g], rz = r[g] == -INFINITY ? 0.f : r[g];
-                o[g] *= blk_ex2(E8 ? rz - mz - 135.f : 0.f);
+                if (lane == 0) s_sum[(warp & 3) * GP + g] = s;
             }
-            float *scratch = reinterpret_cast<float *>(base + C::OffP);      // [GP][D]: warpgroup 1's O
-            named_bar_sync(3, kBlkConsumers);   // the P tiles are free
-            if (wg == 1 && t < D) {
-#pragma unroll
-                for (int g = 0; g < GP; ++g) scratch[g * D + t] = o[g];
-            }
-            if (t == 0) {
-#pragma unroll
-                for (int g = 0; g < GP; ++g) {
-                    const float *w = s_sum + wg * 4 * GP + g;
-                    s_ml[(wg * GP + g) * 2] = m[g];
-                    s_ml[(wg * GP + g) * 2 + 1] = w[0] + w[GP] + w[2 * GP] + w[3 * GP];
-                }
-            }
-            named_bar_sync(3, kBlkConsumers);
+            named_bar_sync(bar_id, 128);
             const bool whole = k.t0 == 0 && k.t1 == k.tb;
-            if (wg == 0 && t < D && !bad) {
-                const int part = (int)blockIdx.x * 2 + (k.t0 == 0 && k.S0 > (int)blockIdx.x * W ? 1 : 0);
+            if (!bad) {
+                const int part = unit * 2 + (k.t0 == 0 && k.S0 % W != 0 ? 1 : 0);
 #pragma unroll
                 for (int g = 0; g < GP; ++g) {
                     if (g >= a.G) break;
-                    const float m0 = s_ml[g * 2], l0 = s_ml[g * 2 + 1], m1 = s_ml[(GP + g) * 2], l1 = s_ml[(GP + g) * 2 + 1];
-                    const float M = fmaxf(m0, m1), Mz = M == -INFINITY ? 0.f : M;
-                    const float w0 = blk_ex2(m0 - Mz), w1 = blk_ex2(m1 - Mz);
-                    const float L = w0 * l0 + w1 * l1, O = w0 * o[g] + w1 * scratch[g * D + t];
+                    const float L = s_sum[g] + s_sum[GP + g] + s_sum[2 * GP + g] + s_sum[3 * GP + g];
+                    // O relative to m: 2^(r - 127 - 8 - m)
+                    const float mz = m[g] == -INFINITY ? 0.f : m[g], rz = r[g] == -INFINITY ? 0.f : r[g];
+                    const float O = E8 ? o[g] * blk_ex2(rz - mz - 135.f) : o[g];
                     const int64_t hq = (int64_t)k.b * a.Hq + k.h * a.G + g;
                     if (whole) {
-                        a.out[hq * D + t] = __float2bfloat16_rn(L != 0.f ? O / L : 0.f);
-                        if (WT && t == 0) a.lse[hq] = L != 0.f ? M + log2f(L) : INFINITY;
+                        if (t < D) a.out[hq * D + t] = __float2bfloat16_rn(L != 0.f ? O / L : 0.f);
+                        if (WT && t == 0) a.lse[hq] = L != 0.f ? m[g] + log2f(L) : INFINITY;
                     } else {
-                        a.o_part[((int64_t)part * a.G + g) * D + t] = O;
+                        if (t < D) a.o_part[((int64_t)part * a.G + g) * D + t] = O;
                         if (t == 0) {
-                            a.ml_part[(part * a.G + g) * 2] = M;
+                            a.ml_part[(part * a.G + g) * 2] = m[g];
                             a.ml_part[(part * a.G + g) * 2 + 1] = L;
                         }
                     }
@@ -791,42 +833,42 @@ __global__ void __launch_bounds__(kBlkThreads, 1) decode_block_kernel(const __gr
             }
             if (!whole) {
                 // a ticket for the piece: the barrier orders the partials' stores before thread 0's acquire-release
-                // addition; the answer is looked at after the CTA's last piece
-                if (wg == 0) {
-                    named_bar_sync(1, 128);
-                    if (t == 0 && !bad) {
-                        const int old = atom_add_acq_rel_gpu(a.tickets + k.S0 / W, 1);
-                        if (shared == 0) ticket[0] = old;
-                        else ticket[1] = old;
-                    }
+                // addition; the answer is looked at after the unit's last piece
+                named_bar_sync(bar_id, 128);
+                if (t == 0 && !bad) {
+                    const int old = atom_add_acq_rel_gpu(a.tickets + k.S0 / W * a.Hkv + k.h, 1);
+                    if (shared == 0) ticket[0] = old;
+                    else ticket[1] = old;
                 }
-                if (shared == 0) shared_b[0] = k.b, shared_h[0] = k.h;
-                else shared_b[1] = k.b, shared_h[1] = k.h;
+                if (shared == 0) shared_b[0] = k.b;
+                else shared_b[1] = k.b;
                 ++shared;
             }
         }
-        // shared segments whose last piece was this CTA's
+        // shared segments whose last piece was this unit's
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             if (i >= shared) break;
-            const BlkSpan s = blk_span(s_pref, a.batch, W, shared_b[i], shared_h[i]);
-            if (tid == 0) s_last[i] = !bad && ticket[i] == s.c1 - s.c0;
-            named_bar_sync(3, kBlkConsumers);
-            if (s_last[i]) {
-                blk_merge<D, GP, WT>(a, s, W, shared_b[i], shared_h[i]);
-                if (tid == 0) a.tickets[s.c0] = 0;
+            const BlkSpan s = blk_span(s_pref, W, shared_b[i]);
+            const int h = unit % a.Hkv;
+            if (t == 0) s_last[wg][i] = !bad && ticket[i] == s.i1 - s.i0;
+            named_bar_sync(bar_id, 128);
+            if (s_last[wg][i]) {
+                blk_merge<D, GP, WT>(a, s, shared_b[i], h, t, bar_id, reinterpret_cast<float *>(smem_raw + (kring - raw)));
+                if (t == 0) a.tickets[s.i0 * a.Hkv + h] = 0;
             }
+        }
         }
         if (__any_sync(0xffffffffu, *s_abort) && (warp & 3) == 0) {
             // aborted: every MMA this lane issued completes before tensor memory is freed
-            if (elect_one()) umma_commit(drain + wg * 8);
+            if (elect_one()) umma_commit(drain);
             __syncwarp();
-            mbar_drain(drain + wg * 8, 0);
+            mbar_drain(drain, 0);
             __syncwarp();
         }
     }
     __syncthreads();
-    if (warp == 0) {
+    if (warp == 4) {
         tc_fence_after();
         tmem_dealloc(tmem, kBlkTmemCols);
     }
@@ -882,18 +924,24 @@ template <int D, bool E8, int GP, bool WT>
 static pa_status launch_block(BlkArgs a, cudaStream_t st)
 {
     using C = BlkCfg<D, E8, GP>;
-    int stages = (int)((kBlkSmemLimit - C::fixed(a.batch)) / C::STAGE);
-    a.stages = stages < kBlkMaxStages ? stages : kBlkMaxStages;
-    static_assert(C::bytes(kBlkMaxBatch, 2) <= kBlkSmemLimit, "two stages fit at the largest batch");
+    // ring stages per worker and operand: as many as fit, K one more than V where half a stage is left
+    const int tiles = (int)((kBlkSmemLimit - C::fixed(a.batch)) / C::TILE) / 2;
+    a.stages_v = tiles / 2 < kBlkMaxStages ? tiles / 2 : kBlkMaxStages;
+    a.stages_k = tiles - a.stages_v < kBlkMaxStages ? tiles - a.stages_v : kBlkMaxStages;
+    static_assert((kBlkSmemLimit - C::fixed(kBlkMaxBatch)) / C::TILE >= 4, "a stage per worker and operand fits at the largest batch");
+    constexpr int kLeast = (int)((kBlkSmemLimit - C::fixed(kBlkMaxBatch)) / C::TILE) / 2;
+    static_assert((kLeast < 2 * kBlkMaxStages ? kLeast : 2 * kBlkMaxStages) * C::TILE >=
+                      (32 + kBlkMaxWorkers * GP + 4 + 4 * GP * D) * 4, "the merge's scratch fits a worker's ring");
     auto kern = decode_block_kernel<D, E8, GP, WT>;
-    const size_t smem = C::bytes(a.batch, a.stages);
+    const size_t smem = C::fixed(a.batch) + (size_t)2 * (a.stages_k + a.stages_v) * C::TILE;
     if (!ensure_dynamic_smem(reinterpret_cast<const void *>(kern), smem)) return PA_ERR_CUDA;
-    a.grid = num_sms() < kBlkMaxCtas ? num_sms() : kBlkMaxCtas;
-    if (launch_kernel(kern, dim3(a.grid), dim3(kBlkThreads), smem, st, a) != cudaSuccess) return PA_ERR_CUDA;
+    const int grid = num_sms() < kBlkMaxWorkers / 2 ? num_sms() : kBlkMaxWorkers / 2;
+    a.workers = 2 * grid;
+    if (launch_kernel(kern, dim3(grid), dim3(kBlkThreads), smem, st, a) != cudaSuccess) return PA_ERR_CUDA;
     if constexpr (WT) {
         const size_t wsmem = ((size_t)a.batch + 1) * 4 + (size_t)a.Hq * 4;
         if (!ensure_dynamic_smem(reinterpret_cast<const void *>(decode_block_weights_kernel), wsmem)) return PA_ERR_CUDA;
-        if (launch_kernel(decode_block_weights_kernel, dim3(4 * a.grid), dim3(kBlkWeightThreads), wsmem, st, a) != cudaSuccess)
+        if (launch_kernel(decode_block_weights_kernel, dim3(4 * grid), dim3(kBlkWeightThreads), wsmem, st, a) != cudaSuccess)
             return PA_ERR_CUDA;
     }
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;

@@ -5,8 +5,8 @@
 
 namespace pa {
 
-// Workspace: header, tickets (one per CTA, zero between calls), partials (two
-// slots per CTA), log-sum-exps, then the score tiles (weights calls).  Offsets
+// Workspace: header, tickets (one per worker, zero between calls), partials (two
+// slots per worker), log-sum-exps, then the score tiles (weights calls).  Offsets
 // depend on the head counts alone; the tickets' on nothing.
 struct BlkWs {
     size_t tickets_off, ml_off, o_off, lse_off, scores_off;
@@ -16,9 +16,9 @@ inline BlkWs blk_ws(int Hq, int Hkv, int D)
     const int G = Hq / Hkv;
     BlkWs w;
     w.tickets_off = kWorkspaceHeader;
-    w.ml_off = align_up(w.tickets_off + kBlkMaxCtas * 4, 256);
-    w.o_off = align_up(w.ml_off + (size_t)2 * kBlkMaxCtas * G * 2 * 4, 256);
-    w.lse_off = align_up(w.o_off + (size_t)2 * kBlkMaxCtas * G * D * 4, 256);
+    w.ml_off = align_up(w.tickets_off + kBlkMaxWorkers * 4, 256);
+    w.o_off = align_up(w.ml_off + (size_t)2 * kBlkMaxWorkers * G * 2 * 4, 256);
+    w.lse_off = align_up(w.o_off + (size_t)2 * kBlkMaxWorkers * G * D * 4, 256);
     w.scores_off = align_up(w.lse_off + (size_t)kBlkMaxBatch * Hq * 4, 256);
     return w;
 }

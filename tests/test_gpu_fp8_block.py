@@ -203,7 +203,7 @@ def test_decode_long_and_deterministic(D):
     q = torch.randn((3, 8, D), generator=c.g).to(torch.bfloat16)
     out, ws = decode(c, q.cuda(), 0.06)
     again, _ = decode(c, q.cuda(), 0.06)
-    ws[1024:].random_(0, 255)         # all but the header and the merge tickets
+    ws[2048:].random_(0, 255)         # all but the header and the merge tickets
     third, _ = decode(c, q.cuda(), 0.06, ws=ws)
     assert torch.equal(out.view(torch.int16), again.view(torch.int16))
     assert torch.equal(out.view(torch.int16), third.view(torch.int16))
