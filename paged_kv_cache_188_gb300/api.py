@@ -253,64 +253,80 @@ def pa_kv_store_fp8(k_buf, v_buf, layer_id, k_new, v_new, loc, k_scale, v_scale,
                                                  T, _p(k_scale), _p(v_scale), _p(error_word), _stream(stream)))
 
 
-def _one_device(*tensors):
-    """All on one device, and that the current one: the library works on the
-    current device and stream."""
-    devs = {t.device for t in tensors if t is not None}
-    if len(devs) != 1 or next(iter(devs)).index != torch.cuda.current_device():
-        raise ValueError(f"tensors must be on the current CUDA device, got {sorted(map(str, devs))}")
+def _device():
+    """The current device's number; the library works on it and on its current stream."""
+    return torch.cuda.current_device()
 
 
-def _kv_shape_block(k_buf, v_buf, k_exp, v_exp, block):
+def _raw_stream(stream, dev):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _all(dev, *specs):
+    """Checks (tensor, dtype, dims, name): contiguous, of that type and number of
+    dimensions, on device ``dev``.  One pass of cheap comparisons; the words are
+    found only for a tensor that fails."""
+    for t, dtype, ndim, name in specs:
+        if t.dtype is not dtype or t.dim() != ndim or t.get_device() != dev or not t.is_contiguous():
+            _need(t, dtype, name, ndim)
+            raise ValueError(f"{name} must be on the current CUDA device {dev}, got {t.device}")
+
+
+def _word(dev, error_word):
+    """Pointer of an optional device error word."""
+    if error_word is None:
+        return None
+    _need(error_word, torch.int32, "error_word")
+    if error_word.get_device() != dev or error_word.numel() < 1:
+        raise ValueError(f"error_word must be an int32 on the current CUDA device {dev}")
+    return error_word.data_ptr()
+
+
+_BLOCKS = frozenset((1, 2, 4, 8, 16, 32, 64, 128))
+
+
+def _kv_shape_block(dev, k_buf, v_buf, k_exp, v_exp, block):
     """A block-scaled e4m3 cache: byte buffers [n_layers, size, Hkv, D] and uint8
     exponents [n_layers, ceil(size / block), Hkv]."""
-    for t, name in ((k_buf, "k_buf"), (v_buf, "v_buf")):
-        if t.dtype not in FP8_DTYPES:
-            raise TypeError(f"{name} must be uint8 or float8_e4m3fn, got {t.dtype}")
-        _need(t, t.dtype, name, 4)
-    if k_buf.shape != v_buf.shape:
-        raise ValueError("k_buf and v_buf shapes differ")
-    _need(k_exp, torch.uint8, "k_exp", 3)
-    _need(v_exp, torch.uint8, "v_exp", 3)
-    n_layers, size, Hkv, _ = k_buf.shape
-    if block not in (1, 2, 4, 8, 16, 32, 64, 128):
+    if k_buf.dtype not in FP8_DTYPES or v_buf.dtype not in FP8_DTYPES:
+        raise TypeError(f"k_buf and v_buf must be uint8 or float8_e4m3fn, got {k_buf.dtype} and {v_buf.dtype}")
+    if block not in _BLOCKS:
         raise ValueError(f"block must be a power of two from 1 to 128, got {block}")
-    if tuple(k_exp.shape) != (n_layers, -(-size // block), Hkv) or v_exp.shape != k_exp.shape:
+    _all(dev, (k_buf, k_buf.dtype, 4, "k_buf"), (v_buf, v_buf.dtype, 4, "v_buf"), (k_exp, torch.uint8, 3, "k_exp"),
+         (v_exp, torch.uint8, 3, "v_exp"))
+    n_layers, size, Hkv, D = shape = k_buf.shape
+    if v_buf.shape != shape:
+        raise ValueError("k_buf and v_buf shapes differ")
+    if k_exp.shape != (n_layers, -(-size // block), Hkv) or v_exp.shape != k_exp.shape:
         raise ValueError("k_exp / v_exp must be [n_layers, ceil(size / block), n_kv_heads]")
-    return KvShape(*k_buf.shape)
+    return KvShape(n_layers, size, Hkv, D)
 
 
 def pa_kv_store_fp8_block(k_buf, v_buf, layer_id, k_new, v_new, loc, k_exp, v_exp, block, error_word=None, stream=None):
     """KV store into an e4m3 cache with a power-of-two scale per (block of slots,
     kv head): scales rise as needed, a block's earlier rows are rounded to a
     risen scale.  Tokens of one block stand next to each other in ``loc``."""
-    s = _kv_shape_block(k_buf, v_buf, k_exp, v_exp, block)
-    _need(k_new, torch.bfloat16, "k_new", 3)
-    _need(v_new, torch.bfloat16, "v_new", 3)
-    _need(loc, torch.int32, "loc", 1)
-    T = loc.numel()
-    if tuple(k_new.shape) != (T, s.n_kv_heads, s.head_dim) or v_new.shape != k_new.shape:
+    dev = _device()
+    s = _kv_shape_block(dev, k_buf, v_buf, k_exp, v_exp, block)
+    _all(dev, (k_new, torch.bfloat16, 3, "k_new"), (v_new, torch.bfloat16, 3, "v_new"), (loc, torch.int32, 1, "loc"))
+    T = loc.shape[0]
+    if k_new.shape != (T, s.n_kv_heads, s.head_dim) or v_new.shape != k_new.shape:
         raise ValueError("k_new / v_new must be [n_tokens, n_kv_heads, head_dim]")
-    if error_word is not None:
-        _need(error_word, torch.int32, "error_word")
-    _one_device(k_buf, v_buf, k_new, v_new, loc, k_exp, v_exp, error_word)
     _ok("pa_kv_store_fp8_block", lib().pa_kv_store_fp8_block(
-        _p(k_buf), _p(v_buf), s, layer_id, _p(k_new), _p(v_new), _p(loc), T, _p(k_exp), _p(v_exp), block,
-        _p(error_word), _stream(stream)))
+        k_buf.data_ptr(), v_buf.data_ptr(), s, layer_id, k_new.data_ptr(), v_new.data_ptr(), loc.data_ptr(), T,
+        k_exp.data_ptr(), v_exp.data_ptr(), block, _word(dev, error_word), _raw_stream(stream, dev)))
 
 
 def pa_kv_reset_fp8_block(k_exp, v_exp, blocks, error_word=None, stream=None):
     """Mark the listed blocks (int32) empty in every layer of a block-scaled cache."""
-    _need(k_exp, torch.uint8, "k_exp", 3)
-    _need(v_exp, torch.uint8, "v_exp", 3)
-    _need(blocks, torch.int32, "blocks", 1)
+    dev = _device()
+    _all(dev, (k_exp, torch.uint8, 3, "k_exp"), (v_exp, torch.uint8, 3, "v_exp"), (blocks, torch.int32, 1, "blocks"))
     if v_exp.shape != k_exp.shape:
         raise ValueError("k_exp and v_exp shapes differ")
-    if error_word is not None:
-        _need(error_word, torch.int32, "error_word")
-    _one_device(k_exp, v_exp, blocks, error_word)
+    n_layers, n_blocks, Hkv = k_exp.shape
     _ok("pa_kv_reset_fp8_block", lib().pa_kv_reset_fp8_block(
-        _p(k_exp), _p(v_exp), *k_exp.shape, _p(blocks), blocks.numel(), _p(error_word), _stream(stream)))
+        k_exp.data_ptr(), v_exp.data_ptr(), n_layers, n_blocks, Hkv, blocks.data_ptr(), blocks.shape[0],
+        _word(dev, error_word), _raw_stream(stream, dev)))
 
 
 def pa_rope_packed(q, k, positions, cos_tab, sin_tab, error_word=None, stream=None):
@@ -380,15 +396,12 @@ def pa_decode_weights_workspace_bytes(max_batch, max_tokens, n_q_heads, n_kv_hea
     return int(lib().pa_decode_weights_workspace_bytes(max_batch, max_tokens, n_q_heads, n_kv_heads, head_dim))
 
 
-def _decode_tensors(q, out, req_to_token, req_pool_indices, seq_lens, workspace, s):
-    _need(q, torch.bfloat16, "q", 3)
-    _need(out, torch.bfloat16, "out", 3)
-    _need(req_to_token, torch.int32, "req_to_token", 2)
-    _need(req_pool_indices, torch.int32, "req_pool_indices", 1)
-    _need(seq_lens, torch.int32, "seq_lens", 1)
-    _need(workspace, torch.uint8, "workspace")
-    B, Hq, D = q.shape
-    if out.shape != q.shape or D != s.head_dim or req_pool_indices.numel() != B or seq_lens.numel() != B:
+def _decode_tensors(dev, q, out, req_to_token, req_pool_indices, seq_lens, workspace, s):
+    _all(dev, (q, torch.bfloat16, 3, "q"), (out, torch.bfloat16, 3, "out"), (req_to_token, torch.int32, 2, "req_to_token"),
+         (req_pool_indices, torch.int32, 1, "req_pool_indices"), (seq_lens, torch.int32, 1, "seq_lens"),
+         (workspace, torch.uint8, 1, "workspace"))
+    B, Hq, D = shape = q.shape
+    if out.shape != shape or D != s.head_dim or req_pool_indices.shape[0] != B or seq_lens.shape[0] != B:
         raise ValueError("q/out [batch, n_q_heads, head_dim], req_pool_indices/seq_lens [batch] expected")
     return B, Hq
 
@@ -396,13 +409,14 @@ def _decode_tensors(q, out, req_to_token, req_pool_indices, seq_lens, workspace,
 def pa_paged_decode_attn_fp8_block(q, k_buf, v_buf, layer_id, req_to_token, req_pool_indices, seq_lens, scale,
                                    k_exp, v_exp, block, workspace, out, stream=None):
     """Decode attention over a block-scaled e4m3 cache."""
-    s = _kv_shape_block(k_buf, v_buf, k_exp, v_exp, block)
-    B, Hq = _decode_tensors(q, out, req_to_token, req_pool_indices, seq_lens, workspace, s)
-    _one_device(q, k_buf, v_buf, req_to_token, req_pool_indices, seq_lens, k_exp, v_exp, workspace, out)
+    dev = _device()
+    s = _kv_shape_block(dev, k_buf, v_buf, k_exp, v_exp, block)
+    B, Hq = _decode_tensors(dev, q, out, req_to_token, req_pool_indices, seq_lens, workspace, s)
+    req_rows, max_ctx = req_to_token.shape
     _ok("pa_paged_decode_attn_fp8_block", lib().pa_paged_decode_attn_fp8_block(
-        _p(q), B, Hq, _p(k_buf), _p(v_buf), s, layer_id, _p(req_to_token), req_to_token.shape[0],
-        req_to_token.shape[1], _p(req_pool_indices), _p(seq_lens), float(scale), _p(k_exp), _p(v_exp), block,
-        _p(workspace), workspace.numel(), _p(out), _stream(stream)))
+        q.data_ptr(), B, Hq, k_buf.data_ptr(), v_buf.data_ptr(), s, layer_id, req_to_token.data_ptr(), req_rows, max_ctx,
+        req_pool_indices.data_ptr(), seq_lens.data_ptr(), scale, k_exp.data_ptr(), v_exp.data_ptr(), block,
+        workspace.data_ptr(), workspace.shape[0], out.data_ptr(), _raw_stream(stream, dev)))
 
 
 def pa_paged_decode_attn_weights(q, k_buf, v_buf, layer_id, req_to_token, req_pool_indices, seq_lens, scale, weights,
@@ -411,19 +425,25 @@ def pa_paged_decode_attn_weights(q, k_buf, v_buf, layer_id, req_to_token, req_po
     ``v_exp``) a block-scaled e4m3 cache, that also adds each cached token's
     attention weight, summed over the query heads, to ``weights`` (fp32, shaped
     like ``req_to_token``)."""
+    dev = _device()
     if block == 0 and k_exp is None and v_exp is None:
+        _all(dev, (k_buf, torch.bfloat16, 4, "k_buf"), (v_buf, torch.bfloat16, 4, "v_buf"))
         s = _kv_shape(k_buf, v_buf)
+        ke = ve = None
     else:
-        s = _kv_shape_block(k_buf, v_buf, k_exp, v_exp, block)
-    B, Hq = _decode_tensors(q, out, req_to_token, req_pool_indices, seq_lens, workspace, s)
-    _need(weights, torch.float32, "weights", 2)
-    if weights.shape != req_to_token.shape:
+        if k_exp is None or v_exp is None:
+            raise ValueError("a block-scaled cache needs k_exp and v_exp")
+        s = _kv_shape_block(dev, k_buf, v_buf, k_exp, v_exp, block)
+        ke, ve = k_exp.data_ptr(), v_exp.data_ptr()
+    B, Hq = _decode_tensors(dev, q, out, req_to_token, req_pool_indices, seq_lens, workspace, s)
+    _all(dev, (weights, torch.float32, 2, "weights"))
+    req_rows, max_ctx = shape = req_to_token.shape
+    if weights.shape != shape:
         raise ValueError("weights must have the shape of req_to_token")
-    _one_device(q, k_buf, v_buf, req_to_token, req_pool_indices, seq_lens, k_exp, v_exp, weights, workspace, out)
     _ok("pa_paged_decode_attn_weights", lib().pa_paged_decode_attn_weights(
-        _p(q), B, Hq, _p(k_buf), _p(v_buf), s, layer_id, _p(req_to_token), req_to_token.shape[0],
-        req_to_token.shape[1], _p(req_pool_indices), _p(seq_lens), float(scale), _p(k_exp), _p(v_exp), block,
-        _p(weights), _p(workspace), workspace.numel(), _p(out), _stream(stream)))
+        q.data_ptr(), B, Hq, k_buf.data_ptr(), v_buf.data_ptr(), s, layer_id, req_to_token.data_ptr(), req_rows, max_ctx,
+        req_pool_indices.data_ptr(), seq_lens.data_ptr(), scale, ke, ve, block, weights.data_ptr(), workspace.data_ptr(),
+        workspace.shape[0], out.data_ptr(), _raw_stream(stream, dev)))
 
 
 def pa_kv_evict(req_to_token, req_pool_indices, seq_lens, weights, budget, recent, new_lens, freed, error_word=None,
@@ -431,23 +451,20 @@ def pa_kv_evict(req_to_token, req_pool_indices, seq_lens, weights, budget, recen
     """Cut every request of more than ``budget`` tokens to its last ``recent`` and
     its heaviest others: table row and weights compacted in place, the evicted
     slots listed in ``freed`` (int32 [batch, max_ctx]), lengths in ``new_lens``."""
-    _need(req_to_token, torch.int32, "req_to_token", 2)
-    _need(req_pool_indices, torch.int32, "req_pool_indices", 1)
-    _need(seq_lens, torch.int32, "seq_lens", 1)
-    _need(weights, torch.float32, "weights", 2)
-    _need(new_lens, torch.int32, "new_lens", 1)
-    _need(freed, torch.int32, "freed", 2)
-    B = seq_lens.numel()
-    if weights.shape != req_to_token.shape or req_pool_indices.numel() != B or new_lens.numel() != B:
+    dev = _device()
+    _all(dev, (req_to_token, torch.int32, 2, "req_to_token"), (req_pool_indices, torch.int32, 1, "req_pool_indices"),
+         (seq_lens, torch.int32, 1, "seq_lens"), (weights, torch.float32, 2, "weights"),
+         (new_lens, torch.int32, 1, "new_lens"), (freed, torch.int32, 2, "freed"))
+    B = seq_lens.shape[0]
+    req_rows, max_ctx = shape = req_to_token.shape
+    if weights.shape != shape or req_pool_indices.shape[0] != B or new_lens.shape[0] != B:
         raise ValueError("weights like req_to_token, req_pool_indices / seq_lens / new_lens [batch] expected")
-    if tuple(freed.shape) != (B, req_to_token.shape[1]):
+    if freed.shape != (B, max_ctx):
         raise ValueError("freed must be [batch, max_ctx]")
-    if error_word is not None:
-        _need(error_word, torch.int32, "error_word")
-    _one_device(req_to_token, req_pool_indices, seq_lens, weights, new_lens, freed, error_word)
     _ok("pa_kv_evict", lib().pa_kv_evict(
-        _p(req_to_token), req_to_token.shape[0], req_to_token.shape[1], _p(req_pool_indices), _p(seq_lens), B,
-        _p(weights), int(budget), int(recent), _p(new_lens), _p(freed), _p(error_word), _stream(stream)))
+        req_to_token.data_ptr(), req_rows, max_ctx, req_pool_indices.data_ptr(), seq_lens.data_ptr(), B,
+        weights.data_ptr(), budget, recent, new_lens.data_ptr(), freed.data_ptr(), _word(dev, error_word),
+        _raw_stream(stream, dev)))
 
 
 def pa_decode_step(q, k_new, v_new, positions, cos_tab, sin_tab, k_buf, v_buf, layer_id, loc, req_to_token,
@@ -536,23 +553,20 @@ def pa_paged_prefill_attn_fp8(q, k_buf, v_buf, layer_id, qo_indptr, kv_indptr, r
 def pa_paged_prefill_attn_fp8_block(q, k_buf, v_buf, layer_id, qo_indptr, kv_indptr, req_to_token, req_pool_indices,
                                     scale, k_exp, v_exp, block, workspace, out, stream=None):
     """Ragged causal prefill over a block-scaled e4m3 cache."""
-    s = _kv_shape_block(k_buf, v_buf, k_exp, v_exp, block)
-    _need(q, torch.bfloat16, "q", 3)
-    _need(out, torch.bfloat16, "out", 3)
-    _need(qo_indptr, torch.int32, "qo_indptr", 1)
-    _need(kv_indptr, torch.int32, "kv_indptr", 1)
-    _need(req_to_token, torch.int32, "req_to_token", 2)
-    _need(req_pool_indices, torch.int32, "req_pool_indices", 1)
-    _need(workspace, torch.uint8, "workspace")
-    T, Hq, D = q.shape
-    R = qo_indptr.numel() - 1
-    if out.shape != q.shape or D != s.head_dim or kv_indptr.numel() != R + 1 or req_pool_indices.numel() != R:
+    dev = _device()
+    s = _kv_shape_block(dev, k_buf, v_buf, k_exp, v_exp, block)
+    _all(dev, (q, torch.bfloat16, 3, "q"), (out, torch.bfloat16, 3, "out"), (qo_indptr, torch.int32, 1, "qo_indptr"),
+         (kv_indptr, torch.int32, 1, "kv_indptr"), (req_to_token, torch.int32, 2, "req_to_token"),
+         (req_pool_indices, torch.int32, 1, "req_pool_indices"), (workspace, torch.uint8, 1, "workspace"))
+    T, Hq, D = shape = q.shape
+    R = qo_indptr.shape[0] - 1
+    if out.shape != shape or D != s.head_dim or kv_indptr.shape[0] != R + 1 or req_pool_indices.shape[0] != R:
         raise ValueError("q/out [T, Hq, D], qo/kv_indptr [R+1], req_pool_indices [R] expected")
-    _one_device(q, k_buf, v_buf, qo_indptr, kv_indptr, req_to_token, req_pool_indices, k_exp, v_exp, workspace, out)
+    req_rows, max_ctx = req_to_token.shape
     _ok("pa_paged_prefill_attn_fp8_block", lib().pa_paged_prefill_attn_fp8_block(
-        _p(q), T, Hq, _p(k_buf), _p(v_buf), s, layer_id, _p(qo_indptr), _p(kv_indptr), R, _p(req_to_token),
-        req_to_token.shape[0], req_to_token.shape[1], _p(req_pool_indices), float(scale), _p(k_exp), _p(v_exp), block,
-        _p(workspace), workspace.numel(), _p(out), _stream(stream)))
+        q.data_ptr(), T, Hq, k_buf.data_ptr(), v_buf.data_ptr(), s, layer_id, qo_indptr.data_ptr(), kv_indptr.data_ptr(),
+        R, req_to_token.data_ptr(), req_rows, max_ctx, req_pool_indices.data_ptr(), scale, k_exp.data_ptr(),
+        v_exp.data_ptr(), block, workspace.data_ptr(), workspace.shape[0], out.data_ptr(), _raw_stream(stream, dev)))
 
 
 def pa_paged_prefill_attn(q, k_buf, v_buf, layer_id, qo_indptr, kv_indptr, req_to_token, req_pool_indices,

@@ -116,15 +116,20 @@ def test_evict_refusals(lib):
     assert call(batch=0, t=0) == 0
 
 
-def test_wrappers_refuse_before_the_library():
+def test_wrappers_refuse_before_the_library(monkeypatch):
+    monkeypatch.setattr(api, "_device", lambda: 0)
     u8 = torch.zeros((1, 32, 2, 64), dtype=torch.uint8)
     e = torch.zeros((1, 2, 2), dtype=torch.uint8)
     with pytest.raises(TypeError, match="uint8 or float8_e4m3fn"):
         api.pa_kv_store_fp8_block(u8.bfloat16(), u8.bfloat16(), 0, None, None, None, e, e, 16)
     with pytest.raises(TypeError, match="CUDA tensor"):
         api.pa_kv_store_fp8_block(u8, u8, 0, None, None, None, e, e, 16)
+    with pytest.raises(ValueError, match="power of two"):
+        api.pa_kv_store_fp8_block(u8, u8, 0, None, None, None, e, e, 12)
     with pytest.raises(TypeError, match="CUDA tensor"):
         api.pa_kv_evict(torch.zeros((1, 4), dtype=torch.int32), None, None, None, 1, 0, None, None)
+    with pytest.raises(ValueError, match="needs k_exp"):
+        api.pa_paged_decode_attn_weights(None, u8, u8, 0, None, None, None, 0.1, None, None, None, block=16)
 
 
 # ------------------------------------------------ the reference itself
