@@ -331,7 +331,8 @@ pa_status pa_paged_prefill_attn_fp8(const void *q, int n_tokens, int n_q_heads, 
  *
  * pa_kv_store_fp8_block: the new tokens' K/V at slots loc[t].  For the rows x
  * of the call that fall into a block, and one kv head,
- *     e    = max(e_old, the smallest e in [1, 254] with amax |x| <= 448 * 2^(e - 127))
+ *     e    = max(e_old, the smallest e in [1, 254] with amax |x| <= 448 * 2^(e - 127),
+ *            0 where every x is 0)
  *     byte = e4m3(x * 2^(127 - e))     (nearest even; finite overflow and
  *            infinities saturate to +-448, a NaN stays NaN; amax over finite x)
  * and where e > e_old > 0 the block's other rows are rounded to the new scale:
@@ -339,8 +340,9 @@ pa_status pa_paged_prefill_attn_fp8(const void *q, int n_tokens, int n_q_heads, 
  * hand a page out again through pa_kv_reset_fp8_block, or its rows keep the
  * largest scale the block ever had.  The tokens of one call that fall into one
  * block must stand next to each other in loc (true where a block belongs to
- * one request and its tokens are packed in order), and locations must be
- * distinct, else the block's bytes are undefined.  Bad locations are skipped
+ * one request and its tokens are packed in order; a bad location between them
+ * parts them), and locations must be distinct, else the block's bytes are
+ * undefined.  Bad locations are skipped
  * (PA_DEVERR_SLOT), as in pa_kv_store.  n_tokens == 0 is a no-op. */
 pa_status pa_kv_store_fp8_block(void *k_buf, void *v_buf, pa_kv_shape s, int layer_id, const void *k_new,
                                 const void *v_new, const int32_t *loc, int n_tokens, uint8_t *k_exp,

@@ -146,10 +146,12 @@ static_assert(N_BARS <= 32, "barrier area holds 32 barriers");
 // (and the warp synchronised) before any of its bf16 chunks is written, so
 // the in-place D = 128 layout is safe.  Exact: e4m3 values are bf16 numbers,
 // and so are their products with a block-scaled row's power of two (BLK:
-// exps[r] is row r's exponent byte e, and e << 7 the bf16 number 2^(e - 127)).
+// exps[r] is row r's exponent byte e, and e << 7 the bf16 number 2^(e - 127);
+// 255 marks a position without a row, which becomes zeros).
 template <int D, bool BLK = false>
 __device__ __forceinline__ void widen_e4m3_tile(uint32_t src, uint32_t dst, int lane, const unsigned char *exps = nullptr)
 {
+    constexpr int PITCH = BLK ? D : 128;   // bytes between rows as loaded
     constexpr int LPR = D / 16;     // lanes per row
     constexpr int RPP = 32 / LPR;   // rows per pass of the warp
     constexpr int U = 4;            // passes whose loads are in flight together
@@ -158,7 +160,7 @@ __device__ __forceinline__ void widen_e4m3_tile(uint32_t src, uint32_t dst, int 
     for (int r0 = 0; r0 < kPfKeys; r0 += RPP * U) {
         uint4 v[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) v[u] = ld_shared_v4(src + (uint32_t)((r0 + u * RPP + rr) * 128 + j * 16));
+        for (int u = 0; u < U; ++u) v[u] = ld_shared_v4(src + (uint32_t)((r0 + u * RPP + rr) * PITCH + j * 16));
         __syncwarp();
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -166,7 +168,7 @@ __device__ __forceinline__ void widen_e4m3_tile(uint32_t src, uint32_t dst, int 
             const uint32_t sc = BLK ? (uint32_t)exps[r] * 0x00800080u : 0u;
             auto wide = [&](uint32_t two) -> uint32_t {
                 const uint32_t w = e4m3x2_to_bf16x2(two);
-                return BLK ? mul_bf16x2(w, sc) : w;
+                return !BLK ? w : sc == 0x7F807F80u ? 0u : mul_bf16x2(w, sc);
             };
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -406,8 +408,8 @@ __global__ void __launch_bounds__(F8 ? kPfThreadsF8 : kPfThreads, 1)
                 for (int e = 0; e < 4; ++e) {
                     const bool in = r[e] >= 0 && r[e] < p.size;
                     const int64_t at = in ? (int64_t)(r[e] >> p.block_shift) * p.Hkv + I.h : 0;
-                    exk[e] = in ? __ldcg(p.k_exp + at) : 0;
-                    exv[e] = in ? __ldcg(p.v_exp + at) : 0;
+                    exk[e] = in ? __ldcg(p.k_exp + at) : 255;
+                    exv[e] = in ? __ldcg(p.v_exp + at) : 255;
                 }
             };
             if constexpr (BLK) {
@@ -460,10 +462,26 @@ __global__ void __launch_bounds__(F8 ? kPfThreadsF8 : kPfThreads, 1)
                                   slot[1] == slot[0] + 1 && slot[2] == slot[0] + 2 && slot[3] == slot[0] + 3;
                 const unsigned contig = __ballot_sync(0xffffffffu, mine);
                 const unsigned anyok = __ballot_sync(0xffffffffu, okp[0] || okp[1] || okp[2] || okp[3]);
+                // (BLK) a valid row of the tile, slot 0 if it has none
+                const int mine_slot = okp[0] ? slot[0] : okp[1] ? slot[1] : okp[2] ? slot[2] : okp[3] ? slot[3] : 0;
+                const int some = __shfl_sync(0xffffffffu, mine_slot, anyok ? __ffs(anyok) - 1 : 0);
                 const bool g_contig = ((contig >> (lane & ~3)) & 0xFu) == 0xFu;
                 const bool g_empty = ((anyok >> (lane & ~3)) & 0xFu) == 0u;
 
                 auto issue = [&](const CUtensorMap *m16, const CUtensorMap *m1, uint32_t dst, uint32_t b) {
+                    if constexpr (BLK) {
+                        // D-byte rows packed: a 16-row box per page group,
+                        // else four rows per gather4 copy; a position without
+                        // a row repeats a valid one (its exponent byte says so)
+                        if (g_contig) {
+                            if (sub == 0) tma_load_2d(dst + gi * 16 * D, m16, col0, row0 + s0, b);
+                        } else {
+                            tma_gather4(dst + lane * 4 * D, m1, col0, row0 + (okp[0] ? slot[0] : some),
+                                        row0 + (okp[1] ? slot[1] : some), row0 + (okp[2] ? slot[2] : some),
+                                        row0 + (okp[3] ? slot[3] : some), b);
+                        }
+                        return;
+                    }
                     if constexpr (F8) {
                         // e4m3 rows of D bytes at a 128-byte pitch: D = 128,
                         // one 16-row box per page group, else a box per row;

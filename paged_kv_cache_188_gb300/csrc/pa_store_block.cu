@@ -31,7 +31,7 @@ struct StoreBlockArgs {
     const int32_t *loc;
     uint8_t *k_exp, *v_exp;            // the layer's [n_blocks, Hkv]
     int32_t *err;
-    int n_tokens, size, Hkv, block, shift, early_meta;
+    int n_tokens, size, Hkv, block, shift, chunk, early_meta;
     int64_t units;                     // (chunk of tokens, head, K or V)
 };
 
@@ -68,98 +68,113 @@ __device__ __forceinline__ uint32_t requant4(uint32_t w, float f)
     return e4m3x2_of(a * f, b * f) | e4m3x2_of(c * f, d * f) << 16;
 }
 
-// GW lanes per (run, head): 32, or a row's D / 16.
+// GW lanes per (run, head): 32, or a row's D / 16.  A unit is a chunk of tokens
+// of one head; it does the runs that begin in its chunk.
 template <int D, int GW>
 __global__ void __launch_bounds__(256) kv_store_block_kernel(const StoreBlockArgs a)
 {
     constexpr int LPR = D / 16, RPP = GW / LPR;     // lanes per row, rows per pass
-    constexpr int KEEP = 4;                         // passes whose rows stay in registers
+    constexpr int KEEP = 16 / RPP < 4 ? 16 / RPP : 4;   // passes whose rows stay in registers
     if (!a.early_meta) pdl_wait();
     const int lane = threadIdx.x & 31, gl = lane % GW;
     const unsigned mask = GW == 32 ? 0xffffffffu : ((1u << GW) - 1u) << (lane - gl);
     const int rr = gl / LPR, c = gl % LPR;
-    const int chunk = a.block > RPP ? a.block : RPP;   // tokens per unit
     if (a.early_meta) pdl_wait();
     pdl_launch_dependents();
+    const int64_t row_elems = (int64_t)a.Hkv * D;
     for (int64_t u = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / GW; u < a.units;
          u += (int64_t)gridDim.x * blockDim.x / GW) {
         const bool isv = u & 1;
-        const int64_t uh = u >> 1;
-        const int h = (int)(uh % a.Hkv);
-        const int64_t ch = uh / a.Hkv;
+        const int64_t uh = u >> 1, ch = uh / a.Hkv;
+        const int h = (int)(uh - ch * a.Hkv);
         const __nv_bfloat16 *src = (isv ? a.v_new : a.k_new) + (int64_t)h * D + c * 16;
         uint8_t *buf = (isv ? a.v_buf : a.k_buf) + (int64_t)h * D + c * 16;
         uint8_t *exp = isv ? a.v_exp : a.k_exp;
-        const int64_t row_elems = (int64_t)a.Hkv * D;
-        const int c0 = (int)(ch * chunk), c1 = min(a.n_tokens, c0 + chunk);
-        auto block_of = [&](int t) -> int {
-            const int s = __ldg(a.loc + t);
-            return s < 0 || s >= a.size ? -1 : s >> a.shift;
-        };
-        int before = c0 > 0 ? block_of(c0 - 1) : -1;
+        const int c0 = (int)(ch * a.chunk), c1 = min(a.n_tokens, c0 + a.chunk);
+        auto block_of = [&](int s) -> int { return s < 0 || s >= a.size ? -1 : s >> a.shift; };
+        int before = c0 > 0 ? block_of(__ldg(a.loc + c0 - 1)) : -1;
         for (int t0 = c0; t0 < c1;) {
-            const int blk = block_of(t0);
+            // lane i of the group: token t0 + i; the tokens that share t0's block
+            const int sl = t0 + gl < a.n_tokens ? __ldg(a.loc + t0 + gl) : -1;
+            const int mine = block_of(sl), blk = __shfl_sync(mask, mine, 0, GW);
+            const unsigned same = __ballot_sync(mask, mine == blk && t0 + gl < a.n_tokens) >> (lane - gl);
+            int len = GW == 32 && same == 0xffffffffu ? 32 : __ffs(~same) - 1;
+            if (GW < 32 && len > GW) len = GW;
             if (blk < 0 || blk == before) {
+                // out of range, or the rest of a run that began before this chunk
                 if (blk < 0 && gl == 0 && h == 0 && !isv) set_error(a.err, PA_DEVERR_SLOT);
                 before = blk;
-                ++t0;
+                t0 += len;
                 continue;
             }
             before = blk;
-            // the run [t0, t1): at most `block` neighbours in this block
-            int t1 = t0 + 1;
-            while (t1 < a.n_tokens && t1 - t0 < a.block && block_of(t1) == blk) ++t1;
+            if (len == GW) {
+                while (t0 + len < a.n_tokens && len < a.block && block_of(__ldg(a.loc + t0 + len)) == blk) ++len;
+            }
+            len = min(len, a.block);
             const int64_t ei = (int64_t)blk * a.Hkv + h;
             const int e_old = exp[ei];
+            // the run's first 16 rows stay in registers, requested together
             uint4 keep[KEEP][2];
-            float mx = 0.f;
-            for (int p = 0, t = t0 + rr; t - rr < t1; ++p, t += RPP) {
-                uint4 w0 = make_uint4(0u, 0u, 0u, 0u), w1 = w0;
-                if (t < t1) {
-                    const uint4 *s = reinterpret_cast<const uint4 *>(src + (int64_t)t * row_elems);
-                    w0 = __ldg(s);
-                    w1 = __ldg(s + 1);
-                }
 #pragma unroll
-                for (int q = 0; q < KEEP; ++q)
-                    if (p == q) keep[q][0] = w0, keep[q][1] = w1;
-                mx = fmaxf(mx, fmaxf(amax8(w0), amax8(w1)));
+            for (int q = 0; q < KEEP; ++q) {
+                const int i = q * RPP + rr;
+                keep[q][0] = keep[q][1] = make_uint4(0u, 0u, 0u, 0u);
+                if (i < len) {
+                    const uint4 *p = reinterpret_cast<const uint4 *>(src + (int64_t)(t0 + i) * row_elems);
+                    keep[q][0] = __ldg(p);
+                    keep[q][1] = __ldg(p + 1);
+                }
+            }
+            float mx = 0.f;
+#pragma unroll
+            for (int q = 0; q < KEEP; ++q) mx = fmaxf(mx, fmaxf(amax8(keep[q][0]), amax8(keep[q][1])));
+            for (int i = KEEP * RPP + rr; i < len; i += RPP) {
+                const uint4 *p = reinterpret_cast<const uint4 *>(src + (int64_t)(t0 + i) * row_elems);
+                mx = fmaxf(mx, fmaxf(amax8(__ldg(p)), amax8(__ldg(p + 1))));
             }
 #pragma unroll
             for (int o = GW / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(mask, mx, o, GW));
             const int e = max(e_old, block_exponent(mx));
             if (e > e_old && e_old > 0) {
-                // earlier rows of the block, rounded again to the larger scale
+                // earlier rows of the block, rounded again to the larger scale; in: the run's rows, a bit each
+                uint32_t in[4] = {0u, 0u, 0u, 0u};
+                for (int i = gl; i < len; i += GW) {
+                    const int off = __ldg(a.loc + t0 + i) & (a.block - 1);
+                    in[0] |= off < 32 ? 1u << off : 0u;
+                    in[1] |= off >= 32 && off < 64 ? 1u << (off - 32) : 0u;
+                    in[2] |= off >= 64 && off < 96 ? 1u << (off - 64) : 0u;
+                    in[3] |= off >= 96 ? 1u << (off - 96) : 0u;
+                }
+#pragma unroll
+                for (int w = 0; w < 4; ++w) in[w] = __reduce_or_sync(mask, in[w]);
                 const float f = __uint_as_float((uint32_t)max(127 + e_old - e, 0) << 23);
-                const int s_lo = blk << a.shift, s_hi = min(a.size, s_lo + a.block);
-                for (int s = s_lo + rr; s - rr < s_hi; s += RPP) {
-                    bool mine = s < s_hi;
-                    for (int t = t0; t < t1; ++t) mine = mine && __ldg(a.loc + t) != s;
-                    if (!mine) continue;
-                    uint4 *p = reinterpret_cast<uint4 *>(buf + (int64_t)s * row_elems);
+                const int s_lo = blk << a.shift, rows = min(a.size - s_lo, a.block);
+#pragma unroll 4
+                for (int r = rr; r < rows; r += RPP) {
+                    if ((r < 32 ? in[0] : r < 64 ? in[1] : r < 96 ? in[2] : in[3]) >> (r & 31) & 1u) continue;
+                    uint4 *p = reinterpret_cast<uint4 *>(buf + (int64_t)(s_lo + r) * row_elems);
                     const uint4 w = *p;
                     *p = make_uint4(requant4(w.x, f), requant4(w.y, f), requant4(w.z, f), requant4(w.w, f));
                 }
             }
             const float inv = __uint_as_float((uint32_t)(254 - e) << 23);
-            for (int p = 0, t = t0 + rr; t - rr < t1; ++p, t += RPP) {
-                if (t >= t1) break;
-                uint4 w0, w1;
-                if (p < KEEP) {
-#pragma unroll
-                    for (int q = 0; q < KEEP; ++q)
-                        if (p == q) w0 = keep[q][0], w1 = keep[q][1];
-                } else {
-                    const uint4 *s = reinterpret_cast<const uint4 *>(src + (int64_t)t * row_elems);
-                    w0 = __ldg(s);
-                    w1 = __ldg(s + 1);
-                }
+            auto put = [&](int i, uint4 w0, uint4 w1, int slot) {
                 const uint2 lo = quant8(w0, inv), hi = quant8(w1, inv);
-                *reinterpret_cast<uint4 *>(buf + (int64_t)__ldg(a.loc + t) * row_elems) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+                *reinterpret_cast<uint4 *>(buf + (int64_t)slot * row_elems) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+            };
+#pragma unroll
+            for (int q = 0; q < KEEP; ++q) {
+                const int i = q * RPP + rr, slot = __shfl_sync(mask, sl, i < GW ? i : 0, GW);
+                if (i < len) put(i, keep[q][0], keep[q][1], i < GW ? slot : __ldg(a.loc + t0 + i));
+            }
+            for (int i = KEEP * RPP + rr; i < len; i += RPP) {
+                const uint4 *p = reinterpret_cast<const uint4 *>(src + (int64_t)(t0 + i) * row_elems);
+                put(i, __ldg(p), __ldg(p + 1), __ldg(a.loc + t0 + i));
             }
             if (gl == 0 && e != e_old) exp[ei] = (uint8_t)e;
             __syncwarp(mask);
-            t0 = t1 < c1 ? t1 : c1;
+            t0 += len;
         }
     }
 }
@@ -187,12 +202,18 @@ __global__ void __launch_bounds__(256) kv_reset_block_kernel(uint8_t *k_exp, uin
 template <int D>
 static pa_status launch_store_block(StoreBlockArgs a, cudaStream_t st)
 {
-    constexpr int RPP = 32 / (D / 16);
-    const bool small = a.block < RPP;
-    const int chunk = small ? a.block : (a.block > RPP ? a.block : RPP), gw = small ? D / 16 : 32;
-    a.units = (((int64_t)a.n_tokens + chunk - 1) / chunk) * a.Hkv * 2;
+    const bool small = a.block < 32 / (D / 16);
+    const int gw = small ? D / 16 : 32;
+    // one token per unit while that is at most about one wave of warps (a run's
+    // other tokens then cost a warp that sees it and leaves: 64 appends take 16
+    // runs one after the other else, 15.6 us), then up to a block: a prompt's
+    // tokens are mostly not the first of their run
+    const int64_t wave = (int64_t)num_sms() * 48 * (32 / gw);
+    a.chunk = 1;
+    while (a.chunk < a.block && ((int64_t)a.n_tokens + a.chunk - 1) / a.chunk * a.Hkv * 2 > wave) a.chunk *= 2;
+    a.units = ((int64_t)a.n_tokens + a.chunk - 1) / a.chunk * a.Hkv * 2;
     int64_t g = (a.units * gw + 255) / 256;
-    const int64_t cap = (int64_t)num_sms() * 16;
+    const int64_t cap = (int64_t)num_sms() * 32;
     if (g > cap) g = cap;
     const cudaError_t rc = small ? launch_kernel(kv_store_block_kernel<D, D / 16>, dim3((unsigned)g), dim3(256), 0, st, a)
                                  : launch_kernel(kv_store_block_kernel<D, 32>, dim3((unsigned)g), dim3(256), 0, st, a);
