@@ -53,6 +53,11 @@ constexpr int kPfRows = 128;            // MMA M: rows of a q tile
 constexpr int kPfKeys = 128;            // keys per kv tile
 constexpr int kPfThreads = 352;         // 8 softmax warps + K producer + MMA issuer + V producer
 constexpr int kPfThreadsF8 = 384;       // e4m3 cache: + two warps widening K / V tiles to bf16
+// block-scaled e4m3 cache: K and V producers and four widening warps (two per
+// operand, half the rows each, one on each of the SM's four schedulers); 128
+// registers a thread, so the softmax holds half a row of S at a time
+constexpr int kPfThreadsBlk = 480;
+constexpr int kWarpCvtBlk = 11;         // warps 11, 12: K rows; 13, 14: V rows
 constexpr int kWarpProducer = 8, kWarpMma = 9, kWarpCvtK = 10, kWarpCvtV = 11;
 constexpr int kWarpProducerV = 10;      // bf16 kernels: V tiles are issued by a warp of their own
 constexpr int kPfMaxReqs = 2048;
@@ -149,7 +154,8 @@ static_assert(N_BARS <= 32, "barrier area holds 32 barriers");
 // exps[r] is row r's exponent byte e, and e << 7 the bf16 number 2^(e - 127);
 // 255 marks a position without a row, which becomes zeros).
 template <int D, bool BLK = false>
-__device__ __forceinline__ void widen_e4m3_tile(uint32_t src, uint32_t dst, int lane, const unsigned char *exps = nullptr)
+__device__ __forceinline__ void widen_e4m3_tile(uint32_t src, uint32_t dst, int lane, const unsigned char *exps = nullptr,
+                                                int row_lo = 0, int row_hi = kPfKeys)
 {
     constexpr int PITCH = BLK ? D : 128;   // bytes between rows as loaded
     constexpr int LPR = D / 16;     // lanes per row
@@ -157,7 +163,7 @@ __device__ __forceinline__ void widen_e4m3_tile(uint32_t src, uint32_t dst, int 
     constexpr int U = 4;            // passes whose loads are in flight together
     const int rr = lane / LPR, j = lane % LPR;
 #pragma unroll 1
-    for (int r0 = 0; r0 < kPfKeys; r0 += RPP * U) {
+    for (int r0 = row_lo; r0 < row_hi; r0 += RPP * U) {
         uint4 v[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) v[u] = ld_shared_v4(src + (uint32_t)((r0 + u * RPP + rr) * PITCH + j * 16));
@@ -165,13 +171,18 @@ __device__ __forceinline__ void widen_e4m3_tile(uint32_t src, uint32_t dst, int 
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int r = r0 + u * RPP + rr;
-            const uint32_t sc = BLK ? (uint32_t)exps[r] * 0x00800080u : 0u;
+            const uint32_t ex = BLK ? exps[r] : 0u, sc = ex * 0x00800080u;
+            if (BLK && ex == 255u) v[u] = make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t mul = BLK && ex == 255u ? 0u : sc;
             auto wide = [&](uint32_t two) -> uint32_t {
                 const uint32_t w = e4m3x2_to_bf16x2(two);
-                return !BLK ? w : sc == 0x7F807F80u ? 0u : mul_bf16x2(w, sc);
+                return BLK ? mul_bf16x2(w, mul) : w;
             };
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
+            for (int hh = 0; hh < 2; ++hh) {
+                // (BLK) the lanes of a row's second half write their odd chunk
+                // first: a row's eight lanes then hit all banks once
+                const int half = BLK ? hh ^ (j >= LPR / 2) : hh;
                 const uint32_t a = half ? v[u].z : v[u].x, b = half ? v[u].w : v[u].y;
                 const int c = 2 * j + half;   // bf16 chunk: d = 8 c .. 8 c + 7
                 st_shared_v4(dst + (uint32_t)((c >> 3) * kHalf + r * 128 + (((c & 7) ^ (r & 7)) << 4)),
@@ -222,13 +233,14 @@ __device__ __forceinline__ PfItem pf_item(const PrefillParams &p, const int *s_p
 // F8: an e4m3 cache, with a scale per kv head or (BLK) per block of slots and
 // kv head.
 template <int D, bool DENSE, bool LAST, bool F8, bool BLK>
-__global__ void __launch_bounds__(F8 ? kPfThreadsF8 : kPfThreads, 1)
+__global__ void __launch_bounds__(BLK ? kPfThreadsBlk : F8 ? kPfThreadsF8 : kPfThreads, 1)
     paged_prefill_kernel(const __grid_constant__ PrefillParams p)
 {
     using PL = PfLayout<D, F8, BLK>;
     static_assert(F8 || !BLK, "block scales belong to an e4m3 cache");
     constexpr int QH = PL::kHalves;   // 64-column halves of a q, K or V row
-    constexpr int NT = F8 ? kPfThreadsF8 : kPfThreads;
+    constexpr int NT = BLK ? kPfThreadsBlk : F8 ? kPfThreadsF8 : kPfThreads;
+    constexpr bool TWO = !F8 || BLK;      // K and V copies issued by a warp each
     static_assert(!(F8 && (DENSE || LAST)), "the e4m3 mode is paged prefill only");
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -255,7 +267,8 @@ __global__ void __launch_bounds__(F8 ? kPfThreadsF8 : kPfThreads, 1)
         for (int i = 0; i < N_BARS; ++i) {
             const bool softmax_arrive = i == PA_FULL || i == PB_FULL || i == OA_EMPTY || i == OB_EMPTY;
             const bool item_read = i >= ITEM_EMPTY && i < ITEM_EMPTY + kRing;
-            mbar_init(bar(i), softmax_arrive ? 128u : item_read ? (uint32_t)(kItemReaders + (F8 ? 2 : 1)) : 1u);
+            const bool widened = BLK && (i == K_FULL || i == K_FULL1 || i == V_FULL || i == V_FULL1);   // by two warps
+            mbar_init(bar(i), softmax_arrive ? 128u : item_read ? (uint32_t)(kItemReaders + (BLK ? 5 : F8 ? 2 : 1)) : widened ? 2u : 1u);
         }
         fence_mbar_init();
     }
@@ -326,7 +339,7 @@ __global__ void __launch_bounds__(F8 ? kPfThreadsF8 : kPfThreads, 1)
     const int total_items = s_pref[p.R];
     const int G = p.G;
 
-    if (warp == kWarpProducer || (!F8 && warp == kWarpProducerV)) {
+    if (warp == kWarpProducer || (TWO && warp == kWarpProducerV)) {
         // ================================================== TMA producers
         // Items are claimed one at a time from a global counter, so a CTA that
         // drew short items takes more of them; each claim (and finally the
@@ -337,7 +350,7 @@ __global__ void __launch_bounds__(F8 ? kPfThreadsF8 : kPfThreads, 1)
         // one warp issuing both tiles had become the step's critical path).
         // fp8: warp 8 loads everything.
         const bool doK = warp == kWarpProducer;
-        const bool doV = F8 || warp == kWarpProducerV;
+        const bool doV = !TWO || warp == kWarpProducerV;
         int kt = 0;
         int nq = 0, nk = 0, nv = 0;   // Q, K and V loads armed (for the drain on abort)
         bool ok = true;
@@ -408,8 +421,8 @@ __global__ void __launch_bounds__(F8 ? kPfThreadsF8 : kPfThreads, 1)
                 for (int e = 0; e < 4; ++e) {
                     const bool in = r[e] >= 0 && r[e] < p.size;
                     const int64_t at = in ? (int64_t)(r[e] >> p.block_shift) * p.Hkv + I.h : 0;
-                    exk[e] = in ? __ldcg(p.k_exp + at) : 255;
-                    exv[e] = in ? __ldcg(p.v_exp + at) : 255;
+                    if (doK) exk[e] = in ? __ldcg(p.k_exp + at) : 255;
+                    if (doV) exv[e] = in ? __ldcg(p.v_exp + at) : 255;
                 }
             };
             if constexpr (BLK) {
@@ -591,7 +604,38 @@ __global__ void __launch_bounds__(F8 ? kPfThreadsF8 : kPfThreads, 1)
             }
         }
         __syncwarp();
-    } else if (F8 && (warp == kWarpCvtK || warp == kWarpCvtV)) {
+    } else if (BLK && warp >= kWarpCvtBlk) {
+        // =========================== e4m3 -> bf16 widening with block scales
+        // Two warps per operand, each half the rows of every tile (one warp's
+        // issue rate was the kernel's limit: 402 us against 292 us with a
+        // scale per head and 205 us over a bf16 cache, 16 ragged prompts).
+        const bool isv = warp >= kWarpCvtBlk + 2;
+        const int row_lo = ((warp - kWarpCvtBlk) & 1) * (kPfKeys / 2);
+        int kt = 0;
+        bool ok = true;
+        auto wait1 = [&](int b, uint32_t parity) -> bool {
+            return __all_sync(0xffffffffu, mbar_wait(bar(b), parity, s_abort, err, PA_DEVERR_TIMEOUT, p.wait_ns));
+        };
+        for (int n = 0; ok; ++n) {
+            if (!wait1(ITEM_FULL + n % kRing, (n / kRing) & 1)) break;
+            const PfItem I = s_ring[n % kRing];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(ITEM_EMPTY + n % kRing));
+            if (I.end) break;
+            for (int t = 0; t < I.ntiles; ++t, ++kt) {
+                const int st = kt & 1;
+                if (!wait1((isv ? V_RAW : K_RAW) + st, (kt >> 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                widen_e4m3_tile<D, true>(raw_tile(isv, st), (isv ? sV : sK) + st * QH * kHalf, lane,
+                                         sb + PL::kOffExp + ((isv ? 2 : 0) + st) * kPfKeys, row_lo, row_lo + kPfKeys / 2);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar((isv ? V_FULL : K_FULL) + st));
+            }
+        }
+    } else if (F8 && !BLK && (warp == kWarpCvtK || warp == kWarpCvtV)) {
         // =========================================== e4m3 -> bf16 widening
         // One warp per operand: each e4m3 tile that lands is widened into its
         // bf16 stage, then handed to the MMA issuer (generic-proxy writes made
@@ -614,8 +658,7 @@ __global__ void __launch_bounds__(F8 ? kPfThreadsF8 : kPfThreads, 1)
                     ok = false;
                     break;
                 }
-                widen_e4m3_tile<D, BLK>(raw_tile(isv, st), (isv ? sV : sK) + st * QH * kHalf, lane,
-                                        BLK ? sb + PL::kOffExp + ((isv ? 2 : 0) + st) * kPfKeys : nullptr);
+                widen_e4m3_tile<D>(raw_tile(isv, st), (isv ? sV : sK) + st * QH * kHalf, lane);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar((isv ? V_FULL : K_FULL) + st));
@@ -781,24 +824,36 @@ __global__ void __launch_bounds__(F8 ? kPfThreadsF8 : kPfThreads, 1)
                 tc_fence_after();
                 const int limit = qpos - t * kPfKeys;    // columns <= limit are visible
                 // the whole row of S in registers: four loads, one wait
-                uint32_t r[128];
-#pragma unroll
-                for (int ch = 0; ch < 4; ++ch)
-                    tmem_ld32(s_addr + ch * 32, *reinterpret_cast<uint32_t(*)[32]>(&r[ch * 32]));
-                tmem_wait_ld();
+                // (BLK: half a row at a time, the first half loaded twice)
+                constexpr int RC = BLK ? 64 : 128;
+                uint32_t r[RC];
                 const bool diag = limit < kPfKeys - 1;
-                if (diag) {
+                auto load_s = [&](int col0) {
 #pragma unroll
-                    for (int c = 0; c < 128; ++c)
-                        if (c > limit) r[c] = __float_as_uint(-INFINITY);
-                }
+                    for (int ch = 0; ch < RC / 32; ++ch)
+                        tmem_ld32(s_addr + col0 + ch * 32, *reinterpret_cast<uint32_t(*)[32]>(&r[ch * 32]));
+                    tmem_wait_ld();
+                    if (diag) {
+#pragma unroll
+                        for (int c = 0; c < RC; ++c)
+                            if (col0 + c > limit) r[c] = __float_as_uint(-INFINITY);
+                    }
+                };
                 float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+                auto row_max = [&]() {
 #pragma unroll
-                for (int c = 0; c < 128; c += 4) {
-                    mx0 = fmaxf(mx0, __uint_as_float(r[c]));
-                    mx1 = fmaxf(mx1, __uint_as_float(r[c + 1]));
-                    mx2 = fmaxf(mx2, __uint_as_float(r[c + 2]));
-                    mx3 = fmaxf(mx3, __uint_as_float(r[c + 3]));
+                    for (int c = 0; c < RC; c += 4) {
+                        mx0 = fmaxf(mx0, __uint_as_float(r[c]));
+                        mx1 = fmaxf(mx1, __uint_as_float(r[c + 1]));
+                        mx2 = fmaxf(mx2, __uint_as_float(r[c + 2]));
+                        mx3 = fmaxf(mx3, __uint_as_float(r[c + 3]));
+                    }
+                };
+                load_s(0);
+                row_max();
+                if constexpr (BLK) {
+                    load_s(64);
+                    row_max();
                 }
                 const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
                 float m_new = m_run;
@@ -816,20 +871,32 @@ __global__ void __launch_bounds__(F8 ? kPfThreadsF8 : kPfThreads, 1)
                 // IEEE round-to-nearest op: the same values as scalar code)
                 const uint64_t sl2x2 = f32x2_pack(sl2, sl2), nmb2 = f32x2_pack(-mb, -mb);
                 uint64_t sum2 = f32x2_pack(0.f, 0.f);   // even and odd columns' sums
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    uint32_t pk[32];
+                // columns c0 + [0, 64) of r
+                auto weights = [&](int c0, uint32_t (&pk)[32]) {
 #pragma unroll
                     for (int c = 0; c < 64; c += 2) {
-                        const uint64_t x = fma_f32x2(f32x2_pack(__uint_as_float(r[hh * 64 + c]),
-                                                                __uint_as_float(r[hh * 64 + c + 1])),
+                        const uint64_t x = fma_f32x2(f32x2_pack(__uint_as_float(r[c0 + c]), __uint_as_float(r[c0 + c + 1])),
                                                      sl2x2, nmb2);
                         const float v0 = ex2f(f32x2_lo(x)), v1 = ex2f(f32x2_hi(x));
                         const uint64_t v2 = f32x2_pack(v0, v1);
                         sum2 = add_f32x2(sum2, v2);
                         pk[c / 2] = pack_bf16x2(v0, v1);
                     }
-                    tmem_st32(s_addr + hh * 32, pk);
+                };
+                if constexpr (BLK) {
+                    uint32_t pk1[32], pk0[32];
+                    weights(0, pk1);             // columns 64 .. 127 are in r
+                    load_s(0);
+                    weights(0, pk0);
+                    tmem_st32(s_addr, pk0);
+                    tmem_st32(s_addr + 32, pk1);
+                } else {
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) {
+                        uint32_t pk[32];
+                        weights(hh * 64, pk);
+                        tmem_st32(s_addr + hh * 32, pk);
+                    }
                 }
                 l_run = l_run * alpha + (f32x2_lo(sum2) + f32x2_hi(sum2));
                 // O_X is stable here: S_X(t) completing implies PV_X(t-1) completed
@@ -928,7 +995,7 @@ static pa_status launch_prefill(const PrefillParams &prm, cudaStream_t st)
     auto kern = paged_prefill_kernel<D, DENSE, LAST, F8, BLK>;
     const size_t smem = (size_t)PfLayout<D, F8, BLK>::kOffPref + (size_t)(prm.R + 1) * 4 + 1024;
     if (!ensure_dynamic_smem(reinterpret_cast<const void *>(kern), smem)) return PA_ERR_CUDA;
-    if (launch_kernel(kern, dim3(num_sms()), dim3(F8 ? kPfThreadsF8 : kPfThreads), smem, st, prm) != cudaSuccess)
+    if (launch_kernel(kern, dim3(num_sms()), dim3(BLK ? kPfThreadsBlk : F8 ? kPfThreadsF8 : kPfThreads), smem, st, prm) != cudaSuccess)
         return PA_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
