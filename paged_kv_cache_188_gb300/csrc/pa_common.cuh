@@ -254,6 +254,14 @@ __device__ __forceinline__ uint32_t rope_pair_bf16(uint32_t w, float c, float s)
     return pack_bf16x2(y0, y1);
 }
 
+// Maximum of three; a NaN is ignored unless all are.
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // Packed pairs of fp32 values (low, high) for the sm_100-family two-float
 // arithmetic; each lane of fma_f32x2 / add_f32x2 is one IEEE round-to-nearest
 // operation, the same value as the scalar fmaf / add.
@@ -267,6 +275,12 @@ __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c
 {
     uint64_t d;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
 __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b)

@@ -82,7 +82,7 @@ struct BlkArgs {
     float *lse;                                 // [batch, Hq]: log2-sum-exp (WT)
     float *scores;                              // [Hkv][cap_tiles][128][G], log2 units (WT)
     float *weights;                             // [req_rows, max_ctx] (WT)
-    int batch, Hq, Hkv, G, size, req_rows, max_ctx, layer_row0, block_shift, cap_tiles, early_meta;
+    int batch, Hq, Hkv, G, size, req_rows, max_ctx, layer_row0, block_shift, cap_tiles, early_meta, total_rows;
     int workers, stages_k, stages_v;            // two workers per CTA; ring stages per worker
     uint64_t wait_ns;
     float scale_log2;
@@ -362,15 +362,18 @@ __device__ __forceinline__ void blk_loader(const BlkArgs &a, const int *s_pref, 
             const bool run = ok[0] && ok[1] && ok[2] && ok[3] && sl[0] == s0 + 4 * (lane & 3) && sl[1] == sl[0] + 1 &&
                              sl[2] == sl[0] + 2 && sl[3] == sl[0] + 3;
             const bool page = ((__ballot_sync(0xffffffffu, run) >> (lane & ~3)) & 0xFu) == 0xFu;
+            const bool none = ((has >> (lane & ~3)) & 0xFu) == 0u;      // the lane's 16 positions have no row
             if (has) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) sl[e] = a.layer_row0 + (ok[e] ? sl[e] : some);
                 const int col = stage->h[u] * D;
-                if (page) {
+                if (page || none) {
+                    // a page's rows, or rows out of range, which read as zeros
                     if ((lane & 3) == 0) {
 #pragma unroll
                         for (int hh = 0; hh < C::HALVES; ++hh)
-                            tma_load_2d(dst + hh * C::HALF + (lane >> 2) * 16 * C::AW, m16, col + hh * (C::AW / C::ES), sl[0], fb);
+                            tma_load_2d(dst + hh * C::HALF + (lane >> 2) * 16 * C::AW, m16, col + hh * (C::AW / C::ES),
+                                        none ? a.total_rows : sl[0], fb);
                     }
                 } else {
 #pragma unroll

@@ -102,6 +102,7 @@ inline bool fill_block(BlkArgs &a, const void *q, int batch, int Hq, const void 
     a.req_rows = req_rows;
     a.max_ctx = max_ctx;
     a.layer_row0 = layer_id * s.size;
+    a.total_rows = s.n_layers * s.size;
     const size_t cap = (workspace_bytes - ws.scores_off) / blk_tile_bytes(Hq);
     a.cap_tiles = cap < (size_t)(1 << 30) ? (int)cap : 1 << 30;
     a.early_meta = early_metadata();

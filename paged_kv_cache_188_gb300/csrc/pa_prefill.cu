@@ -53,11 +53,13 @@ constexpr int kPfRows = 128;            // MMA M: rows of a q tile
 constexpr int kPfKeys = 128;            // keys per kv tile
 constexpr int kPfThreads = 352;         // 8 softmax warps + K producer + MMA issuer + V producer
 constexpr int kPfThreadsF8 = 384;       // e4m3 cache: + two warps widening K / V tiles to bf16
-// block-scaled e4m3 cache: K and V producers and four widening warps (two per
-// operand, half the rows each, one on each of the SM's four schedulers); 128
-// registers a thread, so the softmax holds half a row of S at a time
-constexpr int kPfThreadsBlk = 480;
-constexpr int kWarpCvtBlk = 11;         // warps 11, 12: K rows; 13, 14: V rows
+// block-scaled e4m3 cache (BLK), 384 threads.  K goes to the tensor core as it
+// is: q is split in shared memory into two e4m3 terms (kind::f8f6f4, the same
+// MMA time as bf16), a key's scale multiplies its column of S, q's row scale
+// joins the softmax scale.  Only V is widened to bf16, by two warps, 64 rows
+// each, from a ring of its own in the space that K's bf16 tiles would take.
+constexpr int kWarpCvtBlk = 10;         // warps 10, 11: V rows
+constexpr int kKeyScales = 4;           // tiles whose key scales are kept (softmax lags the K copies by two)
 constexpr int kWarpProducer = 8, kWarpMma = 9, kWarpCvtK = 10, kWarpCvtV = 11;
 constexpr int kWarpProducerV = 10;      // bf16 kernels: V tiles are issued by a warp of their own
 constexpr int kPfMaxReqs = 2048;
@@ -68,12 +70,15 @@ constexpr int kRing = 4;               // claimed work items handed from the pro
 enum { Q_FULL, Q_EMPTY, K_FULL, K_FULL1, K_EMPTY, K_EMPTY1, V_FULL, V_FULL1, V_EMPTY, V_EMPTY1,
        SA_FULL, SB_FULL, PA_FULL, PB_FULL, OA_FINAL, OB_FINAL, OA_EMPTY, OB_EMPTY,
        K_RAW, K_RAW1, V_RAW, V_RAW1, DRAIN,
+       QB_FULL, QA_READY, QB_READY,   // BLK: tile B's q has landed (Q_FULL: tile A's); q split into its terms
+       V_RAW_EMPTY, V_RAW_EMPTY1,     // BLK: the e4m3 V tile has been widened
        ITEM_FULL, ITEM_EMPTY = ITEM_FULL + kRing, N_BARS = ITEM_EMPTY + kRing };
-static_assert(N_BARS <= 32, "barrier area holds 32 barriers");
+static_assert(N_BARS <= 40, "barrier area holds 40 barriers");
 constexpr int kItemReaders = 1 + 8;     // the MMA warp and the eight softmax warps (+ 2 widening warps in fp8 mode)
 constexpr int kStageBytes = 32 * 64;    // per softmax warp: 32 rows x 32 bf16 of the output
 constexpr uint32_t kTmemCols = 512;     // S_A | S_B | O_A | O_B
 constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, 0, 0);   // Q (K-major) x K (K-major)
+constexpr uint32_t kIdescS8 = idesc_e4m3_f32(128, 128, 0, 0);  // the same in e4m3 (BLK)
 
 // Shared-memory layout for head dimension D (64 or 128): a q, K or V tile is
 // D / 64 halves; Q tiles A and B, two K and two V stages, (fp8, D = 64) the
@@ -93,14 +98,16 @@ struct PfLayout {
     static constexpr int kRawPitch = 128;                // bytes per e4m3 row as loaded
     static constexpr int kRawBytes = kPfKeys * kRawPitch;   // one e4m3 tile
     static constexpr int kOffRaw = 6 * kHalves * kHalf;
-    static constexpr int kRawArea = (F8 && D == 64) ? 4 * kRawBytes : 0;   // K stages 0, 1, then V
+    static constexpr int kRawArea = (F8 && !BLK && D == 64) ? 4 * kRawBytes : 0;   // K stages 0, 1, then V
     static constexpr int kOffBar = kOffRaw + kRawArea;
-    static constexpr int kOffMisc = kOffBar + 32 * 8;
+    static constexpr int kOffMisc = kOffBar + 40 * 8;
     static constexpr int kOffRing = kOffMisc + 64;      // kRing work-item descriptions
     static constexpr int kOffStage = kOffMisc + 256;
-    // block-scaled cache: exponent bytes of K stages 0, 1 and V stages 0, 1
-    static constexpr int kOffExp = kOffStage + 8 * kStageBytes;
-    static constexpr int kOffPref = kOffExp + (BLK ? 4 * kPfKeys : 0);
+    // block-scaled cache: key scales (fp32) of kKeyScales tiles, exponent bytes of V stages 0, 1
+    static constexpr int kOffKeyScale = kOffStage + 8 * kStageBytes;
+    static constexpr int kOffExp = kOffKeyScale + (BLK ? kKeyScales * kPfKeys * 4 : 0);
+    static constexpr int kOffGrouped = kOffExp + (BLK ? 2 * kPfKeys : 0);   // int per tile: 16 columns share a scale
+    static constexpr int kOffPref = kOffGrouped + (BLK ? kKeyScales * 4 : 0);
     // tensor-memory columns: S_A | S_B | O_A | O_B
     static constexpr uint32_t kColOA = 256, kColOB = 256 + D;
     static constexpr uint32_t kIdescPV = idesc_bf16_f32(128, D, 0, 1);  // P (tensor memory) x V (MN-major)
@@ -142,7 +149,6 @@ struct alignas(16) PfItem {
 };
 static_assert(PfLayout<128>::kOffRing + kRing * (int)sizeof(PfItem) <= PfLayout<128>::kOffMisc + 256,
               "item ring fits the misc area");
-static_assert(N_BARS <= 32, "barrier area holds 32 barriers");
 
 // Widen one e4m3 tile (128 rows of D bytes at a 128-byte pitch at `src`) to bf16 in the
 // 128-byte-swizzled K/V stage layout at `dst` (16-byte chunk c of row r at
@@ -193,12 +199,71 @@ __device__ __forceinline__ void widen_e4m3_tile(uint32_t src, uint32_t dst, int 
     }
 }
 
+// Row `row` of a q tile (bf16, 128-byte swizzle) into two e4m3 terms in its
+// place: q 2^-k = q1 + q2, k such that the row's largest element is within 448.
+// D = 128: q1 in the first half tile's row, q2 in the second's; D = 64: q1 and q2
+// side by side in the row.  Every element of at least 2^-11 of the largest is
+// exact (a bf16 has 8 significant bits, an e4m3 four), smaller ones are off by
+// at most 2^-19 of it.  A row's bytes belong to one thread.  The terms are
+// those of sg q; returns 2^k.
+template <int D>
+__device__ __forceinline__ float split_q_row(uint32_t tile, int row, float sg)
+{
+    constexpr int NC = D / 8;       // 16-byte chunks of the bf16 row
+    auto at = [&](int c) { return tile + (uint32_t)((c >> 3) * kHalf + row * 128 + (((c & 7) ^ (row & 7)) << 4)); };
+    uint4 w[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) w[c] = ld_shared_v4(at(c));
+    // largest magnitude, as bits (two bf16 per word: NaN and infinity are the largest)
+    uint32_t top = 0;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+        top = __vmaxu2(__vmaxu2(top, __vmaxu2(w[c].x & 0x7FFF7FFFu, w[c].y & 0x7FFF7FFFu)),
+                       __vmaxu2(w[c].z & 0x7FFF7FFFu, w[c].w & 0x7FFF7FFFu));
+    top = max(top & 0xFFFFu, top >> 16);
+    const float mx = __uint_as_float(top << 16);
+    // a row with a NaN or an infinity has no softmax: its scale is NaN
+    if (top >= 0x7F80u) return NAN;
+    auto val = [&](int c, int e) -> float {     // element 8 c + e
+        const uint32_t u = e < 2 ? w[c].x : e < 4 ? w[c].y : e < 6 ? w[c].z : w[c].w;
+        return __uint_as_float(e & 1 ? u & 0xFFFF0000u : u << 16);
+    };
+    const int k = mx > 0.f ? block_exponent(mx) : 127;
+    const float inv = sg * __uint_as_float((uint32_t)(254 - k) << 23);
+#pragma unroll
+    for (int c = 0; c < NC; c += 2) {
+        uint32_t b1[4], b2[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {       // four elements
+            b1[g] = b2[g] = 0;
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+                const float y0 = val(c + (g >> 1), (g & 1) * 4 + e) * inv;
+                const float y1 = val(c + (g >> 1), (g & 1) * 4 + e + 1) * inv;
+                const uint32_t q1 = e4m3x2_of(y0, y1);
+                float f0, f1;
+                e4m3x2_floats(q1, f0, f1);
+                b1[g] |= q1 << (8 * e);
+                b2[g] |= e4m3x2_of(y0 - f0, y1 - f1) << (8 * e);
+            }
+        }
+        st_shared_v4(at(c / 2), b1[0], b1[1], b1[2], b1[3]);
+        st_shared_v4(at(c / 2 + (D == 128 ? 8 : 4)), b2[0], b2[1], b2[2], b2[3]);
+    }
+    return __uint_as_float((uint32_t)k << 23);
+}
+
 __device__ __forceinline__ float ex2f(float x)
 {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+
+template <bool V>
+struct Flag {
+    static constexpr bool value = V;
+};
 
 template <bool DENSE>
 __device__ __forceinline__ PfItem pf_item(const PrefillParams &p, const int *s_pref, int item)
@@ -233,14 +298,13 @@ __device__ __forceinline__ PfItem pf_item(const PrefillParams &p, const int *s_p
 // F8: an e4m3 cache, with a scale per kv head or (BLK) per block of slots and
 // kv head.
 template <int D, bool DENSE, bool LAST, bool F8, bool BLK>
-__global__ void __launch_bounds__(BLK ? kPfThreadsBlk : F8 ? kPfThreadsF8 : kPfThreads, 1)
+__global__ void __launch_bounds__(F8 ? kPfThreadsF8 : kPfThreads, 1)
     paged_prefill_kernel(const __grid_constant__ PrefillParams p)
 {
     using PL = PfLayout<D, F8, BLK>;
     static_assert(F8 || !BLK, "block scales belong to an e4m3 cache");
     constexpr int QH = PL::kHalves;   // 64-column halves of a q, K or V row
-    constexpr int NT = BLK ? kPfThreadsBlk : F8 ? kPfThreadsF8 : kPfThreads;
-    constexpr bool TWO = !F8 || BLK;      // K and V copies issued by a warp each
+    constexpr int NT = F8 ? kPfThreadsF8 : kPfThreads;
     static_assert(!(F8 && (DENSE || LAST)), "the e4m3 mode is paged prefill only");
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -249,6 +313,7 @@ __global__ void __launch_bounds__(BLK ? kPfThreadsBlk : F8 ? kPfThreadsF8 : kPfT
     const uint32_t sQA = base + PL::kOffQA, sQB = base + PL::kOffQB, sK = base + PL::kOffK, sV = base + PL::kOffV;
     // fp8: where stage st's e4m3 K / V tile lands
     auto raw_tile = [&](bool isv, int st) -> uint32_t {
+        if (BLK) return sK + 2 * kPfKeys * D + st * kPfKeys * D;      // V behind the two K tiles
         if (D == 128) return (isv ? sV : sK) + st * QH * kHalf + kHalf;
         return base + PL::kOffRaw + ((isv ? 2 : 0) + st) * PL::kRawBytes;
     };
@@ -265,10 +330,11 @@ __global__ void __launch_bounds__(BLK ? kPfThreadsBlk : F8 ? kPfThreadsF8 : kPfT
     if (tid == 0) {
         *s_abort = 0;
         for (int i = 0; i < N_BARS; ++i) {
-            const bool softmax_arrive = i == PA_FULL || i == PB_FULL || i == OA_EMPTY || i == OB_EMPTY;
+            const bool softmax_arrive = i == PA_FULL || i == PB_FULL || i == OA_EMPTY || i == OB_EMPTY || i == QA_READY ||
+                                        i == QB_READY;
             const bool item_read = i >= ITEM_EMPTY && i < ITEM_EMPTY + kRing;
-            const bool widened = BLK && (i == K_FULL || i == K_FULL1 || i == V_FULL || i == V_FULL1);   // by two warps
-            mbar_init(bar(i), softmax_arrive ? 128u : item_read ? (uint32_t)(kItemReaders + (BLK ? 5 : F8 ? 2 : 1)) : widened ? 2u : 1u);
+            const bool widened = BLK && (i == V_FULL || i == V_FULL1 || i == V_RAW_EMPTY || i == V_RAW_EMPTY1);   // by two warps
+            mbar_init(bar(i), softmax_arrive ? 128u : item_read ? (uint32_t)(kItemReaders + (F8 ? 2 : 1)) : widened ? 2u : 1u);
         }
         fence_mbar_init();
     }
@@ -339,7 +405,7 @@ __global__ void __launch_bounds__(BLK ? kPfThreadsBlk : F8 ? kPfThreadsF8 : kPfT
     const int total_items = s_pref[p.R];
     const int G = p.G;
 
-    if (warp == kWarpProducer || (TWO && warp == kWarpProducerV)) {
+    if (warp == kWarpProducer || (!F8 && warp == kWarpProducerV)) {
         // ================================================== TMA producers
         // Items are claimed one at a time from a global counter, so a CTA that
         // drew short items takes more of them; each claim (and finally the
@@ -350,9 +416,10 @@ __global__ void __launch_bounds__(BLK ? kPfThreadsBlk : F8 ? kPfThreadsF8 : kPfT
         // one warp issuing both tiles had become the step's critical path).
         // fp8: warp 8 loads everything.
         const bool doK = warp == kWarpProducer;
-        const bool doV = !TWO || warp == kWarpProducerV;
+        const bool doV = F8 || warp == kWarpProducerV;
         int kt = 0;
         int nq = 0, nk = 0, nv = 0;   // Q, K and V loads armed (for the drain on abort)
+        int nqb = 0;                  // BLK: tile B's q
         bool ok = true;
         // every lane waits; the warp continues only if all saw the phase
         auto wait1 = [&](int b, uint32_t parity) -> bool {
@@ -386,7 +453,18 @@ __global__ void __launch_bounds__(BLK ? kPfThreadsBlk : F8 ? kPfThreadsF8 : kPfT
             if (I.end) break;
             if (doK && it > 0 && !wait1(Q_EMPTY, (it - 1) & 1)) break;
             if (doK) ++nq;
-            if (doK && lane == 0) {
+            if (BLK && doK && I.nqb > 0) ++nqb;
+            if (BLK && doK && lane == 0) {
+                // a barrier per tile: each softmax warpgroup waits for its own
+                mbar_arrive_expect_tx(bar(Q_FULL), QH * kHalf);
+                if (I.nqb > 0) mbar_arrive_expect_tx(bar(QB_FULL), QH * kHalf);
+#pragma unroll
+                for (int hh = 0; hh < QH; ++hh) {
+                    tma_load_3d(sQA + hh * kHalf, &p.tm_q, 64 * hh, I.h * G, I.qs + I.q0, bar(Q_FULL));
+                    if (I.nqb > 0)
+                        tma_load_3d(sQB + hh * kHalf, &p.tm_q, 64 * hh, I.h * G, I.qs + I.q0 + p.TQ, bar(QB_FULL));
+                }
+            } else if (doK && lane == 0) {
                 mbar_arrive_expect_tx(bar(Q_FULL), 2 * QH * kHalf);
 #pragma unroll
                 for (int hh = 0; hh < QH; ++hh) {
@@ -421,8 +499,8 @@ __global__ void __launch_bounds__(BLK ? kPfThreadsBlk : F8 ? kPfThreadsF8 : kPfT
                 for (int e = 0; e < 4; ++e) {
                     const bool in = r[e] >= 0 && r[e] < p.size;
                     const int64_t at = in ? (int64_t)(r[e] >> p.block_shift) * p.Hkv + I.h : 0;
-                    if (doK) exk[e] = in ? __ldcg(p.k_exp + at) : 255;
-                    if (doV) exv[e] = in ? __ldcg(p.v_exp + at) : 255;
+                    exk[e] = in ? __ldcg(p.k_exp + at) : 255;
+                    exv[e] = in ? __ldcg(p.v_exp + at) : 255;
                 }
             };
             if constexpr (BLK) {
@@ -447,15 +525,6 @@ __global__ void __launch_bounds__(BLK ? kPfThreadsBlk : F8 ? kPfThreadsF8 : kPfT
                 } else {
                     if (t + 1 < I.ntiles) load_raw(t + 1);
                 }
-                // this lane's four exponent bytes into their stage, before the
-                // tile's barrier is armed
-                auto put_exps = [&](const int (&x)[4], int area) {
-                    if constexpr (BLK) {
-                        reinterpret_cast<uint32_t *>(sb + PL::kOffExp + area * kPfKeys)[lane] =
-                            (uint32_t)(x[0] | x[1] << 8 | x[2] << 16 | x[3] << 24);
-                        __syncwarp();
-                    }
-                };
                 // slots of positions k0 + 4*lane + e
                 const int k0 = t * kPfKeys;
                 int slot[4];
@@ -481,20 +550,32 @@ __global__ void __launch_bounds__(BLK ? kPfThreadsBlk : F8 ? kPfThreadsF8 : kPfT
                 const bool g_contig = ((contig >> (lane & ~3)) & 0xFu) == 0xFu;
                 const bool g_empty = ((anyok >> (lane & ~3)) & 0xFu) == 0u;
 
-                auto issue = [&](const CUtensorMap *m16, const CUtensorMap *m1, uint32_t dst, uint32_t b) {
+                // this lane's four exponents into shared memory, before the tile's
+                // barrier is armed
+                auto put_exps = [&](const int (&x)[4], bool key) {
                     if constexpr (BLK) {
-                        // D-byte rows packed: a 16-row box per page group,
-                        // else four rows per gather4 copy; a position without
-                        // a row repeats a valid one (its exponent byte says so)
-                        if (g_contig) {
-                            if (sub == 0) tma_load_2d(dst + gi * 16 * D, m16, col0, row0 + s0, b);
+                        if (key) {
+                            // this lane's four key scales; a position without a row scores 0, as a row of zeros
+                            // (an empty block's 2^-126 instead of 0: a masked column stays -inf)
+                            auto scale_of = [](int e) { return __uint_as_float(e == 255 ? 0u : (uint32_t)max(e, 1) << 23); };
+                            reinterpret_cast<float4 *>(sb + PL::kOffKeyScale + (kt & (kKeyScales - 1)) * kPfKeys * 4)[lane] =
+                                make_float4(scale_of(x[0]), scale_of(x[1]), scale_of(x[2]), scale_of(x[3]));
+                            // do the group's positions share one scale? (those past the last key do not matter)
+                            const int x0 = __shfl_sync(0xffffffffu, x[0], lane & ~3);
+                            bool one = true;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) one = one && (k0 + 4 * lane + e >= I.n_keys || (okp[e] && x[e] == x0));
+                            const bool grouped = __all_sync(0xffffffffu, one);
+                            if (lane == 0)
+                                reinterpret_cast<int *>(sb + PL::kOffGrouped)[kt & (kKeyScales - 1)] = grouped;
                         } else {
-                            tma_gather4(dst + lane * 4 * D, m1, col0, row0 + (okp[0] ? slot[0] : some),
-                                        row0 + (okp[1] ? slot[1] : some), row0 + (okp[2] ? slot[2] : some),
-                                        row0 + (okp[3] ? slot[3] : some), b);
+                            reinterpret_cast<uint32_t *>(sb + PL::kOffExp + st * kPfKeys)[lane] =
+                                (uint32_t)(x[0] | x[1] << 8 | x[2] << 16 | x[3] << 24);
                         }
-                        return;
+                        __syncwarp();
                     }
+                };
+                auto issue = [&](const CUtensorMap *m16, const CUtensorMap *m1, uint32_t dst, uint32_t b) {
                     if constexpr (F8) {
                         // e4m3 rows of D bytes at a 128-byte pitch: D = 128,
                         // one 16-row box per page group, else a box per row;
@@ -556,6 +637,41 @@ __global__ void __launch_bounds__(BLK ? kPfThreadsBlk : F8 ? kPfThreadsF8 : kPfT
                         }
                     }
                 };
+                if constexpr (BLK) {
+                    // K and V together: a group's two copies share their row
+                    if (kt >= 2 && (!wait1(K_EMPTY + st, ph_prev) || !wait1(V_RAW_EMPTY + st, ph_prev))) {
+                        ok = false;
+                        break;
+                    }
+                    put_exps(ek, true);
+                    put_exps(ev, false);
+                    ++nk;
+                    ++nv;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(bar(K_FULL + st), kPfKeys * D);
+                        mbar_arrive_expect_tx(bar(V_RAW + st), kPfKeys * D);
+                    }
+                    __syncwarp();
+                    const uint32_t kd = sK + st * kPfKeys * D, vd = raw_tile(true, st);
+                    // D-byte rows packed: a 16-row box per page group, one out
+                    // of range (zeros) where a group has no row, else four
+                    // rows per gather4 copy; there a position without a row
+                    // repeats a valid one (its exponent byte says so).  (64
+                    // gather4 copies for an item's last tile had cost 60 us.)
+                    if (g_contig || g_empty) {
+                        if (sub == 0) {
+                            const int row = g_empty ? p.total_rows : row0 + s0;
+                            tma_load_2d(kd + gi * 16 * D, &p.tm_k16, col0, row, bar(K_FULL + st));
+                            tma_load_2d(vd + gi * 16 * D, &p.tm_v16, col0, row, bar(V_RAW + st));
+                        }
+                    } else {
+                        const int r0 = row0 + (okp[0] ? slot[0] : some), r1 = row0 + (okp[1] ? slot[1] : some);
+                        const int r2 = row0 + (okp[2] ? slot[2] : some), r3 = row0 + (okp[3] ? slot[3] : some);
+                        tma_gather4(kd + lane * 4 * D, &p.tm_k1, col0, r0, r1, r2, r3, bar(K_FULL + st));
+                        tma_gather4(vd + lane * 4 * D, &p.tm_v1, col0, r0, r1, r2, r3, bar(V_RAW + st));
+                    }
+                    continue;
+                }
                 if (doK) {
                     if (kt >= 2 && !wait1(K_EMPTY + st, ph_prev)) {
                         ok = false;
@@ -568,7 +684,6 @@ __global__ void __launch_bounds__(BLK ? kPfThreadsBlk : F8 ? kPfThreadsF8 : kPfT
                         __syncwarp();
                     }
                     ++nk;
-                    put_exps(ek, st);
                     if (lane == 0) mbar_arrive_expect_tx(bar(kb + st), tile_bytes);
                     __syncwarp();
                     issue(&p.tm_k16, &p.tm_k1, F8 ? raw_tile(false, st) : sK + st * QH * kHalf, bar(kb + st));
@@ -585,7 +700,6 @@ __global__ void __launch_bounds__(BLK ? kPfThreadsBlk : F8 ? kPfThreadsF8 : kPfT
                         __syncwarp();
                     }
                     ++nv;
-                    put_exps(ev, 2 + st);
                     if (lane == 0) mbar_arrive_expect_tx(bar(vb + st), tile_bytes);
                     __syncwarp();
                     issue(&p.tm_v16, &p.tm_v1, F8 ? raw_tile(true, st) : sV + st * QH * kHalf, bar(vb + st));
@@ -596,7 +710,8 @@ __global__ void __launch_bounds__(BLK ? kPfThreadsBlk : F8 ? kPfThreadsF8 : kPfT
             // aborted: every copy this warp issued lands before the CTA's
             // shared memory goes away (each barrier's last armed phase)
             if (nq > 0) mbar_drain(bar(Q_FULL), (nq - 1) & 1);
-            const int kb = F8 ? K_RAW : K_FULL, vb = F8 ? V_RAW : V_FULL;
+            if (nqb > 0) mbar_drain(bar(QB_FULL), (nqb - 1) & 1);
+            const int kb = F8 && !BLK ? K_RAW : K_FULL, vb = F8 ? V_RAW : V_FULL;
             for (int st = 0; st < 2; ++st) {
                 const int ck = (nk - st + 1) / 2, cv = (nv - st + 1) / 2;   // arms of stage st
                 if (ck > 0) mbar_drain(bar(kb + st), (ck - 1) & 1);
@@ -605,12 +720,8 @@ __global__ void __launch_bounds__(BLK ? kPfThreadsBlk : F8 ? kPfThreadsF8 : kPfT
         }
         __syncwarp();
     } else if (BLK && warp >= kWarpCvtBlk) {
-        // =========================== e4m3 -> bf16 widening with block scales
-        // Two warps per operand, each half the rows of every tile (one warp's
-        // issue rate was the kernel's limit: 402 us against 292 us with a
-        // scale per head and 205 us over a bf16 cache, 16 ragged prompts).
-        const bool isv = warp >= kWarpCvtBlk + 2;
-        const int row_lo = ((warp - kWarpCvtBlk) & 1) * (kPfKeys / 2);
+        // ======================== e4m3 -> bf16 widening of V with block scales
+        const int row_lo = (warp - kWarpCvtBlk) * (kPfKeys / 2);
         int kt = 0;
         bool ok = true;
         auto wait1 = [&](int b, uint32_t parity) -> bool {
@@ -624,15 +735,19 @@ __global__ void __launch_bounds__(BLK ? kPfThreadsBlk : F8 ? kPfThreadsF8 : kPfT
             if (I.end) break;
             for (int t = 0; t < I.ntiles; ++t, ++kt) {
                 const int st = kt & 1;
-                if (!wait1((isv ? V_RAW : K_RAW) + st, (kt >> 1) & 1)) {
+                // the tile has landed, and its bf16 stage has been multiplied
+                if (!wait1(V_RAW + st, (kt >> 1) & 1) || (kt >= 2 && !wait1(V_EMPTY + st, ((kt >> 1) - 1) & 1))) {
                     ok = false;
                     break;
                 }
-                widen_e4m3_tile<D, true>(raw_tile(isv, st), (isv ? sV : sK) + st * QH * kHalf, lane,
-                                         sb + PL::kOffExp + ((isv ? 2 : 0) + st) * kPfKeys, row_lo, row_lo + kPfKeys / 2);
+                widen_e4m3_tile<D, true>(raw_tile(true, st), sV + st * QH * kHalf, lane, sb + PL::kOffExp + st * kPfKeys,
+                                         row_lo, row_lo + kPfKeys / 2);
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar((isv ? V_FULL : K_FULL) + st));
+                if (lane == 0) {
+                    mbar_arrive(bar(V_FULL + st));
+                    mbar_arrive(bar(V_RAW_EMPTY + st));
+                }
             }
         }
     } else if (F8 && !BLK && (warp == kWarpCvtK || warp == kWarpCvtV)) {
@@ -678,11 +793,24 @@ __global__ void __launch_bounds__(BLK ? kPfThreadsBlk : F8 ? kPfThreadsF8 : kPfT
             return ok;
         };
         auto qk = [&](uint32_t sQ, int st, uint32_t d_col) {
+            if constexpr (BLK) {
+                // both terms of q against the same keys, 32 of D per step; D = 64: the terms share a 128-byte row
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                const uint64_t a = smem_desc_sw128(sQ + (kk >> 2) * kHalf + (kk & 3) * 32, 16, 1024);
-                const uint64_t b = smem_desc_sw128(sK + st * QH * kHalf + (kk >> 2) * kHalf + (kk & 3) * 32, 16, 1024);
-                umma_ss(tmem + d_col, a, b, kIdescS, kk > 0 ? 1u : 0u);
+                for (int s = 0; s < D / 16; ++s) {
+                    constexpr int SPT = D / 32;
+                    const int term = s / SPT, o = (s % SPT) * 32;
+                    const uint64_t a = smem_desc_sw128(sQ + term * (D == 128 ? kHalf : 64) + o, 16, 1024);
+                    const uint32_t kt_addr = sK + st * kPfKeys * D + o;
+                    const uint64_t b = D == 128 ? smem_desc_sw128(kt_addr, 16, 1024) : smem_desc_sw64(kt_addr, 16, 512);
+                    umma_ss_f8(tmem + d_col, a, b, kIdescS8, s > 0 ? 1u : 0u);
+                }
+            } else {
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint64_t a = smem_desc_sw128(sQ + (kk >> 2) * kHalf + (kk & 3) * 32, 16, 1024);
+                    const uint64_t b = smem_desc_sw128(sK + st * QH * kHalf + (kk >> 2) * kHalf + (kk & 3) * 32, 16, 1024);
+                    umma_ss(tmem + d_col, a, b, kIdescS, kk > 0 ? 1u : 0u);
+                }
             }
         };
         auto pv = [&](uint32_t p_col, uint32_t o_col, int st, bool first) {
@@ -705,8 +833,10 @@ __global__ void __launch_bounds__(BLK ? kPfThreadsBlk : F8 ? kPfThreadsF8 : kPfT
             const bool hasB = I.nqb > 0;
             // S_A(0), S_B(0)
             {
-                const uint32_t b2[2] = {bar(Q_FULL), bar(K_FULL + (kt & 1))};
-                const uint32_t p2[2] = {(uint32_t)ia & 1u, (uint32_t)(kt >> 1) & 1u};
+                const uint32_t b2[3] = {bar(BLK ? QA_READY : Q_FULL), bar(K_FULL + (kt & 1)),
+                                        bar(BLK && hasB ? QB_READY : K_FULL + (kt & 1))};
+                const uint32_t p2[3] = {(uint32_t)ia & 1u, (uint32_t)(kt >> 1) & 1u,
+                                        (uint32_t)(BLK && hasB ? ib : kt >> 1) & 1u};
                 if (!waitn(b2, p2)) break;
             }
             tc_fence_after();
@@ -791,6 +921,7 @@ __global__ void __launch_bounds__(BLK ? kPfThreadsBlk : F8 ? kPfThreadsF8 : kPfT
         const int b_o_final = X ? OB_FINAL : OA_FINAL, b_o_empty = X ? OB_EMPTY : OA_EMPTY;
         float sl2 = p.scale_log2;
         int tx = 0, ix = 0;       // tiles and items this warpgroup has processed
+        int tx_all = 0;           // kv tiles of the CTA (BLK: its ring of key scales)
         bool ok = true;
         for (int n = 0; ok; ++n) {
             if (!__all_sync(0xffffffffu, mbar_wait(bar(ITEM_FULL + n % kRing), (n / kRing) & 1, s_abort, err,
@@ -809,13 +940,27 @@ __global__ void __launch_bounds__(BLK ? kPfThreadsBlk : F8 ? kPfThreadsF8 : kPfT
                 break;
             }
             const int nq = X ? I.nqb : I.nqa;
-            if (nq <= 0) continue;                // no tile B in this pair
+            if (nq <= 0) {                        // no tile B in this pair
+                tx_all += I.ntiles;
+                continue;
+            }
             const int q0 = I.q0 + X * p.TQ;
             if constexpr (F8 && !BLK) sl2 = p.scale_log2 * __ldg(p.k_scale + I.h);   // the head's K scale joins the softmax scale
+            if constexpr (BLK) {
+                // this thread's row of q, in place, into its two e4m3 terms
+                if (!__all_sync(0xffffffffu, mbar_wait(bar(X ? QB_FULL : Q_FULL), ix & 1, s_abort, err, PA_DEVERR_TIMEOUT,
+                                                       p.wait_ns)))
+                    break;
+                // (the softmax scale's sign, or 0, goes into q: the maximum below is of S itself)
+                const float sg = p.scale_log2 > 0.f ? 1.f : p.scale_log2 < 0.f ? -1.f : 0.f;
+                sl2 = (sg != 0.f ? fabsf(p.scale_log2) : 1.f) * split_q_row<D>(X ? sQB : sQA, row, sg);
+                fence_proxy_async_smem();
+                mbar_arrive(bar(X ? QB_READY : QA_READY));
+            }
             const int tok = row / G;              // token of this row within the tile
             const int qpos = I.p + q0 + tok;      // its position in the request
             float m_run = -INFINITY, l_run = 0.f;
-            for (int t = 0; t < I.ntiles; ++t, ++tx) {
+            for (int t = 0; t < I.ntiles; ++t, ++tx, ++tx_all) {
                 if (!__all_sync(0xffffffffu,
                                 mbar_wait(bar(b_s_full), tx & 1, s_abort, err, PA_DEVERR_TIMEOUT, p.wait_ns))) {
                     ok = false;
@@ -823,37 +968,80 @@ __global__ void __launch_bounds__(BLK ? kPfThreadsBlk : F8 ? kPfThreadsF8 : kPfT
                 }
                 tc_fence_after();
                 const int limit = qpos - t * kPfKeys;    // columns <= limit are visible
-                // the whole row of S in registers: four loads, one wait
-                // (BLK: half a row at a time, the first half loaded twice)
-                constexpr int RC = BLK ? 64 : 128;
-                uint32_t r[RC];
-                const bool diag = limit < kPfKeys - 1;
-                auto load_s = [&](int col0) {
+                auto rescale_o = [&](bool rescale, float alpha) {
+                    // O_X is stable here: S_X(t) completing implies PV_X(t-1) completed
+                    if (t > 0 && __any_sync(0xffffffffu, rescale)) {
 #pragma unroll
-                    for (int ch = 0; ch < RC / 32; ++ch)
-                        tmem_ld32(s_addr + col0 + ch * 32, *reinterpret_cast<uint32_t(*)[32]>(&r[ch * 32]));
-                    tmem_wait_ld();
-                    if (diag) {
+                        for (int ch = 0; ch < D / 32; ++ch) {
+                            uint32_t o[32];
+                            tmem_ld32(o_addr + ch * 32, o);
+                            tmem_wait_ld();
 #pragma unroll
-                        for (int c = 0; c < RC; ++c)
-                            if (col0 + c > limit) r[c] = __float_as_uint(-INFINITY);
+                            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+                            tmem_st32(o_addr + ch * 32, o);
+                        }
                     }
                 };
-                float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
-                auto row_max = [&]() {
+                // the whole row of S in registers: four loads, one wait
+                uint32_t r[128];
 #pragma unroll
-                    for (int c = 0; c < RC; c += 4) {
+                for (int ch = 0; ch < 4; ++ch)
+                    tmem_ld32(s_addr + ch * 32, *reinterpret_cast<uint32_t(*)[32]>(&r[ch * 32]));
+                // BLK: column c of S is scaled by its key's power of two.  Where 16
+                // columns share one (blocks of 16 slots or more), the scale joins
+                // each group's multiplier; else the columns are scaled first.
+                float gs[8];
+                bool grouped = true;
+                const float *ks = reinterpret_cast<const float *>(sb + PL::kOffKeyScale) + (tx_all & (kKeyScales - 1)) * kPfKeys;
+                if constexpr (BLK) {
+                    // (read while S is on its way)
+                    grouped = reinterpret_cast<const volatile int *>(sb + PL::kOffGrouped)[tx_all & (kKeyScales - 1)];
+#pragma unroll
+                    for (int g = 0; g < 8; ++g) gs[g] = reinterpret_cast<const volatile float *>(ks)[16 * g];
+                }
+                tmem_wait_ld();
+                if constexpr (BLK) {
+                    if (!grouped) {
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) {
+                            const float4 k4 = reinterpret_cast<const float4 *>(ks)[c];
+                            r[4 * c] = __float_as_uint(__uint_as_float(r[4 * c]) * k4.x);
+                            r[4 * c + 1] = __float_as_uint(__uint_as_float(r[4 * c + 1]) * k4.y);
+                            r[4 * c + 2] = __float_as_uint(__uint_as_float(r[4 * c + 2]) * k4.z);
+                            r[4 * c + 3] = __float_as_uint(__uint_as_float(r[4 * c + 3]) * k4.w);
+                        }
+#pragma unroll
+                        for (int g = 0; g < 8; ++g) gs[g] = 1.f;
+                    }
+                }
+                const bool diag = limit < kPfKeys - 1;
+                if (diag) {
+#pragma unroll
+                    for (int c = 0; c < 128; ++c)
+                        if (c > limit) r[c] = __float_as_uint(-INFINITY);
+                }
+                float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+                if constexpr (BLK) {
+                    // three values per instruction
+                    auto f = [&](int c) { return __uint_as_float(r[c]); };
+#pragma unroll
+                    for (int g = 0; g < 8; ++g) {
+                        const int c = 16 * g;
+                        const float a0 = max3(f(c), f(c + 1), f(c + 2)), a1 = max3(f(c + 3), f(c + 4), f(c + 5));
+                        const float a2 = max3(f(c + 6), f(c + 7), f(c + 8)), a3 = max3(f(c + 9), f(c + 10), f(c + 11));
+                        const float a4 = max3(a0, f(c + 12), f(c + 13)), a5 = max3(a1, f(c + 14), f(c + 15));
+                        const float a = fmaxf(max3(a2, a3, a4), a5) * gs[g];
+                        if (g & 1) mx1 = fmaxf(mx1, a);
+                        else mx0 = fmaxf(mx0, a);
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 128; c += 4) {
                         mx0 = fmaxf(mx0, __uint_as_float(r[c]));
                         mx1 = fmaxf(mx1, __uint_as_float(r[c + 1]));
                         mx2 = fmaxf(mx2, __uint_as_float(r[c + 2]));
                         mx3 = fmaxf(mx3, __uint_as_float(r[c + 3]));
                     }
-                };
-                load_s(0);
-                row_max();
-                if constexpr (BLK) {
-                    load_s(64);
-                    row_max();
                 }
                 const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
                 float m_new = m_run;
@@ -869,48 +1057,40 @@ __global__ void __launch_bounds__(BLK ? kPfThreadsBlk : F8 ? kPfThreadsF8 : kPfT
                 // back as bf16 pairs over the first 64 columns of S_X
                 // column pairs in packed two-float FMAs and adds (each lane an
                 // IEEE round-to-nearest op: the same values as scalar code)
-                const uint64_t sl2x2 = f32x2_pack(sl2, sl2), nmb2 = f32x2_pack(-mb, -mb);
+                const uint64_t nmb2 = f32x2_pack(-mb, -mb);
                 uint64_t sum2 = f32x2_pack(0.f, 0.f);   // even and odd columns' sums
-                // columns c0 + [0, 64) of r
-                auto weights = [&](int c0, uint32_t (&pk)[32]) {
-#pragma unroll
-                    for (int c = 0; c < 64; c += 2) {
-                        const uint64_t x = fma_f32x2(f32x2_pack(__uint_as_float(r[c0 + c]), __uint_as_float(r[c0 + c + 1])),
-                                                     sl2x2, nmb2);
-                        const float v0 = ex2f(f32x2_lo(x)), v1 = ex2f(f32x2_hi(x));
-                        const uint64_t v2 = f32x2_pack(v0, v1);
-                        sum2 = add_f32x2(sum2, v2);
-                        pk[c / 2] = pack_bf16x2(v0, v1);
-                    }
-                };
-                if constexpr (BLK) {
-                    uint32_t pk1[32], pk0[32];
-                    weights(0, pk1);             // columns 64 .. 127 are in r
-                    load_s(0);
-                    weights(0, pk0);
-                    tmem_st32(s_addr, pk0);
-                    tmem_st32(s_addr + 32, pk1);
-                } else {
+                // MASKED (BLK): hidden columns get weight 0 here; -inf times a
+                // group's multiplier would be NaN where that is 0
+                auto weights = [&](auto masked) {
+                    uint64_t sl2x2 = f32x2_pack(sl2, sl2);
 #pragma unroll
                     for (int hh = 0; hh < 2; ++hh) {
                         uint32_t pk[32];
-                        weights(hh * 64, pk);
+#pragma unroll
+                        for (int c = 0; c < 64; c += 2) {
+                            if (BLK && c % 16 == 0) {
+                                const float sg = sl2 * gs[hh * 4 + c / 16];
+                                sl2x2 = f32x2_pack(sg, sg);
+                            }
+                            const uint64_t x = fma_f32x2(f32x2_pack(__uint_as_float(r[hh * 64 + c]),
+                                                                    __uint_as_float(r[hh * 64 + c + 1])),
+                                                         sl2x2, nmb2);
+                            float v0 = ex2f(f32x2_lo(x)), v1 = ex2f(f32x2_hi(x));
+                            if (decltype(masked)::value) {
+                                v0 = hh * 64 + c > limit ? 0.f : v0;
+                                v1 = hh * 64 + c + 1 > limit ? 0.f : v1;
+                            }
+                            const uint64_t v2 = f32x2_pack(v0, v1);
+                            sum2 = add_f32x2(sum2, v2);
+                            pk[c / 2] = pack_bf16x2(v0, v1);
+                        }
                         tmem_st32(s_addr + hh * 32, pk);
                     }
-                }
+                };
+                if (BLK && __any_sync(0xffffffffu, diag)) weights(Flag<true>{});
+                else weights(Flag<false>{});
                 l_run = l_run * alpha + (f32x2_lo(sum2) + f32x2_hi(sum2));
-                // O_X is stable here: S_X(t) completing implies PV_X(t-1) completed
-                if (t > 0 && __any_sync(0xffffffffu, rescale)) {
-#pragma unroll
-                    for (int ch = 0; ch < D / 32; ++ch) {
-                        uint32_t o[32];
-                        tmem_ld32(o_addr + ch * 32, o);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
-                        tmem_st32(o_addr + ch * 32, o);
-                    }
-                }
+                rescale_o(rescale, alpha);
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(bar(b_p_full));
@@ -920,19 +1100,25 @@ __global__ void __launch_bounds__(BLK ? kPfThreadsBlk : F8 ? kPfThreadsF8 : kPfT
             if (!__all_sync(0xffffffffu, mbar_wait(bar(b_o_final), ix & 1, s_abort, err, PA_DEVERR_TIMEOUT, p.wait_ns)))
                 break;
             tc_fence_after();
-            uint32_t o[D];
-#pragma unroll
-            for (int ch = 0; ch < D / 32; ++ch)
-                tmem_ld32(o_addr + ch * 32, *reinterpret_cast<uint32_t(*)[32]>(&o[ch * 32]));
-            tmem_wait_ld();
-            tc_fence_before();
-            mbar_arrive(bar(b_o_empty));          // O_X is in registers: the next item may overwrite it
             // fp8: the head's V scale multiplies the normalised output
             const float inv_l = l_run > 0.f ? (F8 && !BLK ? __ldg(p.v_scale + I.h) : 1.f) / l_run : 0.f;
-            uint32_t ob[D / 2];                   // O / l as bf16 pairs
+            constexpr int OC = D;
+            uint32_t ob[OC / 2];                  // O / l as bf16 pairs
+            auto load_o = [&](int c0) {
+                uint32_t o[OC];
 #pragma unroll
-            for (int c = 0; c < D / 2; ++c)
-                ob[c] = pack_bf16x2(__uint_as_float(o[2 * c]) * inv_l, __uint_as_float(o[2 * c + 1]) * inv_l);
+                for (int ch = 0; ch < OC / 32; ++ch)
+                    tmem_ld32(o_addr + c0 + ch * 32, *reinterpret_cast<uint32_t(*)[32]>(&o[ch * 32]));
+                tmem_wait_ld();
+                if (c0 + OC == D) {
+                    tc_fence_before();
+                    mbar_arrive(bar(b_o_empty));  // O_X is in registers: the next item may overwrite it
+                }
+#pragma unroll
+                for (int c = 0; c < OC / 2; ++c)
+                    ob[c] = pack_bf16x2(__uint_as_float(o[2 * c]) * inv_l, __uint_as_float(o[2 * c + 1]) * inv_l);
+            };
+            if constexpr (!BLK) load_o(0);
             // 32 columns at a time through this warp's staging buffer (row
             // lane, 16-byte chunks XOR-swizzled by row so neither side
             // conflicts), then out with four lanes on 64 contiguous bytes
@@ -940,9 +1126,10 @@ __global__ void __launch_bounds__(BLK ? kPfThreadsBlk : F8 ? kPfThreadsF8 : kPfT
             const int rr0 = lane >> 2, cc = lane & 3;
 #pragma unroll
             for (int ch = 0; ch < D / 32; ++ch) {
+                if constexpr (BLK) load_o(ch * 32);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    const uint32_t *v = &ob[ch * 16 + c * 4];
+                    const uint32_t *v = &ob[(BLK ? 0 : ch * 16) + c * 4];
                     st_shared_v4(stg + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4), v[0], v[1], v[2], v[3]);
                 }
                 __syncwarp();
@@ -995,7 +1182,7 @@ static pa_status launch_prefill(const PrefillParams &prm, cudaStream_t st)
     auto kern = paged_prefill_kernel<D, DENSE, LAST, F8, BLK>;
     const size_t smem = (size_t)PfLayout<D, F8, BLK>::kOffPref + (size_t)(prm.R + 1) * 4 + 1024;
     if (!ensure_dynamic_smem(reinterpret_cast<const void *>(kern), smem)) return PA_ERR_CUDA;
-    if (launch_kernel(kern, dim3(num_sms()), dim3(BLK ? kPfThreadsBlk : F8 ? kPfThreadsF8 : kPfThreads), smem, st, prm) != cudaSuccess)
+    if (launch_kernel(kern, dim3(num_sms()), dim3(F8 ? kPfThreadsF8 : kPfThreads), smem, st, prm) != cudaSuccess)
         return PA_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
@@ -1030,7 +1217,16 @@ static pa_status prefill_call(const void *q, int n_tokens, int n_q_heads, const 
         const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)TQ};
         if (!encode_tmap_bf16(&prm.tm_q, q, 3, dims, strides, box)) return PA_ERR_CUDA;
     }
-    if (f8) {
+    if (k_exp) {
+        // K in the tensor core's swizzle, V plain (widened)
+        const cuuint64_t inner = (cuuint64_t)n_kv_heads * D, dims[2] = {inner, (cuuint64_t)total_rows}, strides[1] = {inner};
+        const cuuint32_t box16[2] = {(cuuint32_t)D, 16}, box1[2] = {(cuuint32_t)D, 1};
+        if (!encode_tmap_rows(&prm.tm_k16, k_rows, false, inner, (cuuint64_t)total_rows, D, 16, D) ||
+            !encode_tmap_rows(&prm.tm_k1, k_rows, false, inner, (cuuint64_t)total_rows, D, 1, D) ||
+            !encode_tmap_u8(&prm.tm_v16, v_rows, 2, dims, strides, box16) ||
+            !encode_tmap_u8(&prm.tm_v1, v_rows, 2, dims, strides, box1))
+            return PA_ERR_CUDA;
+    } else if (f8) {
         // e4m3 rows: D bytes per (slot, kv head), plain boxes of 16 rows or 1
         const cuuint64_t dims[2] = {(cuuint64_t)n_kv_heads * D, (cuuint64_t)total_rows};
         const cuuint64_t strides[1] = {(cuuint64_t)n_kv_heads * D};

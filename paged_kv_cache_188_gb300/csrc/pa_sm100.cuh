@@ -292,6 +292,12 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t lbo
     return d;
 }
 
+// The same with the 64-byte swizzle (layout type 4).
+__device__ __forceinline__ uint64_t smem_desc_sw64(uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_bytes)
+{
+    return (smem_desc_sw128(saddr, lbo_bytes, sbo_bytes) & ~((uint64_t)7 << 61)) | (uint64_t)4 << 61;
+}
+
 // Instruction descriptor for kind::f16 with bf16 A/B and fp32 accumulation.
 //   c_format (F32=1) bits [4,6); a_format (BF16=1) [7,10); b_format [10,13);
 //   a_major [15]; b_major [16] (0 = K-major, 1 = MN-major); N>>3 in [17,23);
@@ -300,6 +306,12 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, int a_mn_maj
 {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn_major << 15) | ((uint32_t)b_mn_major << 16) |
            ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// The same for kind::f8f6f4 with e4m3 A and B (format codes 0).
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, int a_mn_major, int b_mn_major)
+{
+    return idesc_bf16_f32(M, N, a_mn_major, b_mn_major) & ~(1u << 7 | 1u << 10);
 }
 
 // D(tmem) (+)= A(smem desc) x B(smem desc); issued by one thread.

@@ -76,7 +76,7 @@ def values(buf, exp, slots, block):
     return torch.from_numpy(E4M3)[buf[slots].long()] * torch.from_numpy(POWERS)[exp[slots // block].long()][..., None]
 
 
-def attention(q, k, v, scale, first=None):
+def attention(q, k, v, scale, first=None, terms=2.0 ** -22):
     """q [m, Hq, D] over k, v [n, Hkv, D]; row i sees positions 0 .. first + i (first None: all).  Returns the
     output [m, Hq, D], the weights [m, Hq, n], and per output row and head what its error is measured in:
     sum_j p_j |v_j| [m, Hq, D], max_j p_j, max |v|, and the error of a score (natural units) that
@@ -93,9 +93,10 @@ def attention(q, k, v, scale, first=None):
         x = x.masked_fill(hide[:, None], -math.inf)
         mag, top = mag.masked_fill(hide[:, None], 0), top.masked_fill(hide[:, None], 0)
     p = torch.softmax(x, -1)
-    # products summed in fp32 with truncation (2^-20 of their magnitudes), q's second term (2^-22 of the
-    # largest element), the exponent's argument in fp32
-    ds = (2.0 ** -20 * mag + 2.0 ** -22 * top + 2.0 ** -22 * x.abs().nan_to_num(posinf=0.0)).amax(-1)
+    # products summed in fp32 with truncation (2^-20 of their magnitudes), what q's two terms leave out (`terms` of
+    # the row's largest element: 2^-22 where the second term is kept 16 times larger, 2^-19 where it is not), the
+    # exponent's argument in fp32
+    ds = (2.0 ** -20 * mag + terms * top + 2.0 ** -22 * x.abs().nan_to_num(posinf=0.0)).amax(-1)
     return dict(out=torch.einsum("mhn,nhd->mhd", p, vv), p=p, mean=torch.einsum("mhn,nhd->mhd", p, vv.abs()),
                 pmax=p.amax(-1), vmax=float(v.abs().max()) if n else 0.0, ds=ds, n=n)
 

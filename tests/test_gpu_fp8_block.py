@@ -438,9 +438,42 @@ def test_prefill_ragged(G, D, page, block):
     for b, n in enumerate(new):
         if n:
             kk, vv = c.values(b)
-            r = R.attention(q[at:at + n].double(), kk, vv, 0.05, first=pre[b])
+            r = R.attention(q[at:at + n].double(), kk, vv, 0.05, first=pre[b], terms=2.0 ** -19)
             R.check_out(outs[0][at:at + n].cpu(), r, 8, f"prefill G={G} D={D} page={page} block={block} request {b}")
         at += n
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("scale,qmag", [(0.0, 1.0), (-0.05, 1.0), (0.05 * 2.0 ** -60, 2.0 ** 60), (0.4, 1.0)])
+def test_prefill_scales_and_query_magnitudes(D, scale, qmag):
+    """scale 0 (the mean of V), negative, queries far from 1, and scores that raise the maximum inside a tile."""
+    c = Cache([390], 2, D, 16, 16, 62, exp_lo=100, exp_hi=124).cuda()
+    q = (torch.randn((260, 8, D), generator=c.g) * torch.pow(2.0, torch.randint(-8, 1, (260, 8, 1), generator=c.g).float()) * qmag).to(torch.bfloat16)
+    k, v, table, rws, ke, ve = c.dev
+    out = torch.full_like(q, math.nan, device="cuda")
+    ws = api.alloc_workspace(api.pa_prefill_workspace_bytes())
+    api.pa_paged_prefill_attn_fp8_block(q.cuda(), k, v, 1, torch.tensor([0, 260], dtype=torch.int32).cuda(),
+                                        torch.tensor([0, 390], dtype=torch.int32).cuda(), table, rws, scale, ke, ve, 16, ws, out)
+    assert api.pa_get_error(ws) == 0
+    kk, vv = c.values(0)
+    R.check_out(out.cpu(), R.attention(q.double(), kk, vv, scale, first=130, terms=2.0 ** -19), 8, f"prefill scale {scale}")
+
+
+def test_prefill_bad_slots_read_as_zeros():
+    """A slot out of range is flagged; its position has a key and a value of zeros."""
+    c = Cache([300], 1, 128, 16, 16, 63).cuda()
+    q = torch.randn((40, 4, 128), generator=c.g).to(torch.bfloat16)
+    k, v, table, rws, ke, ve = c.dev
+    bad = [3, 150, 151, 290]
+    table[c.rows[0].item(), bad] = torch.tensor([-1, c.size, 2 ** 30, -9], dtype=torch.int32, device="cuda")
+    out = torch.full_like(q, math.nan, device="cuda")
+    ws = api.alloc_workspace(api.pa_prefill_workspace_bytes())
+    api.pa_paged_prefill_attn_fp8_block(q.cuda(), k, v, 1, torch.tensor([0, 40], dtype=torch.int32).cuda(),
+                                        torch.tensor([0, 300], dtype=torch.int32).cuda(), table, rws, 0.05, ke, ve, 16, ws, out)
+    assert api.pa_get_error(ws) == api.DEVERR_SLOT
+    kk, vv = c.values(0)
+    kk[bad], vv[bad] = 0.0, 0.0
+    R.check_out(out.cpu(), R.attention(q.double(), kk, vv, 0.05, first=260, terms=2.0 ** -19), 8, "bad slots")
 
 
 def test_prefill_last_row_is_decode_within_rounding():
@@ -455,8 +488,8 @@ def test_prefill_last_row_is_decode_within_rounding():
                                         api.alloc_workspace(api.pa_prefill_workspace_bytes()), pre)
     kk, vv = c.values(0)
     r = R.attention(q.cpu().double(), kk, vv, 0.05)
-    R.check_out(pre.cpu(), r, 8, "prefill")
     R.check_out(out.cpu(), r, 12, "decode")
+    R.check_out(pre.cpu(), R.attention(q.cpu().double(), kk, vv, 0.05, terms=2.0 ** -19), 8, "prefill")
 
 
 def test_tensors_of_no_device_are_refused():
