@@ -9,7 +9,10 @@
 // How: a cluster of CTAs per request.  The cut is found by a radix select over
 // the weights' bits in an order-preserving integer form: four passes of eight
 // bits, each a 256-bin count per CTA, summed over the cluster through
-// distributed shared memory.  Then one ordered pass: a token is kept if its key
+// distributed shared memory, all ranks' counts requested at once (a loop over
+// them took 1700 cycles a pass; three passes of 11 bits read eight times as much
+// from the other SMs and were slower, 17.5 us for 32K tokens; 1024 threads, or
+// one addition per distinct bin of a warp, 12.3 and 11.0 us against 9.9).  Then one ordered pass: a token is kept if its key
 // is above the cut, or equal to it and among the first `ties` of those; both
 // running counts come from ballots, so positions need no sort.  Kept tokens
 // only ever move towards the front, so a chunk's tokens are all read before any
@@ -26,11 +29,12 @@
 namespace pa {
 namespace cg = cooperative_groups;
 
-constexpr int kEvThreads = 1024;
-constexpr int kEvPer = 4;                              // tokens per thread of a chunk
+constexpr int kEvThreads = 512;
+constexpr int kEvPer = 8;                              // tokens per thread of a chunk
 constexpr int kEvChunk = kEvThreads * kEvPer;          // tokens per CTA and chunk
 constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kEvMaxCluster = 8;
+constexpr int kEvBins = 256;
 
 struct EvictArgs {
     int32_t *req_to_token;
@@ -54,8 +58,8 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(const EvictArgs a)
     const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int b = blockIdx.x / C;
-    __shared__ int s_hist[2][256];
-    __shared__ int s_total[256];
+    __shared__ int s_hist[2][kEvBins];
+    __shared__ int s_sum[kEvWarps];
     __shared__ int2 s_cnt[2];                 // this CTA's (sure, ties) of a chunk
     __shared__ int s_sure[kEvWarps], s_ties[kEvWarps];
     __shared__ int s_bin, s_above;
@@ -86,11 +90,13 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(const EvictArgs a)
 
     // token j of (chunk, e): warps hold 32 kEvPer consecutive tokens
     auto token = [&](int chunk, int e) { return chunk * span + rank * kEvChunk + (warp * kEvPer + e) * 32 + lane; };
-    float w0[kEvPer];                          // the first chunk's weights stay in registers
+    float w0[kEvPer];                          // the first chunk's weights and slots stay in registers
+    int slot0[kEvPer];
 #pragma unroll
     for (int e = 0; e < kEvPer; ++e) {
         const int j = token(0, e);
         w0[e] = j < n ? wts[j] : 0.f;
+        slot0[e] = j < n ? tab[j] : 0;
     }
     // ---- the cut: the `want`-th largest key of the first `cand` tokens
     uint32_t prefix = 0;
@@ -99,7 +105,7 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(const EvictArgs a)
         for (int pass = 0; pass < 4; ++pass) {
             const int shift = 24 - 8 * pass;
             int *hist = s_hist[pass & 1];
-            if (tid < 256) hist[tid] = 0;
+            if (tid < kEvBins) hist[tid] = 0;
             __syncthreads();
             for (int c = 0; c < chunks; ++c) {
 #pragma unroll
@@ -107,37 +113,32 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(const EvictArgs a)
                     const int j = token(c, e);
                     const uint32_t key = weight_key(c == 0 ? w0[e] : j < n ? wts[j] : 0.f);
                     const bool in = j < cand && (pass == 0 || (key >> (shift + 8)) == (prefix >> (shift + 8)));
-                    // one addition per distinct bin of the warp: equal weights are common
-                    const unsigned act = __ballot_sync(0xffffffffu, in);
-                    if (in) {
-                        const unsigned same = __match_any_sync(act, (key >> shift) & 255u);
-                        if (lane == __ffs(same) - 1) atomicAdd(hist + ((key >> shift) & 255u), __popc(same));
-                    }
+                    if (in) atomicAdd(hist + ((key >> shift) & 255u), 1);
                 }
             }
             cl.sync();
-            if (tid < 256) {
-                int s = 0;
-                for (int r = 0; r < C; ++r) s += cl.map_shared_rank(hist, r)[tid];
-                s_total[tid] = s;
-            }
-            __syncthreads();
-            if (warp == 0) {
-                // lane l holds bins 255 - 8 l .. 248 - 8 l; counts from the top
-                int v[8], sum = 0;
+            // thread t < 256 holds bin 255 - t
+            int v = 0, incl = 0;
+            if (tid < kEvBins) {
+                int x[kEvMaxCluster];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) sum += v[i] = s_total[255 - 8 * lane - i];
-                int incl = sum;
+                for (int r = 0; r < kEvMaxCluster; ++r) x[r] = r < C ? cl.map_shared_rank(hist, r)[kEvBins - 1 - tid] : 0;
+#pragma unroll
+                for (int r = 0; r < kEvMaxCluster; ++r) v += x[r];
+                incl = v;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
-                    const int x = __shfl_up_sync(0xffffffffu, incl, o);
-                    if (lane >= o) incl += x;
+                    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += y;
                 }
-                int above = incl - sum;
-                if (above < left && left <= incl) {
-                    int i = 0;
-                    while (above + v[i] < left) above += v[i++];
-                    s_bin = 255 - 8 * lane - i;
+                if (lane == 31) s_sum[warp] = incl;
+            }
+            __syncthreads();
+            if (tid < kEvBins) {
+                int above = incl - v;                         // and the warps with higher bins
+                for (int w = 0; w < warp; ++w) above += s_sum[w];
+                if (above < left && left <= above + v) {
+                    s_bin = kEvBins - 1 - tid;
                     s_above = above;
                 }
             }
@@ -161,7 +162,7 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(const EvictArgs a)
         for (int e = 0; e < kEvPer; ++e) {
             const int j = token(c, e);
             w[e] = c == 0 ? w0[e] : j < n ? wts[j] : 0.f;
-            slot[e] = j < n ? tab[j] : 0;
+            slot[e] = c == 0 ? slot0[e] : j < n ? tab[j] : 0;
             const uint32_t key = weight_key(w[e]);
             sure[e] = __ballot_sync(0xffffffffu, j < n && (j >= cand || key > prefix));
             ties[e] = __ballot_sync(0xffffffffu, j < cand && key == prefix);
@@ -174,24 +175,29 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(const EvictArgs a)
         }
         __syncthreads();
         if (warp == 0) {
-            int x = s_sure[lane], y = s_ties[lane];
+            int x = lane < kEvWarps ? s_sure[lane] : 0, y = lane < kEvWarps ? s_ties[lane] : 0;
             int xi = x, yi = y;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int p = __shfl_up_sync(0xffffffffu, xi, o), q = __shfl_up_sync(0xffffffffu, yi, o);
                 if (lane >= o) xi += p, yi += q;
             }
-            s_sure[lane] = xi - x;
-            s_ties[lane] = yi - y;
+            if (lane < kEvWarps) {
+                s_sure[lane] = xi - x;
+                s_ties[lane] = yi - y;
+            }
             if (lane == 31) s_cnt[c & 1] = make_int2(xi, yi);
         }
         cl.sync();                             // every token of the chunk has been read, every count is there
         int bs = done_sure + s_sure[warp], bt = done_ties + s_ties[warp];
-        for (int r = 0; r < C; ++r) {
-            const int2 x = *cl.map_shared_rank(&s_cnt[c & 1], r);
-            done_sure += x.x;
-            done_ties += x.y;
-            if (r < rank) bs += x.x, bt += x.y;
+        int2 cnt[kEvMaxCluster];
+#pragma unroll
+        for (int r = 0; r < kEvMaxCluster; ++r) cnt[r] = r < C ? *cl.map_shared_rank(&s_cnt[c & 1], r) : make_int2(0, 0);
+#pragma unroll
+        for (int r = 0; r < kEvMaxCluster; ++r) {
+            done_sure += cnt[r].x;
+            done_ties += cnt[r].y;
+            if (r < rank) bs += cnt[r].x, bt += cnt[r].y;
         }
         const unsigned below = (1u << lane) - 1u;
 #pragma unroll
