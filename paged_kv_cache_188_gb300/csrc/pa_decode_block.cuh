@@ -420,82 +420,93 @@ __device__ __forceinline__ BlkSpan blk_span(const int *s_pref, int W, int b)
     return s;
 }
 
-// Merge of a shared segment by the warpgroup that finished its last piece.
-// Warp w sums pieces w, w + 4, ... (a piece's [G][D] partials are contiguous:
-// 16-byte loads), then the four sums are added in order, so the result does not
-// depend on who merges.  The first pieces are requested before the (m, l)
-// pairs, so both travel in one round trip; the weights go through `scratch`,
-// the worker's ring, which is free by now.
+// Merge of a shared segment by the warpgroup that finished its last piece: all
+// partials into `scratch` (the worker's ring, free by now) by asynchronous
+// copies, the (m, l) pairs beside them, one round trip for all the pieces that
+// fit (38 of a single long request do), then every element summed in the
+// pieces' order.
 template <int D, int GP, bool WT>
 __device__ __forceinline__ void blk_merge(const BlkArgs &a, const BlkSpan &s, int b, int h, int t, int bar_id,
-                                          float *scratch)
+                                          float *scratch, int scratch_bytes)
 {
-    constexpr int NJ = GP * D / 128;                       // 16-byte loads per lane and piece
-    constexpr int PF = NJ <= 4 ? 4 : NJ <= 8 ? 2 : 1;      // pieces per warp requested at once
     const int lane = t & 31, warp = t >> 5, G = a.G, np = s.i1 - s.i0 + 1;
     auto slot = [&](int p) { return 2 * ((s.i0 + p) * a.Hkv + h) + (p == 0 ? s.first : 0); };   // piece p's partials
-    float *s_lse = scratch, *s_wt = scratch + 2 * 16;      // [G] log-sum-exp, [G] sums; [np][G] weights
-    float4 v[PF][NJ], acc[NJ];
-    auto load = [&](int p0) {
-#pragma unroll
-        for (int q = 0; q < PF; ++q) {
-            const int p = p0 + 4 * q;
-            const float4 *src = reinterpret_cast<const float4 *>(a.o_part + (int64_t)slot(min(p, np - 1)) * G * D) + lane;
-#pragma unroll
-            for (int j = 0; j < NJ; ++j)
-                v[q][j] = ld_cg_ordered_f4_if(p < np && (j * 32 + lane) * 4 < G * D, src + j * 32);
+    // [G] sums, [G] log-sum-exps; [np][G] maxima, later weights; [np][G] sums; partials
+    float *s_L = scratch, *s_lse = scratch + 16, *s_w = scratch + 32, *s_l = s_w + np * G;
+    float *s_o = scratch + (32 + 2 * np * G + 3) / 4 * 4;
+    const int chunks = G * D / 4;                          // 16-byte chunks of a piece
+    const int cap = (scratch_bytes - (int)((s_o - scratch) * 4)) / (G * D * 4);
+    auto copy = [&](int p0, int n) {
+        for (int i = t; i < n * chunks; i += 128) {
+            const int p = i / chunks, c = i - p * chunks;
+            cp_async_16(smem_u32(s_o) + i * 16, a.o_part + (int64_t)slot(p0 + p) * G * D + c * 4, 16);
         }
     };
-    load(warp);
+    copy(0, min(np, cap));
+    for (int i = t; i < np * G; i += 128) {
+        const int p = i / G;
+        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.ml_part + (slot(p) * G + (i - p * G)) * 2));
+        s_w[i] = ml.x;
+        s_l[i] = ml.y;
+    }
+    named_bar_sync(bar_id, 128);
     for (int g = warp; g < G; g += 4) {
         float M = -INFINITY;
-        for (int p = lane; p < np; p += 32) M = fmaxf(M, __ldcg(a.ml_part + (slot(p) * G + g) * 2));
+        for (int p = lane; p < np; p += 32) M = fmaxf(M, s_w[p * G + g]);
         M = warp_max(M);
         const float Mz = M == -INFINITY ? 0.f : M;
         float L = 0.f;
         for (int p = lane; p < np; p += 32) {
-            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.ml_part + (slot(p) * G + g) * 2));
-            const float w = blk_ex2(ml.x - Mz);
-            s_wt[p * G + g] = w;
-            L += w * ml.y;
+            const float w = blk_ex2(s_w[p * G + g] - Mz);
+            s_w[p * G + g] = w;
+            L += w * s_l[p * G + g];
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
         if (lane == 0) {
+            s_L[g] = L;
             s_lse[g] = L != 0.f ? M + log2f(L) : INFINITY;
-            s_lse[16 + g] = L;
         }
     }
+    constexpr int NJ = (GP * D / 4 + 127) / 128;           // chunks per thread
+    float4 acc[NJ];
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-    named_bar_sync(bar_id, 128);
-    for (int p0 = warp; p0 < np; p0 += 4 * PF) {
-        if (p0 != warp) load(p0);
+    for (int p0 = 0; p0 < np; p0 += cap) {
+        const int n = min(cap, np - p0);
+        if (p0 > 0) {
+            named_bar_sync(bar_id, 128);                   // the last batch has been read
+            copy(p0, n);
+        }
+        cp_async_wait_all();
+        named_bar_sync(bar_id, 128);
 #pragma unroll
-        for (int q = 0; q < PF; ++q) {
-            if (p0 + 4 * q >= np) break;
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                const float w = s_wt[(p0 + 4 * q) * G + min((j * 32 + lane) * 4 / D, G - 1)];
-                acc[j].x += w * v[q][j].x;
-                acc[j].y += w * v[q][j].y;
-                acc[j].z += w * v[q][j].z;
-                acc[j].w += w * v[q][j].w;
+        for (int j = 0; j < NJ; ++j) {
+            const int c = t + j * 128;
+            if (c >= chunks) break;
+            const float4 *so = reinterpret_cast<const float4 *>(s_o) + c;
+            const float *w = s_w + p0 * G + c * 4 / D;
+#pragma unroll 8
+            for (int p = 0; p < n; ++p) {
+                const float4 v = so[p * chunks];
+                const float x = w[p * G];
+                acc[j].x += x * v.x;
+                acc[j].y += x * v.y;
+                acc[j].z += x * v.z;
+                acc[j].w += x * v.w;
             }
         }
     }
-    float4 *s_o = reinterpret_cast<float4 *>(scratch + 2 * 16 + (np * G + 3) / 4 * 4);   // [4 warps][G D]
 #pragma unroll
-    for (int j = 0; j < NJ; ++j)
-        if ((j * 32 + lane) * 4 < G * D) s_o[warp * (GP * D / 4) + j * 32 + lane] = acc[j];
-    named_bar_sync(bar_id, 128);
-    for (int e = t; e < G * D; e += 128) {
-        const float *so = reinterpret_cast<const float *>(s_o) + e;
-        const int g = e / D;
-        const float L = s_lse[16 + g], O = so[0] + so[GP * D] + so[2 * GP * D] + so[3 * GP * D];
+    for (int j = 0; j < NJ; ++j) {
+        const int c = t + j * 128;
+        if (c >= chunks) break;
+        const int g = c * 4 / D;
+        const float L = s_L[g], inv = L != 0.f ? 1.f / L : 0.f;
         const int64_t hq = (int64_t)b * a.Hq + h * G + g;
-        a.out[hq * D + (e - g * D)] = __float2bfloat16_rn(L != 0.f ? O / L : 0.f);
-        if (WT && e == g * D) a.lse[hq] = s_lse[g];
+        const uint2 o = make_uint2(pack_bf16x2(acc[j].x * inv, acc[j].y * inv), pack_bf16x2(acc[j].z * inv, acc[j].w * inv));
+        *reinterpret_cast<uint2 *>(a.out + hq * D + (c * 4 - g * D)) = o;
+        if (WT && c * 4 == g * D) a.lse[hq] = s_lse[g];
     }
     named_bar_sync(bar_id, 128);                           // scratch reuse
 }
@@ -857,7 +868,7 @@ __global__ void __launch_bounds__(kBlkThreads, 1) decode_block_kernel(const __gr
             if (t == 0) s_last[wg][i] = !bad && ticket[i] == s.i1 - s.i0;
             named_bar_sync(bar_id, 128);
             if (s_last[wg][i]) {
-                blk_merge<D, GP, WT>(a, s, shared_b[i], h, t, bar_id, reinterpret_cast<float *>(smem_raw + (kring - raw)));
+                blk_merge<D, GP, WT>(a, s, shared_b[i], h, t, bar_id, reinterpret_cast<float *>(smem_raw + (kring - raw)), ring_bytes);
                 if (t == 0) a.tickets[s.i0 * a.Hkv + h] = 0;
             }
         }
@@ -913,10 +924,24 @@ static __global__ void __launch_bounds__(kBlkWeightThreads) decode_block_weights
         }
         const int j = (x - s_pref[b]) * kBlkTile + tid;
         if (j < n) {
+            const float *sc = a.scores + ((int64_t)x * kBlkTile + tid) * G;
+            const int64_t head = (int64_t)a.cap_tiles * kBlkTile * G;
             float w = 0.f;
-            for (int h = 0; h < a.Hkv; ++h) {
-                const float *sc = a.scores + (((int64_t)h * a.cap_tiles + x) * kBlkTile + tid) * G;
-                for (int g = 0; g < G; ++g) w += blk_ex2(__ldcg(sc + g) - s_lse[h * G + g]);
+            if (G % 4 == 0) {
+                // four scores a load, eight loads on their way
+#pragma unroll 8
+                for (int q = 0; q < a.Hq / 4; ++q) {
+                    const int h = q / (G / 4), g = (q - h * (G / 4)) * 4;
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(sc + h * head + g));
+                    const float *l = s_lse + q * 4;
+                    w += blk_ex2(v.x - l[0]) + blk_ex2(v.y - l[1]) + (blk_ex2(v.z - l[2]) + blk_ex2(v.w - l[3]));
+                }
+            } else {
+#pragma unroll 8
+                for (int hq = 0; hq < a.Hq; ++hq) {
+                    const int h = hq / G;
+                    w += blk_ex2(__ldcg(sc + h * head + hq - h * G) - s_lse[hq]);
+                }
             }
             a.weights[(int64_t)row * a.max_ctx + j] += w;
         }
@@ -934,7 +959,7 @@ static pa_status launch_block(BlkArgs a, cudaStream_t st)
     static_assert((kBlkSmemLimit - C::fixed(kBlkMaxBatch)) / C::TILE >= 4, "a stage per worker and operand fits at the largest batch");
     constexpr int kLeast = (int)((kBlkSmemLimit - C::fixed(kBlkMaxBatch)) / C::TILE) / 2;
     static_assert((kLeast < 2 * kBlkMaxStages ? kLeast : 2 * kBlkMaxStages) * C::TILE >=
-                      (32 + kBlkMaxWorkers * GP + 4 + 4 * GP * D) * 4, "the merge's scratch fits a worker's ring");
+                      (36 + 2 * kBlkMaxWorkers * GP + GP * D) * 4, "the merge's scratch holds a piece");
     auto kern = decode_block_kernel<D, E8, GP, WT>;
     const size_t smem = C::fixed(a.batch) + (size_t)2 * (a.stages_k + a.stages_v) * C::TILE;
     if (!ensure_dynamic_smem(reinterpret_cast<const void *>(kern), smem)) return PA_ERR_CUDA;
