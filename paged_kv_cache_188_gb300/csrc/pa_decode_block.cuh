@@ -323,7 +323,6 @@ __device__ __forceinline__ void blk_loader(const BlkArgs &a, const int *s_pref, 
 #pragma unroll
         for (int u = 0; u < kBlkAhead; ++u) {
             stage->slot[u][lane] = make_int4(slot[u][0], slot[u][1], slot[u][2], slot[u][3]);
-            stage->ex[u][lane] = (uint32_t)(ex[u][0] | ex[u][1] << 8 | ex[u][2] << 16 | ex[u][3] << 24);
             if (lane == 0) {
                 stage->h[u] = h[u];
                 stage->n[u] = n[u];
@@ -385,6 +384,12 @@ __device__ __forceinline__ void blk_loader(const BlkArgs &a, const int *s_pref, 
                 // no valid row at all: zeros (weight zero times whatever bits lie there could be NaN)
                 for (int o = lane * 16; o < C::TILE; o += 512) st_shared_v4(dst + o, 0u, 0u, 0u, 0u);
                 fence_proxy_async_smem();
+            }
+            if (u == 0) {
+                // the batch's exponents, behind its first copies: they may still be on their way
+#pragma unroll
+                for (int w = 0; w < kBlkAhead; ++w)
+                    stage->ex[w][lane] = (uint32_t)(ex[w][0] | ex[w][1] << 8 | ex[w][2] << 16 | ex[w][3] << 24);
             }
             reinterpret_cast<uint32_t *>(meta + st * kBlkTile)[lane] = stage->ex[u][lane];
             __syncwarp();
