@@ -64,7 +64,7 @@ constexpr int kBlkThreads = 256 + 128;  // two warpgroups, two loader warps for 
 constexpr int kBlkMaxWorkers = 320;     // warpgroups of a launch: two per SM (152 SMs)
 constexpr int kBlkMaxStages = 6;        // per warpgroup and operand
 constexpr int kBlkMaxBatch = 4096;
-constexpr int kBlkAhead = 4;            // tiles of a loader's batch
+constexpr int kBlkAhead = 2;            // tiles of a loader's batch
 constexpr int kBlkStageBytes = (kBlkAhead * (32 * 20 + 12) + 15) / 16 * 16;
 constexpr uint32_t kBlkTmemCols = 256; // per warpgroup 128: S at 0, O at 64
 constexpr int kMasked = 255;           // exponent byte of a position without a token
@@ -246,7 +246,9 @@ __device__ __forceinline__ void blk_next(BlkWalk &k)
 // batches of kBlkAhead: while a batch is copied, the next one's table entries
 // are on their way to registers and, from its middle on, the exponents that
 // hang on them.  (With tens of MB in flight a read takes several microseconds;
-// one or two tiles of look-ahead left the copies waiting for their indices.)
+// a look-ahead kept in rotating registers, each move of which waits for the
+// value, left the copies waiting for their indices: 70 us for 48 ragged requests
+// against 57; batches of 4 and 6 tiles took 58.6 and 63.2.)
 // A batch that has arrived is put in shared memory, so that the copies are one
 // rolled loop: a TMA instruction costs its warp about 100 cycles of issue, a
 // tile of 16-slot pages eight of them per operand.
