@@ -84,6 +84,7 @@ struct BlkArgs {
     float *weights;                             // [req_rows, max_ctx] (WT)
     int batch, Hq, Hkv, G, size, req_rows, max_ctx, layer_row0, block_shift, cap_tiles, early_meta, total_rows;
     int workers, stages_k, stages_v;            // two workers per CTA; ring stages per worker
+    int ranges, spread;                         // ranges per head; ranges that a worker per SM serves
     uint64_t wait_ns;
     float scale_log2;
 };
@@ -103,7 +104,8 @@ struct BlkCfg {
     static constexpr int HALF = kBlkTile * AW;
     static constexpr int TILE = kBlkTile * RB;
     static constexpr int QB = NQ * RB;                    // one warpgroup's q
-    static constexpr int PB = NP * kBlkTile * ES;         // and P
+    // and P, which also holds O [GP][128] in fp32 when a piece ends
+    static constexpr int PB = NP * kBlkTile * ES > GP * 512 ? NP * kBlkTile * ES : GP * 512;
     static constexpr int QSteps = RB / 32, PSteps = kBlkTile * ES / 32;   // a K step is 32 bytes of either type
     // offsets behind the rings
     __host__ __device__ static constexpr int align_k(int x) { return (x + 1023) & ~1023; }
@@ -173,6 +175,7 @@ __device__ __forceinline__ void blk_plan(const BlkArgs &a, int *s_pref, int2 *s_
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = a.batch;
     const int per = (B + NT - 1) / NT, lo = min(B, tid * per), hi = min(B, lo + per);
     int run = 0;
+#pragma unroll 1
     for (int b = lo; b < hi; ++b) run += blk_tiles(blk_len(a, b));
     int incl = run;
 #pragma unroll
@@ -183,8 +186,10 @@ __device__ __forceinline__ void blk_plan(const BlkArgs &a, int *s_pref, int2 *s_
     if (lane == 31) s_w[warp] = incl;
     __syncthreads();
     int base = 0;
+#pragma unroll 1
     for (int w = 0; w < warp; ++w) base += s_w[w];
     int excl = base + incl - run;
+#pragma unroll 1
     for (int b = lo; b < hi; ++b) {
         s_pref[b] = excl;
         const int n = blk_len(a, b);
@@ -195,8 +200,7 @@ __device__ __forceinline__ void blk_plan(const BlkArgs &a, int *s_pref, int2 *s_
     __syncthreads();
 }
 
-// Ranges per head, and their length in tiles.
-__device__ __forceinline__ int blk_ranges(int workers, int Hkv) { return max(workers / Hkv, 1); }
+// Length of a head's ranges in tiles.
 __device__ __forceinline__ int blk_width(const int *s_pref, int B, int ranges) { return (s_pref[B] + ranges - 1) / ranges; }
 
 // The walk over one unit's pieces of segments.
@@ -267,11 +271,12 @@ __device__ __forceinline__ void blk_loader(const BlkArgs &a, const int *s_pref, 
     using C = BlkCfg<D, E8, GP>;
     const CUtensorMap *m16 = isv ? &a.tm_v16 : &a.tm_k16, *m1 = isv ? &a.tm_v1 : &a.tm_k1;
     const uint8_t *exps = isv ? a.v_exp : a.k_exp;
-    const int units = blk_ranges(a.workers, a.Hkv) * a.Hkv;
+    const int units = a.ranges * a.Hkv;
     BlkWalk k;
     bool more = false;
     // to the next unit that has a piece
     auto open = [&]() {
+#pragma unroll 1
         for (more = false; !more && unit < units; unit += a.workers) {
             k = blk_begin(s_pref, a.batch, a.Hkv, W, unit);
             more = blk_piece(s_pref, s_req, k);
@@ -284,6 +289,7 @@ __device__ __forceinline__ void blk_loader(const BlkArgs &a, const int *s_pref, 
     auto fetch = [&]() {
 #pragma unroll
         for (int u = 0; u < kBlkAhead; ++u) {
+#pragma unroll 1
             while (more && i >= k.live) {
                 blk_next(k);
                 more = blk_piece(s_pref, s_req, k);
@@ -384,6 +390,7 @@ __device__ __forceinline__ void blk_loader(const BlkArgs &a, const int *s_pref, 
                 }
             } else {
                 // no valid row at all: zeros (weight zero times whatever bits lie there could be NaN)
+    #pragma unroll 1
                 for (int o = lane * 16; o < C::TILE; o += 512) st_shared_v4(dst + o, 0u, 0u, 0u, 0u);
                 fence_proxy_async_smem();
             }
@@ -406,6 +413,7 @@ __device__ __forceinline__ void blk_loader(const BlkArgs &a, const int *s_pref, 
     }
     if (*s_abort) {
         // aborted: the copies already issued land before the shared memory goes away
+#pragma unroll 1
         for (int j = max(0, seq - stages); j < seq; ++j) mbar_drain(full + (j % stages) * 8, (j / stages) & 1);
     }
     if (errs) set_error(a.err, errs);
@@ -444,12 +452,15 @@ __device__ __forceinline__ void blk_merge(const BlkArgs &a, const BlkSpan &s, in
     const int chunks = G * D / 4;                          // 16-byte chunks of a piece
     const int cap = (scratch_bytes - (int)((s_o - scratch) * 4)) / (G * D * 4);
     auto copy = [&](int p0, int n) {
-        for (int i = t; i < n * chunks; i += 128) {
-            const int p = i / chunks, c = i - p * chunks;
-            cp_async_16(smem_u32(s_o) + i * 16, a.o_part + (int64_t)slot(p0 + p) * G * D + c * 4, 16);
+#pragma unroll 2
+        for (int p = 0; p < n; ++p) {
+            const float *src = a.o_part + (int64_t)slot(p0 + p) * G * D;
+#pragma unroll 1
+            for (int c = t; c < chunks; c += 128) cp_async_16(smem_u32(s_o) + (p * chunks + c) * 16, src + c * 4, 16);
         }
     };
     copy(0, min(np, cap));
+#pragma unroll 1
     for (int i = t; i < np * G; i += 128) {
         const int p = i / G;
         const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.ml_part + (slot(p) * G + (i - p * G)) * 2));
@@ -457,12 +468,15 @@ __device__ __forceinline__ void blk_merge(const BlkArgs &a, const BlkSpan &s, in
         s_l[i] = ml.y;
     }
     named_bar_sync(bar_id, 128);
+#pragma unroll 1
     for (int g = warp; g < G; g += 4) {
         float M = -INFINITY;
+#pragma unroll 1
         for (int p = lane; p < np; p += 32) M = fmaxf(M, s_w[p * G + g]);
         M = warp_max(M);
         const float Mz = M == -INFINITY ? 0.f : M;
         float L = 0.f;
+#pragma unroll 1
         for (int p = lane; p < np; p += 32) {
             const float w = blk_ex2(s_w[p * G + g] - Mz);
             s_w[p * G + g] = w;
@@ -479,6 +493,7 @@ __device__ __forceinline__ void blk_merge(const BlkArgs &a, const BlkSpan &s, in
     float4 acc[NJ];
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
     for (int p0 = 0; p0 < np; p0 += cap) {
         const int n = min(cap, np - p0);
         if (p0 > 0) {
@@ -493,7 +508,7 @@ __device__ __forceinline__ void blk_merge(const BlkArgs &a, const BlkSpan &s, in
             if (c >= chunks) break;
             const float4 *so = reinterpret_cast<const float4 *>(s_o) + c;
             const float *w = s_w + p0 * G + c * 4 / D;
-#pragma unroll 8
+#pragma unroll 2
             for (int p = 0; p < n; ++p) {
                 const float4 v = so[p * chunks];
                 const float x = w[p * G];
@@ -560,6 +575,7 @@ __global__ void __launch_bounds__(kBlkThreads, 1) decode_block_kernel(const __gr
     if (a.early_meta) pdl_wait();
     pdl_launch_dependents();
     if (blockIdx.x == 0) {
+#pragma unroll 1
         for (int b = tid; b < a.batch; b += kBlkThreads) {
             const int row = __ldg(a.req_pool_indices + b), n = __ldg(a.seq_lens + b);
             if (row < 0 || row >= a.req_rows) set_error(a.err, PA_DEVERR_ROW);
@@ -568,10 +584,10 @@ __global__ void __launch_bounds__(kBlkThreads, 1) decode_block_kernel(const __gr
     }
     tc_fence_after();
     const uint32_t tmem = s_tmem;
-    const int ranges = blk_ranges(a.workers, a.Hkv), units = ranges * a.Hkv, W = blk_width(s_pref, a.batch, ranges);
+    const int units = a.ranges * a.Hkv, W = blk_width(s_pref, a.batch, a.ranges);
     // few units: one per SM; else the heads of a range side by side on an SM
-    const int worker = (s_pref[a.batch] + W - 1) / W * a.Hkv <= (int)gridDim.x ? (int)blockIdx.x + wg * (int)gridDim.x
-                                                                           : 2 * (int)blockIdx.x + wg;
+    const int worker = s_pref[a.batch] <= (long long)a.spread * W ? (int)blockIdx.x + wg * (int)gridDim.x
+                                                                  : 2 * (int)blockIdx.x + wg;
 
     if (warp >= 8) {
         const bool isv = warp & 1;
@@ -611,6 +627,7 @@ __global__ void __launch_bounds__(kBlkThreads, 1) decode_block_kernel(const __gr
                 if (g < a.G) qn[r] = __ldg(reinterpret_cast<const uint4 *>(a.q + ((int64_t)k.b * a.Hq + k.h * a.G + g) * D) + c);
             }
         };
+#pragma unroll 1
         for (int unit = worker; unit < units; unit += a.workers) {
         BlkWalk kn = blk_begin(s_pref, a.batch, a.Hkv, W, unit);
         bool more = blk_piece(s_pref, s_req, kn);
@@ -671,6 +688,7 @@ __global__ void __launch_bounds__(kBlkThreads, 1) decode_block_kernel(const __gr
 #pragma unroll
             for (int g = 0; g < GP; ++g) m[g] = r[g] = -INFINITY, l[g] = o[g] = 0.f;
 
+#pragma unroll 1
             for (int i = 0; i < k.live; ++i, ++done) {
                 const uint32_t kt = kring + stk * C::TILE, vt = vring + stv * C::TILE;
                 // S = K Q^T
@@ -821,43 +839,46 @@ __global__ void __launch_bounds__(kBlkThreads, 1) decode_block_kernel(const __gr
             blk_next(kn);
             more = blk_piece(s_pref, s_req, kn);
             if (more) load_q(kn);
+            // O, m and r through the P tile (its products are done), so that the stores below are one rolled loop
+            float *so = reinterpret_cast<float *>(base + C::OffP + wg * C::align_k(C::PB)), *smr = s_max;   // [GP][128]; [GP] m, [GP] r
 #pragma unroll
             for (int g = 0; g < GP; ++g) {
                 float s = l[g];
 #pragma unroll
                 for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
                 if (lane == 0) s_sum[(warp & 3) * GP + g] = s;
+                so[g * 128 + t] = o[g];
+                if (t == 0) {
+                    smr[g] = m[g];
+                    smr[GP + g] = r[g];
+                }
             }
             named_bar_sync(bar_id, 128);
             const bool whole = k.t0 == 0 && k.t1 == k.tb;
-            if (!bad) {
-                const int part = unit * 2 + (k.t0 == 0 && k.S0 % W != 0 ? 1 : 0);
-#pragma unroll
-                for (int g = 0; g < GP; ++g) {
-                    if (g >= a.G) break;
-                    const float L = s_sum[g] + s_sum[GP + g] + s_sum[2 * GP + g] + s_sum[3 * GP + g];
-                    // O relative to m: 2^(r - 127 - 8 - m)
-                    const float mz = m[g] == -INFINITY ? 0.f : m[g], rz = r[g] == -INFINITY ? 0.f : r[g];
-                    const float O = E8 ? o[g] * blk_ex2(rz - mz - 135.f) : o[g];
+            const int part = unit * 2 + (k.t0 == 0 && k.S0 % W != 0 ? 1 : 0);
+#pragma unroll 1
+            for (int g = 0; g < a.G && !bad; ++g) {
+                const float L = s_sum[g] + s_sum[GP + g] + s_sum[2 * GP + g] + s_sum[3 * GP + g];
+                const float mg = smr[g], rg = smr[GP + g];
+                // O relative to m: 2^(r - 127 - 8 - m)
+                const float mz = mg == -INFINITY ? 0.f : mg, rz = rg == -INFINITY ? 0.f : rg;
+                const float O = E8 ? so[g * 128 + t] * blk_ex2(rz - mz - 135.f) : so[g * 128 + t];
+                if (whole) {
                     const int64_t hq = (int64_t)k.b * a.Hq + k.h * a.G + g;
-                    if (whole) {
-                        if (t < D) a.out[hq * D + t] = __float2bfloat16_rn(L != 0.f ? O / L : 0.f);
-                        if (WT && t == 0) a.lse[hq] = L != 0.f ? m[g] + log2f(L) : INFINITY;
-                    } else {
-                        if (t < D) a.o_part[((int64_t)part * a.G + g) * D + t] = O;
-                        if (t == 0) {
-                            a.ml_part[(part * a.G + g) * 2] = m[g];
-                            a.ml_part[(part * a.G + g) * 2 + 1] = L;
-                        }
-                    }
+                    if (t < D) a.out[hq * D + t] = __float2bfloat16_rn(L != 0.f ? O / L : 0.f);
+                    if (WT && t == 0) a.lse[hq] = L != 0.f ? mg + log2f(L) : INFINITY;
+                } else {
+                    const int at = part * a.G + g;
+                    if (t < D) a.o_part[at * D + t] = O;
+                    if (t == 0) *reinterpret_cast<float2 *>(a.ml_part + at * 2) = make_float2(mg, L);
                 }
             }
             if (!whole) {
-                // a ticket for the piece: the barrier orders the partials' stores before thread 0's acquire-release
-                // addition; the answer is looked at after the unit's last piece
+                // a ticket for the piece: the barrier orders the partials' stores before thread 0's releasing addition;
+                // the answer is looked at (and acquired from) after the unit's last piece
                 named_bar_sync(bar_id, 128);
                 if (t == 0 && !bad) {
-                    const int old = atom_add_acq_rel_gpu(a.tickets + k.S0 / W * a.Hkv + k.h, 1);
+                    const int old = atom_add_release_gpu(a.tickets + k.S0 / W * a.Hkv + k.h, 1);
                     if (shared == 0) ticket[0] = old;
                     else ticket[1] = old;
                 }
@@ -867,15 +888,19 @@ __global__ void __launch_bounds__(kBlkThreads, 1) decode_block_kernel(const __gr
             }
         }
         // shared segments whose last piece was this unit's
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (i >= shared) break;
-            const BlkSpan s = blk_span(s_pref, W, shared_b[i]);
+#pragma unroll 1
+        for (int i = 0; i < shared; ++i) {
+            const int sb = i == 0 ? shared_b[0] : shared_b[1];
+            const BlkSpan s = blk_span(s_pref, W, sb);
             const int h = unit % a.Hkv;
-            if (t == 0) s_last[wg][i] = !bad && ticket[i] == s.i1 - s.i0;
+            if (t == 0) {
+                const bool last = !bad && (i == 0 ? ticket[0] : ticket[1]) == s.i1 - s.i0;
+                if (last) fence_acq_rel_gpu();      // the other workers' partials are visible to what follows
+                s_last[wg][i] = last;
+            }
             named_bar_sync(bar_id, 128);
             if (s_last[wg][i]) {
-                blk_merge<D, GP, WT>(a, s, shared_b[i], h, t, bar_id, reinterpret_cast<float *>(smem_raw + (kring - raw)), ring_bytes);
+                blk_merge<D, GP, WT>(a, s, sb, h, t, bar_id, reinterpret_cast<float *>(smem_raw + (kring - raw)), ring_bytes);
                 if (t == 0) a.tickets[s.i0 * a.Hkv + h] = 0;
             }
         }
@@ -911,17 +936,21 @@ static __global__ void __launch_bounds__(kBlkWeightThreads) decode_block_weights
     if (a.early_meta) pdl_wait();
     pdl_launch_dependents();
     const int tiles = s_pref[B];
+#pragma unroll 1
     for (int x = blockIdx.x; x < tiles; x += gridDim.x) {
         int lo = 0, hi = B;
-        while (hi - lo > 1) {
+    #pragma unroll 1
+    while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (s_pref[mid] <= x) lo = mid; else hi = mid;
         }
         const int b = lo, n = blk_len(a, b), row = __ldg(a.req_pool_indices + b);
         // two requests of a row would both add to it: the later one is refused
         int again = 0;
+#pragma unroll 1
         for (int c = tid; c < b; c += kBlkWeightThreads) again |= __ldg(a.req_pool_indices + c) == row;
         __syncthreads();   // s_lse is free
+#pragma unroll 1
         for (int hq = tid; hq < a.Hq; hq += kBlkWeightThreads) s_lse[hq] = __ldcg(a.lse + (int64_t)b * a.Hq + hq);
         again = __syncthreads_or(again);
         if (n <= 0) continue;
@@ -944,7 +973,7 @@ static __global__ void __launch_bounds__(kBlkWeightThreads) decode_block_weights
                     w += blk_ex2(v.x - l[0]) + blk_ex2(v.y - l[1]) + (blk_ex2(v.z - l[2]) + blk_ex2(v.w - l[3]));
                 }
             } else {
-#pragma unroll 8
+#pragma unroll 4
                 for (int hq = 0; hq < a.Hq; ++hq) {
                     const int h = hq / G;
                     w += blk_ex2(__ldcg(sc + h * head + hq - h * G) - s_lse[hq]);
@@ -972,6 +1001,8 @@ static pa_status launch_block(BlkArgs a, cudaStream_t st)
     if (!ensure_dynamic_smem(reinterpret_cast<const void *>(kern), smem)) return PA_ERR_CUDA;
     const int grid = num_sms() < kBlkMaxWorkers / 2 ? num_sms() : kBlkMaxWorkers / 2;
     a.workers = 2 * grid;
+    a.ranges = a.workers / a.Hkv > 1 ? a.workers / a.Hkv : 1;
+    a.spread = grid / a.Hkv;
     if (launch_kernel(kern, dim3(grid), dim3(kBlkThreads), smem, st, a) != cudaSuccess) return PA_ERR_CUDA;
     if constexpr (WT) {
         const size_t wsmem = ((size_t)a.batch + 1) * 4 + (size_t)a.Hq * 4;
