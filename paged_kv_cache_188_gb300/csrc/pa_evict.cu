@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(const EvictArgs a)
 
     pdl_wait();
     pdl_launch_dependents();
-    const int len = __ldg(a.seq_lens + b), row = __ldg(a.req_pool_indices + b);
+    const int len = __ldcg(a.seq_lens + b), row = __ldg(a.req_pool_indices + b);
     int bits = 0;
     if (row < 0 || row >= a.req_rows) bits |= PA_DEVERR_ROW;
     if (len < 0 || len > a.max_ctx) bits |= PA_DEVERR_LEN;
@@ -76,6 +76,7 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(const EvictArgs a)
     if (__syncthreads_or(again)) bits |= PA_DEVERR_ROW;
     const int n = len < 0 ? 0 : min(len, a.max_ctx);
     if (bits || n <= a.budget) {              // the same for every CTA of the cluster
+        cl.sync();                            // new_lens may be seq_lens: every CTA has read the length
         if (rank == 0 && tid == 0) {
             a.new_lens[b] = n;
             if (bits) set_error(a.err, bits);

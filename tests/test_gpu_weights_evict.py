@@ -273,6 +273,21 @@ def test_evict_lengths_in_place_and_in_a_graph():
             assert freed[b, :len(gone)].tolist() == gone
 
 
+def test_evict_lengths_in_place_past_the_end():
+    """Lengths past max_ctx or negative, in place, rows wide enough for several CTAs per request: every CTA of a
+    request has to see the length as it was."""
+    B, max_ctx = 40, 33000
+    t = torch.arange(B * max_ctx, dtype=torch.int32, device="cuda").view(B, max_ctx).contiguous()
+    w = torch.rand((B, max_ctx), generator=gen(3)).cuda()
+    t0, w0 = t.clone(), w.clone()
+    lens = [max_ctx + 1 + b if b % 2 else -b for b in range(B)]
+    dev, freed, err = i32(lens), torch.full((B, max_ctx), -1, dtype=torch.int32, device="cuda"), i32([0])
+    api.pa_kv_evict(t, i32(list(range(B))), dev, w, 10, 3, dev, freed, err)
+    assert api.pa_get_error_word(err) == api.DEVERR_LEN
+    assert dev.tolist() == [max_ctx if b % 2 else 0 for b in range(B)]
+    assert torch.equal(t, t0) and torch.equal(w, w0) and (freed == -1).all()
+
+
 # ------------------------------------------------------------ a serving loop
 
 @pytest.mark.parametrize("block", [0, 1])
