@@ -379,7 +379,11 @@ pa_status pa_paged_decode_attn_fp8_block(const void *q, int batch, int n_q_heads
 
 /* pa_paged_prefill_attn_fp8_block: pa_paged_prefill_attn over this cache, the
  * same arguments, workspace, limits and error reporting plus the exponents.
- * The tiles are widened to bf16 with their scale (exact) before the MMAs. */
+ * Q K^T runs on the e4m3 rows as they are, q as a sum of two e4m3 terms (within
+ * 2^-19 of the row's largest element) and each key's scale on its scores; V is
+ * widened to bf16 with its scale (exact) and the weights are rounded to bf16, as
+ * in pa_paged_prefill_attn.  A query row that holds a NaN or an infinity gives
+ * NaN. */
 pa_status pa_paged_prefill_attn_fp8_block(const void *q, int n_tokens, int n_q_heads, const void *k_buf,
                                           const void *v_buf, pa_kv_shape s, int layer_id, const int32_t *qo_indptr,
                                           const int32_t *kv_indptr, int n_reqs, const int32_t *req_to_token,
@@ -400,8 +404,8 @@ pa_status pa_paged_prefill_attn_fp8_block(const void *q, int n_tokens, int n_q_h
  * (a request's additions of one call sum to n_q_heads; calls of several layers
  * may add to one table).  Entries j >= seq_lens[b] are not touched: the caller
  * zeroes a row when it hands it out.  The requests of a call must have rows of
- * their own: a request whose row an earlier one has sets PA_DEVERR_ROW and adds
- * nothing (its output is right).  Workspace:
+ * their own: a request whose row an earlier one of at least one token has sets
+ * PA_DEVERR_ROW and adds nothing (its output is right).  Workspace:
  * pa_decode_weights_workspace_bytes for at most max_batch requests of
  * max_tokens cached tokens in all; a call with more sets PA_DEVERR_LEN and adds
  * nothing for the requests' tiles past that (outputs are right).  Else as
@@ -428,9 +432,12 @@ pa_status pa_paged_decode_attn_weights(const void *q, int batch, int n_q_heads, 
  * they were rotated: positions given to later tokens go on counting from the
  * original length.  K/V rows are not moved; with a block-scaled cache, hand
  * slots out again only when all slots of their block are free.  new_lens may be
- * seq_lens.  A row out of range, or one that an earlier request of the call has
- * too, sets PA_DEVERR_ROW, a length outside [0, max_ctx] PA_DEVERR_LEN; such a
- * request is left as it is (new_lens[b] is its length, clamped). */
+ * seq_lens.  A row out of range, or one that an earlier request of at least one
+ * token has too, sets PA_DEVERR_ROW, a length outside [0, max_ctx] PA_DEVERR_LEN; such a
+ * request is left as it is (new_lens[b] is its length, clamped).  The table and
+ * the lengths are index inputs of later calls: in the early-metadata modes the
+ * call right after this one must not read them (switch the overlap off or to
+ * safe for it). */
 pa_status pa_kv_evict(int32_t *req_to_token, int req_rows, int max_ctx, const int32_t *req_pool_indices,
                       const int32_t *seq_lens, int batch, float *weights, int budget, int recent,
                       int32_t *new_lens, int32_t *freed, int32_t *error_word, cudaStream_t st);

@@ -390,7 +390,7 @@ __device__ __forceinline__ void blk_loader(const BlkArgs &a, const int *s_pref, 
                 }
             } else {
                 // no valid row at all: zeros (weight zero times whatever bits lie there could be NaN)
-    #pragma unroll 1
+#pragma unroll 1
                 for (int o = lane * 16; o < C::TILE; o += 512) st_shared_v4(dst + o, 0u, 0u, 0u, 0u);
                 fence_proxy_async_smem();
             }
@@ -939,16 +939,18 @@ static __global__ void __launch_bounds__(kBlkWeightThreads) decode_block_weights
 #pragma unroll 1
     for (int x = blockIdx.x; x < tiles; x += gridDim.x) {
         int lo = 0, hi = B;
-    #pragma unroll 1
-    while (hi - lo > 1) {
+#pragma unroll 1
+        while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (s_pref[mid] <= x) lo = mid; else hi = mid;
         }
         const int b = lo, n = blk_len(a, b), row = __ldg(a.req_pool_indices + b);
         // two requests of a row would both add to it: the later one is refused
+        // (after one without tokens, a batch's padding, it is not)
         int again = 0;
 #pragma unroll 1
-        for (int c = tid; c < b; c += kBlkWeightThreads) again |= __ldg(a.req_pool_indices + c) == row;
+        for (int c = tid; c < b; c += kBlkWeightThreads)
+            if (__ldg(a.req_pool_indices + c) == row) again |= blk_len(a, c) > 0;
         __syncthreads();   // s_lse is free
 #pragma unroll 1
         for (int hq = tid; hq < a.Hq; hq += kBlkWeightThreads) s_lse[hq] = __ldcg(a.lse + (int64_t)b * a.Hq + hq);

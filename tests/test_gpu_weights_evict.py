@@ -288,6 +288,31 @@ def test_evict_lengths_in_place_past_the_end():
     assert torch.equal(t, t0) and torch.equal(w, w0) and (freed == -1).all()
 
 
+def test_padding_without_tokens_may_share_a_row():
+    """A padded batch: requests of no tokens name the row of a real one, before and after it."""
+    c = Bf16Cache([0, 300, 0, 40], 2, 64, 16, 10).cuda()
+    c.dev[3][0] = c.dev[3][2] = c.dev[3][1]
+    q = torch.randn((4, 4, 64), generator=c.g).to(torch.bfloat16)
+    w = torch.zeros(c.table.shape, device="cuda")
+    out, ws = weights_call(c, q.cuda(), 0.1, w)
+    assert api.pa_get_error(ws) == 0 and not out[0].any() and not out[2].any()
+    for b in (1, 3):
+        k, v = c.values(b)
+        r = R.attention(q[b][None].double(), k, v, 0.1)
+        R.check_out(out[b][None].cpu(), r, 12, "padded batch")
+        want = r["p"][0].sum(0)
+        tol = (r["p"][0] * (2 * r["ds"][0][:, None] + 2.0 ** -18)).sum(0) + 2.0 ** -22 * want + 1e-30
+        assert ((w[int(c.rows[b]), :c.lens[b]].cpu().double() - want).abs() <= tol).all()
+    # eviction of the same batch
+    table, slots, new = c.dev[2].clone(), c.dev[2][int(c.rows[1])].tolist(), i32([-1] * 4)
+    heavy = w[int(c.rows[1])].tolist()
+    freed, err = torch.full((4, table.shape[1]), -1, dtype=torch.int32, device="cuda"), i32([0])
+    api.pa_kv_evict(table, c.dev[3], i32(c.lens), w, 100, 10, new, freed, err)
+    assert api.pa_get_error_word(err) == 0 and new.tolist() == [0, 100, 0, 40]
+    kept, _, gone = R.evict(slots[:300], heavy[:300], 100, 10)
+    assert table[int(c.rows[1]), :100].tolist() == kept and freed[1, :200].tolist() == gone
+
+
 # ------------------------------------------------------------ a serving loop
 
 @pytest.mark.parametrize("block", [0, 1])
