@@ -355,8 +355,8 @@ pa_status pa_kv_reset_fp8_block(uint8_t *k_exp, uint8_t *v_exp, int n_layers, in
                                 const int32_t *blocks, int n, int32_t *error_word, cudaStream_t st);
 
 /* pa_paged_decode_attn_fp8_block: what pa_paged_decode_attn computes, over this
- * cache.  Supported: head_dim 64 or 128, 1 <= G <= 16, batch <= 4096.  QK^T and
- * PV run on tcgen05 with the e4m3 rows as they are; q and the softmax weights
+ * cache.  Supported: head_dim 64 or 128, 1 <= G <= 16, at most 4096 query heads,
+ * batch <= 4096.  QK^T and PV run on tcgen05 with the e4m3 rows as they are; q and the softmax weights
  * enter as sums of e4m3 terms (q within 2^-22 of its head's largest element,
  * weights to 12 bits), products and sums in fp32.  One kernel; a (request, kv
  * head) that several CTAs worked on is merged in a fixed order by the one that

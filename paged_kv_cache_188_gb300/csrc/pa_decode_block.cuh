@@ -64,6 +64,7 @@ constexpr int kBlkThreads = 256 + 128;  // two warpgroups, two loader warps for 
 constexpr int kBlkMaxWorkers = 320;     // warpgroups of a launch: two per SM (152 SMs)
 constexpr int kBlkMaxStages = 6;        // per warpgroup and operand
 constexpr int kBlkMaxBatch = 4096;
+constexpr int kBlkMaxHeads = 4096;      // query heads: their log-sum-exps beside the batch's plan in the weights kernel
 constexpr int kBlkAhead = 2;            // tiles of a loader's batch
 constexpr int kBlkStageBytes = (kBlkAhead * (32 * 20 + 12) + 15) / 16 * 16;
 constexpr uint32_t kBlkTmemCols = 256; // per warpgroup 128: S at 0, O at 64
@@ -1005,10 +1006,10 @@ static pa_status launch_block(BlkArgs a, cudaStream_t st)
     a.workers = 2 * grid;
     a.ranges = a.workers / a.Hkv > 1 ? a.workers / a.Hkv : 1;
     a.spread = grid / a.Hkv;
+    const size_t wsmem = ((size_t)a.batch + 1) * 4 + (size_t)a.Hq * 4;
+    if (WT && !ensure_dynamic_smem(reinterpret_cast<const void *>(decode_block_weights_kernel), wsmem)) return PA_ERR_CUDA;
     if (launch_kernel(kern, dim3(grid), dim3(kBlkThreads), smem, st, a) != cudaSuccess) return PA_ERR_CUDA;
     if constexpr (WT) {
-        const size_t wsmem = ((size_t)a.batch + 1) * 4 + (size_t)a.Hq * 4;
-        if (!ensure_dynamic_smem(reinterpret_cast<const void *>(decode_block_weights_kernel), wsmem)) return PA_ERR_CUDA;
         if (launch_kernel(decode_block_weights_kernel, dim3(4 * grid), dim3(kBlkWeightThreads), wsmem, st, a) != cudaSuccess)
             return PA_ERR_CUDA;
     }

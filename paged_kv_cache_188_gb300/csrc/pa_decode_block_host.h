@@ -38,7 +38,7 @@ inline pa_status check_block(const void *q, int batch, int Hq, const void *k_buf
     if (Hq % s.n_kv_heads != 0) return PA_ERR_SHAPE;
     if (e4m3 && !block_ok(block)) return PA_ERR_SHAPE;
     const int G = Hq / s.n_kv_heads;
-    if (G > 16 || (s.head_dim != 64 && s.head_dim != 128)) return PA_ERR_UNSUPPORTED;
+    if (G > 16 || Hq > kBlkMaxHeads || (s.head_dim != 64 && s.head_dim != 128)) return PA_ERR_UNSUPPORTED;
     if ((int64_t)s.n_layers * s.size >= (int64_t)INT32_MAX - 16) return PA_ERR_SHAPE;
     // tiles of all segments in 32 bits
     if (((int64_t)max_ctx + kBlkTile - 1) / kBlkTile * s.n_kv_heads * (batch > 0 ? batch : 1) >= (int64_t)INT32_MAX / 2)
@@ -81,7 +81,7 @@ inline bool fill_block(BlkArgs &a, const void *q, int batch, int Hq, const void 
     a.req_pool_indices = req_pool_indices;
     a.seq_lens = seq_lens;
     if (e4m3) {
-        const int64_t layer_exps = (int64_t)layer_id * ((s.size + block - 1) / block) * s.n_kv_heads;
+        const int64_t layer_exps = (int64_t)layer_id * (((int64_t)s.size + block - 1) / block) * s.n_kv_heads;
         a.k_exp = k_exp + layer_exps;
         a.v_exp = v_exp + layer_exps;
         while ((1 << a.block_shift) < block) ++a.block_shift;

@@ -63,6 +63,8 @@ def test_decode_refusals(lib):
     assert call(max_ctx=0) == 2 and call(block=0) == 2 and call(block=48) == 2
     assert call(batch=4096, max_ctx=2 ** 30) == 2             # tiles beyond 32 bits
     assert call(s=shape(d=96)) == 4 and call(hq=64) == 4
+    big = api.KvShape(1, 64, 4097, 64)                        # more query heads than are supported
+    assert call(s=big, hq=4097, wsb=1 << 40) == 4
     assert call(q=0) == 1 and call(ke=0) == 1 and call(ws=0) == 1 and call(out=0) == 1
     assert call(q=FAKE + 4) == 3 and call(ws=FAKE + 16) == 3 and call(sl=FAKE + 1) == 3
     assert call(wsb=need - 1) == 5
