@@ -432,8 +432,8 @@ pa_status pa_paged_decode_attn_weights(const void *q, int batch, int n_q_heads, 
  * they were rotated: positions given to later tokens go on counting from the
  * original length.  K/V rows are not moved; with a block-scaled cache, hand
  * slots out again only when all slots of their block are free.  new_lens may be
- * seq_lens.  A row out of range, or one that an earlier request of at least one
- * token has too, sets PA_DEVERR_ROW, a length outside [0, max_ctx] PA_DEVERR_LEN; such a
+ * seq_lens.  A row out of range, or one that an earlier request has too (both
+ * of at least one token), sets PA_DEVERR_ROW, a length outside [0, max_ctx] PA_DEVERR_LEN; such a
  * request is left as it is (new_lens[b] is its length, clamped).  The table and
  * the lengths are index inputs of later calls: in the early-metadata modes the
  * call right after this one must not read them (switch the overlap off or to

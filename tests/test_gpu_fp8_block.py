@@ -237,6 +237,16 @@ def test_decode_scales_far_apart():
     check_decode(c, q, out, 0.05, "far scales")
 
 
+@pytest.mark.parametrize("G,Hkv,D,lens", [(1, 400, 64, [1, 300, 0, 129]), (1, 700, 128, [40, 200]), (16, 256, 64, [130])])
+def test_decode_more_heads_than_workers(G, Hkv, D, lens):
+    """Warpgroups that serve several kv heads one after the other; the most query heads."""
+    c = Cache(lens, Hkv, D, 16, 16, Hkv, layers=1, layer=0).cuda()
+    q = torch.randn((len(lens), Hkv * G, D), generator=c.g).to(torch.bfloat16)
+    out, ws = decode(c, q.cuda(), 0.1)
+    assert api.pa_get_error(ws) == 0
+    check_decode(c, q, out, 0.1, f"{Hkv} kv heads")
+
+
 @pytest.mark.parametrize("mag", [2.0 ** -100, 2.0 ** 90, "mixed"])
 def test_decode_q_magnitudes(mag):
     """Queries far from 1, and heads whose elements differ by 2^20."""
