@@ -71,14 +71,19 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(const EvictArgs a)
     if (row < 0 || row >= a.req_rows) bits |= PA_DEVERR_ROW;
     if (len < 0 || len > a.max_ctx) bits |= PA_DEVERR_LEN;
     // two requests of one row would both compact it: the later one is refused
-    // (requests without tokens, a batch's padding, do not count)
+    // (requests without tokens, a batch's padding, do not count: looked at only
+    // where a row comes twice)
     int again = 0;
-    for (int c = tid; c < b; c += kEvThreads)
-        if (__ldg(a.req_pool_indices + c) == row) again |= __ldcg(a.seq_lens + c) > 0;
-    if (__syncthreads_or(again) && len > 0) bits |= PA_DEVERR_ROW;
+    for (int c = tid; c < b; c += kEvThreads) again |= __ldg(a.req_pool_indices + c) == row;
+    if (__syncthreads_or(again) && len > 0) {
+        again = 0;
+        for (int c = tid; c < b; c += kEvThreads)
+            again |= __ldg(a.req_pool_indices + c) == row && __ldcg(a.seq_lens + c) > 0;
+        if (__syncthreads_or(again)) bits |= PA_DEVERR_ROW;
+    }
     const int n = len < 0 ? 0 : min(len, a.max_ctx);
     if (bits || n <= a.budget) {              // the same for every CTA of the cluster
-        cl.sync();                            // new_lens may be seq_lens: every CTA has read the length
+        if (bits & PA_DEVERR_LEN) cl.sync();  // new_lens may be seq_lens: every CTA has read the length that changes
         if (rank == 0 && tid == 0) {
             a.new_lens[b] = n;
             if (bits) set_error(a.err, bits);
