@@ -60,17 +60,6 @@ __device__ __forceinline__ float ld_cg_ordered_if(bool pred, const float *p)
     return v;
 }
 
-// The same for 16 bytes.
-__device__ __forceinline__ float4 ld_cg_ordered_f4_if(bool pred, const float4 *p)
-{
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %5, 0;\n @q ld.global.cg.v4.f32 {%0,%1,%2,%3}, [%4];\n}\n"
-                 : "+f"(v.x), "+f"(v.y), "+f"(v.z), "+f"(v.w)
-                 : "l"(p), "r"((int)pred)
-                 : "memory");
-    return v;
-}
-
 __device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t &r0, uint32_t &r1, uint32_t &r2, uint32_t &r3)
 {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"

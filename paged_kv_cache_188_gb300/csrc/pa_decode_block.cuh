@@ -35,11 +35,11 @@
 // Work: the requests' 128-token tiles (at least one each), laid end to end, are
 // cut into equal ranges of W tiles, as many as there are warpgroups (two on an
 // SM) per kv head; unit (range i, head h) is worker i Hkv + h's.  All heads of a
-// token are then read at about the same time: a row's 128 bytes of one head
-// alone, 1 KB apart, reach 4.6 TB/s, its neighbours beside them let HBM finish
-// a page it has opened.  A unit has at most two (request, head) segments it
-// shares with others, its first and its last, so the fp32 partials are two
-// slots per unit whatever the batch is.  The one that finishes a shared segment's
+// token are then read at about the same time, so that HBM finishes a page it has
+// opened (a row's 128 bytes of one head alone, 1 KB apart: 70 us for 48 requests
+// of 500 to 8192 tokens, 32 heads over 8, D = 128; 61 side by side).  A unit has
+// at most two (request, head) segments it shares with others, its first and its
+// last, so the fp32 partials are two slots per unit whatever the batch is.  The one that finishes a shared segment's
 // last piece (a ticket per segment) merges its pieces in order (deterministic);
 // a second kernel adds the weights (WT).
 //
@@ -47,9 +47,20 @@
 // tensor-memory columns, so one's softmax, item starts and item ends run beside
 // the other's products; each issues its own MMAs.  Two loader warps serve each
 // warpgroup: one the K tiles and exponents, one the V's.  16 consecutive slots
-// move as one TMA box, any other four rows as one gather4 copy.  Positions past
-// the end repeat a valid row (weight zero), so nothing behind the last token is
-// read.
+// move as one TMA box, any other four rows as one gather4 copy (16-byte cp.async
+// copies instead: at pages of one slot 80.6 us against 75.0 for the 48 requests,
+// 25.6 against 27.5 for one of 32K tokens).  Positions past the end repeat a valid
+// row (weight zero), so nothing behind the last token is read.
+//
+// Bound, and what was measured (e4m3, D = 128, 32 heads over 8, blocks and pages of
+// 16; in a graph): HBM, 2 D + 2 / block bytes per token and head: those 48 requests
+// 56.4 us, 5.2 TB/s (the floor is 42.9 us); one request of 32768 tokens 24.9 us
+// (9.9); of 1000 tokens 9.8 us (0.3): launch and plan, the first tile's chain of
+// table, exponents, rows, the products' chain, then tickets and merge, each one or
+// two round trips; its instructions are cold as well (a quarter of the issue slots
+// lost wait for them).  Two tiles a warpgroup are too few to hide a tile's chain of
+// two products, but issuing the next tile's S before O is read gains nothing (58.7
+// us against 58.0): the copies are what is waited for.
 #include <math.h>
 #include <string.h>
 
@@ -925,7 +936,9 @@ __global__ void __launch_bounds__(kBlkThreads, 1) decode_block_kernel(const __gr
 constexpr int kBlkWeightThreads = 128;
 
 // weights[row, j] += sum over the heads of 2^(score - lse), one 128-token tile
-// of a request at a time, heads in order.
+// of a request at a time, heads in order.  A kernel of its own, because a score's
+// sum is known only when its last piece is; scores pass through L2 (4 Hq bytes per
+// token each way; 32 requests of 700 to 8192 tokens take 61 us with it).
 static __global__ void __launch_bounds__(kBlkWeightThreads) decode_block_weights_kernel(const __grid_constant__ BlkArgs a)
 {
     extern __shared__ int s_pref[];                 // [batch + 1], then float [Hq]

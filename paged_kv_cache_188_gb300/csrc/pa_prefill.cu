@@ -58,6 +58,12 @@ constexpr int kPfThreadsF8 = 384;       // e4m3 cache: + two warps widening K / 
 // MMA time as bf16), a key's scale multiplies its column of S, q's row scale
 // joins the softmax scale.  Only V is widened to bf16, by two warps, 64 rows
 // each, from a ring of its own in the space that K's bf16 tiles would take.
+// 16 prompts of up to 2048 tokens, some behind prefixes, 32 heads over 8, D = 128,
+// blocks of 16: 335 us (the products alone 120 us at the burst rate; 205 us over a
+// bf16 cache, 292 over an e4m3 cache with one scale per head; K widened as well, by
+// four warps, 402 to 337).  Timing variants put 31 us in splitting q, 26 in the key
+// scales and 39 in widening V.  Tried and not kept: the widening warps issue V's
+// copies themselves, 346; q split while the item before ends, 338.
 constexpr int kWarpCvtBlk = 10;         // warps 10, 11: V rows
 constexpr int kKeyScales = 4;           // tiles whose key scales are kept (softmax lags the K copies by two)
 constexpr int kWarpProducer = 8, kWarpMma = 9, kWarpCvtK = 10, kWarpCvtV = 11;
