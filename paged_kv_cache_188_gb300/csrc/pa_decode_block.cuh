@@ -938,7 +938,8 @@ constexpr int kBlkWeightThreads = 128;
 // weights[row, j] += sum over the heads of 2^(score - lse), one 128-token tile
 // of a request at a time, heads in order.  A kernel of its own, because a score's
 // sum is known only when its last piece is; scores pass through L2 (4 Hq bytes per
-// token each way; 32 requests of 700 to 8192 tokens take 61 us with it).
+// token each way; 32 requests of 700 to 8192 tokens take 55.7 us with it;
+// 4 blocks per SM instead of 8, 57.0, the scores loaded behind the sums, 61.3).
 static __global__ void __launch_bounds__(kBlkWeightThreads) decode_block_weights_kernel(const __grid_constant__ BlkArgs a)
 {
     extern __shared__ int s_pref[];                 // [batch + 1], then float [Hq]
@@ -959,6 +960,27 @@ static __global__ void __launch_bounds__(kBlkWeightThreads) decode_block_weights
             if (s_pref[mid] <= x) lo = mid; else hi = mid;
         }
         const int b = lo, n = blk_len(a, b), row = __ldg(a.req_pool_indices + b);
+        if (n <= 0) continue;
+        const int j = (x - s_pref[b]) * kBlkTile + tid;
+        const bool in = j < n && x < a.cap_tiles;
+        const float *sc = a.scores + ((int64_t)x * kBlkTile + tid) * G;
+        const int64_t head = (int64_t)a.cap_tiles * kBlkTile * G;
+        float *dst = a.weights + (int64_t)row * a.max_ctx + j;
+        // four scores a load where G allows it, the first eight loads and the
+        // old weight on their way while the sums arrive
+        const int quads = G % 4 == 0 ? a.Hq / 4 : 0;
+        auto load = [&](int q) {
+            const int h = q / (G / 4), g = (q - h * (G / 4)) * 4;
+            return __ldcg(reinterpret_cast<const float4 *>(sc + h * head + g));
+        };
+        float4 v[8];
+        float w = 0.f, old = 0.f;
+        if (in) {
+            old = __ldcg(dst);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (q < quads) v[q] = load(q);
+        }
         // two requests of a row would both add to it: the later one is refused
         // (after one without tokens, a batch's padding, it is not)
         int again = 0;
@@ -969,34 +991,28 @@ static __global__ void __launch_bounds__(kBlkWeightThreads) decode_block_weights
 #pragma unroll 1
         for (int hq = tid; hq < a.Hq; hq += kBlkWeightThreads) s_lse[hq] = __ldcg(a.lse + (int64_t)b * a.Hq + hq);
         again = __syncthreads_or(again);
-        if (n <= 0) continue;
         if (again || x >= a.cap_tiles) {
             if (tid == 0) set_error(a.err, again ? PA_DEVERR_ROW : PA_DEVERR_LEN);
             continue;
         }
-        const int j = (x - s_pref[b]) * kBlkTile + tid;
-        if (j < n) {
-            const float *sc = a.scores + ((int64_t)x * kBlkTile + tid) * G;
-            const int64_t head = (int64_t)a.cap_tiles * kBlkTile * G;
-            float w = 0.f;
-            if (G % 4 == 0) {
-                // four scores a load, eight loads on their way
-#pragma unroll 8
-                for (int q = 0; q < a.Hq / 4; ++q) {
-                    const int h = q / (G / 4), g = (q - h * (G / 4)) * 4;
-                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(sc + h * head + g));
-                    const float *l = s_lse + q * 4;
-                    w += blk_ex2(v.x - l[0]) + blk_ex2(v.y - l[1]) + (blk_ex2(v.z - l[2]) + blk_ex2(v.w - l[3]));
-                }
-            } else {
+        if (!in) continue;
+        auto add = [&](int q, float4 u) {
+            const float *l = s_lse + q * 4;
+            w += blk_ex2(u.x - l[0]) + blk_ex2(u.y - l[1]) + (blk_ex2(u.z - l[2]) + blk_ex2(u.w - l[3]));
+        };
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            if (q < quads) add(q, v[q]);
 #pragma unroll 4
-                for (int hq = 0; hq < a.Hq; ++hq) {
-                    const int h = hq / G;
-                    w += blk_ex2(__ldcg(sc + h * head + hq - h * G) - s_lse[hq]);
-                }
+        for (int q = 8; q < quads; ++q) add(q, load(q));
+        if (quads == 0) {
+#pragma unroll 4
+            for (int hq = 0; hq < a.Hq; ++hq) {
+                const int h = hq / G;
+                w += blk_ex2(__ldcg(sc + h * head + hq - h * G) - s_lse[hq]);
             }
-            a.weights[(int64_t)row * a.max_ctx + j] += w;
         }
+        *dst = old + w;
     }
 }
 
@@ -1023,7 +1039,7 @@ static pa_status launch_block(BlkArgs a, cudaStream_t st)
     if (WT && !ensure_dynamic_smem(reinterpret_cast<const void *>(decode_block_weights_kernel), wsmem)) return PA_ERR_CUDA;
     if (launch_kernel(kern, dim3(grid), dim3(kBlkThreads), smem, st, a) != cudaSuccess) return PA_ERR_CUDA;
     if constexpr (WT) {
-        if (launch_kernel(decode_block_weights_kernel, dim3(4 * grid), dim3(kBlkWeightThreads), wsmem, st, a) != cudaSuccess)
+        if (launch_kernel(decode_block_weights_kernel, dim3(8 * grid), dim3(kBlkWeightThreads), wsmem, st, a) != cudaSuccess)
             return PA_ERR_CUDA;
     }
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;

@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(256, 4) kv_store_block_kernel(const StoreBlock
                     *p = make_uint4(requant4(w.x, f), requant4(w.y, f), requant4(w.z, f), requant4(w.w, f));
                 }
             }
-            const float inv = __uint_as_float((uint32_t)(254 - e) << 23);
+            const float inv = __uint_as_float(e < 254 ? (uint32_t)(254 - e) << 23 : 1u << 22);   // 2^(127 - e)
             auto put = [&](int i, uint4 w0, uint4 w1, int slot) {
                 const uint2 lo = quant8(w0, inv), hi = quant8(w1, inv);
                 *reinterpret_cast<uint4 *>(buf + (int64_t)slot * row_elems) = make_uint4(lo.x, lo.y, hi.x, hi.y);

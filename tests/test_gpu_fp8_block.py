@@ -107,6 +107,22 @@ def test_reset_marks_listed_blocks_of_every_layer():
     assert api.pa_get_error_word(err) == api.DEVERR_SLOT
 
 
+@pytest.mark.parametrize("e", [253, 254])
+def test_store_at_the_largest_exponents(e):
+    """Rows stored into a block whose scale is 2^126 or 2^127 already."""
+    size, Hkv, D = 16, 1, 64
+    x = rows((4, Hkv, D), gen(e)) * 2.0 ** 126
+    k, v = (torch.zeros((1, size, Hkv, D), dtype=torch.uint8, device="cuda") for _ in range(2))
+    ke, ve = (torch.full((1, 1, Hkv), e, dtype=torch.uint8, device="cuda") for _ in range(2))
+    loc = [2, 3, 4, 9]
+    api.pa_kv_store_fp8_block(k, v, 0, x.cuda(), x.cuda(), torch.tensor(loc, dtype=torch.int32).cuda(), ke, ve, 16)
+    wk, we = np.zeros((size, Hkv, D), np.uint8), np.full((1, Hkv), e, np.uint8)
+    R.store(wk, we, x.double().numpy(), loc, 16)
+    assert wk.any() and ke.item() == e and ve.item() == e
+    same_bytes(k[0].cpu().numpy(), wk, "k")
+    same_bytes(v[0].cpu().numpy(), wk, "v")
+
+
 def test_store_and_reset_of_nothing():
     k = torch.ones((1, 16, 1, 64), dtype=torch.uint8, device="cuda")
     e = torch.ones((1, 1, 1), dtype=torch.uint8, device="cuda")
