@@ -356,19 +356,19 @@ pa_status pa_kv_reset_fp8_block(uint8_t *k_exp, uint8_t *v_exp, int n_layers, in
 
 /* pa_paged_decode_attn_fp8_block: what pa_paged_decode_attn computes, over this
  * cache.  Supported: head_dim 64 or 128, 1 <= G <= 16, at most 4096 query heads,
- * batch <= 4096.  QK^T and PV run on tcgen05 with the e4m3 rows as they are; q and the softmax weights
- * enter as sums of e4m3 terms (q within 2^-22 of its head's largest element,
- * weights to 12 bits), products and sums in fp32.  One kernel; a (request, kv
- * head) that several CTAs worked on is merged in a fixed order by the one that
- * finishes last (run-to-run bit-identical).  Workspace: at least
- * pa_decode_fp8_block_workspace_bytes, whatever the batch, initialised once
- * with pa_workspace_init (its merge tickets are zero between calls); calls that
- * share one are ordered on a stream.  It is no workspace of the other decode
- * calls unless initialised again in between.  A
- * request row out of range sets PA_DEVERR_ROW and gives zeros, a length outside
- * [0, max_ctx] is clamped and sets PA_DEVERR_LEN, a slot outside [0, size) is
- * masked and sets PA_DEVERR_SLOT; a request with nothing to attend to gives
- * zeros.  Under PA_OVERLAP_EARLY_KV it behaves as in early-metadata mode. */
+ * batch <= 4096.  QK^T and PV run on tcgen05 with the e4m3 rows as they are; q
+ * and the softmax weights enter as sums of e4m3 terms (q within 2^-22 of its
+ * head's largest element, weights to 12 bits), products and sums in fp32.  One
+ * kernel; a (request, kv head) that several CTAs worked on is merged in a fixed
+ * order by the one that finishes last (run-to-run bit-identical).  Workspace: at
+ * least pa_decode_fp8_block_workspace_bytes, whatever the batch, initialised
+ * once with pa_workspace_init (its merge tickets are zero between calls); calls
+ * that share one are ordered on a stream.  It is no workspace of the other
+ * decode calls unless initialised again in between.  A request row out of range
+ * sets PA_DEVERR_ROW and gives zeros, a length outside [0, max_ctx] is clamped
+ * and sets PA_DEVERR_LEN, a slot outside [0, size) is masked and sets
+ * PA_DEVERR_SLOT; a request with nothing to attend to gives zeros.  Under
+ * PA_OVERLAP_EARLY_KV it behaves as in early-metadata mode. */
 size_t pa_decode_fp8_block_workspace_bytes(int n_q_heads, int n_kv_heads, int head_dim);
 pa_status pa_paged_decode_attn_fp8_block(const void *q, int batch, int n_q_heads, const void *k_buf,
                                          const void *v_buf, pa_kv_shape s, int layer_id,
