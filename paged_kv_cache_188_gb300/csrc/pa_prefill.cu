@@ -649,15 +649,8 @@ __global__ void __launch_bounds__(F8 ? kPfThreadsF8 : kPfThreads, 1)
                         ok = false;
                         break;
                     }
-                    put_exps(ek, true);
-                    put_exps(ev, false);
                     ++nk;
                     ++nv;
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(bar(K_FULL + st), kPfKeys * D);
-                        mbar_arrive_expect_tx(bar(V_RAW + st), kPfKeys * D);
-                    }
-                    __syncwarp();
                     const uint32_t kd = sK + st * kPfKeys * D, vd = raw_tile(true, st);
                     // D-byte rows packed: a 16-row box per page group, one out
                     // of range (zeros) where a group has no row, else four
@@ -676,6 +669,15 @@ __global__ void __launch_bounds__(F8 ? kPfThreadsF8 : kPfThreads, 1)
                         tma_gather4(kd + lane * 4 * D, &p.tm_k1, col0, r0, r1, r2, r3, bar(K_FULL + st));
                         tma_gather4(vd + lane * 4 * D, &p.tm_v1, col0, r0, r1, r2, r3, bar(V_RAW + st));
                     }
+                    // the exponents, behind the copies: they may still be on
+                    // their way, and a barrier's arrival is yet to come
+                    put_exps(ek, true);
+                    put_exps(ev, false);
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(bar(K_FULL + st), kPfKeys * D);
+                        mbar_arrive_expect_tx(bar(V_RAW + st), kPfKeys * D);
+                    }
+                    __syncwarp();
                     continue;
                 }
                 if (doK) {
@@ -1065,9 +1067,7 @@ __global__ void __launch_bounds__(F8 ? kPfThreadsF8 : kPfThreads, 1)
                 // IEEE round-to-nearest op: the same values as scalar code)
                 const uint64_t nmb2 = f32x2_pack(-mb, -mb);
                 uint64_t sum2 = f32x2_pack(0.f, 0.f);   // even and odd columns' sums
-                // MASKED (BLK): hidden columns get weight 0 here; -inf times a
-                // group's multiplier would be NaN where that is 0
-                auto weights = [&](auto masked) {
+                {
                     uint64_t sl2x2 = f32x2_pack(sl2, sl2);
 #pragma unroll
                     for (int hh = 0; hh < 2; ++hh) {
@@ -1075,26 +1075,21 @@ __global__ void __launch_bounds__(F8 ? kPfThreadsF8 : kPfThreads, 1)
 #pragma unroll
                         for (int c = 0; c < 64; c += 2) {
                             if (BLK && c % 16 == 0) {
-                                const float sg = sl2 * gs[hh * 4 + c / 16];
+                                // (not 0: a hidden column's -inf stays -inf)
+                                const float sg = fmaxf(sl2 * gs[hh * 4 + c / 16], 1.17549435e-38f);
                                 sl2x2 = f32x2_pack(sg, sg);
                             }
                             const uint64_t x = fma_f32x2(f32x2_pack(__uint_as_float(r[hh * 64 + c]),
                                                                     __uint_as_float(r[hh * 64 + c + 1])),
                                                          sl2x2, nmb2);
-                            float v0 = ex2f(f32x2_lo(x)), v1 = ex2f(f32x2_hi(x));
-                            if (decltype(masked)::value) {
-                                v0 = hh * 64 + c > limit ? 0.f : v0;
-                                v1 = hh * 64 + c + 1 > limit ? 0.f : v1;
-                            }
+                            const float v0 = ex2f(f32x2_lo(x)), v1 = ex2f(f32x2_hi(x));
                             const uint64_t v2 = f32x2_pack(v0, v1);
                             sum2 = add_f32x2(sum2, v2);
                             pk[c / 2] = pack_bf16x2(v0, v1);
                         }
                         tmem_st32(s_addr + hh * 32, pk);
                     }
-                };
-                if (BLK && __any_sync(0xffffffffu, diag)) weights(Flag<true>{});
-                else weights(Flag<false>{});
+                }
                 l_run = l_run * alpha + (f32x2_lo(sum2) + f32x2_hi(sum2));
                 rescale_o(rescale, alpha);
                 tmem_wait_st();
