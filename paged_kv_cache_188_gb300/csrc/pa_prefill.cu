@@ -59,11 +59,14 @@ constexpr int kPfThreadsF8 = 384;       // e4m3 cache: + two warps widening K / 
 // joins the softmax scale.  Only V is widened to bf16, by two warps, 64 rows
 // each, from a ring of its own in the space that K's bf16 tiles would take.
 // 16 prompts of up to 2048 tokens, some behind prefixes, 32 heads over 8, D = 128,
-// blocks of 16: 335 us (the products alone 120 us at the burst rate; 205 us over a
+// blocks of 16: 323 us (the products alone 120 us at the burst rate; 205 us over a
 // bf16 cache, 292 over an e4m3 cache with one scale per head; K widened as well, by
-// four warps, 402 to 337).  Timing variants put 31 us in splitting q, 26 in the key
-// scales and 39 in widening V.  Tried and not kept: the widening warps issue V's
-// copies themselves, 346; q split while the item before ends, 338.
+// two or four warps, 402 or 337).  Timing variants put 33 us in widening V, 17 in
+// splitting q, 12 in the copies' warp's exponents, 10 in the key scales; leaving
+// out half of the products or all exponentials changes nothing: the softmax warps'
+// chain and what shares their schedulers is the bound.  Tried and not kept (at 335
+// us): the widening warps issue V's copies themselves, 346; q split while the item
+// before ends, 338; q split in f16 arithmetic, no difference.
 constexpr int kWarpCvtBlk = 10;         // warps 10, 11: V rows
 constexpr int kKeyScales = 4;           // tiles whose key scales are kept (softmax lags the K copies by two)
 constexpr int kWarpProducer = 8, kWarpMma = 9, kWarpCvtK = 10, kWarpCvtV = 11;
@@ -265,11 +268,6 @@ __device__ __forceinline__ float ex2f(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-
-template <bool V>
-struct Flag {
-    static constexpr bool value = V;
-};
 
 template <bool DENSE>
 __device__ __forceinline__ PfItem pf_item(const PrefillParams &p, const int *s_pref, int item)
@@ -1067,28 +1065,26 @@ __global__ void __launch_bounds__(F8 ? kPfThreadsF8 : kPfThreads, 1)
                 // IEEE round-to-nearest op: the same values as scalar code)
                 const uint64_t nmb2 = f32x2_pack(-mb, -mb);
                 uint64_t sum2 = f32x2_pack(0.f, 0.f);   // even and odd columns' sums
-                {
-                    uint64_t sl2x2 = f32x2_pack(sl2, sl2);
+                uint64_t sl2x2 = f32x2_pack(sl2, sl2);
 #pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {
-                        uint32_t pk[32];
+                for (int hh = 0; hh < 2; ++hh) {
+                    uint32_t pk[32];
 #pragma unroll
-                        for (int c = 0; c < 64; c += 2) {
-                            if (BLK && c % 16 == 0) {
-                                // (not 0: a hidden column's -inf stays -inf)
-                                const float sg = fmaxf(sl2 * gs[hh * 4 + c / 16], 1.17549435e-38f);
-                                sl2x2 = f32x2_pack(sg, sg);
-                            }
-                            const uint64_t x = fma_f32x2(f32x2_pack(__uint_as_float(r[hh * 64 + c]),
-                                                                    __uint_as_float(r[hh * 64 + c + 1])),
-                                                         sl2x2, nmb2);
-                            const float v0 = ex2f(f32x2_lo(x)), v1 = ex2f(f32x2_hi(x));
-                            const uint64_t v2 = f32x2_pack(v0, v1);
-                            sum2 = add_f32x2(sum2, v2);
-                            pk[c / 2] = pack_bf16x2(v0, v1);
+                    for (int c = 0; c < 64; c += 2) {
+                        if (BLK && c % 16 == 0) {
+                            // (not 0: a hidden column's -inf stays -inf)
+                            const float sg = fmaxf(sl2 * gs[hh * 4 + c / 16], 1.17549435e-38f);
+                            sl2x2 = f32x2_pack(sg, sg);
                         }
-                        tmem_st32(s_addr + hh * 32, pk);
+                        const uint64_t x = fma_f32x2(f32x2_pack(__uint_as_float(r[hh * 64 + c]),
+                                                                __uint_as_float(r[hh * 64 + c + 1])),
+                                                     sl2x2, nmb2);
+                        const float v0 = ex2f(f32x2_lo(x)), v1 = ex2f(f32x2_hi(x));
+                        const uint64_t v2 = f32x2_pack(v0, v1);
+                        sum2 = add_f32x2(sum2, v2);
+                        pk[c / 2] = pack_bf16x2(v0, v1);
                     }
+                    tmem_st32(s_addr + hh * 32, pk);
                 }
                 l_run = l_run * alpha + (f32x2_lo(sum2) + f32x2_hi(sum2));
                 rescale_o(rescale, alpha);

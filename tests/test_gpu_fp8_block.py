@@ -502,6 +502,25 @@ def test_prefill_bad_slots_read_as_zeros():
     R.check_out(out.cpu(), R.attention(q.double(), kk, vv, 0.05, first=260, terms=2.0 ** -19), 8, "bad slots")
 
 
+@pytest.mark.parametrize("exp,scale", [(0, 1e-20), (1, 1e-3), (1, 1e-30), (0, 0.0)])
+@pytest.mark.parametrize("block", [16, 1])
+def test_prefill_keys_of_the_smallest_scales(exp, scale, block):
+    """Empty blocks (zeros) and scales of 2^-126: scores of nothing, hidden columns of diagonal tiles stay hidden, and
+    each query sees the mean of its values."""
+    c = Cache([200], 2, 128, 16, block, 64, exp_lo=118, exp_hi=120).cuda()
+    c.ke[...] = exp
+    c.dev[4] = c.ke.cuda()
+    q = torch.randn((200, 8, 128), generator=c.g).to(torch.bfloat16)
+    k, v, table, rws, ke, ve = c.dev
+    out = torch.full_like(q, math.nan, device="cuda")
+    ws = api.alloc_workspace(api.pa_prefill_workspace_bytes())
+    api.pa_paged_prefill_attn_fp8_block(q.cuda(), k, v, 1, torch.tensor([0, 200], dtype=torch.int32).cuda(),
+                                        torch.tensor([0, 200], dtype=torch.int32).cuda(), table, rws, scale, ke, ve, block, ws, out)
+    assert api.pa_get_error(ws) == 0
+    kk, vv = c.values(0)
+    R.check_out(out.cpu(), R.attention(q.double(), kk, vv, scale, first=0, terms=2.0 ** -19), 8, f"exponent {exp}")
+
+
 def test_prefill_last_row_is_decode_within_rounding():
     """The same cache and queries through both paths."""
     c = Cache([700], 2, 128, 16, 16, 61).cuda()
