@@ -315,6 +315,68 @@ def test_padding_without_tokens_may_share_a_row():
 
 # ------------------------------------------------------------ a serving loop
 
+@pytest.mark.parametrize("D,block", [(128, 16), (64, 1), (64, 32)])
+def test_captured_chain_in_every_overlap_mode(D, block):
+    """Reset, a prompt stored and prefilled, a token appended, decode with weights and eviction, captured together on a
+    stream of its own: what the calls give one by one, whatever the overlap."""
+    g = gen(D + block)
+    Hkv, G, new, page = 2, 4, [150, 37, 1], 32
+    B, ctx, size, T = len(new), 200, 16 * page, sum(new)
+    perm = torch.randperm(size // page, generator=g)
+    table0, at = torch.zeros((B + 1, ctx), dtype=torch.int32), 0
+    for b, n in enumerate(new):
+        j = torch.arange(n + 1)
+        table0[b + 1, :n + 1] = (perm[at + j // page] * page + j % page).int()
+        at += n // page + 1
+    loc = torch.cat([table0[b + 1, :n] for b, n in enumerate(new)]).cuda()
+    last = torch.tensor([int(table0[b + 1, n]) for b, n in enumerate(new)], dtype=torch.int32).cuda()
+    rnd = lambda *shape: torch.randn(shape, generator=g).to(torch.bfloat16).cuda()  # noqa: E731
+    kp, vp, k1, v1 = rnd(T, Hkv, D), rnd(T, Hkv, D), rnd(B, Hkv, D) * 9, rnd(B, Hkv, D) * 9
+    qp, qd = rnd(T, Hkv * G, D), rnd(B, Hkv * G, D)
+    nb = -(-size // block)
+    k, v = (torch.zeros((1, size, Hkv, D), dtype=torch.uint8, device="cuda") for _ in range(2))
+    ke, ve = (torch.zeros((1, nb, Hkv), dtype=torch.uint8, device="cuda") for _ in range(2))
+    blocks, rws = torch.arange(nb, dtype=torch.int32, device="cuda"), i32(range(1, B + 1))
+    qo, lens = i32([0] + torch.tensor(new).cumsum(0).tolist()), i32([n + 1 for n in new])
+    table, src, w = table0.cuda(), table0.cuda(), torch.zeros((B + 1, ctx), device="cuda")
+    outp, outd, newl = torch.empty_like(qp), torch.empty_like(qd), i32([0] * B)
+    freed = torch.zeros((B, ctx), dtype=torch.int32, device="cuda")
+    ws1 = api.alloc_workspace(api.pa_prefill_workspace_bytes())
+    ws2 = api.alloc_workspace(api.pa_decode_weights_workspace_bytes(B, T + B, Hkv * G, Hkv, D))
+
+    def chain():
+        table.copy_(src)
+        w.zero_()
+        api.pa_kv_reset_fp8_block(ke, ve, blocks)
+        api.pa_kv_store_fp8_block(k, v, 0, kp, vp, loc, ke, ve, block)
+        api.pa_paged_prefill_attn_fp8_block(qp, k, v, 0, qo, qo, table, rws, 0.1, ke, ve, block, ws1, outp)
+        api.pa_kv_store_fp8_block(k, v, 0, k1, v1, last, ke, ve, block)
+        api.pa_paged_decode_attn_weights(qd, k, v, 0, table, rws, lens, 0.1, w, ws2, outd, k_exp=ke, v_exp=ve, block=block)
+        api.pa_kv_evict(table, rws, lens, w, 100, 10, newl, freed)
+
+    got = (outp, outd, w, table, newl, freed)
+    chain()
+    torch.cuda.synchronize()
+    want = [x.clone() for x in got]
+    assert newl.tolist() == [100, 38, 2] and torch.isfinite(outp.float()).all() and float(w[3, :2].sum()) > 7.99
+    try:
+        for mode in (api.OVERLAP_OFF, api.OVERLAP_SAFE, api.OVERLAP_EARLY_METADATA, api.OVERLAP_EARLY_KV):
+            api.pa_set_launch_overlap(mode)
+            gr = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(gr):
+                chain()
+            for _ in range(3):
+                for x in got:
+                    x.zero_()
+                gr.replay()
+                torch.cuda.synchronize()
+                for x, y in zip(got, want):
+                    assert torch.equal(x.view(torch.uint8), y.view(torch.uint8)), mode
+    finally:
+        api.pa_set_launch_overlap(api.OVERLAP_OFF)
+    assert api.pa_get_error(ws1) == 0 and api.pa_get_error(ws2) == 0
+
+
 @pytest.mark.parametrize("block", [0, 1])
 def test_serving_loop_with_eviction(block):
     """Three requests, token by token: store, decode with weights, evict when over budget, the freed slots used
