@@ -423,11 +423,11 @@ __device__ __forceinline__ void blk_loader(const BlkArgs &a, const int *s_pref, 
         }
         __syncwarp();
     }
-    if (*s_abort) {
-        // aborted: the copies already issued land before the shared memory goes away
+    // the warp leaves only when its copies have landed, whether or not anyone has
+    // given up by now: the other warpgroup may do so later, after which nobody
+    // waits for these, and the shared memory would go away under them
 #pragma unroll 1
-        for (int j = max(0, seq - stages); j < seq; ++j) mbar_drain(full + (j % stages) * 8, (j / stages) & 1);
-    }
+    for (int j = max(0, seq - stages); j < seq; ++j) mbar_drain(full + (j % stages) * 8, (j / stages) & 1);
     if (errs) set_error(a.err, errs);
     __syncwarp();
 }
