@@ -712,9 +712,11 @@ __global__ void __launch_bounds__(F8 ? kPfThreadsF8 : kPfThreads, 1)
                 }
             }
         }
-        if (*s_abort && lane == 0) {
-            // aborted: every copy this warp issued lands before the CTA's
-            // shared memory goes away (each barrier's last armed phase)
+        if (lane == 0) {
+            // the warp leaves only when its copies have landed (each barrier's
+            // last armed phase), whether or not anyone has given up by now:
+            // another role may do so later, after which nobody waits for
+            // these, and the shared memory would go away under them
             if (nq > 0) mbar_drain(bar(Q_FULL), (nq - 1) & 1);
             if (nqb > 0) mbar_drain(bar(QB_FULL), (nqb - 1) & 1);
             const int kb = F8 && !BLK ? K_RAW : K_FULL, vb = F8 ? V_RAW : V_FULL;
@@ -908,14 +910,13 @@ __global__ void __launch_bounds__(F8 ? kPfThreadsF8 : kPfThreads, 1)
             ++ia;
             if (hasB) ++ib;
         }
-        if (*s_abort) {
-            // aborted: one more commit, which arrives once every MMA this
-            // lane issued has completed, before tensor memory is freed
-            if (elect_one()) umma_commit(bar(DRAIN));
-            __syncwarp();
-            mbar_drain(bar(DRAIN), 0);
-            __syncwarp();
-        }
+        // one more commit, which arrives once every MMA this lane issued has
+        // completed, before tensor memory is freed (a softmax warp may give up
+        // on the last ones after this warp is through)
+        if (elect_one()) umma_commit(bar(DRAIN));
+        __syncwarp();
+        mbar_drain(bar(DRAIN), 0);
+        __syncwarp();
     } else {
         // ======================= softmax + epilogue: warpgroup X owns tile X
         const int X = warp >> 2;                  // 0: tile A, 1: tile B

@@ -5,10 +5,12 @@ same SMs right behind it is right: nothing of the aborted call lands in its
 shared memory."""
 import math
 
+import numpy as np
 import pytest
 import torch
 
 from paged_kv_cache_188_gb300 import api
+from paged_kv_cache_188_gb300 import workloads as W
 from test_gpu_fp8_block import Cache, decode
 
 pytestmark = pytest.mark.gpu
@@ -67,3 +69,43 @@ def test_block_decode(D, page, block):
     want, _ = decode(c, q, 0.05)
     need = api.pa_decode_fp8_block_workspace_bytes(16, 4, D)
     _drive(lambda ws, out: decode(c, q, 0.05, ws=ws, out=out), want, lambda: api.alloc_workspace(need))
+
+
+@pytest.mark.parametrize("kind", ["block", "e4m3", "bf16"])
+@pytest.mark.parametrize("D", [128, 64])
+def test_prefill(kind, D):
+    new, pre = [300, 77, 700, 5], [500, 0, 64, 3]
+    need = api.pa_prefill_workspace_bytes()
+    if kind == "block":
+        c = Cache([a + b for a, b in zip(new, pre)], 2, D, 16, 16, 52).cuda()
+        q = torch.randn((sum(new), 8, D), generator=c.g).to(torch.bfloat16).cuda()
+        qo = torch.tensor(np.cumsum([0] + new), dtype=torch.int32).cuda()
+        kv = torch.tensor(np.cumsum([0] + c.lens), dtype=torch.int32).cuda()
+        k, v, table, rws, ke, ve = c.dev
+
+        def call(ws, out):
+            api.pa_paged_prefill_attn_fp8_block(q, k, v, c.layer, qo, kv, table, rws, 0.05, ke, ve, 16, ws, out)
+    else:
+        pb = W.make_prefill_batch(new_lens=new, prefix_lens=pre, n_q_heads=8, n_kv_heads=2, head_dim=D, size=2048,
+                                  page_size=16, seed=53, device="cuda")
+        q = pb.q
+        args = (pb.qo_indptr, pb.kv_indptr, pb.kv.req_to_token, pb.kv.req_pool_indices, pb.scale)
+        if kind == "bf16":
+            api.pa_kv_store(pb.kv.k_buf, pb.kv.v_buf, pb.layer, pb.k_new, pb.v_new, pb.loc)
+
+            def call(ws, out):
+                api.pa_paged_prefill_attn(q, pb.kv.k_buf, pb.kv.v_buf, pb.layer, *args, ws, out)
+        else:
+            n_layers, size, Hkv, _ = pb.kv.k_buf.shape
+            ks = torch.full((n_layers, Hkv), 4.5 / 448, dtype=torch.float32, device="cuda")
+            k8 = torch.zeros((n_layers, size, Hkv, D), dtype=torch.uint8, device="cuda")
+            v8 = torch.zeros_like(k8)
+            every = torch.arange(size, dtype=torch.int32, device="cuda")
+            api.pa_kv_store_fp8(k8, v8, pb.layer, pb.kv.k_buf[pb.layer], pb.kv.v_buf[pb.layer], every, ks, ks)
+            api.pa_kv_store_fp8(k8, v8, pb.layer, pb.k_new, pb.v_new, pb.loc, ks, ks)
+
+            def call(ws, out):
+                api.pa_paged_prefill_attn_fp8(q, k8, v8, pb.layer, *args, ks, ks, ws, out)
+    want = torch.empty_like(q)
+    call(api.alloc_workspace(need), want)
+    _drive(call, want, lambda: api.alloc_workspace(need))
