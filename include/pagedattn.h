@@ -408,7 +408,9 @@ pa_status pa_paged_prefill_attn_fp8_block(const void *q, int n_tokens, int n_q_h
  * PA_DEVERR_ROW and adds nothing (its output is right).  Workspace:
  * pa_decode_weights_workspace_bytes for at most max_batch requests of
  * max_tokens cached tokens in all; a call with more sets PA_DEVERR_LEN and adds
- * nothing for the requests' tiles past that (outputs are right).  Else as
+ * nothing for the requests' tiles past that (outputs are right).  A call that
+ * gives up (PA_DEVERR_TIMEOUT) adds nothing at all, and neither does a later one
+ * on its workspace until that is initialised again.  Else as
  * pa_paged_decode_attn_fp8_block (bf16: the weights enter PV as two bf16 terms). */
 size_t pa_decode_weights_workspace_bytes(int max_batch, int64_t max_tokens, int n_q_heads, int n_kv_heads,
                                          int head_dim);

@@ -12,6 +12,7 @@ import torch
 from paged_kv_cache_188_gb300 import api
 from paged_kv_cache_188_gb300 import workloads as W
 from test_gpu_fp8_block import Cache, decode
+from test_gpu_weights_evict import Bf16Cache, weights_call
 
 pytestmark = pytest.mark.gpu
 LIMITS_NS = [0, 1, 300, 1000, 2000, 3000, 5000, 8000, 12000, 20000]
@@ -109,3 +110,42 @@ def test_prefill(kind, D):
     want = torch.empty_like(q)
     call(api.alloc_workspace(need), want)
     _drive(call, want, lambda: api.alloc_workspace(need))
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+def test_weights_table_of_an_aborted_call(bf16):
+    """A call that gave up adds nothing to the table, and neither does one on its workspace before that is initialised
+    again; then the same call is right."""
+    lens = [3000, 40, 777, 0, 1500]
+    c = (Bf16Cache(lens, 2, 128, 16, 54) if bf16 else Cache(lens, 2, 128, 16, 16, 54)).cuda()
+    q = torch.randn((len(lens), 8, 128), generator=c.g).to(torch.bfloat16).cuda()
+    w0 = torch.rand(c.table.shape, generator=c.g).cuda()
+    w1 = w0.clone()
+    want, _ = weights_call(c, q, 0.05, w1)
+    assert not torch.equal(w1, w0)
+    need = api.pa_decode_weights_workspace_bytes(len(lens), sum(lens), 8, 2, 128)
+    gave_up = 0
+    for limit in LIMITS_NS:
+        ws, w, out = api.alloc_workspace(need), w0.clone(), torch.full_like(want, math.nan)
+        torch.cuda.synchronize()
+        try:
+            api.pa_set_wait_timeout_ns(limit)
+            weights_call(c, q, 0.05, w, ws=ws, out=out)
+        finally:
+            api.pa_set_wait_timeout_ns(api.WAIT_TIMEOUT_DEFAULT_NS)
+        torch.cuda.synchronize()
+        err = api.pa_get_error(ws)
+        assert err in (0, api.DEVERR_TIMEOUT) and (limit > 0 or err)
+        if err:
+            gave_up += 1
+            assert torch.equal(w, w0), f"limit {limit} ns: the table changed"
+            # entries of the score and log-sum-exp areas are the aborted call's, whatever they are
+            weights_call(c, q, 0.05, w, ws=ws, out=out)
+            torch.cuda.synchronize()
+            assert torch.equal(w, w0) and api.pa_get_error(ws) == api.DEVERR_TIMEOUT
+            api.pa_workspace_init(ws)
+            weights_call(c, q, 0.05, w, ws=ws, out=out)
+            torch.cuda.synchronize()
+            assert api.pa_get_error(ws) == 0
+        assert torch.equal(w, w1) and torch.equal(bits(out), bits(want)), f"limit {limit} ns"
+    assert gave_up > 0
