@@ -768,7 +768,8 @@ __global__ void __launch_bounds__(kBlkThreads, 1) decode_block_kernel(const __gr
                     const float mz = mn == -INFINITY ? 0.f : mn, rz = rn == -INFINITY ? 0.f : rn;
                     const float rtz = rt == -INFINITY ? 0.f : rt;
                     l[g] = l[g] * blk_ex2(m[g] - mz) + blk_ex2(x[g] - mz);
-                    pp[g] = blk_ex2(x[g] + (float)ev - rtz + kShift);
+                    // (an empty block's values, ev = 0, are 0, not 2^-127: its tokens weigh in l alone)
+                    pp[g] = E8 && ev == 0 ? 0.f : blk_ex2(x[g] + (float)ev - rtz + kShift);
                     at[g] = blk_ex2(r[g] - rz);
                     bt[g] = rt == -INFINITY ? 0.f : blk_ex2(rt - rz);
                     m[g] = mn;
@@ -872,9 +873,12 @@ __global__ void __launch_bounds__(kBlkThreads, 1) decode_block_kernel(const __gr
             for (int g = 0; g < a.G && !bad; ++g) {
                 const float L = s_sum[g] + s_sum[GP + g] + s_sum[2 * GP + g] + s_sum[3 * GP + g];
                 const float mg = smr[g], rg = smr[GP + g];
-                // O relative to m: 2^(r - 127 - 8 - m)
+                // O relative to m: 2^(r - 127 - 8 - m), in two factors where one would be flushed to 0 (r - m is the
+                // exponent byte of the largest weight's value or more: down to 2^-134)
                 const float mz = mg == -INFINITY ? 0.f : mg, rz = rg == -INFINITY ? 0.f : rg;
-                const float O = E8 ? so[g * 128 + t] * blk_ex2(rz - mz - 135.f) : so[g * 128 + t];
+                const float d = rz - mz - 135.f;
+                const float O = E8 ? so[g * 128 + t] * (d < -64.f ? 0x1p-64f : 1.f) * blk_ex2(d < -64.f ? d + 64.f : d)
+                                   : so[g * 128 + t];
                 if (whole) {
                     const int64_t hq = (int64_t)k.b * a.Hq + k.h * a.G + g;
                     if (t < D) a.out[hq * D + t] = __float2bfloat16_rn(L != 0.f ? O / L : 0.f);
