@@ -81,7 +81,7 @@ inline bool fill_block(BlkArgs &a, const void *q, int batch, int Hq, const void 
     a.req_pool_indices = req_pool_indices;
     a.seq_lens = seq_lens;
     if (e4m3) {
-        const int64_t layer_exps = (int64_t)layer_id * (((int64_t)s.size + block - 1) / block) * s.n_kv_heads;
+        const int64_t layer_exps = block_layer_offset(layer_id, s.size, s.n_kv_heads, block);
         a.k_exp = k_exp + layer_exps;
         a.v_exp = v_exp + layer_exps;
         while ((1 << a.block_shift) < block) ++a.block_shift;

@@ -24,6 +24,12 @@ inline bool aligned256(const void *p) { return (reinterpret_cast<uintptr_t>(p) &
 
 // block sizes of a block-scaled cache: powers of two from 1 to 128
 inline bool block_ok(int block) { return block >= 1 && block <= 128 && (block & (block - 1)) == 0; }
+// exponent bytes in front of layer `layer_id`: [n_layers, ceil(size / block), n_kv_heads], 64-bit throughout (a layer
+// may have nearly 2^31 slots)
+constexpr int64_t block_layer_offset(int layer_id, int size, int n_kv_heads, int block)
+{
+    return (int64_t)layer_id * (((int64_t)size + block - 1) / block) * n_kv_heads;
+}
 
 // SM count of the current device (cached per device; a property, not call state).
 int num_sms();

@@ -1389,7 +1389,7 @@ extern "C" pa_status pa_paged_prefill_attn_fp8_block(const void *q, int n_tokens
                                nullptr);
     if (rc != PA_OK || n_tokens == 0 || n_reqs == 0) return rc;
     if (!k_exp || !v_exp) return PA_ERR_NULL;
-    const int64_t off = (int64_t)layer_id * ((s.size + block - 1) / block) * s.n_kv_heads;   // the layer's exponents
+    const int64_t off = block_layer_offset(layer_id, s.size, s.n_kv_heads, block);   // the layer's exponents
     return prefill_call(q, n_tokens, n_q_heads, k_buf, v_buf, s.n_kv_heads, s.head_dim, (int64_t)s.n_layers * s.size,
                         layer_id * s.size, s.size, qo_indptr, kv_indptr, n_reqs, req_to_token, req_rows, max_ctx,
                         req_pool_indices, scale, workspace, workspace_bytes, out, nullptr, false, st, nullptr, nullptr,

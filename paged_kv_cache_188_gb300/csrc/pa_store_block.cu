@@ -254,7 +254,7 @@ extern "C" pa_status pa_kv_store_fp8_block(void *k_buf, void *v_buf, pa_kv_shape
         return PA_ERR_ALIGN;
     StoreBlockArgs a{};
     const int64_t rows = (int64_t)layer_id * s.size * s.n_kv_heads * s.head_dim;
-    const int64_t exps = (int64_t)layer_id * (((int64_t)s.size + block - 1) / block) * s.n_kv_heads;
+    const int64_t exps = block_layer_offset(layer_id, s.size, s.n_kv_heads, block);
     a.k_buf = static_cast<uint8_t *>(k_buf) + rows;
     a.v_buf = static_cast<uint8_t *>(v_buf) + rows;
     a.k_new = static_cast<const __nv_bfloat16 *>(k_new);
