@@ -119,6 +119,7 @@ struct PfLayout {
     static constexpr int kOffPref = kOffGrouped + (BLK ? kKeyScales * 4 : 0);
     // tensor-memory columns: S_A | S_B | O_A | O_B
     static constexpr uint32_t kColOA = 256, kColOB = 256 + D;
+    static_assert(kColOB + D <= kTmemCols, "S and O of both tiles fit the tensor memory");
     static constexpr uint32_t kIdescPV = idesc_bf16_f32(128, D, 0, 1);  // P (tensor memory) x V (MN-major)
 };
 
@@ -1100,23 +1101,17 @@ __global__ void __launch_bounds__(F8 ? kPfThreadsF8 : kPfThreads, 1)
             tc_fence_after();
             // fp8: the head's V scale multiplies the normalised output
             const float inv_l = l_run > 0.f ? (F8 && !BLK ? __ldg(p.v_scale + I.h) : 1.f) / l_run : 0.f;
-            constexpr int OC = D;
-            uint32_t ob[OC / 2];                  // O / l as bf16 pairs
-            auto load_o = [&](int c0) {
-                uint32_t o[OC];
+            uint32_t o[D];
 #pragma unroll
-                for (int ch = 0; ch < OC / 32; ++ch)
-                    tmem_ld32(o_addr + c0 + ch * 32, *reinterpret_cast<uint32_t(*)[32]>(&o[ch * 32]));
-                tmem_wait_ld();
-                if (c0 + OC == D) {
-                    tc_fence_before();
-                    mbar_arrive(bar(b_o_empty));  // O_X is in registers: the next item may overwrite it
-                }
+            for (int ch = 0; ch < D / 32; ++ch)
+                tmem_ld32(o_addr + ch * 32, *reinterpret_cast<uint32_t(*)[32]>(&o[ch * 32]));
+            tmem_wait_ld();
+            tc_fence_before();
+            mbar_arrive(bar(b_o_empty));          // O_X is in registers: the next item may overwrite it
+            uint32_t ob[D / 2];                   // O / l as bf16 pairs
 #pragma unroll
-                for (int c = 0; c < OC / 2; ++c)
-                    ob[c] = pack_bf16x2(__uint_as_float(o[2 * c]) * inv_l, __uint_as_float(o[2 * c + 1]) * inv_l);
-            };
-            if constexpr (!BLK) load_o(0);
+            for (int c = 0; c < D / 2; ++c)
+                ob[c] = pack_bf16x2(__uint_as_float(o[2 * c]) * inv_l, __uint_as_float(o[2 * c + 1]) * inv_l);
             // 32 columns at a time through this warp's staging buffer (row
             // lane, 16-byte chunks XOR-swizzled by row so neither side
             // conflicts), then out with four lanes on 64 contiguous bytes
@@ -1124,10 +1119,9 @@ __global__ void __launch_bounds__(F8 ? kPfThreadsF8 : kPfThreads, 1)
             const int rr0 = lane >> 2, cc = lane & 3;
 #pragma unroll
             for (int ch = 0; ch < D / 32; ++ch) {
-                if constexpr (BLK) load_o(ch * 32);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    const uint32_t *v = &ob[(BLK ? 0 : ch * 16) + c * 4];
+                    const uint32_t *v = &ob[ch * 16 + c * 4];
                     st_shared_v4(stg + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4), v[0], v[1], v[2], v[3]);
                 }
                 __syncwarp();
