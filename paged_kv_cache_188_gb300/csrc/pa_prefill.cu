@@ -550,8 +550,11 @@ __global__ void __launch_bounds__(F8 ? kPfThreadsF8 : kPfThreads, 1)
                 const unsigned contig = __ballot_sync(0xffffffffu, mine);
                 const unsigned anyok = __ballot_sync(0xffffffffu, okp[0] || okp[1] || okp[2] || okp[3]);
                 // (BLK) a valid row of the tile, slot 0 if it has none
-                const int mine_slot = okp[0] ? slot[0] : okp[1] ? slot[1] : okp[2] ? slot[2] : okp[3] ? slot[3] : 0;
-                const int some = __shfl_sync(0xffffffffu, mine_slot, anyok ? __ffs(anyok) - 1 : 0);
+                int some = 0;
+                if constexpr (BLK) {
+                    const int mine_slot = okp[0] ? slot[0] : okp[1] ? slot[1] : okp[2] ? slot[2] : okp[3] ? slot[3] : 0;
+                    some = __shfl_sync(0xffffffffu, mine_slot, anyok ? __ffs(anyok) - 1 : 0);
+                }
                 const bool g_contig = ((contig >> (lane & ~3)) & 0xFu) == 0xFu;
                 const bool g_empty = ((anyok >> (lane & ~3)) & 0xFu) == 0u;
 
@@ -842,10 +845,14 @@ __global__ void __launch_bounds__(F8 ? kPfThreadsF8 : kPfThreads, 1)
             const bool hasB = I.nqb > 0;
             // S_A(0), S_B(0)
             {
-                const uint32_t b2[3] = {bar(BLK ? QA_READY : Q_FULL), bar(K_FULL + (kt & 1)),
-                                        bar(BLK && hasB ? QB_READY : K_FULL + (kt & 1))};
-                const uint32_t p2[3] = {(uint32_t)ia & 1u, (uint32_t)(kt >> 1) & 1u,
-                                        (uint32_t)(BLK && hasB ? ib : kt >> 1) & 1u};
+                // (BLK: the q tiles apart, as each is split by its own warpgroup)
+                constexpr int NB = BLK ? 3 : 2;
+                uint32_t b2[NB] = {bar(BLK ? QA_READY : Q_FULL), bar(K_FULL + (kt & 1))};
+                uint32_t p2[NB] = {(uint32_t)ia & 1u, (uint32_t)(kt >> 1) & 1u};
+                if constexpr (BLK) {
+                    b2[2] = bar(hasB ? QB_READY : K_FULL + (kt & 1));
+                    p2[2] = (uint32_t)(hasB ? ib : kt >> 1) & 1u;
+                }
                 if (!waitn(b2, p2)) break;
             }
             tc_fence_after();
@@ -1099,8 +1106,6 @@ __global__ void __launch_bounds__(F8 ? kPfThreadsF8 : kPfThreads, 1)
             if (!__all_sync(0xffffffffu, mbar_wait(bar(b_o_final), ix & 1, s_abort, err, PA_DEVERR_TIMEOUT, p.wait_ns)))
                 break;
             tc_fence_after();
-            // fp8: the head's V scale multiplies the normalised output
-            const float inv_l = l_run > 0.f ? (F8 && !BLK ? __ldg(p.v_scale + I.h) : 1.f) / l_run : 0.f;
             uint32_t o[D];
 #pragma unroll
             for (int ch = 0; ch < D / 32; ++ch)
@@ -1108,6 +1113,8 @@ __global__ void __launch_bounds__(F8 ? kPfThreadsF8 : kPfThreads, 1)
             tmem_wait_ld();
             tc_fence_before();
             mbar_arrive(bar(b_o_empty));          // O_X is in registers: the next item may overwrite it
+            // fp8: the head's V scale multiplies the normalised output
+            const float inv_l = l_run > 0.f ? (F8 && !BLK ? __ldg(p.v_scale + I.h) : 1.f) / l_run : 0.f;
             uint32_t ob[D / 2];                   // O / l as bf16 pairs
 #pragma unroll
             for (int c = 0; c < D / 2; ++c)
