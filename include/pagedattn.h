@@ -326,13 +326,16 @@ pa_status pa_paged_prefill_attn_fp8(const void *q, int n_tokens, int n_q_heads, 
  * [n_layers, size, n_kv_heads, head_dim] as above; exponents k_exp, v_exp uint8
  * [n_layers, ceil(size / block), n_kv_heads], one byte e each; an element is
  *     e4m3_value(byte) * 2^(e - 127)        (e = 0: 0, a block nothing was stored in)
- * block is a power of two from 1 (a scale per token) to 128.  head_dim 64 or
- * 128.  Zeroed buffers and exponents are an empty cache.
+ * and a NaN code is a NaN whatever e is.  block is a power of two from 1 (a scale
+ * per token) to 128.  head_dim 64 or 128.  Zeroed buffers and exponents are an empty
+ * cache.  Attention keeps its sums in fp32 before they meet q's scale and the sum of
+ * the weights: keys of magnitude 2^111 and more, or values of 2^128 / seq_len and
+ * more, may overflow on the way.
  *
  * pa_kv_store_fp8_block: the new tokens' K/V at slots loc[t].  For the rows x
  * of the call that fall into a block, and one kv head,
  *     e    = max(e_old, the smallest e in [1, 254] with amax |x| <= 448 * 2^(e - 127),
- *            0 where every x is 0)
+ *            0 where every finite x is 0)
  *     byte = e4m3(x * 2^(127 - e))     (nearest even; finite overflow and
  *            infinities saturate to +-448, a NaN stays NaN; amax over finite x)
  * and where e > e_old > 0 the block's other rows are rounded to the new scale:
@@ -381,8 +384,10 @@ pa_status pa_paged_decode_attn_fp8_block(const void *q, int batch, int n_q_heads
  * same arguments, workspace, limits and error reporting plus the exponents.
  * Q K^T runs on the e4m3 rows as they are, q as a sum of two e4m3 terms (within
  * 2^-19 of the row's largest element) and each key's scale on its scores; V is
- * widened to bf16 with its scale (exact) and the weights are rounded to bf16, as
- * in pa_paged_prefill_attn.  A query row that holds a NaN or an infinity gives
+ * widened to bf16 with its scale (exact down to bf16's subnormal step, 2^-133) and
+ * the weights are rounded to bf16, as in pa_paged_prefill_attn.  (Keys of an empty
+ * block count as their codes times 2^-126, which only queries beyond 1e27 can tell
+ * from 0.)  A query row that holds a NaN or an infinity gives
  * NaN. */
 pa_status pa_paged_prefill_attn_fp8_block(const void *q, int n_tokens, int n_q_heads, const void *k_buf,
                                           const void *v_buf, pa_kv_shape s, int layer_id, const int32_t *qo_indptr,
@@ -433,8 +438,10 @@ pa_status pa_paged_decode_attn_weights(const void *q, int batch, int n_q_heads, 
  * `budget` tokens keeps its row and weights and new_lens[b] = n.  Keys stay as
  * they were rotated: positions given to later tokens go on counting from the
  * original length.  K/V rows are not moved; with a block-scaled cache, hand
- * slots out again only when all slots of their block are free.  new_lens may be
- * seq_lens.  A row out of range, or one that an earlier request has too (both
+ * slots out again only when all slots of their block are free.  (Tokens kept by
+ * weight are spread over the blocks, so on blocks larger than one few blocks
+ * come free: the budget then bounds what decode reads, hardly what the cache
+ * holds.)  new_lens may be seq_lens.  A row out of range, or one that an earlier request has too (both
  * of at least one token), sets PA_DEVERR_ROW, a length outside [0, max_ctx] PA_DEVERR_LEN; such a
  * request is left as it is (new_lens[b] is its length, clamped).  The table and
  * the lengths are index inputs of later calls: in the early-metadata modes the

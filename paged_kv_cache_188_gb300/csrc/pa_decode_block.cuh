@@ -54,8 +54,8 @@
 //
 // Bound, and what was measured (e4m3, D = 128, 32 heads over 8, blocks and pages of
 // 16; in a graph): HBM, 2 D + 2 / block bytes per token and head: those 48 requests
-// 56.4 us, 5.2 TB/s (the floor is 42.9 us); one request of 32768 tokens 24.9 us
-// (9.9); of 1000 tokens 9.8 us (0.3): launch and plan, the first tile's chain of
+// 56.4 to 57.7 us from one GPU to another, 5.1 TB/s (the floor is 42.9 us); one of
+// 32768 tokens 24.9 to 25.7 (9.9); of 1000 tokens 9.7 to 10.1 (0.3): launch and plan, the first tile's chain of
 // table, exponents, rows, the products' chain, then tickets and merge, each one or
 // two round trips; its instructions are cold as well (a quarter of the issue slots
 // lost wait for them).  Two tiles a warpgroup are too few to hide a tile's chain of
@@ -942,8 +942,10 @@ constexpr int kBlkWeightThreads = 128;
 // weights[row, j] += sum over the heads of 2^(score - lse), one 128-token tile
 // of a request at a time, heads in order.  A kernel of its own, because a score's
 // sum is known only when its last piece is; scores pass through L2 (4 Hq bytes per
-// token each way; 32 requests of 700 to 8192 tokens take 55.7 us with it;
-// 4 blocks per SM instead of 8, 57.0, the scores loaded behind the sums, 61.3).
+// token each way).  32 requests of 700 to 8192 tokens take 57.2 us with it, this
+// kernel about 7 of them; at 64 registers eight blocks fit an SM.  (In one session at
+// 55.7 us: 4 blocks per SM 57.0, the scores loaded behind the sums 61.3.  The look at
+// the error word costs 0.5 us.)
 static __global__ void __launch_bounds__(kBlkWeightThreads) decode_block_weights_kernel(const __grid_constant__ BlkArgs a)
 {
     extern __shared__ int s_pref[];                 // [batch + 1], then float [Hq]

@@ -19,8 +19,8 @@
 // chunk's tokens are all read before any is written (one cluster barrier) and
 // later chunks are never overwritten.
 // Bound: latency (a handful of cluster barriers); 8 n bytes read, 8 per kept
-// token and 8 per evicted one written.  32768 tokens to 8192: 9.9 us (the bytes
-// alone 0.1); 64 requests of up to 16000 tokens to 2000: 12.5 us (0.5).
+// token and 8 per evicted one written.  32768 tokens to 8192: 10.1 us (the bytes
+// alone 0.1); 64 requests of up to 16000 tokens to 2000: 12.6 us (0.5).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -43,7 +43,7 @@ struct EvictArgs {
     float *weights;
     const int32_t *req_pool_indices, *seq_lens;
     int32_t *new_lens, *freed, *err;
-    int req_rows, max_ctx, budget, recent, early_meta;
+    int req_rows, max_ctx, budget, recent;
 };
 
 // weights as unsigned integers in the same order; -0 = +0, NaN = -infinity

@@ -59,12 +59,13 @@ constexpr int kPfThreadsF8 = 384;       // e4m3 cache: + two warps widening K / 
 // joins the softmax scale.  Only V is widened to bf16, by two warps, 64 rows
 // each, from a ring of its own in the space that K's bf16 tiles would take.
 // 16 prompts of up to 2048 tokens, some behind prefixes, 32 heads over 8, D = 128,
-// blocks of 16: 323 us (the products alone 120 us at the burst rate; 205 us over a
+// blocks of 16: 327 us (the products alone 120 us at the burst rate; 205 us over a
 // bf16 cache, 292 over an e4m3 cache with one scale per head; K widened as well, by
-// two or four warps, 402 or 337).  Timing variants put 33 us in widening V, 17 in
-// splitting q, 12 in the copies' warp's exponents, 10 in the key scales; leaving
-// out half of the products or all exponentials changes nothing: the softmax warps'
-// chain and what shares their schedulers is the bound.  Tried and not kept (at 335
+// two or four warps, 402 or 337).  Timing variants (at 335 us) put 33 us in widening
+// V, which every pair of query tiles that reads a key does again, 17 in splitting q,
+// 12 in the copies' warp's exponents, 10 in the key scales; without all four, 260.
+// What lies between that and the bf16 cache's 205 is not explained: leaving out half
+// of the products or all exponentials changes nothing.  Tried and not kept (at 335
 // us): the widening warps issue V's copies themselves, 346; q split while the item
 // before ends, 338; q split in f16 arithmetic, no difference.
 constexpr int kWarpCvtBlk = 10;         // warps 10, 11: V rows
@@ -166,7 +167,8 @@ static_assert(PfLayout<128>::kOffRing + kRing * (int)sizeof(PfItem) <= PfLayout<
 // row, each widening one 16-byte chunk into two; every row's bytes are read
 // (and the warp synchronised) before any of its bf16 chunks is written, so
 // the in-place D = 128 layout is safe.  Exact: e4m3 values are bf16 numbers,
-// and so are their products with a block-scaled row's power of two (BLK:
+// and so are their products with a block-scaled row's power of two, down to
+// bf16's subnormal step of 2^-133 (at e = 1 and 2 an e4m3 subnormal is finer) (BLK:
 // exps[r] is row r's exponent byte e, and e << 7 the bf16 number 2^(e - 127);
 // 255 marks a position without a row, which becomes zeros).
 template <int D, bool BLK = false>

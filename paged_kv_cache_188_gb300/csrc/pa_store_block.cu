@@ -18,8 +18,11 @@
 // a row, 16 values each.  Blocks of at least as many rows as a warp holds at once
 // (32 / (D/16)) take a warp per run; smaller ones a row's lanes per run.
 // Bound: HBM, 2 D bytes read and D written per row and head: 8000 prompt tokens
-// into fresh pages, 8 heads of 128, blocks of 16, take 16.9 us with the reset
-// before it (the bytes alone 7.2 us); 64 appends into partly filled blocks 2.7 us.
+// into fresh pages, 8 heads of 128, blocks of 16, take 13.8 us with the reset
+// before it (the bytes alone 7.2 us); 64 appends into partly filled blocks 2.2 us.
+// Larger blocks are latency: one warp does a whole run, and finds the end of one of
+// more than 32 rows a row at a time: the 8000 tokens take 14.1 us in blocks of 32,
+// 22.7 of 64 and 41.2 of 128 (24.1 us in blocks of 1: an exponent per row and head).
 #include <cuda_runtime.h>
 
 #include "pa_common.cuh"
@@ -33,7 +36,7 @@ struct StoreBlockArgs {
     const int32_t *loc;
     uint8_t *k_exp, *v_exp;            // the layer's [n_blocks, Hkv]
     int32_t *err;
-    int n_tokens, size, Hkv, block, shift, chunk, early_meta;
+    int n_tokens, size, Hkv, block, shift, chunk;
     int64_t units;                     // (chunk of tokens, head, K or V)
 };
 
@@ -84,11 +87,10 @@ __global__ void __launch_bounds__(256, 4) kv_store_block_kernel(const StoreBlock
 {
     constexpr int LPR = D / 16, RPP = GW / LPR;     // lanes per row, rows per pass
     constexpr int KEEP = 16 / RPP < 2 ? 16 / RPP : 2;   // passes whose rows stay in registers
-    if (!a.early_meta) pdl_wait();
     const int lane = threadIdx.x & 31, gl = lane % GW;
     const unsigned mask = GW == 32 ? 0xffffffffu : ((1u << GW) - 1u) << (lane - gl);
     const int rr = gl / LPR, c = gl % LPR;
-    if (a.early_meta) pdl_wait();
+    pdl_wait();
     pdl_launch_dependents();
     const int64_t row_elems = (int64_t)a.Hkv * D;
     for (int64_t u = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / GW; u < a.units;
@@ -123,7 +125,9 @@ __global__ void __launch_bounds__(256, 4) kv_store_block_kernel(const StoreBlock
             len = min(len, a.block);
             const int64_t ei = (int64_t)blk * a.Hkv + h;
             const int e_old = exp[ei];
-            // the run's first 16 rows stay in registers, requested together
+            // the run's first KEEP * RPP rows stay in registers, requested together (8 rows at D = 128 and 16 at 64 where
+            // a warp takes a run, 2 where a row's lanes do); the others are read again after the maximum.  Four passes
+            // instead of two, for 16 rows at D = 128, were slower: 14.6 us against 13.8 for the 8000 tokens below
             uint4 keep[KEEP][2];
 #pragma unroll
             for (int q = 0; q < KEEP; ++q) {
@@ -196,7 +200,7 @@ __global__ void __launch_bounds__(256, 4) kv_store_block_kernel(const StoreBlock
 
 __global__ void __launch_bounds__(256) kv_reset_block_kernel(uint8_t *k_exp, uint8_t *v_exp, int n_layers, int n_blocks,
                                                              int Hkv, const int32_t *blocks, int64_t total, int n,
-                                                             int32_t *err, int early_meta)
+                                                             int32_t *err)
 {
     pdl_wait();
     pdl_launch_dependents();
@@ -268,7 +272,6 @@ extern "C" pa_status pa_kv_store_fp8_block(void *k_buf, void *v_buf, pa_kv_shape
     a.Hkv = s.n_kv_heads;
     a.block = block;
     while ((1 << a.shift) < block) ++a.shift;
-    a.early_meta = early_metadata();
     return s.head_dim == 128 ? launch_store_block<128>(a, st) : launch_store_block<64>(a, st);
 }
 
@@ -284,7 +287,7 @@ extern "C" pa_status pa_kv_reset_fp8_block(uint8_t *k_exp, uint8_t *v_exp, int n
     const int64_t cap = (int64_t)num_sms() * 16;
     if (g > cap) g = cap;
     if (launch_kernel(kv_reset_block_kernel, dim3((unsigned)g), dim3(256), 0, st, k_exp, v_exp, n_layers, n_blocks,
-                      n_kv_heads, blocks, total, n, error_word, (int)early_metadata()) != cudaSuccess)
+                      n_kv_heads, blocks, total, n, error_word) != cudaSuccess)
         return PA_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
