@@ -388,7 +388,9 @@ pa_status pa_paged_decode_attn_fp8_block(const void *q, int batch, int n_q_heads
  * the weights are rounded to bf16, as in pa_paged_prefill_attn.  (Keys of an empty
  * block count as their codes times 2^-126, which only queries beyond 1e27 can tell
  * from 0.)  A query row that holds a NaN or an infinity gives
- * NaN. */
+ * NaN.  A NaN key reaches the queries that see it; a NaN value may reach earlier
+ * ones of its request as well (its weight of 0 times NaN), as in
+ * pa_paged_prefill_attn. */
 pa_status pa_paged_prefill_attn_fp8_block(const void *q, int n_tokens, int n_q_heads, const void *k_buf,
                                           const void *v_buf, pa_kv_shape s, int layer_id, const int32_t *qo_indptr,
                                           const int32_t *kv_indptr, int n_reqs, const int32_t *req_to_token,

@@ -94,6 +94,22 @@ def test_decode_over_empty_blocks_gives_zeros():
         assert float((w[int(c.rows[b]), :n] * n - 8).abs().max()) < 1e-4
 
 
+@pytest.mark.parametrize("block", [16, 1])
+def test_prefill_nan_key_is_seen_from_its_token_on(block):
+    """A NaN among a later token's keys reaches the queries that see it and no other."""
+    c = Cache([300], 2, 128, 16, block, 89)
+    c.k[1, c.slots[0][150], 1, 7] = 127
+    c.cuda()
+    q = torch.randn((300, 8, 128), generator=c.g).to(torch.bfloat16)
+    out = prefill(c, q.cuda(), [0, 300], 0.05)
+    assert torch.isnan(out[150:, 4:].float()).all()
+    k, v = c.values(0)
+    r = R.attention(q[:, :4].double(), k[:, :1], v[:, :1], 0.05, first=0, terms=2.0 ** -19)
+    R.check_out(out[:, :4].cpu(), r, 8, "the other kv head")
+    r = R.attention(q[:150, 4:].double(), k[:150, 1:], v[:150, 1:], 0.05, first=0, terms=2.0 ** -19)
+    R.check_out(out[:150, 4:].cpu(), r, 8, "queries before the NaN")
+
+
 # ------------------------------------------------------------- long contexts
 
 @pytest.mark.parametrize("block", [0, 16])
