@@ -62,6 +62,7 @@ typedef enum {
 #define PA_DEVERR_LEN 0x4       /* a seq_len / indptr length outside [0, max_ctx] or n_r > L_r */
 #define PA_DEVERR_POS 0x8       /* a rotary position outside [0, max_pos) */
 #define PA_DEVERR_TIMEOUT 0x10  /* a bounded pipeline wait gave up (internal error); the call aborted */
+#define PA_DEVERR_TREE 0x20     /* a drafted token's parent or id, or an accepted path, out of range */
 
 /* Shape of one of the two KV buffers, bf16 [n_layers, size, n_kv_heads, head_dim];
  * slot `loc` of layer `l` starts at element ((l * size + loc) * n_kv_heads) * head_dim. */
@@ -452,6 +453,100 @@ pa_status pa_paged_decode_attn_weights(const void *q, int batch, int n_q_heads, 
 pa_status pa_kv_evict(int32_t *req_to_token, int req_rows, int max_ctx, const int32_t *req_pool_indices,
                       const int32_t *seq_lens, int batch, float *weights, int budget, int recent,
                       int32_t *new_lens, int32_t *freed, int32_t *error_word, cudaStream_t st);
+
+/* ------------------------------------------- drafted tokens: attention
+ * No counterpart on the pages (nor of the two calls below): speculative
+ * decoding, several drafted tokens per request and step.  A request's drafted
+ * tokens ("nodes") are its last cached tokens, a tree or a chain; their K/V are
+ * stored like any new tokens'.
+ *
+ * pa_paged_tree_attn: request r has the packed query rows qo_indptr[r] ..
+ * qo_indptr[r+1]-1, its n_r nodes, and L_r = seq_lens[r] cached tokens through
+ * req_to_token[req_pool_indices[r]], of which the last n_r are the nodes in their
+ * order and the c_r = L_r - n_r in front its context.  Node i sees the whole context, and node k
+ * (position c_r + k) where bit k % 32 of tree_mask[qo_indptr[r] + i, k / 32] is
+ * set (int32 [n_tokens, mask_words]; a node sees itself only if its own bit is
+ * set); tree_mask == NULL (mask_words 0): where k <= i, a chain.  Over what it sees
+ *     s_j = scale * <q[t, hq], K_j>,   out[t, hq] = sum_j softmax(s)_j V_j
+ * and zeros where it sees nothing (or every s_j is minus infinity).  A K or V row
+ * that a node does not see does not reach it, whatever it holds.  q, out: bf16
+ * [n_tokens, n_q_heads, head_dim]; rows from qo_indptr[n_reqs] on are not written.
+ * block == 0: the bf16 cache, k_exp and v_exp NULL; block >= 1: the e4m3 cache
+ * with scales per block of slots.  Supported: head_dim 64 or 128, 1 <= G <= 16,
+ * n_reqs <= 4096.  Workspace: pa_tree_workspace_bytes, whatever the batch,
+ * initialised once with pa_workspace_init; calls that share one are ordered on a
+ * stream.  Two kernels: partial results over equal ranges of cached tokens, then
+ * their merge in a fixed order (run-to-run bit-identical).  A range qo_indptr[r] ..
+ * qo_indptr[r+1] outside [0, n_tokens] sets PA_DEVERR_LEN and skips the request; a
+ * request row out of range (PA_DEVERR_ROW), L_r outside [n_r, max_ctx] or more nodes
+ * than the mask has bits (PA_DEVERR_LEN) give zeros; a slot outside [0, size) is
+ * masked and sets PA_DEVERR_SLOT.  Under PA_OVERLAP_EARLY_KV it behaves as in
+ * early-metadata mode, in which qo_indptr is an index input and tree_mask is not. */
+size_t pa_tree_workspace_bytes(int n_q_heads, int n_kv_heads, int head_dim);
+pa_status pa_paged_tree_attn(const void *q, int n_tokens, int n_q_heads, const void *k_buf, const void *v_buf,
+                             pa_kv_shape s, int layer_id, const int32_t *qo_indptr, int n_reqs,
+                             const int32_t *req_to_token, int req_rows, int max_ctx,
+                             const int32_t *req_pool_indices, const int32_t *seq_lens, const int32_t *tree_mask,
+                             int mask_words, float scale, const uint8_t *k_exp, const uint8_t *v_exp, int block,
+                             void *workspace, size_t workspace_bytes, void *out, cudaStream_t st);
+
+/* ---------------------------------------- drafted tokens: verification
+ * Which drafted tokens are kept, so that the kept ones and the one that follows
+ * are distributed as if drawn from the target alone.  Node 0 of a request is its
+ * root, the newest certain token, always kept; node i >= 1 is drafted token
+ * tokens[t] behind node parents[t] (local, parents < i; parents of node 0 is not
+ * looked at), t = qo_indptr[r] + i.  target_probs p, fp32 [n_tokens, vocab]: row t is the target's
+ * distribution behind node i.  draft_probs f: likewise the draft's, from which
+ * the node's children were drawn one by one (with replacement); NULL: the
+ * children were chosen, not drawn (the draft's likeliest, say).  With
+ * cur = 0, w = p[cur], Z = 1, the nodes i = 1, 2, ... whose parent is cur are tried in order:
+ *   f given: kept if u_accept[t] * (Z * f[cur][x]) < w[x], x the node's token; if
+ *            not, w <- max(w - Z * f[cur], 0), then Z <- sum w
+ *   f NULL:  kept if u_accept[t] * Z < w[x]; if not, Z <- max(Z - w[x], 0), then w[x] <- 0
+ * (fp32, each operation rounded); a kept node becomes cur, with w = p[cur] and
+ * Z = 1.  The path ends when no node is left, or at max_path nodes.  The token
+ * that follows is the smallest v with sum_{x <= v} w[x] > u_sample[r] * sum w (w =
+ * p[cur] if w sums to 0; -1 if that does too).  Sums count each w in whole
+ * steps of 2^-48 (nearest, ties to even), so they do not depend on any order; they must stay
+ * below 2^15.  NaN and negative probabilities count as 0; u lie in [0, 1).
+ *   accepted int32 [n_reqs, max_path]: the kept nodes (local, from the root on), -1 behind
+ *   n_accepted int32 [n_reqs]: their number, the root among them (0: a request without nodes)
+ *   next_token int32 [n_reqs]
+ * A parent outside [0, i) or a token outside [0, vocab) sets PA_DEVERR_TREE, and the node is
+ * not kept.  A qo_indptr range outside [0, n_tokens], or of more than 1024 nodes,
+ * sets PA_DEVERR_LEN and counts as no nodes.  One kernel, a cluster of CTAs per request;
+ * vocab <= 2^24, n_reqs <= 65536.  All inputs are read behind the preceding kernel in every overlap mode. */
+pa_status pa_tree_verify(const float *target_probs, const float *draft_probs, int vocab, const int32_t *tokens,
+                         const int32_t *parents, int n_tokens, const int32_t *qo_indptr, int n_reqs,
+                         const float *u_accept, const float *u_sample, int32_t *accepted, int max_path,
+                         int32_t *n_accepted, int32_t *next_token, int32_t *error_word, cudaStream_t st);
+
+/* ------------------------------------------- drafted tokens: acceptance
+ * pa_kv_accept: the accepted path's tokens become the request's newest, the other
+ * nodes go.  Nodes, context and lengths as in pa_paged_tree_attn; accepted and
+ * n_accepted as pa_tree_verify leaves them: a_r = n_accepted[r] nodes e_0 < e_1 < ...
+ *   Table form (k_buf and v_buf NULL; any cache): table row entry c_r + k becomes
+ * the slot of node e_k, k < a_r (in place; entries behind are left as they are), and
+ * freed[qo_indptr[r] ..] lists the n_r - a_r other nodes' slots in their order.
+ *   Move form (K and V buffers of elem_bytes 2, bf16, or 1, e4m3 with scales per
+ * (layer, head); a block-scaled cache takes the table form): in every layer
+ * the K/V row of node e_k is copied to the slot of position c_r + k; the table stays, and
+ * freed[qo_indptr[r] ..] lists the slots of positions c_r + a_r .. L_r - 1: whole pages
+ * come free.
+ * new_lens[r] = c_r + a_r; freed int32 [n_tokens], entries not listed are left as they are.
+ * new_lens may be seq_lens in the table form; in the move form they must not overlap
+ * (PA_ERR_SHAPE).  A path that is not increasing within [0, n_r), or longer than max_path or n_r, sets
+ * PA_DEVERR_TREE; a row out of range, or one that an earlier request with nodes has too,
+ * PA_DEVERR_ROW; L_r outside [n_r, max_ctx], or a qo_indptr range outside [0, n_tokens],
+ * PA_DEVERR_LEN: such a request is left as it is (new_lens[r] is its length, clamped to [0, max_ctx]).  A
+ * slot outside [0, size) is not moved (PA_DEVERR_SLOT).  Requests must not share slots of nodes.
+ * Table and lengths are index inputs of later calls: as behind pa_kv_evict, in the
+ * early-metadata modes the call right after this one must not read them. */
+pa_status pa_kv_accept(int32_t *req_to_token, int req_rows, int max_ctx, const int32_t *req_pool_indices,
+                       const int32_t *seq_lens, const int32_t *qo_indptr, int n_tokens, int n_reqs,
+                       const int32_t *accepted, int max_path, const int32_t *n_accepted, int32_t *new_lens,
+                       int32_t *freed, void *k_buf, void *v_buf, pa_kv_shape s, int elem_bytes,
+                       int32_t *error_word, cudaStream_t st);
 
 /* ------------------------------------------------------ fused decode step
  * One layer's decode step in one launch (commit 398e8a3: the CUDA-graph

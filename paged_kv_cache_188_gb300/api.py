@@ -26,7 +26,7 @@ LIB_PATH = os.path.join(_HERE, "libpagedattn.so")
 PA_OK = 0
 STATUS = {0: "PA_OK", 1: "PA_ERR_NULL", 2: "PA_ERR_SHAPE", 3: "PA_ERR_ALIGN", 4: "PA_ERR_UNSUPPORTED",
           5: "PA_ERR_WORKSPACE", 6: "PA_ERR_CUDA", 7: "PA_ERR_DEVICE_INDEX"}
-DEVERR_SLOT, DEVERR_ROW, DEVERR_LEN, DEVERR_POS, DEVERR_TIMEOUT = 0x1, 0x2, 0x4, 0x8, 0x10
+DEVERR_SLOT, DEVERR_ROW, DEVERR_LEN, DEVERR_POS, DEVERR_TIMEOUT, DEVERR_TREE = 0x1, 0x2, 0x4, 0x8, 0x10, 0x20
 OVERLAP_OFF, OVERLAP_SAFE, OVERLAP_EARLY_METADATA, OVERLAP_EARLY_KV = 0, 1, 2, 3
 
 
@@ -55,7 +55,8 @@ EXPORTS = ["pa_status_string", "pa_decode_workspace_bytes", "pa_prefill_workspac
            "pa_paged_prefill_attn_fp8", "pa_set_wait_timeout_ns", "pa_get_wait_timeout_ns",
            "pa_kv_store_fp8_block", "pa_kv_reset_fp8_block", "pa_decode_fp8_block_workspace_bytes",
            "pa_paged_decode_attn_fp8_block", "pa_paged_prefill_attn_fp8_block", "pa_decode_weights_workspace_bytes",
-           "pa_paged_decode_attn_weights", "pa_kv_evict"]
+           "pa_paged_decode_attn_weights", "pa_kv_evict", "pa_tree_workspace_bytes", "pa_paged_tree_attn", "pa_tree_verify",
+           "pa_kv_accept"]
 
 _lib = None
 
@@ -111,6 +112,11 @@ def lib():
     L.pa_paged_decode_attn_weights.argtypes = [P, i32, i32, P, P, KvShape, i32, P, i32, i32, P, P, f32, P, P, i32, P, P,
                                                sz, P, P]
     L.pa_kv_evict.argtypes = [P, i32, i32, P, P, i32, P, i32, i32, P, P, P, P]
+    L.pa_tree_workspace_bytes.argtypes = [i32, i32, i32]
+    L.pa_paged_tree_attn.argtypes = [P, i32, i32, P, P, KvShape, i32, P, i32, P, i32, i32, P, P, P, i32, f32, P, P, i32, P,
+                                     sz, P, P]
+    L.pa_tree_verify.argtypes = [P, P, i32, P, P, i32, P, i32, P, P, P, i32, P, P, P, P]
+    L.pa_kv_accept.argtypes = [P, i32, i32, P, P, P, i32, i32, P, i32, P, P, P, P, P, KvShape, i32, P, P]
     L.pa_set_launch_overlap.argtypes = [i32]
     L.pa_get_launch_overlap.argtypes = []
     L.pa_set_wait_timeout_ns.argtypes = [ctypes.c_uint64]
@@ -120,6 +126,7 @@ def lib():
     L.pa_cascade_workspace_bytes.restype = sz
     L.pa_decode_fp8_block_workspace_bytes.restype = sz
     L.pa_decode_weights_workspace_bytes.restype = sz
+    L.pa_tree_workspace_bytes.restype = sz
     L.pa_set_wait_timeout_ns.restype = None
     L.pa_get_wait_timeout_ns.restype = ctypes.c_uint64
     _lib = L
@@ -465,6 +472,110 @@ def pa_kv_evict(req_to_token, req_pool_indices, seq_lens, weights, budget, recen
         req_to_token.data_ptr(), req_rows, max_ctx, req_pool_indices.data_ptr(), seq_lens.data_ptr(), B,
         weights.data_ptr(), budget, recent, new_lens.data_ptr(), freed.data_ptr(), _word(dev, error_word),
         _raw_stream(stream, dev)))
+
+
+def pa_tree_workspace_bytes(n_q_heads, n_kv_heads, head_dim):
+    return int(lib().pa_tree_workspace_bytes(n_q_heads, n_kv_heads, head_dim))
+
+
+def pa_paged_tree_attn(q, k_buf, v_buf, layer_id, qo_indptr, req_to_token, req_pool_indices, seq_lens, scale, workspace,
+                       out, tree_mask=None, k_exp=None, v_exp=None, block=0, stream=None):
+    """Attention of each request's drafted tokens, its last cached ones, over a
+    bf16 cache or (``block`` >= 1, with ``k_exp`` and ``v_exp``) a block-scaled
+    e4m3 cache.  ``tree_mask`` (int32 [T, words]): the bits of the drafted tokens
+    that each of them sees; None: a chain."""
+    dev = _device()
+    if block == 0 and k_exp is None and v_exp is None:
+        _all(dev, (k_buf, torch.bfloat16, 4, "k_buf"), (v_buf, torch.bfloat16, 4, "v_buf"))
+        s = _kv_shape(k_buf, v_buf)
+        ke = ve = None
+    else:
+        if k_exp is None or v_exp is None:
+            raise ValueError("a block-scaled cache needs k_exp and v_exp")
+        s = _kv_shape_block(dev, k_buf, v_buf, k_exp, v_exp, block)
+        ke, ve = k_exp.data_ptr(), v_exp.data_ptr()
+    _all(dev, (q, torch.bfloat16, 3, "q"), (out, torch.bfloat16, 3, "out"), (qo_indptr, torch.int32, 1, "qo_indptr"),
+         (req_to_token, torch.int32, 2, "req_to_token"), (req_pool_indices, torch.int32, 1, "req_pool_indices"),
+         (seq_lens, torch.int32, 1, "seq_lens"), (workspace, torch.uint8, 1, "workspace"))
+    T, Hq, D = shape = q.shape
+    R = seq_lens.shape[0]
+    if out.shape != shape or D != s.head_dim or qo_indptr.shape[0] != R + 1 or req_pool_indices.shape[0] != R:
+        raise ValueError("q/out [T, Hq, D], qo_indptr [R+1], req_pool_indices/seq_lens [R] expected")
+    mask, words = None, 0
+    if tree_mask is not None:
+        _all(dev, (tree_mask, torch.int32, 2, "tree_mask"))
+        words = tree_mask.shape[1]
+        if tree_mask.shape[0] != T or words < 1:
+            raise ValueError("tree_mask must be [T, words], words >= 1")
+        mask = tree_mask.data_ptr()
+    req_rows, max_ctx = req_to_token.shape
+    _ok("pa_paged_tree_attn", lib().pa_paged_tree_attn(
+        q.data_ptr(), T, Hq, k_buf.data_ptr(), v_buf.data_ptr(), s, layer_id, qo_indptr.data_ptr(), R,
+        req_to_token.data_ptr(), req_rows, max_ctx, req_pool_indices.data_ptr(), seq_lens.data_ptr(), mask, words, scale,
+        ke, ve, block, workspace.data_ptr(), workspace.shape[0], out.data_ptr(), _raw_stream(stream, dev)))
+
+
+def pa_tree_verify(target_probs, tokens, parents, qo_indptr, u_accept, u_sample, accepted, n_accepted, next_token,
+                   draft_probs=None, error_word=None, stream=None):
+    """Which drafted tokens are kept, and the token behind them, from the target's
+    probabilities (fp32 [T, V]), the draft's (None: the tokens were chosen, not
+    drawn) and uniform random numbers ``u_accept`` [T], ``u_sample`` [R]: the kept
+    nodes in ``accepted`` (int32 [R, max_path], -1 behind), their number in
+    ``n_accepted``."""
+    dev = _device()
+    _all(dev, (target_probs, torch.float32, 2, "target_probs"), (tokens, torch.int32, 1, "tokens"),
+         (parents, torch.int32, 1, "parents"), (qo_indptr, torch.int32, 1, "qo_indptr"),
+         (u_accept, torch.float32, 1, "u_accept"), (u_sample, torch.float32, 1, "u_sample"),
+         (accepted, torch.int32, 2, "accepted"), (n_accepted, torch.int32, 1, "n_accepted"),
+         (next_token, torch.int32, 1, "next_token"))
+    T, V = target_probs.shape
+    R, max_path = accepted.shape
+    draft = None
+    if draft_probs is not None:
+        _all(dev, (draft_probs, torch.float32, 2, "draft_probs"))
+        if draft_probs.shape != (T, V):
+            raise ValueError("draft_probs must have the shape of target_probs")
+        draft = draft_probs.data_ptr()
+    if tokens.shape[0] != T or parents.shape[0] != T or u_accept.shape[0] != T:
+        raise ValueError("tokens, parents and u_accept [T] expected")
+    if qo_indptr.shape[0] != R + 1 or u_sample.shape[0] != R or n_accepted.shape[0] != R or next_token.shape[0] != R:
+        raise ValueError("qo_indptr [R+1], u_sample/n_accepted/next_token [R] expected")
+    _ok("pa_tree_verify", lib().pa_tree_verify(
+        target_probs.data_ptr(), draft, V, tokens.data_ptr(), parents.data_ptr(), T, qo_indptr.data_ptr(), R,
+        u_accept.data_ptr(), u_sample.data_ptr(), accepted.data_ptr(), max_path, n_accepted.data_ptr(),
+        next_token.data_ptr(), _word(dev, error_word), _raw_stream(stream, dev)))
+
+
+def pa_kv_accept(req_to_token, req_pool_indices, seq_lens, qo_indptr, accepted, n_accepted, new_lens, freed, k_buf=None,
+                 v_buf=None, error_word=None, stream=None):
+    """Keep each request's accepted nodes and free its others: in the page table, or
+    (``k_buf``, ``v_buf``: bf16 or e4m3 with scales per head) by moving the K/V rows
+    of every layer.  Lengths in ``new_lens``, the slots handed back in ``freed``
+    (int32 [T], a request's from ``qo_indptr`` on)."""
+    dev = _device()
+    _all(dev, (req_to_token, torch.int32, 2, "req_to_token"), (req_pool_indices, torch.int32, 1, "req_pool_indices"),
+         (seq_lens, torch.int32, 1, "seq_lens"), (qo_indptr, torch.int32, 1, "qo_indptr"),
+         (accepted, torch.int32, 2, "accepted"), (n_accepted, torch.int32, 1, "n_accepted"),
+         (new_lens, torch.int32, 1, "new_lens"), (freed, torch.int32, 1, "freed"))
+    R, max_path = accepted.shape
+    if (qo_indptr.shape[0] != R + 1 or req_pool_indices.shape[0] != R or seq_lens.shape[0] != R
+            or n_accepted.shape[0] != R or new_lens.shape[0] != R):
+        raise ValueError("qo_indptr [R+1], req_pool_indices/seq_lens/n_accepted/new_lens [R] expected")
+    s, elem, kp, vp = KvShape(0, 0, 0, 0), 0, None, None
+    if k_buf is not None or v_buf is not None:
+        if k_buf is None or v_buf is None:
+            raise ValueError("k_buf and v_buf go together")
+        if k_buf.dtype is not torch.bfloat16 and k_buf.dtype not in FP8_DTYPES:
+            raise TypeError(f"k_buf must be bfloat16, uint8 or float8_e4m3fn, got {k_buf.dtype}")
+        _all(dev, (k_buf, k_buf.dtype, 4, "k_buf"), (v_buf, k_buf.dtype, 4, "v_buf"))
+        if k_buf.shape != v_buf.shape:
+            raise ValueError("k_buf and v_buf shapes differ")
+        s, elem, kp, vp = KvShape(*k_buf.shape), k_buf.element_size(), k_buf.data_ptr(), v_buf.data_ptr()
+    req_rows, max_ctx = req_to_token.shape
+    _ok("pa_kv_accept", lib().pa_kv_accept(
+        req_to_token.data_ptr(), req_rows, max_ctx, req_pool_indices.data_ptr(), seq_lens.data_ptr(), qo_indptr.data_ptr(),
+        freed.shape[0], R, accepted.data_ptr(), max_path, n_accepted.data_ptr(), new_lens.data_ptr(), freed.data_ptr(), kp,
+        vp, s, elem, _word(dev, error_word), _raw_stream(stream, dev)))
 
 
 def pa_decode_step(q, k_new, v_new, positions, cos_tab, sin_tab, k_buf, v_buf, layer_id, loc, req_to_token,
