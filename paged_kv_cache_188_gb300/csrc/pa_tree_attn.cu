@@ -1,28 +1,875 @@
 // pa_tree_attn.cu -- attention of drafted tokens (a tree or a chain per request)
-// over the paged cache, bf16 or block-scaled e4m3.
+// over the paged cache on tcgen05, bf16 or block-scaled e4m3.
 //
+// For node i of a request (n nodes, the last of its L cached tokens, context c = L
+// - n) and query head hq = h G + g:
 //     s_j = scale <q_i, K_j>,   out_i = sum_j softmax(s)_j V_j
-// over the context and the nodes whose bits the mask has.  One warp per (node,
-// query head) walks the keys with a running maximum and sum: the simplest form.
+// over j < c and the nodes whose bits the mask has for it.
+//
+// How.  All (node, head) pairs of a kv head read the same keys, so they are the
+// rows of one product: a tile of M = 128 rows, row = node G + g.  K and V come
+// once per 256 rows (a "pair" of tiles), and decode's problem stays: few rows, many
+// keys, the keys' bytes are the bound (up to about 256 rows: 128 x 128 x D x 4
+// operations take the tensor core half of the time that HBM takes for the
+// 128-token tile).  So the work is cut along the keys: the segments (request,
+// pair), 128-token tiles laid end to end, are cut into equal ranges, as many as
+// there are CTAs per kv head; (range i, head h) is unit i Hkv + h, so that the heads
+// of a token are read at about the same time.  A unit shares at most its first
+// and its last segment with others: two slots of fp32 partials per unit, merged
+// by a second kernel in the pieces' order (deterministic).
+//
+// A CTA has two streams, X = A and B, each with a warpgroup, S columns, O columns
+// and running maximum and sum:
+//   more than 128 rows:  A and B are the two tiles of rows, over every token tile;
+//   up to 128 rows:      A takes the even token tiles, B the odd ones, of the same
+//                        rows, joined when the piece ends.
+// Either way step i = 0, 1, ... belongs to stream i & 1, and the tensor core runs
+// S(0) S(1) | PV(0) S(2) | PV(1) S(3) | ...: a step's softmax has the time of the
+// other stream's products.
+//   S = Q K^T      A = Q, B = K tile as TMA left it, fp32 in tensor memory
+//   P over S       bf16, read by the second product from tensor memory
+//   O += P V       fp32 in tensor memory, rescaled only when the running maximum
+//                  grows by more than 2^8
+// Warps 0-7: softmax, one row a thread; 8 and 9: K and V copies through the page
+// table (16 consecutive slots are one TMA box, any other four rows one gather4
+// copy); 10: the products.
+//
+// Hidden rows: a hidden token's weight is 0, but 0 times a NaN or an infinity in
+// its V row would reach every node.  Only drafted tokens are ever hidden (context
+// is seen by all), so the products' warp looks through their V rows in shared
+// memory, zeroes one that holds such a value, and the rows that do see it add its
+// part by hand when the piece ends.
 #include <math.h>
+#include <string.h>
 
-#include "pa_common.cuh"
 #include "pa_internal.h"
+#include "pa_sm100.cuh"
 
 namespace pa {
+using namespace sm100;
 
 constexpr int kTreeMaxReqs = 4096;
+constexpr int kTrTile = 128;             // tokens of a tile, rows of a stream
+constexpr int kTrPair = 256;             // rows that share a token tile
+constexpr int kTrThreads = 352;
+constexpr int kTrHalf = 128 * 128;       // 128 rows of 64 bf16, 128-byte swizzle
+constexpr int kTrMeta = 8;               // tiles whose valid positions are kept: see tr_copy
+constexpr int kTrMaxCtas = 160;
+constexpr int kTrMaxUnits = 2 * kTrMaxCtas;   // units that share segments
+constexpr uint32_t kTrTmemCols = 512;    // S_A | S_B | O_A | O_B
 
 struct TreeArgs {
+    CUtensorMap tm_k16, tm_k1, tm_v16, tm_v1;    // 2-D (element, row): boxes of 16 rows, and one row (gather4)
     const __nv_bfloat16 *q;
     const uint8_t *k, *v;                        // the layer's rows
     const uint8_t *k_exp, *v_exp;                // the layer's exponents (e4m3 cache)
     const int32_t *qo_indptr, *req_to_token, *req_pool_indices, *seq_lens, *tree_mask;
     __nv_bfloat16 *out;
     int32_t *err;
-    int T, R, Hq, Hkv, G, size, req_rows, max_ctx, mask_words, block_shift;
-    float scale_log2;
+    float *ml_part;                              // [2 units][256][2]: maximum (log2 units), sum
+    float *o_part;                               // [2 units][256][D]: relative to that maximum
+    int T, R, Hq, Hkv, G, size, req_rows, max_ctx, mask_words, block_shift, layer_row0, total_rows, early_meta;
+    int ranges;                                  // per kv head
+    uint64_t wait_ns;
+    float scale_log2;                            // of the scale's magnitude; its sign goes into q
+    int sign;                                    // of the scale: -1, 0, 1
 };
+
+// ------------------------------------------------------------------- plan
+struct TrReq {
+    int q0, n, L, row;      // n = 0: nothing to do; L = 0: zeros
+};
+__device__ __forceinline__ TrReq tr_request(const TreeArgs &a, int r, int &bits)
+{
+    TrReq q;
+    q.q0 = __ldg(a.qo_indptr + r);
+    const int q1 = __ldg(a.qo_indptr + r + 1);
+    q.L = __ldg(a.seq_lens + r);
+    q.row = __ldg(a.req_pool_indices + r);
+    q.n = q1 - q.q0;
+    bits = 0;
+    if (q1 <= q.q0 || q.q0 < 0 || q1 > a.T) {
+        if (q1 != q.q0) bits = PA_DEVERR_LEN;
+        q.n = q.L = 0;
+        return q;
+    }
+    if (q.row < 0 || q.row >= a.req_rows) bits |= PA_DEVERR_ROW;
+    if (q.L < q.n || q.L > a.max_ctx || (a.tree_mask && q.n > 32 * (int64_t)a.mask_words)) bits |= PA_DEVERR_LEN;
+    if (bits) q.L = q.row = 0;
+    return q;
+}
+__device__ __forceinline__ int tr_pairs(const TreeArgs &a, int n) { return (int)(((int64_t)n * a.G + kTrPair - 1) / kTrPair); }
+__device__ __forceinline__ int tr_ktiles(int L) { return L > 0 ? (L + kTrTile - 1) / kTrTile : 1; }
+__device__ __forceinline__ int tr_tiles(const TreeArgs &a, const TrReq &q) { return q.n > 0 ? tr_pairs(a, q.n) * tr_ktiles(q.L) : 0; }
+
+// A warp's walk over the pieces of a unit's range: tiles [x, xe) of the segments laid end to end.
+struct TrWalk {
+    int x, xe, r, S0;       // next tile, end; request and its first tile
+    int w0;                 // the lanes hold requests w0 + lane
+    TrReq w;
+    // the piece: token tiles [t0, t1) of rows 256 pair .. of request r
+    TrReq q;
+    int kt, pair, t0, t1, first;    // kt: the request's tiles; first: the piece starts the range
+    int x0;
+};
+__device__ __forceinline__ void tr_begin(TrWalk &k, int x, int xe, int r, int S0)
+{
+    k.x = k.x0 = x;
+    k.xe = xe;
+    k.r = r;
+    k.S0 = S0;
+    k.w0 = -64;
+}
+__device__ __forceinline__ bool tr_next(const TreeArgs &a, TrWalk &k, int lane)
+{
+    if (k.x >= k.xe) return false;
+    while (true) {
+        if (k.r - k.w0 >= 32) {
+            k.w0 = k.r;
+            int bits;
+            k.w = TrReq{0, 0, 0, 0};
+            if (k.r + lane < a.R) k.w = tr_request(a, k.r + lane, bits);
+        }
+        const int i = k.r - k.w0;
+        k.q.q0 = __shfl_sync(0xffffffffu, k.w.q0, i);
+        k.q.n = __shfl_sync(0xffffffffu, k.w.n, i);
+        k.q.L = __shfl_sync(0xffffffffu, k.w.L, i);
+        k.q.row = __shfl_sync(0xffffffffu, k.w.row, i);
+        const int tiles = tr_tiles(a, k.q);
+        if (k.x < k.S0 + tiles || k.r >= a.R) break;
+        k.S0 += tiles;
+        ++k.r;
+    }
+    if (k.r >= a.R) return false;
+    k.kt = tr_ktiles(k.q.L);
+    const int off = k.x - k.S0;
+    k.pair = off / k.kt;
+    k.t0 = off - k.pair * k.kt;
+    k.t1 = min(k.kt, k.t0 + k.xe - k.x);
+    k.first = k.x == k.x0;
+    k.x += k.t1 - k.t0;
+    return true;
+}
+// rows of the piece, and its steps: a token tile is one step of each stream, or of one of them in turn
+__device__ __forceinline__ int tr_rows(const TreeArgs &a, const TrWalk &k)
+{
+    return (int)min((int64_t)kTrPair, (int64_t)k.q.n * a.G - (int64_t)k.pair * kTrPair);
+}
+
+// 32 bits of what node i (row `qrow` of the mask) sees, from node s on (s < 0: context, all ones)
+__device__ __forceinline__ uint32_t tr_seen(const TreeArgs &a, int64_t qrow, int i, int s)
+{
+    if (!a.tree_mask) {
+        const int ones = i - s + 1;
+        return ones <= 0 ? 0u : ones >= 32 ? 0xFFFFFFFFu : (1u << ones) - 1u;
+    }
+    const int w = s >> 5;
+    const int32_t *m = a.tree_mask + qrow * a.mask_words;
+    const uint32_t lo = w < 0 ? 0xFFFFFFFFu : w < a.mask_words ? (uint32_t)__ldg(m + w) : 0u;
+    const uint32_t hi = w + 1 < 0 ? 0xFFFFFFFFu : w + 1 < a.mask_words ? (uint32_t)__ldg(m + w + 1) : 0u;
+    return __funnelshift_r(lo, hi, s & 31);
+}
+
+template <int D>
+struct TrCfg {
+    static constexpr int HALVES = D / 64;
+    static constexpr int TILE = HALVES * kTrHalf;
+    static constexpr int NK = D == 128 ? 3 : 5, NV = D == 128 ? 2 : 5;   // ring stages
+    static constexpr int OffK = 2 * TILE;                // behind Q of both streams
+    static constexpr int OffV = OffK + NK * TILE;
+    static constexpr int OffBar = OffV + NV * TILE;
+    enum { K_FULL, K_EMPTY = K_FULL + NK, V_FULL = K_EMPTY + NK, V_EMPTY = V_FULL + NV, S_FULL = V_EMPTY + NV,
+           P_READY = S_FULL + 2, O_FULL = P_READY + 2, Q_READY = O_FULL + 2, DRAIN = Q_READY + 2, N_BARS };
+    static constexpr int OffMeta = (OffBar + N_BARS * 8 + 15) & ~15;     // uint4 [kTrMeta]: valid positions
+    static constexpr int OffML = OffMeta + kTrMeta * 16;                 // float2 [128]: stream B's (m, l)
+    static constexpr int OffEnd = OffML + 128 * 8;
+    static constexpr int Smem = OffEnd + 1024;
+    static constexpr uint32_t ColO = 256;
+    static constexpr uint32_t kIdS = idesc_bf16_f32(128, 128, 0, 0), kIdPV = idesc_bf16_f32(128, D, 0, 1);
+};
+static_assert(TrCfg<128>::Smem <= 232448 - 256, "fits with the static shared memory");
+static_assert(kTrMeta >= TrCfg<64>::NK + 3 && kTrMeta >= TrCfg<128>::NK + 3, "a tile's valid positions outlive its ring stage");
+
+__device__ __forceinline__ float tr_ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// ----------------------------------------------------------------- copies
+// K (isv false) or V tiles of the CTA's units.  Positions without a row (past the
+// end, or a bad slot) are zeros; the K warp also writes which positions are valid:
+// a ring of its own, because softmax reads them behind S, when the K stage is
+// already free.  (Tile x is copied when S(x - NK) is done, which was issued behind
+// softmax of tile x - NK - 1 at the latest.)
+template <int D, typename Begin>
+__device__ __forceinline__ void tr_copy(const TreeArgs &a, const Begin &begin, bool isv, uint32_t ring, uint32_t full,
+                                        uint32_t empty, uint4 *meta, volatile int *s_abort, int lane)
+{
+    using C = TrCfg<D>;
+    const int stages = isv ? C::NV : C::NK, units = a.ranges * a.Hkv;
+    const CUtensorMap *m16 = isv ? &a.tm_v16 : &a.tm_k16, *m1 = isv ? &a.tm_v1 : &a.tm_k1;
+    int st = 0, seq = 0, errs = 0;
+    uint32_t ph = 0;
+    bool go = true;
+#pragma unroll 1
+    for (int unit = blockIdx.x, u = 0; unit < units && go; unit += gridDim.x, ++u) {
+        TrWalk k;
+        begin(k, unit, u);
+        const int col = unit % a.Hkv * D;
+        while (go && tr_next(a, k, lane)) {
+            if (k.q.L == 0) continue;
+            const int32_t *tab = a.req_to_token + (int64_t)k.q.row * a.max_ctx;
+            int nx[4];
+            auto fetch = [&](int t) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int p = t * kTrTile + 4 * lane + e;
+                    nx[e] = ld_nc_ordered_s32_if(p < k.q.L, tab + (p < k.q.L ? p : 0));
+                }
+            };
+            fetch(k.t0);
+#pragma unroll 1
+            for (int t = k.t0; t < k.t1; ++t) {
+                int sl[4] = {nx[0], nx[1], nx[2], nx[3]};
+                if (t + 1 < k.t1) fetch(t + 1);
+                if (seq >= stages &&
+                    !__all_sync(0xffffffffu, mbar_wait(empty + st * 8, ph ^ 1, s_abort, a.err, PA_DEVERR_TIMEOUT, a.wait_ns))) {
+                    go = false;
+                    break;
+                }
+                const uint32_t dst = ring + st * C::TILE, fb = full + st * 8;
+                bool ok[4];
+                uint32_t nib = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const bool in = t * kTrTile + 4 * lane + e < k.q.L;
+                    ok[e] = in && sl[e] >= 0 && sl[e] < a.size;
+                    if (in && !ok[e]) errs |= PA_DEVERR_SLOT;
+                    nib |= (uint32_t)ok[e] << e;
+                }
+                const int s0 = __shfl_sync(0xffffffffu, sl[0], lane & ~3);
+                const bool run = nib == 15u && sl[0] == s0 + 4 * (lane & 3) && sl[1] == sl[0] + 1 && sl[2] == sl[0] + 2 &&
+                                 sl[3] == sl[0] + 3;
+                const bool page = ((__ballot_sync(0xffffffffu, run) >> (lane & ~3)) & 0xFu) == 0xFu;
+                const bool none = ((__ballot_sync(0xffffffffu, nib != 0u) >> (lane & ~3)) & 0xFu) == 0u;
+                if (page || none) {
+                    // a page's rows, or rows out of range, which read as zeros
+                    if ((lane & 3) == 0) {
+#pragma unroll
+                        for (int hh = 0; hh < C::HALVES; ++hh)
+                            tma_load_2d(dst + hh * kTrHalf + (lane >> 2) * 16 * 128, m16, col + hh * 64,
+                                        none ? a.total_rows : a.layer_row0 + sl[0], fb);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sl[e] = ok[e] ? a.layer_row0 + sl[e] : a.total_rows;
+#pragma unroll
+                    for (int hh = 0; hh < C::HALVES; ++hh) {
+                        const uint32_t d = dst + hh * kTrHalf + lane * 4 * 128;
+                        if (nib == 15u) {
+                            tma_gather4(d, m1, col + hh * 64, sl[0], sl[1], sl[2], sl[3], fb);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) tma_load_2d(d + e * 128, m1, col + hh * 64, sl[e], fb);
+                        }
+                    }
+                }
+                if (!isv) {
+                    uint32_t w = nib << (4 * (lane & 7));
+#pragma unroll
+                    for (int o = 1; o < 8; o <<= 1) w |= __shfl_xor_sync(0xffffffffu, w, o);
+                    if ((lane & 7) == 0) reinterpret_cast<uint32_t *>(meta + seq % kTrMeta)[lane >> 3] = w;
+                    __syncwarp();
+                }
+                if (lane == 0) mbar_arrive_expect_tx(fb, C::TILE);
+                __syncwarp();
+                ++seq;
+                if (++st == stages) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            }
+        }
+    }
+    // the warp leaves only when its copies have landed, whether or not anyone has given up by now
+#pragma unroll 1
+    for (int j = max(0, seq - stages); j < seq; ++j) mbar_drain(full + (j % stages) * 8, (j / stages) & 1);
+    if (errs && !isv) set_error(a.err, errs);
+    __syncwarp();
+}
+
+// Does a 16-byte chunk hold a bf16 NaN or infinity?
+__device__ __forceinline__ bool tr_wild(const uint4 &v)
+{
+    auto w = [](uint32_t x) { return (x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u; };
+    return w(v.x) || w(v.y) || w(v.z) || w(v.w);
+}
+
+// Rows lo .. hi of a V tile that hold a NaN or an infinity become zeros; true if there was one.  Whole warp.
+template <int D>
+__device__ __forceinline__ bool tr_tame(uint32_t tile, int lo, int hi, int lane)
+{
+    constexpr int CH = D / 8, PER = 32 / CH;        // chunks of a row, rows at a time
+    bool any = false;
+#pragma unroll 1
+    for (int r0 = lo; r0 < hi; r0 += 4 * PER) {
+        // every chunk of the rows, in any order
+        uint4 v[4];
+        uint32_t at[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int r = r0 + e * PER + lane / CH;
+            at[e] = tile + ((lane % CH) >> 3) * kTrHalf + r * 128 + (lane & 7) * 16;
+            v[e] = r < hi ? ld_shared_v4(at[e]) : make_uint4(0u, 0u, 0u, 0u);
+        }
+        const bool bad = tr_wild(v[0]) || tr_wild(v[1]) || tr_wild(v[2]) || tr_wild(v[3]);
+        if (!__any_sync(0xffffffffu, bad)) continue;
+        any = true;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const unsigned b = __ballot_sync(0xffffffffu, tr_wild(v[e]));
+            if ((b >> (lane / CH * CH)) & ((1u << CH) - 1u)) st_shared_v4(at[e], 0u, 0u, 0u, 0u);
+        }
+    }
+    if (any) fence_proxy_async_smem();
+    return any;
+}
+
+// What tr_tame took out, for one row of the piece (node i, query head hq) and 32 columns from d0 on: the parts of the
+// nodes' V rows in tiles [t0, t1) that hold a NaN or an infinity and that the node sees, weights relative to m2.
+template <int D>
+__device__ __noinline__ void tr_wild_rows(const TreeArgs &a, const TrReq &q, int t0, int t1, int h, int i, int hq, float m2,
+                                          int d0, float *o)
+{
+    const int c = q.L - q.n;
+    const int32_t *tab = a.req_to_token + (int64_t)q.row * a.max_ctx;
+    const __nv_bfloat16 *qr = a.q + ((int64_t)(q.q0 + i) * a.Hq + hq) * D;
+#pragma unroll 1
+    for (int j = max(c, t0 * kTrTile); j < min(q.L, t1 * kTrTile); ++j) {
+        const int slot = __ldg(tab + j);
+        if (slot < 0 || slot >= a.size) continue;
+        const int64_t at = ((int64_t)slot * a.Hkv + h) * D;
+        const __nv_bfloat16 *kr = reinterpret_cast<const __nv_bfloat16 *>(a.k) + at, *vr = reinterpret_cast<const __nv_bfloat16 *>(a.v) + at;
+        bool wild = false;
+#pragma unroll 1
+        for (int d = 0; d < D; d += 8) wild |= tr_wild(__ldg(reinterpret_cast<const uint4 *>(vr + d)));
+        if (!wild || !(tr_seen(a, q.q0 + i, i, j - c) & 1u)) continue;
+        float s = 0.f;
+#pragma unroll 1
+        for (int d = 0; d < D; ++d) s = fmaf(__bfloat162float(qr[d]), __bfloat162float(kr[d]), s);
+        s = a.sign == 0 ? 0.f : a.sign < 0 ? -s : s;
+        const float p = tr_ex2(fmaf(s, a.scale_log2, -m2));
+#pragma unroll 1
+        for (int d = 0; d < 32; ++d) o[d] = fmaf(p, __bfloat162float(vr[d0 + d]), o[d]);
+    }
+}
+
+// ----------------------------------------------------------------- kernel
+template <int D>
+__global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_constant__ TreeArgs a)
+{
+    using C = TrCfg<D>;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ int s_w[kTrThreads / 32];
+    __shared__ int s_abort_storage, s_total;
+    __shared__ int s_start[2][2];              // (request, its first tile) at the start of the CTA's units
+    __shared__ int s_wild[4];                  // per piece, modulo 4: a V row was taken out
+    __shared__ uint32_t s_tmem;
+    const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+    unsigned char *sb = smem_raw + (base - raw);
+    volatile int *s_abort = &s_abort_storage;
+    uint4 *meta = reinterpret_cast<uint4 *>(sb + C::OffMeta);
+    float2 *s_ml = reinterpret_cast<float2 *>(sb + C::OffML);
+    auto bar = [&](int i) -> uint32_t { return base + C::OffBar + i * 8; };
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid < C::N_BARS) {
+        const bool softmax = (tid >= C::P_READY && tid < C::P_READY + 2) || (tid >= C::Q_READY && tid < C::Q_READY + 2);
+        mbar_init(bar(tid), softmax ? 128u : 1u);
+    }
+    static_assert(C::N_BARS <= 32, "one warp initialises the barriers");
+    if (warp == 0) fence_mbar_init();
+    if (tid == 0) {
+        s_abort_storage = 0;
+        s_wild[0] = s_wild[1] = s_wild[2] = s_wild[3] = 0;
+    }
+    if (warp == 10) tmem_alloc(smem_u32(&s_tmem), kTrTmemCols);
+    if (warp == 8 && lane == 0) {
+        prefetch_tmap(&a.tm_k16);
+        prefetch_tmap(&a.tm_k1);
+    }
+    if (warp == 9 && lane == 0) {
+        prefetch_tmap(&a.tm_v16);
+        prefetch_tmap(&a.tm_v1);
+    }
+    if (!a.early_meta) pdl_wait();
+
+    // ---- plan: the segments' tiles in all, and where this CTA's units start
+    const int units = a.ranges * a.Hkv;
+    int bits = 0;
+    {
+        const int per = (a.R + kTrThreads - 1) / kTrThreads, lo = min(a.R, tid * per), hi = min(a.R, lo + per);
+        int run = 0, b;
+#pragma unroll 1
+        for (int r = lo; r < hi; ++r) {
+            run += tr_tiles(a, tr_request(a, r, b));
+            bits |= b;
+        }
+        int incl = run;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) s_w[warp] = incl;
+        __syncthreads();
+        int before = incl - run;
+        int total = 0;
+#pragma unroll 1
+        for (int w = 0; w < kTrThreads / 32; ++w) {
+            if (w < warp) before += s_w[w];
+            total += s_w[w];
+        }
+        if (tid == 0) s_total = total;
+        const int W = (total + a.ranges - 1) / a.ranges;
+        if (a.ranges > 1 && run > 0) {
+#pragma unroll 1
+            for (int u = 0; u < 2; ++u) {
+                const int x = (int)((blockIdx.x + u * gridDim.x) / a.Hkv) * W;
+                if (x < before || x >= before + run) continue;
+                int S0 = before, r = lo;
+#pragma unroll 1
+                for (; r < hi; ++r) {
+                    const int t = tr_tiles(a, tr_request(a, r, b));
+                    if (x < S0 + t) break;
+                    S0 += t;
+                }
+                s_start[u][0] = r;
+                s_start[u][1] = S0;
+            }
+        }
+    }
+    if (a.early_meta) pdl_wait();
+    pdl_launch_dependents();
+    if (bits && blockIdx.x == 0) set_error(a.err, bits);
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    const int total = s_total, W = (total + a.ranges - 1) / a.ranges;
+
+    // unit u of this CTA as a walk
+    auto begin = [&](TrWalk &k, int unit, int u) {
+        const int i = unit / a.Hkv;
+        tr_begin(k, (int)min((int64_t)total, (int64_t)i * W), (int)min((int64_t)total, (int64_t)(i + 1) * W),
+                 a.ranges > 1 ? s_start[u][0] : 0, a.ranges > 1 ? s_start[u][1] : 0);
+    };
+
+    if (warp == 8 || warp == 9) {
+        const bool isv = warp == 9;
+        tr_copy<D>(a, begin, isv, base + (isv ? C::OffV : C::OffK), bar(isv ? C::V_FULL : C::K_FULL),
+                   bar(isv ? C::V_EMPTY : C::K_EMPTY), meta, s_abort, lane);
+    } else if (warp == 10) {
+        // ======================================================= products
+        const uint32_t sQ = base, sK = base + C::OffK, sV = base + C::OffV;
+        int kseq = 0, vseq = 0, piece = 0, pb = 0;   // token tiles, pieces, pieces with steps of stream B before
+        int px[2] = {0, 0};                    // steps of each stream before
+        bool bad = false;
+        auto wait = [&](uint32_t b, uint32_t parity) {
+            if (!bad) bad = !__all_sync(0xffffffffu, mbar_wait(b, parity, s_abort, a.err, PA_DEVERR_TIMEOUT, a.wait_ns));
+        };
+#pragma unroll 1
+        for (int unit = blockIdx.x, u = 0; unit < units; unit += gridDim.x, ++u) {
+            TrWalk k;
+            begin(k, unit, u);
+            while (tr_next(a, k, lane)) {
+                if (k.q.L == 0) continue;
+                const int nt = k.t1 - k.t0, two = tr_rows(a, k) > kTrTile;
+                const int N = two ? 2 * nt : nt, c = k.q.L - k.q.n;
+                if (lane == 0) s_wild[(piece + 2) & 3] = 0;
+                wait(bar(C::Q_READY), piece & 1);
+                if (N > 1) wait(bar(C::Q_READY + 1), pb++ & 1);
+                // S(i): its K tile is waited for by the first step that reads it
+                auto tile_of = [&](int i) { return two ? i >> 1 : i; };
+                auto first_of = [&](int i) { return !two || !(i & 1); };
+                auto last_of = [&](int i) { return !two || (i & 1); };
+                auto wait_k = [&](int i) {
+                    const int s = kseq + tile_of(i);
+                    if (first_of(i)) wait(bar(C::K_FULL + s % C::NK), (s / C::NK) & 1);
+                };
+                auto qk = [&](int i) {
+                    const int st = (kseq + tile_of(i)) % C::NK, X = i & 1;
+                    const uint32_t q = sQ + (two ? X : 0) * C::TILE, kk = sK + st * C::TILE;
+#pragma unroll
+                    for (int s = 0; s < D / 16; ++s)
+                        umma_ss(tmem + X * 128, smem_desc_sw128(q + (s >> 2) * kTrHalf + (s & 3) * 32, 16, 1024),
+                                smem_desc_sw128(kk + (s >> 2) * kTrHalf + (s & 3) * 32, 16, 1024), C::kIdS, s > 0);
+                    umma_commit(bar(C::S_FULL + X));
+                    if (last_of(i)) umma_commit(bar(C::K_EMPTY + st));
+                };
+#pragma unroll 1
+                for (int i = 0; i < 2 && i < N; ++i) {
+                    wait_k(i);
+                    tc_fence_after();
+                    if (!bad) if (elect_one()) qk(i);
+                    __syncwarp();
+                }
+#pragma unroll 1
+                for (int i = 0; i < N; ++i) {
+                    const int X = i & 1, s = vseq + tile_of(i), st = s % C::NV;
+                    const uint32_t vt = sV + st * C::TILE;
+                    if (first_of(i)) {
+                        wait(bar(C::V_FULL + st), (s / C::NV) & 1);
+                        // drafted tokens' rows must not hold what a weight of 0 does not cancel
+                        const int p0 = (k.t0 + tile_of(i)) * kTrTile, lo = max(0, c - p0), hi = min(kTrTile, k.q.L - p0);
+                        if (!bad && lo < hi && tr_tame<D>(vt, lo, hi, lane)) {
+                            if (lane == 0) *(volatile int *)&s_wild[piece & 3] = 1;
+                            __threadfence_block();
+                            __syncwarp();
+                        }
+                    }
+                    wait(bar(C::P_READY + X), px[X] & 1);
+                    ++px[X];
+                    tc_fence_after();
+                    if (!bad) if (elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < kTrTile / 16; ++kk)
+                            umma_ts(tmem + C::ColO + X * D, tmem + X * 128 + kk * 8,
+                                    smem_desc_sw128(vt + kk * 2048, kTrHalf, 1024), C::kIdPV, kk > 0 || i >= 2);
+                        if (last_of(i)) umma_commit(bar(C::V_EMPTY + st));
+                        if (i + 2 >= N) umma_commit(bar(C::O_FULL + X));
+                    }
+                    __syncwarp();
+                    if (i + 2 < N) {
+                        wait_k(i + 2);
+                        tc_fence_after();
+                        if (!bad) if (elect_one()) qk(i + 2);
+                        __syncwarp();
+                    }
+                }
+                kseq += nt;
+                vseq += nt;
+                ++piece;
+            }
+        }
+        // one more commit, which arrives once every product issued has completed, before tensor memory is freed
+        if (elect_one()) umma_commit(bar(C::DRAIN));
+        __syncwarp();
+        mbar_drain(bar(C::DRAIN), 0);
+        __syncwarp();
+    } else {
+        // ======================================== softmax, and the piece's end
+        const int X = warp >> 2, row = tid & 127;
+        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t s_addr = tmem + lane_base + X * 128;
+        const float sl2 = a.scale_log2;
+        int piece = 0, sx = 0, ox = 0, kseq = 0;   // pieces, steps, ends of this stream, token tiles
+        bool bad = false;
+        auto wait = [&](uint32_t b, uint32_t parity) {
+            if (!bad) bad = !__all_sync(0xffffffffu, mbar_wait(b, parity, s_abort, a.err, PA_DEVERR_TIMEOUT, a.wait_ns));
+        };
+#pragma unroll 1
+        for (int unit = blockIdx.x, u = 0; unit < units; unit += gridDim.x, ++u) {
+            TrWalk k;
+            begin(k, unit, u);
+            const int h = unit % a.Hkv;
+            while (tr_next(a, k, lane)) {
+                const int rows = tr_rows(a, k), nt = k.t1 - k.t0, c = k.q.L - k.q.n;
+                const bool two = rows > kTrTile;
+                const int mine = (two ? X * kTrTile : 0) + row;           // this thread's row of the pair
+                const int at = k.pair * kTrPair + mine, node = at / a.G, g = at - node * a.G;
+                const bool live = mine < rows;
+                const int64_t out_row = ((int64_t)(k.q.q0 + (live ? node : 0)) * a.Hq + h * a.G + g) * D;
+                if (k.q.L == 0) {
+                    // nothing to attend to
+                    if (live && (two || X == 0))
+#pragma unroll 1
+                        for (int d = 0; d < D; d += 8) *reinterpret_cast<uint4 *>(a.out + out_row + d) = make_uint4(0u, 0u, 0u, 0u);
+                    continue;
+                }
+                if (a.wait_ns == 0 && !bad) {
+                    // a wait limit of 0: give up at the first piece, as a timed-out wait would
+                    *s_abort = 1;
+                    set_error(a.err, PA_DEVERR_TIMEOUT);
+                    bad = true;
+                }
+                // ---- Q of this stream's rows, zeros behind the last
+                if (two || X == 0) {
+                    constexpr int CH = D / 8, PER = 128 / CH;
+                    const int cc = row % CH;
+#pragma unroll 8
+                    for (int r0 = 0; r0 < 128; r0 += PER) {
+                        const int r = r0 + row / CH, p = (two ? X * kTrTile : 0) + r, gr = k.pair * kTrPair + p;
+                        const int nd = gr / a.G;
+                        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                        if (p < rows && a.sign != 0)
+                            w = __ldg(reinterpret_cast<const uint4 *>(
+                                          a.q + ((int64_t)(k.q.q0 + nd) * a.Hq + h * a.G + (gr - nd * a.G)) * D) + cc);
+                        if (a.sign < 0) w.x ^= 0x80008000u, w.y ^= 0x80008000u, w.z ^= 0x80008000u, w.w ^= 0x80008000u;
+                        st_shared_v4(base + X * C::TILE + (cc >> 3) * kTrHalf + r * 128 + (((cc & 7) ^ (r & 7)) << 4), w.x, w.y,
+                                     w.z, w.w);
+                    }
+                    fence_proxy_async_smem();
+                }
+                tc_fence_before();
+                // (a stream without steps is not waited for: it would run ahead)
+                const int N = two ? 2 * nt : nt;
+                if (X < N) mbar_arrive(bar(C::Q_READY + X));
+                float m = -INFINITY, l = 0.f;      // maximum of s (not yet scaled), sum
+#pragma unroll 1
+                for (int i = X; i < N; i += 2, ++sx) {
+                    const int t = two ? i >> 1 : i, p0 = (k.t0 + t) * kTrTile;
+                    // what of the tile this row sees, before S is there
+                    uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
+                    const bool nodes = p0 + kTrTile > c;
+                    if (nodes) {
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            const int s = p0 - c + 32 * w;
+                            if (s > -32) seen[w] = live ? tr_seen(a, k.q.q0 + node, node, s) : 0u;
+                        }
+                    }
+                    wait(bar(C::S_FULL + X), sx & 1);
+                    tc_fence_after();
+                    uint32_t r[128];
+#pragma unroll
+                    for (int ch = 0; ch < 4; ++ch) tmem_ld32(s_addr + ch * 32, *reinterpret_cast<uint32_t(*)[32]>(&r[ch * 32]));
+                    const uint4 valid = meta[(kseq + t) % kTrMeta];
+                    const bool masked = nodes || (valid.x & valid.y & valid.z & valid.w) != ~0u;
+                    tmem_wait_ld();
+                    if (masked) {
+                        seen[0] &= valid.x, seen[1] &= valid.y, seen[2] &= valid.z, seen[3] &= valid.w;
+#pragma unroll
+                        for (int j = 0; j < 128; ++j)
+                            if (!(seen[j >> 5] >> (j & 31) & 1u)) r[j] = __float_as_uint(-INFINITY);
+                    }
+                    float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+#pragma unroll
+                    for (int j = 0; j < 128; j += 8) {
+                        mx0 = max3(mx0, __uint_as_float(r[j]), __uint_as_float(r[j + 1]));
+                        mx1 = max3(mx1, __uint_as_float(r[j + 2]), __uint_as_float(r[j + 3]));
+                        mx2 = max3(mx2, __uint_as_float(r[j + 4]), __uint_as_float(r[j + 5]));
+                        mx3 = max3(mx3, __uint_as_float(r[j + 6]), __uint_as_float(r[j + 7]));
+                    }
+                    const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
+                    bool rescale = false;
+                    float m_new = m;
+                    if (mx > m && (m == -INFINITY || (mx - m) * sl2 > 8.f)) {
+                        rescale = m != -INFINITY;
+                        m_new = mx;
+                    }
+                    const float alpha = rescale ? tr_ex2((m - m_new) * sl2) : 1.f;
+                    m = m_new;
+                    const float mb = m == -INFINITY ? 0.f : m * sl2;
+                    const uint64_t nmb2 = f32x2_pack(-mb, -mb), sl22 = f32x2_pack(sl2, sl2);
+                    uint64_t sum2 = f32x2_pack(0.f, 0.f);
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) {
+                        uint32_t pk[32];
+#pragma unroll
+                        for (int j = 0; j < 64; j += 2) {
+                            const uint64_t x = fma_f32x2(
+                                f32x2_pack(__uint_as_float(r[hh * 64 + j]), __uint_as_float(r[hh * 64 + j + 1])), sl22, nmb2);
+                            const float v0 = tr_ex2(f32x2_lo(x)), v1 = tr_ex2(f32x2_hi(x));
+                            sum2 = add_f32x2(sum2, f32x2_pack(v0, v1));
+                            pk[j / 2] = pack_bf16x2(v0, v1);
+                        }
+                        tmem_st32(s_addr + hh * 32, pk);
+                    }
+                    l = l * alpha + (f32x2_lo(sum2) + f32x2_hi(sum2));
+                    // O is stable here: S(i) completing implies that the stream's product before it did
+                    if (i >= 2 && __any_sync(0xffffffffu, rescale)) {
+#pragma unroll
+                        for (int ch = 0; ch < D / 32; ++ch) {
+                            uint32_t o[32];
+                            tmem_ld32(tmem + lane_base + C::ColO + X * D + ch * 32, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+                            tmem_st32(tmem + lane_base + C::ColO + X * D + ch * 32, o);
+                        }
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(bar(C::P_READY + X));
+                }
+                kseq += nt;
+                // ---- the piece ends
+                if (X < N) wait(bar(C::O_FULL + X), ox & 1), ++ox;
+                tc_fence_after();
+                float m2 = m == -INFINITY ? -INFINITY : m * sl2, fa = 1.f, fb = 0.f;
+                const bool join = !two && N > 1;   // stream B's part of the same rows
+                if (join) {
+                    if (X == 1) s_ml[row] = make_float2(m2, l);
+                    named_bar_sync(1, 256);
+                    if (X == 0) {
+                        const float2 b = s_ml[row];
+                        const float mm = fmaxf(m2, b.x), mz = mm == -INFINITY ? 0.f : mm;
+                        fa = tr_ex2(m2 - mz);
+                        fb = tr_ex2(b.x - mz);
+                        l = l * fa + b.y * fb;
+                        m2 = mm;
+                    }
+                }
+                if (two || X == 0) {
+                    const bool whole = k.t0 == 0 && k.t1 == k.kt;
+                    const bool wild = *(volatile int *)&s_wild[piece & 3];
+                    const float inv = l != 0.f ? 1.f / l : 0.f;
+                    const int64_t part = (int64_t)(2 * unit + (k.first ? 0 : 1)) * kTrPair + mine;
+#pragma unroll 1
+                    for (int ch = 0; ch < D / 32; ++ch) {
+                        uint32_t ob[32];
+                        float o[32];
+                        tmem_ld32(tmem + lane_base + C::ColO + X * D + ch * 32, ob);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = __uint_as_float(ob[j]);
+                        if (join) {
+                            tmem_ld32(tmem + lane_base + C::ColO + D + ch * 32, ob);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) o[j] = o[j] * fa + __uint_as_float(ob[j]) * fb;
+                        }
+                        if (wild && live) {
+                            float x[32];           // (a copy, so that o stays in registers)
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) x[j] = o[j];
+                            tr_wild_rows<D>(a, k.q, k.t0, k.t1, h, node, h * a.G + g, m2 == -INFINITY ? 0.f : m2, ch * 32, x);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) o[j] = x[j];
+                        }
+                        if (live && !bad && whole) {
+#pragma unroll
+                            for (int j = 0; j < 32; j += 8) {
+                                uint32_t p[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) p[e] = l != 0.f ? pack_bf16x2(o[j + 2 * e] * inv, o[j + 2 * e + 1] * inv) : 0u;
+                                *reinterpret_cast<uint4 *>(a.out + out_row + ch * 32 + j) = make_uint4(p[0], p[1], p[2], p[3]);
+                            }
+                        } else if (live && !bad) {
+#pragma unroll
+                            for (int j = 0; j < 32; j += 4)
+                                *reinterpret_cast<float4 *>(a.o_part + part * D + ch * 32 + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                        }
+                        __syncwarp();
+                    }
+                    if (!whole && live && !bad) *reinterpret_cast<float2 *>(a.ml_part + part * 2) = make_float2(m2, l);
+                    tc_fence_before();
+                }
+                ++piece;
+            }
+        }
+    }
+    __syncthreads();
+    if (warp == 10) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTrTmemCols);
+    }
+}
+
+// ------------------------------------------------------------------ merge
+// The rows of segments that several units worked on: a warp per (node, query
+// head), its pieces in order.  The plan is made while the first kernel ends.
+constexpr int kTrMergeThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kTrMergeThreads) tree_merge_kernel(const __grid_constant__ TreeArgs a)
+{
+    constexpr int LPR = D / 4, RPW = 32 / LPR;         // lanes of a row, rows of a warp
+    extern __shared__ int s_pref[];                    // [R + 1] first tiles, [R] first rows of q
+    __shared__ int s_w[kTrMergeThreads / 32];
+    int *s_q0 = s_pref + a.R + 1;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    {
+        const int per = (a.R + kTrMergeThreads - 1) / kTrMergeThreads, lo = min(a.R, tid * per), hi = min(a.R, lo + per);
+        int run = 0, b;
+#pragma unroll 1
+        for (int r = lo; r < hi; ++r) {
+            const TrReq q = tr_request(a, r, b);
+            s_pref[r] = run;
+            s_q0[r] = q.q0;
+            run += tr_tiles(a, q);
+        }
+        int incl = run;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) s_w[warp] = incl;
+        __syncthreads();
+        int before = incl - run;
+#pragma unroll 1
+        for (int w = 0; w < warp; ++w) before += s_w[w];
+#pragma unroll 1
+        for (int r = lo; r < hi; ++r) s_pref[r] += before;
+        if (tid == kTrMergeThreads - 1) s_pref[a.R] = before + run;
+    }
+    __syncthreads();
+    pdl_wait();
+    pdl_launch_dependents();
+    const int total = s_pref[a.R], W = (total + a.ranges - 1) / a.ranges;
+    if (total == 0) return;
+    const int sub = lane / LPR, c4 = lane % LPR;
+    const int64_t rows = (int64_t)a.T * a.Hq;
+#pragma unroll 1
+    for (int64_t w = ((int64_t)blockIdx.x * (kTrMergeThreads / 32) + warp) * RPW + sub; w < rows;
+         w += (int64_t)gridDim.x * (kTrMergeThreads / 32) * RPW) {
+        const int t = (int)(w / a.Hq), hq = (int)(w - (int64_t)t * a.Hq), h = hq / a.G;
+        // the last request that starts at or in front of t and has nodes
+        int lo = 0, hi = a.R;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (s_q0[mid] <= t) lo = mid; else hi = mid;
+        }
+        const int tiles = s_pref[lo + 1] - s_pref[lo];
+        int b;
+        const TrReq q = tr_request(a, lo, b);
+        if (tiles == 0 || t < q.q0 || t >= q.q0 + q.n) continue;
+        const int64_t at = (int64_t)(t - q.q0) * a.G + (hq - h * a.G);
+        const int kt = tr_ktiles(q.L), pair = (int)(at / kTrPair), S = s_pref[lo] + pair * kt;
+        const int i0 = S / W, i1 = (S + kt - 1) / W;
+        if (i0 == i1) continue;
+        const int row = (int)(at - (int64_t)pair * kTrPair);
+        auto part = [&](int i) { return (int64_t)(2 * (i * a.Hkv + h) + (i == i0 && S > i0 * W ? 1 : 0)) * kTrPair + row; };
+        float M = -INFINITY, L = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int i = i0; i <= i1; i += 8) {
+            float2 ml[8];
+            float4 v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (i + e <= i1) {
+                    const int64_t p = part(i + e);
+                    ml[e] = __ldcg(reinterpret_cast<const float2 *>(a.ml_part + p * 2));
+                    v[e] = __ldcg(reinterpret_cast<const float4 *>(a.o_part + p * D) + c4);
+                }
+            float mn = M;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (i + e <= i1) mn = fmaxf(mn, ml[e].x);
+            const float mz = mn == -INFINITY ? 0.f : mn, f = tr_ex2(M - mz);
+            o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+            L *= f;
+            M = mn;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (i + e <= i1) {
+                    const float x = tr_ex2(ml[e].x - mz);
+                    L = fmaf(x, ml[e].y, L);
+                    o.x = fmaf(x, v[e].x, o.x);
+                    o.y = fmaf(x, v[e].y, o.y);
+                    o.z = fmaf(x, v[e].z, o.z);
+                    o.w = fmaf(x, v[e].w, o.w);
+                }
+        }
+        const float inv = L != 0.f ? 1.f / L : 0.f;
+        const uint2 y = L != 0.f ? make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv)) : make_uint2(0u, 0u);
+        *reinterpret_cast<uint2 *>(a.out + w * D + c4 * 4) = y;
+    }
+}
 
 template <int D, bool E8>
 __device__ __forceinline__ void load_row(const uint8_t *rows, const uint8_t *exps, int64_t slot, int Hkv, int h, int shift,
@@ -47,7 +894,7 @@ __device__ __forceinline__ void load_row(const uint8_t *rows, const uint8_t *exp
 }
 
 template <int D, bool E8>
-__global__ void __launch_bounds__(256) tree_attn_kernel(const TreeArgs a)
+__global__ void __launch_bounds__(256) tree_attn_simple_kernel(const TreeArgs a)
 {
     constexpr int N = D / 32;
     pdl_wait();
@@ -107,6 +954,58 @@ __global__ void __launch_bounds__(256) tree_attn_kernel(const TreeArgs a)
     }
 }
 
+
+// --------------------------------------------------------------- host side
+// Workspace: header, then two slots of partials per unit that shares segments.
+struct TrWs {
+    size_t ml_off, o_off, total;
+};
+static TrWs tr_ws(int D)
+{
+    TrWs w;
+    w.ml_off = kWorkspaceHeader;
+    w.o_off = align_up(w.ml_off + (size_t)2 * kTrMaxUnits * kTrPair * 8, 256);
+    w.total = w.o_off + (size_t)2 * kTrMaxUnits * kTrPair * D * 4;
+    return w;
+}
+
+// Ranges per kv head: a unit per CTA, or two where that leaves fewer CTAs without one.
+static int tr_ranges(int grid, int Hkv)
+{
+    const int r1 = grid / Hkv, r2 = 2 * grid / Hkv;
+    if (r1 < 1) return 1;
+    return r2 * Hkv > 2 * r1 * Hkv + grid / 16 ? r2 : r1;
+}
+
+template <int D>
+static pa_status tr_launch(const TreeArgs &a, cudaStream_t st)
+{
+    auto kern = tree_attn_kernel<D>;
+    if (!ensure_dynamic_smem(reinterpret_cast<const void *>(kern), TrCfg<D>::Smem)) return PA_ERR_CUDA;
+    const int grid = num_sms() < kTrMaxCtas ? num_sms() : kTrMaxCtas;
+    TreeArgs b = a;
+    b.ranges = tr_ranges(grid, a.Hkv);
+    if (launch_kernel(kern, dim3(grid), dim3(kTrThreads), TrCfg<D>::Smem, st, b) != cudaSuccess) return PA_ERR_CUDA;
+    if (b.ranges > 1) {
+        // behind this call's own kernel, whose end it waits for: overlapped whatever the mode
+        auto merge = tree_merge_kernel<D>;
+        const size_t smem = ((size_t)2 * a.R + 1) * 4;
+        const int64_t want = ((int64_t)a.T * a.Hq * (D / 4) + kTrMergeThreads - 1) / kTrMergeThreads;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(want < 4 * grid ? want : 4 * grid));
+        cfg.blockDim = dim3(kTrMergeThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = st;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaLaunchKernelEx(&cfg, merge, b) != cudaSuccess) return PA_ERR_CUDA;
+    }
+    return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
 }  // namespace pa
 
 using namespace pa;
@@ -114,7 +1013,7 @@ using namespace pa;
 extern "C" size_t pa_tree_workspace_bytes(int n_q_heads, int n_kv_heads, int head_dim)
 {
     if (n_q_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0 || n_q_heads % n_kv_heads != 0) return 0;
-    return kWorkspaceHeader;
+    return tr_ws(head_dim).total;
 }
 
 extern "C" pa_status pa_paged_tree_attn(const void *q, int n_tokens, int n_q_heads, const void *k_buf, const void *v_buf,
@@ -147,7 +1046,24 @@ extern "C" pa_status pa_paged_tree_attn(const void *q, int n_tokens, int n_q_hea
     if (!aligned16(q) || !aligned16(k_buf) || !aligned16(v_buf) || !aligned16(out) || !aligned4(qo_indptr) ||
         !aligned4(req_to_token) || !aligned4(req_pool_indices) || !aligned4(seq_lens) || !aligned4(tree_mask))
         return PA_ERR_ALIGN;
-    TreeArgs a{};
+    TreeArgs a;
+    memset(&a, 0, sizeof a);
+    const int row_bytes = s.head_dim * (e4m3 ? 1 : 2), sw = row_bytes < 128 ? row_bytes : 128;
+    const cuuint64_t inner = (cuuint64_t)s.n_kv_heads * s.head_dim, rows = (cuuint64_t)s.n_layers * s.size;
+    const cuuint32_t box = sw / (e4m3 ? 1 : 2);
+    if (!encode_tmap_rows(&a.tm_k16, k_buf, !e4m3, inner, rows, box, 16, sw) ||
+        !encode_tmap_rows(&a.tm_k1, k_buf, !e4m3, inner, rows, box, 1, sw) ||
+        !encode_tmap_rows(&a.tm_v16, v_buf, !e4m3, inner, rows, box, 16, sw) ||
+        !encode_tmap_rows(&a.tm_v1, v_buf, !e4m3, inner, rows, box, 1, sw))
+        return PA_ERR_CUDA;
+    const TrWs ws = tr_ws(s.head_dim);
+    unsigned char *wp = static_cast<unsigned char *>(workspace);
+    a.ml_part = reinterpret_cast<float *>(wp + ws.ml_off);
+    a.o_part = reinterpret_cast<float *>(wp + ws.o_off);
+    a.layer_row0 = layer_id * s.size;
+    a.total_rows = s.n_layers * s.size;
+    a.early_meta = early_metadata();
+    a.wait_ns = wait_limit_ns();
     const int64_t layer = (int64_t)layer_id * s.size * s.n_kv_heads * s.head_dim * (e4m3 ? 1 : 2);
     a.q = static_cast<const __nv_bfloat16 *>(q);
     a.k = static_cast<const uint8_t *>(k_buf) + layer;
@@ -174,13 +1090,17 @@ extern "C" pa_status pa_paged_tree_attn(const void *q, int n_tokens, int n_q_hea
     a.size = s.size;
     a.req_rows = req_rows;
     a.max_ctx = max_ctx;
+    a.scale_log2 = (float)(fabs((double)scale) * 1.4426950408889634);
+    a.sign = scale < 0.f ? -1 : 1;
+    if (a.scale_log2 == 0.f) {
+        a.scale_log2 = 1.f;      // q is taken as 0
+        a.sign = 0;
+    }
+    if (!e4m3) return s.head_dim == 64 ? tr_launch<64>(a, st) : tr_launch<128>(a, st);
     a.scale_log2 = (float)((double)scale * 1.4426950408889634);
     const dim3 grid(256, n_reqs);
-    cudaError_t rc;
-    if (e4m3) rc = s.head_dim == 64 ? launch_kernel(tree_attn_kernel<64, true>, grid, dim3(256), 0, st, a)
-                                    : launch_kernel(tree_attn_kernel<128, true>, grid, dim3(256), 0, st, a);
-    else rc = s.head_dim == 64 ? launch_kernel(tree_attn_kernel<64, false>, grid, dim3(256), 0, st, a)
-                               : launch_kernel(tree_attn_kernel<128, false>, grid, dim3(256), 0, st, a);
+    const cudaError_t rc = s.head_dim == 64 ? launch_kernel(tree_attn_simple_kernel<64, true>, grid, dim3(256), 0, st, a)
+                                            : launch_kernel(tree_attn_simple_kernel<128, true>, grid, dim3(256), 0, st, a);
     if (rc != cudaSuccess) return PA_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
