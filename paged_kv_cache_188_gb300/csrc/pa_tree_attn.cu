@@ -32,7 +32,7 @@
 //                  grows by more than 2^8
 // Warps 0-7: softmax, one row a thread; 8 and 9: K and V copies through the page
 // table (16 consecutive slots are one TMA box, any other four rows one gather4
-// copy); 10: the products.
+// copy); 10 and 11: a stream's products each.
 //
 // Hidden rows: a hidden token's weight is 0, but 0 times a NaN or an infinity in
 // its V row would reach every node.  Only drafted tokens are ever hidden (context
@@ -50,8 +50,8 @@ using namespace sm100;
 
 constexpr int kTreeMaxReqs = 4096;
 constexpr int kTrTile = 128;             // tokens of a tile, rows of a stream
-constexpr int kTrPair = 256;             // rows that share a token tile
-constexpr int kTrThreads = 352;
+constexpr int kTrPair = 256;             // rows of two streams
+constexpr int kTrThreads = 384;
 constexpr int kTrHalf = 128 * 128;       // 128 rows of 64 bf16, 128-byte swizzle
 constexpr int kTrMeta = 8;               // tiles whose valid positions are kept: see tr_copy
 constexpr int kTrMaxCtas = 160;
@@ -59,6 +59,7 @@ constexpr int kTrMaxUnits = 2 * kTrMaxCtas;   // units that share segments
 constexpr uint32_t kTrTmemCols = 512;    // S_A | S_B | O_A | O_B
 
 struct TreeArgs {
+    CUtensorMap tm_q;                            // 3-D (element, head, token): boxes of 64 x G x TQ
     CUtensorMap tm_k16, tm_k1, tm_v16, tm_v1;    // 2-D (element, row): boxes of 16 rows, and one row (gather4)
     const __nv_bfloat16 *q;
     const uint8_t *k, *v;                        // the layer's rows
@@ -67,19 +68,22 @@ struct TreeArgs {
     __nv_bfloat16 *out;
     int32_t *err;
     float *ml_part;                              // [2 units][256][2]: maximum (log2 units), sum
-    float *o_part;                               // [2 units][256][D]: relative to that maximum
+    float *o_part;                               // [2 units][D / 4][256][4]: relative to that maximum
     int T, R, Hq, Hkv, G, size, req_rows, max_ctx, mask_words, block_shift, layer_row0, total_rows, early_meta;
     int ranges;                                  // per kv head
     uint64_t wait_ns;
     float scale_log2;                            // of the scale's magnitude; its sign goes into q
     int sign;                                    // of the scale: -1, 0, 1
+    int tq;                                      // nodes of a stream's tile of rows: 128 / G
+    int inv_g;                                   // 65536 / G + 1: x / G = x inv_g >> 16 for x below 272
 };
 
 // ------------------------------------------------------------------- plan
-struct TrReq {
-    int q0, n, L, row;      // n = 0: nothing to do; L = 0: zeros
+struct alignas(16) TrReq {
+    int q0, n, L, row;      // n = 0: nothing to do
 };
-__device__ __forceinline__ TrReq tr_request(const TreeArgs &a, int r, int &bits)
+// A request, and what is wrong with it: `zeros` where its rows become zeros.
+__device__ __forceinline__ TrReq tr_request(const TreeArgs &a, int r, int &bits, bool &zeros)
 {
     TrReq q;
     q.q0 = __ldg(a.qo_indptr + r);
@@ -88,73 +92,106 @@ __device__ __forceinline__ TrReq tr_request(const TreeArgs &a, int r, int &bits)
     q.row = __ldg(a.req_pool_indices + r);
     q.n = q1 - q.q0;
     bits = 0;
+    zeros = false;
     if (q1 <= q.q0 || q.q0 < 0 || q1 > a.T) {
         if (q1 != q.q0) bits = PA_DEVERR_LEN;
-        q.n = q.L = 0;
+        q.n = 0;
         return q;
     }
     if (q.row < 0 || q.row >= a.req_rows) bits |= PA_DEVERR_ROW;
     if (q.L < q.n || q.L > a.max_ctx || (a.tree_mask && q.n > 32 * (int64_t)a.mask_words)) bits |= PA_DEVERR_LEN;
-    if (bits) q.L = q.row = 0;
+    zeros = bits != 0;
     return q;
 }
-__device__ __forceinline__ int tr_pairs(const TreeArgs &a, int n) { return (int)(((int64_t)n * a.G + kTrPair - 1) / kTrPair); }
-__device__ __forceinline__ int tr_ktiles(int L) { return L > 0 ? (L + kTrTile - 1) / kTrTile : 1; }
+__device__ __forceinline__ TrReq tr_request(const TreeArgs &a, int r)
+{
+    int bits;
+    bool zeros;
+    TrReq q = tr_request(a, r, bits, zeros);
+    if (zeros) q.n = 0;
+    return q;
+}
+__device__ __forceinline__ int tr_pairs(const TreeArgs &a, int n) { return n <= 2 * a.tq ? 1 : (n + 2 * a.tq - 1) / (2 * a.tq); }
+__device__ __forceinline__ int tr_ktiles(int L) { return (L + kTrTile - 1) / kTrTile; }
 __device__ __forceinline__ int tr_tiles(const TreeArgs &a, const TrReq &q) { return q.n > 0 ? tr_pairs(a, q.n) * tr_ktiles(q.L) : 0; }
 
-// A warp's walk over the pieces of a unit's range: tiles [x, xe) of the segments laid end to end.
+// A warp's walk over the pieces of its CTA's units (blockIdx, + grid, ...): range i = unit / Hkv is the tiles [i W,
+// (i + 1) W) of the segments laid end to end.
+constexpr int kTrWindow = 8;            // requests at the start of a range that the plan leaves in shared memory
+struct TrPlan {
+    int total, W;
+    int start[2][2];        // (request, its first tile) where the CTA's units start (a third unit exists only where all
+                            // of them are the whole of one kv head)
+    TrReq win[2][kTrWindow];    // requests from there on
+};
 struct TrWalk {
-    int x, xe, r, S0;       // next tile, end; request and its first tile
-    int w0;                 // the lanes hold requests w0 + lane
+    int unit, u, h;         // unit, its number in the CTA, kv head
+    int x, xe, x0, r, S0;   // next tile, end, start of the range; request and its first tile
+    int w0;                 // past the window: the lanes hold requests w0 + lane
     TrReq w;
-    // the piece: token tiles [t0, t1) of rows 256 pair .. of request r
+    // the piece: token tiles [t0, t1) of nodes 2 tq pair .. of request q
     TrReq q;
     int kt, pair, t0, t1, first;    // kt: the request's tiles; first: the piece starts the range
-    int x0;
 };
-__device__ __forceinline__ void tr_begin(TrWalk &k, int x, int xe, int r, int S0)
+__device__ __forceinline__ void tr_unit(const TreeArgs &a, const TrPlan &p, TrWalk &k)
 {
-    k.x = k.x0 = x;
-    k.xe = xe;
-    k.r = r;
-    k.S0 = S0;
+    const int i = k.unit / a.Hkv, v = a.ranges > 1 ? k.u : 0;
+    k.h = k.unit - i * a.Hkv;
+    k.x = k.x0 = (int)min((int64_t)p.total, (int64_t)i * p.W);
+    k.xe = min(p.total, k.x + p.W);
+    k.r = p.start[v][0];
+    k.S0 = p.start[v][1];
     k.w0 = -64;
 }
-__device__ __forceinline__ bool tr_next(const TreeArgs &a, TrWalk &k, int lane)
+__device__ __forceinline__ void tr_begin(const TreeArgs &a, const TrPlan &p, TrWalk &k)
 {
-    if (k.x >= k.xe) return false;
-    while (true) {
-        if (k.r - k.w0 >= 32) {
-            k.w0 = k.r;
-            int bits;
-            k.w = TrReq{0, 0, 0, 0};
-            if (k.r + lane < a.R) k.w = tr_request(a, k.r + lane, bits);
-        }
-        const int i = k.r - k.w0;
-        k.q.q0 = __shfl_sync(0xffffffffu, k.w.q0, i);
-        k.q.n = __shfl_sync(0xffffffffu, k.w.n, i);
-        k.q.L = __shfl_sync(0xffffffffu, k.w.L, i);
-        k.q.row = __shfl_sync(0xffffffffu, k.w.row, i);
-        const int tiles = tr_tiles(a, k.q);
-        if (k.x < k.S0 + tiles || k.r >= a.R) break;
-        k.S0 += tiles;
-        ++k.r;
+    k.unit = blockIdx.x;
+    k.u = 0;
+    k.x = k.xe = 0;
+    if (k.unit < a.ranges * a.Hkv) tr_unit(a, p, k);
+}
+__device__ __forceinline__ bool tr_next(const TreeArgs &a, const TrPlan &p, TrWalk &k, int lane)
+{
+    while (k.x >= k.xe) {
+        k.unit += gridDim.x;
+        ++k.u;
+        if (k.unit >= a.ranges * a.Hkv) return false;
+        tr_unit(a, p, k);
     }
-    if (k.r >= a.R) return false;
+    const int v = a.ranges > 1 ? k.u : 0, r0 = p.start[v][0];
+    int tiles;
+#pragma unroll 1
+    while (true) {
+        if (k.r - r0 < kTrWindow) {
+            k.q = p.win[v][k.r - r0];
+        } else {
+            if (k.r - k.w0 >= 32) {
+                k.w0 = k.r;
+                k.w = TrReq{0, 0, 0, 0};
+                if (k.r + lane < a.R) k.w = tr_request(a, k.r + lane);
+            }
+            const int i = k.r - k.w0;
+            k.q.q0 = __shfl_sync(0xffffffffu, k.w.q0, i);
+            k.q.n = __shfl_sync(0xffffffffu, k.w.n, i);
+            k.q.L = __shfl_sync(0xffffffffu, k.w.L, i);
+            k.q.row = __shfl_sync(0xffffffffu, k.w.row, i);
+        }
+        tiles = tr_tiles(a, k.q);
+        if (k.x < k.S0 + tiles) break;
+        k.S0 += tiles;
+        if (++k.r >= a.R) return false;      // (not reached: x lies below the total)
+    }
     k.kt = tr_ktiles(k.q.L);
     const int off = k.x - k.S0;
-    k.pair = off / k.kt;
+    k.pair = tiles == k.kt ? 0 : off / k.kt;
     k.t0 = off - k.pair * k.kt;
     k.t1 = min(k.kt, k.t0 + k.xe - k.x);
     k.first = k.x == k.x0;
     k.x += k.t1 - k.t0;
     return true;
 }
-// rows of the piece, and its steps: a token tile is one step of each stream, or of one of them in turn
-__device__ __forceinline__ int tr_rows(const TreeArgs &a, const TrWalk &k)
-{
-    return (int)min((int64_t)kTrPair, (int64_t)k.q.n * a.G - (int64_t)k.pair * kTrPair);
-}
+// the piece has rows for both streams
+__device__ __forceinline__ bool tr_two(const TreeArgs &a, const TrWalk &k) { return k.q.n - 2 * a.tq * k.pair > a.tq; }
 
 // 32 bits of what node i (row `qrow` of the mask) sees, from node s on (s < 0: context, all ones)
 __device__ __forceinline__ uint32_t tr_seen(const TreeArgs &a, int64_t qrow, int i, int s)
@@ -179,7 +216,7 @@ struct TrCfg {
     static constexpr int OffV = OffK + NK * TILE;
     static constexpr int OffBar = OffV + NV * TILE;
     enum { K_FULL, K_EMPTY = K_FULL + NK, V_FULL = K_EMPTY + NK, V_EMPTY = V_FULL + NV, S_FULL = V_EMPTY + NV,
-           P_READY = S_FULL + 2, O_FULL = P_READY + 2, Q_READY = O_FULL + 2, DRAIN = Q_READY + 2, N_BARS };
+           P_READY = S_FULL + 2, O_FULL = P_READY + 2, O_FREE = O_FULL + 2, Q_FULL = O_FREE + 2, DRAIN = Q_FULL + 2, JOINT = DRAIN + 2, N_BARS };   // JOINT: stream A's Q, for stream B
     static constexpr int OffMeta = (OffBar + N_BARS * 8 + 15) & ~15;     // uint4 [kTrMeta]: valid positions
     static constexpr int OffML = OffMeta + kTrMeta * 16;                 // float2 [128]: stream B's (m, l)
     static constexpr int OffEnd = OffML + 128 * 8;
@@ -203,23 +240,21 @@ __device__ __forceinline__ float tr_ex2(float x)
 // a ring of its own, because softmax reads them behind S, when the K stage is
 // already free.  (Tile x is copied when S(x - NK) is done, which was issued behind
 // softmax of tile x - NK - 1 at the latest.)
-template <int D, typename Begin>
-__device__ __forceinline__ void tr_copy(const TreeArgs &a, const Begin &begin, bool isv, uint32_t ring, uint32_t full,
+template <int D>
+__device__ __forceinline__ void tr_copy(const TreeArgs &a, const TrPlan &plan, bool isv, uint32_t ring, uint32_t full,
                                         uint32_t empty, uint4 *meta, volatile int *s_abort, int lane)
 {
     using C = TrCfg<D>;
-    const int stages = isv ? C::NV : C::NK, units = a.ranges * a.Hkv;
+    const int stages = isv ? C::NV : C::NK;
     const CUtensorMap *m16 = isv ? &a.tm_v16 : &a.tm_k16, *m1 = isv ? &a.tm_v1 : &a.tm_k1;
     int st = 0, seq = 0, errs = 0;
     uint32_t ph = 0;
     bool go = true;
+    TrWalk k;
+    tr_begin(a, plan, k);
 #pragma unroll 1
-    for (int unit = blockIdx.x, u = 0; unit < units && go; unit += gridDim.x, ++u) {
-        TrWalk k;
-        begin(k, unit, u);
-        const int col = unit % a.Hkv * D;
-        while (go && tr_next(a, k, lane)) {
-            if (k.q.L == 0) continue;
+        while (go && tr_next(a, plan, k, lane)) {
+            const int col = k.h * D;
             const int32_t *tab = a.req_to_token + (int64_t)k.q.row * a.max_ctx;
             int nx[4];
             auto fetch = [&](int t) {
@@ -292,7 +327,6 @@ __device__ __forceinline__ void tr_copy(const TreeArgs &a, const Begin &begin, b
                 }
             }
         }
-    }
     // the warp leaves only when its copies have landed, whether or not anyone has given up by now
 #pragma unroll 1
     for (int j = max(0, seq - stages); j < seq; ++j) mbar_drain(full + (j % stages) * 8, (j / stages) & 1);
@@ -373,9 +407,10 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
     using C = TrCfg<D>;
     extern __shared__ unsigned char smem_raw[];
     __shared__ int s_w[kTrThreads / 32];
-    __shared__ int s_abort_storage, s_total;
-    __shared__ int s_start[2][2];              // (request, its first tile) at the start of the CTA's units
-    __shared__ int s_wild[4];                  // per piece, modulo 4: a V row was taken out
+    __shared__ int s_abort_storage;
+    __shared__ TrPlan plan;
+    __shared__ int s_wild[2][8];               // per stream, at piece % 8: piece + 1 where a V row was taken out (the
+                                               // rings keep the streams within 8 pieces of one another)
     __shared__ uint32_t s_tmem;
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     unsigned char *sb = smem_raw + (base - raw);
@@ -386,14 +421,16 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid < C::N_BARS) {
-        const bool softmax = (tid >= C::P_READY && tid < C::P_READY + 2) || (tid >= C::Q_READY && tid < C::Q_READY + 2);
-        mbar_init(bar(tid), softmax ? 128u : 1u);
+        const bool softmax = (tid >= C::P_READY && tid < C::O_FULL) || (tid >= C::O_FREE && tid < C::Q_FULL);
+        const bool empty = (tid >= C::K_EMPTY && tid < C::V_FULL) || (tid >= C::V_EMPTY && tid < C::S_FULL);
+        mbar_init(bar(tid), softmax ? 128u : empty ? 2u : 1u);
     }
-    static_assert(C::N_BARS <= 32, "one warp initialises the barriers");
-    if (warp == 0) fence_mbar_init();
+    static_assert(C::N_BARS <= 64, "two warps initialise the barriers");
+    if (warp < 2) fence_mbar_init();
+    if (tid >= 64 && tid < 80) s_wild[(tid >> 3) & 1][tid & 7] = 0;
     if (tid == 0) {
         s_abort_storage = 0;
-        s_wild[0] = s_wild[1] = s_wild[2] = s_wild[3] = 0;
+        plan.start[0][0] = plan.start[0][1] = plan.start[1][0] = plan.start[1][1] = 0;
     }
     if (warp == 10) tmem_alloc(smem_u32(&s_tmem), kTrTmemCols);
     if (warp == 8 && lane == 0) {
@@ -406,16 +443,23 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
     }
     if (!a.early_meta) pdl_wait();
 
+    if (warp == 4 && lane == 0) prefetch_tmap(&a.tm_q);
     // ---- plan: the segments' tiles in all, and where this CTA's units start
-    const int units = a.ranges * a.Hkv;
     int bits = 0;
+    bool zeros = false;
     {
         const int per = (a.R + kTrThreads - 1) / kTrThreads, lo = min(a.R, tid * per), hi = min(a.R, lo + per);
-        int run = 0, b;
+        int run = 0;
+        TrReq q;                               // the thread's last request
 #pragma unroll 1
         for (int r = lo; r < hi; ++r) {
-            run += tr_tiles(a, tr_request(a, r, b));
+            int b;
+            bool z;
+            q = tr_request(a, r, b, z);
+            if (z) q.n = 0;
+            run += tr_tiles(a, q);
             bits |= b;
+            zeros |= z;
         }
         int incl = run;
 #pragma unroll
@@ -424,16 +468,20 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
             if (lane >= o) incl += v;
         }
         if (lane == 31) s_w[warp] = incl;
-        __syncthreads();
-        int before = incl - run;
-        int total = 0;
-#pragma unroll 1
+        zeros = __syncthreads_or(zeros);
+        int before = incl - run, total = 0, sums[kTrThreads / 32];
+#pragma unroll
+        for (int w = 0; w < kTrThreads / 32; ++w) sums[w] = s_w[w];
+#pragma unroll
         for (int w = 0; w < kTrThreads / 32; ++w) {
-            if (w < warp) before += s_w[w];
-            total += s_w[w];
+            if (w < warp) before += sums[w];
+            total += sums[w];
         }
-        if (tid == 0) s_total = total;
         const int W = (total + a.ranges - 1) / a.ranges;
+        if (tid == 0) {
+            plan.total = total;
+            plan.W = W;
+        }
         if (a.ranges > 1 && run > 0) {
 #pragma unroll 1
             for (int u = 0; u < 2; ++u) {
@@ -441,14 +489,21 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
                 if (x < before || x >= before + run) continue;
                 int S0 = before, r = lo;
 #pragma unroll 1
-                for (; r < hi; ++r) {
-                    const int t = tr_tiles(a, tr_request(a, r, b));
+                for (; r < hi - 1; ++r) {
+                    const int t = tr_tiles(a, tr_request(a, r));
                     if (x < S0 + t) break;
                     S0 += t;
                 }
-                s_start[u][0] = r;
-                s_start[u][1] = S0;
+                plan.start[u][0] = r;
+                plan.start[u][1] = S0;
             }
+        }
+        __syncthreads();
+#pragma unroll 1
+        for (int u = 0; u < 2; ++u) {
+            const int r0 = plan.start[u][0];
+#pragma unroll 1
+            for (int r = max(lo, r0); r < min(hi, r0 + kTrWindow); ++r) plan.win[u][r - r0] = r == hi - 1 ? q : tr_request(a, r);
         }
     }
     if (a.early_meta) pdl_wait();
@@ -457,106 +512,111 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
-    const int total = s_total, W = (total + a.ranges - 1) / a.ranges;
-
-    // unit u of this CTA as a walk
-    auto begin = [&](TrWalk &k, int unit, int u) {
-        const int i = unit / a.Hkv;
-        tr_begin(k, (int)min((int64_t)total, (int64_t)i * W), (int)min((int64_t)total, (int64_t)(i + 1) * W),
-                 a.ranges > 1 ? s_start[u][0] : 0, a.ranges > 1 ? s_start[u][1] : 0);
-    };
+    if (zeros) {
+        // requests that cannot be read: their rows become zeros
+#pragma unroll 1
+        for (int r = blockIdx.x; r < a.R; r += gridDim.x) {
+            int b;
+            bool z;
+            const TrReq q = tr_request(a, r, b, z);
+            if (!z) continue;
+            uint4 *dst = reinterpret_cast<uint4 *>(a.out + (int64_t)q.q0 * a.Hq * D);
+            for (int64_t x = tid; x < (int64_t)q.n * a.Hq * D / 8; x += kTrThreads) dst[x] = make_uint4(0u, 0u, 0u, 0u);
+        }
+    }
 
     if (warp == 8 || warp == 9) {
         const bool isv = warp == 9;
-        tr_copy<D>(a, begin, isv, base + (isv ? C::OffV : C::OffK), bar(isv ? C::V_FULL : C::K_FULL),
+        tr_copy<D>(a, plan, isv, base + (isv ? C::OffV : C::OffK), bar(isv ? C::V_FULL : C::K_FULL),
                    bar(isv ? C::V_EMPTY : C::K_EMPTY), meta, s_abort, lane);
-    } else if (warp == 10) {
+    } else if (warp >= 10) {
         // ======================================================= products
+        // A warp per stream: while one waits for its weights, the tensor core has the other's products.
+        const int X = warp - 10;
         const uint32_t sQ = base, sK = base + C::OffK, sV = base + C::OffV;
-        int kseq = 0, vseq = 0, piece = 0, pb = 0;   // token tiles, pieces, pieces with steps of stream B before
-        int px[2] = {0, 0};                    // steps of each stream before
+        int seq = 0, piece = 0, px = 0, pq = 0, p2 = 0, pj = 0;   // token tiles, pieces before; this stream's steps, pieces; of
+                                                                  // stream B: those with rows of its own, and with A's
         bool bad = false;
         auto wait = [&](uint32_t b, uint32_t parity) {
             if (!bad) bad = !__all_sync(0xffffffffu, mbar_wait(b, parity, s_abort, a.err, PA_DEVERR_TIMEOUT, a.wait_ns));
         };
+        TrWalk k;
+        tr_begin(a, plan, k);
 #pragma unroll 1
-        for (int unit = blockIdx.x, u = 0; unit < units; unit += gridDim.x, ++u) {
-            TrWalk k;
-            begin(k, unit, u);
-            while (tr_next(a, k, lane)) {
-                if (k.q.L == 0) continue;
-                const int nt = k.t1 - k.t0, two = tr_rows(a, k) > kTrTile;
+            while (tr_next(a, plan, k, lane)) {
+                const int nt = k.t1 - k.t0, two = tr_two(a, k);
                 const int N = two ? 2 * nt : nt, c = k.q.L - k.q.n;
-                if (lane == 0) s_wild[(piece + 2) & 3] = 0;
-                wait(bar(C::Q_READY), piece & 1);
-                if (N > 1) wait(bar(C::Q_READY + 1), pb++ & 1);
-                // S(i): its K tile is waited for by the first step that reads it
-                auto tile_of = [&](int i) { return two ? i >> 1 : i; };
-                auto first_of = [&](int i) { return !two || !(i & 1); };
-                auto last_of = [&](int i) { return !two || (i & 1); };
-                auto wait_k = [&](int i) {
-                    const int s = kseq + tile_of(i);
-                    if (first_of(i)) wait(bar(C::K_FULL + s % C::NK), (s / C::NK) & 1);
+                // a ring stage is free when both streams are through with it, or twice the one that uses it
+                auto release = [&](uint32_t b) {
+                    umma_commit(b);
+                    if (!two) umma_commit(b);
                 };
-                auto qk = [&](int i) {
-                    const int st = (kseq + tile_of(i)) % C::NK, X = i & 1;
+                auto qk = [&](int st) {
                     const uint32_t q = sQ + (two ? X : 0) * C::TILE, kk = sK + st * C::TILE;
 #pragma unroll
                     for (int s = 0; s < D / 16; ++s)
                         umma_ss(tmem + X * 128, smem_desc_sw128(q + (s >> 2) * kTrHalf + (s & 3) * 32, 16, 1024),
                                 smem_desc_sw128(kk + (s >> 2) * kTrHalf + (s & 3) * 32, 16, 1024), C::kIdS, s > 0);
                     umma_commit(bar(C::S_FULL + X));
-                    if (last_of(i)) umma_commit(bar(C::K_EMPTY + st));
+                    release(bar(C::K_EMPTY + st));
                 };
-#pragma unroll 1
-                for (int i = 0; i < 2 && i < N; ++i) {
-                    wait_k(i);
+                const int dt = two ? 1 : 2;        // token tiles from one step of the stream to the next
+                if (X < N) {
+                    const int s = seq + (two ? 0 : X), st = s % C::NK;
+                    // (stream B hears of A's Q from A's warp: it does not follow every phase of that barrier)
+                    if (X == 0) {
+                        wait(bar(C::Q_FULL), piece & 1);
+                        if (!two && N > 1 && lane == 0) mbar_arrive(bar(C::JOINT));
+                    } else {
+                        wait(two ? bar(C::Q_FULL + 1) : bar(C::JOINT), (two ? p2 : pj) & 1);
+                        if (two) ++p2;
+                        else ++pj;
+                    }
+                    wait(bar(C::K_FULL + st), (s / C::NK) & 1);
                     tc_fence_after();
-                    if (!bad) if (elect_one()) qk(i);
+                    if (!bad) if (elect_one()) qk(st);
                     __syncwarp();
                 }
 #pragma unroll 1
-                for (int i = 0; i < N; ++i) {
-                    const int X = i & 1, s = vseq + tile_of(i), st = s % C::NV;
+                for (int t = two ? 0 : X; t < nt; t += dt, ++px) {
+                    const int s = seq + t, st = s % C::NV, sk = (s + dt) % C::NK;
                     const uint32_t vt = sV + st * C::TILE;
-                    if (first_of(i)) {
-                        wait(bar(C::V_FULL + st), (s / C::NV) & 1);
-                        // drafted tokens' rows must not hold what a weight of 0 does not cancel
-                        const int p0 = (k.t0 + tile_of(i)) * kTrTile, lo = max(0, c - p0), hi = min(kTrTile, k.q.L - p0);
-                        if (!bad && lo < hi && tr_tame<D>(vt, lo, hi, lane)) {
-                            if (lane == 0) *(volatile int *)&s_wild[piece & 3] = 1;
-                            __threadfence_block();
+                    wait(bar(C::V_FULL + st), (s / C::NV) & 1);
+                    // drafted tokens' rows must not hold what a weight of 0 does not cancel
+                    const int p0 = (k.t0 + t) * kTrTile, lo = max(0, c - p0), hi = min(kTrTile, k.q.L - p0);
+                    if (lo < hi) {
+                        if (X == 0 || !two) {
+                            if (!bad && tr_tame<D>(vt, lo, hi, lane)) {
+                                if (lane == 0) *(volatile int *)&s_wild[X][piece & 7] = piece + 1;
+                                __threadfence_block();
+                            }
                             __syncwarp();
                         }
+                        if (two) named_bar_sync(2, 64);
                     }
-                    wait(bar(C::P_READY + X), px[X] & 1);
-                    ++px[X];
+                    if (t + dt < nt) wait(bar(C::K_FULL + sk), ((s + dt) / C::NK) & 1);
+                    // the piece's first product overwrites O
+                    if (t < dt && pq++ > 0) wait(bar(C::O_FREE + X), pq & 1);
+                    wait(bar(C::P_READY + X), px & 1);
                     tc_fence_after();
                     if (!bad) if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < kTrTile / 16; ++kk)
                             umma_ts(tmem + C::ColO + X * D, tmem + X * 128 + kk * 8,
-                                    smem_desc_sw128(vt + kk * 2048, kTrHalf, 1024), C::kIdPV, kk > 0 || i >= 2);
-                        if (last_of(i)) umma_commit(bar(C::V_EMPTY + st));
-                        if (i + 2 >= N) umma_commit(bar(C::O_FULL + X));
+                                    smem_desc_sw128(vt + kk * 2048, kTrHalf, 1024), C::kIdPV, kk > 0 || t >= dt);
+                        release(bar(C::V_EMPTY + st));
+                        if (t + dt < nt) qk(sk);
+                        else umma_commit(bar(C::O_FULL + X));
                     }
                     __syncwarp();
-                    if (i + 2 < N) {
-                        wait_k(i + 2);
-                        tc_fence_after();
-                        if (!bad) if (elect_one()) qk(i + 2);
-                        __syncwarp();
-                    }
                 }
-                kseq += nt;
-                vseq += nt;
+                seq += nt;
                 ++piece;
             }
-        }
         // one more commit, which arrives once every product issued has completed, before tensor memory is freed
-        if (elect_one()) umma_commit(bar(C::DRAIN));
+        if (elect_one()) umma_commit(bar(C::DRAIN + X));
         __syncwarp();
-        mbar_drain(bar(C::DRAIN), 0);
+        mbar_drain(bar(C::DRAIN + X), 0);
         __syncwarp();
     } else {
         // ======================================== softmax, and the piece's end
@@ -565,57 +625,42 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
         const uint32_t s_addr = tmem + lane_base + X * 128;
         const float sl2 = a.scale_log2;
         int piece = 0, sx = 0, ox = 0, kseq = 0;   // pieces, steps, ends of this stream, token tiles
+        int qloads = 0;
         bool bad = false;
         auto wait = [&](uint32_t b, uint32_t parity) {
             if (!bad) bad = !__all_sync(0xffffffffu, mbar_wait(b, parity, s_abort, a.err, PA_DEVERR_TIMEOUT, a.wait_ns));
         };
+        // this stream's rows of Q (rows of nodes past the piece's are another's, or zeros: nobody reads their results)
+        auto load_q = [&](const TrWalk &k) {
+            const bool two = tr_two(a, k);
+            if (row == 0 && (two || X == 0) && !bad) {
+                mbar_arrive_expect_tx(bar(C::Q_FULL + X), C::HALVES * 128 * a.G * a.tq);
+#pragma unroll
+                for (int hh = 0; hh < C::HALVES; ++hh)
+                    tma_load_3d(base + X * C::TILE + hh * kTrHalf, &a.tm_q, hh * 64, k.h * a.G,
+                                k.q.q0 + (2 * k.pair + X) * a.tq, bar(C::Q_FULL + X));
+                ++qloads;
+            }
+        };
+        TrWalk k;
+        tr_begin(a, plan, k);
+        bool more = tr_next(a, plan, k, lane);
+        if (more) load_q(k);
 #pragma unroll 1
-        for (int unit = blockIdx.x, u = 0; unit < units; unit += gridDim.x, ++u) {
-            TrWalk k;
-            begin(k, unit, u);
-            const int h = unit % a.Hkv;
-            while (tr_next(a, k, lane)) {
-                const int rows = tr_rows(a, k), nt = k.t1 - k.t0, c = k.q.L - k.q.n;
-                const bool two = rows > kTrTile;
-                const int mine = (two ? X * kTrTile : 0) + row;           // this thread's row of the pair
-                const int at = k.pair * kTrPair + mine, node = at / a.G, g = at - node * a.G;
-                const bool live = mine < rows;
-                const int64_t out_row = ((int64_t)(k.q.q0 + (live ? node : 0)) * a.Hq + h * a.G + g) * D;
-                if (k.q.L == 0) {
-                    // nothing to attend to
-                    if (live && (two || X == 0))
-#pragma unroll 1
-                        for (int d = 0; d < D; d += 8) *reinterpret_cast<uint4 *>(a.out + out_row + d) = make_uint4(0u, 0u, 0u, 0u);
-                    continue;
-                }
+            while (more) {
+                const int nt = k.t1 - k.t0, c = k.q.L - k.q.n;
+                const bool two = tr_two(a, k);
+                const int N = two ? 2 * nt : nt;
+                // this thread's row: a node and a head of its own
+                const int nd = (row * a.inv_g) >> 16, node = (2 * k.pair + (two ? X : 0)) * a.tq + nd, hq = k.h * a.G + row - nd * a.G;
+                const bool live = nd < a.tq && node < k.q.n;
+                const int64_t qrow = k.q.q0 + node;
                 if (a.wait_ns == 0 && !bad) {
                     // a wait limit of 0: give up at the first piece, as a timed-out wait would
                     *s_abort = 1;
                     set_error(a.err, PA_DEVERR_TIMEOUT);
                     bad = true;
                 }
-                // ---- Q of this stream's rows, zeros behind the last
-                if (two || X == 0) {
-                    constexpr int CH = D / 8, PER = 128 / CH;
-                    const int cc = row % CH;
-#pragma unroll 8
-                    for (int r0 = 0; r0 < 128; r0 += PER) {
-                        const int r = r0 + row / CH, p = (two ? X * kTrTile : 0) + r, gr = k.pair * kTrPair + p;
-                        const int nd = gr / a.G;
-                        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-                        if (p < rows && a.sign != 0)
-                            w = __ldg(reinterpret_cast<const uint4 *>(
-                                          a.q + ((int64_t)(k.q.q0 + nd) * a.Hq + h * a.G + (gr - nd * a.G)) * D) + cc);
-                        if (a.sign < 0) w.x ^= 0x80008000u, w.y ^= 0x80008000u, w.z ^= 0x80008000u, w.w ^= 0x80008000u;
-                        st_shared_v4(base + X * C::TILE + (cc >> 3) * kTrHalf + r * 128 + (((cc & 7) ^ (r & 7)) << 4), w.x, w.y,
-                                     w.z, w.w);
-                    }
-                    fence_proxy_async_smem();
-                }
-                tc_fence_before();
-                // (a stream without steps is not waited for: it would run ahead)
-                const int N = two ? 2 * nt : nt;
-                if (X < N) mbar_arrive(bar(C::Q_READY + X));
                 float m = -INFINITY, l = 0.f;      // maximum of s (not yet scaled), sum
 #pragma unroll 1
                 for (int i = X; i < N; i += 2, ++sx) {
@@ -627,32 +672,44 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
 #pragma unroll
                         for (int w = 0; w < 4; ++w) {
                             const int s = p0 - c + 32 * w;
-                            if (s > -32) seen[w] = live ? tr_seen(a, k.q.q0 + node, node, s) : 0u;
+                            if (s > -32) seen[w] = live ? tr_seen(a, qrow, node, s) : 0u;
                         }
                     }
                     wait(bar(C::S_FULL + X), sx & 1);
                     tc_fence_after();
-                    uint32_t r[128];
-#pragma unroll
-                    for (int ch = 0; ch < 4; ++ch) tmem_ld32(s_addr + ch * 32, *reinterpret_cast<uint32_t(*)[32]>(&r[ch * 32]));
                     const uint4 valid = meta[(kseq + t) % kTrMeta];
                     const bool masked = nodes || (valid.x & valid.y & valid.z & valid.w) != ~0u;
-                    tmem_wait_ld();
-                    if (masked) {
-                        seen[0] &= valid.x, seen[1] &= valid.y, seen[2] &= valid.z, seen[3] &= valid.w;
+                    seen[0] &= valid.x, seen[1] &= valid.y, seen[2] &= valid.z, seen[3] &= valid.w;
+                    // 64 columns of S at a time, in registers: the upper ones are read twice, once for the maximum
+                    uint32_t r[64];
+                    float mx = -INFINITY;
+                    auto load = [&](int half) {
+                        tmem_ld32(s_addr + half * 64, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
+                        tmem_ld32(s_addr + half * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
+                        tmem_wait_ld();
+                        if (a.sign <= 0) {
 #pragma unroll
-                        for (int j = 0; j < 128; ++j)
-                            if (!(seen[j >> 5] >> (j & 31) & 1u)) r[j] = __float_as_uint(-INFINITY);
-                    }
-                    float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+                            for (int j = 0; j < 64; ++j) r[j] = a.sign < 0 ? r[j] ^ 0x80000000u : 0u;
+                        }
+                        if (masked) {
 #pragma unroll
-                    for (int j = 0; j < 128; j += 8) {
-                        mx0 = max3(mx0, __uint_as_float(r[j]), __uint_as_float(r[j + 1]));
-                        mx1 = max3(mx1, __uint_as_float(r[j + 2]), __uint_as_float(r[j + 3]));
-                        mx2 = max3(mx2, __uint_as_float(r[j + 4]), __uint_as_float(r[j + 5]));
-                        mx3 = max3(mx3, __uint_as_float(r[j + 6]), __uint_as_float(r[j + 7]));
-                    }
-                    const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
+                            for (int j = 0; j < 64; ++j)
+                                if (!(seen[half * 2 + (j >> 5)] >> (j & 31) & 1u)) r[j] = __float_as_uint(-INFINITY);
+                        }
+                    };
+                    auto maximum = [&]() {
+                        float mx0 = mx, mx1 = -INFINITY;
+#pragma unroll
+                        for (int j = 0; j < 64; j += 4) {
+                            mx0 = max3(mx0, __uint_as_float(r[j]), __uint_as_float(r[j + 1]));
+                            mx1 = max3(mx1, __uint_as_float(r[j + 2]), __uint_as_float(r[j + 3]));
+                        }
+                        mx = fmaxf(mx0, mx1);
+                    };
+                    load(1);
+                    maximum();
+                    load(0);
+                    maximum();
                     bool rescale = false;
                     float m_new = m;
                     if (mx > m && (m == -INFINITY || (mx - m) * sl2 > 8.f)) {
@@ -666,11 +723,11 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
                     uint64_t sum2 = f32x2_pack(0.f, 0.f);
 #pragma unroll
                     for (int hh = 0; hh < 2; ++hh) {
+                        if (hh == 1) load(1);
                         uint32_t pk[32];
 #pragma unroll
                         for (int j = 0; j < 64; j += 2) {
-                            const uint64_t x = fma_f32x2(
-                                f32x2_pack(__uint_as_float(r[hh * 64 + j]), __uint_as_float(r[hh * 64 + j + 1])), sl22, nmb2);
+                            const uint64_t x = fma_f32x2(f32x2_pack(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), sl22, nmb2);
                             const float v0 = tr_ex2(f32x2_lo(x)), v1 = tr_ex2(f32x2_hi(x));
                             sum2 = add_f32x2(sum2, f32x2_pack(v0, v1));
                             pk[j / 2] = pack_bf16x2(v0, v1);
@@ -712,30 +769,40 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
                         m2 = mm;
                     }
                 }
-                if (two || X == 0) {
-                    const bool whole = k.t0 == 0 && k.t1 == k.kt;
-                    const bool wild = *(volatile int *)&s_wild[piece & 3];
+                // the next piece's Q comes while this one ends (both streams are through with S)
+                const bool ends = two || X == 0, whole = k.t0 == 0 && k.t1 == k.kt;
+                const int64_t slot = 2 * k.unit + (k.first ? 0 : 1), out_row = (qrow * a.Hq + hq) * D;
+                const int t0 = k.t0, t1 = k.t1, h = k.h;
+                const TrReq q = k.q;
+                more = tr_next(a, plan, k, lane);
+                if (more) load_q(k);
+                if (ends) {
+                    const bool wild = *(volatile int *)&s_wild[0][piece & 7] == piece + 1 ||
+                                      *(volatile int *)&s_wild[1][piece & 7] == piece + 1;
                     const float inv = l != 0.f ? 1.f / l : 0.f;
-                    const int64_t part = (int64_t)(2 * unit + (k.first ? 0 : 1)) * kTrPair + mine;
+                    const int mine = (two ? X * kTrTile : 0) + row;
+                    float4 *part = reinterpret_cast<float4 *>(a.o_part + slot * kTrPair * D) + mine;   // [D / 4][256]
 #pragma unroll 1
                     for (int ch = 0; ch < D / 32; ++ch) {
                         uint32_t ob[32];
                         float o[32];
                         tmem_ld32(tmem + lane_base + C::ColO + X * D + ch * 32, ob);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = __uint_as_float(ob[j]);
                         if (join) {
-                            tmem_ld32(tmem + lane_base + C::ColO + D + ch * 32, ob);
+                            uint32_t oc[32];
+                            tmem_ld32(tmem + lane_base + C::ColO + D + ch * 32, oc);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) o[j] = o[j] * fa + __uint_as_float(ob[j]) * fb;
+                            for (int j = 0; j < 32; ++j) o[j] = __uint_as_float(ob[j]) * fa + __uint_as_float(oc[j]) * fb;
+                        } else {
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) o[j] = __uint_as_float(ob[j]);
                         }
                         if (wild && live) {
                             float x[32];           // (a copy, so that o stays in registers)
 #pragma unroll
                             for (int j = 0; j < 32; ++j) x[j] = o[j];
-                            tr_wild_rows<D>(a, k.q, k.t0, k.t1, h, node, h * a.G + g, m2 == -INFINITY ? 0.f : m2, ch * 32, x);
+                            tr_wild_rows<D>(a, q, t0, t1, h, node, hq, m2 == -INFINITY ? 0.f : m2, ch * 32, x);
 #pragma unroll
                             for (int j = 0; j < 32; ++j) o[j] = x[j];
                         }
@@ -750,16 +817,19 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
                         } else if (live && !bad) {
 #pragma unroll
                             for (int j = 0; j < 32; j += 4)
-                                *reinterpret_cast<float4 *>(a.o_part + part * D + ch * 32 + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                                part[(ch * 8 + j / 4) * kTrPair] = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
                         }
                         __syncwarp();
                     }
-                    if (!whole && live && !bad) *reinterpret_cast<float2 *>(a.ml_part + part * 2) = make_float2(m2, l);
+                    if (!whole && live && !bad) reinterpret_cast<float2 *>(a.ml_part)[slot * kTrPair + mine] = make_float2(m2, l);
                     tc_fence_before();
+                    mbar_arrive(bar(C::O_FREE + X));
+                    if (join) mbar_arrive(bar(C::O_FREE + 1));
                 }
                 ++piece;
             }
-        }
+        // the copies of Q have landed before the shared memory goes
+        if (qloads > 0) mbar_drain(bar(C::Q_FULL + X), (qloads - 1) & 1);
     }
     __syncthreads();
     if (warp == 10) {
@@ -769,24 +839,25 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
 }
 
 // ------------------------------------------------------------------ merge
-// The rows of segments that several units worked on: a warp per (node, query
-// head), its pieces in order.  The plan is made while the first kernel ends.
+// The rows of segments that several units worked on, pieces in order: a thread
+// has 16 columns of a row, the threads of a warp consecutive rows, as the
+// partials lie.
 constexpr int kTrMergeThreads = 256;
 
 template <int D>
 __global__ void __launch_bounds__(kTrMergeThreads) tree_merge_kernel(const __grid_constant__ TreeArgs a)
 {
-    constexpr int LPR = D / 4, RPW = 32 / LPR;         // lanes of a row, rows of a warp
+    constexpr int COLS = 16, GROUPS = D / COLS;
     extern __shared__ int s_pref[];                    // [R + 1] first tiles, [R] first rows of q
     __shared__ int s_w[kTrMergeThreads / 32];
     int *s_q0 = s_pref + a.R + 1;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     {
         const int per = (a.R + kTrMergeThreads - 1) / kTrMergeThreads, lo = min(a.R, tid * per), hi = min(a.R, lo + per);
-        int run = 0, b;
+        int run = 0;
 #pragma unroll 1
         for (int r = lo; r < hi; ++r) {
-            const TrReq q = tr_request(a, r, b);
+            const TrReq q = tr_request(a, r);
             s_pref[r] = run;
             s_q0[r] = q.q0;
             run += tr_tiles(a, q);
@@ -800,8 +871,9 @@ __global__ void __launch_bounds__(kTrMergeThreads) tree_merge_kernel(const __gri
         if (lane == 31) s_w[warp] = incl;
         __syncthreads();
         int before = incl - run;
-#pragma unroll 1
-        for (int w = 0; w < warp; ++w) before += s_w[w];
+#pragma unroll
+        for (int w = 0; w < kTrMergeThreads / 32; ++w)
+            if (w < warp) before += s_w[w];
 #pragma unroll 1
         for (int r = lo; r < hi; ++r) s_pref[r] += before;
         if (tid == kTrMergeThreads - 1) s_pref[a.R] = before + run;
@@ -811,63 +883,80 @@ __global__ void __launch_bounds__(kTrMergeThreads) tree_merge_kernel(const __gri
     pdl_launch_dependents();
     const int total = s_pref[a.R], W = (total + a.ranges - 1) / a.ranges;
     if (total == 0) return;
-    const int sub = lane / LPR, c4 = lane % LPR;
-    const int64_t rows = (int64_t)a.T * a.Hq;
+    const int per_row = a.Hq * GROUPS;                 // threads per row of q
+    const int64_t all = (int64_t)a.T * per_row;
 #pragma unroll 1
-    for (int64_t w = ((int64_t)blockIdx.x * (kTrMergeThreads / 32) + warp) * RPW + sub; w < rows;
-         w += (int64_t)gridDim.x * (kTrMergeThreads / 32) * RPW) {
-        const int t = (int)(w / a.Hq), hq = (int)(w - (int64_t)t * a.Hq), h = hq / a.G;
-        // the last request that starts at or in front of t and has nodes
+    for (int64_t e = (int64_t)blockIdx.x * kTrMergeThreads + tid; e < all; e += (int64_t)gridDim.x * kTrMergeThreads) {
+        // the last request that starts at or in front of the row
+        const int t = (int)(e / per_row);
         int lo = 0, hi = a.R;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (s_q0[mid] <= t) lo = mid; else hi = mid;
         }
-        const int tiles = s_pref[lo + 1] - s_pref[lo];
-        int b;
-        const TrReq q = tr_request(a, lo, b);
-        if (tiles == 0 || t < q.q0 || t >= q.q0 + q.n) continue;
-        const int64_t at = (int64_t)(t - q.q0) * a.G + (hq - h * a.G);
-        const int kt = tr_ktiles(q.L), pair = (int)(at / kTrPair), S = s_pref[lo] + pair * kt;
+        const int S0 = s_pref[lo], tiles = s_pref[lo + 1] - S0;
+        // (a request whose tiles lie in one range was never shared)
+        if (tiles == 0 || S0 / W == (S0 + tiles - 1) / W) continue;
+        const TrReq q = tr_request(a, lo);
+        if (t < q.q0 || t >= q.q0 + q.n) continue;
+        // thread of the request: (head, column group, row of the head)
+        const int64_t f = e - (int64_t)q.q0 * per_row, rows = (int64_t)q.n * a.G, hc = f / rows, at = f - hc * rows;
+        const int h = (int)hc / GROUPS, cg = (int)hc - h * GROUPS;
+        const int node = (int)(at / a.G), g = (int)(at - (int64_t)node * a.G);
+        const int tile = node / a.tq, pair = tile >> 1, kt = tr_ktiles(q.L), S = S0 + pair * kt;
         const int i0 = S / W, i1 = (S + kt - 1) / W;
         if (i0 == i1) continue;
-        const int row = (int)(at - (int64_t)pair * kTrPair);
-        auto part = [&](int i) { return (int64_t)(2 * (i * a.Hkv + h) + (i == i0 && S > i0 * W ? 1 : 0)) * kTrPair + row; };
-        float M = -INFINITY, L = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-        for (int i = i0; i <= i1; i += 8) {
-            float2 ml[8];
-            float4 v[8];
+        const int row = (tile & 1) * kTrTile + (node - tile * a.tq) * a.G + g;   // of the pair's 256
+        auto slot = [&](int i) { return (int64_t)(2 * (i * a.Hkv + h) + (i == i0 && S > i0 * W ? 1 : 0)); };
+        float M = -INFINITY, L = 0.f, o[COLS];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (i + e <= i1) {
-                    const int64_t p = part(i + e);
-                    ml[e] = __ldcg(reinterpret_cast<const float2 *>(a.ml_part + p * 2));
-                    v[e] = __ldcg(reinterpret_cast<const float4 *>(a.o_part + p * D) + c4);
-                }
+        for (int x = 0; x < COLS; ++x) o[x] = 0.f;
+        constexpr int U = 4;
+#pragma unroll 1
+        for (int i = i0; i <= i1; i += U) {
+            float2 ml[U];
+            float4 v[U][COLS / 4];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                ml[u] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+                for (int x = 0; x < COLS / 4; ++x) v[u][x] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i + u > i1) continue;
+                const int64_t s = slot(i + u);
+                ml[u] = __ldcg(reinterpret_cast<const float2 *>(a.ml_part) + s * kTrPair + row);
+                const float4 *src = reinterpret_cast<const float4 *>(a.o_part + s * kTrPair * D) + cg * (COLS / 4) * kTrPair + row;
+#pragma unroll
+                for (int x = 0; x < COLS / 4; ++x) v[u][x] = __ldcg(src + x * kTrPair);
+            }
             float mn = M;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (i + e <= i1) mn = fmaxf(mn, ml[e].x);
-            const float mz = mn == -INFINITY ? 0.f : mn, f = tr_ex2(M - mz);
-            o.x *= f, o.y *= f, o.z *= f, o.w *= f;
-            L *= f;
+            for (int u = 0; u < U; ++u) mn = fmaxf(mn, ml[u].x);
+            const float mz = mn == -INFINITY ? 0.f : mn, f0 = tr_ex2(M - mz);
+            L *= f0;
+#pragma unroll
+            for (int x = 0; x < COLS; ++x) o[x] *= f0;
             M = mn;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (i + e <= i1) {
-                    const float x = tr_ex2(ml[e].x - mz);
-                    L = fmaf(x, ml[e].y, L);
-                    o.x = fmaf(x, v[e].x, o.x);
-                    o.y = fmaf(x, v[e].y, o.y);
-                    o.z = fmaf(x, v[e].z, o.z);
-                    o.w = fmaf(x, v[e].w, o.w);
+            for (int u = 0; u < U; ++u) {
+                if (i + u > i1) continue;
+                const float w = tr_ex2(ml[u].x - mz);
+                L = fmaf(w, ml[u].y, L);
+#pragma unroll
+                for (int x = 0; x < COLS / 4; ++x) {
+                    o[4 * x] = fmaf(w, v[u][x].x, o[4 * x]);
+                    o[4 * x + 1] = fmaf(w, v[u][x].y, o[4 * x + 1]);
+                    o[4 * x + 2] = fmaf(w, v[u][x].z, o[4 * x + 2]);
+                    o[4 * x + 3] = fmaf(w, v[u][x].w, o[4 * x + 3]);
                 }
+            }
         }
         const float inv = L != 0.f ? 1.f / L : 0.f;
-        const uint2 y = L != 0.f ? make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv)) : make_uint2(0u, 0u);
-        *reinterpret_cast<uint2 *>(a.out + w * D + c4 * 4) = y;
+        uint32_t y[COLS / 2];
+#pragma unroll
+        for (int x = 0; x < COLS / 2; ++x) y[x] = L != 0.f ? pack_bf16x2(o[2 * x] * inv, o[2 * x + 1] * inv) : 0u;
+        uint4 *dst = reinterpret_cast<uint4 *>(a.out + ((int64_t)(q.q0 + node) * a.Hq + h * a.G + g) * D + cg * COLS);
+        dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
+        dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
     }
 }
 
@@ -990,7 +1079,7 @@ static pa_status tr_launch(const TreeArgs &a, cudaStream_t st)
         // behind this call's own kernel, whose end it waits for: overlapped whatever the mode
         auto merge = tree_merge_kernel<D>;
         const size_t smem = ((size_t)2 * a.R + 1) * 4;
-        const int64_t want = ((int64_t)a.T * a.Hq * (D / 4) + kTrMergeThreads - 1) / kTrMergeThreads;
+        const int64_t want = ((int64_t)a.T * a.Hq * (D / 16) + kTrMergeThreads - 1) / kTrMergeThreads;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(want < 4 * grid ? want : 4 * grid));
         cfg.blockDim = dim3(kTrMergeThreads);
@@ -1035,8 +1124,8 @@ extern "C" pa_status pa_paged_tree_attn(const void *q, int n_tokens, int n_q_hea
     const int G = n_q_heads / s.n_kv_heads;
     if (G > 16 || (s.head_dim != 64 && s.head_dim != 128)) return PA_ERR_UNSUPPORTED;
     if ((int64_t)s.n_layers * s.size >= (int64_t)INT32_MAX - 16) return PA_ERR_SHAPE;
-    // tiles of all segments (256 rows of nodes and heads over 128 cached tokens) in 32 bits
-    if (((int64_t)n_tokens * G / 256 + n_reqs) * (((int64_t)max_ctx + 127) / 128) >= (int64_t)1 << 30) return PA_ERR_SHAPE;
+    // tiles of all segments (2 x 128 / G nodes over 128 cached tokens) in 32 bits
+    if (((int64_t)n_tokens / (2 * (kTrTile / G)) + n_reqs) * (((int64_t)max_ctx + 127) / 128) >= (int64_t)1 << 30) return PA_ERR_SHAPE;
     if (!workspace) return PA_ERR_NULL;
     if (!aligned256(workspace)) return PA_ERR_ALIGN;
     if (workspace_bytes < pa_tree_workspace_bytes(n_q_heads, s.n_kv_heads, s.head_dim)) return PA_ERR_WORKSPACE;
@@ -1056,6 +1145,12 @@ extern "C" pa_status pa_paged_tree_attn(const void *q, int n_tokens, int n_q_hea
         !encode_tmap_rows(&a.tm_v16, v_buf, !e4m3, inner, rows, box, 16, sw) ||
         !encode_tmap_rows(&a.tm_v1, v_buf, !e4m3, inner, rows, box, 1, sw))
         return PA_ERR_CUDA;
+    {
+        const cuuint64_t dims[3] = {(cuuint64_t)s.head_dim, (cuuint64_t)n_q_heads, (cuuint64_t)n_tokens};
+        const cuuint64_t strides[2] = {(cuuint64_t)s.head_dim * 2, (cuuint64_t)n_q_heads * s.head_dim * 2};
+        const cuuint32_t qbox[3] = {64, (cuuint32_t)G, (cuuint32_t)(kTrTile / G)};
+        if (!encode_tmap_bf16(&a.tm_q, q, 3, dims, strides, qbox)) return PA_ERR_CUDA;
+    }
     const TrWs ws = tr_ws(s.head_dim);
     unsigned char *wp = static_cast<unsigned char *>(workspace);
     a.ml_part = reinterpret_cast<float *>(wp + ws.ml_off);
@@ -1087,6 +1182,8 @@ extern "C" pa_status pa_paged_tree_attn(const void *q, int n_tokens, int n_q_hea
     a.Hq = n_q_heads;
     a.Hkv = s.n_kv_heads;
     a.G = G;
+    a.inv_g = 65536 / G + 1;
+    a.tq = kTrTile / G;
     a.size = s.size;
     a.req_rows = req_rows;
     a.max_ctx = max_ctx;
