@@ -54,6 +54,8 @@ constexpr int kTrPair = 256;             // rows of two streams
 constexpr int kTrThreads = 384;
 constexpr int kTrHalf = 128 * 128;       // 128 rows of 64 bf16, 128-byte swizzle
 constexpr int kTrMeta = 8;               // tiles whose valid positions are kept: see tr_copy
+constexpr int kTrPieces = 4;             // pieces handed from the walk to the other roles
+constexpr int kTrReaders = 1 + 2 + 8;    // V copies, products, softmax warps
 constexpr int kTrMaxCtas = 160;
 constexpr int kTrMaxUnits = 2 * kTrMaxCtas;   // units that share segments
 constexpr uint32_t kTrTmemCols = 512;    // S_A | S_B | O_A | O_B
@@ -72,8 +74,8 @@ struct TreeArgs {
     int T, R, Hq, Hkv, G, size, req_rows, max_ctx, mask_words, block_shift, layer_row0, total_rows, early_meta;
     int ranges;                                  // per kv head
     uint64_t wait_ns;
-    float scale_log2;                            // of the scale's magnitude; its sign goes into q
-    int sign;                                    // of the scale: -1, 0, 1
+    float scale_log2;                            // of the scale's magnitude, not 0
+    int negate;                                  // the scale is negative: the products take Q with its sign changed
     int tq;                                      // nodes of a stream's tile of rows: 128 / G
     int inv_g;                                   // 65536 / G + 1: x / G = x inv_g >> 16 for x below 272
 };
@@ -115,55 +117,60 @@ __device__ __forceinline__ int tr_pairs(const TreeArgs &a, int n) { return n <= 
 __device__ __forceinline__ int tr_ktiles(int L) { return (L + kTrTile - 1) / kTrTile; }
 __device__ __forceinline__ int tr_tiles(const TreeArgs &a, const TrReq &q) { return q.n > 0 ? tr_pairs(a, q.n) * tr_ktiles(q.L) : 0; }
 
-// A warp's walk over the pieces of its CTA's units (blockIdx, + grid, ...): range i = unit / Hkv is the tiles [i W,
-// (i + 1) W) of the segments laid end to end.
-constexpr int kTrWindow = 8;            // requests at the start of a range that the plan leaves in shared memory
 struct TrPlan {
     int total, W;
     int start[2][2];        // (request, its first tile) where the CTA's units start (a third unit exists only where all
                             // of them are the whole of one kv head)
-    TrReq win[2][kTrWindow];    // requests from there on
+    TrReq req[2];           // that request
 };
+// A piece of a unit's range, for every role of the CTA: token tiles [t0, t1) of nodes 2 tq pair .. of a request.
+struct alignas(16) TrPiece {
+    int q0, n, L, row;
+    int t0, t1, h, unit;
+    int pair, whole, first, end;    // whole: all of its segment; first: it starts the range; end: no more pieces
+};
+// Walk over the pieces of the CTA's units (blockIdx, + grid, ...): range i = unit / Hkv is the tiles [i W, (i + 1) W) of
+// the segments laid end to end.  One warp walks and hands the pieces on.
 struct TrWalk {
     int unit, u, h;         // unit, its number in the CTA, kv head
     int x, xe, x0, r, S0;   // next tile, end, start of the range; request and its first tile
-    int w0;                 // past the window: the lanes hold requests w0 + lane
+    int w0;                 // the lanes hold requests w0 + lane
     TrReq w;
-    // the piece: token tiles [t0, t1) of nodes 2 tq pair .. of request q
-    TrReq q;
-    int kt, pair, t0, t1, first;    // kt: the request's tiles; first: the piece starts the range
 };
-__device__ __forceinline__ void tr_unit(const TreeArgs &a, const TrPlan &p, TrWalk &k)
+__device__ __forceinline__ void tr_unit(const TreeArgs &a, const TrPlan &p, TrWalk &k, int lane)
 {
     const int i = k.unit / a.Hkv, v = a.ranges > 1 ? k.u : 0;
     k.h = k.unit - i * a.Hkv;
     k.x = k.x0 = (int)min((int64_t)p.total, (int64_t)i * p.W);
     k.xe = min(p.total, k.x + p.W);
-    k.r = p.start[v][0];
+    k.r = k.w0 = p.start[v][0];
     k.S0 = p.start[v][1];
-    k.w0 = -64;
+    k.w = TrReq{0, 0, 0, 0};
+    if (k.r + lane < a.R) k.w = tr_request(a, k.r + lane);
 }
-__device__ __forceinline__ void tr_begin(const TreeArgs &a, const TrPlan &p, TrWalk &k)
+__device__ __forceinline__ void tr_begin(const TreeArgs &a, const TrPlan &p, TrWalk &k, int lane)
 {
     k.unit = blockIdx.x;
     k.u = 0;
     k.x = k.xe = 0;
-    if (k.unit < a.ranges * a.Hkv) tr_unit(a, p, k);
+    if (k.unit < a.ranges * a.Hkv) tr_unit(a, p, k, lane);
 }
-__device__ __forceinline__ bool tr_next(const TreeArgs &a, const TrPlan &p, TrWalk &k, int lane)
+__device__ __forceinline__ bool tr_next(const TreeArgs &a, const TrPlan &p, TrWalk &k, TrPiece &o, int lane)
 {
+#pragma unroll 1
     while (k.x >= k.xe) {
         k.unit += gridDim.x;
         ++k.u;
         if (k.unit >= a.ranges * a.Hkv) return false;
-        tr_unit(a, p, k);
+        tr_unit(a, p, k, lane);
     }
-    const int v = a.ranges > 1 ? k.u : 0, r0 = p.start[v][0];
+    TrReq q;
     int tiles;
 #pragma unroll 1
     while (true) {
-        if (k.r - r0 < kTrWindow) {
-            k.q = p.win[v][k.r - r0];
+        const int v = a.ranges > 1 ? k.u : 0;
+        if (k.x == k.x0 && k.r == p.start[v][0] && p.total > 0 && a.ranges > 1) {
+            q = p.req[v];               // the plan has it; the lanes' are on their way
         } else {
             if (k.r - k.w0 >= 32) {
                 k.w0 = k.r;
@@ -171,27 +178,31 @@ __device__ __forceinline__ bool tr_next(const TreeArgs &a, const TrPlan &p, TrWa
                 if (k.r + lane < a.R) k.w = tr_request(a, k.r + lane);
             }
             const int i = k.r - k.w0;
-            k.q.q0 = __shfl_sync(0xffffffffu, k.w.q0, i);
-            k.q.n = __shfl_sync(0xffffffffu, k.w.n, i);
-            k.q.L = __shfl_sync(0xffffffffu, k.w.L, i);
-            k.q.row = __shfl_sync(0xffffffffu, k.w.row, i);
+            q.q0 = __shfl_sync(0xffffffffu, k.w.q0, i);
+            q.n = __shfl_sync(0xffffffffu, k.w.n, i);
+            q.L = __shfl_sync(0xffffffffu, k.w.L, i);
+            q.row = __shfl_sync(0xffffffffu, k.w.row, i);
         }
-        tiles = tr_tiles(a, k.q);
+        tiles = tr_tiles(a, q);
         if (k.x < k.S0 + tiles) break;
         k.S0 += tiles;
         if (++k.r >= a.R) return false;      // (not reached: x lies below the total)
     }
-    k.kt = tr_ktiles(k.q.L);
-    const int off = k.x - k.S0;
-    k.pair = tiles == k.kt ? 0 : off / k.kt;
-    k.t0 = off - k.pair * k.kt;
-    k.t1 = min(k.kt, k.t0 + k.xe - k.x);
-    k.first = k.x == k.x0;
-    k.x += k.t1 - k.t0;
+    const int kt = tr_ktiles(q.L), off = k.x - k.S0;
+    o.q0 = q.q0, o.n = q.n, o.L = q.L, o.row = q.row;
+    o.pair = tiles == kt ? 0 : off / kt;
+    o.t0 = off - o.pair * kt;
+    o.t1 = min(kt, o.t0 + k.xe - k.x);
+    o.h = k.h;
+    o.unit = k.unit;
+    o.whole = o.t0 == 0 && o.t1 == kt;
+    o.first = k.x == k.x0;
+    o.end = 0;
+    k.x += o.t1 - o.t0;
     return true;
 }
 // the piece has rows for both streams
-__device__ __forceinline__ bool tr_two(const TreeArgs &a, const TrWalk &k) { return k.q.n - 2 * a.tq * k.pair > a.tq; }
+__device__ __forceinline__ bool tr_two(const TreeArgs &a, const TrPiece &k) { return k.n - 2 * a.tq * k.pair > a.tq; }
 
 // 32 bits of what node i (row `qrow` of the mask) sees, from node s on (s < 0: context, all ones)
 __device__ __forceinline__ uint32_t tr_seen(const TreeArgs &a, int64_t qrow, int i, int s)
@@ -216,7 +227,8 @@ struct TrCfg {
     static constexpr int OffV = OffK + NK * TILE;
     static constexpr int OffBar = OffV + NV * TILE;
     enum { K_FULL, K_EMPTY = K_FULL + NK, V_FULL = K_EMPTY + NK, V_EMPTY = V_FULL + NV, S_FULL = V_EMPTY + NV,
-           P_READY = S_FULL + 2, O_FULL = P_READY + 2, O_FREE = O_FULL + 2, Q_FULL = O_FREE + 2, DRAIN = Q_FULL + 2, JOINT = DRAIN + 2, N_BARS };   // JOINT: stream A's Q, for stream B
+           P_READY = S_FULL + 2, O_FULL = P_READY + 2, O_FREE = O_FULL + 2, Q_FULL = O_FREE + 2, DRAIN = Q_FULL + 2, JOINT = DRAIN + 2, ITEM_FULL, ITEM_EMPTY = ITEM_FULL + kTrPieces,
+           N_BARS = ITEM_EMPTY + kTrPieces };   // JOINT: stream A's Q, for stream B
     static constexpr int OffMeta = (OffBar + N_BARS * 8 + 15) & ~15;     // uint4 [kTrMeta]: valid positions
     static constexpr int OffML = OffMeta + kTrMeta * 16;                 // float2 [128]: stream B's (m, l)
     static constexpr int OffEnd = OffML + 128 * 8;
@@ -234,6 +246,36 @@ __device__ __forceinline__ float tr_ex2(float x)
     return y;
 }
 
+// mbar_wait without a call, so that nothing is kept in memory for one: whole warp, the same answer in every lane.
+__device__ __forceinline__ bool tr_wait(const TreeArgs &a, uint32_t bar, uint32_t parity, volatile int *s_abort)
+{
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    const uint64_t t0 = global_ns();
+    bool ok = false;
+#pragma unroll 1
+    while (a.wait_ns != 0) {
+        ok = mbar_try_wait(bar, parity);
+        if (ok || *s_abort || global_ns() - t0 > a.wait_ns) break;
+    }
+    if (!ok && !*s_abort) {
+        *s_abort = 1;
+        set_error(a.err, PA_DEVERR_TIMEOUT);
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+
+// The ring of pieces.  These two wait for nothing but other warps' control flow, and the roles run through every
+// piece even when a copy or product has been given up (without waiting or issuing), so that no warp is missed at a
+// barrier: the limit is only a last resort.
+__device__ __forceinline__ void tr_wait_ring(uint32_t bar, uint32_t parity)
+{
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return;
+    const uint64_t t0 = global_ns();
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity) && global_ns() - t0 < 10000000000ull) {}
+    __syncwarp();
+}
+
 // ----------------------------------------------------------------- copies
 // K (isv false) or V tiles of the CTA's units.  Positions without a row (past the
 // end, or a bad slot) are zeros; the K warp also writes which positions are valid:
@@ -241,8 +283,9 @@ __device__ __forceinline__ float tr_ex2(float x)
 // already free.  (Tile x is copied when S(x - NK) is done, which was issued behind
 // softmax of tile x - NK - 1 at the latest.)
 template <int D>
-__device__ __forceinline__ void tr_copy(const TreeArgs &a, const TrPlan &plan, bool isv, uint32_t ring, uint32_t full,
-                                        uint32_t empty, uint4 *meta, volatile int *s_abort, int lane)
+__device__ __forceinline__ void tr_copy(const TreeArgs &a, const TrPlan &plan, TrPiece *pieces, uint32_t item_full,
+                                        uint32_t item_empty, bool isv, uint32_t ring, uint32_t full, uint32_t empty,
+                                        uint4 *meta, volatile int *s_abort, int lane)
 {
     using C = TrCfg<D>;
     const int stages = isv ? C::NV : C::NK;
@@ -250,27 +293,44 @@ __device__ __forceinline__ void tr_copy(const TreeArgs &a, const TrPlan &plan, b
     int st = 0, seq = 0, errs = 0;
     uint32_t ph = 0;
     bool go = true;
-    TrWalk k;
-    tr_begin(a, plan, k);
+    TrWalk w;
+    if (!isv) tr_begin(a, plan, w, lane);
 #pragma unroll 1
-        while (go && tr_next(a, plan, k, lane)) {
-            const int col = k.h * D;
-            const int32_t *tab = a.req_to_token + (int64_t)k.q.row * a.max_ctx;
+    for (int it = 0;; ++it) {
+        TrPiece k;
+        const int slot = it % kTrPieces;
+        if (isv) {
+            tr_wait_ring(item_full + slot * 8, (it / kTrPieces) & 1);
+            k = pieces[slot];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(item_empty + slot * 8);
+        } else {
+            // this warp walks, and hands the pieces on
+            k.end = !tr_next(a, plan, w, k, lane);
+            if (it >= kTrPieces) tr_wait_ring(item_empty + slot * 8, (it / kTrPieces - 1) & 1);
+            if (lane == 0) {
+                pieces[slot] = k;
+                mbar_arrive(item_full + slot * 8);
+            }
+        }
+        if (k.end) break;
+        const int col = k.h * D;
+        const int32_t *tab = a.req_to_token + (int64_t)k.row * a.max_ctx;
             int nx[4];
             auto fetch = [&](int t) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int p = t * kTrTile + 4 * lane + e;
-                    nx[e] = ld_nc_ordered_s32_if(p < k.q.L, tab + (p < k.q.L ? p : 0));
+                    nx[e] = ld_nc_ordered_s32_if(p < k.L, tab + (p < k.L ? p : 0));
                 }
             };
             fetch(k.t0);
 #pragma unroll 1
-            for (int t = k.t0; t < k.t1; ++t) {
+            for (int t = k.t0; t < k.t1 && go; ++t) {
                 int sl[4] = {nx[0], nx[1], nx[2], nx[3]};
                 if (t + 1 < k.t1) fetch(t + 1);
                 if (seq >= stages &&
-                    !__all_sync(0xffffffffu, mbar_wait(empty + st * 8, ph ^ 1, s_abort, a.err, PA_DEVERR_TIMEOUT, a.wait_ns))) {
+                    !tr_wait(a, empty + st * 8, ph ^ 1, s_abort)) {
                     go = false;
                     break;
                 }
@@ -279,7 +339,7 @@ __device__ __forceinline__ void tr_copy(const TreeArgs &a, const TrPlan &plan, b
                 uint32_t nib = 0;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const bool in = t * kTrTile + 4 * lane + e < k.q.L;
+                    const bool in = t * kTrTile + 4 * lane + e < k.L;
                     ok[e] = in && sl[e] >= 0 && sl[e] < a.size;
                     if (in && !ok[e]) errs |= PA_DEVERR_SLOT;
                     nib |= (uint32_t)ok[e] << e;
@@ -374,17 +434,17 @@ __device__ __forceinline__ bool tr_tame(uint32_t tile, int lo, int hi, int lane)
 // What tr_tame took out, for one row of the piece (node i, query head hq) and 32 columns from d0 on: the parts of the
 // nodes' V rows in tiles [t0, t1) that hold a NaN or an infinity and that the node sees, weights relative to m2.
 template <int D>
-__device__ __noinline__ void tr_wild_rows(const TreeArgs &a, const TrReq &q, int t0, int t1, int h, int i, int hq, float m2,
-                                          int d0, float *o)
+__device__ __forceinline__ void tr_wild_rows(const TreeArgs &a, const TrPiece &q, int i, int hq, float m2, int d0,
+                                             float (&o)[32])
 {
     const int c = q.L - q.n;
     const int32_t *tab = a.req_to_token + (int64_t)q.row * a.max_ctx;
     const __nv_bfloat16 *qr = a.q + ((int64_t)(q.q0 + i) * a.Hq + hq) * D;
 #pragma unroll 1
-    for (int j = max(c, t0 * kTrTile); j < min(q.L, t1 * kTrTile); ++j) {
+    for (int j = max(c, q.t0 * kTrTile); j < min(q.L, q.t1 * kTrTile); ++j) {
         const int slot = __ldg(tab + j);
         if (slot < 0 || slot >= a.size) continue;
-        const int64_t at = ((int64_t)slot * a.Hkv + h) * D;
+        const int64_t at = ((int64_t)slot * a.Hkv + q.h) * D;
         const __nv_bfloat16 *kr = reinterpret_cast<const __nv_bfloat16 *>(a.k) + at, *vr = reinterpret_cast<const __nv_bfloat16 *>(a.v) + at;
         bool wild = false;
 #pragma unroll 1
@@ -393,9 +453,8 @@ __device__ __noinline__ void tr_wild_rows(const TreeArgs &a, const TrReq &q, int
         float s = 0.f;
 #pragma unroll 1
         for (int d = 0; d < D; ++d) s = fmaf(__bfloat162float(qr[d]), __bfloat162float(kr[d]), s);
-        s = a.sign == 0 ? 0.f : a.sign < 0 ? -s : s;
-        const float p = tr_ex2(fmaf(s, a.scale_log2, -m2));
-#pragma unroll 1
+        const float p = tr_ex2(fmaf(a.negate ? -s : s, a.scale_log2, -m2));
+#pragma unroll
         for (int d = 0; d < 32; ++d) o[d] = fmaf(p, __bfloat162float(vr[d0 + d]), o[d]);
     }
 }
@@ -409,6 +468,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
     __shared__ int s_w[kTrThreads / 32];
     __shared__ int s_abort_storage;
     __shared__ TrPlan plan;
+    __shared__ TrPiece s_piece[kTrPieces];
     __shared__ int s_wild[2][8];               // per stream, at piece % 8: piece + 1 where a V row was taken out (the
                                                // rings keep the streams within 8 pieces of one another)
     __shared__ uint32_t s_tmem;
@@ -423,7 +483,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
     if (tid < C::N_BARS) {
         const bool softmax = (tid >= C::P_READY && tid < C::O_FULL) || (tid >= C::O_FREE && tid < C::Q_FULL);
         const bool empty = (tid >= C::K_EMPTY && tid < C::V_FULL) || (tid >= C::V_EMPTY && tid < C::S_FULL);
-        mbar_init(bar(tid), softmax ? 128u : empty ? 2u : 1u);
+        mbar_init(bar(tid), softmax ? 128u : empty ? 2u : tid >= C::ITEM_EMPTY ? (uint32_t)kTrReaders : 1u);
     }
     static_assert(C::N_BARS <= 64, "two warps initialise the barriers");
     if (warp < 2) fence_mbar_init();
@@ -496,14 +556,8 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
                 }
                 plan.start[u][0] = r;
                 plan.start[u][1] = S0;
+                plan.req[u] = r == hi - 1 ? q : tr_request(a, r);
             }
-        }
-        __syncthreads();
-#pragma unroll 1
-        for (int u = 0; u < 2; ++u) {
-            const int r0 = plan.start[u][0];
-#pragma unroll 1
-            for (int r = max(lo, r0); r < min(hi, r0 + kTrWindow); ++r) plan.win[u][r - r0] = r == hi - 1 ? q : tr_request(a, r);
         }
     }
     if (a.early_meta) pdl_wait();
@@ -527,25 +581,30 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
 
     if (warp == 8 || warp == 9) {
         const bool isv = warp == 9;
-        tr_copy<D>(a, plan, isv, base + (isv ? C::OffV : C::OffK), bar(isv ? C::V_FULL : C::K_FULL),
+        tr_copy<D>(a, plan, s_piece, bar(C::ITEM_FULL), bar(C::ITEM_EMPTY), isv, base + (isv ? C::OffV : C::OffK), bar(isv ? C::V_FULL : C::K_FULL),
                    bar(isv ? C::V_EMPTY : C::K_EMPTY), meta, s_abort, lane);
     } else if (warp >= 10) {
         // ======================================================= products
         // A warp per stream: while one waits for its weights, the tensor core has the other's products.
         const int X = warp - 10;
         const uint32_t sQ = base, sK = base + C::OffK, sV = base + C::OffV;
+        const uint32_t id_s = C::kIdS | (a.negate ? 1u << 13 : 0u);   // bit 13: A negated
         int seq = 0, piece = 0, px = 0, pq = 0, p2 = 0, pj = 0;   // token tiles, pieces before; this stream's steps, pieces; of
                                                                   // stream B: those with rows of its own, and with A's
         bool bad = false;
         auto wait = [&](uint32_t b, uint32_t parity) {
-            if (!bad) bad = !__all_sync(0xffffffffu, mbar_wait(b, parity, s_abort, a.err, PA_DEVERR_TIMEOUT, a.wait_ns));
+            if (!bad) bad = !tr_wait(a, b, parity, s_abort);
         };
-        TrWalk k;
-        tr_begin(a, plan, k);
 #pragma unroll 1
-            while (tr_next(a, plan, k, lane)) {
+            for (int it = 0;; ++it) {
+                const int slot = it % kTrPieces;
+                tr_wait_ring(bar(C::ITEM_FULL + slot), (it / kTrPieces) & 1);
+                const TrPiece k = s_piece[slot];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::ITEM_EMPTY + slot));
+                if (k.end) break;
                 const int nt = k.t1 - k.t0, two = tr_two(a, k);
-                const int N = two ? 2 * nt : nt, c = k.q.L - k.q.n;
+                const int N = two ? 2 * nt : nt, c = k.L - k.n;
                 // a ring stage is free when both streams are through with it, or twice the one that uses it
                 auto release = [&](uint32_t b) {
                     umma_commit(b);
@@ -556,7 +615,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
 #pragma unroll
                     for (int s = 0; s < D / 16; ++s)
                         umma_ss(tmem + X * 128, smem_desc_sw128(q + (s >> 2) * kTrHalf + (s & 3) * 32, 16, 1024),
-                                smem_desc_sw128(kk + (s >> 2) * kTrHalf + (s & 3) * 32, 16, 1024), C::kIdS, s > 0);
+                                smem_desc_sw128(kk + (s >> 2) * kTrHalf + (s & 3) * 32, 16, 1024), id_s, s > 0);
                     umma_commit(bar(C::S_FULL + X));
                     release(bar(C::K_EMPTY + st));
                 };
@@ -583,7 +642,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
                     const uint32_t vt = sV + st * C::TILE;
                     wait(bar(C::V_FULL + st), (s / C::NV) & 1);
                     // drafted tokens' rows must not hold what a weight of 0 does not cancel
-                    const int p0 = (k.t0 + t) * kTrTile, lo = max(0, c - p0), hi = min(kTrTile, k.q.L - p0);
+                    const int p0 = (k.t0 + t) * kTrTile, lo = max(0, c - p0), hi = min(kTrTile, k.L - p0);
                     if (lo < hi) {
                         if (X == 0 || !two) {
                             if (!bad && tr_tame<D>(vt, lo, hi, lane)) {
@@ -628,33 +687,31 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
         int qloads = 0;
         bool bad = false;
         auto wait = [&](uint32_t b, uint32_t parity) {
-            if (!bad) bad = !__all_sync(0xffffffffu, mbar_wait(b, parity, s_abort, a.err, PA_DEVERR_TIMEOUT, a.wait_ns));
+            if (!bad) bad = !tr_wait(a, b, parity, s_abort);
         };
         // this stream's rows of Q (rows of nodes past the piece's are another's, or zeros: nobody reads their results)
-        auto load_q = [&](const TrWalk &k) {
-            const bool two = tr_two(a, k);
-            if (row == 0 && (two || X == 0) && !bad) {
+        auto load_q = [&](const TrPiece &k) {
+            if (row == 0 && (X == 0 || tr_two(a, k)) && !bad) {
                 mbar_arrive_expect_tx(bar(C::Q_FULL + X), C::HALVES * 128 * a.G * a.tq);
 #pragma unroll
                 for (int hh = 0; hh < C::HALVES; ++hh)
-                    tma_load_3d(base + X * C::TILE + hh * kTrHalf, &a.tm_q, hh * 64, k.h * a.G,
-                                k.q.q0 + (2 * k.pair + X) * a.tq, bar(C::Q_FULL + X));
+                    tma_load_3d(base + X * C::TILE + hh * kTrHalf, &a.tm_q, hh * 64, k.h * a.G, k.q0 + (2 * k.pair + X) * a.tq,
+                                bar(C::Q_FULL + X));
                 ++qloads;
             }
         };
-        TrWalk k;
-        tr_begin(a, plan, k);
-        bool more = tr_next(a, plan, k, lane);
-        if (more) load_q(k);
+        tr_wait_ring(bar(C::ITEM_FULL), 0);
+        if (!s_piece[0].end) load_q(s_piece[0]);
 #pragma unroll 1
-            while (more) {
-                const int nt = k.t1 - k.t0, c = k.q.L - k.q.n;
+            while (!s_piece[piece % kTrPieces].end) {
+                const TrPiece &k = s_piece[piece % kTrPieces];
+                const int nt = k.t1 - k.t0, c = k.L - k.n;
                 const bool two = tr_two(a, k);
-                const int N = two ? 2 * nt : nt;
+                const int N = two ? 2 * nt : nt, t00 = k.t0;
                 // this thread's row: a node and a head of its own
-                const int nd = (row * a.inv_g) >> 16, node = (2 * k.pair + (two ? X : 0)) * a.tq + nd, hq = k.h * a.G + row - nd * a.G;
-                const bool live = nd < a.tq && node < k.q.n;
-                const int64_t qrow = k.q.q0 + node;
+                const int nd = (row * a.inv_g) >> 16, node = (2 * k.pair + (two ? X : 0)) * a.tq + nd;
+                const bool live = nd < a.tq && node < k.n;
+                const int64_t qrow = k.q0 + node;
                 if (a.wait_ns == 0 && !bad) {
                     // a wait limit of 0: give up at the first piece, as a timed-out wait would
                     *s_abort = 1;
@@ -664,7 +721,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
                 float m = -INFINITY, l = 0.f;      // maximum of s (not yet scaled), sum
 #pragma unroll 1
                 for (int i = X; i < N; i += 2, ++sx) {
-                    const int t = two ? i >> 1 : i, p0 = (k.t0 + t) * kTrTile;
+                    const int t = two ? i >> 1 : i, p0 = (t00 + t) * kTrTile;
                     // what of the tile this row sees, before S is there
                     uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
                     const bool nodes = p0 + kTrTile > c;
@@ -680,36 +737,24 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
                     const uint4 valid = meta[(kseq + t) % kTrMeta];
                     const bool masked = nodes || (valid.x & valid.y & valid.z & valid.w) != ~0u;
                     seen[0] &= valid.x, seen[1] &= valid.y, seen[2] &= valid.z, seen[3] &= valid.w;
-                    // 64 columns of S at a time, in registers: the upper ones are read twice, once for the maximum
-                    uint32_t r[64];
-                    float mx = -INFINITY;
-                    auto load = [&](int half) {
-                        tmem_ld32(s_addr + half * 64, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
-                        tmem_ld32(s_addr + half * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
-                        tmem_wait_ld();
-                        if (a.sign <= 0) {
+                    uint32_t r[128];
 #pragma unroll
-                            for (int j = 0; j < 64; ++j) r[j] = a.sign < 0 ? r[j] ^ 0x80000000u : 0u;
-                        }
-                        if (masked) {
+                    for (int ch = 0; ch < 4; ++ch) tmem_ld32(s_addr + ch * 32, *reinterpret_cast<uint32_t(*)[32]>(&r[ch * 32]));
+                    tmem_wait_ld();
+                    if (masked) {
 #pragma unroll
-                            for (int j = 0; j < 64; ++j)
-                                if (!(seen[half * 2 + (j >> 5)] >> (j & 31) & 1u)) r[j] = __float_as_uint(-INFINITY);
-                        }
-                    };
-                    auto maximum = [&]() {
-                        float mx0 = mx, mx1 = -INFINITY;
+                        for (int j = 0; j < 128; ++j)
+                            if (!(seen[j >> 5] >> (j & 31) & 1u)) r[j] = __float_as_uint(-INFINITY);
+                    }
+                    float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
 #pragma unroll
-                        for (int j = 0; j < 64; j += 4) {
-                            mx0 = max3(mx0, __uint_as_float(r[j]), __uint_as_float(r[j + 1]));
-                            mx1 = max3(mx1, __uint_as_float(r[j + 2]), __uint_as_float(r[j + 3]));
-                        }
-                        mx = fmaxf(mx0, mx1);
-                    };
-                    load(1);
-                    maximum();
-                    load(0);
-                    maximum();
+                    for (int j = 0; j < 128; j += 8) {
+                        mx0 = max3(mx0, __uint_as_float(r[j]), __uint_as_float(r[j + 1]));
+                        mx1 = max3(mx1, __uint_as_float(r[j + 2]), __uint_as_float(r[j + 3]));
+                        mx2 = max3(mx2, __uint_as_float(r[j + 4]), __uint_as_float(r[j + 5]));
+                        mx3 = max3(mx3, __uint_as_float(r[j + 6]), __uint_as_float(r[j + 7]));
+                    }
+                    const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
                     bool rescale = false;
                     float m_new = m;
                     if (mx > m && (m == -INFINITY || (mx - m) * sl2 > 8.f)) {
@@ -723,11 +768,11 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
                     uint64_t sum2 = f32x2_pack(0.f, 0.f);
 #pragma unroll
                     for (int hh = 0; hh < 2; ++hh) {
-                        if (hh == 1) load(1);
                         uint32_t pk[32];
 #pragma unroll
                         for (int j = 0; j < 64; j += 2) {
-                            const uint64_t x = fma_f32x2(f32x2_pack(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), sl22, nmb2);
+                            const uint64_t x = fma_f32x2(
+                                f32x2_pack(__uint_as_float(r[hh * 64 + j]), __uint_as_float(r[hh * 64 + j + 1])), sl22, nmb2);
                             const float v0 = tr_ex2(f32x2_lo(x)), v1 = tr_ex2(f32x2_hi(x));
                             sum2 = add_f32x2(sum2, f32x2_pack(v0, v1));
                             pk[j / 2] = pack_bf16x2(v0, v1);
@@ -770,17 +815,16 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
                     }
                 }
                 // the next piece's Q comes while this one ends (both streams are through with S)
-                const bool ends = two || X == 0, whole = k.t0 == 0 && k.t1 == k.kt;
-                const int64_t slot = 2 * k.unit + (k.first ? 0 : 1), out_row = (qrow * a.Hq + hq) * D;
-                const int t0 = k.t0, t1 = k.t1, h = k.h;
-                const TrReq q = k.q;
-                more = tr_next(a, plan, k, lane);
-                if (more) load_q(k);
+                tr_wait_ring(bar(C::ITEM_FULL + (piece + 1) % kTrPieces), ((piece + 1) / kTrPieces) & 1);
+                if (!s_piece[(piece + 1) % kTrPieces].end) load_q(s_piece[(piece + 1) % kTrPieces]);
+                const bool ends = two || X == 0;
                 if (ends) {
                     const bool wild = *(volatile int *)&s_wild[0][piece & 7] == piece + 1 ||
                                       *(volatile int *)&s_wild[1][piece & 7] == piece + 1;
                     const float inv = l != 0.f ? 1.f / l : 0.f;
-                    const int mine = (two ? X * kTrTile : 0) + row;
+                    const int mine = (two ? X * kTrTile : 0) + row, hq = k.h * a.G + row - nd * a.G;
+                    const bool whole = k.whole;
+                    const int64_t slot = 2 * k.unit + (k.first ? 0 : 1), out_row = (qrow * a.Hq + hq) * D;
                     float4 *part = reinterpret_cast<float4 *>(a.o_part + slot * kTrPair * D) + mine;   // [D / 4][256]
 #pragma unroll 1
                     for (int ch = 0; ch < D / 32; ++ch) {
@@ -798,14 +842,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
 #pragma unroll
                             for (int j = 0; j < 32; ++j) o[j] = __uint_as_float(ob[j]);
                         }
-                        if (wild && live) {
-                            float x[32];           // (a copy, so that o stays in registers)
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) x[j] = o[j];
-                            tr_wild_rows<D>(a, q, t0, t1, h, node, hq, m2 == -INFINITY ? 0.f : m2, ch * 32, x);
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) o[j] = x[j];
-                        }
+                        if (wild && live) tr_wild_rows<D>(a, k, node, hq, m2 == -INFINITY ? 0.f : m2, ch * 32, o);
                         if (live && !bad && whole) {
 #pragma unroll
                             for (int j = 0; j < 32; j += 8) {
@@ -826,6 +863,8 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
                     mbar_arrive(bar(C::O_FREE + X));
                     if (join) mbar_arrive(bar(C::O_FREE + 1));
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::ITEM_EMPTY + piece % kTrPieces));
                 ++piece;
             }
         // the copies of Q have landed before the shared memory goes
@@ -1188,11 +1227,9 @@ extern "C" pa_status pa_paged_tree_attn(const void *q, int n_tokens, int n_q_hea
     a.req_rows = req_rows;
     a.max_ctx = max_ctx;
     a.scale_log2 = (float)(fabs((double)scale) * 1.4426950408889634);
-    a.sign = scale < 0.f ? -1 : 1;
-    if (a.scale_log2 == 0.f) {
-        a.scale_log2 = 1.f;      // q is taken as 0
-        a.sign = 0;
-    }
+    a.negate = scale < 0.f;
+    // a scale of 0 as one that no score survives: a hidden key's minus infinity stays what it is
+    if (a.scale_log2 < 0x1p-126f) a.scale_log2 = 0x1p-126f;
     if (!e4m3) return s.head_dim == 64 ? tr_launch<64>(a, st) : tr_launch<128>(a, st);
     a.scale_log2 = (float)((double)scale * 1.4426950408889634);
     const dim3 grid(256, n_reqs);
