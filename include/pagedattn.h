@@ -472,7 +472,9 @@ pa_status pa_kv_evict(int32_t *req_to_token, int req_rows, int max_ctx, const in
  * that a node does not see does not reach it, whatever it holds.  q, out: bf16
  * [n_tokens, n_q_heads, head_dim]; rows from qo_indptr[n_reqs] on are not written.
  * block == 0: the bf16 cache, k_exp and v_exp NULL; block >= 1: the e4m3 cache
- * with scales per block of slots.  Supported: head_dim 64 or 128, 1 <= G <= 16,
+ * with scales per block of slots, its arithmetic that of
+ * pa_paged_prefill_attn_fp8_block (q within 2^-17 of its row's largest element).  The weights are
+ * rounded to bf16.  Supported: head_dim 64 or 128, 1 <= G <= 16,
  * n_reqs <= 4096.  Workspace: pa_tree_workspace_bytes, whatever the batch,
  * initialised once with pa_workspace_init; calls that share one are ordered on a
  * stream.  Two kernels: partial results over equal ranges of cached tokens, then

@@ -42,6 +42,7 @@
 #include <math.h>
 #include <string.h>
 
+#include "pa_e4m3_tiles.cuh"
 #include "pa_internal.h"
 #include "pa_sm100.cuh"
 
@@ -218,26 +219,37 @@ __device__ __forceinline__ uint32_t tr_seen(const TreeArgs &a, int64_t qrow, int
     return __funnelshift_r(lo, hi, s & 31);
 }
 
-template <int D>
+// Shared memory: Q of both streams; (e4m3) V widened to bf16, a buffer per stream; the rings of K and V as they are in
+// the cache; barriers; what goes with the tiles.
+template <int D, bool E8>
 struct TrCfg {
     static constexpr int HALVES = D / 64;
-    static constexpr int TILE = HALVES * kTrHalf;
+    static constexpr int TILE = HALVES * kTrHalf;        // bf16
+    static constexpr int RAW = E8 ? kTrTile * D : TILE;  // as cached
     static constexpr int NK = D == 128 ? 3 : 5, NV = D == 128 ? 2 : 5;   // ring stages
-    static constexpr int OffK = 2 * TILE;                // behind Q of both streams
-    static constexpr int OffV = OffK + NK * TILE;
-    static constexpr int OffBar = OffV + NV * TILE;
+    static constexpr int OffWide = 2 * TILE;
+    static constexpr int OffK = OffWide + (E8 ? 2 * TILE : 0);
+    static constexpr int OffV = OffK + NK * RAW;
+    static constexpr int OffBar = OffV + NV * RAW;
     enum { K_FULL, K_EMPTY = K_FULL + NK, V_FULL = K_EMPTY + NK, V_EMPTY = V_FULL + NV, S_FULL = V_EMPTY + NV,
-           P_READY = S_FULL + 2, O_FULL = P_READY + 2, O_FREE = O_FULL + 2, Q_FULL = O_FREE + 2, DRAIN = Q_FULL + 2, JOINT = DRAIN + 2, ITEM_FULL, ITEM_EMPTY = ITEM_FULL + kTrPieces,
-           N_BARS = ITEM_EMPTY + kTrPieces };   // JOINT: stream A's Q, for stream B
+           P_READY = S_FULL + 2, O_FULL = P_READY + 2, O_FREE = O_FULL + 2, Q_FULL = O_FREE + 2, DRAIN = Q_FULL + 2,
+           Q_SPLIT = DRAIN + 2,                          // e4m3: Q is there in its terms
+           JOINT = Q_SPLIT + 2,                          // stream A's Q, for stream B
+           ITEM_FULL, ITEM_EMPTY = ITEM_FULL + kTrPieces, N_BARS = ITEM_EMPTY + kTrPieces };
     static constexpr int OffMeta = (OffBar + N_BARS * 8 + 15) & ~15;     // uint4 [kTrMeta]: valid positions
     static constexpr int OffML = OffMeta + kTrMeta * 16;                 // float2 [128]: stream B's (m, l)
-    static constexpr int OffEnd = OffML + 128 * 8;
+    static constexpr int OffKS = OffML + 128 * 8;                        // e4m3: float [kTrMeta][128], keys' scales
+    static constexpr int OffVE = OffKS + (E8 ? kTrMeta * 512 : 0);       // bytes [NV][128], values' exponents
+    static constexpr int OffQS = OffVE + (E8 ? NV * 128 : 0);            // float [128], rows' scales of a joint piece
+    static constexpr int OffEnd = OffQS + (E8 ? 512 : 0);
     static constexpr int Smem = OffEnd + 1024;
     static constexpr uint32_t ColO = 256;
-    static constexpr uint32_t kIdS = idesc_bf16_f32(128, 128, 0, 0), kIdPV = idesc_bf16_f32(128, D, 0, 1);
+    static constexpr uint32_t kIdS = E8 ? idesc_e4m3_f32(128, 128, 0, 0) : idesc_bf16_f32(128, 128, 0, 0);
+    static constexpr uint32_t kIdPV = idesc_bf16_f32(128, D, 0, 1);
+    static_assert(N_BARS <= 64, "two warps initialise the barriers");
+    static_assert(Smem <= 232448 - 512, "fits with the static shared memory");
+    static_assert(kTrMeta >= NK + 3, "a tile's valid positions and scales outlive its ring stage");
 };
-static_assert(TrCfg<128>::Smem <= 232448 - 256, "fits with the static shared memory");
-static_assert(kTrMeta >= TrCfg<64>::NK + 3 && kTrMeta >= TrCfg<128>::NK + 3, "a tile's valid positions outlive its ring stage");
 
 __device__ __forceinline__ float tr_ex2(float x)
 {
@@ -245,6 +257,9 @@ __device__ __forceinline__ float tr_ex2(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+
+// a softmax scale that is not 0, as which a hidden key's minus infinity would be a NaN
+__device__ __forceinline__ float tr_scale(float x) { return x < 0x1p-126f ? 0x1p-126f : x; }
 
 // mbar_wait without a call, so that nothing is kept in memory for one: whole warp, the same answer in every lane.
 __device__ __forceinline__ bool tr_wait(const TreeArgs &a, uint32_t bar, uint32_t parity, volatile int *s_abort)
@@ -282,12 +297,14 @@ __device__ __forceinline__ void tr_wait_ring(uint32_t bar, uint32_t parity)
 // a ring of its own, because softmax reads them behind S, when the K stage is
 // already free.  (Tile x is copied when S(x - NK) is done, which was issued behind
 // softmax of tile x - NK - 1 at the latest.)
-template <int D>
+template <int D, bool E8>
 __device__ __forceinline__ void tr_copy(const TreeArgs &a, const TrPlan &plan, TrPiece *pieces, uint32_t item_full,
                                         uint32_t item_empty, bool isv, uint32_t ring, uint32_t full, uint32_t empty,
-                                        uint4 *meta, volatile int *s_abort, int lane)
+                                        unsigned char *sb, volatile int *s_abort, int lane)
 {
-    using C = TrCfg<D>;
+    using C = TrCfg<D, E8>;
+    uint4 *meta = reinterpret_cast<uint4 *>(sb + C::OffMeta);
+    const uint8_t *exps = isv ? a.v_exp : a.k_exp;
     const int stages = isv ? C::NV : C::NK;
     const CUtensorMap *m16 = isv ? &a.tm_v16 : &a.tm_k16, *m1 = isv ? &a.tm_v1 : &a.tm_k1;
     int st = 0, seq = 0, errs = 0;
@@ -316,15 +333,27 @@ __device__ __forceinline__ void tr_copy(const TreeArgs &a, const TrPlan &plan, T
         if (k.end) break;
         const int col = k.h * D;
         const int32_t *tab = a.req_to_token + (int64_t)k.row * a.max_ctx;
-            int nx[4];
-            auto fetch = [&](int t) {
+        // a tile's table entries are requested while the tile before is copied, and (e4m3) its exponents, which hang on
+        // them, behind that one's copies
+        int nx[4], ex[4] = {0, 0, 0, 0};
+        auto fetch = [&](int t) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int p = t * kTrTile + 4 * lane + e;
+                nx[e] = ld_nc_ordered_s32_if(p < k.L, tab + (p < k.L ? p : 0));
+            }
+        };
+        auto fetch_exps = [&]() {
+            if constexpr (E8) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int p = t * kTrTile + 4 * lane + e;
-                    nx[e] = ld_nc_ordered_s32_if(p < k.L, tab + (p < k.L ? p : 0));
+                    const bool in = nx[e] >= 0 && nx[e] < a.size;
+                    ex[e] = in ? __ldcg(exps + (int64_t)(nx[e] >> a.block_shift) * a.Hkv + k.h) : 255;
                 }
-            };
-            fetch(k.t0);
+            }
+        };
+        fetch(k.t0);
+        fetch_exps();
 #pragma unroll 1
             for (int t = k.t0; t < k.t1 && go; ++t) {
                 int sl[4] = {nx[0], nx[1], nx[2], nx[3]};
@@ -334,7 +363,7 @@ __device__ __forceinline__ void tr_copy(const TreeArgs &a, const TrPlan &plan, T
                     go = false;
                     break;
                 }
-                const uint32_t dst = ring + st * C::TILE, fb = full + st * 8;
+                const uint32_t dst = ring + st * C::RAW, fb = full + st * 8;
                 bool ok[4];
                 uint32_t nib = 0;
 #pragma unroll
@@ -348,15 +377,26 @@ __device__ __forceinline__ void tr_copy(const TreeArgs &a, const TrPlan &plan, T
                 const bool run = nib == 15u && sl[0] == s0 + 4 * (lane & 3) && sl[1] == sl[0] + 1 && sl[2] == sl[0] + 2 &&
                                  sl[3] == sl[0] + 3;
                 const bool page = ((__ballot_sync(0xffffffffu, run) >> (lane & ~3)) & 0xFu) == 0xFu;
-                const bool none = ((__ballot_sync(0xffffffffu, nib != 0u) >> (lane & ~3)) & 0xFu) == 0u;
+                const unsigned has = __ballot_sync(0xffffffffu, nib != 0u);
+                const bool none = ((has >> (lane & ~3)) & 0xFu) == 0u;
+                int some = 0;              // a valid row of the tile
+                if constexpr (E8)
+                    some = __shfl_sync(0xffffffffu, nib & 1u ? sl[0] : nib & 2u ? sl[1] : nib & 4u ? sl[2] : sl[3],
+                                       has ? __ffs(has) - 1 : 0);
+                constexpr int HV = E8 ? 1 : C::HALVES, PITCH = E8 ? D : 128;     // boxes of a row, and their bytes
                 if (page || none) {
                     // a page's rows, or rows out of range, which read as zeros
                     if ((lane & 3) == 0) {
 #pragma unroll
-                        for (int hh = 0; hh < C::HALVES; ++hh)
-                            tma_load_2d(dst + hh * kTrHalf + (lane >> 2) * 16 * 128, m16, col + hh * 64,
+                        for (int hh = 0; hh < HV; ++hh)
+                            tma_load_2d(dst + hh * kTrHalf + (lane >> 2) * 16 * PITCH, m16, col + hh * 64,
                                         none ? a.total_rows : a.layer_row0 + sl[0], fb);
                     }
+                } else if constexpr (E8) {
+                    // a position without a row repeats a valid one of the tile: its exponent byte and its bit say so
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sl[e] = a.layer_row0 + (ok[e] ? sl[e] : some);
+                    tma_gather4(dst + lane * 4 * PITCH, m1, col, sl[0], sl[1], sl[2], sl[3], fb);
                 } else {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) sl[e] = ok[e] ? a.layer_row0 + sl[e] : a.total_rows;
@@ -378,8 +418,23 @@ __device__ __forceinline__ void tr_copy(const TreeArgs &a, const TrPlan &plan, T
                     if ((lane & 7) == 0) reinterpret_cast<uint32_t *>(meta + seq % kTrMeta)[lane >> 3] = w;
                     __syncwarp();
                 }
-                if (lane == 0) mbar_arrive_expect_tx(fb, C::TILE);
+                if constexpr (E8) {
+                    if (isv) {
+                        reinterpret_cast<uint32_t *>(sb + C::OffVE + st * 128)[lane] =
+                            (uint32_t)((ok[0] ? ex[0] : 255) | (ok[1] ? ex[1] : 255) << 8 | (ok[2] ? ex[2] : 255) << 16 |
+                                       (ok[3] ? ex[3] : 255) << 24);
+                    } else {
+                        // (an empty block's scale is 2^-126 in place of 0: a hidden column's minus infinity stays that)
+                        auto scale_of = [](int e) { return __uint_as_float((uint32_t)max(e, 1) << 23); };
+                        reinterpret_cast<float4 *>(sb + C::OffKS + seq % kTrMeta * 512)[lane] =
+                            make_float4(scale_of(ok[0] ? ex[0] : 0), scale_of(ok[1] ? ex[1] : 0), scale_of(ok[2] ? ex[2] : 0),
+                                        scale_of(ok[3] ? ex[3] : 0));
+                    }
+                    __syncwarp();
+                }
+                if (lane == 0) mbar_arrive_expect_tx(fb, C::RAW);
                 __syncwarp();
+                if (t + 1 < k.t1) fetch_exps();
                 ++seq;
                 if (++st == stages) {
                     st = 0;
@@ -431,9 +486,20 @@ __device__ __forceinline__ bool tr_tame(uint32_t tile, int lo, int hi, int lane)
     return any;
 }
 
+// Element d of a cached row (K, or V: their bytes and exponents) at `at` = (slot, head) D.
+template <bool E8>
+__device__ __forceinline__ float tr_element(const uint8_t *rows, const uint8_t *exps, int64_t at, int64_t block, int d)
+{
+    if constexpr (!E8) return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(rows)[at + d]);
+    const int e = exps[block];
+    float x, y;
+    e4m3x2_floats(rows[at + d], x, y);
+    return e == 0 && x == x ? 0.f : x * __uint_as_float((uint32_t)e << 23);
+}
+
 // What tr_tame took out, for one row of the piece (node i, query head hq) and 32 columns from d0 on: the parts of the
-// nodes' V rows in tiles [t0, t1) that hold a NaN or an infinity and that the node sees, weights relative to m2.
-template <int D>
+// nodes' V rows that hold a NaN or an infinity and that the node sees, weights relative to m2.
+template <int D, bool E8>
 __device__ __forceinline__ void tr_wild_rows(const TreeArgs &a, const TrPiece &q, int i, int hq, float m2, int d0,
                                              float (&o)[32])
 {
@@ -443,27 +509,26 @@ __device__ __forceinline__ void tr_wild_rows(const TreeArgs &a, const TrPiece &q
 #pragma unroll 1
     for (int j = max(c, q.t0 * kTrTile); j < min(q.L, q.t1 * kTrTile); ++j) {
         const int slot = __ldg(tab + j);
-        if (slot < 0 || slot >= a.size) continue;
-        const int64_t at = ((int64_t)slot * a.Hkv + q.h) * D;
-        const __nv_bfloat16 *kr = reinterpret_cast<const __nv_bfloat16 *>(a.k) + at, *vr = reinterpret_cast<const __nv_bfloat16 *>(a.v) + at;
+        if (slot < 0 || slot >= a.size || !(tr_seen(a, q.q0 + i, i, j - c) & 1u)) continue;
+        const int64_t at = ((int64_t)slot * a.Hkv + q.h) * D, block = (int64_t)(slot >> a.block_shift) * a.Hkv + q.h;
         bool wild = false;
 #pragma unroll 1
-        for (int d = 0; d < D; d += 8) wild |= tr_wild(__ldg(reinterpret_cast<const uint4 *>(vr + d)));
-        if (!wild || !(tr_seen(a, q.q0 + i, i, j - c) & 1u)) continue;
+        for (int d = 0; d < D; ++d) wild |= !isfinite(tr_element<E8>(a.v, a.v_exp, at, block, d));
+        if (!wild) continue;
         float s = 0.f;
 #pragma unroll 1
-        for (int d = 0; d < D; ++d) s = fmaf(__bfloat162float(qr[d]), __bfloat162float(kr[d]), s);
+        for (int d = 0; d < D; ++d) s = fmaf(__bfloat162float(qr[d]), tr_element<E8>(a.k, a.k_exp, at, block, d), s);
         const float p = tr_ex2(fmaf(a.negate ? -s : s, a.scale_log2, -m2));
 #pragma unroll
-        for (int d = 0; d < 32; ++d) o[d] = fmaf(p, __bfloat162float(vr[d0 + d]), o[d]);
+        for (int d = 0; d < 32; ++d) o[d] = fmaf(p, tr_element<E8>(a.v, a.v_exp, at, block, d0 + d), o[d]);
     }
 }
 
 // ----------------------------------------------------------------- kernel
-template <int D>
+template <int D, bool E8>
 __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_constant__ TreeArgs a)
 {
-    using C = TrCfg<D>;
+    using C = TrCfg<D, E8>;
     extern __shared__ unsigned char smem_raw[];
     __shared__ int s_w[kTrThreads / 32];
     __shared__ int s_abort_storage;
@@ -481,11 +546,12 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid < C::N_BARS) {
-        const bool softmax = (tid >= C::P_READY && tid < C::O_FULL) || (tid >= C::O_FREE && tid < C::Q_FULL);
-        const bool empty = (tid >= C::K_EMPTY && tid < C::V_FULL) || (tid >= C::V_EMPTY && tid < C::S_FULL);
-        mbar_init(bar(tid), softmax ? 128u : empty ? 2u : tid >= C::ITEM_EMPTY ? (uint32_t)kTrReaders : 1u);
+        const bool softmax = (tid >= C::P_READY && tid < C::O_FULL) || (tid >= C::O_FREE && tid < C::Q_FULL) ||
+                             (tid >= C::Q_SPLIT && tid < C::JOINT);
+        const bool kempty = tid >= C::K_EMPTY && tid < C::V_FULL, vempty = tid >= C::V_EMPTY && tid < C::S_FULL;
+        mbar_init(bar(tid), softmax ? 128u : kempty ? 2u : vempty ? (E8 ? 8u : 2u)
+                                           : tid >= C::ITEM_EMPTY ? (uint32_t)kTrReaders : 1u);
     }
-    static_assert(C::N_BARS <= 64, "two warps initialise the barriers");
     if (warp < 2) fence_mbar_init();
     if (tid >= 64 && tid < 80) s_wild[(tid >> 3) & 1][tid & 7] = 0;
     if (tid == 0) {
@@ -581,14 +647,14 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
 
     if (warp == 8 || warp == 9) {
         const bool isv = warp == 9;
-        tr_copy<D>(a, plan, s_piece, bar(C::ITEM_FULL), bar(C::ITEM_EMPTY), isv, base + (isv ? C::OffV : C::OffK), bar(isv ? C::V_FULL : C::K_FULL),
-                   bar(isv ? C::V_EMPTY : C::K_EMPTY), meta, s_abort, lane);
+        tr_copy<D, E8>(a, plan, s_piece, bar(C::ITEM_FULL), bar(C::ITEM_EMPTY), isv, base + (isv ? C::OffV : C::OffK),
+                       bar(isv ? C::V_FULL : C::K_FULL), bar(isv ? C::V_EMPTY : C::K_EMPTY), sb, s_abort, lane);
     } else if (warp >= 10) {
         // ======================================================= products
         // A warp per stream: while one waits for its weights, the tensor core has the other's products.
         const int X = warp - 10;
         const uint32_t sQ = base, sK = base + C::OffK, sV = base + C::OffV;
-        const uint32_t id_s = C::kIdS | (a.negate ? 1u << 13 : 0u);   // bit 13: A negated
+        const uint32_t id_s = C::kIdS | (!E8 && a.negate ? 1u << 13 : 0u);   // bit 13: A negated
         int seq = 0, piece = 0, px = 0, pq = 0, p2 = 0, pj = 0;   // token tiles, pieces before; this stream's steps, pieces; of
                                                                   // stream B: those with rows of its own, and with A's
         bool bad = false;
@@ -611,7 +677,18 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
                     if (!two) umma_commit(b);
                 };
                 auto qk = [&](int st) {
-                    const uint32_t q = sQ + (two ? X : 0) * C::TILE, kk = sK + st * C::TILE;
+                    const uint32_t q = sQ + (two ? X : 0) * C::TILE, kk = sK + st * C::RAW;
+                    if constexpr (E8) {
+                        // both terms of q against the same keys, 32 of D a step; D = 64: the terms share a 128-byte row
+#pragma unroll
+                        for (int s = 0; s < D / 16; ++s) {
+                            constexpr int SPT = D / 32;
+                            const int term = s / SPT, o = (s % SPT) * 32;
+                            const uint64_t kd = D == 128 ? smem_desc_sw128(kk + o, 16, 1024) : smem_desc_sw64(kk + o, 16, 512);
+                            umma_ss_f8(tmem + X * 128, smem_desc_sw128(q + term * (D == 128 ? kTrHalf : 64) + o, 16, 1024), kd,
+                                       id_s, s > 0);
+                        }
+                    } else
 #pragma unroll
                     for (int s = 0; s < D / 16; ++s)
                         umma_ss(tmem + X * 128, smem_desc_sw128(q + (s >> 2) * kTrHalf + (s & 3) * 32, 16, 1024),
@@ -624,10 +701,10 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
                     const int s = seq + (two ? 0 : X), st = s % C::NK;
                     // (stream B hears of A's Q from A's warp: it does not follow every phase of that barrier)
                     if (X == 0) {
-                        wait(bar(C::Q_FULL), piece & 1);
+                        wait(bar(E8 ? C::Q_SPLIT : C::Q_FULL), piece & 1);
                         if (!two && N > 1 && lane == 0) mbar_arrive(bar(C::JOINT));
                     } else {
-                        wait(two ? bar(C::Q_FULL + 1) : bar(C::JOINT), (two ? p2 : pj) & 1);
+                        wait(two ? bar((E8 ? C::Q_SPLIT : C::Q_FULL) + 1) : bar(C::JOINT), (two ? p2 : pj) & 1);
                         if (two) ++p2;
                         else ++pj;
                     }
@@ -639,11 +716,12 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
 #pragma unroll 1
                 for (int t = two ? 0 : X; t < nt; t += dt, ++px) {
                     const int s = seq + t, st = s % C::NV, sk = (s + dt) % C::NK;
-                    const uint32_t vt = sV + st * C::TILE;
-                    wait(bar(C::V_FULL + st), (s / C::NV) & 1);
+                    // (e4m3: the softmax warpgroup has widened V into the stream's buffer when the weights are there)
+                    const uint32_t vt = E8 ? base + C::OffWide + X * C::TILE : sV + st * C::RAW;
+                    if constexpr (!E8) wait(bar(C::V_FULL + st), (s / C::NV) & 1);
                     // drafted tokens' rows must not hold what a weight of 0 does not cancel
                     const int p0 = (k.t0 + t) * kTrTile, lo = max(0, c - p0), hi = min(kTrTile, k.L - p0);
-                    if (lo < hi) {
+                    if (!E8 && lo < hi) {
                         if (X == 0 || !two) {
                             if (!bad && tr_tame<D>(vt, lo, hi, lane)) {
                                 if (lane == 0) *(volatile int *)&s_wild[X][piece & 7] = piece + 1;
@@ -663,7 +741,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
                         for (int kk = 0; kk < kTrTile / 16; ++kk)
                             umma_ts(tmem + C::ColO + X * D, tmem + X * 128 + kk * 8,
                                     smem_desc_sw128(vt + kk * 2048, kTrHalf, 1024), C::kIdPV, kk > 0 || t >= dt);
-                        release(bar(C::V_EMPTY + st));
+                        if constexpr (!E8) release(bar(C::V_EMPTY + st));
                         if (t + dt < nt) qk(sk);
                         else umma_commit(bar(C::O_FULL + X));
                     }
@@ -682,8 +760,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
         const int X = warp >> 2, row = tid & 127;
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_addr = tmem + lane_base + X * 128;
-        const float sl2 = a.scale_log2;
-        int piece = 0, sx = 0, ox = 0, kseq = 0;   // pieces, steps, ends of this stream, token tiles
+        int piece = 0, sx = 0, ox = 0, kseq = 0, p2 = 0;   // pieces, steps, ends of this stream, token tiles, pairs
         int qloads = 0;
         bool bad = false;
         auto wait = [&](uint32_t b, uint32_t parity) {
@@ -712,11 +789,24 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
                 const int nd = (row * a.inv_g) >> 16, node = (2 * k.pair + (two ? X : 0)) * a.tq + nd;
                 const bool live = nd < a.tq && node < k.n;
                 const int64_t qrow = k.q0 + node;
+                float sl2 = a.scale_log2;
                 if (a.wait_ns == 0 && !bad) {
                     // a wait limit of 0: give up at the first piece, as a timed-out wait would
                     *s_abort = 1;
                     set_error(a.err, PA_DEVERR_TIMEOUT);
                     bad = true;
+                }
+                if constexpr (E8) {
+                    // this thread's row of q, in place, into its two e4m3 terms; the row's scale joins the softmax scale
+                    if (X == 0 || two) {
+                        wait(bar(C::Q_FULL + X), (X == 0 ? piece : p2) & 1);
+                        const float qs = split_q_row<D>(base + X * C::TILE, row, a.negate ? -1.f : 1.f);
+                        if (X == 0) reinterpret_cast<float *>(sb + C::OffQS)[row] = qs;
+                        fence_proxy_async_smem();
+                        mbar_arrive(bar(C::Q_SPLIT + X));
+                        sl2 = tr_scale(sl2 * qs);
+                    }
+                    p2 += two;
                 }
                 float m = -INFINITY, l = 0.f;      // maximum of s (not yet scaled), sum
 #pragma unroll 1
@@ -735,12 +825,41 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
                     wait(bar(C::S_FULL + X), sx & 1);
                     tc_fence_after();
                     const uint4 valid = meta[(kseq + t) % kTrMeta];
+                    if constexpr (E8) {
+                        if (i == 1 && X == 1 && !two) sl2 = tr_scale(sl2 * reinterpret_cast<const float *>(sb + C::OffQS)[row]);
+                        // V in bf16 with its scales, 32 rows a warp.  The stream's product before this step is done (S is
+                        // behind it), so its buffer is free
+                        const int s = kseq + t, st = s % C::NV, r0 = (warp & 3) * 32;
+                        const uint32_t wide = base + C::OffWide + X * C::TILE;
+                        wait(bar(C::V_FULL + st), (s / C::NV) & 1);
+                        widen_e4m3_tile<D, true>(base + C::OffV + st * C::RAW, wide, lane, sb + C::OffVE + st * 128, r0, r0 + 32);
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(bar(C::V_EMPTY + st));
+                            if (!two) mbar_arrive(bar(C::V_EMPTY + st));
+                        }
+                        const int lo = max(c - p0, r0), hi = min(k.L - p0, r0 + 32);
+                        if (lo < hi && tr_tame<D>(wide, lo, hi, lane) && lane == 0) *(volatile int *)&s_wild[X][piece & 7] = piece + 1;
+                        fence_proxy_async_smem();
+                    }
                     const bool masked = nodes || (valid.x & valid.y & valid.z & valid.w) != ~0u;
                     seen[0] &= valid.x, seen[1] &= valid.y, seen[2] &= valid.z, seen[3] &= valid.w;
                     uint32_t r[128];
 #pragma unroll
                     for (int ch = 0; ch < 4; ++ch) tmem_ld32(s_addr + ch * 32, *reinterpret_cast<uint32_t(*)[32]>(&r[ch * 32]));
                     tmem_wait_ld();
+                    if constexpr (E8) {
+                        // a column's key scale
+                        const float4 *ks = reinterpret_cast<const float4 *>(sb + C::OffKS + (kseq + t) % kTrMeta * 512);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            const float4 f = ks[j];
+                            r[4 * j] = __float_as_uint(__uint_as_float(r[4 * j]) * f.x);
+                            r[4 * j + 1] = __float_as_uint(__uint_as_float(r[4 * j + 1]) * f.y);
+                            r[4 * j + 2] = __float_as_uint(__uint_as_float(r[4 * j + 2]) * f.z);
+                            r[4 * j + 3] = __float_as_uint(__uint_as_float(r[4 * j + 3]) * f.w);
+                        }
+                    }
                     if (masked) {
 #pragma unroll
                         for (int j = 0; j < 128; ++j)
@@ -842,7 +961,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
 #pragma unroll
                             for (int j = 0; j < 32; ++j) o[j] = __uint_as_float(ob[j]);
                         }
-                        if (wild && live) tr_wild_rows<D>(a, k, node, hq, m2 == -INFINITY ? 0.f : m2, ch * 32, o);
+                        if (wild && live) tr_wild_rows<D, E8>(a, k, node, hq, m2 == -INFINITY ? 0.f : m2, ch * 32, o);
                         if (live && !bad && whole) {
 #pragma unroll
                             for (int j = 0; j < 32; j += 8) {
@@ -999,90 +1118,6 @@ __global__ void __launch_bounds__(kTrMergeThreads) tree_merge_kernel(const __gri
     }
 }
 
-template <int D, bool E8>
-__device__ __forceinline__ void load_row(const uint8_t *rows, const uint8_t *exps, int64_t slot, int Hkv, int h, int shift,
-                                         int lane, float (&x)[D / 32])
-{
-    constexpr int N = D / 32;
-    const int64_t at = (slot * Hkv + h) * D + lane * N;
-    if constexpr (E8) {
-        const int e = exps[(slot >> shift) * Hkv + h];
-        const float sc = e == 0 ? 0.f : __uint_as_float((uint32_t)e << 23);
-#pragma unroll
-        for (int i = 0; i < N; i += 2) {
-            e4m3x2_floats(*reinterpret_cast<const uint16_t *>(rows + at + i), x[i], x[i + 1]);
-            x[i] *= sc;
-            x[i + 1] *= sc;
-        }
-    } else {
-        const __nv_bfloat16 *r = reinterpret_cast<const __nv_bfloat16 *>(rows) + at;
-#pragma unroll
-        for (int i = 0; i < N; ++i) x[i] = __bfloat162float(r[i]);
-    }
-}
-
-template <int D, bool E8>
-__global__ void __launch_bounds__(256) tree_attn_simple_kernel(const TreeArgs a)
-{
-    constexpr int N = D / 32;
-    pdl_wait();
-    pdl_launch_dependents();
-    const int lane = threadIdx.x & 31, r = blockIdx.y;
-    const int q0 = __ldg(a.qo_indptr + r), q1 = __ldg(a.qo_indptr + r + 1), n = q1 - q0;
-    if (n <= 0 || q0 < 0 || q1 > a.T) {
-        if (n != 0) set_error(a.err, PA_DEVERR_LEN);
-        return;
-    }
-    int L = __ldg(a.seq_lens + r);
-    const int row = __ldg(a.req_pool_indices + r);
-    int bits = 0;
-    if (row < 0 || row >= a.req_rows) bits |= PA_DEVERR_ROW;
-    if (L < n || L > a.max_ctx || (a.tree_mask && n > 32 * (int64_t)a.mask_words)) bits |= PA_DEVERR_LEN;
-    if (bits) {
-        set_error(a.err, bits);
-        L = 0;
-    }
-    const int c = L - n;
-    const int32_t *tab = a.req_to_token + (int64_t)(bits ? 0 : row) * a.max_ctx;
-    for (int64_t w = blockIdx.x * 8 + (threadIdx.x >> 5); w < (int64_t)n * a.Hq; w += gridDim.x * 8) {
-        const int i = (int)(w / a.Hq), hq = (int)(w % a.Hq), h = hq / a.G;
-        const int64_t at = ((int64_t)(q0 + i) * a.Hq + hq) * D + lane * N;
-        float q[N], o[N], m = -INFINITY, l = 0.f;
-#pragma unroll
-        for (int e = 0; e < N; ++e) q[e] = __bfloat162float(a.q[at + e]), o[e] = 0.f;
-        for (int j = 0; j < L; ++j) {
-            if (j >= c) {
-                const int k = j - c;
-                const bool seen = a.tree_mask ? a.tree_mask[(int64_t)(q0 + i) * a.mask_words + (k >> 5)] >> (k & 31) & 1 : k <= i;
-                if (!seen) continue;
-            }
-            const int slot = tab[j];
-            if (slot < 0 || slot >= a.size) {
-                set_error(a.err, PA_DEVERR_SLOT);
-                continue;
-            }
-            float x[N], s = 0.f;
-            load_row<D, E8>(a.k, a.k_exp, slot, a.Hkv, h, a.block_shift, lane, x);
-#pragma unroll
-            for (int e = 0; e < N; ++e) s = fmaf(q[e], x[e], s);
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-            s *= a.scale_log2;
-            const float mn = fmaxf(m, s), mz = mn == -INFINITY ? 0.f : mn;
-            const float f = exp2f(m - mz), p = exp2f(s - mz);
-            l = l * f + p;
-            m = mn;
-            if (p == 0.f && s == -INFINITY) continue;
-            load_row<D, E8>(a.v, a.v_exp, slot, a.Hkv, h, a.block_shift, lane, x);
-#pragma unroll
-            for (int e = 0; e < N; ++e) o[e] = fmaf(p, x[e], o[e] * f);
-        }
-#pragma unroll
-        for (int e = 0; e < N; ++e) a.out[at + e] = __float2bfloat16_rn(l != 0.f ? o[e] / l : 0.f);
-    }
-}
-
-
 // --------------------------------------------------------------- host side
 // Workspace: header, then two slots of partials per unit that shares segments.
 struct TrWs {
@@ -1105,24 +1140,24 @@ static int tr_ranges(int grid, int Hkv)
     return r2 * Hkv > 2 * r1 * Hkv + grid / 16 ? r2 : r1;
 }
 
-template <int D>
+template <int D, bool E8>
 static pa_status tr_launch(const TreeArgs &a, cudaStream_t st)
 {
-    auto kern = tree_attn_kernel<D>;
-    if (!ensure_dynamic_smem(reinterpret_cast<const void *>(kern), TrCfg<D>::Smem)) return PA_ERR_CUDA;
+    auto kern = tree_attn_kernel<D, E8>;
+    constexpr int smem = TrCfg<D, E8>::Smem;
+    if (!ensure_dynamic_smem(reinterpret_cast<const void *>(kern), smem)) return PA_ERR_CUDA;
     const int grid = num_sms() < kTrMaxCtas ? num_sms() : kTrMaxCtas;
     TreeArgs b = a;
     b.ranges = tr_ranges(grid, a.Hkv);
-    if (launch_kernel(kern, dim3(grid), dim3(kTrThreads), TrCfg<D>::Smem, st, b) != cudaSuccess) return PA_ERR_CUDA;
+    if (launch_kernel(kern, dim3(grid), dim3(kTrThreads), smem, st, b) != cudaSuccess) return PA_ERR_CUDA;
     if (b.ranges > 1) {
         // behind this call's own kernel, whose end it waits for: overlapped whatever the mode
         auto merge = tree_merge_kernel<D>;
-        const size_t smem = ((size_t)2 * a.R + 1) * 4;
         const int64_t want = ((int64_t)a.T * a.Hq * (D / 16) + kTrMergeThreads - 1) / kTrMergeThreads;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(want < 4 * grid ? want : 4 * grid));
         cfg.blockDim = dim3(kTrMergeThreads);
-        cfg.dynamicSmemBytes = smem;
+        cfg.dynamicSmemBytes = ((size_t)2 * a.R + 1) * 4;
         cfg.stream = st;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1176,13 +1211,17 @@ extern "C" pa_status pa_paged_tree_attn(const void *q, int n_tokens, int n_q_hea
         return PA_ERR_ALIGN;
     TreeArgs a;
     memset(&a, 0, sizeof a);
-    const int row_bytes = s.head_dim * (e4m3 ? 1 : 2), sw = row_bytes < 128 ? row_bytes : 128;
+    // rows as the tensor core takes them, but an e4m3 cache's V, which is widened, as they are
     const cuuint64_t inner = (cuuint64_t)s.n_kv_heads * s.head_dim, rows = (cuuint64_t)s.n_layers * s.size;
-    const cuuint32_t box = sw / (e4m3 ? 1 : 2);
+    const cuuint32_t box = e4m3 ? s.head_dim : 64, box16[2] = {box, 16}, box1[2] = {box, 1};
+    const int sw = e4m3 ? s.head_dim : 128;
+    const cuuint64_t dims[2] = {inner, rows}, strides[1] = {inner};
     if (!encode_tmap_rows(&a.tm_k16, k_buf, !e4m3, inner, rows, box, 16, sw) ||
-        !encode_tmap_rows(&a.tm_k1, k_buf, !e4m3, inner, rows, box, 1, sw) ||
-        !encode_tmap_rows(&a.tm_v16, v_buf, !e4m3, inner, rows, box, 16, sw) ||
-        !encode_tmap_rows(&a.tm_v1, v_buf, !e4m3, inner, rows, box, 1, sw))
+        !encode_tmap_rows(&a.tm_k1, k_buf, !e4m3, inner, rows, box, 1, sw))
+        return PA_ERR_CUDA;
+    if (e4m3 ? !encode_tmap_u8(&a.tm_v16, v_buf, 2, dims, strides, box16) || !encode_tmap_u8(&a.tm_v1, v_buf, 2, dims, strides, box1)
+             : !encode_tmap_rows(&a.tm_v16, v_buf, true, inner, rows, box, 16, sw) ||
+                   !encode_tmap_rows(&a.tm_v1, v_buf, true, inner, rows, box, 1, sw))
         return PA_ERR_CUDA;
     {
         const cuuint64_t dims[3] = {(cuuint64_t)s.head_dim, (cuuint64_t)n_q_heads, (cuuint64_t)n_tokens};
@@ -1230,11 +1269,6 @@ extern "C" pa_status pa_paged_tree_attn(const void *q, int n_tokens, int n_q_hea
     a.negate = scale < 0.f;
     // a scale of 0 as one that no score survives: a hidden key's minus infinity stays what it is
     if (a.scale_log2 < 0x1p-126f) a.scale_log2 = 0x1p-126f;
-    if (!e4m3) return s.head_dim == 64 ? tr_launch<64>(a, st) : tr_launch<128>(a, st);
-    a.scale_log2 = (float)((double)scale * 1.4426950408889634);
-    const dim3 grid(256, n_reqs);
-    const cudaError_t rc = s.head_dim == 64 ? launch_kernel(tree_attn_simple_kernel<64, true>, grid, dim3(256), 0, st, a)
-                                            : launch_kernel(tree_attn_simple_kernel<128, true>, grid, dim3(256), 0, st, a);
-    if (rc != cudaSuccess) return PA_ERR_CUDA;
-    return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    if (e4m3) return s.head_dim == 64 ? tr_launch<64, true>(a, st) : tr_launch<128, true>(a, st);
+    return s.head_dim == 64 ? tr_launch<64, false>(a, st) : tr_launch<128, false>(a, st);
 }

@@ -34,7 +34,8 @@ def mask_words(seen, words):
 
 def attention(q, k, v, scale, seen, terms=0.0):
     """q [m, Hq, D] of the last m of n cached tokens, k, v [n, Hkv, D] in doubles, seen [m, m]: the output and what its
-    error is measured in (as the other references': sum p |v|, the largest score error `ds` that fp32 products allow).
+    error is measured in (as the other references': sum p |v|, the largest score error `ds` that fp32 products allow and
+    q's terms, which leave out up to `terms` of its row's largest element).
     A row that is not seen enters nothing, whatever it holds."""
     m, Hq, D = q.shape
     n, Hkv, _ = k.shape
@@ -55,7 +56,8 @@ def attention(q, k, v, scale, seen, terms=0.0):
         out[i] = torch.einsum("hn,nhd->hd", p, vv)
         mean[i] = torch.einsum("hn,nhd->hd", p, vv.abs())
         pmax[i] = p.amax(-1)
-        ds[i] = (2.0 ** -20 * mag + 2.0 ** -22 * x.abs()).amax(-1)
+        top = q[i].abs().amax(-1)[:, None] * kk.abs().sum(-1).T * abs(scale)
+        ds[i] = (2.0 ** -20 * mag + 2.0 ** -22 * x.abs() + terms * top).amax(-1)
         vmax = max(vmax, float(vv.abs().max()))
     return dict(out=out, mean=mean, ds=ds, pmax=pmax, vmax=vmax, n=n, p=None)
 

@@ -13,6 +13,10 @@ from test_gpu_weights_evict import Bf16Cache
 
 pytestmark = pytest.mark.gpu
 P_BITS = 8      # the weights enter the second product in bf16: off by at most 2^-8, relative
+# over an e4m3 cache q, scaled so that its row's largest element lies in (224, 448], is a sum of two e4m3 terms.  A bf16
+# number y of exponent e has 8 significant bits, the first term leaves a multiple of 2^(e - 7) of at most 2^(e - 4), which
+# the second holds where e >= -2; below, its steps of 2^-9 leave at most 2^-10 out: 2^-10 / 224 < 2^-17 of the largest
+TERMS = 2.0 ** -17
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -66,7 +70,7 @@ def check(c, q, out, scale, seen, what, reqs=None):
         if lo == hi:
             continue
         k, v = c.values(r)
-        ref = S.attention(q[lo:hi].double(), k, v, scale, seen[r])
+        ref = S.attention(q[lo:hi].double(), k, v, scale, seen[r], terms=TERMS if c.block else 0.0)
         R.check_out(out[lo:hi].cpu(), ref, P_BITS, f"{what}, request {r}: {hi - lo} of {len(k)}")
 
 
@@ -189,7 +193,8 @@ def test_hidden_rows_may_hold_anything(block, what, operand):
         lo = c.qo[r]
         k, v = c.values(r)
         blind = [i for i in range(c.nodes[r]) if not seen[r][i, b]]
-        ref = S.attention(q[lo:c.qo[r + 1]].double(), k.nan_to_num(1.0, 1.0), v.nan_to_num(1.0, 1.0), 0.05, seen[r])
+        ref = S.attention(q[lo:c.qo[r + 1]].double(), k.nan_to_num(1.0, 1.0), v.nan_to_num(1.0, 1.0), 0.05, seen[r],
+                          terms=TERMS if block else 0.0)
         part = {x: (y[blind] if torch.is_tensor(y) and y.dim() > 1 else y) for x, y in ref.items()}
         R.check_out(out[lo:c.qo[r + 1]][blind], part, P_BITS, f"{what} in {operand}")
         for i in range(c.nodes[r]):
@@ -268,7 +273,8 @@ def test_bad_requests_and_slots(block):
                 vis = torch.cat([torch.ones(100, dtype=torch.bool), s2[i]])
                 vis[at] = False
                 j = vis.nonzero()[:, 0]
-                ref = S.attention(q[4 + i:5 + i].double(), k[j], v[j], 0.05, torch.ones((1, 1), dtype=torch.bool))
+                ref = S.attention(q[4 + i:5 + i].double(), k[j], v[j], 0.05, torch.ones((1, 1), dtype=torch.bool),
+                                  terms=TERMS if block else 0.0)
                 R.check_out(out[4 + i:5 + i].cpu(), ref, P_BITS, f"slot {bad} at {at}")
             assert len(keep) == 103
     qo = c.qo
