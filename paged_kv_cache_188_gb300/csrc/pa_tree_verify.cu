@@ -25,11 +25,10 @@
 namespace pa {
 namespace cg = cooperative_groups;
 
-constexpr int kVfThreads = 512;
-constexpr int kVfWarps = kVfThreads / 32;
 constexpr int kVfMaxNodes = 1024;
 constexpr int kVfMaxCluster = 8;
 constexpr int kVfAhead = 4;              // chunks of four probabilities that a lane has on their way
+constexpr int kVfGroups = 8;             // running sums kept of a warp's piece, so that little of it is looked through again
 
 struct VerifyArgs {
     const float *p, *f;
@@ -43,8 +42,38 @@ typedef unsigned long long u64;
 
 // a probability: NaN and negative numbers are 0
 __device__ __forceinline__ float prob(float x) { return x > 0.f ? x : 0.f; }
-// in whole steps of 2^-48, nearest even (the product is exact or overflows)
-__device__ __forceinline__ u64 steps(float x) { return __float2ull_rn(x * 0x1p48f); }
+
+// Whole steps of 2^-48, nearest even, without the conversion to 64 bits (83 cycles a warp: a row of 131072 took 13 us
+// in it).  Below 2, adding a power of two leaves w rounded to that sum's last place in its low bits, and what is left
+// over is exact: three such sums take 22, 22 and 4 bits.  The words are added as they are; what the powers of two
+// contribute is taken off at the end.
+struct Steps {
+    uint32_t hi, mid, lo;
+};
+constexpr uint32_t kOneHi = 0x40000000u, kOneMid = 0x35400000u, kOneLo = 0x33400000u;   // 2, 1.5 2^-21, 1.5 2^-25
+__device__ __forceinline__ void steps_add(Steps &s, float w)
+{
+    const float m1 = __uint_as_float(kOneHi), m2 = __uint_as_float(kOneMid), m3 = __uint_as_float(kOneLo);
+    const float t1 = __fadd_rn(w, m1), r1 = __fsub_rn(w, __fsub_rn(t1, m1));         // places of 2^-22
+    const float t2 = __fadd_rn(r1, m2), r2 = __fsub_rn(r1, __fsub_rn(t2, m2));       // 2^-44
+    const float t3 = __fadd_rn(r2, m3);                                             // 2^-48
+    s.hi += __float_as_uint(t1);
+    s.mid += __float_as_uint(t2);
+    s.lo += __float_as_uint(t3);
+}
+// of n additions (at most 1024 of values below 2: 22 + 10 bits)
+__device__ __forceinline__ u64 steps_sum(const Steps &s, uint32_t n)
+{
+    const long long mid = (int32_t)(s.mid - n * kOneMid), lo = (int32_t)(s.lo - n * kOneLo);
+    return ((u64)(s.hi - n * kOneHi) << 26) + (u64)((mid << 4) + lo);
+}
+__device__ __forceinline__ u64 steps(float w)
+{
+    if (!(w < 2.f)) return __float2ull_rn(w * 0x1p48f);
+    Steps s{0, 0, 0};
+    steps_add(s, w);
+    return steps_sum(s, 1);
+}
 
 // The row that is summed: w of row `row` after the refusals behind it.
 struct VfRow {
@@ -68,50 +97,61 @@ __device__ __forceinline__ float4 vf_load(const float *row, int c, int lead, int
     return r;
 }
 
-// w of the four elements of chunk c, from their probabilities
-__device__ __forceinline__ void vf_weights(const VfRow &r, int c, const float4 &p4, const float4 &f4, float (&w)[4])
+// w of the four elements of a chunk, from their probabilities (chosen tokens are not taken out here)
+__device__ __forceinline__ void vf_weights(const VfRow &r, const float4 &p4, const float4 &f4, float (&w)[4])
 {
     w[0] = prob(p4.x), w[1] = prob(p4.y), w[2] = prob(p4.z), w[3] = prob(p4.w);
     if (r.f) {
         const float f[4] = {prob(f4.x), prob(f4.y), prob(f4.z), prob(f4.w)};
+#pragma unroll 1
         for (int j = 0; j < r.refused; ++j) {
             const float z = r.z[j];
 #pragma unroll
             for (int e = 0; e < 4; ++e) w[e] = prob(__fsub_rn(w[e], __fmul_rn(z, f[e])));
         }
-    } else {
-        for (int j = 0; j < r.refused; ++j) {
-            const int d = r.x[j] - (4 * c - r.lead);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (d == e) w[e] = 0.f;
-        }
     }
 }
 
-// The sum of a warp's chunks c0 .. c1, every lane has it.
-__device__ __forceinline__ u64 vf_sum(const VfRow &r, int c0, int c1, int lane)
+// The sum of a warp's chunks c0 .. c1, every lane has it.  groups[g]: of the chunks in front of c0 + g stride.
+__device__ __forceinline__ u64 vf_sum(const VfRow &r, int c0, int c1, int stride, u64 *groups, int lane)
 {
     u64 sum = 0;
 #pragma unroll 1
-    for (int c = c0 + lane; c < c1; c += 32 * kVfAhead) {
-        float4 p4[kVfAhead], f4[kVfAhead];
+    for (int cb = c0, g = 0; cb < c1; ++g) {
+        if (lane == 0) groups[g] = sum;
+        u64 mine = 0;
+#pragma unroll 1
+        for (const int end = min(c1, cb + stride); cb < end; cb += 32 * kVfAhead) {
+            const int c = cb + lane;
+            float4 p4[kVfAhead], f4[kVfAhead];
 #pragma unroll
-        for (int i = 0; i < kVfAhead; ++i) {
-            const int cc = c + 32 * i;
-            p4[i] = cc < c1 ? vf_load(r.p, cc, r.lead, r.V) : make_float4(0.f, 0.f, 0.f, 0.f);
-            f4[i] = cc < c1 && r.f ? vf_load(r.f, cc, r.lead, r.V) : make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int i = 0; i < kVfAhead; ++i) {
+                const int cc = c + 32 * i;
+                p4[i] = cc < end ? vf_load(r.p, cc, r.lead, r.V) : make_float4(0.f, 0.f, 0.f, 0.f);
+                f4[i] = cc < end && r.f ? vf_load(r.f, cc, r.lead, r.V) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            Steps s{0, 0, 0};
+            uint32_t n = 0;
+#pragma unroll
+            for (int i = 0; i < kVfAhead; ++i) {
+                float w[4];
+                vf_weights(r, p4[i], f4[i], w);
+                if (fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3])) < 2.f) {
+                    n += 4;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) steps_add(s, w[e]);
+                } else {
+                    // (no probability)
+                    mine += steps(w[0]) + steps(w[1]) + steps(w[2]) + steps(w[3]);
+                }
+            }
+            mine += steps_sum(s, n);
         }
+        cb = min(c1, c0 + (g + 1) * stride);
 #pragma unroll
-        for (int i = 0; i < kVfAhead; ++i) {
-            float w[4];
-            vf_weights(r, c + 32 * i, p4[i], f4[i], w);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sum += steps(w[e]);
-        }
+        for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+        sum += mine;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     return sum;
 }
 
@@ -119,42 +159,61 @@ __device__ __forceinline__ u64 vf_sum(const VfRow &r, int c0, int c1, int lane)
 __device__ __forceinline__ int vf_find(const VfRow &r, int c0, int c1, u64 run, u64 goal, int lane)
 {
 #pragma unroll 1
-    for (int cb = c0; cb < c1; cb += 32) {
-        const int c = cb + lane;
-        float w[4] = {0.f, 0.f, 0.f, 0.f};
-        if (c < c1)
-            vf_weights(r, c, vf_load(r.p, c, r.lead, r.V),
-                       r.f ? vf_load(r.f, c, r.lead, r.V) : make_float4(0.f, 0.f, 0.f, 0.f), w);
-        u64 s[4];
+    for (int cb = c0; cb < c1; cb += 32 * kVfAhead) {
+        float4 p4[kVfAhead], f4[kVfAhead];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[e] = steps(w[e]);
-        const u64 mine = s[0] + s[1] + s[2] + s[3];
-        u64 incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const u64 y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
+        for (int i = 0; i < kVfAhead; ++i) {
+            const int c = cb + 32 * i + lane;
+            p4[i] = c < c1 ? vf_load(r.p, c, r.lead, r.V) : make_float4(0.f, 0.f, 0.f, 0.f);
+            f4[i] = c < c1 && r.f ? vf_load(r.f, c, r.lead, r.V) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        const unsigned hit = __ballot_sync(0xffffffffu, run + incl > goal);
-        if (hit) {
-            const int src = __ffs(hit) - 1;
-            u64 at = run + incl - mine;
-            int v = 4 * c - r.lead;
 #pragma unroll
-            for (int e = 0; e < 3; ++e) {
-                at += s[e];
-                if (at > goal) break;
-                ++v;
+        for (int i = 0; i < kVfAhead; ++i) {
+            const int c = cb + 32 * i + lane;
+            float w[4];
+            vf_weights(r, p4[i], f4[i], w);
+            if (!r.f) {
+#pragma unroll 1
+                for (int j = 0; j < r.refused; ++j) {
+                    const int d = r.x[j] - (4 * c - r.lead);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (d == e) w[e] = 0.f;
+                }
             }
-            return __shfl_sync(0xffffffffu, v, src);
+            u64 s[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[e] = steps(w[e]);
+            const u64 mine = s[0] + s[1] + s[2] + s[3];
+            u64 incl = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const u64 y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, run + incl > goal);
+            if (hit) {
+                const int src = __ffs(hit) - 1;
+                u64 at = run + incl - mine;
+                int v = 4 * c - r.lead;
+#pragma unroll
+                for (int e = 0; e < 3; ++e) {
+                    at += s[e];
+                    if (at > goal) break;
+                    ++v;
+                }
+                return __shfl_sync(0xffffffffu, v, src);
+            }
+            run += __shfl_sync(0xffffffffu, incl, 31);
         }
-        run += __shfl_sync(0xffffffffu, incl, 31);
     }
     return -1;
 }
 
-__global__ void __launch_bounds__(kVfThreads) tree_verify_kernel(const VerifyArgs a)
+template <int kVfThreads>
+__global__ void __launch_bounds__(kVfThreads, 1024 / kVfThreads) tree_verify_kernel(const VerifyArgs a)
 {
+    constexpr int kVfWarps = kVfThreads / 32;
     cg::cluster_group cl = cg::this_cluster();
     const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -162,8 +221,10 @@ __global__ void __launch_bounds__(kVfThreads) tree_verify_kernel(const VerifyArg
     __shared__ int s_parent[kVfMaxNodes], s_tok[kVfMaxNodes];
     __shared__ float s_p[kVfMaxNodes], s_f[kVfMaxNodes], s_u[kVfMaxNodes];
     __shared__ float s_z[kVfMaxNodes];             // Z of each refusal behind cur (f given)
-    __shared__ int s_x[kVfMaxNodes];               // or its token (chosen)
-    __shared__ u64 s_sum[kVfWarps], s_total[2];
+    __shared__ int s_x[kVfMaxNodes];               // or its token (chosen), each once
+    __shared__ float s_xp[kVfMaxNodes];            // and that one's probability
+    __shared__ u64 s_sum[2][kVfWarps], s_total[2][kVfMaxCluster];   // sums of this CTA's warps, of the cluster's CTAs
+    __shared__ u64 s_groups[kVfWarps][kVfGroups];
     __shared__ int s_state[4];                     // cur, refusals behind it, next node to try, kept
 
     pdl_wait();
@@ -182,6 +243,7 @@ __global__ void __launch_bounds__(kVfThreads) tree_verify_kernel(const VerifyArg
         }
         return;
     }
+    cl.barrier_arrive();                           // every CTA of the cluster runs before any writes into it
     for (int i = tid; i < n; i += kVfThreads) {
         const int par = i > 0 ? __ldg(a.parents + q0 + i) : -1, x = __ldg(a.tokens + q0 + i);
         const bool ok = i > 0 && par >= 0 && par < i && x >= 0 && x < a.V;
@@ -201,53 +263,71 @@ __global__ void __launch_bounds__(kVfThreads) tree_verify_kernel(const VerifyArg
     const float us = __ldg(a.u_sample + r);
     __syncthreads();
 
+    cl.barrier_wait();
     int round = 0;
     float Z = 1.f;                                 // warp 0: of the weights behind the refusals so far
     VfRow w;
-    int c0 = 0, c1 = 0;
+    int c0 = 0, c1 = 0, stride = 1;
     u64 mine = 0, total = 0, before = 0;
     while (true) {
         if (warp == 0) {
             // nodes from `next` on whose parent is cur, in order; stops at one that needs a Z which is yet to be summed
             int cur = s_state[0], refused = s_state[1], next = s_state[2], kept = s_state[3];
             bool pending = false, sum = false;     // pending: the last refusal's Z is not known
-            while (kept < a.max_path) {
-                int found = -1;
-                for (int b = next & ~31; b < n && found < 0; b += 32) {
-                    const int i = b + lane;
-                    const unsigned hit = __ballot_sync(0xffffffffu, i >= next && i < n && s_parent[i] == cur);
-                    if (hit) found = b + __ffs(hit) - 1;
+            int older = refused;                   // refused tokens that are not among the chunk's lanes
+            unsigned gone = 0;                     // lanes whose tokens were refused behind cur
+            // 32 nodes at a time, a lane's in its registers
+#pragma unroll 1
+            for (int b = next & ~31; b < n && !sum; b += 32) {
+                const int i = b + lane;
+                const bool in = i < n;
+                const int par = in ? s_parent[i] : -1, tok = in ? s_tok[i] : -1;
+                const float np = in ? s_p[i] : 0.f, nf = in ? s_f[i] : 0.f, nu = in ? s_u[i] : 0.f;
+                while (kept < a.max_path) {
+                    const unsigned hit = __ballot_sync(0xffffffffu, i >= next && par == cur);
+                    if (!hit) break;
+                    const int src = __ffs(hit) - 1;
+                    next = b + src;
+                    sum = pending;
+                    if (sum) break;
+                    ++next;
+                    // w[x] behind the refusals
+                    float have = __shfl_sync(0xffffffffu, np, src);
+                    const float f = __shfl_sync(0xffffffffu, nf, src), u = __shfl_sync(0xffffffffu, nu, src);
+                    const int x = __shfl_sync(0xffffffffu, tok, src);
+                    if (a.f) {
+#pragma unroll 1
+                        for (int j = 0; j < refused; ++j) have = prob(__fsub_rn(have, __fmul_rn(s_z[j], f)));
+                    } else {
+#pragma unroll 1
+                        for (int j = 0; j < older; j += 32)
+                            if (__any_sync(0xffffffffu, j + lane < older && s_x[j + lane] == x)) have = 0.f;
+                        if (__ballot_sync(0xffffffffu, tok == x) & gone) have = 0.f;
+                    }
+                    const float share = __fmul_rn(u, a.f ? __fmul_rn(Z, f) : Z);
+                    if (share < have) {
+                        if (lane == 0 && rank == 0) path[kept] = b + src;
+                        ++kept;
+                        cur = b + src;
+                        refused = older = 0;
+                        gone = 0;
+                        Z = 1.f;
+                    } else if (a.f) {
+                        ++refused;                 // s_z[refused] is Z once it is summed
+                        pending = true;
+                    } else if (have > 0.f) {       // (else it adds nothing, or was refused before)
+                        if (lane == 0) {
+                            s_x[refused] = x;
+                            s_xp[refused] = have;
+                        }
+                        ++refused;
+                        gone |= 1u << src;
+                        Z = prob(__fsub_rn(Z, have));
+                    }
                 }
-                if (found < 0) break;
-                next = found;
-                sum = pending;
-                if (sum) break;
-                ++next;
-                // w[x] behind the refusals
-                float have = s_p[found];
-                const float f = s_f[found];
-                if (a.f) {
-                    for (int j = 0; j < refused; ++j) have = prob(__fsub_rn(have, __fmul_rn(s_z[j], f)));
-                } else {
-                    for (int j = 0; j < refused; ++j)
-                        if (s_x[j] == s_tok[found]) have = 0.f;
-                }
-                const float share = __fmul_rn(s_u[found], a.f ? __fmul_rn(Z, f) : Z);
-                if (share < have) {
-                    if (lane == 0 && rank == 0) path[kept] = found;
-                    ++kept;
-                    cur = found;
-                    refused = 0;
-                    Z = 1.f;
-                } else if (a.f) {
-                    ++refused;                     // s_z[refused] is Z once it is summed
-                    pending = true;
-                } else {
-                    if (lane == 0) s_x[refused] = s_tok[found];
-                    ++refused;
-                    Z = prob(__fsub_rn(Z, have));
-                    __syncwarp();
-                }
+                older = refused;
+                gone = 0;
+                __syncwarp();
             }
             __syncwarp();
             if (lane == 0) {
@@ -268,25 +348,41 @@ __global__ void __launch_bounds__(kVfThreads) tree_verify_kernel(const VerifyArg
         const int per = (w.chunks + C * kVfWarps - 1) / (C * kVfWarps);
         c0 = min(w.chunks, (rank * kVfWarps + warp) * per);
         c1 = min(w.chunks, c0 + per);
+        stride = ((per + kVfGroups - 1) / kVfGroups + 32 * kVfAhead - 1) / (32 * kVfAhead) * (32 * kVfAhead);
         bool plain = false;
         while (true) {
-            mine = vf_sum(w, c0, c1, lane);
-            if (lane == 0) s_sum[warp] = mine;
+            u64 *sums = s_sum[round & 1], *totals = s_total[round & 1];
+            mine = vf_sum(w, c0, c1, stride, s_groups[warp], lane);
+            if (lane == 0) sums[warp] = mine;
             __syncthreads();
+            if (!w.f && w.refused > 0) {
+                // chosen tokens that were refused come off the sums of the pieces that hold them
+                for (int j = tid; j < w.refused; j += kVfThreads) {
+                    const int g = (s_x[j] + w.lead) / 4 / per - rank * kVfWarps;
+                    if (g < 0 || g >= kVfWarps) continue;
+                    const u64 off = 0ull - steps(s_xp[j]);
+                    atomicAdd(sums + g, off);
+                    for (int i = ((s_x[j] + w.lead) / 4 - (g + rank * kVfWarps) * per) / stride + 1; i < kVfGroups; ++i)
+                        atomicAdd(s_groups[g] + i, off);
+                }
+                __syncthreads();
+                mine = sums[warp];
+            }
             u64 block = 0;
             before = 0;
 #pragma unroll
             for (int i = 0; i < kVfWarps; ++i) {
-                const u64 x = s_sum[i];
+                const u64 x = sums[i];
                 if (i < warp) before += x;
                 block += x;
             }
-            if (tid == 0) s_total[round & 1] = block;
+            // every CTA's sum goes to all of them
+            if (tid < C) *cl.map_shared_rank(totals + rank, tid) = block;
             cl.sync();
             total = 0;
             u64 t[kVfMaxCluster];
 #pragma unroll
-            for (int i = 0; i < kVfMaxCluster; ++i) t[i] = i < C ? *cl.map_shared_rank(&s_total[round & 1], i) : 0;
+            for (int i = 0; i < kVfMaxCluster; ++i) t[i] = i < C ? totals[i] : 0;
 #pragma unroll
             for (int i = 0; i < kVfMaxCluster; ++i) {
                 if (i < rank) before += t[i];
@@ -298,7 +394,6 @@ __global__ void __launch_bounds__(kVfThreads) tree_verify_kernel(const VerifyArg
             plain = true;
             w.refused = 0;
             w.f = nullptr;
-            __syncthreads();                       // s_sum reuse
         }
         if (s_state[2] >= n) break;
         Z = __fmul_rn(__ull2float_rn(total), 0x1p-48f);
@@ -318,11 +413,14 @@ __global__ void __launch_bounds__(kVfThreads) tree_verify_kernel(const VerifyArg
         // floor(u total), u in steps of 2^-64 (exact for u of 2^-40 and more, as of 24 bits)
         const u64 goal = __umul64hi(us > 0.f ? (us < 1.f ? __float2ull_rz(us * 0x1p64f) : ~0ull) : 0ull, total);
         if (goal >= before && goal < before + mine) {
-            const int v = vf_find(w, c0, c1, before, goal, lane);
+            // its group of the piece, from the running sums in front of them
+            const int groups = (c1 - c0 + stride - 1) / stride;
+            const int g = __popc(__ballot_sync(0xffffffffu, lane < groups && before + s_groups[warp][lane % kVfGroups] <= goal)) - 1;
+            before += s_groups[warp][g];
+            const int v = vf_find(w, c0 + g * stride, c1, before, goal, lane);
             if (lane == 0) a.next_token[r] = v;
         }
     }
-    cl.sync();                                     // no CTA leaves while another reads its sums
 }
 
 }  // namespace pa
@@ -360,9 +458,13 @@ extern "C" pa_status pa_tree_verify(const float *target_probs, const float *draf
     a.max_path = max_path;
     int cs = 1;
     while (cs < kVfMaxCluster && cs * 4096 < vocab) cs *= 2;
+    // the more threads the fewer round trips a piece of a row takes: 512 (two CTAs an SM) where all CTAs are then on the
+    // GPU at once, else 256 (four)
+    const int64_t ctas = (int64_t)n_reqs * cs;
+    const int threads = ctas <= 2 * num_sms() ? 512 : 256;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(n_reqs * cs));
-    cfg.blockDim = dim3(kVfThreads);
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(threads);
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -373,6 +475,7 @@ extern "C" pa_status pa_tree_verify(const float *target_probs, const float *draf
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = launch_overlap() != PA_OVERLAP_OFF ? 2 : 1;
-    if (cudaLaunchKernelEx(&cfg, tree_verify_kernel, a) != cudaSuccess) return PA_ERR_CUDA;
+    auto kern = threads == 512 ? tree_verify_kernel<512> : tree_verify_kernel<256>;
+    if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) return PA_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
