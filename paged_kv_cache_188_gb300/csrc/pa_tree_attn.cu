@@ -234,19 +234,22 @@ struct TrCfg {
     enum { K_FULL, K_EMPTY = K_FULL + NK, V_FULL = K_EMPTY + NK, V_EMPTY = V_FULL + NV, S_FULL = V_EMPTY + NV,
            P_READY = S_FULL + 2, O_FULL = P_READY + 2, O_FREE = O_FULL + 2, Q_FULL = O_FREE + 2, DRAIN = Q_FULL + 2,
            Q_SPLIT = DRAIN + 2,                          // e4m3: Q is there in its terms
-           JOINT = Q_SPLIT + 2,                          // stream A's Q, for stream B
+           WIDE_FREE = Q_SPLIT + 2,                      // and the stream's product with V is done
+           JOINT = WIDE_FREE + 2,                          // stream A's Q, for stream B
            ITEM_FULL, ITEM_EMPTY = ITEM_FULL + kTrPieces, N_BARS = ITEM_EMPTY + kTrPieces };
     static constexpr int OffMeta = (OffBar + N_BARS * 8 + 15) & ~15;     // uint4 [kTrMeta]: valid positions
     static constexpr int OffML = OffMeta + kTrMeta * 16;                 // float2 [128]: stream B's (m, l)
     static constexpr int OffKS = OffML + 128 * 8;                        // e4m3: float [kTrMeta][128], keys' scales
-    static constexpr int OffVE = OffKS + (E8 ? kTrMeta * 512 : 0);       // bytes [NV][128], values' exponents
-    static constexpr int OffQS = OffVE + (E8 ? NV * 128 : 0);            // float [128], rows' scales of a joint piece
+    static constexpr int OffVE = OffKS + (E8 ? kTrMeta * 512 : 0);       // bytes [kTrMeta][128], values' exponents
+    static constexpr int OffGr = OffVE + (E8 ? kTrMeta * 128 : 0);       // int [kTrMeta]: 16 keys share a scale
+    static constexpr int OffQS = OffGr + (E8 ? kTrMeta * 4 : 0);         // float [128], rows' scales of a joint piece
     static constexpr int OffEnd = OffQS + (E8 ? 512 : 0);
     static constexpr int Smem = OffEnd + 1024;
     static constexpr uint32_t ColO = 256;
     static constexpr uint32_t kIdS = E8 ? idesc_e4m3_f32(128, 128, 0, 0) : idesc_bf16_f32(128, 128, 0, 0);
     static constexpr uint32_t kIdPV = idesc_bf16_f32(128, D, 0, 1);
     static_assert(N_BARS <= 64, "two warps initialise the barriers");
+    static_assert(OffKS % 16 == 0 && OffVE % 16 == 0 && OffQS % 16 == 0);
     static_assert(Smem <= 232448 - 512, "fits with the static shared memory");
     static_assert(kTrMeta >= NK + 3, "a tile's valid positions and scales outlive its ring stage");
 };
@@ -419,14 +422,22 @@ __device__ __forceinline__ void tr_copy(const TreeArgs &a, const TrPlan &plan, T
                     __syncwarp();
                 }
                 if constexpr (E8) {
+                    const int at = seq % kTrMeta;
                     if (isv) {
-                        reinterpret_cast<uint32_t *>(sb + C::OffVE + st * 128)[lane] =
+                        reinterpret_cast<uint32_t *>(sb + C::OffVE + at * 128)[lane] =
                             (uint32_t)((ok[0] ? ex[0] : 255) | (ok[1] ? ex[1] : 255) << 8 | (ok[2] ? ex[2] : 255) << 16 |
                                        (ok[3] ? ex[3] : 255) << 24);
                     } else {
+                        // do 16 keys share a scale? (those past the end do not matter)
+                        const int x0 = __shfl_sync(0xffffffffu, ex[0], lane & ~3);
+                        bool one = true;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) one = one && (t * kTrTile + 4 * lane + e >= k.L || (ok[e] && ex[e] == x0));
+                        const bool grouped = __all_sync(0xffffffffu, one);
+                        if (lane == 0) reinterpret_cast<int *>(sb + C::OffGr)[at] = grouped;
                         // (an empty block's scale is 2^-126 in place of 0: a hidden column's minus infinity stays that)
                         auto scale_of = [](int e) { return __uint_as_float((uint32_t)max(e, 1) << 23); };
-                        reinterpret_cast<float4 *>(sb + C::OffKS + seq % kTrMeta * 512)[lane] =
+                        reinterpret_cast<float4 *>(sb + C::OffKS + at * 512)[lane] =
                             make_float4(scale_of(ok[0] ? ex[0] : 0), scale_of(ok[1] ? ex[1] : 0), scale_of(ok[2] ? ex[2] : 0),
                                         scale_of(ok[3] ? ex[3] : 0));
                     }
@@ -452,7 +463,8 @@ __device__ __forceinline__ void tr_copy(const TreeArgs &a, const TrPlan &plan, T
 // Does a 16-byte chunk hold a bf16 NaN or infinity?
 __device__ __forceinline__ bool tr_wild(const uint4 &v)
 {
-    auto w = [](uint32_t x) { return (x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u; };
+    constexpr uint32_t M = 0x7F80u;
+    auto w = [](uint32_t x) { return (x & M) == M || (x & M << 16) == M << 16; };
     return w(v.x) || w(v.y) || w(v.z) || w(v.w);
 }
 
@@ -547,7 +559,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
 
     if (tid < C::N_BARS) {
         const bool softmax = (tid >= C::P_READY && tid < C::O_FULL) || (tid >= C::O_FREE && tid < C::Q_FULL) ||
-                             (tid >= C::Q_SPLIT && tid < C::JOINT);
+                             (tid >= C::Q_SPLIT && tid < C::WIDE_FREE);
         const bool kempty = tid >= C::K_EMPTY && tid < C::V_FULL, vempty = tid >= C::V_EMPTY && tid < C::S_FULL;
         mbar_init(bar(tid), softmax ? 128u : kempty ? 2u : vempty ? (E8 ? 8u : 2u)
                                            : tid >= C::ITEM_EMPTY ? (uint32_t)kTrReaders : 1u);
@@ -741,7 +753,8 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
                         for (int kk = 0; kk < kTrTile / 16; ++kk)
                             umma_ts(tmem + C::ColO + X * D, tmem + X * 128 + kk * 8,
                                     smem_desc_sw128(vt + kk * 2048, kTrHalf, 1024), C::kIdPV, kk > 0 || t >= dt);
-                        if constexpr (!E8) release(bar(C::V_EMPTY + st));
+                        if constexpr (E8) umma_commit(bar(C::WIDE_FREE + X));
+                        else release(bar(C::V_EMPTY + st));
                         if (t + dt < nt) qk(sk);
                         else umma_commit(bar(C::O_FULL + X));
                     }
@@ -822,25 +835,28 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
                             if (s > -32) seen[w] = live ? tr_seen(a, qrow, node, s) : 0u;
                         }
                     }
-                    wait(bar(C::S_FULL + X), sx & 1);
-                    tc_fence_after();
-                    const uint4 valid = meta[(kseq + t) % kTrMeta];
                     if constexpr (E8) {
-                        if (i == 1 && X == 1 && !two) sl2 = tr_scale(sl2 * reinterpret_cast<const float *>(sb + C::OffQS)[row]);
-                        // V in bf16 with its scales, 32 rows a warp.  The stream's product before this step is done (S is
-                        // behind it), so its buffer is free
+                        // V in bf16 with its scales, 32 rows a warp, while S is on its way: the stream's product before this step is done
                         const int s = kseq + t, st = s % C::NV, r0 = (warp & 3) * 32;
                         const uint32_t wide = base + C::OffWide + X * C::TILE;
                         wait(bar(C::V_FULL + st), (s / C::NV) & 1);
-                        widen_e4m3_tile<D, true>(base + C::OffV + st * C::RAW, wide, lane, sb + C::OffVE + st * 128, r0, r0 + 32);
+                        if (sx > 0) wait(bar(C::WIDE_FREE + X), (sx - 1) & 1);
+                        widen_e4m3_tile<D, true>(base + C::OffV + st * C::RAW, wide, lane, sb + C::OffVE + s % kTrMeta * 128, r0, r0 + 32);
                         __syncwarp();
                         if (lane == 0) {
                             mbar_arrive(bar(C::V_EMPTY + st));
                             if (!two) mbar_arrive(bar(C::V_EMPTY + st));
                         }
                         const int lo = max(c - p0, r0), hi = min(k.L - p0, r0 + 32);
-                        if (lo < hi && tr_tame<D>(wide, lo, hi, lane) && lane == 0) *(volatile int *)&s_wild[X][piece & 7] = piece + 1;
+                        if (lo < hi && tr_tame<D>(wide, lo, hi, lane) && lane == 0)
+                            *(volatile int *)&s_wild[X][piece & 7] = piece + 1;
                         fence_proxy_async_smem();
+                    }
+                    wait(bar(C::S_FULL + X), sx & 1);
+                    tc_fence_after();
+                    const uint4 valid = meta[(kseq + t) % kTrMeta];
+                    if constexpr (E8) {
+                        if (i == 1 && X == 1 && !two) sl2 = tr_scale(sl2 * reinterpret_cast<const float *>(sb + C::OffQS)[row]);
                     }
                     const bool masked = nodes || (valid.x & valid.y & valid.z & valid.w) != ~0u;
                     seen[0] &= valid.x, seen[1] &= valid.y, seen[2] &= valid.z, seen[3] &= valid.w;
@@ -848,16 +864,25 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
 #pragma unroll
                     for (int ch = 0; ch < 4; ++ch) tmem_ld32(s_addr + ch * 32, *reinterpret_cast<uint32_t(*)[32]>(&r[ch * 32]));
                     tmem_wait_ld();
+                    // e4m3: a column's key scale joins the softmax scale where 16 columns share one, else S takes it now
+                    const int at = (kseq + t) % kTrMeta;
+                    float gs[8];
                     if constexpr (E8) {
-                        // a column's key scale
-                        const float4 *ks = reinterpret_cast<const float4 *>(sb + C::OffKS + (kseq + t) % kTrMeta * 512);
+                        const float *ks = reinterpret_cast<const float *>(sb + C::OffKS + at * 512);
+                        if (reinterpret_cast<const int *>(sb + C::OffGr)[at]) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const float4 f = ks[j];
-                            r[4 * j] = __float_as_uint(__uint_as_float(r[4 * j]) * f.x);
-                            r[4 * j + 1] = __float_as_uint(__uint_as_float(r[4 * j + 1]) * f.y);
-                            r[4 * j + 2] = __float_as_uint(__uint_as_float(r[4 * j + 2]) * f.z);
-                            r[4 * j + 3] = __float_as_uint(__uint_as_float(r[4 * j + 3]) * f.w);
+                            for (int g = 0; g < 8; ++g) gs[g] = ks[16 * g];
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) {
+                                const float4 f = reinterpret_cast<const float4 *>(ks)[j];
+                                r[4 * j] = __float_as_uint(__uint_as_float(r[4 * j]) * f.x);
+                                r[4 * j + 1] = __float_as_uint(__uint_as_float(r[4 * j + 1]) * f.y);
+                                r[4 * j + 2] = __float_as_uint(__uint_as_float(r[4 * j + 2]) * f.z);
+                                r[4 * j + 3] = __float_as_uint(__uint_as_float(r[4 * j + 3]) * f.w);
+                            }
+#pragma unroll
+                            for (int g = 0; g < 8; ++g) gs[g] = 1.f;
                         }
                     }
                     if (masked) {
@@ -865,15 +890,15 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
                         for (int j = 0; j < 128; ++j)
                             if (!(seen[j >> 5] >> (j & 31) & 1u)) r[j] = __float_as_uint(-INFINITY);
                     }
-                    float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+                    float mx = -INFINITY;
 #pragma unroll
-                    for (int j = 0; j < 128; j += 8) {
-                        mx0 = max3(mx0, __uint_as_float(r[j]), __uint_as_float(r[j + 1]));
-                        mx1 = max3(mx1, __uint_as_float(r[j + 2]), __uint_as_float(r[j + 3]));
-                        mx2 = max3(mx2, __uint_as_float(r[j + 4]), __uint_as_float(r[j + 5]));
-                        mx3 = max3(mx3, __uint_as_float(r[j + 6]), __uint_as_float(r[j + 7]));
+                    for (int g = 0; g < 8; ++g) {
+                        auto f = [&](int j) { return __uint_as_float(r[16 * g + j]); };
+                        const float a0 = max3(f(0), f(1), f(2)), a1 = max3(f(3), f(4), f(5)), a2 = max3(f(6), f(7), f(8));
+                        const float a3 = max3(f(9), f(10), f(11)), a4 = max3(a0, f(12), f(13)), a5 = max3(a1, f(14), f(15));
+                        const float top = fmaxf(max3(a2, a3, a4), a5);
+                        mx = fmaxf(mx, E8 ? top * gs[g] : top);
                     }
-                    const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
                     bool rescale = false;
                     float m_new = m;
                     if (mx > m && (m == -INFINITY || (mx - m) * sl2 > 8.f)) {
@@ -883,13 +908,17 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
                     const float alpha = rescale ? tr_ex2((m - m_new) * sl2) : 1.f;
                     m = m_new;
                     const float mb = m == -INFINITY ? 0.f : m * sl2;
-                    const uint64_t nmb2 = f32x2_pack(-mb, -mb), sl22 = f32x2_pack(sl2, sl2);
-                    uint64_t sum2 = f32x2_pack(0.f, 0.f);
+                    const uint64_t nmb2 = f32x2_pack(-mb, -mb);
+                    uint64_t sl22 = f32x2_pack(sl2, sl2), sum2 = f32x2_pack(0.f, 0.f);
 #pragma unroll
                     for (int hh = 0; hh < 2; ++hh) {
                         uint32_t pk[32];
 #pragma unroll
                         for (int j = 0; j < 64; j += 2) {
+                            if (E8 && j % 16 == 0) {
+                                const float sg = tr_scale(sl2 * gs[hh * 4 + j / 16]);
+                                sl22 = f32x2_pack(sg, sg);
+                            }
                             const uint64_t x = fma_f32x2(
                                 f32x2_pack(__uint_as_float(r[hh * 64 + j]), __uint_as_float(r[hh * 64 + j + 1])), sl22, nmb2);
                             const float v0 = tr_ex2(f32x2_lo(x)), v1 = tr_ex2(f32x2_hi(x));

@@ -119,7 +119,8 @@ def test_long_contexts_over_many_ctas(block):
     c = make([20000, 3, 5000], [40, 7, 64], 2, 128, 16, block, 3, layers=1, layer=0)
     seen, mask = trees(c)
     q = queries(c, 4, 128)
-    out, _ = tree(c, q.cuda(), 0.05, mask)
+    out, ws = tree(c, q.cuda(), 0.05, mask)
+    assert api.pa_get_error(ws) == 0
     check(c, q, out, 0.05, seen, "long")
     again, _ = tree(c, q.cuda(), 0.05, mask)
     assert torch.equal(out.view(torch.int16), again.view(torch.int16))      # run to run
