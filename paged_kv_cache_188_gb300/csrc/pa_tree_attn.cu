@@ -138,23 +138,22 @@ struct TrWalk {
     int w0;                 // the lanes hold requests w0 + lane
     TrReq w;
 };
-__device__ __forceinline__ void tr_unit(const TreeArgs &a, const TrPlan &p, TrWalk &k, int lane)
+__device__ __forceinline__ void tr_unit(const TreeArgs &a, const TrPlan &p, TrWalk &k)
 {
     const int i = k.unit / a.Hkv, v = a.ranges > 1 ? k.u : 0;
     k.h = k.unit - i * a.Hkv;
     k.x = k.x0 = (int)min((int64_t)p.total, (int64_t)i * p.W);
     k.xe = min(p.total, k.x + p.W);
-    k.r = k.w0 = p.start[v][0];
+    k.r = p.start[v][0];
     k.S0 = p.start[v][1];
-    k.w = TrReq{0, 0, 0, 0};
-    if (k.r + lane < a.R) k.w = tr_request(a, k.r + lane);
+    k.w0 = k.r - 32;        // nothing there yet: the first request comes from the plan
 }
-__device__ __forceinline__ void tr_begin(const TreeArgs &a, const TrPlan &p, TrWalk &k, int lane)
+__device__ __forceinline__ void tr_begin(const TreeArgs &a, const TrPlan &p, TrWalk &k)
 {
     k.unit = blockIdx.x;
     k.u = 0;
     k.x = k.xe = 0;
-    if (k.unit < a.ranges * a.Hkv) tr_unit(a, p, k, lane);
+    if (k.unit < a.ranges * a.Hkv) tr_unit(a, p, k);
 }
 __device__ __forceinline__ bool tr_next(const TreeArgs &a, const TrPlan &p, TrWalk &k, TrPiece &o, int lane)
 {
@@ -163,7 +162,7 @@ __device__ __forceinline__ bool tr_next(const TreeArgs &a, const TrPlan &p, TrWa
         k.unit += gridDim.x;
         ++k.u;
         if (k.unit >= a.ranges * a.Hkv) return false;
-        tr_unit(a, p, k, lane);
+        tr_unit(a, p, k);
     }
     TrReq q;
     int tiles;
@@ -171,7 +170,7 @@ __device__ __forceinline__ bool tr_next(const TreeArgs &a, const TrPlan &p, TrWa
     while (true) {
         const int v = a.ranges > 1 ? k.u : 0;
         if (k.x == k.x0 && k.r == p.start[v][0] && p.total > 0 && a.ranges > 1) {
-            q = p.req[v];               // the plan has it; the lanes' are on their way
+            q = p.req[v];
         } else {
             if (k.r - k.w0 >= 32) {
                 k.w0 = k.r;
@@ -235,7 +234,8 @@ struct TrCfg {
            P_READY = S_FULL + 2, O_FULL = P_READY + 2, O_FREE = O_FULL + 2, Q_FULL = O_FREE + 2, DRAIN = Q_FULL + 2,
            Q_SPLIT = DRAIN + 2,                          // e4m3: Q is there in its terms
            WIDE_FREE = Q_SPLIT + 2,                      // and the stream's product with V is done
-           JOINT = WIDE_FREE + 2,                          // stream A's Q, for stream B
+           TURN = WIDE_FREE + 2,                         // whose products are next
+           JOINT = TURN + 2,                          // stream A's Q, for stream B
            ITEM_FULL, ITEM_EMPTY = ITEM_FULL + kTrPieces, N_BARS = ITEM_EMPTY + kTrPieces };
     static constexpr int OffMeta = (OffBar + N_BARS * 8 + 15) & ~15;     // uint4 [kTrMeta]: valid positions
     static constexpr int OffML = OffMeta + kTrMeta * 16;                 // float2 [128]: stream B's (m, l)
@@ -314,7 +314,7 @@ __device__ __forceinline__ void tr_copy(const TreeArgs &a, const TrPlan &plan, T
     uint32_t ph = 0;
     bool go = true;
     TrWalk w;
-    if (!isv) tr_begin(a, plan, w, lane);
+    if (!isv) tr_begin(a, plan, w);
 #pragma unroll 1
     for (int it = 0;; ++it) {
         TrPiece k;
@@ -663,13 +663,16 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
                        bar(isv ? C::V_FULL : C::K_FULL), bar(isv ? C::V_EMPTY : C::K_EMPTY), sb, s_abort, lane);
     } else if (warp >= 10) {
         // ======================================================= products
-        // A warp per stream: while one waits for its weights, the tensor core has the other's products.
+        // A warp per stream, so that one waits for its weights while the other issues; they issue a step's two products in
+        // turn, in the order of the steps.  (Interleaved, both streams' products would end at the same time, and their
+        // softmaxes, which want the same units, would run at the same time again.)
         const int X = warp - 10;
         const uint32_t sQ = base, sK = base + C::OffK, sV = base + C::OffV;
         const uint32_t id_s = C::kIdS | (!E8 && a.negate ? 1u << 13 : 0u);   // bit 13: A negated
         int seq = 0, piece = 0, px = 0, pq = 0, p2 = 0, pj = 0;   // token tiles, pieces before; this stream's steps, pieces; of
                                                                   // stream B: those with rows of its own, and with A's
-        bool bad = false;
+        bool bad = false, turn = X == 0;
+        int turns = 0;
         auto wait = [&](uint32_t b, uint32_t parity) {
             if (!bad) bad = !tr_wait(a, b, parity, s_abort);
         };
@@ -747,6 +750,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
                     // the piece's first product overwrites O
                     if (t < dt && pq++ > 0) wait(bar(C::O_FREE + X), pq & 1);
                     wait(bar(C::P_READY + X), px & 1);
+                    if (!turn) wait(bar(C::TURN + X), turns++ & 1);
                     tc_fence_after();
                     if (!bad) if (elect_one()) {
 #pragma unroll
@@ -759,6 +763,9 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
                         else umma_commit(bar(C::O_FULL + X));
                     }
                     __syncwarp();
+                    // the next step, or the next piece's first
+                    turn = X == 0 && t + 1 >= nt && !two;
+                    if (!turn && lane == 0) mbar_arrive(bar(C::TURN + 1 - X));
                 }
                 seq += nt;
                 ++piece;
@@ -1026,18 +1033,21 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
 }
 
 // ------------------------------------------------------------------ merge
-// The rows of segments that several units worked on, pieces in order: a thread
-// has 16 columns of a row, the threads of a warp consecutive rows, as the
-// partials lie.
-constexpr int kTrMergeThreads = 256;
+// The rows of segments that several units worked on, pieces in order.  A CTA
+// takes a part of a node's heads; a thread has 8 columns of a row, its
+// neighbours the other heads of the group, whose partials lie side by side.  PG
+// threads share those pieces where there are few nodes (a long request's 19 pieces are
+// then one round trip or two).
+constexpr int kTrMergeThreads = 256, kTrMergeCols = 8;
 
-template <int D>
-__global__ void __launch_bounds__(kTrMergeThreads) tree_merge_kernel(const __grid_constant__ TreeArgs a)
+template <int D, int PG>
+__global__ void __launch_bounds__(kTrMergeThreads, 2) tree_merge_kernel(const __grid_constant__ TreeArgs a)
 {
-    constexpr int COLS = 16, GROUPS = D / COLS;
-    extern __shared__ int s_pref[];                    // [R + 1] first tiles, [R] first rows of q
+    constexpr int NC = kTrMergeCols / 4, GROUPS = D / kTrMergeCols, U = PG > 1 ? 6 : 4;
+    constexpr int EPC = kTrMergeThreads / PG, EPW = 32 / PG;     // elements of a CTA, of a warp
+    extern __shared__ int s_pref[];                    // [R + 1] first tiles, [R] first rows of q, tiles of a segment
     __shared__ int s_w[kTrMergeThreads / 32];
-    int *s_q0 = s_pref + a.R + 1;
+    int *s_q0 = s_pref + a.R + 1, *s_kt = s_q0 + a.R;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     {
         const int per = (a.R + kTrMergeThreads - 1) / kTrMergeThreads, lo = min(a.R, tid * per), hi = min(a.R, lo + per);
@@ -1047,6 +1057,7 @@ __global__ void __launch_bounds__(kTrMergeThreads) tree_merge_kernel(const __gri
             const TrReq q = tr_request(a, r);
             s_pref[r] = run;
             s_q0[r] = q.q0;
+            s_kt[r] = q.n > 0 ? tr_ktiles(q.L) : 0;
             run += tr_tiles(a, q);
         }
         int incl = run;
@@ -1066,54 +1077,49 @@ __global__ void __launch_bounds__(kTrMergeThreads) tree_merge_kernel(const __gri
         if (tid == kTrMergeThreads - 1) s_pref[a.R] = before + run;
     }
     __syncthreads();
-    pdl_wait();
-    pdl_launch_dependents();
     const int total = s_pref[a.R], W = (total + a.ranges - 1) / a.ranges;
-    if (total == 0) return;
-    const int per_row = a.Hq * GROUPS;                 // threads per row of q
-    const int64_t all = (int64_t)a.T * per_row;
+    const int per_row = a.Hq * GROUPS, parts = (per_row + EPC - 1) / EPC, sub = lane / EPW;
+    bool waited = false;
 #pragma unroll 1
-    for (int64_t e = (int64_t)blockIdx.x * kTrMergeThreads + tid; e < all; e += (int64_t)gridDim.x * kTrMergeThreads) {
-        // the last request that starts at or in front of the row
-        const int t = (int)(e / per_row);
+    for (int64_t item = blockIdx.x; item < (int64_t)a.T * parts; item += gridDim.x) {
+        const int t = (int)(item / parts), e = (int)(item - (int64_t)t * parts) * EPC + warp * EPW + lane % EPW;
+        // the last request that starts at or in front of the node
         int lo = 0, hi = a.R;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (s_q0[mid] <= t) lo = mid; else hi = mid;
         }
-        const int S0 = s_pref[lo], tiles = s_pref[lo + 1] - S0;
-        // (a request whose tiles lie in one range was never shared)
-        if (tiles == 0 || S0 / W == (S0 + tiles - 1) / W) continue;
-        const TrReq q = tr_request(a, lo);
-        if (t < q.q0 || t >= q.q0 + q.n) continue;
-        // thread of the request: (head, column group, row of the head)
-        const int64_t f = e - (int64_t)q.q0 * per_row, rows = (int64_t)q.n * a.G, hc = f / rows, at = f - hc * rows;
-        const int h = (int)hc / GROUPS, cg = (int)hc - h * GROUPS;
-        const int node = (int)(at / a.G), g = (int)(at - (int64_t)node * a.G);
-        const int tile = node / a.tq, pair = tile >> 1, kt = tr_ktiles(q.L), S = S0 + pair * kt;
-        const int i0 = S / W, i1 = (S + kt - 1) / W;
-        if (i0 == i1) continue;
-        const int row = (tile & 1) * kTrTile + (node - tile * a.tq) * a.G + g;   // of the pair's 256
+        const int S0 = s_pref[lo], tiles = s_pref[lo + 1] - S0, node = t - s_q0[lo], tile = node / a.tq;
+        const int pair = tile >> 1, kt = s_kt[lo], S = S0 + pair * kt;
+        // (past the request's nodes; or its segment lies in one range and was never shared)
+        if (tiles == 0 || node < 0 || (pair + 1) * kt > tiles || S / W == (S + kt - 1) / W) continue;
+        if (node >= __ldg(a.qo_indptr + lo + 1) - s_q0[lo]) continue;
+        if (!waited) {
+            pdl_wait();
+            waited = true;
+        }
+        const bool in = e < per_row;
+        const int hc = (in ? e : 0) / a.G, g = (in ? e : 0) - hc * a.G, h = hc / GROUPS, cg = hc - h * GROUPS;
+        const int i0 = S / W, i1 = (S + kt - 1) / W, row = (tile & 1) * kTrTile + (node - tile * a.tq) * a.G + g;   // of the pair's 256
         auto slot = [&](int i) { return (int64_t)(2 * (i * a.Hkv + h) + (i == i0 && S > i0 * W ? 1 : 0)); };
-        float M = -INFINITY, L = 0.f, o[COLS];
+        float M = -INFINITY, L = 0.f, o[kTrMergeCols];
 #pragma unroll
-        for (int x = 0; x < COLS; ++x) o[x] = 0.f;
-        constexpr int U = 4;
+        for (int x = 0; x < kTrMergeCols; ++x) o[x] = 0.f;
 #pragma unroll 1
-        for (int i = i0; i <= i1; i += U) {
+        for (int i = i0 + sub; i <= i1; i += PG * U) {
             float2 ml[U];
-            float4 v[U][COLS / 4];
+            float4 v[U][NC];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 ml[u] = make_float2(-INFINITY, 0.f);
 #pragma unroll
-                for (int x = 0; x < COLS / 4; ++x) v[u][x] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (i + u > i1) continue;
-                const int64_t s = slot(i + u);
+                for (int x = 0; x < NC; ++x) v[u][x] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i + u * PG > i1) continue;
+                const int64_t s = slot(i + u * PG);
                 ml[u] = __ldcg(reinterpret_cast<const float2 *>(a.ml_part) + s * kTrPair + row);
-                const float4 *src = reinterpret_cast<const float4 *>(a.o_part + s * kTrPair * D) + cg * (COLS / 4) * kTrPair + row;
+                const float4 *src = reinterpret_cast<const float4 *>(a.o_part + s * kTrPair * D) + cg * NC * kTrPair + row;
 #pragma unroll
-                for (int x = 0; x < COLS / 4; ++x) v[u][x] = __ldcg(src + x * kTrPair);
+                for (int x = 0; x < NC; ++x) v[u][x] = __ldcg(src + x * kTrPair);
             }
             float mn = M;
 #pragma unroll
@@ -1121,15 +1127,15 @@ __global__ void __launch_bounds__(kTrMergeThreads) tree_merge_kernel(const __gri
             const float mz = mn == -INFINITY ? 0.f : mn, f0 = tr_ex2(M - mz);
             L *= f0;
 #pragma unroll
-            for (int x = 0; x < COLS; ++x) o[x] *= f0;
+            for (int x = 0; x < kTrMergeCols; ++x) o[x] *= f0;
             M = mn;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (i + u > i1) continue;
+                if (i + u * PG > i1) continue;
                 const float w = tr_ex2(ml[u].x - mz);
                 L = fmaf(w, ml[u].y, L);
 #pragma unroll
-                for (int x = 0; x < COLS / 4; ++x) {
+                for (int x = 0; x < NC; ++x) {
                     o[4 * x] = fmaf(w, v[u][x].x, o[4 * x]);
                     o[4 * x + 1] = fmaf(w, v[u][x].y, o[4 * x + 1]);
                     o[4 * x + 2] = fmaf(w, v[u][x].z, o[4 * x + 2]);
@@ -1137,14 +1143,31 @@ __global__ void __launch_bounds__(kTrMergeThreads) tree_merge_kernel(const __gri
                 }
             }
         }
-        const float inv = L != 0.f ? 1.f / L : 0.f;
-        uint32_t y[COLS / 2];
+        if constexpr (PG > 1) {
+            // the threads' parts, in their order
+            float mn = M;
 #pragma unroll
-        for (int x = 0; x < COLS / 2; ++x) y[x] = L != 0.f ? pack_bf16x2(o[2 * x] * inv, o[2 * x + 1] * inv) : 0u;
-        uint4 *dst = reinterpret_cast<uint4 *>(a.out + ((int64_t)(q.q0 + node) * a.Hq + h * a.G + g) * D + cg * COLS);
-        dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
-        dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
+            for (int d = EPW; d < 32; d <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, d));
+            const float f0 = tr_ex2(M - (mn == -INFINITY ? 0.f : mn));
+            L *= f0;
+#pragma unroll
+            for (int x = 0; x < kTrMergeCols; ++x) o[x] *= f0;
+#pragma unroll
+            for (int d = EPW; d < 32; d <<= 1) {
+                L += __shfl_xor_sync(0xffffffffu, L, d);
+#pragma unroll
+                for (int x = 0; x < kTrMergeCols; ++x) o[x] += __shfl_xor_sync(0xffffffffu, o[x], d);
+            }
+        }
+        if (!in || sub != 0) continue;
+        const float inv = L != 0.f ? 1.f / L : 0.f;
+        uint32_t y[kTrMergeCols / 2];
+#pragma unroll
+        for (int x = 0; x < kTrMergeCols / 2; ++x) y[x] = L != 0.f ? pack_bf16x2(o[2 * x] * inv, o[2 * x + 1] * inv) : 0u;
+        *reinterpret_cast<uint4 *>(a.out + ((int64_t)t * a.Hq + h * a.G + g) * D + cg * kTrMergeCols) = make_uint4(y[0], y[1], y[2], y[3]);
     }
+    if (!waited) pdl_wait();
+    pdl_launch_dependents();
 }
 
 // --------------------------------------------------------------- host side
@@ -1181,12 +1204,17 @@ static pa_status tr_launch(const TreeArgs &a, cudaStream_t st)
     if (launch_kernel(kern, dim3(grid), dim3(kTrThreads), smem, st, b) != cudaSuccess) return PA_ERR_CUDA;
     if (b.ranges > 1) {
         // behind this call's own kernel, whose end it waits for: overlapped whatever the mode
-        auto merge = tree_merge_kernel<D>;
-        const int64_t want = ((int64_t)a.T * a.Hq * (D / 16) + kTrMergeThreads - 1) / kTrMergeThreads;
+        const int64_t elems = (int64_t)a.Hq * (D / kTrMergeCols);
+        auto parts = [&](int pg) { return (elems * pg + kTrMergeThreads - 1) / kTrMergeThreads * a.T; };
+        const bool few = parts(1) <= grid;
+        auto merge = few ? tree_merge_kernel<D, 4> : tree_merge_kernel<D, 1>;
+        const int64_t want = parts(few ? 4 : 1);
+        const size_t msmem = ((size_t)3 * a.R + 1) * 4;
+        if (!ensure_dynamic_smem(reinterpret_cast<const void *>(merge), msmem)) return PA_ERR_CUDA;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(want < 4 * grid ? want : 4 * grid));
         cfg.blockDim = dim3(kTrMergeThreads);
-        cfg.dynamicSmemBytes = ((size_t)2 * a.R + 1) * 4;
+        cfg.dynamicSmemBytes = msmem;
         cfg.stream = st;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
