@@ -485,18 +485,22 @@ def pa_paged_tree_attn(q, k_buf, v_buf, layer_id, qo_indptr, req_to_token, req_p
     e4m3 cache.  ``tree_mask`` (int32 [T, words]): the bits of the drafted tokens
     that each of them sees; None: a chain."""
     dev = _device()
+    bf16, i32 = torch.bfloat16, torch.int32
     if block == 0 and k_exp is None and v_exp is None:
-        _all(dev, (k_buf, torch.bfloat16, 4, "k_buf"), (v_buf, torch.bfloat16, 4, "v_buf"))
-        s = _kv_shape(k_buf, v_buf)
+        _all(dev, (k_buf, bf16, 4, "k_buf"), (v_buf, bf16, 4, "v_buf"))
+        shape = k_buf.shape
+        if v_buf.shape != shape:
+            raise ValueError("k_buf and v_buf shapes differ")
+        s = KvShape(*shape)
         ke = ve = None
     else:
         if k_exp is None or v_exp is None:
             raise ValueError("a block-scaled cache needs k_exp and v_exp")
         s = _kv_shape_block(dev, k_buf, v_buf, k_exp, v_exp, block)
         ke, ve = k_exp.data_ptr(), v_exp.data_ptr()
-    _all(dev, (q, torch.bfloat16, 3, "q"), (out, torch.bfloat16, 3, "out"), (qo_indptr, torch.int32, 1, "qo_indptr"),
-         (req_to_token, torch.int32, 2, "req_to_token"), (req_pool_indices, torch.int32, 1, "req_pool_indices"),
-         (seq_lens, torch.int32, 1, "seq_lens"), (workspace, torch.uint8, 1, "workspace"))
+    _all(dev, (q, bf16, 3, "q"), (out, bf16, 3, "out"), (qo_indptr, i32, 1, "qo_indptr"), (req_to_token, i32, 2, "req_to_token"),
+         (req_pool_indices, i32, 1, "req_pool_indices"), (seq_lens, i32, 1, "seq_lens"),
+         (workspace, torch.uint8, 1, "workspace"))
     T, Hq, D = shape = q.shape
     R = seq_lens.shape[0]
     if out.shape != shape or D != s.head_dim or qo_indptr.shape[0] != R + 1 or req_pool_indices.shape[0] != R:
@@ -546,6 +550,9 @@ def pa_tree_verify(target_probs, tokens, parents, qo_indptr, u_accept, u_sample,
         next_token.data_ptr(), _word(dev, error_word), _raw_stream(stream, dev)))
 
 
+_NO_KV = KvShape(0, 0, 0, 0)
+
+
 def pa_kv_accept(req_to_token, req_pool_indices, seq_lens, qo_indptr, accepted, n_accepted, new_lens, freed, k_buf=None,
                  v_buf=None, error_word=None, stream=None):
     """Keep each request's accepted nodes and free its others: in the page table, or
@@ -561,7 +568,7 @@ def pa_kv_accept(req_to_token, req_pool_indices, seq_lens, qo_indptr, accepted, 
     if (qo_indptr.shape[0] != R + 1 or req_pool_indices.shape[0] != R or seq_lens.shape[0] != R
             or n_accepted.shape[0] != R or new_lens.shape[0] != R):
         raise ValueError("qo_indptr [R+1], req_pool_indices/seq_lens/n_accepted/new_lens [R] expected")
-    s, elem, kp, vp = KvShape(0, 0, 0, 0), 0, None, None
+    s, elem, kp, vp = _NO_KV, 0, None, None
     if k_buf is not None or v_buf is not None:
         if k_buf is None or v_buf is None:
             raise ValueError("k_buf and v_buf go together")

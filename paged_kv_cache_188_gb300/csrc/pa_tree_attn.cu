@@ -509,6 +509,41 @@ __device__ __forceinline__ float tr_element(const uint8_t *rows, const uint8_t *
     return e == 0 && x == x ? 0.f : x * __uint_as_float((uint32_t)e << 23);
 }
 
+// Rows r0 .. r0 + 31 of an e4m3 tile (rows of D bytes) times their scales as bf16, in the swizzled layout of the second
+// product's operand; exponent byte 255 marks a position without a row, which becomes zeros.  Whole warp, D / 16 lanes a
+// row; everything is read before anything is converted.
+template <int D>
+__device__ __forceinline__ void tr_widen(uint32_t src, uint32_t dst, const unsigned char *exps, int r0, int lane)
+{
+    constexpr int LPR = D / 16, RPP = 32 / LPR, N = 32 / RPP;    // lanes of a row, rows at a time, times
+    const int rr = lane / LPR, j = lane % LPR;
+    uint4 v[N];
+    uint32_t ex[N];
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+        v[u] = ld_shared_v4(src + (uint32_t)((r0 + u * RPP + rr) * D + j * 16));
+        ex[u] = exps[r0 + u * RPP + rr];
+    }
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+        const int r = r0 + u * RPP + rr;
+        const bool row = ex[u] != 255u;
+        const uint32_t mul = row ? ex[u] * 0x00800080u : 0u;     // 2^(e - 127) as a pair of bf16
+        if (!row) v[u] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+            // (a row's second half of lanes writes its odd chunk first: eight lanes then hit all banks once)
+            const int half = hh ^ (j >= LPR / 2);
+            const uint32_t a = half ? v[u].z : v[u].x, b = half ? v[u].w : v[u].y;
+            const int c = 2 * j + half;
+            st_shared_v4(dst + (uint32_t)((c >> 3) * kTrHalf + r * 128 + (((c & 7) ^ (r & 7)) << 4)),
+                         mul_bf16x2(e4m3x2_to_bf16x2(a), mul), mul_bf16x2(e4m3x2_to_bf16x2(a >> 16), mul),
+                         mul_bf16x2(e4m3x2_to_bf16x2(b), mul), mul_bf16x2(e4m3x2_to_bf16x2(b >> 16), mul));
+        }
+    }
+    __syncwarp();
+}
+
 // What tr_tame took out, for one row of the piece (node i, query head hq) and 32 columns from d0 on: the parts of the
 // nodes' V rows that hold a NaN or an infinity and that the node sees, weights relative to m2.
 template <int D, bool E8>
@@ -843,13 +878,14 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
                         }
                     }
                     if constexpr (E8) {
-                        // V in bf16 with its scales, 32 rows a warp, while S is on its way: the stream's product before this step is done
-                        const int s = kseq + t, st = s % C::NV, r0 = (warp & 3) * 32;
+                        // V in bf16 with its scales, 32 rows a warp, while S is on its way: the stream's product before this
+                        // step is done
+                        const int s = kseq + t, st = s % C::NV;
                         const uint32_t wide = base + C::OffWide + X * C::TILE;
                         wait(bar(C::V_FULL + st), (s / C::NV) & 1);
                         if (sx > 0) wait(bar(C::WIDE_FREE + X), (sx - 1) & 1);
-                        widen_e4m3_tile<D, true>(base + C::OffV + st * C::RAW, wide, lane, sb + C::OffVE + s % kTrMeta * 128, r0, r0 + 32);
-                        __syncwarp();
+                        const int r0 = (warp & 3) * 32;
+                        tr_widen<D>(base + C::OffV + st * C::RAW, wide, sb + C::OffVE + s % kTrMeta * 128, r0, lane);
                         if (lane == 0) {
                             mbar_arrive(bar(C::V_EMPTY + st));
                             if (!two) mbar_arrive(bar(C::V_EMPTY + st));
