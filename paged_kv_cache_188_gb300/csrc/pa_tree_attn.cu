@@ -400,18 +400,31 @@ __device__ __forceinline__ void tr_copy(const TreeArgs &a, const TrPlan &plan, T
 #pragma unroll
                     for (int e = 0; e < 4; ++e) sl[e] = a.layer_row0 + (ok[e] ? sl[e] : some);
                     tma_gather4(dst + lane * 4 * PITCH, m1, col, sl[0], sl[1], sl[2], sl[3], fb);
-                } else {
+                }
+                uint32_t bytes = C::RAW;
+                if constexpr (!E8) {
+                    // rows anywhere: 16-byte copies, four lanes on 64 bytes of a row, waited for here (as gather4 copies, two
+                    // of a row's halves each, a tile took 3200 cycles to issue; zeros where there is no row)
+                    const bool gathered = !page && !none;
+                    if (__any_sync(0xffffffffu, gathered)) {
+                        const uint8_t *rows = isv ? a.v : a.k;
+                        bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, (lane & 3) == 0 && !gathered)) * 16u * 128u * C::HALVES;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) sl[e] = ok[e] ? a.layer_row0 + sl[e] : a.total_rows;
+                        for (int x = 0; x < 16; ++x) {
+                            const int from = __shfl_sync(0xffffffffu, sl[x & 3], (lane & ~3) + (x >> 2));
+                            const bool row = __shfl_sync(0xffffffffu, (int)ok[x & 3], (lane & ~3) + (x >> 2));
+                            if (!gathered) continue;
+                            const int r = (lane >> 2) * 16 + x;
+                            const uint8_t *src = rows + ((int64_t)(row ? from : 0) * a.Hkv + k.h) * (2 * D);
 #pragma unroll
-                    for (int hh = 0; hh < C::HALVES; ++hh) {
-                        const uint32_t d = dst + hh * kTrHalf + lane * 4 * 128;
-                        if (nib == 15u) {
-                            tma_gather4(d, m1, col + hh * 64, sl[0], sl[1], sl[2], sl[3], fb);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) tma_load_2d(d + e * 128, m1, col + hh * 64, sl[e], fb);
+                            for (int q = 0; q < 2 * C::HALVES; ++q) {
+                                const int ch = q * 4 + (lane & 3);
+                                cp_async_16(dst + (ch >> 3) * kTrHalf + r * 128 + (((ch & 7) ^ (r & 7)) << 4), src + ch * 16, row ? 16 : 0);
+                            }
                         }
+                        cp_async_wait_all();
+                        fence_proxy_async_smem();
+                        __syncwarp();
                     }
                 }
                 if (!isv) {
@@ -443,7 +456,7 @@ __device__ __forceinline__ void tr_copy(const TreeArgs &a, const TrPlan &plan, T
                     }
                     __syncwarp();
                 }
-                if (lane == 0) mbar_arrive_expect_tx(fb, C::RAW);
+                if (lane == 0) mbar_arrive_expect_tx(fb, bytes);
                 __syncwarp();
                 if (t + 1 < k.t1) fetch_exps();
                 ++seq;
