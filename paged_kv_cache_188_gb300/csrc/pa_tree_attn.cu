@@ -63,7 +63,7 @@ constexpr uint32_t kTrTmemCols = 512;    // S_A | S_B | O_A | O_B
 
 struct TreeArgs {
     CUtensorMap tm_q;                            // 3-D (element, head, token): boxes of 64 x G x TQ
-    CUtensorMap tm_k16, tm_k1, tm_v16, tm_v1;    // 2-D (element, row): boxes of 16 rows, and one row (gather4)
+    CUtensorMap tm_k16, tm_k1, tm_v16, tm_v1;    // 2-D (element, row): boxes of 16 rows, and (e4m3) one row (gather4)
     const __nv_bfloat16 *q;
     const uint8_t *k, *v;                        // the layer's rows
     const uint8_t *k_exp, *v_exp;                // the layer's exponents (e4m3 cache)
@@ -313,6 +313,17 @@ __device__ __forceinline__ void tr_copy(const TreeArgs &a, const TrPlan &plan, T
     int st = 0, seq = 0, errs = 0;
     uint32_t ph = 0;
     bool go = true;
+    // bf16: the tile whose 16-byte copies are on their way.  It is handed on when the next one's have been issued, or
+    // before this warp waits for anything else
+    uint32_t held = 0, held_bytes = 0;
+    auto release_held = [&](int later) {
+        if (later) cp_async_wait<1>();
+        else cp_async_wait_all();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(held, held_bytes);
+        held = 0;
+    };
     TrWalk w;
     if (!isv) tr_begin(a, plan, w);
 #pragma unroll 1
@@ -361,8 +372,9 @@ __device__ __forceinline__ void tr_copy(const TreeArgs &a, const TrPlan &plan, T
             for (int t = k.t0; t < k.t1 && go; ++t) {
                 int sl[4] = {nx[0], nx[1], nx[2], nx[3]};
                 if (t + 1 < k.t1) fetch(t + 1);
-                if (seq >= stages &&
-                    !tr_wait(a, empty + st * 8, ph ^ 1, s_abort)) {
+                if (!E8 && seq >= stages && held != 0 && !__all_sync(0xffffffffu, mbar_try_wait(empty + st * 8, ph ^ 1)))
+                    release_held(0);
+                if (seq >= stages && !tr_wait(a, empty + st * 8, ph ^ 1, s_abort)) {
                     go = false;
                     break;
                 }
@@ -402,13 +414,16 @@ __device__ __forceinline__ void tr_copy(const TreeArgs &a, const TrPlan &plan, T
                     tma_gather4(dst + lane * 4 * PITCH, m1, col, sl[0], sl[1], sl[2], sl[3], fb);
                 }
                 uint32_t bytes = C::RAW;
+                bool copied = false;
                 if constexpr (!E8) {
-                    // rows anywhere: 16-byte copies, four lanes on 64 bytes of a row, waited for here (as gather4 copies, two
-                    // of a row's halves each, a tile took 3200 cycles to issue; zeros where there is no row)
+                    // rows anywhere, and the ends of pages: 16-byte copies, four lanes on 64 bytes of a row; zeros where there
+                    // is no row.  (gather4 copies cost 100 cycles of issue each, 64 a tile at D = 128: 32 requests of up to
+                    // 8192 tokens at pages of one slot took 139 us against 115; at D = 64 there is no difference.)
                     const bool gathered = !page && !none;
-                    if (__any_sync(0xffffffffu, gathered)) {
+                    copied = __any_sync(0xffffffffu, gathered);
+                    if (copied) {
                         const uint8_t *rows = isv ? a.v : a.k;
-                        bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, (lane & 3) == 0 && !gathered)) * 16u * 128u * C::HALVES;
+                        bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, !gathered)) * 4u * 128u * C::HALVES;
 #pragma unroll
                         for (int x = 0; x < 16; ++x) {
                             const int from = __shfl_sync(0xffffffffu, sl[x & 3], (lane & ~3) + (x >> 2));
@@ -422,10 +437,8 @@ __device__ __forceinline__ void tr_copy(const TreeArgs &a, const TrPlan &plan, T
                                 cp_async_16(dst + (ch >> 3) * kTrHalf + r * 128 + (((ch & 7) ^ (r & 7)) << 4), src + ch * 16, row ? 16 : 0);
                             }
                         }
-                        cp_async_wait_all();
-                        fence_proxy_async_smem();
-                        __syncwarp();
                     }
+                    cp_async_commit();
                 }
                 if (!isv) {
                     uint32_t w = nib << (4 * (lane & 7));
@@ -456,7 +469,14 @@ __device__ __forceinline__ void tr_copy(const TreeArgs &a, const TrPlan &plan, T
                     }
                     __syncwarp();
                 }
-                if (lane == 0) mbar_arrive_expect_tx(fb, bytes);
+                if constexpr (!E8) {
+                    if (held != 0) release_held(1);
+                    if (copied) {
+                        held = fb;
+                        held_bytes = bytes;
+                    }
+                }
+                if (!copied && lane == 0) mbar_arrive_expect_tx(fb, bytes);
                 __syncwarp();
                 if (t + 1 < k.t1) fetch_exps();
                 ++seq;
@@ -465,6 +485,7 @@ __device__ __forceinline__ void tr_copy(const TreeArgs &a, const TrPlan &plan, T
                     ph ^= 1;
                 }
             }
+            if (!E8 && held != 0) release_held(0);
         }
     // the warp leaves only when its copies have landed, whether or not anyone has given up by now
 #pragma unroll 1
@@ -621,11 +642,11 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
     if (warp == 10) tmem_alloc(smem_u32(&s_tmem), kTrTmemCols);
     if (warp == 8 && lane == 0) {
         prefetch_tmap(&a.tm_k16);
-        prefetch_tmap(&a.tm_k1);
+        if (E8) prefetch_tmap(&a.tm_k1);
     }
     if (warp == 9 && lane == 0) {
         prefetch_tmap(&a.tm_v16);
-        prefetch_tmap(&a.tm_v1);
+        if (E8) prefetch_tmap(&a.tm_v1);
     }
     if (!a.early_meta) pdl_wait();
 
@@ -1322,12 +1343,10 @@ extern "C" pa_status pa_paged_tree_attn(const void *q, int n_tokens, int n_q_hea
     const cuuint32_t box = e4m3 ? s.head_dim : 64, box16[2] = {box, 16}, box1[2] = {box, 1};
     const int sw = e4m3 ? s.head_dim : 128;
     const cuuint64_t dims[2] = {inner, rows}, strides[1] = {inner};
-    if (!encode_tmap_rows(&a.tm_k16, k_buf, !e4m3, inner, rows, box, 16, sw) ||
-        !encode_tmap_rows(&a.tm_k1, k_buf, !e4m3, inner, rows, box, 1, sw))
-        return PA_ERR_CUDA;
-    if (e4m3 ? !encode_tmap_u8(&a.tm_v16, v_buf, 2, dims, strides, box16) || !encode_tmap_u8(&a.tm_v1, v_buf, 2, dims, strides, box1)
-             : !encode_tmap_rows(&a.tm_v16, v_buf, true, inner, rows, box, 16, sw) ||
-                   !encode_tmap_rows(&a.tm_v1, v_buf, true, inner, rows, box, 1, sw))
+    if (!encode_tmap_rows(&a.tm_k16, k_buf, !e4m3, inner, rows, box, 16, sw)) return PA_ERR_CUDA;
+    if (e4m3 ? !encode_tmap_rows(&a.tm_k1, k_buf, false, inner, rows, box, 1, sw) ||
+                   !encode_tmap_u8(&a.tm_v16, v_buf, 2, dims, strides, box16) || !encode_tmap_u8(&a.tm_v1, v_buf, 2, dims, strides, box1)
+             : !encode_tmap_rows(&a.tm_v16, v_buf, true, inner, rows, box, 16, sw))
         return PA_ERR_CUDA;
     {
         const cuuint64_t dims[3] = {(cuuint64_t)s.head_dim, (cuuint64_t)n_q_heads, (cuuint64_t)n_tokens};
