@@ -155,6 +155,60 @@ __device__ __forceinline__ u64 vf_sum(const VfRow &r, int c0, int c1, int stride
     return sum;
 }
 
+// A piece of at most 128 chunks, kept in the registers of its warp from one refusal to the next: w is not computed, nor
+// the row read, again.
+struct VfHeld {
+    int64_t row;            // -1: nothing
+    int refused;            // taken off so far
+    float4 w[kVfAhead], f[kVfAhead];
+};
+__device__ __forceinline__ u64 vf_sum_held(const VfRow &r, int64_t row, int c0, int c1, VfHeld &h, int lane)
+{
+    if (h.row != row) {
+        h.row = row;
+        h.refused = 0;
+#pragma unroll
+        for (int i = 0; i < kVfAhead; ++i) {
+            const int c = c0 + lane + 32 * i;
+            const float4 p = c < c1 ? vf_load(r.p, c, r.lead, r.V) : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float4 f = c < c1 && r.f ? vf_load(r.f, c, r.lead, r.V) : make_float4(0.f, 0.f, 0.f, 0.f);
+            h.w[i] = make_float4(prob(p.x), prob(p.y), prob(p.z), prob(p.w));
+            h.f[i] = make_float4(prob(f.x), prob(f.y), prob(f.z), prob(f.w));
+        }
+    }
+    if (r.f) {
+#pragma unroll 1
+        for (; h.refused < r.refused; ++h.refused) {
+            const float z = r.z[h.refused];
+#pragma unroll
+            for (int i = 0; i < kVfAhead; ++i) {
+                h.w[i].x = prob(__fsub_rn(h.w[i].x, __fmul_rn(z, h.f[i].x)));
+                h.w[i].y = prob(__fsub_rn(h.w[i].y, __fmul_rn(z, h.f[i].y)));
+                h.w[i].z = prob(__fsub_rn(h.w[i].z, __fmul_rn(z, h.f[i].z)));
+                h.w[i].w = prob(__fsub_rn(h.w[i].w, __fmul_rn(z, h.f[i].w)));
+            }
+        }
+    }
+    u64 sum = 0;
+    Steps s{0, 0, 0};
+    uint32_t n = 0;
+#pragma unroll
+    for (int i = 0; i < kVfAhead; ++i) {
+        const float w[4] = {h.w[i].x, h.w[i].y, h.w[i].z, h.w[i].w};
+        if (fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3])) < 2.f) {
+            n += 4;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) steps_add(s, w[e]);
+        } else {
+            sum += steps(w[0]) + steps(w[1]) + steps(w[2]) + steps(w[3]);
+        }
+    }
+    sum += steps_sum(s, n);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return sum;
+}
+
 // The first element of chunks c0 .. c1 at which the running sum, from `run` on, passes `goal`.
 __device__ __forceinline__ int vf_find(const VfRow &r, int c0, int c1, u64 run, u64 goal, int lane)
 {
@@ -210,8 +264,8 @@ __device__ __forceinline__ int vf_find(const VfRow &r, int c0, int c1, u64 run, 
     return -1;
 }
 
-template <int kVfThreads>
-__global__ void __launch_bounds__(kVfThreads, 1024 / kVfThreads) tree_verify_kernel(const VerifyArgs a)
+template <int kVfThreads, int kBlocks, bool HELD>
+__global__ void __launch_bounds__(kVfThreads, kBlocks) tree_verify_kernel(const VerifyArgs a)
 {
     constexpr int kVfWarps = kVfThreads / 32;
     cg::cluster_group cl = cg::this_cluster();
@@ -267,6 +321,8 @@ __global__ void __launch_bounds__(kVfThreads, 1024 / kVfThreads) tree_verify_ker
     int round = 0;
     float Z = 1.f;                                 // warp 0: of the weights behind the refusals so far
     VfRow w;
+    VfHeld held;
+    held.row = -1;
     int c0 = 0, c1 = 0, stride = 1;
     u64 mine = 0, total = 0, before = 0;
     while (true) {
@@ -352,7 +408,12 @@ __global__ void __launch_bounds__(kVfThreads, 1024 / kVfThreads) tree_verify_ker
         bool plain = false;
         while (true) {
             u64 *sums = s_sum[round & 1], *totals = s_total[round & 1];
-            mine = vf_sum(w, c0, c1, stride, s_groups[warp], lane);
+            if constexpr (HELD) {
+                if (lane == 0) s_groups[warp][0] = 0;
+                mine = vf_sum_held(w, plain ? row + ((int64_t)1 << 62) : row, c0, c1, held, lane);
+            } else {
+                mine = vf_sum(w, c0, c1, stride, s_groups[warp], lane);
+            }
             if (lane == 0) sums[warp] = mine;
             __syncthreads();
             if (!w.f && w.refused > 0) {
@@ -459,8 +520,10 @@ extern "C" pa_status pa_tree_verify(const float *target_probs, const float *draf
     int cs = 1;
     while (cs < kVfMaxCluster && cs * 4096 < vocab) cs *= 2;
     // the more threads the fewer round trips a piece of a row takes: 512 (two CTAs an SM) where all CTAs are then on the
-    // GPU at once, else 256 (four)
+    // GPU at once, else 256 (four).  Drawn nodes' rows are summed after every refusal: kept in registers where a warp's
+    // piece fits (512 chunks of four to a CTA of 16 warps, 128 a warp) and an SM has one CTA
     const int64_t ctas = (int64_t)n_reqs * cs;
+    const bool held = draft_probs && ctas <= num_sms() && (vocab + (vocab % 4 ? 3 : 0) + 3) / 4 <= cs * 16 * 32 * kVfAhead;
     const int threads = ctas <= 2 * num_sms() ? 512 : 256;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
@@ -475,7 +538,8 @@ extern "C" pa_status pa_tree_verify(const float *target_probs, const float *draf
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = launch_overlap() != PA_OVERLAP_OFF ? 2 : 1;
-    auto kern = threads == 512 ? tree_verify_kernel<512> : tree_verify_kernel<256>;
+    auto kern = held ? tree_verify_kernel<512, 1, true>
+                     : threads == 512 ? tree_verify_kernel<512, 2, false> : tree_verify_kernel<256, 4, false>;
     if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) return PA_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
