@@ -18,27 +18,50 @@
 // and its last segment with others: two slots of fp32 partials per unit, merged
 // by a second kernel in the pieces' order (deterministic).
 //
-// A CTA has two streams, X = A and B, each with a warpgroup, S columns, O columns
-// and running maximum and sum:
+// A CTA has two streams, X = A and B, each with a warpgroup, a warp that issues its
+// products, S columns, O columns and running maximum and sum:
 //   more than 128 rows:  A and B are the two tiles of rows, over every token tile;
 //   up to 128 rows:      A takes the even token tiles, B the odd ones, of the same
 //                        rows, joined when the piece ends.
-// Either way step i = 0, 1, ... belongs to stream i & 1, and the tensor core runs
-// S(0) S(1) | PV(0) S(2) | PV(1) S(3) | ...: a step's softmax has the time of the
-// other stream's products.
+// The tensor core runs S_A S_B | PV_A S_A | PV_B S_B | ..., in turn (TURN): a step's
+// softmax has the time of the other stream's products.
 //   S = Q K^T      A = Q, B = K tile as TMA left it, fp32 in tensor memory
-//   P over S       bf16, read by the second product from tensor memory
+//   P over S       bf16 (2^-8 of a weight; the sum is of the unrounded ones), read by
+//                  the second product from tensor memory
 //   O += P V       fp32 in tensor memory, rescaled only when the running maximum
 //                  grows by more than 2^8
 // Warps 0-7: softmax, one row a thread; 8 and 9: K and V copies through the page
-// table (16 consecutive slots are one TMA box, any other four rows one gather4
-// copy); 10 and 11: a stream's products each.
+// table, of which 8 also walks the units' pieces and hands them to every role; 10
+// and 11: a stream's products each.  16 consecutive slots are one TMA box.  Any
+// other rows are 16-byte asynchronous copies (bf16), handed on when the next tile's
+// have been issued: pages of one slot, 32 requests of up to 8192 tokens, 139 us by
+// gather4 copies, 104 us so; and the end of a request's last page, 97.7 -> 93.6 us
+// over 32 ragged requests.
+//
+// e4m3 cache.  K stays e4m3 in its product, against q's row as two e4m3 terms that
+// share a scale (q within 2^-17 of its row's largest element); a key's scale joins
+// the softmax scale where 16 keys share one.  V becomes bf16 with its scale, exactly,
+// by the softmax warpgroups while S is on its way (48 requests of 500 to 8192
+// tokens: behind the exponentials 193 us, like this 160; to fp16 with a running
+// exponent 209; by warps whose rows are no nodes' 178 to 192).
 //
 // Hidden rows: a hidden token's weight is 0, but 0 times a NaN or an infinity in
 // its V row would reach every node.  Only drafted tokens are ever hidden (context
-// is seen by all), so the products' warp looks through their V rows in shared
-// memory, zeroes one that holds such a value, and the rows that do see it add its
+// is seen by all), so these V rows are looked through in shared memory, one
+// that holds such a value becomes zeros, and the rows that do see it add its
 // part by hand when the piece ends.
+//
+// Measured, both kernels in a graph, D = 128, 8 kv heads of 4 query heads: 403 MB of
+// cache (32 requests of 500 to 8192 tokens, trees of up to 32 nodes) 93.6 us, 64 % of
+// a copy's rate (6.78 TB/s); ncu over the first kernel: 91.0 us, 403.4 MB read,
+// tensor pipe active 28 %, issue slots 20 %.  One request of 32K tokens 49.6 us for
+// 136 MB; of 1K 11.6 us, which is start, plan, two steps and the merge.  e4m3: 48
+// requests, 320 MB, 159.6 us: the widening and the softmax share the warps.
+// What bounds it is the chain of a step (S, its read-back of 128 columns,
+// exponentials, P, PV: 2050 cycles), of which two are in flight.  S in two halves of
+// 64 columns (2900 cycles a step), a tile kept from one piece to the next (99.6 us
+// for 93.6) and rows without nodes skipped (spills: 26 -> 29 us at 96 small
+// requests) lost.
 #include <math.h>
 #include <string.h>
 
@@ -235,7 +258,7 @@ struct TrCfg {
            Q_SPLIT = DRAIN + 2,                          // e4m3: Q is there in its terms
            WIDE_FREE = Q_SPLIT + 2,                      // and the stream's product with V is done
            TURN = WIDE_FREE + 2,                         // whose products are next
-           JOINT = TURN + 2,                          // stream A's Q, for stream B
+           JOINT = TURN + 2,                             // stream A's Q, for stream B
            ITEM_FULL, ITEM_EMPTY = ITEM_FULL + kTrPieces, N_BARS = ITEM_EMPTY + kTrPieces };
     static constexpr int OffMeta = (OffBar + N_BARS * 8 + 15) & ~15;     // uint4 [kTrMeta]: valid positions
     static constexpr int OffML = OffMeta + kTrMeta * 16;                 // float2 [128]: stream B's (m, l)
@@ -369,123 +392,123 @@ __device__ __forceinline__ void tr_copy(const TreeArgs &a, const TrPlan &plan, T
         fetch(k.t0);
         fetch_exps();
 #pragma unroll 1
-            for (int t = k.t0; t < k.t1 && go; ++t) {
-                int sl[4] = {nx[0], nx[1], nx[2], nx[3]};
-                if (t + 1 < k.t1) fetch(t + 1);
-                if (!E8 && seq >= stages && held != 0 && !__all_sync(0xffffffffu, mbar_try_wait(empty + st * 8, ph ^ 1)))
-                    release_held(0);
-                if (seq >= stages && !tr_wait(a, empty + st * 8, ph ^ 1, s_abort)) {
-                    go = false;
-                    break;
+        for (int t = k.t0; t < k.t1 && go; ++t) {
+            int sl[4] = {nx[0], nx[1], nx[2], nx[3]};
+            if (t + 1 < k.t1) fetch(t + 1);
+            if (!E8 && seq >= stages && held != 0 && !__all_sync(0xffffffffu, mbar_try_wait(empty + st * 8, ph ^ 1)))
+                release_held(0);
+            if (seq >= stages && !tr_wait(a, empty + st * 8, ph ^ 1, s_abort)) {
+                go = false;
+                break;
+            }
+            const uint32_t dst = ring + st * C::RAW, fb = full + st * 8;
+            bool ok[4];
+            uint32_t nib = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool in = t * kTrTile + 4 * lane + e < k.L;
+                ok[e] = in && sl[e] >= 0 && sl[e] < a.size;
+                if (in && !ok[e]) errs |= PA_DEVERR_SLOT;
+                nib |= (uint32_t)ok[e] << e;
+            }
+            const int s0 = __shfl_sync(0xffffffffu, sl[0], lane & ~3);
+            const bool run = nib == 15u && sl[0] == s0 + 4 * (lane & 3) && sl[1] == sl[0] + 1 && sl[2] == sl[0] + 2 &&
+                             sl[3] == sl[0] + 3;
+            const bool page = ((__ballot_sync(0xffffffffu, run) >> (lane & ~3)) & 0xFu) == 0xFu;
+            const unsigned has = __ballot_sync(0xffffffffu, nib != 0u);
+            const bool none = ((has >> (lane & ~3)) & 0xFu) == 0u;
+            int some = 0;              // a valid row of the tile
+            if constexpr (E8)
+                some = __shfl_sync(0xffffffffu, nib & 1u ? sl[0] : nib & 2u ? sl[1] : nib & 4u ? sl[2] : sl[3],
+                                   has ? __ffs(has) - 1 : 0);
+            constexpr int HV = E8 ? 1 : C::HALVES, PITCH = E8 ? D : 128;     // boxes of a row, and their bytes
+            if (page || none) {
+                // a page's rows, or rows out of range, which read as zeros
+                if ((lane & 3) == 0) {
+#pragma unroll
+                    for (int hh = 0; hh < HV; ++hh)
+                        tma_load_2d(dst + hh * kTrHalf + (lane >> 2) * 16 * PITCH, m16, col + hh * 64,
+                                    none ? a.total_rows : a.layer_row0 + sl[0], fb);
                 }
-                const uint32_t dst = ring + st * C::RAW, fb = full + st * 8;
-                bool ok[4];
-                uint32_t nib = 0;
+            } else if constexpr (E8) {
+                // a position without a row repeats a valid one of the tile: its exponent byte and its bit say so
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const bool in = t * kTrTile + 4 * lane + e < k.L;
-                    ok[e] = in && sl[e] >= 0 && sl[e] < a.size;
-                    if (in && !ok[e]) errs |= PA_DEVERR_SLOT;
-                    nib |= (uint32_t)ok[e] << e;
-                }
-                const int s0 = __shfl_sync(0xffffffffu, sl[0], lane & ~3);
-                const bool run = nib == 15u && sl[0] == s0 + 4 * (lane & 3) && sl[1] == sl[0] + 1 && sl[2] == sl[0] + 2 &&
-                                 sl[3] == sl[0] + 3;
-                const bool page = ((__ballot_sync(0xffffffffu, run) >> (lane & ~3)) & 0xFu) == 0xFu;
-                const unsigned has = __ballot_sync(0xffffffffu, nib != 0u);
-                const bool none = ((has >> (lane & ~3)) & 0xFu) == 0u;
-                int some = 0;              // a valid row of the tile
-                if constexpr (E8)
-                    some = __shfl_sync(0xffffffffu, nib & 1u ? sl[0] : nib & 2u ? sl[1] : nib & 4u ? sl[2] : sl[3],
-                                       has ? __ffs(has) - 1 : 0);
-                constexpr int HV = E8 ? 1 : C::HALVES, PITCH = E8 ? D : 128;     // boxes of a row, and their bytes
-                if (page || none) {
-                    // a page's rows, or rows out of range, which read as zeros
-                    if ((lane & 3) == 0) {
+                for (int e = 0; e < 4; ++e) sl[e] = a.layer_row0 + (ok[e] ? sl[e] : some);
+                tma_gather4(dst + lane * 4 * PITCH, m1, col, sl[0], sl[1], sl[2], sl[3], fb);
+            }
+            uint32_t bytes = C::RAW;
+            bool copied = false;
+            if constexpr (!E8) {
+                // rows anywhere, and the ends of pages: 16-byte copies, four lanes on 64 bytes of a row; zeros where there
+                // is no row.  (gather4 copies cost 100 cycles of issue each, 64 a tile at D = 128: 32 requests of up to
+                // 8192 tokens at pages of one slot took 139 us against 115; at D = 64 there is no difference.)
+                const bool gathered = !page && !none;
+                copied = __any_sync(0xffffffffu, gathered);
+                if (copied) {
+                    const uint8_t *rows = isv ? a.v : a.k;
+                    bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, !gathered)) * 4u * 128u * C::HALVES;
 #pragma unroll
-                        for (int hh = 0; hh < HV; ++hh)
-                            tma_load_2d(dst + hh * kTrHalf + (lane >> 2) * 16 * PITCH, m16, col + hh * 64,
-                                        none ? a.total_rows : a.layer_row0 + sl[0], fb);
-                    }
-                } else if constexpr (E8) {
-                    // a position without a row repeats a valid one of the tile: its exponent byte and its bit say so
+                    for (int x = 0; x < 16; ++x) {
+                        const int from = __shfl_sync(0xffffffffu, sl[x & 3], (lane & ~3) + (x >> 2));
+                        const bool row = __shfl_sync(0xffffffffu, (int)ok[x & 3], (lane & ~3) + (x >> 2));
+                        if (!gathered) continue;
+                        const int r = (lane >> 2) * 16 + x;
+                        const uint8_t *src = rows + ((int64_t)(row ? from : 0) * a.Hkv + k.h) * (2 * D);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) sl[e] = a.layer_row0 + (ok[e] ? sl[e] : some);
-                    tma_gather4(dst + lane * 4 * PITCH, m1, col, sl[0], sl[1], sl[2], sl[3], fb);
-                }
-                uint32_t bytes = C::RAW;
-                bool copied = false;
-                if constexpr (!E8) {
-                    // rows anywhere, and the ends of pages: 16-byte copies, four lanes on 64 bytes of a row; zeros where there
-                    // is no row.  (gather4 copies cost 100 cycles of issue each, 64 a tile at D = 128: 32 requests of up to
-                    // 8192 tokens at pages of one slot took 139 us against 115; at D = 64 there is no difference.)
-                    const bool gathered = !page && !none;
-                    copied = __any_sync(0xffffffffu, gathered);
-                    if (copied) {
-                        const uint8_t *rows = isv ? a.v : a.k;
-                        bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, !gathered)) * 4u * 128u * C::HALVES;
-#pragma unroll
-                        for (int x = 0; x < 16; ++x) {
-                            const int from = __shfl_sync(0xffffffffu, sl[x & 3], (lane & ~3) + (x >> 2));
-                            const bool row = __shfl_sync(0xffffffffu, (int)ok[x & 3], (lane & ~3) + (x >> 2));
-                            if (!gathered) continue;
-                            const int r = (lane >> 2) * 16 + x;
-                            const uint8_t *src = rows + ((int64_t)(row ? from : 0) * a.Hkv + k.h) * (2 * D);
-#pragma unroll
-                            for (int q = 0; q < 2 * C::HALVES; ++q) {
-                                const int ch = q * 4 + (lane & 3);
-                                cp_async_16(dst + (ch >> 3) * kTrHalf + r * 128 + (((ch & 7) ^ (r & 7)) << 4), src + ch * 16, row ? 16 : 0);
-                            }
+                        for (int q = 0; q < 2 * C::HALVES; ++q) {
+                            const int ch = q * 4 + (lane & 3);
+                            cp_async_16(dst + (ch >> 3) * kTrHalf + r * 128 + (((ch & 7) ^ (r & 7)) << 4), src + ch * 16, row ? 16 : 0);
                         }
                     }
-                    cp_async_commit();
                 }
-                if (!isv) {
-                    uint32_t w = nib << (4 * (lane & 7));
+                cp_async_commit();
+            }
+            if (!isv) {
+                uint32_t w = nib << (4 * (lane & 7));
 #pragma unroll
-                    for (int o = 1; o < 8; o <<= 1) w |= __shfl_xor_sync(0xffffffffu, w, o);
-                    if ((lane & 7) == 0) reinterpret_cast<uint32_t *>(meta + seq % kTrMeta)[lane >> 3] = w;
-                    __syncwarp();
-                }
-                if constexpr (E8) {
-                    const int at = seq % kTrMeta;
-                    if (isv) {
-                        reinterpret_cast<uint32_t *>(sb + C::OffVE + at * 128)[lane] =
-                            (uint32_t)((ok[0] ? ex[0] : 255) | (ok[1] ? ex[1] : 255) << 8 | (ok[2] ? ex[2] : 255) << 16 |
-                                       (ok[3] ? ex[3] : 255) << 24);
-                    } else {
-                        // do 16 keys share a scale? (those past the end do not matter)
-                        const int x0 = __shfl_sync(0xffffffffu, ex[0], lane & ~3);
-                        bool one = true;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) one = one && (t * kTrTile + 4 * lane + e >= k.L || (ok[e] && ex[e] == x0));
-                        const bool grouped = __all_sync(0xffffffffu, one);
-                        if (lane == 0) reinterpret_cast<int *>(sb + C::OffGr)[at] = grouped;
-                        // (an empty block's scale is 2^-126 in place of 0: a hidden column's minus infinity stays that)
-                        auto scale_of = [](int e) { return __uint_as_float((uint32_t)max(e, 1) << 23); };
-                        reinterpret_cast<float4 *>(sb + C::OffKS + at * 512)[lane] =
-                            make_float4(scale_of(ok[0] ? ex[0] : 0), scale_of(ok[1] ? ex[1] : 0), scale_of(ok[2] ? ex[2] : 0),
-                                        scale_of(ok[3] ? ex[3] : 0));
-                    }
-                    __syncwarp();
-                }
-                if constexpr (!E8) {
-                    if (held != 0) release_held(1);
-                    if (copied) {
-                        held = fb;
-                        held_bytes = bytes;
-                    }
-                }
-                if (!copied && lane == 0) mbar_arrive_expect_tx(fb, bytes);
+                for (int o = 1; o < 8; o <<= 1) w |= __shfl_xor_sync(0xffffffffu, w, o);
+                if ((lane & 7) == 0) reinterpret_cast<uint32_t *>(meta + seq % kTrMeta)[lane >> 3] = w;
                 __syncwarp();
-                if (t + 1 < k.t1) fetch_exps();
-                ++seq;
-                if (++st == stages) {
-                    st = 0;
-                    ph ^= 1;
+            }
+            if constexpr (E8) {
+                const int at = seq % kTrMeta;
+                if (isv) {
+                    reinterpret_cast<uint32_t *>(sb + C::OffVE + at * 128)[lane] =
+                        (uint32_t)((ok[0] ? ex[0] : 255) | (ok[1] ? ex[1] : 255) << 8 | (ok[2] ? ex[2] : 255) << 16 |
+                                   (ok[3] ? ex[3] : 255) << 24);
+                } else {
+                    // do 16 keys share a scale? (those past the end do not matter)
+                    const int x0 = __shfl_sync(0xffffffffu, ex[0], lane & ~3);
+                    bool one = true;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) one = one && (t * kTrTile + 4 * lane + e >= k.L || (ok[e] && ex[e] == x0));
+                    const bool grouped = __all_sync(0xffffffffu, one);
+                    if (lane == 0) reinterpret_cast<int *>(sb + C::OffGr)[at] = grouped;
+                    // (an empty block's scale is 2^-126 in place of 0: a hidden column's minus infinity stays that)
+                    auto scale_of = [](int e) { return __uint_as_float((uint32_t)max(e, 1) << 23); };
+                    reinterpret_cast<float4 *>(sb + C::OffKS + at * 512)[lane] =
+                        make_float4(scale_of(ok[0] ? ex[0] : 0), scale_of(ok[1] ? ex[1] : 0), scale_of(ok[2] ? ex[2] : 0),
+                                    scale_of(ok[3] ? ex[3] : 0));
+                }
+                __syncwarp();
+            }
+            if constexpr (!E8) {
+                if (held != 0) release_held(1);
+                if (copied) {
+                    held = fb;
+                    held_bytes = bytes;
                 }
             }
-            if (!E8 && held != 0) release_held(0);
+            if (!copied && lane == 0) mbar_arrive_expect_tx(fb, bytes);
+            __syncwarp();
+            if (t + 1 < k.t1) fetch_exps();
+            ++seq;
+            if (++st == stages) {
+                st = 0;
+                ph ^= 1;
+            }
+        }
+        if (!E8 && held != 0) release_held(0);
         }
     // the warp leaves only when its copies have landed, whether or not anyone has given up by now
 #pragma unroll 1
@@ -746,99 +769,99 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
             if (!bad) bad = !tr_wait(a, b, parity, s_abort);
         };
 #pragma unroll 1
-            for (int it = 0;; ++it) {
-                const int slot = it % kTrPieces;
-                tr_wait_ring(bar(C::ITEM_FULL + slot), (it / kTrPieces) & 1);
-                const TrPiece k = s_piece[slot];
+        for (int it = 0;; ++it) {
+            const int slot = it % kTrPieces;
+            tr_wait_ring(bar(C::ITEM_FULL + slot), (it / kTrPieces) & 1);
+            const TrPiece k = s_piece[slot];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::ITEM_EMPTY + slot));
+            if (k.end) break;
+            const int nt = k.t1 - k.t0, two = tr_two(a, k);
+            const int N = two ? 2 * nt : nt, c = k.L - k.n;
+            // a ring stage is free when both streams are through with it, or twice the one that uses it
+            auto release = [&](uint32_t b) {
+                umma_commit(b);
+                if (!two) umma_commit(b);
+            };
+            auto qk = [&](int st) {
+                const uint32_t q = sQ + (two ? X : 0) * C::TILE, kk = sK + st * C::RAW;
+                if constexpr (E8) {
+                    // both terms of q against the same keys, 32 of D a step; D = 64: the terms share a 128-byte row
+#pragma unroll
+                    for (int s = 0; s < D / 16; ++s) {
+                        constexpr int SPT = D / 32;
+                        const int term = s / SPT, o = (s % SPT) * 32;
+                        const uint64_t kd = D == 128 ? smem_desc_sw128(kk + o, 16, 1024) : smem_desc_sw64(kk + o, 16, 512);
+                        umma_ss_f8(tmem + X * 128, smem_desc_sw128(q + term * (D == 128 ? kTrHalf : 64) + o, 16, 1024), kd,
+                                   id_s, s > 0);
+                    }
+                } else
+#pragma unroll
+                for (int s = 0; s < D / 16; ++s)
+                    umma_ss(tmem + X * 128, smem_desc_sw128(q + (s >> 2) * kTrHalf + (s & 3) * 32, 16, 1024),
+                            smem_desc_sw128(kk + (s >> 2) * kTrHalf + (s & 3) * 32, 16, 1024), id_s, s > 0);
+                umma_commit(bar(C::S_FULL + X));
+                release(bar(C::K_EMPTY + st));
+            };
+            const int dt = two ? 1 : 2;        // token tiles from one step of the stream to the next
+            if (X < N) {
+                const int s = seq + (two ? 0 : X), st = s % C::NK;
+                // (stream B hears of A's Q from A's warp: it does not follow every phase of that barrier)
+                if (X == 0) {
+                    wait(bar(E8 ? C::Q_SPLIT : C::Q_FULL), piece & 1);
+                    if (!two && N > 1 && lane == 0) mbar_arrive(bar(C::JOINT));
+                } else {
+                    wait(two ? bar((E8 ? C::Q_SPLIT : C::Q_FULL) + 1) : bar(C::JOINT), (two ? p2 : pj) & 1);
+                    if (two) ++p2;
+                    else ++pj;
+                }
+                wait(bar(C::K_FULL + st), (s / C::NK) & 1);
+                tc_fence_after();
+                if (!bad) if (elect_one()) qk(st);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(C::ITEM_EMPTY + slot));
-                if (k.end) break;
-                const int nt = k.t1 - k.t0, two = tr_two(a, k);
-                const int N = two ? 2 * nt : nt, c = k.L - k.n;
-                // a ring stage is free when both streams are through with it, or twice the one that uses it
-                auto release = [&](uint32_t b) {
-                    umma_commit(b);
-                    if (!two) umma_commit(b);
-                };
-                auto qk = [&](int st) {
-                    const uint32_t q = sQ + (two ? X : 0) * C::TILE, kk = sK + st * C::RAW;
-                    if constexpr (E8) {
-                        // both terms of q against the same keys, 32 of D a step; D = 64: the terms share a 128-byte row
-#pragma unroll
-                        for (int s = 0; s < D / 16; ++s) {
-                            constexpr int SPT = D / 32;
-                            const int term = s / SPT, o = (s % SPT) * 32;
-                            const uint64_t kd = D == 128 ? smem_desc_sw128(kk + o, 16, 1024) : smem_desc_sw64(kk + o, 16, 512);
-                            umma_ss_f8(tmem + X * 128, smem_desc_sw128(q + term * (D == 128 ? kTrHalf : 64) + o, 16, 1024), kd,
-                                       id_s, s > 0);
-                        }
-                    } else
-#pragma unroll
-                    for (int s = 0; s < D / 16; ++s)
-                        umma_ss(tmem + X * 128, smem_desc_sw128(q + (s >> 2) * kTrHalf + (s & 3) * 32, 16, 1024),
-                                smem_desc_sw128(kk + (s >> 2) * kTrHalf + (s & 3) * 32, 16, 1024), id_s, s > 0);
-                    umma_commit(bar(C::S_FULL + X));
-                    release(bar(C::K_EMPTY + st));
-                };
-                const int dt = two ? 1 : 2;        // token tiles from one step of the stream to the next
-                if (X < N) {
-                    const int s = seq + (two ? 0 : X), st = s % C::NK;
-                    // (stream B hears of A's Q from A's warp: it does not follow every phase of that barrier)
-                    if (X == 0) {
-                        wait(bar(E8 ? C::Q_SPLIT : C::Q_FULL), piece & 1);
-                        if (!two && N > 1 && lane == 0) mbar_arrive(bar(C::JOINT));
-                    } else {
-                        wait(two ? bar((E8 ? C::Q_SPLIT : C::Q_FULL) + 1) : bar(C::JOINT), (two ? p2 : pj) & 1);
-                        if (two) ++p2;
-                        else ++pj;
-                    }
-                    wait(bar(C::K_FULL + st), (s / C::NK) & 1);
-                    tc_fence_after();
-                    if (!bad) if (elect_one()) qk(st);
-                    __syncwarp();
-                }
-#pragma unroll 1
-                for (int t = two ? 0 : X; t < nt; t += dt, ++px) {
-                    const int s = seq + t, st = s % C::NV, sk = (s + dt) % C::NK;
-                    // (e4m3: the softmax warpgroup has widened V into the stream's buffer when the weights are there)
-                    const uint32_t vt = E8 ? base + C::OffWide + X * C::TILE : sV + st * C::RAW;
-                    if constexpr (!E8) wait(bar(C::V_FULL + st), (s / C::NV) & 1);
-                    // drafted tokens' rows must not hold what a weight of 0 does not cancel
-                    const int p0 = (k.t0 + t) * kTrTile, lo = max(0, c - p0), hi = min(kTrTile, k.L - p0);
-                    if (!E8 && lo < hi) {
-                        if (X == 0 || !two) {
-                            if (!bad && tr_tame<D>(vt, lo, hi, lane)) {
-                                if (lane == 0) *(volatile int *)&s_wild[X][piece & 7] = piece + 1;
-                                __threadfence_block();
-                            }
-                            __syncwarp();
-                        }
-                        if (two) named_bar_sync(2, 64);
-                    }
-                    if (t + dt < nt) wait(bar(C::K_FULL + sk), ((s + dt) / C::NK) & 1);
-                    // the piece's first product overwrites O
-                    if (t < dt && pq++ > 0) wait(bar(C::O_FREE + X), pq & 1);
-                    wait(bar(C::P_READY + X), px & 1);
-                    if (!turn) wait(bar(C::TURN + X), turns++ & 1);
-                    tc_fence_after();
-                    if (!bad) if (elect_one()) {
-#pragma unroll
-                        for (int kk = 0; kk < kTrTile / 16; ++kk)
-                            umma_ts(tmem + C::ColO + X * D, tmem + X * 128 + kk * 8,
-                                    smem_desc_sw128(vt + kk * 2048, kTrHalf, 1024), C::kIdPV, kk > 0 || t >= dt);
-                        if constexpr (E8) umma_commit(bar(C::WIDE_FREE + X));
-                        else release(bar(C::V_EMPTY + st));
-                        if (t + dt < nt) qk(sk);
-                        else umma_commit(bar(C::O_FULL + X));
-                    }
-                    __syncwarp();
-                    // the next step, or the next piece's first
-                    turn = X == 0 && t + 1 >= nt && !two;
-                    if (!turn && lane == 0) mbar_arrive(bar(C::TURN + 1 - X));
-                }
-                seq += nt;
-                ++piece;
             }
+#pragma unroll 1
+            for (int t = two ? 0 : X; t < nt; t += dt, ++px) {
+                const int s = seq + t, st = s % C::NV, sk = (s + dt) % C::NK;
+                // (e4m3: the softmax warpgroup has widened V into the stream's buffer when the weights are there)
+                const uint32_t vt = E8 ? base + C::OffWide + X * C::TILE : sV + st * C::RAW;
+                if constexpr (!E8) wait(bar(C::V_FULL + st), (s / C::NV) & 1);
+                // drafted tokens' rows must not hold what a weight of 0 does not cancel
+                const int p0 = (k.t0 + t) * kTrTile, lo = max(0, c - p0), hi = min(kTrTile, k.L - p0);
+                if (!E8 && lo < hi) {
+                    if (X == 0 || !two) {
+                        if (!bad && tr_tame<D>(vt, lo, hi, lane)) {
+                            if (lane == 0) *(volatile int *)&s_wild[X][piece & 7] = piece + 1;
+                            __threadfence_block();
+                        }
+                        __syncwarp();
+                    }
+                    if (two) named_bar_sync(2, 64);
+                }
+                if (t + dt < nt) wait(bar(C::K_FULL + sk), ((s + dt) / C::NK) & 1);
+                // the piece's first product overwrites O
+                if (t < dt && pq++ > 0) wait(bar(C::O_FREE + X), pq & 1);
+                wait(bar(C::P_READY + X), px & 1);
+                if (!turn) wait(bar(C::TURN + X), turns++ & 1);
+                tc_fence_after();
+                if (!bad) if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < kTrTile / 16; ++kk)
+                        umma_ts(tmem + C::ColO + X * D, tmem + X * 128 + kk * 8,
+                                smem_desc_sw128(vt + kk * 2048, kTrHalf, 1024), C::kIdPV, kk > 0 || t >= dt);
+                    if constexpr (E8) umma_commit(bar(C::WIDE_FREE + X));
+                    else release(bar(C::V_EMPTY + st));
+                    if (t + dt < nt) qk(sk);
+                    else umma_commit(bar(C::O_FULL + X));
+                }
+                __syncwarp();
+                // the next step, or the next piece's first
+                turn = X == 0 && t + 1 >= nt && !two;
+                if (!turn && lane == 0) mbar_arrive(bar(C::TURN + 1 - X));
+            }
+            seq += nt;
+            ++piece;
+        }
         // one more commit, which arrives once every product issued has completed, before tensor memory is freed
         if (elect_one()) umma_commit(bar(C::DRAIN + X));
         __syncwarp();
@@ -869,229 +892,229 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
         tr_wait_ring(bar(C::ITEM_FULL), 0);
         if (!s_piece[0].end) load_q(s_piece[0]);
 #pragma unroll 1
-            while (!s_piece[piece % kTrPieces].end) {
-                const TrPiece &k = s_piece[piece % kTrPieces];
-                const int nt = k.t1 - k.t0, c = k.L - k.n;
-                const bool two = tr_two(a, k);
-                const int N = two ? 2 * nt : nt, t00 = k.t0;
-                // this thread's row: a node and a head of its own
-                const int nd = (row * a.inv_g) >> 16, node = (2 * k.pair + (two ? X : 0)) * a.tq + nd;
-                const bool live = nd < a.tq && node < k.n;
-                const int64_t qrow = k.q0 + node;
-                float sl2 = a.scale_log2;
-                if (a.wait_ns == 0 && !bad) {
-                    // a wait limit of 0: give up at the first piece, as a timed-out wait would
-                    *s_abort = 1;
-                    set_error(a.err, PA_DEVERR_TIMEOUT);
-                    bad = true;
+        while (!s_piece[piece % kTrPieces].end) {
+            const TrPiece &k = s_piece[piece % kTrPieces];
+            const int nt = k.t1 - k.t0, c = k.L - k.n;
+            const bool two = tr_two(a, k);
+            const int N = two ? 2 * nt : nt, t00 = k.t0;
+            // this thread's row: a node and a head of its own
+            const int nd = (row * a.inv_g) >> 16, node = (2 * k.pair + (two ? X : 0)) * a.tq + nd;
+            const bool live = nd < a.tq && node < k.n;
+            const int64_t qrow = k.q0 + node;
+            float sl2 = a.scale_log2;
+            if (a.wait_ns == 0 && !bad) {
+                // a wait limit of 0: give up at the first piece, as a timed-out wait would
+                *s_abort = 1;
+                set_error(a.err, PA_DEVERR_TIMEOUT);
+                bad = true;
+            }
+            if constexpr (E8) {
+                // this thread's row of q, in place, into its two e4m3 terms; the row's scale joins the softmax scale
+                if (X == 0 || two) {
+                    wait(bar(C::Q_FULL + X), (X == 0 ? piece : p2) & 1);
+                    const float qs = split_q_row<D>(base + X * C::TILE, row, a.negate ? -1.f : 1.f);
+                    if (X == 0) reinterpret_cast<float *>(sb + C::OffQS)[row] = qs;
+                    fence_proxy_async_smem();
+                    mbar_arrive(bar(C::Q_SPLIT + X));
+                    sl2 = tr_scale(sl2 * qs);
+                }
+                p2 += two;
+            }
+            float m = -INFINITY, l = 0.f;      // maximum of s (not yet scaled), sum
+#pragma unroll 1
+            for (int i = X; i < N; i += 2, ++sx) {
+                const int t = two ? i >> 1 : i, p0 = (t00 + t) * kTrTile;
+                // what of the tile this row sees, before S is there
+                uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
+                const bool nodes = p0 + kTrTile > c;
+                if (nodes) {
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const int s = p0 - c + 32 * w;
+                        if (s > -32) seen[w] = live ? tr_seen(a, qrow, node, s) : 0u;
+                    }
                 }
                 if constexpr (E8) {
-                    // this thread's row of q, in place, into its two e4m3 terms; the row's scale joins the softmax scale
-                    if (X == 0 || two) {
-                        wait(bar(C::Q_FULL + X), (X == 0 ? piece : p2) & 1);
-                        const float qs = split_q_row<D>(base + X * C::TILE, row, a.negate ? -1.f : 1.f);
-                        if (X == 0) reinterpret_cast<float *>(sb + C::OffQS)[row] = qs;
-                        fence_proxy_async_smem();
-                        mbar_arrive(bar(C::Q_SPLIT + X));
-                        sl2 = tr_scale(sl2 * qs);
+                    // V in bf16 with its scales, 32 rows a warp, while S is on its way: the stream's product before this
+                    // step is done
+                    const int s = kseq + t, st = s % C::NV;
+                    const uint32_t wide = base + C::OffWide + X * C::TILE;
+                    wait(bar(C::V_FULL + st), (s / C::NV) & 1);
+                    if (sx > 0) wait(bar(C::WIDE_FREE + X), (sx - 1) & 1);
+                    const int r0 = (warp & 3) * 32;
+                    tr_widen<D>(base + C::OffV + st * C::RAW, wide, sb + C::OffVE + s % kTrMeta * 128, r0, lane);
+                    if (lane == 0) {
+                        mbar_arrive(bar(C::V_EMPTY + st));
+                        if (!two) mbar_arrive(bar(C::V_EMPTY + st));
                     }
-                    p2 += two;
+                    const int lo = max(c - p0, r0), hi = min(k.L - p0, r0 + 32);
+                    if (lo < hi && tr_tame<D>(wide, lo, hi, lane) && lane == 0)
+                        *(volatile int *)&s_wild[X][piece & 7] = piece + 1;
+                    fence_proxy_async_smem();
                 }
-                float m = -INFINITY, l = 0.f;      // maximum of s (not yet scaled), sum
-#pragma unroll 1
-                for (int i = X; i < N; i += 2, ++sx) {
-                    const int t = two ? i >> 1 : i, p0 = (t00 + t) * kTrTile;
-                    // what of the tile this row sees, before S is there
-                    uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
-                    const bool nodes = p0 + kTrTile > c;
-                    if (nodes) {
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            const int s = p0 - c + 32 * w;
-                            if (s > -32) seen[w] = live ? tr_seen(a, qrow, node, s) : 0u;
-                        }
-                    }
-                    if constexpr (E8) {
-                        // V in bf16 with its scales, 32 rows a warp, while S is on its way: the stream's product before this
-                        // step is done
-                        const int s = kseq + t, st = s % C::NV;
-                        const uint32_t wide = base + C::OffWide + X * C::TILE;
-                        wait(bar(C::V_FULL + st), (s / C::NV) & 1);
-                        if (sx > 0) wait(bar(C::WIDE_FREE + X), (sx - 1) & 1);
-                        const int r0 = (warp & 3) * 32;
-                        tr_widen<D>(base + C::OffV + st * C::RAW, wide, sb + C::OffVE + s % kTrMeta * 128, r0, lane);
-                        if (lane == 0) {
-                            mbar_arrive(bar(C::V_EMPTY + st));
-                            if (!two) mbar_arrive(bar(C::V_EMPTY + st));
-                        }
-                        const int lo = max(c - p0, r0), hi = min(k.L - p0, r0 + 32);
-                        if (lo < hi && tr_tame<D>(wide, lo, hi, lane) && lane == 0)
-                            *(volatile int *)&s_wild[X][piece & 7] = piece + 1;
-                        fence_proxy_async_smem();
-                    }
-                    wait(bar(C::S_FULL + X), sx & 1);
-                    tc_fence_after();
-                    const uint4 valid = meta[(kseq + t) % kTrMeta];
-                    if constexpr (E8) {
-                        if (i == 1 && X == 1 && !two) sl2 = tr_scale(sl2 * reinterpret_cast<const float *>(sb + C::OffQS)[row]);
-                    }
-                    const bool masked = nodes || (valid.x & valid.y & valid.z & valid.w) != ~0u;
-                    seen[0] &= valid.x, seen[1] &= valid.y, seen[2] &= valid.z, seen[3] &= valid.w;
-                    uint32_t r[128];
-#pragma unroll
-                    for (int ch = 0; ch < 4; ++ch) tmem_ld32(s_addr + ch * 32, *reinterpret_cast<uint32_t(*)[32]>(&r[ch * 32]));
-                    tmem_wait_ld();
-                    // e4m3: a column's key scale joins the softmax scale where 16 columns share one, else S takes it now
-                    const int at = (kseq + t) % kTrMeta;
-                    float gs[8];
-                    if constexpr (E8) {
-                        const float *ks = reinterpret_cast<const float *>(sb + C::OffKS + at * 512);
-                        if (reinterpret_cast<const int *>(sb + C::OffGr)[at]) {
-#pragma unroll
-                            for (int g = 0; g < 8; ++g) gs[g] = ks[16 * g];
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) {
-                                const float4 f = reinterpret_cast<const float4 *>(ks)[j];
-                                r[4 * j] = __float_as_uint(__uint_as_float(r[4 * j]) * f.x);
-                                r[4 * j + 1] = __float_as_uint(__uint_as_float(r[4 * j + 1]) * f.y);
-                                r[4 * j + 2] = __float_as_uint(__uint_as_float(r[4 * j + 2]) * f.z);
-                                r[4 * j + 3] = __float_as_uint(__uint_as_float(r[4 * j + 3]) * f.w);
-                            }
-#pragma unroll
-                            for (int g = 0; g < 8; ++g) gs[g] = 1.f;
-                        }
-                    }
-                    if (masked) {
-#pragma unroll
-                        for (int j = 0; j < 128; ++j)
-                            if (!(seen[j >> 5] >> (j & 31) & 1u)) r[j] = __float_as_uint(-INFINITY);
-                    }
-                    float mx = -INFINITY;
-#pragma unroll
-                    for (int g = 0; g < 8; ++g) {
-                        auto f = [&](int j) { return __uint_as_float(r[16 * g + j]); };
-                        const float a0 = max3(f(0), f(1), f(2)), a1 = max3(f(3), f(4), f(5)), a2 = max3(f(6), f(7), f(8));
-                        const float a3 = max3(f(9), f(10), f(11)), a4 = max3(a0, f(12), f(13)), a5 = max3(a1, f(14), f(15));
-                        const float top = fmaxf(max3(a2, a3, a4), a5);
-                        mx = fmaxf(mx, E8 ? top * gs[g] : top);
-                    }
-                    bool rescale = false;
-                    float m_new = m;
-                    if (mx > m && (m == -INFINITY || (mx - m) * sl2 > 8.f)) {
-                        rescale = m != -INFINITY;
-                        m_new = mx;
-                    }
-                    const float alpha = rescale ? tr_ex2((m - m_new) * sl2) : 1.f;
-                    m = m_new;
-                    const float mb = m == -INFINITY ? 0.f : m * sl2;
-                    const uint64_t nmb2 = f32x2_pack(-mb, -mb);
-                    uint64_t sl22 = f32x2_pack(sl2, sl2), sum2 = f32x2_pack(0.f, 0.f);
-#pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {
-                        uint32_t pk[32];
-#pragma unroll
-                        for (int j = 0; j < 64; j += 2) {
-                            if (E8 && j % 16 == 0) {
-                                const float sg = tr_scale(sl2 * gs[hh * 4 + j / 16]);
-                                sl22 = f32x2_pack(sg, sg);
-                            }
-                            const uint64_t x = fma_f32x2(
-                                f32x2_pack(__uint_as_float(r[hh * 64 + j]), __uint_as_float(r[hh * 64 + j + 1])), sl22, nmb2);
-                            const float v0 = tr_ex2(f32x2_lo(x)), v1 = tr_ex2(f32x2_hi(x));
-                            sum2 = add_f32x2(sum2, f32x2_pack(v0, v1));
-                            pk[j / 2] = pack_bf16x2(v0, v1);
-                        }
-                        tmem_st32(s_addr + hh * 32, pk);
-                    }
-                    l = l * alpha + (f32x2_lo(sum2) + f32x2_hi(sum2));
-                    // O is stable here: S(i) completing implies that the stream's product before it did
-                    if (i >= 2 && __any_sync(0xffffffffu, rescale)) {
-#pragma unroll
-                        for (int ch = 0; ch < D / 32; ++ch) {
-                            uint32_t o[32];
-                            tmem_ld32(tmem + lane_base + C::ColO + X * D + ch * 32, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-                            tmem_st32(tmem + lane_base + C::ColO + X * D + ch * 32, o);
-                        }
-                    }
-                    tmem_wait_st();
-                    tc_fence_before();
-                    mbar_arrive(bar(C::P_READY + X));
-                }
-                kseq += nt;
-                // ---- the piece ends
-                if (X < N) wait(bar(C::O_FULL + X), ox & 1), ++ox;
+                wait(bar(C::S_FULL + X), sx & 1);
                 tc_fence_after();
-                float m2 = m == -INFINITY ? -INFINITY : m * sl2, fa = 1.f, fb = 0.f;
-                const bool join = !two && N > 1;   // stream B's part of the same rows
-                if (join) {
-                    if (X == 1) s_ml[row] = make_float2(m2, l);
-                    named_bar_sync(1, 256);
-                    if (X == 0) {
-                        const float2 b = s_ml[row];
-                        const float mm = fmaxf(m2, b.x), mz = mm == -INFINITY ? 0.f : mm;
-                        fa = tr_ex2(m2 - mz);
-                        fb = tr_ex2(b.x - mz);
-                        l = l * fa + b.y * fb;
-                        m2 = mm;
+                const uint4 valid = meta[(kseq + t) % kTrMeta];
+                if constexpr (E8) {
+                    if (i == 1 && X == 1 && !two) sl2 = tr_scale(sl2 * reinterpret_cast<const float *>(sb + C::OffQS)[row]);
+                }
+                const bool masked = nodes || (valid.x & valid.y & valid.z & valid.w) != ~0u;
+                seen[0] &= valid.x, seen[1] &= valid.y, seen[2] &= valid.z, seen[3] &= valid.w;
+                uint32_t r[128];
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch) tmem_ld32(s_addr + ch * 32, *reinterpret_cast<uint32_t(*)[32]>(&r[ch * 32]));
+                tmem_wait_ld();
+                // e4m3: a column's key scale joins the softmax scale where 16 columns share one, else S takes it now
+                const int at = (kseq + t) % kTrMeta;
+                float gs[8];
+                if constexpr (E8) {
+                    const float *ks = reinterpret_cast<const float *>(sb + C::OffKS + at * 512);
+                    if (reinterpret_cast<const int *>(sb + C::OffGr)[at]) {
+#pragma unroll
+                        for (int g = 0; g < 8; ++g) gs[g] = ks[16 * g];
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            const float4 f = reinterpret_cast<const float4 *>(ks)[j];
+                            r[4 * j] = __float_as_uint(__uint_as_float(r[4 * j]) * f.x);
+                            r[4 * j + 1] = __float_as_uint(__uint_as_float(r[4 * j + 1]) * f.y);
+                            r[4 * j + 2] = __float_as_uint(__uint_as_float(r[4 * j + 2]) * f.z);
+                            r[4 * j + 3] = __float_as_uint(__uint_as_float(r[4 * j + 3]) * f.w);
+                        }
+#pragma unroll
+                        for (int g = 0; g < 8; ++g) gs[g] = 1.f;
                     }
                 }
-                // the next piece's Q comes while this one ends (both streams are through with S)
-                tr_wait_ring(bar(C::ITEM_FULL + (piece + 1) % kTrPieces), ((piece + 1) / kTrPieces) & 1);
-                if (!s_piece[(piece + 1) % kTrPieces].end) load_q(s_piece[(piece + 1) % kTrPieces]);
-                const bool ends = two || X == 0;
-                if (ends) {
-                    const bool wild = *(volatile int *)&s_wild[0][piece & 7] == piece + 1 ||
-                                      *(volatile int *)&s_wild[1][piece & 7] == piece + 1;
-                    const float inv = l != 0.f ? 1.f / l : 0.f;
-                    const int mine = (two ? X * kTrTile : 0) + row, hq = k.h * a.G + row - nd * a.G;
-                    const bool whole = k.whole;
-                    const int64_t slot = 2 * k.unit + (k.first ? 0 : 1), out_row = (qrow * a.Hq + hq) * D;
-                    float4 *part = reinterpret_cast<float4 *>(a.o_part + slot * kTrPair * D) + mine;   // [D / 4][256]
-#pragma unroll 1
+                if (masked) {
+#pragma unroll
+                    for (int j = 0; j < 128; ++j)
+                        if (!(seen[j >> 5] >> (j & 31) & 1u)) r[j] = __float_as_uint(-INFINITY);
+                }
+                float mx = -INFINITY;
+#pragma unroll
+                for (int g = 0; g < 8; ++g) {
+                    auto f = [&](int j) { return __uint_as_float(r[16 * g + j]); };
+                    const float a0 = max3(f(0), f(1), f(2)), a1 = max3(f(3), f(4), f(5)), a2 = max3(f(6), f(7), f(8));
+                    const float a3 = max3(f(9), f(10), f(11)), a4 = max3(a0, f(12), f(13)), a5 = max3(a1, f(14), f(15));
+                    const float top = fmaxf(max3(a2, a3, a4), a5);
+                    mx = fmaxf(mx, E8 ? top * gs[g] : top);
+                }
+                bool rescale = false;
+                float m_new = m;
+                if (mx > m && (m == -INFINITY || (mx - m) * sl2 > 8.f)) {
+                    rescale = m != -INFINITY;
+                    m_new = mx;
+                }
+                const float alpha = rescale ? tr_ex2((m - m_new) * sl2) : 1.f;
+                m = m_new;
+                const float mb = m == -INFINITY ? 0.f : m * sl2;
+                const uint64_t nmb2 = f32x2_pack(-mb, -mb);
+                uint64_t sl22 = f32x2_pack(sl2, sl2), sum2 = f32x2_pack(0.f, 0.f);
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int j = 0; j < 64; j += 2) {
+                        if (E8 && j % 16 == 0) {
+                            const float sg = tr_scale(sl2 * gs[hh * 4 + j / 16]);
+                            sl22 = f32x2_pack(sg, sg);
+                        }
+                        const uint64_t x = fma_f32x2(
+                            f32x2_pack(__uint_as_float(r[hh * 64 + j]), __uint_as_float(r[hh * 64 + j + 1])), sl22, nmb2);
+                        const float v0 = tr_ex2(f32x2_lo(x)), v1 = tr_ex2(f32x2_hi(x));
+                        sum2 = add_f32x2(sum2, f32x2_pack(v0, v1));
+                        pk[j / 2] = pack_bf16x2(v0, v1);
+                    }
+                    tmem_st32(s_addr + hh * 32, pk);
+                }
+                l = l * alpha + (f32x2_lo(sum2) + f32x2_hi(sum2));
+                // O is stable here: S(i) completing implies that the stream's product before it did
+                if (i >= 2 && __any_sync(0xffffffffu, rescale)) {
+#pragma unroll
                     for (int ch = 0; ch < D / 32; ++ch) {
-                        uint32_t ob[32];
-                        float o[32];
-                        tmem_ld32(tmem + lane_base + C::ColO + X * D + ch * 32, ob);
-                        if (join) {
-                            uint32_t oc[32];
-                            tmem_ld32(tmem + lane_base + C::ColO + D + ch * 32, oc);
-                            tmem_wait_ld();
+                        uint32_t o[32];
+                        tmem_ld32(tmem + lane_base + C::ColO + X * D + ch * 32, o);
+                        tmem_wait_ld();
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) o[j] = __uint_as_float(ob[j]) * fa + __uint_as_float(oc[j]) * fb;
-                        } else {
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) o[j] = __uint_as_float(ob[j]);
-                        }
-                        if (wild && live) tr_wild_rows<D, E8>(a, k, node, hq, m2 == -INFINITY ? 0.f : m2, ch * 32, o);
-                        if (live && !bad && whole) {
-#pragma unroll
-                            for (int j = 0; j < 32; j += 8) {
-                                uint32_t p[4];
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) p[e] = l != 0.f ? pack_bf16x2(o[j + 2 * e] * inv, o[j + 2 * e + 1] * inv) : 0u;
-                                *reinterpret_cast<uint4 *>(a.out + out_row + ch * 32 + j) = make_uint4(p[0], p[1], p[2], p[3]);
-                            }
-                        } else if (live && !bad) {
-#pragma unroll
-                            for (int j = 0; j < 32; j += 4)
-                                part[(ch * 8 + j / 4) * kTrPair] = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
-                        }
-                        __syncwarp();
+                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+                        tmem_st32(tmem + lane_base + C::ColO + X * D + ch * 32, o);
                     }
-                    if (!whole && live && !bad) reinterpret_cast<float2 *>(a.ml_part)[slot * kTrPair + mine] = make_float2(m2, l);
-                    tc_fence_before();
-                    mbar_arrive(bar(C::O_FREE + X));
-                    if (join) mbar_arrive(bar(C::O_FREE + 1));
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(C::ITEM_EMPTY + piece % kTrPieces));
-                ++piece;
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(bar(C::P_READY + X));
             }
+            kseq += nt;
+            // ---- the piece ends
+            if (X < N) wait(bar(C::O_FULL + X), ox & 1), ++ox;
+            tc_fence_after();
+            float m2 = m == -INFINITY ? -INFINITY : m * sl2, fa = 1.f, fb = 0.f;
+            const bool join = !two && N > 1;   // stream B's part of the same rows
+            if (join) {
+                if (X == 1) s_ml[row] = make_float2(m2, l);
+                named_bar_sync(1, 256);
+                if (X == 0) {
+                    const float2 b = s_ml[row];
+                    const float mm = fmaxf(m2, b.x), mz = mm == -INFINITY ? 0.f : mm;
+                    fa = tr_ex2(m2 - mz);
+                    fb = tr_ex2(b.x - mz);
+                    l = l * fa + b.y * fb;
+                    m2 = mm;
+                }
+            }
+            // the next piece's Q comes while this one ends (both streams are through with S)
+            tr_wait_ring(bar(C::ITEM_FULL + (piece + 1) % kTrPieces), ((piece + 1) / kTrPieces) & 1);
+            if (!s_piece[(piece + 1) % kTrPieces].end) load_q(s_piece[(piece + 1) % kTrPieces]);
+            const bool ends = two || X == 0;
+            if (ends) {
+                const bool wild = *(volatile int *)&s_wild[0][piece & 7] == piece + 1 ||
+                                  *(volatile int *)&s_wild[1][piece & 7] == piece + 1;
+                const float inv = l != 0.f ? 1.f / l : 0.f;
+                const int mine = (two ? X * kTrTile : 0) + row, hq = k.h * a.G + row - nd * a.G;
+                const bool whole = k.whole;
+                const int64_t slot = 2 * k.unit + (k.first ? 0 : 1), out_row = (qrow * a.Hq + hq) * D;
+                float4 *part = reinterpret_cast<float4 *>(a.o_part + slot * kTrPair * D) + mine;   // [D / 4][256]
+#pragma unroll 1
+                for (int ch = 0; ch < D / 32; ++ch) {
+                    uint32_t ob[32];
+                    float o[32];
+                    tmem_ld32(tmem + lane_base + C::ColO + X * D + ch * 32, ob);
+                    if (join) {
+                        uint32_t oc[32];
+                        tmem_ld32(tmem + lane_base + C::ColO + D + ch * 32, oc);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = __uint_as_float(ob[j]) * fa + __uint_as_float(oc[j]) * fb;
+                    } else {
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = __uint_as_float(ob[j]);
+                    }
+                    if (wild && live) tr_wild_rows<D, E8>(a, k, node, hq, m2 == -INFINITY ? 0.f : m2, ch * 32, o);
+                    if (live && !bad && whole) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 8) {
+                            uint32_t p[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) p[e] = l != 0.f ? pack_bf16x2(o[j + 2 * e] * inv, o[j + 2 * e + 1] * inv) : 0u;
+                            *reinterpret_cast<uint4 *>(a.out + out_row + ch * 32 + j) = make_uint4(p[0], p[1], p[2], p[3]);
+                        }
+                    } else if (live && !bad) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4)
+                            part[(ch * 8 + j / 4) * kTrPair] = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                    }
+                    __syncwarp();
+                }
+                if (!whole && live && !bad) reinterpret_cast<float2 *>(a.ml_part)[slot * kTrPair + mine] = make_float2(m2, l);
+                tc_fence_before();
+                mbar_arrive(bar(C::O_FREE + X));
+                if (join) mbar_arrive(bar(C::O_FREE + 1));
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::ITEM_EMPTY + piece % kTrPieces));
+            ++piece;
+        }
         // the copies of Q have landed before the shared memory goes
         if (qloads > 0) mbar_drain(bar(C::Q_FULL + X), (qloads - 1) & 1);
     }
