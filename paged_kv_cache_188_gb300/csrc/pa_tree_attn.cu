@@ -1194,6 +1194,7 @@ __global__ void __launch_bounds__(kTrMergeThreads, 2) tree_merge_kernel(const __
         const bool in = e < per_row;
         const int hc = (in ? e : 0) / a.G, g = (in ? e : 0) - hc * a.G, h = hc / GROUPS, cg = hc - h * GROUPS;
         const int i0 = S / W, i1 = (S + kt - 1) / W, row = (tile & 1) * kTrTile + (node - tile * a.tq) * a.G + g;   // of the pair's 256
+        if (i0 < 0 || i1 < i0 || i1 >= a.ranges) continue;       // (sums that overflowed, of requests that overlap)
         auto slot = [&](int i) { return (int64_t)(2 * (i * a.Hkv + h) + (i == i0 && S > i0 * W ? 1 : 0)); };
         float M = -INFINITY, L = 0.f, o[kTrMergeCols];
 #pragma unroll
