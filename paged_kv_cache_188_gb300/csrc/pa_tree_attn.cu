@@ -838,7 +838,6 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
                     }
                     if (two) named_bar_sync(2, 64);
                 }
-                if (t + dt < nt) wait(bar(C::K_FULL + sk), ((s + dt) / C::NK) & 1);
                 // the piece's first product overwrites O
                 if (t < dt && pq++ > 0) wait(bar(C::O_FREE + X), pq & 1);
                 wait(bar(C::P_READY + X), px & 1);
@@ -851,10 +850,17 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
                                 smem_desc_sw128(vt + kk * 2048, kTrHalf, 1024), C::kIdPV, kk > 0 || t >= dt);
                     if constexpr (E8) umma_commit(bar(C::WIDE_FREE + X));
                     else release(bar(C::V_EMPTY + st));
-                    if (t + dt < nt) qk(sk);
-                    else umma_commit(bar(C::O_FULL + X));
+                    if (t + dt >= nt) umma_commit(bar(C::O_FULL + X));
                 }
                 __syncwarp();
+                if (t + dt < nt) {
+                    // (looked for in its turn only: the tile that was in the stage before may be the other stream's, whose
+                    // arrival this warp has not followed, and a wait for a phase passes two phases early as well)
+                    wait(bar(C::K_FULL + sk), ((s + dt) / C::NK) & 1);
+                    tc_fence_after();
+                    if (!bad) if (elect_one()) qk(sk);
+                    __syncwarp();
+                }
                 // the next step, or the next piece's first
                 turn = X == 0 && t + 1 >= nt && !two;
                 if (!turn && lane == 0) mbar_arrive(bar(C::TURN + 1 - X));
@@ -1050,9 +1056,11 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
             tc_fence_after();
             float m2 = m == -INFINITY ? -INFINITY : m * sl2, fa = 1.f, fb = 0.f;
             const bool join = !two && N > 1;   // stream B's part of the same rows
+            // one tile of rows: the warpgroups end it together, with or without steps for stream B, whose roles else got ahead
+            // of tiles that they do not follow: a wait for a stage's next tile would pass before this one's has come
+            if (join && X == 1) s_ml[row] = make_float2(m2, l);
+            if (!two) named_bar_sync(1, 256);
             if (join) {
-                if (X == 1) s_ml[row] = make_float2(m2, l);
-                named_bar_sync(1, 256);
                 if (X == 0) {
                     const float2 b = s_ml[row];
                     const float mm = fmaxf(m2, b.x), mz = mm == -INFINITY ? 0.f : mm;

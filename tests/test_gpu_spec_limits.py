@@ -10,7 +10,7 @@ import _block_ref as R
 import _spec_ref as S
 from paged_kv_cache_188_gb300 import api
 from test_gpu_abort_midway import _drive
-from test_gpu_tree import P_BITS, make, queries, tree, trees
+from test_gpu_tree import P_BITS, check, make, queries, tree, trees
 from test_gpu_verify_accept import Drafts, i32
 
 pytestmark = pytest.mark.gpu
@@ -178,3 +178,19 @@ def test_masks_wider_than_the_nodes_need():
     b, ws = tree(c, q, 0.05, wide)
     assert api.pa_get_error(ws) == 0 and torch.equal(a.view(torch.int16), b.view(torch.int16))
     assert np.isfinite(a.float().cpu().numpy()).all()
+
+
+@pytest.mark.parametrize("D,block", [(128, 16), (64, 16), (128, 0), (64, 0)])
+@pytest.mark.parametrize("order", [0, 1, 2])
+def test_short_and_long_requests_in_turn(D, block, order):
+    """Several requests to a CTA: of one tile of cached tokens (one stream has nothing to do), of many, of more rows than
+    a stream has, behind one another in every order."""
+    kinds = [(40, 3), (400, 9), (90, 5), (300, 40), (20, 1), (60, 2), (700, 33), (100, 6), (1000, 4), (5, 40)]
+    g = torch.Generator().manual_seed(order)
+    picks = [kinds[int(i)] for i in torch.randint(0, len(kinds), (70,), generator=g)]
+    c = make([x[0] for x in picks], [x[1] for x in picks], 8, D, 16, block, 50 + order, layers=1, layer=0)
+    seen, mask = trees(c)
+    q = queries(c, 4, D)
+    out, ws = tree(c, q.cuda(), 0.05, mask)
+    assert api.pa_get_error(ws) == 0
+    check(c, q, out, 0.05, seen, f"D={D} block={block} order {order}")
