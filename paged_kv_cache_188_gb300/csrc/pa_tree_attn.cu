@@ -80,6 +80,7 @@ constexpr int kTrHalf = 128 * 128;       // 128 rows of 64 bf16, 128-byte swizzl
 constexpr int kTrMeta = 8;               // tiles whose valid positions are kept: see tr_copy
 constexpr int kTrPieces = 4;             // pieces handed from the walk to the other roles
 constexpr int kTrReaders = 1 + 2 + 8;    // V copies, products, softmax warps
+constexpr int kTrPieceCost = 4;          // what a piece's start and end take, in tiles
 constexpr int kTrMaxCtas = 160;
 constexpr int kTrMaxUnits = 2 * kTrMaxCtas;   // units that share segments
 constexpr uint32_t kTrTmemCols = 512;    // S_A | S_B | O_A | O_B
@@ -139,11 +140,25 @@ __device__ __forceinline__ TrReq tr_request(const TreeArgs &a, int r)
 }
 __device__ __forceinline__ int tr_pairs(const TreeArgs &a, int n) { return n <= 2 * a.tq ? 1 : (n + 2 * a.tq - 1) / (2 * a.tq); }
 __device__ __forceinline__ int tr_ktiles(int L) { return (L + kTrTile - 1) / kTrTile; }
-__device__ __forceinline__ int tr_tiles(const TreeArgs &a, const TrReq &q) { return q.n > 0 ? tr_pairs(a, q.n) * tr_ktiles(q.L) : 0; }
+// The segments laid end to end: a segment is `cost` places that nobody works on and then its tiles, so that a range with
+// several segments has fewer tiles (32 ragged requests 93.0 -> 89.6 us, 48 over e4m3 164.5 -> 145.5).  A range of few
+// tiles is not made longer for it.
+__device__ __forceinline__ int tr_places(const TreeArgs &a, const TrReq &q, int cost)
+{
+    return q.n > 0 ? tr_pairs(a, q.n) * (tr_ktiles(q.L) + cost) : 0;
+}
+// segments and tiles, to be summed together
+__device__ __forceinline__ uint64_t tr_load(const TreeArgs &a, const TrReq &q)
+{
+    const uint32_t pairs = q.n > 0 ? tr_pairs(a, q.n) : 0;
+    return (uint64_t)pairs << 32 | (pairs ? pairs * (uint32_t)tr_ktiles(q.L) : 0u);
+}
+__device__ __forceinline__ int tr_cost(const TreeArgs &a, uint64_t total) { return min(kTrPieceCost, (int)((uint32_t)total / (8u * a.ranges))); }
+__device__ __forceinline__ int tr_places(uint64_t load, int cost) { return (int)((uint32_t)load + (uint32_t)(load >> 32) * cost); }
 
 struct TrPlan {
-    int total, W;
-    int start[2][2];        // (request, its first tile) where the CTA's units start (a third unit exists only where all
+    int total, W, cost;     // places in all, of a range, of a segment before its tiles
+    int start[2][2];        // (request, its first place) where the CTA's units start (a third unit exists only where all
                             // of them are the whole of one kv head)
     TrReq req[2];           // that request
 };
@@ -153,11 +168,11 @@ struct alignas(16) TrPiece {
     int t0, t1, h, unit;
     int pair, whole, first, end;    // whole: all of its segment; first: it starts the range; end: no more pieces
 };
-// Walk over the pieces of the CTA's units (blockIdx, + grid, ...): range i = unit / Hkv is the tiles [i W, (i + 1) W) of
+// Walk over the pieces of the CTA's units (blockIdx, + grid, ...): range i = unit / Hkv is the places [i W, (i + 1) W) of
 // the segments laid end to end.  One warp walks and hands the pieces on.
 struct TrWalk {
     int unit, u, h;         // unit, its number in the CTA, kv head
-    int x, xe, x0, r, S0;   // next tile, end, start of the range; request and its first tile
+    int x, xe, x0, r, S0;   // next place, end, start of the range; request and its first place
     int w0;                 // the lanes hold requests w0 + lane
     TrReq w;
 };
@@ -181,48 +196,53 @@ __device__ __forceinline__ void tr_begin(const TreeArgs &a, const TrPlan &p, TrW
 __device__ __forceinline__ bool tr_next(const TreeArgs &a, const TrPlan &p, TrWalk &k, TrPiece &o, int lane)
 {
 #pragma unroll 1
-    while (k.x >= k.xe) {
-        k.unit += gridDim.x;
-        ++k.u;
-        if (k.unit >= a.ranges * a.Hkv) return false;
-        tr_unit(a, p, k);
-    }
-    TrReq q;
-    int tiles;
-#pragma unroll 1
     while (true) {
-        const int v = a.ranges > 1 ? k.u : 0;
-        if (k.x == k.x0 && k.r == p.start[v][0] && p.total > 0 && a.ranges > 1) {
-            q = p.req[v];
-        } else {
-            if (k.r - k.w0 >= 32) {
-                k.w0 = k.r;
-                k.w = TrReq{0, 0, 0, 0};
-                if (k.r + lane < a.R) k.w = tr_request(a, k.r + lane);
-            }
-            const int i = k.r - k.w0;
-            q.q0 = __shfl_sync(0xffffffffu, k.w.q0, i);
-            q.n = __shfl_sync(0xffffffffu, k.w.n, i);
-            q.L = __shfl_sync(0xffffffffu, k.w.L, i);
-            q.row = __shfl_sync(0xffffffffu, k.w.row, i);
+#pragma unroll 1
+        while (k.x >= k.xe) {
+            k.unit += gridDim.x;
+            ++k.u;
+            if (k.unit >= a.ranges * a.Hkv) return false;
+            tr_unit(a, p, k);
         }
-        tiles = tr_tiles(a, q);
-        if (k.x < k.S0 + tiles) break;
-        k.S0 += tiles;
-        if (++k.r >= a.R) return false;      // (not reached: x lies below the total)
+        TrReq q;
+        int places;
+#pragma unroll 1
+        while (true) {
+            const int v = a.ranges > 1 ? k.u : 0;
+            if (k.x == k.x0 && k.r == p.start[v][0] && p.total > 0 && a.ranges > 1) {
+                q = p.req[v];
+            } else {
+                if (k.r - k.w0 >= 32) {
+                    k.w0 = k.r;
+                    k.w = TrReq{0, 0, 0, 0};
+                    if (k.r + lane < a.R) k.w = tr_request(a, k.r + lane);
+                }
+                const int i = k.r - k.w0;
+                q.q0 = __shfl_sync(0xffffffffu, k.w.q0, i);
+                q.n = __shfl_sync(0xffffffffu, k.w.n, i);
+                q.L = __shfl_sync(0xffffffffu, k.w.L, i);
+                q.row = __shfl_sync(0xffffffffu, k.w.row, i);
+            }
+            places = tr_places(a, q, p.cost);
+            if (k.x < k.S0 + places) break;
+            k.S0 += places;
+            if (++k.r >= a.R) return false;      // (not reached: x lies below the total)
+        }
+        const int kt = tr_ktiles(q.L), off = k.x - k.S0, seg = kt + p.cost;
+        o.q0 = q.q0, o.n = q.n, o.L = q.L, o.row = q.row;
+        o.pair = places == seg ? 0 : off / seg;
+        const int at = off - o.pair * seg - p.cost;      // the tile at place x, below 0 in front of them
+        const int len = min(k.xe - k.x, kt - at);
+        o.t0 = max(at, 0);
+        o.t1 = at + len;
+        o.h = k.h;
+        o.unit = k.unit;
+        o.whole = o.t0 == 0 && o.t1 == kt;
+        o.first = k.x == k.x0 && at >= 0;
+        o.end = 0;
+        k.x += len;
+        if (o.t1 > o.t0) return true;
     }
-    const int kt = tr_ktiles(q.L), off = k.x - k.S0;
-    o.q0 = q.q0, o.n = q.n, o.L = q.L, o.row = q.row;
-    o.pair = tiles == kt ? 0 : off / kt;
-    o.t0 = off - o.pair * kt;
-    o.t1 = min(kt, o.t0 + k.xe - k.x);
-    o.h = k.h;
-    o.unit = k.unit;
-    o.whole = o.t0 == 0 && o.t1 == kt;
-    o.first = k.x == k.x0;
-    o.end = 0;
-    k.x += o.t1 - o.t0;
-    return true;
 }
 // the piece has rows for both streams
 __device__ __forceinline__ bool tr_two(const TreeArgs &a, const TrPiece &k) { return k.n - 2 * a.tq * k.pair > a.tq; }
@@ -509,7 +529,7 @@ __device__ __forceinline__ void tr_copy(const TreeArgs &a, const TrPlan &plan, T
             }
         }
         if (!E8 && held != 0) release_held(0);
-        }
+    }
     // the warp leaves only when its copies have landed, whether or not anyone has given up by now
 #pragma unroll 1
     for (int j = max(0, seq - stages); j < seq; ++j) mbar_drain(full + (j % stages) * 8, (j / stages) & 1);
@@ -634,7 +654,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
 {
     using C = TrCfg<D, E8>;
     extern __shared__ unsigned char smem_raw[];
-    __shared__ int s_w[kTrThreads / 32];
+    __shared__ uint64_t s_w[kTrThreads / 32];
     __shared__ int s_abort_storage;
     __shared__ TrPlan plan;
     __shared__ TrPiece s_piece[kTrPieces];
@@ -679,7 +699,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
     bool zeros = false;
     {
         const int per = (a.R + kTrThreads - 1) / kTrThreads, lo = min(a.R, tid * per), hi = min(a.R, lo + per);
-        int run = 0;
+        uint64_t run = 0;
         TrReq q;                               // the thread's last request
 #pragma unroll 1
         for (int r = lo; r < hi; ++r) {
@@ -687,40 +707,42 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
             bool z;
             q = tr_request(a, r, b, z);
             if (z) q.n = 0;
-            run += tr_tiles(a, q);
+            run += tr_load(a, q);
             bits |= b;
             zeros |= z;
         }
-        int incl = run;
+        uint64_t incl = run;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            const uint64_t v = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += v;
         }
         if (lane == 31) s_w[warp] = incl;
         zeros = __syncthreads_or(zeros);
-        int before = incl - run, total = 0, sums[kTrThreads / 32];
+        uint64_t before = incl - run, all = 0, sums[kTrThreads / 32];
 #pragma unroll
         for (int w = 0; w < kTrThreads / 32; ++w) sums[w] = s_w[w];
 #pragma unroll
         for (int w = 0; w < kTrThreads / 32; ++w) {
             if (w < warp) before += sums[w];
-            total += sums[w];
+            all += sums[w];
         }
+        const int cost = tr_cost(a, all), total = tr_places(all, cost), mine = tr_places(before, cost), len = tr_places(run, cost);
         const int W = (total + a.ranges - 1) / a.ranges;
         if (tid == 0) {
             plan.total = total;
             plan.W = W;
+            plan.cost = cost;
         }
-        if (a.ranges > 1 && run > 0) {
+        if (a.ranges > 1 && len > 0) {
 #pragma unroll 1
             for (int u = 0; u < 2; ++u) {
                 const int x = (int)((blockIdx.x + u * gridDim.x) / a.Hkv) * W;
-                if (x < before || x >= before + run) continue;
-                int S0 = before, r = lo;
+                if (x < mine || x >= mine + len) continue;
+                int S0 = mine, r = lo;
 #pragma unroll 1
                 for (; r < hi - 1; ++r) {
-                    const int t = tr_tiles(a, tr_request(a, r));
+                    const int t = tr_places(a, tr_request(a, r), cost);
                     if (x < S0 + t) break;
                     S0 += t;
                 }
@@ -1146,39 +1168,51 @@ __global__ void __launch_bounds__(kTrMergeThreads, 2) tree_merge_kernel(const __
 {
     constexpr int NC = kTrMergeCols / 4, GROUPS = D / kTrMergeCols, U = PG > 1 ? 6 : 4;
     constexpr int EPC = kTrMergeThreads / PG, EPW = 32 / PG;     // elements of a CTA, of a warp
-    extern __shared__ int s_pref[];                    // [R + 1] first tiles, [R] first rows of q, tiles of a segment
-    __shared__ int s_w[kTrMergeThreads / 32];
+    extern __shared__ int s_pref[];                    // [R + 1] first places, [R] first rows of q, tiles of a segment
+    __shared__ uint64_t s_w[kTrMergeThreads / 32];
+    __shared__ int s_cost;
     int *s_q0 = s_pref + a.R + 1, *s_kt = s_q0 + a.R;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     {
         const int per = (a.R + kTrMergeThreads - 1) / kTrMergeThreads, lo = min(a.R, tid * per), hi = min(a.R, lo + per);
-        int run = 0;
+        uint64_t run = 0;
 #pragma unroll 1
         for (int r = lo; r < hi; ++r) {
             const TrReq q = tr_request(a, r);
-            s_pref[r] = run;
+            s_pref[r] = q.n > 0 ? tr_pairs(a, q.n) : 0;
             s_q0[r] = q.q0;
             s_kt[r] = q.n > 0 ? tr_ktiles(q.L) : 0;
-            run += tr_tiles(a, q);
+            run += tr_load(a, q);
         }
-        int incl = run;
+        uint64_t incl = run;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            const uint64_t v = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += v;
         }
         if (lane == 31) s_w[warp] = incl;
         __syncthreads();
-        int before = incl - run;
+        uint64_t before = incl - run, all = 0;
 #pragma unroll
-        for (int w = 0; w < kTrMergeThreads / 32; ++w)
+        for (int w = 0; w < kTrMergeThreads / 32; ++w) {
             if (w < warp) before += s_w[w];
+            all += s_w[w];
+        }
+        const int c = tr_cost(a, all);
+        int at = tr_places(before, c);
 #pragma unroll 1
-        for (int r = lo; r < hi; ++r) s_pref[r] += before;
-        if (tid == kTrMergeThreads - 1) s_pref[a.R] = before + run;
+        for (int r = lo; r < hi; ++r) {
+            const int places = s_pref[r] * (s_kt[r] + c);
+            s_pref[r] = at;
+            at += places;
+        }
+        if (tid == kTrMergeThreads - 1) {
+            s_pref[a.R] = tr_places(all, c);
+            s_cost = c;
+        }
     }
     __syncthreads();
-    const int total = s_pref[a.R], W = (total + a.ranges - 1) / a.ranges;
+    const int total = s_pref[a.R], W = (total + a.ranges - 1) / a.ranges, cost = s_cost;
     const int per_row = a.Hq * GROUPS, parts = (per_row + EPC - 1) / EPC, sub = lane / EPW;
     bool waited = false;
 #pragma unroll 1
@@ -1190,10 +1224,10 @@ __global__ void __launch_bounds__(kTrMergeThreads, 2) tree_merge_kernel(const __
             const int mid = (lo + hi) >> 1;
             if (s_q0[mid] <= t) lo = mid; else hi = mid;
         }
-        const int S0 = s_pref[lo], tiles = s_pref[lo + 1] - S0, node = t - s_q0[lo], tile = node / a.tq;
-        const int pair = tile >> 1, kt = s_kt[lo], S = S0 + pair * kt;
+        const int S0 = s_pref[lo], places = s_pref[lo + 1] - S0, node = t - s_q0[lo], tile = node / a.tq;
+        const int pair = tile >> 1, kt = s_kt[lo], S = S0 + pair * (kt + cost) + cost;      // place of its first tile
         // (past the request's nodes; or its segment lies in one range and was never shared)
-        if (tiles == 0 || node < 0 || (pair + 1) * kt > tiles || S / W == (S + kt - 1) / W) continue;
+        if (places == 0 || node < 0 || (pair + 1) * (kt + cost) > places || S / W == (S + kt - 1) / W) continue;
         if (node >= __ldg(a.qo_indptr + lo + 1) - s_q0[lo]) continue;
         if (!waited) {
             pdl_wait();
@@ -1357,8 +1391,8 @@ extern "C" pa_status pa_paged_tree_attn(const void *q, int n_tokens, int n_q_hea
     const int G = n_q_heads / s.n_kv_heads;
     if (G > 16 || (s.head_dim != 64 && s.head_dim != 128)) return PA_ERR_UNSUPPORTED;
     if ((int64_t)s.n_layers * s.size >= (int64_t)INT32_MAX - 16) return PA_ERR_SHAPE;
-    // tiles of all segments (2 x 128 / G nodes over 128 cached tokens) in 32 bits
-    if (((int64_t)n_tokens / (2 * (kTrTile / G)) + n_reqs) * (((int64_t)max_ctx + 127) / 128) >= (int64_t)1 << 30) return PA_ERR_SHAPE;
+    // places of all segments (2 x 128 / G nodes over 128 cached tokens) in 32 bits
+    if (((int64_t)n_tokens / (2 * (kTrTile / G)) + n_reqs) * (((int64_t)max_ctx + 127) / 128 + kTrPieceCost) >= (int64_t)1 << 30) return PA_ERR_SHAPE;
     if (!workspace) return PA_ERR_NULL;
     if (!aligned256(workspace)) return PA_ERR_ALIGN;
     if (workspace_bytes < pa_tree_workspace_bytes(n_q_heads, s.n_kv_heads, s.head_dim)) return PA_ERR_WORKSPACE;
