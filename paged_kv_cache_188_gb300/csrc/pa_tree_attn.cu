@@ -80,7 +80,7 @@ constexpr int kTrHalf = 128 * 128;       // 128 rows of 64 bf16, 128-byte swizzl
 constexpr int kTrMeta = 8;               // tiles whose valid positions are kept: see tr_copy
 constexpr int kTrPieces = 4;             // pieces handed from the walk to the other roles
 constexpr int kTrReaders = 1 + 2 + 8;    // V copies, products, softmax warps
-constexpr int kTrPieceCost = 4;          // what a piece's start and end take, in tiles
+constexpr int kTrMaxPieceCost = 6;
 constexpr int kTrMaxCtas = 160;
 constexpr int kTrMaxUnits = 2 * kTrMaxCtas;   // units that share segments
 constexpr uint32_t kTrTmemCols = 512;    // S_A | S_B | O_A | O_B
@@ -98,6 +98,7 @@ struct TreeArgs {
     float *o_part;                               // [2 units][D / 4][256][4]: relative to that maximum
     int T, R, Hq, Hkv, G, size, req_rows, max_ctx, mask_words, block_shift, layer_row0, total_rows, early_meta;
     int ranges;                                  // per kv head
+    int piece_cost;                              // what a piece's start and end take, in tiles
     uint64_t wait_ns;
     float scale_log2;                            // of the scale's magnitude, not 0
     int negate;                                  // the scale is negative: the products take Q with its sign changed
@@ -153,7 +154,7 @@ __device__ __forceinline__ uint64_t tr_load(const TreeArgs &a, const TrReq &q)
     const uint32_t pairs = q.n > 0 ? tr_pairs(a, q.n) : 0;
     return (uint64_t)pairs << 32 | (pairs ? pairs * (uint32_t)tr_ktiles(q.L) : 0u);
 }
-__device__ __forceinline__ int tr_cost(const TreeArgs &a, uint64_t total) { return min(kTrPieceCost, (int)((uint32_t)total / (8u * a.ranges))); }
+__device__ __forceinline__ int tr_cost(const TreeArgs &a, uint64_t total) { return min(a.piece_cost, (int)((uint32_t)total / (4u * a.ranges))); }
 __device__ __forceinline__ int tr_places(uint64_t load, int cost) { return (int)((uint32_t)load + (uint32_t)(load >> 32) * cost); }
 
 struct TrPlan {
@@ -1392,7 +1393,7 @@ extern "C" pa_status pa_paged_tree_attn(const void *q, int n_tokens, int n_q_hea
     if (G > 16 || (s.head_dim != 64 && s.head_dim != 128)) return PA_ERR_UNSUPPORTED;
     if ((int64_t)s.n_layers * s.size >= (int64_t)INT32_MAX - 16) return PA_ERR_SHAPE;
     // places of all segments (2 x 128 / G nodes over 128 cached tokens) in 32 bits
-    if (((int64_t)n_tokens / (2 * (kTrTile / G)) + n_reqs) * (((int64_t)max_ctx + 127) / 128 + kTrPieceCost) >= (int64_t)1 << 30) return PA_ERR_SHAPE;
+    if (((int64_t)n_tokens / (2 * (kTrTile / G)) + n_reqs) * (((int64_t)max_ctx + 127) / 128 + kTrMaxPieceCost) >= (int64_t)1 << 30) return PA_ERR_SHAPE;
     if (!workspace) return PA_ERR_NULL;
     if (!aligned256(workspace)) return PA_ERR_ALIGN;
     if (workspace_bytes < pa_tree_workspace_bytes(n_q_heads, s.n_kv_heads, s.head_dim)) return PA_ERR_WORKSPACE;
@@ -1452,6 +1453,8 @@ extern "C" pa_status pa_paged_tree_attn(const void *q, int n_tokens, int n_q_hea
     a.Hkv = s.n_kv_heads;
     a.G = G;
     a.inv_g = 65536 / G + 1;
+    // (6 in place of 4: 48 ragged requests over e4m3 146 -> 141 us, 32 over bf16 in pages of one slot 97.8 -> 100)
+    a.piece_cost = e4m3 ? kTrMaxPieceCost : 4;
     a.tq = kTrTile / G;
     a.size = s.size;
     a.req_rows = req_rows;
