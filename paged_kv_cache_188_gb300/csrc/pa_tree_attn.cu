@@ -42,8 +42,8 @@
 // share a scale (q within 2^-17 of its row's largest element); a key's scale joins
 // the softmax scale where 16 keys share one.  V becomes bf16 with its scale, exactly,
 // by the softmax warpgroups while S is on its way (48 requests of 500 to 8192
-// tokens: behind the exponentials 193 us, like this 160; to fp16 with a running
-// exponent 209; by warps whose rows are no nodes' 178 to 192).
+// tokens, before ranges counted pieces: behind the exponentials 193 us, like this
+// 160; to fp16 with a running exponent 209; by warps without nodes' rows 178 to 192).
 //
 // Hidden rows: a hidden token's weight is 0, but 0 times a NaN or an infinity in
 // its V row would reach every node.  Only drafted tokens are ever hidden (context
@@ -52,16 +52,19 @@
 // part by hand when the piece ends.
 //
 // Measured, both kernels in a graph, D = 128, 8 kv heads of 4 query heads: 403 MB of
-// cache (32 requests of 500 to 8192 tokens, trees of up to 32 nodes) 93.6 us, 64 % of
-// a copy's rate (6.78 TB/s); ncu over the first kernel: 91.0 us, 403.4 MB read,
-// tensor pipe active 28 %, issue slots 20 %.  One request of 32K tokens 49.6 us for
-// 136 MB; of 1K 11.6 us, which is start, plan, two steps and the merge.  e4m3: 48
-// requests, 320 MB, 159.6 us: the widening and the softmax share the warps.
-// What bounds it is the chain of a step (S, its read-back of 128 columns,
-// exponentials, P, PV: 2050 cycles), of which two are in flight.  S in two halves of
-// 64 columns (2900 cycles a step), a tile kept from one piece to the next (99.6 us
-// for 93.6) and rows without nodes skipped (spills: 26 -> 29 us at 96 small
-// requests) lost.
+// cache (32 requests of 500 to 8192 tokens, trees of up to 32 nodes) 89.6 us, 66 % of
+// a copy's rate (6.78 TB/s); ncu over the first kernel: 403.4 MB read, tensor pipe
+// active 28 %, issue slots 20 %.  One request of 32K tokens 51 us for 136 MB; of 1K
+// 11.8 us, which is start, plan, two steps and the merge.  e4m3: 48 requests, 320 MB,
+// 141 us: the widening and the softmax share the warps.
+// What bounds it.  Within a long piece over bf16 pages, HBM: a tile of 64 KB every
+// 2700 cycles and SM.  Around it the start (10000 cycles to the first S), and each
+// piece's end (5000 to 8000 for the partials, the next piece's Q and first tiles).
+// With 256 rows, and over e4m3, a step's chain (S, its read-back of 128 columns,
+// exponentials, P, PV), of which two are in flight.  S in two halves of 64 columns
+// (2900 cycles a step for 2050), a tile kept from one piece to the next (99.6 us for
+// 93.6), one ring for K and V in the order of their use (96.0 for 93.0), and rows
+// without nodes skipped (spills: 26 -> 29 us at 96 small requests) lost.
 #include <math.h>
 #include <string.h>
 
@@ -142,8 +145,9 @@ __device__ __forceinline__ TrReq tr_request(const TreeArgs &a, int r)
 __device__ __forceinline__ int tr_pairs(const TreeArgs &a, int n) { return n <= 2 * a.tq ? 1 : (n + 2 * a.tq - 1) / (2 * a.tq); }
 __device__ __forceinline__ int tr_ktiles(int L) { return (L + kTrTile - 1) / kTrTile; }
 // The segments laid end to end: a segment is `cost` places that nobody works on and then its tiles, so that a range with
-// several segments has fewer tiles (32 ragged requests 93.0 -> 89.6 us, 48 over e4m3 164.5 -> 145.5).  A range of few
-// tiles is not made longer for it.
+// several segments has fewer tiles (32 ragged requests 93.0 -> 89.6 us, 48 over e4m3 164.5 -> 141).  At most half of a
+// range's tiles: 96 requests of up to 4000 tokens, two kv heads, 28.7 us at an eighth, 22.3 at a quarter, 20.3 at half,
+// 21.3 at all of them; few long requests take the same time at each.
 __device__ __forceinline__ int tr_places(const TreeArgs &a, const TrReq &q, int cost)
 {
     return q.n > 0 ? tr_pairs(a, q.n) * (tr_ktiles(q.L) + cost) : 0;
@@ -154,7 +158,7 @@ __device__ __forceinline__ uint64_t tr_load(const TreeArgs &a, const TrReq &q)
     const uint32_t pairs = q.n > 0 ? tr_pairs(a, q.n) : 0;
     return (uint64_t)pairs << 32 | (pairs ? pairs * (uint32_t)tr_ktiles(q.L) : 0u);
 }
-__device__ __forceinline__ int tr_cost(const TreeArgs &a, uint64_t total) { return min(a.piece_cost, (int)((uint32_t)total / (4u * a.ranges))); }
+__device__ __forceinline__ int tr_cost(const TreeArgs &a, uint64_t total) { return min(a.piece_cost, (int)((uint32_t)total / (2u * a.ranges))); }
 __device__ __forceinline__ int tr_places(uint64_t load, int cost) { return (int)((uint32_t)load + (uint32_t)(load >> 32) * cost); }
 
 struct TrPlan {
