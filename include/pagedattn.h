@@ -463,18 +463,18 @@ pa_status pa_kv_evict(int32_t *req_to_token, int req_rows, int max_ctx, const in
  * pa_paged_tree_attn: request r has the packed query rows qo_indptr[r] ..
  * qo_indptr[r+1]-1, its n_r nodes, and L_r = seq_lens[r] cached tokens through
  * req_to_token[req_pool_indices[r]], of which the last n_r are the nodes in their
- * order and the c_r = L_r - n_r in front its context.  Node i sees the whole context, and node k
- * (position c_r + k) where bit k % 32 of tree_mask[qo_indptr[r] + i, k / 32] is
+ * order and the c_r = L_r - n_r in front its context.  Node i sees the whole
+ * context, and node k (position c_r + k) where bit k % 32 of tree_mask[qo_indptr[r] + i, k / 32] is
  * set (int32 [n_tokens, mask_words]; a node sees itself only if its own bit is
  * set); tree_mask == NULL (mask_words 0): where k <= i, a chain.  Over what it sees
  *     s_j = scale * <q[t, hq], K_j>,   out[t, hq] = sum_j softmax(s)_j V_j
  * and zeros where it sees nothing (or every s_j is minus infinity).  A K or V row
  * that a node does not see does not reach it, whatever it holds.  q, out: bf16
- * [n_tokens, n_q_heads, head_dim]; rows from qo_indptr[n_reqs] on are not written.
+ * [n_tokens, n_q_heads, head_dim], not overlapping; rows from qo_indptr[n_reqs] on are not written.
  * block == 0: the bf16 cache, k_exp and v_exp NULL; block >= 1: the e4m3 cache
  * with scales per block of slots, its arithmetic that of
- * pa_paged_prefill_attn_fp8_block (q within 2^-17 of its row's largest element).  The weights are
- * rounded to bf16.  Supported: head_dim 64 or 128, 1 <= G <= 16,
+ * pa_paged_prefill_attn_fp8_block (q within 2^-17 of its row's largest element).
+ * The weights are rounded to bf16.  Supported: head_dim 64 or 128, 1 <= G <= 16,
  * n_reqs <= 4096.  Workspace: pa_tree_workspace_bytes, whatever the batch,
  * initialised once with pa_workspace_init; calls that share one are ordered on a
  * stream.  Two kernels: partial results over equal ranges of cached tokens, then
