@@ -377,12 +377,11 @@ def _verify(s):
     w = _steps(r)
     w = torch.where(w.sum(1, keepdim=True) > 0, w, _steps(s.p[first + cur].clamp(min=0)))
     cum = torch.cumsum(w, 1)
-    # u * total in whole numbers: u is a number of 24 bits behind the point, or finer; 64 bits hold 40 of them here
-    u = s.u_sample.double()
+    # floor(u * total) in whole numbers: u = m 2^-(24 + k), m below 2^24, the total in halves of 24 bits
+    m, k = torch.frexp(s.u_sample)
+    m, k = (m * 2.0 ** 24).long(), (-k).clamp(0, 63)
     total = cum[:, -1]
-    hi, lo = total >> 24, total & 0xFFFFFF
-    steps = torch.floor(u * 2.0 ** 24).long()                           # exact for the numbers that torch draws
-    goal = steps * hi + ((steps * lo) >> 24)                            # floor(u * total)
+    goal = (m * (total >> 24) + ((m * (total & 0xFFFFFF)) >> 24)) >> k
     s.next.copy_((cum <= goal[:, None]).sum(1))
     s.count.copy_(kept)
     return _verified(s)
