@@ -142,6 +142,17 @@ __device__ __forceinline__ TrReq tr_request(const TreeArgs &a, int r)
     if (zeros) q.n = 0;
     return q;
 }
+// The largest end of the ranges in front of request r that lie in [0, T].
+__device__ __forceinline__ int tr_front(const TreeArgs &a, int r)
+{
+    int front = 0;
+#pragma unroll 1
+    for (int j = 0; j < r; ++j) {
+        const int q0 = __ldg(a.qo_indptr + j), q1 = __ldg(a.qo_indptr + j + 1);
+        if (q0 >= 0 && q0 < q1 && q1 <= a.T) front = max(front, q1);
+    }
+    return front;
+}
 __device__ __forceinline__ int tr_pairs(const TreeArgs &a, int n) { return n <= 2 * a.tq ? 1 : (n + 2 * a.tq - 1) / (2 * a.tq); }
 __device__ __forceinline__ int tr_ktiles(int L) { return (L + kTrTile - 1) / kTrTile; }
 // The segments laid end to end: a segment is `cost` places that nobody works on and then its tiles, so that a range with
@@ -1181,9 +1192,11 @@ __global__ void __launch_bounds__(kTrMergeThreads, 2) tree_merge_kernel(const __
     {
         const int per = (a.R + kTrMergeThreads - 1) / kTrMergeThreads, lo = min(a.R, tid * per), hi = min(a.R, lo + per);
         uint64_t run = 0;
+        bool down = false;
 #pragma unroll 1
         for (int r = lo; r < hi; ++r) {
             const TrReq q = tr_request(a, r);
+            down |= __ldg(a.qo_indptr + r + 1) < q.q0;
             s_pref[r] = q.n > 0 ? tr_pairs(a, q.n) : 0;
             s_q0[r] = q.q0;
             s_kt[r] = q.n > 0 ? tr_ktiles(q.L) : 0;
@@ -1196,7 +1209,13 @@ __global__ void __launch_bounds__(kTrMergeThreads, 2) tree_merge_kernel(const __
             if (lane >= o) incl += v;
         }
         if (lane == 31) s_w[warp] = incl;
-        __syncthreads();
+        // a node's request is found by bisection over the starts: where they decrease, a request that is left out gets
+        // the end of those in front of it in place of its own start
+        if (__syncthreads_or(down)) {
+#pragma unroll 1
+            for (int r = lo; r < hi; ++r)
+                if (s_kt[r] == 0) s_q0[r] = tr_front(a, r);
+        }
         uint64_t before = incl - run, all = 0;
 #pragma unroll
         for (int w = 0; w < kTrMergeThreads / 32; ++w) {

@@ -1,0 +1,75 @@
+"""Drafted tokens' calls where a batch holds requests that cannot be read: the others
+are answered as they are in a batch without them."""
+import pytest
+import torch
+
+import _spec_ref as S
+from paged_kv_cache_188_gb300 import api
+from test_gpu_tree import check, make, pack, tree
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    api.lib()
+
+
+def batch(qo, T, valid, context, Hkv, D, block, seed):
+    """Requests with the starts `qo`, of which those of `valid` can be read, over contexts that several CTAs share."""
+    nodes = [qo[r + 1] - qo[r] if r in valid else 1 for r in range(len(qo) - 1)]
+    c = make([context if r in valid else 10 for r in range(len(nodes))], nodes, Hkv, D, 16, block, seed, layers=1, layer=0)
+    c.qo = qo
+    seen = [S.tree_seen(S.random_parents(n, c.g)) for n in nodes]
+    q = torch.randn((T, 4 * Hkv, D), generator=c.g).to(torch.bfloat16)
+    mask = torch.zeros((T, 1), dtype=torch.int32, device="cuda")
+    for r in valid:
+        mask[qo[r]:qo[r + 1]] = pack([seen[r]])
+    return c, q, seen, mask
+
+
+def others(out, qo, valid):
+    """Rows of no request that is read."""
+    mine = [t for r in valid for t in range(qo[r], qo[r + 1])]
+    return out[[t for t in range(out.shape[0]) if t not in mine]]
+
+
+BAD_STARTS = [([0, 9, 5, 8], 8, [2]),
+              ([0, 4, 1000, 12, 16], 16, [0, 3]),
+              ([0, 4, -7, -7, 4, 9], 9, [0, 4]),
+              ([0, 4, 1000, 1000, 12, 12, 16], 16, [0, 5]),
+              ([7, 7, 0, 6], 6, [2]),
+              ([-4, 4, 8, 12, 16], 16, [1, 2, 3]),
+              ([0, 4, 8, 12, 20], 16, [0, 1, 2])]
+
+
+@pytest.mark.parametrize("qo,T,valid", BAD_STARTS)
+@pytest.mark.parametrize("context", [100, 9000])
+@pytest.mark.parametrize("block", [0, 16])
+def test_starts_out_of_range(qo, T, valid, context, block):
+    """A start that is out of range leaves out the requests that it bounds, and no other."""
+    c, q, seen, mask = batch(qo, T, valid, context, 2, 64, block, 60 + T)
+    out, ws = tree(c, q.cuda(), 0.05, mask)
+    assert api.pa_get_error(ws) == api.DEVERR_LEN
+    check(c, q, out, 0.05, seen, f"starts {qo}", reqs=valid)
+    assert torch.isnan(others(out, qo, valid).float()).all()
+
+
+def test_a_start_out_of_range_among_many():
+    """One bad start in the middle of a batch: the two requests around it are left out."""
+    g = torch.Generator().manual_seed(5)
+    counts = torch.randint(0, 7, (90,), generator=g).tolist()
+    qo = [0]
+    for n in counts:
+        qo.append(qo[-1] + n)
+    T, at = qo[-1], 41
+    for bad in (-1, T + 1, 2 ** 31 - 1, -2 ** 31):
+        starts = qo[:at] + [bad] + qo[at + 1:]
+        valid = [r for r in range(90) if r not in (at - 1, at) and counts[r]]
+        c, q, seen, mask = batch(starts, T, valid, 700, 8, 128, 0, 61)
+        out, ws = tree(c, q.cuda(), 0.05, mask)
+        assert api.pa_get_error(ws) == api.DEVERR_LEN
+        check(c, q, out, 0.05, seen, f"start {bad}", reqs=valid)
+        assert torch.isnan(others(out, starts, valid).float()).all()
