@@ -479,8 +479,8 @@ pa_status pa_kv_evict(int32_t *req_to_token, int req_rows, int max_ctx, const in
  * initialised once with pa_workspace_init; calls that share one are ordered on a
  * stream.  Two kernels: partial results over equal ranges of cached tokens, then
  * their merge in a fixed order (run-to-run bit-identical).  A range qo_indptr[r] ..
- * qo_indptr[r+1] outside [0, n_tokens] sets PA_DEVERR_LEN and skips the request; a
- * request row out of range (PA_DEVERR_ROW), L_r outside [n_r, max_ctx] or more nodes
+ * qo_indptr[r+1] outside [0, n_tokens], or one that begins in front of the end of an
+ * earlier one inside it, sets PA_DEVERR_LEN and skips the request; a request row out of range (PA_DEVERR_ROW), L_r outside [n_r, max_ctx] or more nodes
  * than the mask has bits (PA_DEVERR_LEN) give zeros; a slot outside [0, size) is
  * masked and sets PA_DEVERR_SLOT.  Under PA_OVERLAP_EARLY_KV it behaves as in
  * early-metadata mode, in which qo_indptr is an index input and tree_mask is not. */

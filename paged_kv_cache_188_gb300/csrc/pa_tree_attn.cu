@@ -113,35 +113,6 @@ struct TreeArgs {
 struct alignas(16) TrReq {
     int q0, n, L, row;      // n = 0: nothing to do
 };
-// A request, and what is wrong with it: `zeros` where its rows become zeros.
-__device__ __forceinline__ TrReq tr_request(const TreeArgs &a, int r, int &bits, bool &zeros)
-{
-    TrReq q;
-    q.q0 = __ldg(a.qo_indptr + r);
-    const int q1 = __ldg(a.qo_indptr + r + 1);
-    q.L = __ldg(a.seq_lens + r);
-    q.row = __ldg(a.req_pool_indices + r);
-    q.n = q1 - q.q0;
-    bits = 0;
-    zeros = false;
-    if (q1 <= q.q0 || q.q0 < 0 || q1 > a.T) {
-        if (q1 != q.q0) bits = PA_DEVERR_LEN;
-        q.n = 0;
-        return q;
-    }
-    if (q.row < 0 || q.row >= a.req_rows) bits |= PA_DEVERR_ROW;
-    if (q.L < q.n || q.L > a.max_ctx || (a.tree_mask && q.n > 32 * (int64_t)a.mask_words)) bits |= PA_DEVERR_LEN;
-    zeros = bits != 0;
-    return q;
-}
-__device__ __forceinline__ TrReq tr_request(const TreeArgs &a, int r)
-{
-    int bits;
-    bool zeros;
-    TrReq q = tr_request(a, r, bits, zeros);
-    if (zeros) q.n = 0;
-    return q;
-}
 // The largest end of the ranges in front of request r that lie in [0, T].
 __device__ __forceinline__ int tr_front(const TreeArgs &a, int r)
 {
@@ -152,6 +123,37 @@ __device__ __forceinline__ int tr_front(const TreeArgs &a, int r)
         if (q0 >= 0 && q0 < q1 && q1 <= a.T) front = max(front, q1);
     }
     return front;
+}
+// A request, and what is wrong with it: `zeros` where its rows become zeros.  `down`: the starts decrease somewhere.  Only
+// then can a range begin in front of an earlier one's end; such a request is left out, so that no row is two requests'
+// and all segments together are no more than the host allowed for.
+__device__ __forceinline__ TrReq tr_request(const TreeArgs &a, int r, bool down, int &bits, bool &zeros)
+{
+    TrReq q;
+    q.q0 = __ldg(a.qo_indptr + r);
+    const int q1 = __ldg(a.qo_indptr + r + 1);
+    q.L = __ldg(a.seq_lens + r);
+    q.row = __ldg(a.req_pool_indices + r);
+    q.n = q1 - q.q0;
+    bits = 0;
+    zeros = false;
+    if (q1 <= q.q0 || q.q0 < 0 || q1 > a.T || (down && q.q0 < tr_front(a, r))) {
+        if (q1 != q.q0) bits = PA_DEVERR_LEN;
+        q.n = 0;
+        return q;
+    }
+    if (q.row < 0 || q.row >= a.req_rows) bits |= PA_DEVERR_ROW;
+    if (q.L < q.n || q.L > a.max_ctx || (a.tree_mask && q.n > 32 * (int64_t)a.mask_words)) bits |= PA_DEVERR_LEN;
+    zeros = bits != 0;
+    return q;
+}
+__device__ __forceinline__ TrReq tr_request(const TreeArgs &a, int r, bool down)
+{
+    int bits;
+    bool zeros;
+    TrReq q = tr_request(a, r, down, bits, zeros);
+    if (zeros) q.n = 0;
+    return q;
 }
 __device__ __forceinline__ int tr_pairs(const TreeArgs &a, int n) { return n <= 2 * a.tq ? 1 : (n + 2 * a.tq - 1) / (2 * a.tq); }
 __device__ __forceinline__ int tr_ktiles(int L) { return (L + kTrTile - 1) / kTrTile; }
@@ -174,6 +176,7 @@ __device__ __forceinline__ int tr_places(uint64_t load, int cost) { return (int)
 
 struct TrPlan {
     int total, W, cost;     // places in all, of a range, of a segment before its tiles
+    int down;               // the starts decrease somewhere
     int start[2][2];        // (request, its first place) where the CTA's units start (a third unit exists only where all
                             // of them are the whole of one kv head)
     TrReq req[2];           // that request
@@ -231,7 +234,7 @@ __device__ __forceinline__ bool tr_next(const TreeArgs &a, const TrPlan &p, TrWa
                 if (k.r - k.w0 >= 32) {
                     k.w0 = k.r;
                     k.w = TrReq{0, 0, 0, 0};
-                    if (k.r + lane < a.R) k.w = tr_request(a, k.r + lane);
+                    if (k.r + lane < a.R) k.w = tr_request(a, k.r + lane, p.down);
                 }
                 const int i = k.r - k.w0;
                 q.q0 = __shfl_sync(0xffffffffu, k.w.q0, i);
@@ -711,30 +714,41 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
 
     if (warp == 4 && lane == 0) prefetch_tmap(&a.tm_q);
     // ---- plan: the segments' tiles in all, and where this CTA's units start
-    int bits = 0;
-    bool zeros = false;
+    int bits;
+    bool zeros, down = false;
     {
         const int per = (a.R + kTrThreads - 1) / kTrThreads, lo = min(a.R, tid * per), hi = min(a.R, lo + per);
-        uint64_t run = 0;
+        uint64_t run, incl;
         TrReq q;                               // the thread's last request
 #pragma unroll 1
-        for (int r = lo; r < hi; ++r) {
-            int b;
-            bool z;
-            q = tr_request(a, r, b, z);
-            if (z) q.n = 0;
-            run += tr_load(a, q);
-            bits |= b;
-            zeros |= z;
-        }
-        uint64_t incl = run;
+        while (true) {                         // (again where the starts turn out to decrease)
+            bool less = false;
+            run = 0;
+            bits = 0;
+            zeros = false;
+#pragma unroll 1
+            for (int r = lo; r < hi; ++r) {
+                int b;
+                bool z;
+                q = tr_request(a, r, down, b, z);
+                less |= __ldg(a.qo_indptr + r + 1) < q.q0;
+                if (z) q.n = 0;
+                run += tr_load(a, q);
+                bits |= b;
+                zeros |= z;
+            }
+            incl = run;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += v;
+            }
+            if (lane == 31) s_w[warp] = incl;
+            if (!__syncthreads_or(zeros || (less && !down))) break;
+            zeros = __syncthreads_or(zeros);
+            if (down || !__syncthreads_or(less)) break;
+            down = true;
         }
-        if (lane == 31) s_w[warp] = incl;
-        zeros = __syncthreads_or(zeros);
         uint64_t before = incl - run, all = 0, sums[kTrThreads / 32];
 #pragma unroll
         for (int w = 0; w < kTrThreads / 32; ++w) sums[w] = s_w[w];
@@ -749,6 +763,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
             plan.total = total;
             plan.W = W;
             plan.cost = cost;
+            plan.down = down;
         }
         if (a.ranges > 1 && len > 0) {
 #pragma unroll 1
@@ -758,13 +773,13 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
                 int S0 = mine, r = lo;
 #pragma unroll 1
                 for (; r < hi - 1; ++r) {
-                    const int t = tr_places(a, tr_request(a, r), cost);
+                    const int t = tr_places(a, tr_request(a, r, down), cost);
                     if (x < S0 + t) break;
                     S0 += t;
                 }
                 plan.start[u][0] = r;
                 plan.start[u][1] = S0;
-                plan.req[u] = r == hi - 1 ? q : tr_request(a, r);
+                plan.req[u] = r == hi - 1 ? q : tr_request(a, r, down);
             }
         }
     }
@@ -780,7 +795,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
         for (int r = blockIdx.x; r < a.R; r += gridDim.x) {
             int b;
             bool z;
-            const TrReq q = tr_request(a, r, b, z);
+            const TrReq q = tr_request(a, r, down, b, z);
             if (!z) continue;
             uint4 *dst = reinterpret_cast<uint4 *>(a.out + (int64_t)q.q0 * a.Hq * D);
             for (int64_t x = tid; x < (int64_t)q.n * a.Hq * D / 8; x += kTrThreads) dst[x] = make_uint4(0u, 0u, 0u, 0u);
@@ -1191,30 +1206,32 @@ __global__ void __launch_bounds__(kTrMergeThreads, 2) tree_merge_kernel(const __
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     {
         const int per = (a.R + kTrMergeThreads - 1) / kTrMergeThreads, lo = min(a.R, tid * per), hi = min(a.R, lo + per);
-        uint64_t run = 0;
+        uint64_t run, incl;
         bool down = false;
 #pragma unroll 1
-        for (int r = lo; r < hi; ++r) {
-            const TrReq q = tr_request(a, r);
-            down |= __ldg(a.qo_indptr + r + 1) < q.q0;
-            s_pref[r] = q.n > 0 ? tr_pairs(a, q.n) : 0;
-            s_q0[r] = q.q0;
-            s_kt[r] = q.n > 0 ? tr_ktiles(q.L) : 0;
-            run += tr_load(a, q);
-        }
-        uint64_t incl = run;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
-        }
-        if (lane == 31) s_w[warp] = incl;
-        // a node's request is found by bisection over the starts: where they decrease, a request that is left out gets
-        // the end of those in front of it in place of its own start
-        if (__syncthreads_or(down)) {
+        while (true) {
+            bool less = false;
+            run = 0;
 #pragma unroll 1
-            for (int r = lo; r < hi; ++r)
-                if (s_kt[r] == 0) s_q0[r] = tr_front(a, r);
+            for (int r = lo; r < hi; ++r) {
+                const TrReq q = tr_request(a, r, down);
+                less |= __ldg(a.qo_indptr + r + 1) < q.q0;
+                s_pref[r] = q.n > 0 ? tr_pairs(a, q.n) : 0;
+                // a node's request is found by bisection over the starts: where they decrease, a request that is left out
+                // gets the end of those in front of it in place of its own start
+                s_q0[r] = down && q.n == 0 ? tr_front(a, r) : q.q0;
+                s_kt[r] = q.n > 0 ? tr_ktiles(q.L) : 0;
+                run += tr_load(a, q);
+            }
+            incl = run;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += v;
+            }
+            if (lane == 31) s_w[warp] = incl;
+            if (!__syncthreads_or(less && !down)) break;
+            down = true;
         }
         uint64_t before = incl - run, all = 0;
 #pragma unroll
@@ -1260,7 +1277,6 @@ __global__ void __launch_bounds__(kTrMergeThreads, 2) tree_merge_kernel(const __
         const bool in = e < per_row;
         const int hc = (in ? e : 0) / a.G, g = (in ? e : 0) - hc * a.G, h = hc / GROUPS, cg = hc - h * GROUPS;
         const int i0 = S / W, i1 = (S + kt - 1) / W, row = (tile & 1) * kTrTile + (node - tile * a.tq) * a.G + g;   // of the pair's 256
-        if (i0 < 0 || i1 < i0 || i1 >= a.ranges) continue;       // (sums that overflowed, of requests that overlap)
         auto slot = [&](int i) { return (int64_t)(2 * (i * a.Hkv + h) + (i == i0 && S > i0 * W ? 1 : 0)); };
         float M = -INFINITY, L = 0.f, o[kTrMergeCols];
 #pragma unroll

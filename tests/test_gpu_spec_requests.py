@@ -73,3 +73,36 @@ def test_a_start_out_of_range_among_many():
         assert api.pa_get_error(ws) == api.DEVERR_LEN
         check(c, q, out, 0.05, seen, f"start {bad}", reqs=valid)
         assert torch.isnan(others(out, starts, valid).float()).all()
+
+
+OVERLAPS = [([0, 5, 3, 8], 8, [0]),
+            ([0, 8, 2, 6, 8], 8, [0]),
+            ([0, 4, 2, 8, 12], 12, [0, 3]),
+            ([0, 3, 1, 6, 4, 8, 9], 9, [0, 5]),
+            ([5, 12, 0, 12, 12, 16], 16, [0, 4])]
+
+
+@pytest.mark.parametrize("qo,T,valid", OVERLAPS)
+@pytest.mark.parametrize("context", [100, 9000])
+@pytest.mark.parametrize("block", [0, 16])
+def test_ranges_that_begin_before_an_earlier_end(qo, T, valid, context, block):
+    """Of two requests that would have the same rows the first has them."""
+    c, q, seen, mask = batch(qo, T, valid, context, 2, 64, block, 70 + T)
+    out, ws = tree(c, q.cuda(), 0.05, mask)
+    assert api.pa_get_error(ws) == api.DEVERR_LEN
+    check(c, q, out, 0.05, seen, f"starts {qo}", reqs=valid)
+    assert torch.isnan(others(out, qo, valid).float()).all()
+
+
+def test_the_same_range_many_times():
+    """Starts that go back again and again: the first request has the rows, whatever the number of the others."""
+    c, q, seen, mask = batch([0, 4], 4, [0], 5000, 2, 64, 0, 80)
+    want, _ = tree(c, q.cuda(), 0.05, mask)
+    k, v, table, rws, _, _ = c.dev
+    R = 4095
+    qo = torch.tensor([0, 4], dtype=torch.int32, device="cuda").repeat((R + 1) // 2)
+    ws = api.alloc_workspace(api.pa_tree_workspace_bytes(8, 2, 64))
+    out = torch.zeros_like(want)
+    api.pa_paged_tree_attn(q.cuda(), k, v, 0, qo, table, rws.repeat(R), c.dlens.repeat(R), 0.05, ws, out, tree_mask=mask)
+    assert api.pa_get_error(ws) == api.DEVERR_LEN
+    assert torch.equal(out.view(torch.int16), want.view(torch.int16))
