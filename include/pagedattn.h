@@ -473,7 +473,8 @@ pa_status pa_kv_evict(int32_t *req_to_token, int req_rows, int max_ctx, const in
  * [n_tokens, n_q_heads, head_dim], not overlapping; rows from qo_indptr[n_reqs] on are not written.
  * block == 0: the bf16 cache, k_exp and v_exp NULL; block >= 1: the e4m3 cache
  * with scales per block of slots, its arithmetic that of
- * pa_paged_prefill_attn_fp8_block (q within 2^-17 of its row's largest element).
+ * pa_paged_prefill_attn_fp8_block (q within 2^-17 of its row's largest element; a row of
+ * q that holds a NaN or an infinity gives NaN where it sees anything).
  * The weights are rounded to bf16.  Supported: head_dim 64 or 128, 1 <= G <= 16,
  * n_reqs <= 4096.  Workspace: pa_tree_workspace_bytes, whatever the batch,
  * initialised once with pa_workspace_init; calls that share one are ordered on a

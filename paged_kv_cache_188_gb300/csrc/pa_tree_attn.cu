@@ -971,7 +971,16 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
                 // this thread's row of q, in place, into its two e4m3 terms; the row's scale joins the softmax scale
                 if (X == 0 || two) {
                     wait(bar(C::Q_FULL + X), (X == 0 ? piece : p2) & 1);
-                    const float qs = split_q_row<D>(base + X * C::TILE, row, a.negate ? -1.f : 1.f);
+                    const uint32_t qt = base + X * C::TILE;
+                    float qs = split_q_row<D>(qt, row, a.negate ? -1.f : 1.f);
+                    if (!(qs == qs)) {
+                        // a NaN or an infinity in the row: its first term becomes NaN, and with it every score.  (As the
+                        // softmax scale it would reach what the row does not see as well.)
+#pragma unroll 1
+                        for (int c = 0; c < D / 16; ++c)
+                            st_shared_v4(qt + row * 128 + ((c ^ (row & 7)) << 4), 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+                        qs = 1.f;
+                    }
                     if (X == 0) reinterpret_cast<float *>(sb + C::OffQS)[row] = qs;
                     fence_proxy_async_smem();
                     mbar_arrive(bar(C::Q_SPLIT + X));

@@ -1,11 +1,13 @@
-"""Drafted tokens' calls where a batch holds requests that cannot be read: the others
-are answered as they are in a batch without them."""
+"""Drafted tokens' calls where a batch holds requests that cannot be read, or rows whose
+query is no number: the others are answered as they are in a batch without them."""
+import math
+
 import pytest
 import torch
 
 import _spec_ref as S
 from paged_kv_cache_188_gb300 import api
-from test_gpu_tree import check, make, pack, tree
+from test_gpu_tree import check, make, pack, queries, tree
 
 pytestmark = pytest.mark.gpu
 
@@ -106,3 +108,30 @@ def test_the_same_range_many_times():
     api.pa_paged_tree_attn(q.cuda(), k, v, 0, qo, table, rws.repeat(R), c.dlens.repeat(R), 0.05, ws, out, tree_mask=mask)
     assert api.pa_get_error(ws) == api.DEVERR_LEN
     assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("what", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("block", [0, 16])
+def test_rows_that_see_nothing_whatever_their_query(what, D, block):
+    """A row that sees nothing is zeros, its query a NaN or not; one that sees something is NaN then, and the other
+    rows are what they are."""
+    c = make([0, 0, 300], [4, 140, 5], 2, D, 16, block, 62)
+    seen = [torch.eye(4, dtype=torch.bool), S.chain_seen(140), S.chain_seen(5)]
+    seen[0][1] = False                         # blind rows: 1, and 4 + 130 in the second tile of its piece
+    seen[1][130] = False
+    mask = pack(seen)
+    q = queries(c, 4, D)
+    rows = [1, 4 + 130, 2, 4 + 7, 4 + 140 + 3]
+    q[rows, :, 3] = what
+    out, ws = tree(c, q.cuda(), 0.05, mask)
+    assert api.pa_get_error(ws) == 0
+    out = out.cpu()
+    assert torch.count_nonzero(out[rows[:2]]) == 0
+    if block or math.isnan(what):
+        assert torch.isnan(out[rows[2:]].float()).all()
+    good, clean = [t for t in range(c.qo[-1]) if t not in rows], q.clone()
+    clean[rows] = 1.0
+    base, _ = tree(c, clean.cuda(), 0.05, mask)
+    assert torch.equal(out[good].view(torch.int16), base.cpu()[good].view(torch.int16))
+    check(c, clean, base, 0.05, seen, f"D={D} block={block}")
