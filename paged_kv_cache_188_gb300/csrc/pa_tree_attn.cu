@@ -1121,7 +1121,12 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_attn_kernel(const __grid_c
             // one tile of rows: the warpgroups end it together, with or without steps for stream B, whose roles else got ahead
             // of tiles that they do not follow: a wait for a stage's next tile would pass before this one's has come
             if (join && X == 1) s_ml[row] = make_float2(m2, l);
-            if (!two) named_bar_sync(1, 256);
+            if (!two) {
+                // (stream A reads B's O below: B's wait for its last product is ordered in front of that)
+                tc_fence_before();
+                named_bar_sync(1, 256);
+                tc_fence_after();
+            }
             if (join) {
                 if (X == 0) {
                     const float2 b = s_ml[row];
