@@ -113,21 +113,8 @@ struct TreeArgs {
 struct alignas(16) TrReq {
     int q0, n, L, row;      // n = 0: nothing to do
 };
-// The largest end of the ranges in front of request r that lie in [0, T].
-__device__ __forceinline__ int tr_front(const TreeArgs &a, int r)
-{
-    int front = 0;
-#pragma unroll 1
-    for (int j = 0; j < r; ++j) {
-        const int q0 = __ldg(a.qo_indptr + j), q1 = __ldg(a.qo_indptr + j + 1);
-        if (q0 >= 0 && q0 < q1 && q1 <= a.T) front = max(front, q1);
-    }
-    return front;
-}
-// A request, and what is wrong with it: `zeros` where its rows become zeros.  `down`: the starts decrease somewhere.  Only
-// then can a range begin in front of an earlier one's end; such a request is left out, so that no row is two requests'
-// and all segments together are no more than the host allowed for.
-__device__ __forceinline__ TrReq tr_request(const TreeArgs &a, int r, bool down, int &bits, bool &zeros)
+// A request, and what is wrong with it: `zeros` where its rows become zeros.
+__device__ __forceinline__ TrReq tr_request(const TreeArgs &a, int r, int &bits, bool &zeros)
 {
     TrReq q;
     q.q0 = __ldg(a.qo_indptr + r);
@@ -137,7 +124,7 @@ __device__ __forceinline__ TrReq tr_request(const TreeArgs &a, int r, bool down,
     q.n = q1 - q.q0;
     bits = 0;
     zeros = false;
-    if (q1 <= q.q0 || q.q0 < 0 || q1 > a.T || (down && q.q0 < tr_front(a, r))) {
+    if (q1 <= q.q0 || q.q0 < 0 || q1 > a.T) {
         if (q1 != q.q0) bits = PA_DEVERR_LEN;
         q.n = 0;
         return q;
@@ -145,6 +132,30 @@ __device__ __forceinline__ TrReq tr_request(const TreeArgs &a, int r, bool down,
     if (q.row < 0 || q.row >= a.req_rows) bits |= PA_DEVERR_ROW;
     if (q.L < q.n || q.L > a.max_ctx || (a.tree_mask && q.n > 32 * (int64_t)a.mask_words)) bits |= PA_DEVERR_LEN;
     zeros = bits != 0;
+    return q;
+}
+// The largest end of the ranges in front of request r that lie in [0, T].  (A call: only a broken batch makes it, and
+// copies of it in each place took 0.2 us to fetch.)
+__device__ __noinline__ int tr_front(const int32_t *qo_indptr, int T, int r)
+{
+    int front = 0;
+#pragma unroll 1
+    for (int j = 0; j < r; ++j) {
+        const int q0 = __ldg(qo_indptr + j), q1 = __ldg(qo_indptr + j + 1);
+        if (q0 >= 0 && q0 < q1 && q1 <= T) front = max(front, q1);
+    }
+    return front;
+}
+// `down`: the starts decrease somewhere.  Only then can a range begin in front of an earlier one's end; such a request is
+// left out, so that no row is two requests' and all segments together are no more than the host allowed for.
+__device__ __forceinline__ TrReq tr_request(const TreeArgs &a, int r, bool down, int &bits, bool &zeros)
+{
+    TrReq q = tr_request(a, r, bits, zeros);
+    if (down && q.n > 0 && q.q0 < tr_front(a.qo_indptr, a.T, r)) {
+        q.n = 0;
+        bits = PA_DEVERR_LEN;
+        zeros = false;
+    }
     return q;
 }
 __device__ __forceinline__ TrReq tr_request(const TreeArgs &a, int r, bool down)
@@ -1220,10 +1231,10 @@ __global__ void __launch_bounds__(kTrMergeThreads, 2) tree_merge_kernel(const __
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     {
         const int per = (a.R + kTrMergeThreads - 1) / kTrMergeThreads, lo = min(a.R, tid * per), hi = min(a.R, lo + per);
-        uint64_t run, incl;
+        uint64_t run, before, all;
         bool down = false;
 #pragma unroll 1
-        while (true) {
+        while (true) {                         // (again where the starts turn out to decrease)
             bool less = false;
             run = 0;
 #pragma unroll 1
@@ -1233,25 +1244,33 @@ __global__ void __launch_bounds__(kTrMergeThreads, 2) tree_merge_kernel(const __
                 s_pref[r] = q.n > 0 ? tr_pairs(a, q.n) : 0;
                 // a node's request is found by bisection over the starts: where they decrease, a request that is left out
                 // gets the end of those in front of it in place of its own start
-                s_q0[r] = down && q.n == 0 ? tr_front(a, r) : q.q0;
+                s_q0[r] = down && q.n == 0 ? tr_front(a.qo_indptr, a.T, r) : q.q0;
                 s_kt[r] = q.n > 0 ? tr_ktiles(q.L) : 0;
                 run += tr_load(a, q);
             }
-            incl = run;
+            uint64_t incl = run;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const uint64_t v = __shfl_up_sync(0xffffffffu, incl, o);
                 if (lane >= o) incl += v;
             }
-            if (lane == 31) s_w[warp] = incl;
-            if (!__syncthreads_or(less && !down)) break;
-            down = true;
-        }
-        uint64_t before = incl - run, all = 0;
+            // (bit 63, which no sum reaches: a start below the one before.  With the warps' sums it costs no barrier more)
+            less = __any_sync(0xffffffffu, less && !down);
+            if (lane == 31) s_w[warp] = incl | (uint64_t)less << 63;
+            __syncthreads();
+            uint64_t flags = 0;
+            before = incl - run;
+            all = 0;
 #pragma unroll
-        for (int w = 0; w < kTrMergeThreads / 32; ++w) {
-            if (w < warp) before += s_w[w];
-            all += s_w[w];
+            for (int w = 0; w < kTrMergeThreads / 32; ++w) {
+                const uint64_t x = s_w[w];
+                if (w < warp) before += x;
+                all += x;
+                flags |= x;
+            }
+            if (!(flags >> 63)) break;
+            down = true;
+            __syncthreads();
         }
         const int c = tr_cost(a, all);
         int at = tr_places(before, c);
