@@ -32,10 +32,11 @@ struct AcceptArgs {
     int T, R, req_rows, max_ctx, max_path, n_layers, size, row_bytes;
 };
 
-// A request's nodes [q0, q0 + n), context c and accepted number; false (and its length in `left`) where it is left
-// as it is.  Whole CTA; `report` by one CTA per request.
+// A request's nodes [q0, q0 + n), context c and accepted number; false where it is left as it is, for a fault or because
+// it has no nodes (a batch's padding, whose row and length may be anything); its length then is `len`.  Whole CTA;
+// `report` by one CTA per request.
 struct AcReq {
-    int q0, n, c, kept, row, left;
+    int q0, n, c, kept, row, len;
 };
 __device__ __forceinline__ bool ac_request(const AcceptArgs &a, int r, bool report, AcReq &q)
 {
@@ -46,10 +47,10 @@ __device__ __forceinline__ bool ac_request(const AcceptArgs &a, int r, bool repo
     q.kept = __ldcg(a.n_accepted + r);
     q.n = q1 - q.q0;
     q.c = L - q.n;
-    q.left = max(0, min(L, a.max_ctx));
+    q.len = max(0, min(L, a.max_ctx));
     int bits = 0;
     const bool range = q.n >= 0 && q.q0 >= 0 && q1 <= a.T;
-    if (!range || L < q.n || L > a.max_ctx || L < 0) bits |= PA_DEVERR_LEN;
+    if (q.n != 0 && (!range || L < q.n || L > a.max_ctx || L < 0)) bits |= PA_DEVERR_LEN;
     if (q.n > 0 && (q.row < 0 || q.row >= a.req_rows)) bits |= PA_DEVERR_ROW;
     const bool count = q.kept >= 0 && q.kept <= a.max_path && q.kept <= max(q.n, 0);
     int again = 0, wrong = !count;
@@ -66,7 +67,9 @@ __device__ __forceinline__ bool ac_request(const AcceptArgs &a, int r, bool repo
     if (__syncthreads_or(again)) bits |= PA_DEVERR_ROW;
     if (__syncthreads_or(wrong)) bits |= PA_DEVERR_TREE;
     if (bits && report && tid == 0) set_error(a.err, bits);
-    return bits == 0;
+    if (bits != 0 || q.n == 0) return false;
+    q.len = q.c + q.kept;
+    return true;
 }
 
 __global__ void __launch_bounds__(kAcThreads) kv_accept_table_kernel(const AcceptArgs a)
@@ -76,7 +79,7 @@ __global__ void __launch_bounds__(kAcThreads) kv_accept_table_kernel(const Accep
     const int r = blockIdx.x, tid = threadIdx.x;
     AcReq q;
     const bool ok = ac_request(a, r, true, q);     // every thread has read the length (new_lens may be seq_lens)
-    if (tid == 0) a.new_lens[r] = ok ? q.c + q.kept : q.left;
+    if (tid == 0) a.new_lens[r] = q.len;
     if (!ok) return;
     int32_t *tab = a.req_to_token + (int64_t)q.row * a.max_ctx + q.c;
     const int32_t *path = a.accepted + (int64_t)r * a.max_path;
@@ -109,7 +112,7 @@ __global__ void __launch_bounds__(kAcThreads) kv_accept_move_kernel(const Accept
     const int r = (int)(blockIdx.x / layers2), y = (int)(blockIdx.x % layers2);
     AcReq q;
     const bool ok = ac_request(a, r, y == 0, q);
-    if (y == 0 && tid == 0) a.new_lens[r] = ok ? q.c + q.kept : q.left;
+    if (y == 0 && tid == 0) a.new_lens[r] = q.len;
     if (!ok) return;
     const int32_t *tab = a.req_to_token + (int64_t)q.row * a.max_ctx + q.c;
     const int32_t *path = a.accepted + (int64_t)r * a.max_path;

@@ -8,6 +8,7 @@ import torch
 import _spec_ref as S
 from paged_kv_cache_188_gb300 import api
 from test_gpu_tree import check, make, pack, queries, tree
+from test_gpu_verify_accept import Batch, i32
 
 pytestmark = pytest.mark.gpu
 
@@ -135,3 +136,23 @@ def test_rows_that_see_nothing_whatever_their_query(what, D, block):
     base, _ = tree(c, clean.cuda(), 0.05, mask)
     assert torch.equal(out[good].view(torch.int16), base.cpu()[good].view(torch.int16))
     check(c, clean, base, 0.05, seen, f"D={D} block={block}")
+
+
+@pytest.mark.parametrize("move", [False, True])
+@pytest.mark.parametrize("length", [-5, 10 ** 6, 0, 7])
+def test_accept_requests_without_nodes(move, length):
+    """A request without nodes pads a batch whatever its length and row, as in the attention."""
+    b = Batch([30, 0, 9], [20, 0, 4], 63)
+    b.lens[1] = length
+    b.rows[1] = 77
+    kv = {}
+    if move:
+        k = torch.zeros((1, b.size, 1, 64), dtype=torch.bfloat16, device="cuda")
+        kv = dict(k=k, v=k.clone())
+    err = i32([0])
+    table, lens, freed = b.call(err=err, **kv)
+    assert api.pa_get_error_word(err) == 0
+    b.rows[1] = b.rows[0]                      # (nobody's)
+    b.lens[1] = max(0, min(length, b.table.shape[1]))
+    t, l, f, _ = b.want(move=move, skip={1})
+    assert torch.equal(table, t) and lens == l and freed == f
