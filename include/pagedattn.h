@@ -540,8 +540,8 @@ pa_status pa_tree_verify(const float *target_probs, const float *draft_probs, in
  * new_lens may be seq_lens in the table form; in the move form they must not overlap
  * (PA_ERR_SHAPE).  A path that is not increasing within [0, n_r), or longer than max_path or n_r, sets
  * PA_DEVERR_TREE; a row out of range, or one that an earlier request with nodes has too,
- * PA_DEVERR_ROW; L_r outside [n_r, max_ctx], or a qo_indptr range outside [0, n_tokens],
- * PA_DEVERR_LEN: such a request is left as it is (new_lens[r] is its length, clamped to [0, max_ctx]).  So is a
+ * PA_DEVERR_ROW; L_r outside [n_r, max_ctx], or a qo_indptr range outside [0, n_tokens] or
+ * that begins in front of the end of an earlier one inside it, PA_DEVERR_LEN: such a request is left as it is (new_lens[r] is its length, clamped to [0, max_ctx]).  So is a
  * request without nodes, a batch's padding, whatever its row and length, without an error.  A
  * slot outside [0, size) is not moved (PA_DEVERR_SLOT).  Requests must not share slots of nodes.
  * Table and lengths are index inputs of later calls: as behind pa_kv_evict, in the

@@ -53,10 +53,15 @@ __device__ __forceinline__ bool ac_request(const AcceptArgs &a, int r, bool repo
     if (q.n != 0 && (!range || L < q.n || L > a.max_ctx || L < 0)) bits |= PA_DEVERR_LEN;
     if (q.n > 0 && (q.row < 0 || q.row >= a.req_rows)) bits |= PA_DEVERR_ROW;
     const bool count = q.kept >= 0 && q.kept <= a.max_path && q.kept <= max(q.n, 0);
-    int again = 0, wrong = !count;
+    // earlier requests with nodes: of the same row, or whose range ends behind this one's start (two would list their slots
+    // in the same entries)
+    int again = 0, over = 0, wrong = !count;
     if (range && q.n > 0) {
-        for (int b = tid; b < r; b += kAcThreads)
-            if (__ldg(a.req_pool_indices + b) == q.row) again |= __ldg(a.qo_indptr + b + 1) > __ldg(a.qo_indptr + b);
+        for (int b = tid; b < r; b += kAcThreads) {
+            const int s = __ldg(a.qo_indptr + b), e = __ldg(a.qo_indptr + b + 1);
+            again |= s < e && __ldg(a.req_pool_indices + b) == q.row;
+            over |= s >= 0 && s < e && e <= a.T && e > q.q0;
+        }
         const int32_t *path = a.accepted + (int64_t)r * a.max_path;
         if (count)
             for (int k = tid; k < q.kept; k += kAcThreads) {
@@ -64,8 +69,11 @@ __device__ __forceinline__ bool ac_request(const AcceptArgs &a, int r, bool repo
                 wrong |= e < 0 || e >= q.n || (k > 0 && e <= __ldcg(path + k - 1));
             }
     }
-    if (__syncthreads_or(again)) bits |= PA_DEVERR_ROW;
-    if (__syncthreads_or(wrong)) bits |= PA_DEVERR_TREE;
+    if (__syncthreads_or(again | over | wrong)) {
+        if (__syncthreads_or(again)) bits |= PA_DEVERR_ROW;
+        if (__syncthreads_or(over)) bits |= PA_DEVERR_LEN;
+        if (__syncthreads_or(wrong)) bits |= PA_DEVERR_TREE;
+    }
     if (bits && report && tid == 0) set_error(a.err, bits);
     if (bits != 0 || q.n == 0) return false;
     q.len = q.c + q.kept;

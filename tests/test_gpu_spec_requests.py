@@ -156,3 +156,23 @@ def test_accept_requests_without_nodes(move, length):
     b.lens[1] = max(0, min(length, b.table.shape[1]))
     t, l, f, _ = b.want(move=move, skip={1})
     assert torch.equal(table, t) and lens == l and freed == f
+
+
+@pytest.mark.parametrize("move", [False, True])
+def test_accept_ranges_that_begin_before_an_earlier_end(move):
+    """Two requests with the same entries of the list of free slots: the first has them, the other one is left as it is."""
+    b = Batch([30, 5, 9, 12], [6, 1, 7, 3], 64)
+    b.qo = [0, 6, 2, 9, 12]
+    k = torch.randn((2, b.size, 2, 64), generator=b.g).to(torch.bfloat16)
+    kv = dict(k=k.cuda(), v=k.flip(0).contiguous().cuda()) if move else {}
+    err = i32([0])
+    table, lens, freed = b.call(err=err, **kv)
+    # (request 1, from 6 to 2, has a path of one node, which is longer than its range)
+    assert api.pa_get_error_word(err) == api.DEVERR_LEN | api.DEVERR_TREE
+    t, l, f, moves = b.want(move=move, skip={1, 2})
+    assert torch.equal(table, t) and lens == l and freed == f
+    if move:
+        now = k.clone()
+        for src, dst in moves:
+            now[:, dst] = k[:, src]
+        assert torch.equal(kv["k"].cpu(), now) and torch.equal(kv["v"].cpu(), now.flip(0))
