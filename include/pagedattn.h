@@ -537,7 +537,7 @@ pa_status pa_tree_verify(const float *target_probs, const float *draft_probs, in
  * freed[qo_indptr[r] ..] lists the slots of positions c_r + a_r .. L_r - 1: whole pages
  * come free.
  * new_lens[r] = c_r + a_r; freed int32 [n_tokens], entries not listed are left as they are.
- * new_lens may be seq_lens in the table form; in the move form they must not overlap
+ * new_lens may be seq_lens in the table form; else they must not overlap
  * (PA_ERR_SHAPE).  A path that is not increasing within [0, n_r), or longer than max_path or n_r, sets
  * PA_DEVERR_TREE; a row out of range, or one that an earlier request with nodes has too,
  * PA_DEVERR_ROW; L_r outside [n_r, max_ctx], or a qo_indptr range outside [0, n_tokens] or

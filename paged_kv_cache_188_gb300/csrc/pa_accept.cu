@@ -171,8 +171,6 @@ extern "C" pa_status pa_kv_accept(int32_t *req_to_token, int req_rows, int max_c
             (int64_t)n_reqs * s.n_layers * 2 >= (int64_t)INT32_MAX)
             return PA_ERR_SHAPE;
         if (s.n_kv_heads * s.head_dim * elem_bytes % 16 != 0) return PA_ERR_UNSUPPORTED;
-        const int32_t *lo = seq_lens, *hi = new_lens;
-        if (lo && hi && lo < hi + n_reqs && hi < lo + n_reqs) return PA_ERR_SHAPE;
     }
     if (n_reqs == 0) return PA_OK;
     if (!req_to_token || !req_pool_indices || !seq_lens || !qo_indptr || !accepted || !n_accepted || !new_lens)
@@ -183,6 +181,9 @@ extern "C" pa_status pa_kv_accept(int32_t *req_to_token, int req_rows, int max_c
         !aligned4(accepted) || !aligned4(n_accepted) || !aligned4(new_lens) || !aligned4(freed) || !aligned4(error_word) ||
         !aligned16(k_buf) || !aligned16(v_buf))
         return PA_ERR_ALIGN;
+    // a request's length is written while other requests' are read, and in the move form its own as well
+    if ((move || seq_lens != new_lens) && seq_lens < new_lens + n_reqs && new_lens < seq_lens + n_reqs)
+        return PA_ERR_SHAPE;
     AcceptArgs a{};
     a.req_to_token = req_to_token;
     a.req_pool_indices = req_pool_indices;
