@@ -384,7 +384,7 @@ pa_status pa_paged_decode_attn_fp8_block(const void *q, int batch, int n_q_heads
 /* pa_paged_prefill_attn_fp8_block: pa_paged_prefill_attn over this cache, the
  * same arguments, workspace, limits and error reporting plus the exponents.
  * Q K^T runs on the e4m3 rows as they are, q as a sum of two e4m3 terms (within
- * 2^-19 of the row's largest element) and each key's scale on its scores; V is
+ * 2^-17 of the row's largest element) and each key's scale on its scores; V is
  * widened to bf16 with its scale (exact down to bf16's subnormal step, 2^-133) and
  * the weights are rounded to bf16, as in pa_paged_prefill_attn.  (Keys of an empty
  * block count as their codes times 2^-126, which only queries beyond 1e27 can tell

@@ -63,10 +63,11 @@ __device__ __forceinline__ void widen_e4m3_tile(uint32_t src, uint32_t dst, int 
 // Row `row` of a q tile (bf16, 128-byte swizzle) into two e4m3 terms in its
 // place: q 2^-k = q1 + q2, k such that the row's largest element is within 448.
 // D = 128: q1 in the first half tile's row, q2 in the second's; D = 64: q1 and q2
-// side by side in the row.  Every element of at least 2^-11 of the largest is
+// side by side in the row.  Every element of at least 2^-9 of the largest is
 // exact (a bf16 has 8 significant bits, an e4m3 four), smaller ones are off by
-// at most 2^-19 of it.  A row's bytes belong to one thread.  The terms are
-// those of sg q; returns 2^k.
+// less than 2^-17 of it: the largest is above 224 2^k, and below 2^-2 2^k the second
+// term's step of 2^-9 2^k leaves half of it out.  A row's bytes belong to one thread.
+// The terms are those of sg q; returns 2^k.
 template <int D>
 __device__ __forceinline__ float split_q_row(uint32_t tile, int row, float sg)
 {

@@ -69,7 +69,9 @@ __device__ __forceinline__ void steps_add(Steps &s, float w)
     s.mid += __float_as_uint(t2);
     s.lo += __float_as_uint(t3);
 }
-// of n additions (at most 1024 of values below 2: 22 + 10 bits)
+// of n additions: a value below 2 is at most 2^23 places of the first word, so 511 of them stay in its 32 bits
+constexpr int kStepsMost = 511;
+static_assert(4 * kVfAhead <= kStepsMost, "a lane's additions between two sums");
 __device__ __forceinline__ u64 steps_sum(const Steps &s, uint32_t n)
 {
     const long long mid = (int32_t)(s.mid - n * kOneMid), lo = (int32_t)(s.lo - n * kOneLo);
