@@ -557,7 +557,9 @@ def pa_kv_accept(req_to_token, req_pool_indices, seq_lens, qo_indptr, accepted, 
                  v_buf=None, error_word=None, stream=None):
     """Keep each request's accepted nodes and free its others: in the page table, or
     (``k_buf``, ``v_buf``: bf16 or e4m3 with scales per head) by moving the K/V rows
-    of every layer.  Lengths in ``new_lens``, the slots handed back in ``freed``
+    of every layer.  Not so the rows of a block-scaled cache, which are bytes of the
+    same types (nothing here can tell them apart): a row's scale is its block's, so that
+    cache takes the table form.  Lengths in ``new_lens``, the slots handed back in ``freed``
     (int32 [T], a request's from ``qo_indptr`` on)."""
     dev = _device()
     _all(dev, (req_to_token, torch.int32, 2, "req_to_token"), (req_pool_indices, torch.int32, 1, "req_pool_indices"),
