@@ -176,3 +176,13 @@ def test_accept_ranges_that_begin_before_an_earlier_end(move):
         for src, dst in moves:
             now[:, dst] = k[:, src]
         assert torch.equal(kv["k"].cpu(), now) and torch.equal(kv["v"].cpu(), now.flip(0))
+
+
+def test_more_kv_heads_than_sms_set_no_error():
+    """One range per kv head, several heads to a CTA, no merge: the error word stays 0, every row of every head is written."""
+    c = make([300, 0, 40], [5, 1, 140], 200, 64, 16, 0, 65, layers=1, layer=0)
+    seen = [S.chain_seen(n) for n in c.nodes]
+    q = queries(c, 1, 64)
+    out, ws = tree(c, q.cuda(), 0.1, None)
+    assert api.pa_get_error(ws) == 0
+    check(c, q, out, 0.1, seen, "200 kv heads")
