@@ -52,11 +52,13 @@
 // part by hand when the piece ends.
 //
 // Measured, both kernels in a graph, D = 128, 8 kv heads of 4 query heads: 403 MB of
-// cache (32 requests of 500 to 8192 tokens, trees of up to 32 nodes) 89.6 us, 66 % of
+// cache (32 requests of 500 to 8192 tokens, trees of up to 32 nodes) 90.5 us, 66 % of
 // a copy's rate (6.78 TB/s); ncu over the first kernel: 403.4 MB read, tensor pipe
 // active 28 %, issue slots 20 %.  One request of 32K tokens 51 us for 136 MB; of 1K
-// 11.8 us, which is start, plan, two steps and the merge.  e4m3: 48 requests, 320 MB,
-// 141 us: the widening and the softmax share the warps.
+// 12.0 us, which is start, plan, two steps and the merge.  e4m3: 48 requests, 320 MB,
+// 142 us; left out in copies that measured nothing else: the widening with the look through
+// nodes' V rows 109, that look alone 133, q's split 139 (ncu: tensor pipe 25 %, issue slots 39 %
+// of active cycles, DRAM 29 %: the widening and the softmax of a step follow one another).
 // What bounds it.  Within a long piece over bf16 pages, HBM: a tile of 64 KB every
 // 2700 cycles and SM.  Around it the start (10000 cycles to the first S), and each
 // piece's end (5000 to 8000 for the partials, the next piece's Q and first tiles).
@@ -135,7 +137,7 @@ __device__ __forceinline__ TrReq tr_request(const TreeArgs &a, int r, int &bits,
     return q;
 }
 // The largest end of the ranges in front of request r that lie in [0, T].  (A call: only a broken batch makes it, and
-// copies of it in each place took 0.2 us to fetch.)
+// copies of it in each place took 0.1 to 0.5 us more.)
 __device__ __noinline__ int tr_front(const int32_t *qo_indptr, int T, int r)
 {
     int front = 0;
