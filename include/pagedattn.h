@@ -481,10 +481,11 @@ pa_status pa_kv_evict(int32_t *req_to_token, int req_rows, int max_ctx, const in
  * stream.  Two kernels: partial results over equal ranges of cached tokens, then
  * their merge in a fixed order (run-to-run bit-identical).  A range qo_indptr[r] ..
  * qo_indptr[r+1] outside [0, n_tokens], or one that begins in front of the end of an
- * earlier one inside it, sets PA_DEVERR_LEN and skips the request; a request row out of range (PA_DEVERR_ROW), L_r outside [n_r, max_ctx] or more nodes
- * than the mask has bits (PA_DEVERR_LEN) give zeros; a slot outside [0, size) is
- * masked and sets PA_DEVERR_SLOT.  Under PA_OVERLAP_EARLY_KV it behaves as in
- * early-metadata mode, in which qo_indptr is an index input and tree_mask is not. */
+ * earlier one inside it, sets PA_DEVERR_LEN and skips the request; a request row out of
+ * range (PA_DEVERR_ROW), L_r outside [n_r, max_ctx] or more nodes than the mask has bits
+ * (PA_DEVERR_LEN) give zeros; a slot outside [0, size) is masked and sets PA_DEVERR_SLOT.
+ * Under PA_OVERLAP_EARLY_KV it behaves as in early-metadata mode, in which qo_indptr is an
+ * index input and tree_mask is not. */
 size_t pa_tree_workspace_bytes(int n_q_heads, int n_kv_heads, int head_dim);
 pa_status pa_paged_tree_attn(const void *q, int n_tokens, int n_q_heads, const void *k_buf, const void *v_buf,
                              pa_kv_shape s, int layer_id, const int32_t *qo_indptr, int n_reqs,
@@ -536,16 +537,18 @@ pa_status pa_tree_verify(const float *target_probs, const float *draft_probs, in
  * the K/V row of node e_k is copied to the slot of position c_r + k; the table stays, and
  * freed[qo_indptr[r] ..] lists the slots of positions c_r + a_r .. L_r - 1: whole pages
  * come free.
- * new_lens[r] = c_r + a_r; freed int32 [n_tokens], entries not listed are left as they are.
- * new_lens may be seq_lens in the table form; else they must not overlap
- * (PA_ERR_SHAPE).  A path that is not increasing within [0, n_r), or longer than max_path or n_r, sets
- * PA_DEVERR_TREE; a row out of range, or one that an earlier request with nodes has too,
- * PA_DEVERR_ROW; L_r outside [n_r, max_ctx], or a qo_indptr range outside [0, n_tokens] or
- * that begins in front of the end of an earlier one inside it, PA_DEVERR_LEN: such a request is left as it is (new_lens[r] is its length, clamped to [0, max_ctx]).  So is a
- * request without nodes, a batch's padding, whatever its row and length, without an error.  A
- * slot outside [0, size) is not moved (PA_DEVERR_SLOT).  Requests must not share slots of nodes.
- * Table and lengths are index inputs of later calls: as behind pa_kv_evict, in the
- * early-metadata modes the call right after this one must not read them. */
+ * new_lens[r] = c_r + a_r; freed int32 [n_tokens], entries not listed are left as they
+ * are. new_lens may be seq_lens in the table form; else they must not overlap
+ * (PA_ERR_SHAPE).  A path that is not increasing within [0, n_r), or longer than max_path
+ * or n_r, sets PA_DEVERR_TREE; a row out of range, or one that an earlier request with
+ * nodes has too, PA_DEVERR_ROW; L_r outside [n_r, max_ctx], or a qo_indptr range outside
+ * [0, n_tokens] or that begins in front of the end of an earlier one inside it,
+ * PA_DEVERR_LEN: such a request is left as it is (new_lens[r] is its length, clamped to
+ * [0, max_ctx]).  So is a request without nodes, a batch's padding, whatever its row and
+ * length (its path is empty), without an error.  A slot outside [0, size) is not moved (PA_DEVERR_SLOT).
+ * Requests must not share slots of nodes. Table and lengths are index inputs of later
+ * calls: as behind pa_kv_evict, in the early-metadata modes the call right after this one
+ * must not read them. */
 pa_status pa_kv_accept(int32_t *req_to_token, int req_rows, int max_ctx, const int32_t *req_pool_indices,
                        const int32_t *seq_lens, const int32_t *qo_indptr, int n_tokens, int n_reqs,
                        const int32_t *accepted, int max_path, const int32_t *n_accepted, int32_t *new_lens,

@@ -10,9 +10,9 @@
 // row and takes the path's entries in order, several read before they are written:
 // position c + k never lies behind node e_k >= k, nor is it a later entry's node.
 //
-// Measured, in a graph: 64 requests' entries 3.7 us, which is a launch and four
+// Measured, in a graph: 64 requests' entries 3.8 us, which is a launch and four
 // dependent reads; 32 requests' rows in 16 layers (19 MB read and written, 2.8 us at
-// a copy's rate) 5.6 us.
+// a copy's rate) 5.7 us.
 #include <cuda_runtime.h>
 
 #include "pa_common.cuh"

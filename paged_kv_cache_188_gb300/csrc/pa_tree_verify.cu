@@ -17,11 +17,11 @@
 // the token do not depend on how the row is cut.
 //
 // Measured, in a graph: 64 chains of 5 drafted tokens, V = 131072 (67 MB of rows that
-// are drawn from: 9.9 us at a copy's rate) 19.0 us: sums by 64-bit conversions 39.8,
+// are drawn from: 9.9 us at a copy's rate) 19.4 us: sums by 64-bit conversions 39.8,
 // exact float additions 33, running sums of a piece's groups and 512 threads 19.  32
-// trees of chosen tokens, V = 100003, 14.7 us; 16 of drawn ones 21.9 (refusals wait
+// trees of chosen tokens, V = 100003, 15.1 us; 16 of drawn ones 21.9 (refusals wait
 // for one another, each a pass over rows that are kept in registers where they fit;
-// read again each time 29.7).  One chain 7.1 us: the kernel's start, four dependent
+// read again each time 29.7).  One chain 7.4 us: the kernel's start, four dependent
 // reads and a row's sum across the cluster.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
